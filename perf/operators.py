@@ -96,8 +96,8 @@ def _sizes(case):
 
 
 def _quantize(x, words):
-    """The 8-bit words and the scale of every row of x (32 bits)."""
-    most = 127.0 if words == "int8" else 448.0
+    """The 8-bit words and the scale of every row of x (32 bits, both quotients rounded as IEEE divisions)."""
+    most = torch.full((), 127.0 if words == "int8" else 448.0, device=x.device)  # a number would multiply by its inverse
     d = x.abs().amax(-1, keepdim=True) / most
     t = torch.where(d > 0, x / d, torch.zeros_like(x))
     if words == "int8":
