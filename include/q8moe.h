@@ -338,6 +338,94 @@ Q8_API int q8_model_check(q8_model *model, q8_stream stream);
  * error word, which the next q8_model_check reports as Q8_ETIMEOUT.  Nothing else is touched. */
 Q8_API int q8_model_wait_selftest(q8_model *model, unsigned polls, q8_stream stream);
 
+/* ---- the paged, quantized key/value cache ----------------------------------------------------------------------------
+ * Keys and values in pages of 8-bit words, for serving several sequences whose cached lengths differ: writing new rows
+ * (with the per-head norm and rotation of qwen_emit's layer, emit_qwen30b_generate), reading rows back, and causal
+ * attention of each sequence's new rows over its cached positions.  The pages' lane keeps f32 caches only
+ * (ForwardShim::supports refuses KvCacheQuant), so the formats below are this library's. */
+
+typedef enum {
+    Q8_KV_INT8 = 0, /* signed words: d = max|x|/127, word = round-half-away-from-zero(x/d) clamped to +-127 */
+    Q8_KV_E4M3 = 1  /* 8-bit floats (4 exponent, 3 mantissa bits): d = max|x|/448, word = x/d rounded to nearest even */
+} q8_kv_words;
+
+/* Device pages.  A cached row (one position of one key/value head: head_dim values) is head_dim words and one f32 scale
+ * d, both divisions of the rule IEEE f32, and stands for word * d; a row of zeros (or one whose d rounds to 0) has d = 0
+ * and zero words, and a row holding an infinity or a NaN has a NaN scale and zero words, so it reads back as NaN.  One
+ * scale a row and not one per 32 values: it then factors out of the attention's score and value sums, whose words enter
+ * the tensor cores exactly.
+ *   k, v    [pages][kv_heads][page_size][head_dim] words, 32-byte aligned
+ *   ks, vs  [pages][kv_heads][page_size] f32, 16-byte aligned
+ * page_size is a power of two from 16 to 1024, head_dim 64 or 128. */
+typedef struct {
+    void *k, *v;
+    float *ks, *vs;
+    int64_t pages, page_size, kv_heads, head_dim;
+    q8_kv_words words;
+} q8_kv_pages;
+
+/* Bits of a batch's error word. */
+#define Q8_KV_ERR_LENGTH 1  /* rows outside the call's, or a kv_len below the sequence's rows or past the table's end */
+#define Q8_KV_ERR_PAGE 2    /* a page id outside [0, pages) */
+#define Q8_KV_ERR_ROPE 4    /* a position past the rotation tables */
+#define Q8_KV_ERR_WAIT 8    /* a bounded device-side wait gave up (the call's outputs are incomplete) */
+
+/* A batch of sequences over pages, all of it device memory that is read when the call runs (a captured graph replays with
+ * what the arrays hold then).  Sequence b owns the activation rows row_start[b] .. row_start[b+1]-1 (row_start does not
+ * decrease; a sequence may own none; rows outside every sequence are left as they were) and has kv_len[b] cached
+ * positions, its own rows the last of them: row row_start[b] + i is position kv_len[b] - (row_start[b+1] -
+ * row_start[b]) + i.  Position p lives in page table[b*table_stride + p/page_size], slot p % page_size.
+ * What the host cannot check is checked on the device, and recorded in *error (or-ed into it) when error is not NULL:
+ *   - a sequence whose rows are not within the call's, or whose kv_len is out of range, is skipped by q8_kv_append and
+ *     q8_kv_read; q8_paged_attention skips the former and gives the latter's rows zeros (and an lse of -infinity);
+ *   - nothing is written to, or read from, a page id out of range: q8_kv_append drops the row's keys and values (its
+ *     queries are written), q8_kv_read leaves the row as it was, q8_paged_attention leaves the page's positions out. */
+typedef struct {
+    const int32_t *row_start; /* [seqs + 1] */
+    const int32_t *kv_len;    /* [seqs] */
+    const int32_t *table;     /* [seqs][table_stride], the first table_pages of each row in use */
+    int64_t seqs, table_pages, table_stride;
+    int32_t *error;           /* [1] or NULL */
+} q8_kv_batch;
+
+/* The rotation tables of q8_model_create: cos and sin (device f32 [positions][head_dim/2]) of
+ * position * theta^(-2i/head_dim), the angles in f64 and the results rounded once. */
+Q8_API int q8_rope_table(double theta, int64_t positions, int64_t head_dim, float *cos, float *sin, q8_stream stream);
+
+/* Norm, rotation and cache write of `rows` activation rows in one pass.  q (device f32, `heads` heads a row, or NULL with
+ * heads 0), k and v (kv_heads heads a row) have rows q_stride, k_stride and v_stride values apart, so columns of one
+ * merged projection do; the heads of a row are consecutive.  For each query and key head x:
+ *     y = x / sqrt(mean(x^2) + eps) * w          (w = q_norm or k_norm, device f32 [head_dim]; NULL: y = x)
+ *     z_i = y_i c_i - y_{i+h} s_i,  z_{i+h} = y_i s_i + y_{i+h} c_i    (h = head_dim/2; c, s the row's position's table
+ *                                                 rows, rope_positions of them; both tables NULL: z = y)
+ * Queries go to q_out (device f32, rows q_out_stride apart; may be q itself); keys z and values v are quantized into
+ * their page slots.  The keys' z is formed to about 2^-44 and rounded to f32 once, so that the words follow the formula.
+ * A row past the rotation tables is skipped (Q8_KV_ERR_ROPE).  Two rows must not share a slot.  Addresses are 16-byte
+ * aligned and strides multiples of 4. */
+Q8_API int q8_kv_append(const q8_kv_pages *pages, const q8_kv_batch *batch, int64_t rows, int64_t heads, const float *q,
+                        int64_t q_stride, const float *k, int64_t k_stride, const float *v, int64_t v_stride,
+                        const float *q_norm, const float *k_norm, float eps, const float *cos, const float *sin,
+                        int64_t rope_positions, float *q_out, int64_t q_out_stride, q8_stream stream);
+
+/* The inverse: word * d of the keys and values of the batch's rows (the last row_start[b+1] - row_start[b] positions of
+ * sequence b; all of them where it owns kv_len[b] rows), into k_out and v_out (device f32, either may be NULL, 32-byte
+ * aligned), value i of head g of row r at r*row_stride + g*head_stride + i (strides multiples of 8).  A dense cache
+ * [kv_heads][ctx][head_dim] is row_stride head_dim and head_stride ctx*head_dim. */
+Q8_API int q8_kv_read(const q8_kv_pages *pages, const q8_kv_batch *batch, int64_t rows, float *k_out, float *v_out,
+                      int64_t row_stride, int64_t head_stride, q8_stream stream);
+
+/* Causal attention of the batch's rows over the pages (which hold the rows' own keys and values already): for each row,
+ * at position p of its sequence, and head h (reading key/value head h / (heads/kv_heads), at most 64 heads each):
+ *     out = sum_{t<=p} e^{scale q.k_t - m} v_t / sum_{t<=p} e^{scale q.k_t - m}     (m the largest score)
+ *     lse = m + log sum_{t<=p} e^{scale q.k_t - m}                                (device f32 [rows][heads], or NULL)
+ * q and out are device f32, rows q_stride and out_stride values apart, heads of a row consecutive, 16-byte aligned,
+ * strides multiples of 4; out must not overlap q.  Sequences of one row and of many run in the same call, and the work
+ * is divided over the GPU by what the device arrays hold.  A row with no position left gets zeros and an lse of
+ * -infinity.  ws holds the partial results of sequences that several CTAs share (at most 26 MiB). */
+Q8_API int q8_paged_attention(const q8_kv_pages *pages, const q8_kv_batch *batch, int64_t rows, int64_t heads,
+                              const float *q, int64_t q_stride, float scale, float *out, int64_t out_stride, float *lse,
+                              q8_ws *ws, q8_stream stream);
+
 /* ---- errors --------------------------------------------------------------------------------------------------- */
 /* The text of the calling thread's last error (empty when none); valid until the thread's next call. */
 Q8_API const char *q8_last_error(void);

@@ -48,6 +48,21 @@ class q8_moe_plan(ctypes.Structure):
                 ("active", ctypes.c_void_p)]
 
 
+KV_INT8 = 0  # cached words: signed 8-bit integers, a scale a row
+KV_E4M3 = 1  # cached words: 8-bit floats of 4 exponent and 3 mantissa bits, a scale a row
+KV_ERR_LENGTH, KV_ERR_PAGE, KV_ERR_ROPE, KV_ERR_WAIT = 1, 2, 4, 8  # bits of a batch's error word
+
+
+class q8_kv_pages(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "ks", "vs")] + [
+        (n, ctypes.c_int64) for n in ("pages", "page_size", "kv_heads", "head_dim")] + [("words", ctypes.c_int)]
+
+
+class q8_kv_batch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("row_start", "kv_len", "table")] + [
+        (n, ctypes.c_int64) for n in ("seqs", "table_pages", "table_stride")] + [("error", ctypes.c_void_p)]
+
+
 class q8_model_desc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("layers", "d", "heads", "kv_heads", "head_dim", "experts", "k", "dff",
                                                 "vocab", "ctx")] + [
@@ -85,6 +100,11 @@ _SIGS = {
                     _P(q8_act), _P(q8_shared_expert), _vp, _vp],
     "moe_down_combine": [_P(q8_mat), _i64, _i32, _vp, _P(q8_act), _i64, _i32, _vp, _vp, _P(q8_moe_plan), _vp, _vp,
                          _vp, _P(q8_shared_expert), _vp, _vp],
+    "q8_rope_table": [ctypes.c_double, _i64, _i64, _vp, _vp, _vp],
+    "q8_kv_append": [_P(q8_kv_pages), _P(q8_kv_batch), _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _f32, _vp,
+                     _vp, _i64, _vp, _i64, _vp],
+    "q8_kv_read": [_P(q8_kv_pages), _P(q8_kv_batch), _i64, _vp, _vp, _i64, _i64, _vp],
+    "q8_paged_attention": [_P(q8_kv_pages), _P(q8_kv_batch), _i64, _i64, _vp, _i64, _f32, _vp, _i64, _vp, _vp, _vp],
     "q8_model_create": [_P(q8_model_desc), _P(_vp)],
     "q8_model_destroy": [_vp],
     "decode_step": [_vp, _vp],
@@ -271,6 +291,129 @@ def moe_down_combine(dq, ds, d, mode, k, ids, gates, y, h=None, hq=None, hs=None
     _check(lib.moe_down_combine(ctypes.byref(Dm), int(d), int(mode), _ptr(h), ha, rows, int(k), _ptr(ids),
                                 _ptr(gates), pl, _ptr(residual), _ptr(y), _ptr(expert_out), sh,
                                 ws.handle if ws else None, _stream(stream)))
+
+
+def _refuse(cond, msg):
+    if cond:
+        raise Q8Error(-1, msg)
+
+
+def _elsewhere(t):
+    """Whether t is not on the current device."""
+    import torch
+    d = t.get_device()
+    return d < 0 or d != torch.cuda.current_device()
+
+
+def _rows(t, heads, hd, name):
+    """The address and row stride of f32 rows [rows, heads, hd] whose heads are consecutive."""
+    import torch
+    _refuse(t.dtype != torch.float32 or _elsewhere(t), f"{name}: not an f32 tensor of the current device")
+    shape, stride = t.shape, t.stride()
+    _refuse(len(shape) != 3 or shape[1] != heads or shape[2] != hd, f"{name}: {tuple(shape)}, expected [rows, {heads}, {hd}]")
+    _refuse(stride[2] != 1 or (heads > 1 and stride[1] != hd), f"{name}: the heads of a row are not consecutive")
+    return t.data_ptr(), stride[0] if shape[0] > 1 else heads * hd
+
+
+def _vec(t, n, name):
+    """The address of a contiguous device f32 tensor of n values (None: NULL)."""
+    if t is None:
+        return None
+    import torch
+    _refuse(t.dtype != torch.float32 or _elsewhere(t) or not t.is_contiguous() or t.numel() != n,
+            f"{name}: not a contiguous f32 tensor of {n} values on the current device")
+    return t.data_ptr()
+
+
+def kv_pages(k, ks, v, vs) -> q8_kv_pages:
+    """Pages over device tensors: words k and v [pages, kv_heads, page_size, head_dim] (int8 or float8_e4m3fn), scales ks
+    and vs f32 [pages, kv_heads, page_size].  The tensors must outlive the struct."""
+    import torch
+    words = {torch.int8: KV_INT8, torch.float8_e4m3fn: KV_E4M3}.get(k.dtype)
+    shape = k.shape
+    _refuse(words is None or len(shape) != 4, "k: not int8 or e4m3 words [pages, kv_heads, page_size, head_dim]")
+    for t, kind, want, name in ((k, k.dtype, shape, "k"), (v, k.dtype, shape, "v"), (ks, torch.float32, shape[:3], "ks"),
+                                (vs, torch.float32, shape[:3], "vs")):
+        _refuse(t.dtype != kind or t.shape != want or not t.is_contiguous() or _elsewhere(t),
+                f"{name}: not a contiguous {kind} tensor {tuple(want)} on the current device")
+    return q8_kv_pages(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape[0], shape[2], shape[1], shape[3],
+                       words)
+
+
+def kv_batch(row_start, kv_len, table, error=None) -> q8_kv_batch:
+    """A batch of sequences over pages (q8moe.h, q8_kv_batch): device int32 row_start [seqs + 1], kv_len [seqs] and table
+    [seqs, pages], and optionally an int32 error word.  The tensors must outlive the struct."""
+    import torch
+    seqs = kv_len.shape[0]
+    _refuse(kv_len.dim() != 1 or row_start.shape != (seqs + 1,) or table.dim() != 2 or table.shape[0] != seqs,
+            "batch: expected row_start [seqs + 1], kv_len [seqs], table [seqs, pages]")
+    for t, name in ((row_start, "row_start"), (kv_len, "kv_len"), (table, "table"), (error, "error")):
+        if t is not None:
+            _refuse(t.dtype != torch.int32 or _elsewhere(t) or (t.numel() > 1 and t.shape[-1] > 1 and t.stride(-1) != 1),
+                    f"{name}: not an int32 tensor of consecutive values on the current device")
+    _refuse(error is not None and error.numel() != 1, "error: not one value")
+    pages = table.shape[1]
+    return q8_kv_batch(row_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), seqs, pages,
+                       table.stride(0) if seqs > 1 else pages, error.data_ptr() if error is not None else None)
+
+
+def q8_rope_table(theta, cos, sin, stream=None):
+    """Fills cos and sin (device f32 [positions, head_dim/2]) with the rotation tables of base theta."""
+    n, half = cos.shape
+    _check(lib.q8_rope_table(float(theta), n, 2 * half, _vec(cos, n * half, "cos"), _vec(sin, n * half, "sin"),
+                             _stream(stream)))
+
+
+def q8_kv_append(pages, batch, q, k, v, q_out, q_norm=None, k_norm=None, eps=1e-6, cos=None, sin=None, stream=None):
+    """Norms and rotates the rows' query and key heads (q [rows, heads, hd] into q_out; k, v [rows, kv_heads, hd]) and
+    quantizes the keys and values into their page slots.  q and q_out may be None (keys and values only)."""
+    kv, hd = pages.kv_heads, pages.head_dim
+    rows = k.shape[0]
+    _refuse(v.shape[0] != rows or (q is None) != (q_out is None), "q, k, v, q_out: rows differ")
+    heads, qa, qs, oa, os_ = 0, None, 0, None, 0
+    if q is not None:
+        heads = q.shape[1]
+        _refuse(q.shape[0] != rows or q_out.shape[0] != rows, "q, k, v, q_out: rows differ")
+        qa, qs = _rows(q, heads, hd, "q")
+        oa, os_ = _rows(q_out, heads, hd, "q_out")
+    ka, ks = _rows(k, kv, hd, "k")
+    va, vs = _rows(v, kv, hd, "v")
+    positions = cos.shape[0] if cos is not None else 0
+    _check(lib.q8_kv_append(ctypes.byref(pages), ctypes.byref(batch), rows, heads, qa, qs, ka, ks, va, vs,
+                            _vec(q_norm, hd, "q_norm"), _vec(k_norm, hd, "k_norm"), eps,
+                            _vec(cos, positions * hd // 2, "cos"), _vec(sin, positions * hd // 2, "sin"), positions, oa, os_,
+                            _stream(stream)))
+
+
+def q8_kv_read(pages, batch, k_out=None, v_out=None, stream=None):
+    """The values of the batch's rows into k_out and v_out [rows, kv_heads, hd] (either may be None; rows and heads any
+    multiple of 8 values apart, as in the transposed view of a dense cache [kv_heads, ctx, hd])."""
+    import torch
+    kv, hd = pages.kv_heads, pages.head_dim
+    one = k_out if k_out is not None else v_out
+    _refuse(one is None, "k_out and v_out: both None")
+    rows = one.shape[0]
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None:
+            _refuse(t.dtype != torch.float32 or _elsewhere(t) or t.shape != (rows, kv, hd) or t.stride(2) != 1 or
+                    t.stride() != one.stride(),
+                    f"{name}: not f32 [rows, {kv}, {hd}] on the current device, laid out as the other")
+    rs, hs = one.stride(0) if rows > 1 else kv * hd, one.stride(1) if kv > 1 else hd
+    _check(lib.q8_kv_read(ctypes.byref(pages), ctypes.byref(batch), rows, _ptr(k_out), _ptr(v_out), rs, hs,
+                          _stream(stream)))
+
+
+def q8_paged_attention(pages, batch, q, out, scale=None, lse=None, ws=None, stream=None):
+    """Causal attention of the rows q [rows, heads, hd] over their sequences' cached positions, into out; scale defaults
+    to hd^-1/2, lse (optional) is f32 [rows, heads]."""
+    hd = pages.head_dim
+    rows, heads = q.shape[0], q.shape[1]
+    qa, qs = _rows(q, heads, hd, "q")
+    oa, os_ = _rows(out, heads, hd, "out")
+    _refuse(out.shape[0] != rows, "out: rows differ")
+    _check(lib.q8_paged_attention(ctypes.byref(pages), ctypes.byref(batch), rows, heads, qa, qs,
+                                  hd ** -0.5 if scale is None else scale, oa, os_, _vec(lse, rows * heads, "lse"),
+                                  ws.handle if ws else None, _stream(stream)))
 
 
 class Model:

@@ -320,6 +320,56 @@ cudaError_t launch_pos_add(int32_t* pos, int add, const int* err, cudaStream_t s
 // The scratch and counters of a caller's workspace, for the launches of one call (the C ABI's q8_ws).
 Carve workspace_carve(const q8_ws* ws);
 
+// ---- the paged, quantized key/value cache (kv_pages.cu, paged_attn.cu) --------------------------------------------
+// A batch over pages as the kernels read it (q8_kv_pages and q8_kv_batch, checked).
+struct KvView {
+    int8_t* k = nullptr;               // [pages][kv][page][hd] words (8 bits of either type)
+    int8_t* v = nullptr;
+    float* ks = nullptr;               // [pages][kv][page]
+    float* vs = nullptr;
+    int pages = 0, kv = 0, page_log2 = 0;
+    const int32_t* row_start = nullptr;  // [seqs + 1]
+    const int32_t* kv_len = nullptr;     // [seqs]
+    const int32_t* table = nullptr;
+    int64_t table_stride = 0;
+    int seqs = 0;
+    int cap = 0;                       // positions a table row holds
+    int rows = 0;                      // activation rows of the call
+    int* error = nullptr;
+};
+
+struct KvAppendCall {
+    KvView view;
+    int hd = 0, heads = 0, words = 0;
+    const float *q = nullptr, *k = nullptr, *v = nullptr;
+    int64_t q_stride = 0, k_stride = 0, v_stride = 0, q_out_stride = 0;
+    const float *q_norm = nullptr, *k_norm = nullptr;
+    float eps = 0.f;
+    const float *cos_t = nullptr, *sin_t = nullptr;
+    int64_t rope_positions = 0;
+    float* q_out = nullptr;
+};
+cudaError_t launch_kv_append(const KvAppendCall& c, cudaStream_t st);
+
+struct KvReadCall {
+    KvView view;
+    int hd = 0, words = 0;
+    float *k_out = nullptr, *v_out = nullptr;
+    int64_t row_stride = 0, head_stride = 0;
+};
+cudaError_t launch_kv_read(const KvReadCall& c, cudaStream_t st);
+
+struct PagedAttnCall {
+    KvView view;
+    int hd = 0, heads = 0, words = 0;
+    const float* q = nullptr;
+    int64_t q_stride = 0, out_stride = 0;
+    float scale = 0.f;
+    float* out = nullptr;
+    float* lse = nullptr;
+};
+cudaError_t launch_paged_attention(const PagedAttnCall& c, Carve& ws, cudaStream_t st);
+
 // A persistent grid for `kernel`: enough CTAs of Q8_THREADS threads for `warps` warps, at most the CTAs that fit on
 // the device at once (occupancy times SMs).
 // ---- the decode step's layers in one persistent launch (decode_persistent.cu) ----------------------------------
