@@ -1,104 +1,522 @@
-// Causal attention of a ragged batch's rows over pages of 8-bit key and value words (q8moe.h, q8_paged_attention).
+// Causal attention of a ragged batch's rows over pages of 8-bit key and value words (q8moe.h, q8_paged_attention): the
+// kernel for few query vectors a key/value head (decoding), and the choice between it and paged_attn_tc.cu's.
 //
-// A CTA a (row, head): its warps take the row's positions in turn, a lane HD/32 dimensions, with a running maximum and
-// sum of the softmax each; the warps' results meet in shared memory.
+// What it computes: qwen_emit docs, emit_qwen30b_generate (causal attention over a cache, query heads grouped evenly over
+// key/value heads) for rows of several sequences over pages; out = sum_t w_t d_t v_t / sum_t w_t with
+// w_t = 2^(s_t - m), s_t = log2(e) scale c_t (q . k_t), c and d the cached rows' scales, k and v their words.
+//
+// How: a position is read once (2 (hd + 4) bytes a key/value head) for all the query vectors of its group, so the words'
+// bytes bound it; on the CUDA cores the products of 8 vectors already cost more than the bytes (4 * 8 * 128 flops on 264
+// bytes: about 100 TFLOP/s at the memory's rate, above the part's f32 rate), so they run on the tensor cores' warp-wide
+// form, m16n8k16: 16 positions (or dimensions) by 8 vectors.  Words are exact in f16.  The f32 operand (query, or weight
+// times value scale) is scaled by a power of two and split into two f16 parts, x = hi + lo to 2^-22, both products
+// accumulated in f32.
+//  - A warp takes 16 positions at a time straight from the pages into registers (no shared memory: a position's words are
+//    used by one warp).  The order of a contraction's index is free, so each lane loads 32 (hd 128) consecutive bytes of
+//    a key row as its share of the scores' dimensions, and 16 of four value rows as its share of the output's.
+//  - Scores come out as positions by vectors and go back in as the second product's operand after an 8 x 8 transpose of
+//    their f16 parts across the warp.
+//  - Every warp keeps its own running maximum and sums.  The tensor cores truncate as they accumulate, so every 8 steps
+//    the products are added (rounded) to the warp's f32 totals in shared memory.
+//  - 16 warps a CTA, one CTA an SM, each CTA an equal run of 128-position units over the whole batch.  The warps' results
+//    meet in shared memory; an item that several CTAs share meets in the workspace, folded in order by the last to arrive.
 #include <cuda_fp16.h>
-#include <float.h>
-#include <math.h>
 
-#include "common.cuh"
-#include "kv_pages.cuh"
+#include "paged_attn.cuh"
 
 namespace q8 {
 
 namespace {
 
-struct PagedParams {
-    KvView view;
-    int heads;
-    const float* q;
-    int64_t q_stride, out_stride;
-    float scale;
-    float* out;
-    float* lse;
-};
+constexpr int PR_WARPS = 16, PR_THREADS = PR_WARPS * 32;
+constexpr int PR_UNIT = 128;   // positions a unit
+constexpr int PR_STEP = 16;    // positions a warp takes at a time
+constexpr int PR_FLUSH = 8;    // steps between additions to the totals
+constexpr int PR_PEXP = 14;    // weights are split as values of up to 2^(PR_PEXP + 1)
+
+// The bytes of w (flipped by 0x80 each for int8) that `SEL` picks, two of them, as two f16 values.
+template <int WORDS, int HALF>
+__device__ __forceinline__ uint32_t words2_f16(uint32_t w) {
+    if (WORDS == Q8_KV_INT8) {
+        // byte + 128 in the low mantissa byte of 1024.0, less 1152: exact
+        const uint32_t u = __byte_perm(w, 0x64646464u, HALF ? 0x4342 : 0x4140);
+        const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return e4m3x2_to_f16x2((uint16_t)(HALF ? w >> 16 : w & 0xffffu));
+}
 
 template <int WORDS>
-__device__ __forceinline__ float word_value(const int8_t* p) {
-    if (WORDS == Q8_KV_INT8) return (float)*p;
-    const uint32_t h = e4m3x2_to_f16x2((uint16_t) * reinterpret_cast<const uint8_t*>(p));
-    return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
+__device__ __forceinline__ uint32_t words_flip(uint32_t w) {
+    return WORDS == Q8_KV_INT8 ? w ^ 0x80808080u : w;
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Two f32 values as two f16 parts each.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = pack_f16(a, b);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    lo = pack_f16(a - f.x, b - f.y);
+}
+
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }  // e in [-126, 127]
+
+// The unbiased exponent of a non-negative float's bits, at least -100 (so that scalings by its inverse and by 2^14 stay
+// finite); infinities and NaN: 0 (whatever they scale stays not finite).
+__device__ __forceinline__ int exponent_of(unsigned bits) {
+    return bits >= 0x7f800000u ? 0 : max((int)(bits >> 23) - 127, -100);
+}
+
+
+template <int BYTES>
+struct Bytes {
+    uint32_t w[BYTES / 4];
+};
+
+template <int BYTES>
+__device__ __forceinline__ void load_words(const int8_t* p, Bytes<BYTES>& b) {
+    if constexpr (BYTES == 32) {
+        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(b.w[0]), "=r"(b.w[1]), "=r"(b.w[2]), "=r"(b.w[3]), "=r"(b.w[4]), "=r"(b.w[5]), "=r"(b.w[6]),
+                       "=r"(b.w[7])
+                     : "l"(p));
+    } else if constexpr (BYTES == 16) {
+        asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(b.w[0]), "=r"(b.w[1]), "=r"(b.w[2]), "=r"(b.w[3])
+                     : "l"(p));
+    } else {
+        asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0,%1}, [%2];" : "=r"(b.w[0]), "=r"(b.w[1]) : "l"(p));
+    }
+}
+
+// NT: 8-vector tiles an item (1 or 2).
+template <int HD, int NT>
+struct RowsShared {
+    static constexpr int MT = 8 * NT, FR = HD / 16 * NT;   // vectors an item; float4 totals a lane
+    uint4 q[NT][HD / 16][32];          // the queries' parts in the scores' operand order: hi (2 registers), lo
+    float4 o[PR_WARPS][FR][32];        // the warps' totals, in the accumulators' order
+    float m[PR_WARPS][MT], l[PR_WARPS][MT], f[PR_WARPS][MT];
+    float qf[MT];                      // what turns a scaled product into a score, without the key's scale
+    int lim[MT];                       // the last position a vector attends (-1: none)
+    int64_t at[MT];                    // where a vector's output starts (-1: no such vector)
+    int64_t lse_at[MT];
+    int last;
+};
+
+template <int HD, int WORDS, int NT>
+__global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedParams pk) {
+    constexpr int MT = 8 * NT, KB = HD / 4, KS = HD / 16, DPG = HD / 8, FR = HD / 16 * NT;
+    constexpr int SLOT = FR * 32 * 4 + 2 * MT;  // floats of a partial result
+    extern __shared__ __align__(16) unsigned char raw[];
+    RowsShared<HD, NT>& sh = *reinterpret_cast<RowsShared<HD, NT>*>(raw);
+    const KvView& kv = pk.view;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int G = pk.group;
+
+    auto tiles_of = [&](const KvSeq& s) { return (s.n * G + MT - 1) / MT; };
+    auto span_of = [&](const KvSeq& s) -> int64_t {  // units of one item
+        return s.len_ok ? (s.len + PR_UNIT - 1) / PR_UNIT : 1;
+    };
+    auto units = [&](const KvSeq& s) -> int64_t {
+        return paged_takes(pk, s) ? kv.kv * tiles_of(s) * span_of(s) : 0;
+    };
+    const PagedRun run = paged_run<PR_THREADS>(pk, units);
+    if ((int)blockIdx.x >= run.ctas) return;
+
+    int b = run.seq;
+    int64_t b_at = run.seq_at;
+    KvSeq s = kv_seq(kv, b);
+    for (int64_t cur = run.lo; cur < run.hi;) {
+        int64_t n_units;
+        while (cur >= b_at + (n_units = units(s))) {  // the sequence of unit `cur`
+            b_at += n_units;
+            s = kv_seq(kv, ++b);
+        }
+        const int64_t U = span_of(s), tiles = tiles_of(s), item = (cur - b_at) / U;
+        const int h = (int)(item / tiles);
+        const int64_t m0 = item % tiles * MT;  // the item's first vector
+        const int64_t item_at = b_at + item * U;
+        const int64_t u0 = cur - item_at, u1 = min(U, u0 + (run.hi - cur));
+        const int end = s.len_ok ? (int)min((int64_t)s.len, u1 * PR_UNIT) : 0;  // positions before which the piece ends
+        const int begin = (int)(u0 * PR_UNIT);
+
+        // ---- the item's queries: a warp a vector, split into two f16 parts after a scaling by a power of two
+        if (wid < MT) {
+            const int64_t m = m0 + wid;
+            const bool valid = m < s.n * G;
+            const int64_t row = s.first + m / G;
+            const int head = h * G + (int)(m % G);
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (valid && lane < HD / 4)
+                x = *reinterpret_cast<const float4*>(pk.q + row * pk.q_stride + (int64_t)head * HD + 4 * lane);
+            const unsigned big = __reduce_max_sync(
+                0xffffffffu, max(max(__float_as_uint(fabsf(x.x)), __float_as_uint(fabsf(x.y))),
+                                 max(__float_as_uint(fabsf(x.z)), __float_as_uint(fabsf(x.w)))));
+            const int e = big == 0u ? 0 : 14 - exponent_of(big);
+            const float f = pow2i(e);
+            uint4 r;
+            split2(x.x * f, x.y * f, r.x, r.z);
+            split2(x.z * f, x.w * f, r.y, r.w);
+            if (lane < HD / 4) sh.q[wid / 8][lane % KS][(wid % 8) * 4 + lane / KS] = r;
+            if (lane == 0) {
+                sh.qf[wid] = pow2i(-e) * pk.scale;
+                sh.lim[wid] = valid && s.len_ok ? (int)(s.len - s.n + m / G) : -1;
+                sh.at[wid] = valid ? row * pk.out_stride + (int64_t)head * HD : -1;
+                sh.lse_at[wid] = row * pk.heads + head;
+            }
+        }
+        __syncthreads();
+
+        // ---- this warp's positions
+        float m_run[NT][2], l_run[NT][2], fac[NT][2], qf[NT][2];
+        int lim[NT][2];
+        float acc[NT][HD / 16][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                m_run[n][c] = -INFINITY;
+                l_run[n][c] = 0.f;
+                fac[n][c] = 1.f;
+                qf[n][c] = sh.qf[8 * n + 2 * t + c];
+                lim[n][c] = sh.lim[8 * n + 2 * t + c];
+            }
+#pragma unroll
+            for (int i = 0; i < HD / 16; ++i) {
+                sh.o[wid][n * (HD / 16) + i][lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[n][i][c] = 0.f;
+            }
+        }
+        int exp_run = -100, exp_top = -100;  // the weights' scaling, and the largest it has been
+        const int steps = end > begin ? (end - begin + PR_STEP - 1) / PR_STEP : 0;  // of all warps
+        Bytes<KB> kw[2];
+        Bytes<DPG> vw[4];
+        float ks[2], vs[2];
+        int page_l = -1;  // this lane's: the page of the warp's step (batch of 32 steps)
+        auto look_up = [&](int i) {  // the pages of the warp's steps i .. i + 31
+            const int step = wid + (i + lane) * PR_WARPS;
+            page_l = -1;
+            if (step < steps) {
+                page_l = kv_page(kv, b, begin + step * PR_STEP);
+                if (page_l < 0) kv_flag(kv, Q8_KV_ERR_PAGE);
+            }
+        };
+        auto row_of = [&](int i, int& page) -> int64_t {  // the cached row of step i's first position
+            page = __shfl_sync(0xffffffffu, page_l, i & 31);
+            return kv_row(kv, max(page, 0), h, begin + (wid + i * PR_WARPS) * PR_STEP);
+        };
+        auto load_k = [&](int64_t row) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                load_words<KB>(kv.k + (row + g + 8 * j) * HD + KB * t, kw[j]);
+                ks[j] = ld_scale_stream(kv.ks + row + g + 8 * j);
+            }
+        };
+        auto load_v = [&](int64_t row) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) load_words<DPG>(kv.v + (row + 2 * t + (j & 1) + 8 * (j >> 1)) * HD + DPG * g, vw[j]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) vs[j] = ld_scale_stream(kv.vs + row + g + 8 * j);
+        };
+        const int mine = steps > wid ? (steps - wid + PR_WARPS - 1) / PR_WARPS : 0;
+        int page = -1, page_next = -1;
+        int64_t row_next = 0;
+        if (mine > 0) {
+            look_up(0);
+            row_next = row_of(0, page_next);
+            load_k(row_next);
+            load_v(row_next);
+        }
+#pragma unroll 1
+        for (int i = 0; i < mine; ++i) {
+            page = page_next;
+            const int p0 = begin + (wid + i * PR_WARPS) * PR_STEP;
+            if (i + 1 < mine) {
+                if (((i + 1) & 31) == 0) look_up(i + 1);
+                row_next = row_of(i + 1, page_next);
+            }
+            // scores: positions g, g + 8 by vectors 2t, 2t + 1 of each tile
+            float sh_hi[NT][4], sh_lo[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) sh_hi[n][c] = 0.f, sh_lo[n][c] = 0.f;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                const uint32_t w0 = words_flip<WORDS>(kw[0].w[k]), w1 = words_flip<WORDS>(kw[1].w[k]);
+                const uint32_t a0 = words2_f16<WORDS, 0>(w0), a1 = words2_f16<WORDS, 0>(w1);
+                const uint32_t a2 = words2_f16<WORDS, 1>(w0), a3 = words2_f16<WORDS, 1>(w1);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const uint4 q = sh.q[n][k][lane];
+                    mma16816(sh_hi[n], a0, a1, a2, a3, q.x, q.y);
+                    mma16816(sh_lo[n], a0, a1, a2, a3, q.z, q.w);
+                }
+            }
+            const float kscale[2] = {ks[0], ks[1]};
+            if (i + 1 < mine) load_k(row_next);
+            // the softmax's running maximum and sums, and the weights' parts
+            const bool here = page >= 0;
+            float vscale[2];
+            unsigned vtop = 0u;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                vscale[j] = here && p0 + g + 8 * j < end ? vs[j] : 0.f;
+                vtop = max(vtop, __float_as_uint(fabsf(vscale[j])));
+            }
+            vtop = __reduce_max_sync(0xffffffffu, vtop);
+            const int exp_old = exp_run;
+            if (vtop != 0u) {
+                const int e = exponent_of(vtop);
+                exp_top = max(exp_top, e);
+                exp_run = max(e, exp_top - 40);  // (so that rescaling the sums never overflows)
+            }
+            const float wscale = pow2i(PR_PEXP - exp_run);
+            const float eshift = exp_old - exp_run <= -126 ? 0.f : pow2i(exp_old - exp_run);
+            uint32_t ph[NT][2], pl[NT][2];
+            bool same = true;
+            float alpha[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float sc[4];
+                bool seen[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    seen[c] = here && p0 + g + 8 * (c >> 1) <= lim[n][c & 1];
+                    sc[c] = seen[c] ? (sh_hi[n][c] + sh_lo[n][c]) * kscale[c >> 1] * qf[n][c & 1] : -INFINITY;
+                }
+                float wt[4];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float mx = fmaxf(sc[c], sc[c + 2]);
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    const float mn = fmaxf(m_run[n][c], mx), ms = mn == -INFINITY ? 0.f : mn;
+                    alpha[n][c] = ex2(m_run[n][c] - ms);
+                    m_run[n][c] = mn;
+                    const float e0 = ex2(sc[c] - ms), e1 = ex2(sc[c + 2] - ms);
+                    l_run[n][c] = l_run[n][c] * alpha[n][c] + (e0 + e1);
+                    wt[c] = seen[c] ? e0 * (vscale[0] * wscale) : 0.f;
+                    wt[c + 2] = seen[c + 2] ? e1 * (vscale[1] * wscale) : 0.f;
+                    alpha[n][c] *= eshift;
+                    fac[n][c] *= alpha[n][c];
+                    same = same && alpha[n][c] == 1.f;
+                }
+                split2(wt[0], wt[1], ph[n][0], pl[n][0]);
+                split2(wt[2], wt[3], ph[n][1], pl[n][1]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) ph[n][j] = transpose8x8(ph[n][j]), pl[n][j] = transpose8x8(pl[n][j]);
+            }
+            if (!__all_sync(0xffffffffu, same)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < HD / 16; ++j)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) acc[n][j][c] *= alpha[n][c & 1];
+            }
+            if (p0 + PR_STEP > end || !here) {  // words past the end are whatever the page holds: left out
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (!here || p0 + 2 * t + (j & 1) + 8 * (j >> 1) >= end)
+#pragma unroll
+                        for (int x = 0; x < DPG / 4; ++x) vw[j].w[x] = 0u;
+            }
+            // weighted values: dimensions by vectors
+#pragma unroll
+            for (int x = 0; x < DPG / 4; ++x) {
+                uint32_t a[2][4];  // [positions 2t, 2t+1 | 2t+8, 2t+9][dimension 4x + .]
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t lo = words_flip<WORDS>(__byte_perm(vw[2 * j].w[x], vw[2 * j + 1].w[x], 0x5140));
+                    const uint32_t hi = words_flip<WORDS>(__byte_perm(vw[2 * j].w[x], vw[2 * j + 1].w[x], 0x7362));
+                    a[j][0] = words2_f16<WORDS, 0>(lo), a[j][1] = words2_f16<WORDS, 1>(lo);
+                    a[j][2] = words2_f16<WORDS, 0>(hi), a[j][3] = words2_f16<WORDS, 1>(hi);
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma16816(acc[n][2 * x + y], a[0][2 * y], a[0][2 * y + 1], a[1][2 * y], a[1][2 * y + 1], pl[n][0], pl[n][1]);
+                        mma16816(acc[n][2 * x + y], a[0][2 * y], a[0][2 * y + 1], a[1][2 * y], a[1][2 * y + 1], ph[n][0], ph[n][1]);
+                    }
+            }
+            if (i + 1 < mine) load_v(row_next);
+            if (i % PR_FLUSH == PR_FLUSH - 1 || i + 1 == mine) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                    for (int j = 0; j < HD / 16; ++j) {
+                        float4& o = sh.o[wid][n * (HD / 16) + j][lane];
+                        float4 v = o;
+                        v.x = fmaf(v.x, fac[n][0], acc[n][j][0]), v.y = fmaf(v.y, fac[n][1], acc[n][j][1]);
+                        v.z = fmaf(v.z, fac[n][0], acc[n][j][2]), v.w = fmaf(v.w, fac[n][1], acc[n][j][3]);
+                        o = v;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) acc[n][j][c] = 0.f;
+                    }
+                    fac[n][0] = fac[n][1] = 1.f;
+                }
+            }
+        }
+        // ---- the warps meet: every vector's maximum and sum, then the totals with each warp's factor
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float l = l_run[n][c];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                if (g == 0) {
+                    sh.m[wid][8 * n + 2 * t + c] = m_run[n][c];
+                    sh.l[wid][8 * n + 2 * t + c] = l;
+                    sh.f[wid][8 * n + 2 * t + c] = pow2i(exp_run - PR_PEXP);
+                }
+            }
+        __syncthreads();
+        float M = -INFINITY, L = 0.f;
+        if (tid < MT) {
+            for (int w = 0; w < PR_WARPS; ++w) M = fmaxf(M, sh.m[w][tid]);
+            for (int w = 0; w < PR_WARPS; ++w) {
+                const float f = M == -INFINITY ? 0.f : ex2(sh.m[w][tid] - M);
+                if (sh.m[w][tid] != -INFINITY) L += sh.l[w][tid] * f;
+                sh.f[w][tid] *= f;
+            }
+            sh.m[0][tid] = M;
+            sh.l[0][tid] = L;
+        }
+        __syncthreads();
+        const bool whole = u0 == 0 && u1 == U;
+        float* slot = pk.part + (int64_t)(2 * blockIdx.x + (cur == run.lo ? 0 : 1)) * SLOT;
+        auto write_out = [&](int i, int ln, float4 v, const float* m, const float* l) {
+            const int n = i / (HD / 16), dim = DPG * (ln >> 2) + 2 * (i % (HD / 16)), c = 8 * n + 2 * (ln & 3);
+            const float x0 = l[c] == 0.f ? 0.f : 1.f / l[c], x1 = l[c + 1] == 0.f ? 0.f : 1.f / l[c + 1];
+            if (sh.at[c] >= 0) *reinterpret_cast<float2*>(pk.out + sh.at[c] + dim) = make_float2(v.x * x0, v.z * x0);
+            if (sh.at[c + 1] >= 0)
+                *reinterpret_cast<float2*>(pk.out + sh.at[c + 1] + dim) = make_float2(v.y * x1, v.w * x1);
+            if (pk.lse && i % (HD / 16) == 0 && (ln >> 2) == 0)
+                for (int j = 0; j < 2; ++j)
+                    if (sh.at[c + j] >= 0)
+                        pk.lse[sh.lse_at[c + j]] = l[c + j] == 0.f ? -INFINITY : (m[c + j] + log2f(l[c + j])) * 0.693147180559945f;
+        };
+        for (int i = tid; i < FR * 32; i += PR_THREADS) {
+            const int fr = i >> 5, ln = i & 31, c = 8 * (fr / (HD / 16)) + 2 * (ln & 3);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = 0; w < PR_WARPS; ++w) {
+                const float4 o = sh.o[w][fr][ln];
+                const float f0 = sh.f[w][c], f1 = sh.f[w][c + 1];
+                v.x = fmaf(o.x, f0, v.x), v.y = fmaf(o.y, f1, v.y), v.z = fmaf(o.z, f0, v.z), v.w = fmaf(o.w, f1, v.w);
+            }
+            if (whole) write_out(fr, ln, v, sh.m[0], sh.l[0]);
+            else __stcg(reinterpret_cast<float4*>(slot) + i, v);
+        }
+        if (!whole) {
+            // ---- the item's pieces meet: the last CTA to arrive folds them in order
+            if (tid < MT) {
+                __stcg(slot + FR * 128 + tid, M);
+                __stcg(slot + FR * 128 + MT + tid, L);
+            }
+            const int c0 = run.owner(item_at), c1 = run.owner(item_at + U - 1);
+            __syncthreads();
+            if (tid == 0) sh.last = atomic_add_acq_rel_gpu(pk.counters + c0, 1) == c1 - c0;
+            __syncthreads();
+            if (sh.last) {
+                if (tid == 0) pk.counters[c0] = 0;
+                auto slot_of = [&](int c) {  // (the first CTA's piece may be the last of its run, the others' open theirs)
+                    return pk.part + (int64_t)(2 * c + (run.start(c) >= item_at ? 0 : 1)) * SLOT;
+                };
+                if (tid < MT) {
+                    float Mx = -INFINITY, Lx = 0.f;
+                    for (int c = c0; c <= c1; ++c) Mx = fmaxf(Mx, __ldcg(slot_of(c) + FR * 128 + tid));
+                    for (int c = c0; c <= c1; ++c) {
+                        const float mc = __ldcg(slot_of(c) + FR * 128 + tid);
+                        if (mc != -INFINITY) Lx += __ldcg(slot_of(c) + FR * 128 + MT + tid) * ex2(mc - Mx);
+                    }
+                    sh.m[0][tid] = Mx;
+                    sh.l[0][tid] = Lx;
+                }
+                __syncthreads();
+                for (int i = tid; i < FR * 32; i += PR_THREADS) {
+                    const int fr = i >> 5, ln = i & 31, c = 8 * (fr / (HD / 16)) + 2 * (ln & 3);
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int p = c0; p <= c1; ++p) {
+                        const float* sl = slot_of(p);
+                        const float4 o = __ldcg(reinterpret_cast<const float4*>(sl) + i);
+                        const float f0 = sh.m[0][c] == -INFINITY ? 0.f : ex2(__ldcg(sl + FR * 128 + c) - sh.m[0][c]);
+                        const float f1 = sh.m[0][c + 1] == -INFINITY ? 0.f : ex2(__ldcg(sl + FR * 128 + c + 1) - sh.m[0][c + 1]);
+                        v.x = fmaf(o.x, f0, v.x), v.y = fmaf(o.y, f1, v.y), v.z = fmaf(o.z, f0, v.z), v.w = fmaf(o.w, f1, v.w);
+                    }
+                    write_out(fr, ln, v, sh.m[0], sh.l[0]);
+                }
+            }
+        }
+        __syncthreads();  // the shared arrays are the next item's
+        cur += u1 - u0;
+    }
+}
+
+template <int HD, int WORDS, int NT>
+cudaError_t rows_launch(const PagedParams& p, cudaStream_t st) {
+    auto kernel = paged_rows_kernel<HD, WORDS, NT>;
+    constexpr size_t smem = sizeof(RowsShared<HD, NT>);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<device_info().sms, PR_THREADS, smem, st>>>(p);
+    return cudaGetLastError();
 }
 
 template <int HD, int WORDS>
-__global__ void __launch_bounds__(Q8_THREADS) paged_attention_kernel(const PagedParams pk) {
-    constexpr int DPL = HD / 32;
-    __shared__ float sm[Q8_WARPS], sl[Q8_WARPS], so[Q8_WARPS][HD];
-    const KvView& kv = pk.view;
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, h = blockIdx.y;
-    const int64_t r = blockIdx.x;
-    const int g = h / (pk.heads / kv.kv);
-    const int b = kv_find_seq(kv, r);
-    if (b < 0) return;
-    const KvSeq s = kv_seq(kv, b);
-    if ((!s.rows_ok || !s.len_ok) && threadIdx.x == 0) kv_flag(kv, Q8_KV_ERR_LENGTH);
-    if (!s.rows_ok) return;
-    const int end = s.len_ok ? (int)(s.len - s.n + (r - s.first)) + 1 : 0;  // positions the row attends
-    float q[DPL], o[DPL], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < DPL; ++i) {
-        q[i] = pk.q[r * pk.q_stride + (int64_t)h * HD + lane + 32 * i] * pk.scale;
-        o[i] = 0.f;
-    }
-    for (int p = w; p < end; p += Q8_WARPS) {
-        const int page = kv_page(kv, b, p);
-        if (page < 0) {
-            if (lane == 0) kv_flag(kv, Q8_KV_ERR_PAGE);
-            continue;
-        }
-        const int64_t row = kv_row(kv, page, g, p);
-        float d = 0.f;
-#pragma unroll
-        for (int i = 0; i < DPL; ++i) d = fmaf(q[i], word_value<WORDS>(kv.k + row * HD + lane + 32 * i), d);
-        const float sc = group_sum<32>(d) * kv.ks[row];
-        const float mn = fmaxf(m, sc), a = m == -INFINITY ? 0.f : expf(m - mn), e = expf(sc - mn);
-        l = l * a + e;
-#pragma unroll
-        for (int i = 0; i < DPL; ++i) o[i] = o[i] * a + e * kv.vs[row] * word_value<WORDS>(kv.v + row * HD + lane + 32 * i);
-        m = mn;
-    }
-    if (lane == 0) sm[w] = m, sl[w] = l;
-#pragma unroll
-    for (int i = 0; i < DPL; ++i) so[w][lane + 32 * i] = o[i];
-    __syncthreads();
-    float M = -INFINITY, L = 0.f;
-    for (int i = 0; i < Q8_WARPS; ++i) M = fmaxf(M, sm[i]);
-    for (int i = 0; i < Q8_WARPS; ++i) L += sm[i] == -INFINITY ? 0.f : sl[i] * expf(sm[i] - M);
-    for (int d = threadIdx.x; d < HD; d += Q8_THREADS) {
-        float acc = 0.f;
-        for (int i = 0; i < Q8_WARPS; ++i) acc += sm[i] == -INFINITY ? 0.f : so[i][d] * expf(sm[i] - M);
-        pk.out[r * pk.out_stride + (int64_t)h * HD + d] = L == 0.f ? 0.f : acc / L;
-    }
-    if (threadIdx.x == 0 && pk.lse) pk.lse[r * pk.heads + h] = L == 0.f ? -INFINITY : M + logf(L);
+cudaError_t rows_launch_nt(const PagedParams& p, int tiles, cudaStream_t st) {
+    return tiles == 1 ? rows_launch<HD, WORDS, 1>(p, st) : rows_launch<HD, WORDS, 2>(p, st);
 }
+
+constexpr int kRowsMost = 16;  // query vectors a key/value head that this kernel's item holds
 
 }  // namespace
 
-cudaError_t launch_paged_attention(const PagedAttnCall& c, Carve&, cudaStream_t st) {
+size_t paged_rows_slot(int hd) { return (size_t)kRowsMost * (hd + 2) * sizeof(float); }
+
+cudaError_t launch_paged_rows(const PagedParams& p, int hd, int words, int tiles, cudaStream_t st) {
+    if (hd == 128)
+        return words == Q8_KV_INT8 ? rows_launch_nt<128, Q8_KV_INT8>(p, tiles, st) : rows_launch_nt<128, Q8_KV_E4M3>(p, tiles, st);
+    return words == Q8_KV_INT8 ? rows_launch_nt<64, Q8_KV_INT8>(p, tiles, st) : rows_launch_nt<64, Q8_KV_E4M3>(p, tiles, st);
+}
+
+cudaError_t launch_paged_attention(const PagedAttnCall& c, Carve& ws, cudaStream_t st) {
     PagedParams p;
     p.view = c.view;
     p.heads = c.heads;
+    p.group = c.heads / c.view.kv;
     p.q = c.q;
     p.q_stride = c.q_stride, p.out_stride = c.out_stride;
-    p.scale = c.scale;
+    p.scale = (float)((double)c.scale * 1.4426950408889634);
     p.out = c.out;
     p.lse = c.lse;
-    const dim3 grid((unsigned)c.view.rows, (unsigned)c.heads);
-    if (c.hd == 128 && c.words == Q8_KV_INT8) paged_attention_kernel<128, Q8_KV_INT8><<<grid, Q8_THREADS, 0, st>>>(p);
-    else if (c.hd == 128) paged_attention_kernel<128, Q8_KV_E4M3><<<grid, Q8_THREADS, 0, st>>>(p);
-    else if (c.words == Q8_KV_INT8) paged_attention_kernel<64, Q8_KV_INT8><<<grid, Q8_THREADS, 0, st>>>(p);
-    else paged_attention_kernel<64, Q8_KV_E4M3><<<grid, Q8_THREADS, 0, st>>>(p);
-    return cudaGetLastError();
+    const int sms = device_info().sms;
+    p.part = ws.take<float>(2 * (size_t)sms * paged_rows_slot(c.hd) / sizeof(float));
+    p.counters = ws.take_counters(sms);
+    if (ws.overflow) return cudaSuccess;  // refused by the caller
+    p.above = 0, p.upto = INT64_MAX;
+    return launch_paged_rows(p, c.hd, c.words, p.group <= 8 && c.view.rows <= c.view.seqs ? 1 : 2, st);
 }
 
 }  // namespace q8

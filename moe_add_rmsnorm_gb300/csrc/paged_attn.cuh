@@ -1,0 +1,114 @@
+// What the two kernels of the paged attention share: the call as they read it, and the division of a batch's work over
+// the CTAs of one launch.
+#pragma once
+#include <cuda_runtime.h>
+#include <limits.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "kv_pages.cuh"
+
+namespace q8 {
+
+// A key/value head's query vectors of one sequence are its rows' heads of the group, vector m = row * group + head.  A
+// kernel takes them in tiles, and a tile's positions in units; one (sequence, key/value head, tile) is an item.
+struct PagedParams {
+    KvView view;
+    int heads = 0, group = 0;       // query heads, and query heads a key/value head
+    const float* q = nullptr;
+    int64_t q_stride = 0, out_stride = 0;
+    float scale = 0.f;              // times log2(e): scores are kept in the base-2 logarithm
+    float* out = nullptr;
+    float* lse = nullptr;
+    int64_t above = 0, upto = 0;    // the sequences taken: above < vectors a key/value head <= upto
+    float* part = nullptr;          // partial results: two slots a CTA
+    int* counters = nullptr;        // one a CTA, zero between launches
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The launch's units in one line, sequence by sequence, cut into equal runs: CTA c takes units c*T/C .. (c+1)*T/C - 1 of
+// T, so ragged batches load every SM alike, whatever the device arrays hold when the launch runs.  C is the launch's
+// CTAs, or T when there are fewer units (the other CTAs leave), so every CTA below C has a unit.
+struct PagedRun {
+    int64_t total = 0, lo = 0, hi = 0;
+    int ctas = 0;
+    int seq = 0;          // the sequence of unit lo
+    int64_t seq_at = 0;   // its first unit
+    __device__ int64_t start(int64_t c) const { return c * total / ctas; }
+    __device__ int owner(int64_t unit) const { return (int)(((unit + 1) * ctas - 1) / total); }
+};
+
+// Forms the run; `units(s)` is a sequence's unit count (0: not this kernel's).  Every thread of the CTA calls it.  Each
+// thread sums a run of sequences, the CTA scans the sums, and the thread whose sequences hold unit lo finds it.
+template <int THREADS, typename Units>
+__device__ __forceinline__ PagedRun paged_run(const PagedParams& pk, Units units) {
+    __shared__ int64_t warp_sum[THREADS / 32];
+    __shared__ int64_t found_at;
+    __shared__ int found;
+    const KvView& kv = pk.view;
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+    const int each = (kv.seqs + THREADS - 1) / THREADS;
+    const int b0 = min(kv.seqs, t * each), b1 = min(kv.seqs, b0 + each);
+    int64_t sum = 0;
+    for (int b = b0; b < b1; ++b) {
+        const KvSeq s = kv_seq(kv, b);
+        if (blockIdx.x == 0 && (!s.rows_ok || (s.n > 0 && !s.len_ok))) kv_flag(kv, Q8_KV_ERR_LENGTH);
+        sum += units(s);
+    }
+    int64_t pre = sum;  // inclusive scan
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, pre, o);
+        if (lane >= o) pre += up;
+    }
+    if (lane == 31) warp_sum[w] = pre;
+    if (t == 0) found = 0, found_at = 0;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int i = 0; i < THREADS / 32; ++i) {
+        if (i < w) before += warp_sum[i];
+        total += warp_sum[i];
+    }
+    PagedRun r;
+    r.total = total;
+    r.ctas = (int)(total < gridDim.x ? total : gridDim.x);
+    if (r.ctas > 0 && (int)blockIdx.x < r.ctas) {
+        r.lo = r.start(blockIdx.x);
+        r.hi = r.start(blockIdx.x + 1);
+        int64_t at = before + pre - sum;
+        if (at <= r.lo && r.lo < at + sum) {
+            for (int b = b0; b < b1; ++b) {
+                const int64_t n = units(kv_seq(kv, b));
+                if (r.lo < at + n) {
+                    found = b;
+                    found_at = at;
+                    break;
+                }
+                at += n;
+            }
+        }
+    }
+    __syncthreads();
+    r.seq = found;
+    r.seq_at = found_at;
+    return r;
+}
+
+// Whether a sequence is one of this launch's.
+__device__ __forceinline__ bool paged_takes(const PagedParams& pk, const KvSeq& s) {
+    const int64_t vectors = s.n * pk.group;
+    return s.rows_ok && s.n > 0 && vectors > pk.above && vectors <= pk.upto;
+}
+
+cudaError_t launch_paged_rows(const PagedParams& p, int hd, int words, int tiles, cudaStream_t st);
+size_t paged_rows_slot(int hd);   // bytes of one partial result
+cudaError_t launch_paged_tiles(const PagedParams& p, int hd, int words, cudaStream_t st);
+size_t paged_tiles_slot(int hd);
+
+}  // namespace q8
