@@ -511,12 +511,28 @@ cudaError_t launch_paged_attention(const PagedAttnCall& c, Carve& ws, cudaStream
     p.scale = (float)((double)c.scale * 1.4426950408889634);
     p.out = c.out;
     p.lse = c.lse;
+    // Which kernel takes a sequence goes by its vectors a key/value head, which the device holds: up to kRowsMost the
+    // rows kernel.  A launch that could find no sequence is left out: a batch of no more rows than sequences is taken as
+    // decoding (whatever its sequences turn out to hold, the rows kernel takes all of it), one sequence by its rows.
+    const int64_t most = c.view.seqs == 1 ? (int64_t)c.view.rows * p.group : c.view.rows > c.view.seqs ? INT64_MAX : p.group;
+    const bool rows = p.group <= kRowsMost && (c.view.seqs > 1 || most <= kRowsMost);
+    const bool tiles = most > kRowsMost;
     const int sms = device_info().sms;
-    p.part = ws.take<float>(2 * (size_t)sms * paged_rows_slot(c.hd) / sizeof(float));
-    p.counters = ws.take_counters(sms);
-    if (ws.overflow) return cudaSuccess;  // refused by the caller
-    p.above = 0, p.upto = INT64_MAX;
-    return launch_paged_rows(p, c.hd, c.words, p.group <= 8 && c.view.rows <= c.view.seqs ? 1 : 2, st);
+    PagedParams t = p;
+    auto scratch = [&](PagedParams& x, size_t slot) {
+        x.part = ws.take<float>(2 * (size_t)sms * slot / sizeof(float));
+        x.counters = ws.take_counters(sms);
+    };
+    if (rows) scratch(p, paged_rows_slot(c.hd));
+    if (tiles) scratch(t, paged_tiles_slot(c.hd));
+    if (ws.overflow) return cudaSuccess;  // refused by the caller; nothing is launched
+    p.upto = tiles ? kRowsMost : INT64_MAX;
+    t.above = rows ? kRowsMost : 0;
+    t.upto = INT64_MAX;
+    cudaError_t e = cudaSuccess;
+    if (rows) e = launch_paged_rows(p, c.hd, c.words, most <= 8 ? 1 : 2, st);
+    if (tiles && e == cudaSuccess) e = launch_paged_tiles(t, c.hd, c.words, st);
+    return e;
 }
 
 }  // namespace q8

@@ -1,0 +1,836 @@
+// Causal attention of a ragged batch's rows over pages of 8-bit words (q8moe.h, q8_paged_attention): the kernel for many
+// query vectors a key/value head (prompt chunks, drafted tokens, wide groups), on the 5th-generation tensor cores.
+//
+// What it computes: as paged_attn.cu, for tiles of 128 query vectors (whole rows' heads of one group) against tiles of 128
+// positions: S = Q K^T, the running softmax of S times the key scales, and the sums P V with P the weights times the
+// value scales.
+//
+// How: both products have one operand that is exact in f16 (the words) and one that is f32 and split into two f16 parts,
+// so each is two tensor-core products (4 x 128 x 128 x hd multiply-adds a tile pair, twice the formula's): those bound it.
+// One CTA an SM works through an equal run of tile pairs; its warps divide the work and meet only at barriers in shared
+// memory:
+//  - warps 0-3 and 4-7 (a thread a query vector) take the odd and the even tiles of positions: scores out of tensor
+//    memory, maximum, weights, and the weights' parts back into tensor memory over the scores, where the second product
+//    reads them as its first operand.  While one group does so the tensor cores work for the other.  Each group keeps
+//    its own maximum, sum and f32 output sums in registers (a tile's product is added, rounded, to them: the tensor
+//    cores truncate as they accumulate); the two meet at an item's end.
+//  - warps 8-11 turn the words into f16 operand tiles (the values transposed), and an item's queries into their parts.
+//  - warp 12 issues the products, warps 13 and 14 copy the words of 64 positions at a time from the pages into a ring
+//    (asynchronously, zeros for positions past the end), warp 15 deals out the items and prepares the scales.
+// Registers are moved from the last eight warps to the first eight (200 and 56 a thread).
+#include <cuda_fp16.h>
+
+#include "paged_attn.cuh"
+#include "stream.cuh"
+#include "tcgen05.cuh"
+
+namespace q8 {
+
+namespace {
+
+constexpr int PT_M = 128, PT_P = 128;      // query vectors and positions a tile
+constexpr int PT_THREADS = 512;
+constexpr int PT_HALF = 64;                // positions a copied stage
+constexpr int PT_STAGES = 3;
+constexpr int PT_ITEMS = 4;                // items dealt out ahead
+constexpr int PT_READERS = 15;             // warps that read an item
+constexpr unsigned PT_WAIT = 1u << 18;      // polls before a wait gives up
+constexpr int PT_PEXP = 14;                // weights are split as values of up to 2^(PT_PEXP + 1)
+
+// One item's piece as the roles read it.
+struct PtItem {
+    int64_t at, units;     // the item's first unit and its units
+    int64_t row0;          // activation row of its first token
+    int seq, head, tokens; // key/value head; tokens of the tile
+    int pos;               // position of the first token
+    int end;               // positions before which the sequence ends (0: a length out of range)
+    int t0, t1;            // the piece's tiles of positions (t0 == t1: no more items)
+    int opens;             // whether the piece opens the CTA's run
+};
+
+template <int HD>
+struct PtShared {
+    static constexpr uint32_t SBO_Q = HD / 8 * 128;        // bytes between 8-row groups of queries and keys
+    static constexpr uint32_t SBO_V = PT_P / 8 * 128 + 16; // and of transposed values (the pad spreads the writes' banks)
+    unsigned char qh[PT_M * HD * 2], ql[PT_M * HD * 2];
+    unsigned char k[2][PT_P * HD * 2];
+    unsigned char v[2][HD / 8 * SBO_V];
+    unsigned char raw[PT_STAGES][PT_HALF * HD];
+    float ks[2][PT_P], vs[2][PT_P];
+    float qf[4][PT_M];
+    float mg_m[PT_M], mg_l[PT_M];
+    float ce[2];
+    unsigned groups[2];    // which 16-position groups of a tile are there
+    PtItem item[PT_ITEMS];
+    uint64_t d_full[PT_ITEMS], d_empty[PT_ITEMS], raw_full[PT_STAGES], raw_empty[PT_STAGES];
+    uint64_t sc_full[2], sc_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t s_full[2], p_full[2], t_full[2], t_empty[2], q_full, q_empty, mg_full, met, drained;
+    uint32_t tmem;
+    int dead;              // a wait gave up: every role leaves
+    int last;
+};
+
+__device__ __forceinline__ uint64_t pk2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void upk2(uint64_t r, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// D[tmem] (+)= A * B^T for one K = 16 slice, A in tensor memory.
+__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+
+// 32 columns of this warp's 32 lanes written; complete after tc_wait_st().
+__device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+          "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+          "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 16 bytes from global into shared memory (zeros where !there), counted by async_arrive.
+__device__ __forceinline__ void async_copy16(void* dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+// This thread arrives on bar when the copies it issued so far are complete.
+__device__ __forceinline__ void async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// sum_{i<n} floor((a i + b) / m), n, a, b >= 0, m > 0 (Euclid's steps on (a, m)).
+__device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+    int64_t sum = 0;
+    while (n > 0) {
+        sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
+        a %= m;
+        b %= m;
+        const int64_t top = a * n + b;
+        if (top < m) break;
+        n = top / m;
+        b = top % m;
+        const int64_t x = m;
+        m = a;
+        a = x;
+    }
+    return sum;
+}
+
+// A sequence's tiles of query vectors: `per` whole tokens each, tile i attending the positions before len - n +
+// min((i + 1) per, n), in units of 128.
+struct PtTiles {
+    int64_t n, per, count, base;
+    int len;
+    __device__ PtTiles(const KvSeq& s, int group) {
+        n = s.n;
+        per = PT_M / group;
+        count = (n + per - 1) / per;
+        len = s.len_ok ? s.len : 0;
+        base = s.len - s.n;
+    }
+    __device__ int64_t units(int64_t i) const {
+        if (len == 0) return 1;  // a length out of range: zeros to write
+        const int64_t ends = i + 1 < count ? base + (i + 1) * per : len;
+        return (ends + PT_P - 1) / PT_P;
+    }
+    __device__ int64_t before(int64_t i) const {  // units of the tiles before i (i < count)
+        return len == 0 ? i : floor_sum(i, PT_P, per, base + per + PT_P - 1);
+    }
+    __device__ int64_t all() const { return before(count - 1) + units(count - 1); }
+};
+
+__device__ __forceinline__ uint32_t f16_pack(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }  // e in [-126, 127]
+// (as in paged_attn.cu)
+__device__ __forceinline__ int exponent_of(unsigned bits) {
+    return bits >= 0x7f800000u ? 0 : max((int)(bits >> 23) - 127, -100);
+}
+
+template <int WORDS, int HALF>
+__device__ __forceinline__ uint32_t words2_f16(uint32_t w) {
+    if (WORDS == Q8_KV_INT8) {
+        const uint32_t u = __byte_perm(w, 0x64646464u, HALF ? 0x4342 : 0x4140);
+        const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return e4m3x2_to_f16x2((uint16_t)(HALF ? w >> 16 : w & 0xffffu));
+}
+template <int WORDS>
+__device__ __forceinline__ uint32_t words_flip(uint32_t w) {
+    return WORDS == Q8_KV_INT8 ? w ^ 0x80808080u : w;
+}
+
+// Byte offset of 16-byte chunk c of row r in a copied stage: chunks are permuted within 128 bytes so that eight rows'
+// equal chunks lie in different banks.
+template <int HD>
+__device__ __forceinline__ uint32_t raw_off(int r, int c) {
+    return HD == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+template <bool B>
+struct Flag {
+    static constexpr bool value = B;
+};
+
+template <int HD, int WORDS>
+__global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedParams pk) {
+    using Sh = PtShared<HD>;
+    constexpr uint32_t SBO_Q = Sh::SBO_Q, SBO_V = Sh::SBO_V;
+    constexpr int SLOT = PT_M * (HD + 2);
+    extern __shared__ __align__(128) unsigned char smem[];
+    Sh& sh = *reinterpret_cast<Sh*>(smem);
+    const KvView& kv = pk.view;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, wg = wid >> 2;
+    const int G = pk.group;
+
+    const PagedRun run = paged_run<PT_THREADS>(pk, [&](const KvSeq& s) -> int64_t {
+        return paged_takes(pk, s) ? kv.kv * PtTiles(s, G).all() : 0;
+    });
+    if ((int)blockIdx.x >= run.ctas) return;
+
+    if (tid == 0) {
+        for (int i = 0; i < PT_ITEMS; ++i) mbar_init(&sh.d_full[i], 1), mbar_init(&sh.d_empty[i], PT_READERS);
+        for (int i = 0; i < PT_STAGES; ++i) mbar_init(&sh.raw_full[i], 64), mbar_init(&sh.raw_empty[i], 4);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.sc_full[i], 1), mbar_init(&sh.sc_empty[i], 4);
+            mbar_init(&sh.k_full[i], 4), mbar_init(&sh.k_empty[i], 1);
+            mbar_init(&sh.v_full[i], 4), mbar_init(&sh.v_empty[i], 1);
+            mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 4);
+            mbar_init(&sh.t_full[i], 1), mbar_init(&sh.t_empty[i], 4);
+        }
+        mbar_init(&sh.q_full, 4), mbar_init(&sh.q_empty, 1), mbar_init(&sh.mg_full, 4), mbar_init(&sh.met, 4);
+        mbar_init(&sh.drained, 1);
+        sh.dead = 0;
+        fence_barrier_init();
+    }
+    if (wid == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc_smem(&sh.tmem)), "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;  // columns: scores and weights of the even and odd tiles, then their products
+
+    // A bounded wait, the same answer in every lane of the warp; false once any role's wait has given up.
+    auto wait = [&](uint64_t* bar, unsigned parity) -> bool {
+        bool got = false;
+        for (unsigned i = 0; i < PT_WAIT && !(got = mbar_try_wait(bar, parity & 1u)); ++i) {
+            if ((i & 63u) == 63u) {
+                if (*(volatile int*)&sh.dead) break;
+                if (i > 2048u) __nanosleep(32);
+            }
+        }
+        if (__all_sync(0xffffffffu, got)) return true;
+        *(volatile int*)&sh.dead = 1;
+        kv_flag(kv, Q8_KV_ERR_WAIT);
+        return false;
+    };
+    auto arrive = [&](uint64_t* bar) {  // one arrival a warp, after all its lanes
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
+    auto next_item = [&](int it, PtItem& d) -> bool {  // a reader's copy of item `it`; false: no more
+        if (!wait(&sh.d_full[it % PT_ITEMS], it / PT_ITEMS)) return false;
+        d = sh.item[it % PT_ITEMS];
+        arrive(&sh.d_empty[it % PT_ITEMS]);
+        return d.t1 > d.t0;
+    };
+
+    if (wg < 2) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        // ================ scores, weights and output sums: thread = query vector
+        const int m = 32 * (wid & 3) + lane;
+        const uint32_t lanes = (uint32_t)(32 * (wid & 3)) << 16;
+        const uint32_t s_at = tmem + lanes + 128 * wg, t_at = tmem + lanes + 256 + 128 * wg;
+        int tau = 0, merges = 0, meets = 0;
+        PtItem d;
+        bool ok = true;
+        for (int it = 0; ok && next_item(it, d); ++it) {
+            const int tiles = d.t1 - d.t0;
+            const bool valid = m < d.tokens * G;
+            const int token = m / G;
+            const int lim = !valid ? INT_MAX : d.end ? d.pos + token : -1;
+            const bool active = 32 * (wid & 3) < d.tokens * G;  // (warp-uniform)
+            float mr = -INFINITY, l = 0.f, qf = 0.f;
+            uint64_t o[HD / 2];
+#pragma unroll
+            for (int i = 0; i < HD / 2; ++i) o[i] = 0ull;
+            int mine = 0;
+            for (int x = (tau + wg) & 1; x < tiles; x += 2, ++mine) {
+                const int tl = d.t0 + x, n = (tau + x) >> 1, p0 = tl * PT_P;
+                const bool last_odd = wg == 1 && x + 2 >= tiles;
+                if (!(ok = wait(&sh.s_full[wg], n) && wait(&sh.sc_full[wg], n))) break;
+                tc_fence_after();
+                float alpha = 1.f, ce = 1.f;
+                if (active) {
+                    if (mine == 0) qf = sh.qf[it & 3][m];
+                    ce = sh.ce[wg];
+                    const unsigned groups = sh.groups[wg];
+                    const float4* ks4 = reinterpret_cast<const float4*>(sh.ks[wg]);
+                    const float4* vs4 = reinterpret_cast<const float4*>(sh.vs[wg]);
+                    const bool masked = __any_sync(0xffffffffu, lim < p0 + PT_P - 1) || groups != 0xffu;
+                    const int rel = lim - p0;
+                    auto seen = [&](int c) { return c <= rel && ((groups >> (c >> 4)) & 1u); };
+                    auto softmax = [&](auto with_mask) {
+                        constexpr bool MASK = decltype(with_mask)::value;
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t s[32];
+                            tc_ld32(s_at + 32 * c, s);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 k4 = ks4[8 * c + i];
+                                float a[4];
+                                upk2(mul2(pk2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), pk2(k4.x, k4.y)), a[0], a[1]);
+                                upk2(mul2(pk2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), pk2(k4.z, k4.w)), a[2], a[3]);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    if (MASK) a[j] = seen(32 * c + 4 * i + j) ? a[j] : -INFINITY;
+                                    mx = fmaxf(mx, a[j]);
+                                }
+                            }
+                        }
+                        // (rounded up, so that no weight exceeds 1; and a factor of 0, an invalid vector's, must not
+                        // meet the masks' infinity)
+                        const float mn = fmaxf(mr, mx == -INFINITY ? -INFINITY : __fmul_ru(mx, qf));
+                        const float ms = mn == -INFINITY ? 0.f : mn;
+                        alpha = ex2(mr - ms);
+                        mr = mn;
+                        uint64_t sum = 0ull;
+                        const uint64_t qf2 = pk2(qf, qf), nm2 = pk2(-ms, -ms);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t s[32], w[32];
+                            tc_ld32(s_at + 32 * c, s);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 k4 = ks4[8 * c + i], v4 = vs4[8 * c + i];
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const int e = 4 * i + 2 * j;
+                                    const uint64_t ks2 = j ? pk2(k4.z, k4.w) : pk2(k4.x, k4.y);
+                                    const uint64_t vs2 = j ? pk2(v4.z, v4.w) : pk2(v4.x, v4.y);
+                                    const uint64_t t2 = fma2(mul2(pk2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), ks2), qf2, nm2);
+                                    float a, b;
+                                    upk2(t2, a, b);
+                                    a = ex2(a), b = ex2(b);
+                                    if (MASK) a = seen(32 * c + e) ? a : 0.f, b = seen(32 * c + e + 1) ? b : 0.f;
+                                    const uint64_t p2 = pk2(a, b);
+                                    sum = add2(sum, p2);
+                                    uint64_t w2 = mul2(p2, vs2);
+                                    float wa, wb;
+                                    upk2(w2, wa, wb);
+                                    if (MASK) {  // (a value scale that is not a number stays behind the mask)
+                                        wa = seen(32 * c + e) ? wa : 0.f, wb = seen(32 * c + e + 1) ? wb : 0.f;
+                                        w2 = pk2(wa, wb);
+                                    }
+                                    const uint32_t hi = f16_pack(wa, wb);
+                                    const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                                    float la, lb;
+                                    upk2(add2(w2, pk2(-hf.x, -hf.y)), la, lb);
+                                    w[2 * i + j] = hi;
+                                    w[16 + 2 * i + j] = f16_pack(la, lb);
+                                }
+                            }
+                            tc_st32(s_at + 32 * c, w);
+                        }
+                        float sa, sb;
+                        upk2(sum, sa, sb);
+                        l = l * alpha + (sa + sb);
+                    };
+                    if (masked) softmax(Flag<true>());
+                    else softmax(Flag<false>());
+                    tc_wait_st();
+                }
+                tc_fence_before();
+                arrive(&sh.p_full[wg]);
+                if (lane == 0) mbar_arrive(&sh.sc_empty[wg]);
+                if (!(ok = wait(&sh.t_full[wg], n))) break;
+                tc_fence_after();
+                if (active) {
+                    const uint64_t al2 = pk2(alpha, alpha), ce2 = pk2(ce, ce);
+#pragma unroll
+                    for (int c = 0; c < HD / 32; ++c) {
+                        uint32_t r[32];
+                        tc_ld32(t_at + 32 * c, r);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            o[16 * c + i] = fma2(pk2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), ce2,
+                                                 mul2(o[16 * c + i], al2));
+                    }
+                }
+                tc_fence_before();
+                if (!last_odd) arrive(&sh.t_empty[wg]);
+            }
+            if (!ok) break;
+            const int odd = ((tau + 1) & 1) ? tiles / 2 : (tiles + 1) / 2;  // tiles of the second group
+            tau += tiles;
+            if (wg == 1) {
+                if (odd == 0) continue;
+                if (active) {  // its sums go to the first group over the last product, read by now
+#pragma unroll
+                    for (int c = 0; c < HD / 32; ++c) {
+                        uint32_t r[32];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float a, b;
+                            upk2(o[16 * c + i], a, b);
+                            r[2 * i] = __float_as_uint(a), r[2 * i + 1] = __float_as_uint(b);
+                        }
+                        tc_st32(t_at + 32 * c, r);
+                    }
+                    sh.mg_m[m] = mr;
+                    sh.mg_l[m] = l;
+                    tc_wait_st();
+                }
+                tc_fence_before();
+                arrive(&sh.mg_full);
+                continue;
+            }
+            if (odd) {
+                if (!(ok = wait(&sh.mg_full, merges++))) break;
+                tc_fence_after();
+                if (active) {
+                    const float m1 = sh.mg_m[m], mx = fmaxf(mr, m1), ms = mx == -INFINITY ? 0.f : mx;
+                    const float f0 = ex2(mr - ms), f1 = ex2(m1 - ms);
+                    l = l * f0 + sh.mg_l[m] * f1;
+                    mr = mx;
+                    const uint64_t f02 = pk2(f0, f0), f12 = pk2(f1, f1);
+#pragma unroll
+                    for (int c = 0; c < HD / 32; ++c) {
+                        uint32_t r[32];
+                        tc_ld32(t_at + 128 + 32 * c, r);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            o[16 * c + i] = fma2(pk2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f12,
+                                                 mul2(o[16 * c + i], f02));
+                    }
+                }
+                tc_fence_before();
+                arrive(&sh.t_empty[1]);
+            }
+            // ---- the item's output, or its part of it
+            const int64_t row = d.row0 + token;
+            const int head = d.head * G + (m - token * G);
+            auto write_out = [&]() {
+                if (!valid) return;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                float4* dst = reinterpret_cast<float4*>(pk.out + row * pk.out_stride + (int64_t)head * HD);
+#pragma unroll
+                for (int i = 0; i < HD / 4; ++i) {
+                    float4 v;
+                    upk2(o[2 * i], v.x, v.y), upk2(o[2 * i + 1], v.z, v.w);
+                    dst[i] = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                }
+                if (pk.lse) pk.lse[row * pk.heads + head] = l == 0.f ? -INFINITY : (mr + log2f(l)) * 0.693147180559945f;
+            };
+            if (d.t0 == 0 && d.t1 == d.units) {
+                write_out();
+                continue;
+            }
+            float* slot = pk.part + (int64_t)(2 * blockIdx.x + (d.opens ? 0 : 1)) * SLOT;
+            if (valid) {
+#pragma unroll
+                for (int i = 0; i < HD / 4; ++i) {
+                    float4 v;
+                    upk2(o[2 * i], v.x, v.y), upk2(o[2 * i + 1], v.z, v.w);
+                    __stcg(reinterpret_cast<float4*>(slot) + i * PT_M + m, v);
+                }
+                __stcg(slot + PT_M * HD + m, mr);
+                __stcg(slot + PT_M * (HD + 1) + m, l);
+            }
+            const int c0 = run.owner(d.at), c1 = run.owner(d.at + d.units - 1);
+            arrive(&sh.met);
+            if (!(ok = wait(&sh.met, meets++))) break;
+            if (tid == 0) {
+                sh.last = atomic_add_acq_rel_gpu(pk.counters + c0, 1) == c1 - c0;
+                if (sh.last) pk.counters[c0] = 0;
+            }
+            arrive(&sh.met);
+            if (!(ok = wait(&sh.met, meets++))) break;
+            if (sh.last && valid) {
+                auto slot_of = [&](int c) {
+                    return pk.part + (int64_t)(2 * c + (run.start(c) >= d.at ? 0 : 1)) * SLOT;
+                };
+                float mx = -INFINITY;
+                for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, __ldcg(slot_of(c) + PT_M * HD + m));
+                const float ms = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+                for (int i = 0; i < HD / 2; ++i) o[i] = 0ull;
+                l = 0.f;
+                for (int c = c0; c <= c1; ++c) {
+                    const float* sl = slot_of(c);
+                    const float f = ex2(__ldcg(sl + PT_M * HD + m) - ms);
+                    l += __ldcg(sl + PT_M * (HD + 1) + m) * f;
+                    const uint64_t f2 = pk2(f, f);
+#pragma unroll
+                    for (int i = 0; i < HD / 4; ++i) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(sl) + i * PT_M + m);
+                        o[2 * i] = fma2(pk2(v.x, v.y), f2, o[2 * i]);
+                        o[2 * i + 1] = fma2(pk2(v.z, v.w), f2, o[2 * i + 1]);
+                    }
+                }
+                mr = mx;
+                write_out();
+            }
+        }
+    } else if (wg == 2) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        // ================ operand tiles in f16
+        const int w = wid - 8;
+        int tau = 0, stage = 0, uses = 0;  // uses: stages taken so far
+        PtItem d;
+        bool ok = true;
+        for (int it = 0; ok && next_item(it, d); ++it) {
+            if (!(ok = wait(&sh.q_empty, it + 1))) break;
+            const int r = lane & 7, cc = lane >> 3;
+            for (int i = 0; i < 4; ++i) {  // 8 query vectors at a time, a lane HD / 32 chunks of 8 dimensions
+                const int m = 32 * w + 8 * i + r;
+                const int64_t row = d.row0 + m / G;
+                const bool valid = m < d.tokens * G;
+                const float* src = pk.q + (valid ? row * pk.q_stride + (int64_t)(d.head * G + m % G) * HD : 0);
+                float x[HD / 32][8];
+                unsigned big = 0u;
+#pragma unroll
+                for (int c = 0; c < HD / 32; ++c) {
+                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+                    if (valid) {
+                        a = *reinterpret_cast<const float4*>(src + 8 * (cc + 4 * c));
+                        b = *reinterpret_cast<const float4*>(src + 8 * (cc + 4 * c) + 4);
+                    }
+                    x[c][0] = a.x, x[c][1] = a.y, x[c][2] = a.z, x[c][3] = a.w;
+                    x[c][4] = b.x, x[c][5] = b.y, x[c][6] = b.z, x[c][7] = b.w;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) big = max(big, __float_as_uint(fabsf(x[c][j])));
+                }
+                big = max(big, __shfl_xor_sync(0xffffffffu, big, 8));
+                big = max(big, __shfl_xor_sync(0xffffffffu, big, 16));
+                const int e = big == 0u ? 0 : 14 - exponent_of(big);
+                const float f = pow2i(e);
+                if (cc == 0) sh.qf[it & 3][m] = valid ? pow2i(-e) * pk.scale : 0.f;
+#pragma unroll
+                for (int c = 0; c < HD / 32; ++c) {
+                    uint32_t h[4], lo[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float a = x[c][2 * j] * f, b = x[c][2 * j + 1] * f;
+                        h[j] = f16_pack(a, b);
+                        const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+                        lo[j] = f16_pack(a - hf.x, b - hf.y);
+                    }
+                    const uint32_t off = (uint32_t)(m >> 3) * SBO_Q + (uint32_t)(cc + 4 * c) * 128 + (uint32_t)(m & 7) * 16;
+                    *reinterpret_cast<uint4*>(sh.qh + off) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4*>(sh.ql + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+            }
+            fence_async();
+            arrive(&sh.q_full);
+            for (int x = 0; ok && x < d.t1 - d.t0; ++x, ++tau) {
+                const int b = tau & 1, n = tau >> 1;
+                // keys: rows as they are; a lane 16 dimensions (one 16-byte chunk of words) of a position
+                if (!(ok = wait(&sh.k_empty[b], n + 1))) break;
+                for (int half = 0; half < 2; ++half) {
+                    if (!(ok = wait(&sh.raw_full[stage], uses / PT_STAGES))) break;
+                    const unsigned char* src = sh.raw[stage];
+#pragma unroll
+                    for (int i = 0; i < HD / 32; ++i) {  // (HD / 16 chunks) x 8 groups of 8 rows, 4 warps x 4 chunks at a time
+                        const int task = i * 4 + w;
+                        const int c = (lane >> 3) + 4 * (task & (HD / 64 - 1)), p = 8 * (task / (HD / 64)) + (lane & 7);
+                        const uint4 u = *reinterpret_cast<const uint4*>(src + raw_off<HD>(p, c));
+                        const uint32_t in[4] = {words_flip<WORDS>(u.x), words_flip<WORDS>(u.y), words_flip<WORDS>(u.z), words_flip<WORDS>(u.w)};
+                        uint32_t h[8];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) h[2 * j] = words2_f16<WORDS, 0>(in[j]), h[2 * j + 1] = words2_f16<WORDS, 1>(in[j]);
+                        const int pp = PT_HALF * half + p;
+                        unsigned char* dst = sh.k[b] + (uint32_t)(pp >> 3) * SBO_Q + (uint32_t)c * 256 + (uint32_t)(pp & 7) * 16;
+                        *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4*>(dst + 128) = make_uint4(h[4], h[5], h[6], h[7]);
+                    }
+                    arrive(&sh.raw_empty[stage]);
+                    stage = stage + 1 == PT_STAGES ? 0 : stage + 1;
+                    ++uses;
+                }
+                if (!ok) break;
+                fence_async();
+                arrive(&sh.k_full[b]);
+                // values: transposed; a lane 4 dimensions of 8 positions
+                if (!(ok = wait(&sh.v_empty[b], n + 1))) break;
+                for (int half = 0; half < 2; ++half) {
+                    if (!(ok = wait(&sh.raw_full[stage], uses / PT_STAGES))) break;
+                    const unsigned char* src = sh.raw[stage];
+#pragma unroll
+                    for (int i = 0; i < HD / 64; ++i) {
+                        const int task = (i * 128 + 32 * w + lane);
+                        const int d4 = task % (HD / 4), p8 = task / (HD / 4);  // of 8 groups of 8 positions
+                        uint32_t in[8], h[4][4];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            in[j] = *reinterpret_cast<const uint32_t*>(src + raw_off<HD>(8 * p8 + j, d4 >> 2) + 4 * (d4 & 3));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t a = words_flip<WORDS>(__byte_perm(in[2 * j], in[2 * j + 1], 0x5140));
+                            const uint32_t c = words_flip<WORDS>(__byte_perm(in[2 * j], in[2 * j + 1], 0x7362));
+                            h[0][j] = words2_f16<WORDS, 0>(a), h[1][j] = words2_f16<WORDS, 1>(a);
+                            h[2][j] = words2_f16<WORDS, 0>(c), h[3][j] = words2_f16<WORDS, 1>(c);
+                        }
+                        unsigned char* dst = sh.v[b] + (uint32_t)(d4 >> 1) * SBO_V + (uint32_t)(p8 + 8 * half) * 128 + (uint32_t)(d4 & 1) * 64;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<uint4*>(dst + 16 * j) = make_uint4(h[j][0], h[j][1], h[j][2], h[j][3]);
+                    }
+                    arrive(&sh.raw_empty[stage]);
+                    stage = stage + 1 == PT_STAGES ? 0 : stage + 1;
+                    ++uses;
+                }
+                if (!ok) break;
+                fence_async();
+                arrive(&sh.v_full[b]);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        PtItem d;
+        bool ok = true;
+        if (wid == 12) {
+            // ================ the products
+            const uint32_t id_s = tc_idesc_f16(PT_M, PT_P), id_o = tc_idesc_f16(PT_M, HD);
+            auto weigh = [&](int tau) -> bool {  // the second product of tile tau
+                const int b = tau & 1, n = tau >> 1;
+                if (!wait(&sh.p_full[b], n) || !wait(&sh.v_full[b], n) || !wait(&sh.t_empty[b], n + 1)) return false;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t p_at = tmem + 128 * b, t_at = tmem + 256 + 128 * b;
+                    const uint64_t dv = tc_desc(sh.v[b], SBO_V);
+#pragma unroll
+                    for (int part = 1; part >= 0; --part)  // the small parts first
+#pragma unroll
+                        for (int j = 0; j < PT_P / 16; ++j)  // 16 positions: 8 columns of weights, two core matrices
+                            tc_mma_f16_ta(t_at, p_at + 32 * (j >> 1) + 8 * (j & 1) + 16 * part, dv + j * (256 >> 4), id_o,
+                                          part == 1 && j == 0 ? 0u : 1u);
+                    tc_commit(&sh.t_full[b]);
+                    tc_commit(&sh.v_empty[b]);
+                }
+                __syncwarp();
+                return true;
+            };
+            int tau = 0;
+            bool pending = false;  // whether tile tau - 1's second product is still to be issued
+            for (int it = 0; ok && next_item(it, d); ++it) {
+                if (pending) {
+                    if (!(ok = weigh(tau - 1))) break;
+                    pending = false;
+                }
+                if (!(ok = wait(&sh.q_full, it))) break;
+                for (int x = 0; x < d.t1 - d.t0; ++x, ++tau) {
+                    const int b = tau & 1, n = tau >> 1;
+                    // the scores overwrite tile tau - 2's weights: its second product has to be done
+                    if (!(ok = wait(&sh.k_full[b], n) && wait(&sh.t_full[b], n + 1))) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint64_t dh = tc_desc(sh.qh, SBO_Q), dl = tc_desc(sh.ql, SBO_Q), dk = tc_desc(sh.k[b], SBO_Q);
+#pragma unroll
+                        for (int part = 1; part >= 0; --part)
+#pragma unroll
+                            for (int j = 0; j < HD / 16; ++j)
+                                tc_mma_f16(tmem + 128 * b, (part ? dl : dh) + j * (256 >> 4), dk + j * (256 >> 4), id_s,
+                                           part == 1 && j == 0 ? 0u : 1u);
+                        tc_commit(&sh.s_full[b]);
+                        tc_commit(&sh.k_empty[b]);
+                        if (x + 1 == d.t1 - d.t0) tc_commit(&sh.q_empty);
+                    }
+                    __syncwarp();
+                    if (pending && !(ok = weigh(tau - 1))) break;
+                    pending = true;
+                }
+            }
+            if (ok && pending) weigh(tau - 1);
+            if (lane == 0) tc_commit(&sh.drained);  // nothing is in flight when the CTA gives its tensor memory back
+            for (unsigned i = 0; i < PT_WAIT && !mbar_try_wait(&sh.drained, 0); ++i)
+                if (i > 2048u) __nanosleep(32);
+        } else if (wid < 15) {
+            // ================ copies of the words
+            constexpr int CH = HD / 16, ROWS = 64 / CH;  // 16-byte chunks a row, rows a pass of the two warps
+            const int c = (wid - 13) * 32 + lane, chunk = c % CH, r0 = c / CH;
+            int stage = 0, uses = 0;
+            for (int it = 0; ok && next_item(it, d); ++it) {
+                for (int tl = d.t0; ok && tl < d.t1; ++tl) {
+                    int page[2][PT_HALF / ROWS];
+#pragma unroll
+                    for (int i = 0; i < 2 * PT_HALF / ROWS; ++i) {
+                        const int p = tl * PT_P + i * ROWS + r0;
+                        int& pg = page[i / (PT_HALF / ROWS)][i % (PT_HALF / ROWS)];
+                        pg = -1;
+                        if (p < d.end) {
+                            pg = kv_page(kv, d.seq, p);
+                            if (pg < 0) kv_flag(kv, Q8_KV_ERR_PAGE);
+                        }
+                    }
+#pragma unroll
+                    for (int part = 0; part < 4; ++part) {  // the keys' halves, then the values'
+                        const int half = part & 1;
+                        const int8_t* from = part < 2 ? kv.k : kv.v;
+                        if (!(ok = wait(&sh.raw_empty[stage], uses / PT_STAGES + 1))) break;
+#pragma unroll
+                        for (int i = 0; i < PT_HALF / ROWS; ++i) {
+                            const int r = i * ROWS + r0, pg = page[half][i];
+                            const int64_t row = kv_row(kv, max(pg, 0), d.head, tl * PT_P + half * PT_HALF + r);
+                            async_copy16(sh.raw[stage] + raw_off<HD>(r, chunk), from + row * HD + 16 * chunk, pg >= 0);
+                        }
+                        async_arrive(&sh.raw_full[stage]);
+                        stage = stage + 1 == PT_STAGES ? 0 : stage + 1;
+                        ++uses;
+                    }
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        } else {
+            // ================ items and scales
+            int b = run.seq;
+            int64_t b_at = run.seq_at, i = 0, h = 0, cur = run.lo;
+            bool found = false;
+            int tau = 0, it = 0;
+            for (; ok; ++it) {
+                PtItem& e = sh.item[it % PT_ITEMS];
+                if (!(ok = wait(&sh.d_empty[it % PT_ITEMS], it / PT_ITEMS + 1))) break;
+                const bool more = cur < run.hi;
+                if (more) {
+                    KvSeq s = kv_seq(kv, b);
+                    if (!found) {  // the run's first item: the head and the tile of unit run.lo
+                        const PtTiles t(s, G);
+                        const int64_t all = t.all();
+                        h = (cur - b_at) / all;
+                        b_at += h * all;  // from here on the first unit of the head
+                        int64_t lo = 0, hi = t.count - 1;
+                        while (lo < hi) {
+                            const int64_t mid = (lo + hi + 1) / 2;
+                            if (t.before(mid) <= cur - b_at) lo = mid;
+                            else hi = mid - 1;
+                        }
+                        i = lo;
+                        b_at += t.before(i);  // and of the item
+                        found = true;
+                    }
+                    const PtTiles t(s, G);
+                    const int64_t U = t.units(i), u0 = cur - b_at;
+                    d.at = b_at;
+                    d.units = U;
+                    d.row0 = s.first + i * t.per;
+                    d.seq = b;
+                    d.head = (int)h;
+                    d.tokens = (int)min(t.per, t.n - i * t.per);
+                    d.pos = (int)(t.base + i * t.per);
+                    d.end = t.len;
+                    d.t0 = (int)u0;
+                    d.t1 = (int)min(U, u0 + (run.hi - cur));
+                    d.opens = cur == run.lo;
+                    cur += d.t1 - d.t0;
+                    if (d.t1 == U) {  // on to the next item: the next tile, head or sequence
+                        b_at += U;
+                        if (++i == t.count) {
+                            i = 0;
+                            if (++h == kv.kv) {
+                                h = 0;
+                                ++b;
+                                while (cur < run.hi && !paged_takes(pk, kv_seq(kv, b))) ++b;
+                            }
+                        }
+                    }
+                } else {
+                    d.t0 = d.t1 = 0;
+                }
+                if (lane == 0) e = d;
+                arrive(&sh.d_full[it % PT_ITEMS]);
+                if (!more) break;
+                for (int tl = d.t0; tl < d.t1; ++tl, ++tau) {
+                    const int bf = tau & 1, p = tl * PT_P + 4 * lane;
+                    float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f), v4 = k4;
+                    const int pg = p < d.end ? kv_page(kv, d.seq, p) : -1;
+                    if (pg >= 0) {
+                        const int64_t row = kv_row(kv, pg, d.head, p);
+                        k4 = *reinterpret_cast<const float4*>(kv.ks + row);
+                        v4 = *reinterpret_cast<const float4*>(kv.vs + row);
+                        if (p + 1 >= d.end) k4.y = v4.y = 0.f;
+                        if (p + 2 >= d.end) k4.z = v4.z = 0.f;
+                        if (p + 3 >= d.end) k4.w = v4.w = 0.f;
+                    }
+                    const unsigned ballot = __ballot_sync(0xffffffffu, pg >= 0);
+                    unsigned groups = 0u;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) groups |= ((ballot >> (4 * j)) & 1u) << j;
+                    const unsigned top = __reduce_max_sync(
+                        0xffffffffu, max(max(__float_as_uint(fabsf(v4.x)), __float_as_uint(fabsf(v4.y))),
+                                         max(__float_as_uint(fabsf(v4.z)), __float_as_uint(fabsf(v4.w)))));
+                    const int ex = top == 0u ? 0 : exponent_of(top);
+                    const float f = pow2i(PT_PEXP - ex);
+                    if (!(ok = wait(&sh.sc_empty[bf], (tau >> 1) + 1))) break;
+                    reinterpret_cast<float4*>(sh.ks[bf])[lane] = k4;
+                    reinterpret_cast<float4*>(sh.vs[bf])[lane] = make_float4(v4.x * f, v4.y * f, v4.z * f, v4.w * f);
+                    if (lane == 0) sh.ce[bf] = pow2i(ex - PT_PEXP), sh.groups[bf] = groups;
+                    arrive(&sh.sc_full[bf]);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (wid == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
+template <int HD, int WORDS>
+cudaError_t tiles_launch(const PagedParams& p, cudaStream_t st) {
+    auto kernel = paged_tiles_kernel<HD, WORDS>;
+    constexpr size_t smem = sizeof(PtShared<HD>);
+    static_assert(smem + 2048 <= 232448, "dynamic plus static shared memory within the 227 KB a CTA may hold");
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<device_info().sms, PT_THREADS, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t paged_tiles_slot(int hd) { return (size_t)PT_M * (hd + 2) * sizeof(float); }
+
+cudaError_t launch_paged_tiles(const PagedParams& p, int hd, int words, cudaStream_t st) {
+    if (hd == 128) return words == Q8_KV_INT8 ? tiles_launch<128, Q8_KV_INT8>(p, st) : tiles_launch<128, Q8_KV_E4M3>(p, st);
+    return words == Q8_KV_INT8 ? tiles_launch<64, Q8_KV_INT8>(p, st) : tiles_launch<64, Q8_KV_E4M3>(p, st);
+}
+
+}  // namespace q8
