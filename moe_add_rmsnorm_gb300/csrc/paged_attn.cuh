@@ -56,6 +56,7 @@ __device__ __forceinline__ PagedRun paged_run(const PagedParams& pk, Units units
     const int each = (kv.seqs + THREADS - 1) / THREADS;
     const int b0 = min(kv.seqs, t * each), b1 = min(kv.seqs, b0 + each);
     int64_t sum = 0;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
         const KvSeq s = kv_seq(kv, b);
         if (blockIdx.x == 0 && (!s.rows_ok || (s.n > 0 && !s.len_ok))) kv_flag(kv, Q8_KV_ERR_LENGTH);
@@ -71,6 +72,7 @@ __device__ __forceinline__ PagedRun paged_run(const PagedParams& pk, Units units
     if (t == 0) found = 0, found_at = 0;
     __syncthreads();
     int64_t before = 0, total = 0;
+#pragma unroll 1
     for (int i = 0; i < THREADS / 32; ++i) {
         if (i < w) before += warp_sum[i];
         total += warp_sum[i];
@@ -83,6 +85,7 @@ __device__ __forceinline__ PagedRun paged_run(const PagedParams& pk, Units units
         r.hi = r.start(blockIdx.x + 1);
         int64_t at = before + pre - sum;
         if (at <= r.lo && r.lo < at + sum) {
+#pragma unroll 1
             for (int b = b0; b < b1; ++b) {
                 const int64_t n = units(kv_seq(kv, b));
                 if (r.lo < at + n) {

@@ -9,15 +9,16 @@
 // so each is two tensor-core products (4 x 128 x 128 x hd multiply-adds a tile pair, twice the formula's): those bound it.
 // One CTA an SM works through an equal run of tile pairs; its warps divide the work and meet only at barriers in shared
 // memory:
-//  - warps 0-3 and 4-7 (a thread a query vector) take the odd and the even tiles of positions: scores out of tensor
-//    memory, maximum, weights, and the weights' parts back into tensor memory over the scores, where the second product
-//    reads them as its first operand.  While one group does so the tensor cores work for the other.  Each group keeps
-//    its own maximum, sum and f32 output sums in registers (a tile's product is added, rounded, to them: the tensor
-//    cores truncate as they accumulate); the two meet at an item's end.
+//  - warps 0-3 and 4-7 (a thread half a query vector: one group the first, the other the last 64 positions of a tile)
+//    take the scores out of tensor memory once, trade maxima, and put the weights' parts back over the scores, where the
+//    second product reads them as its first operand; then they add the product of the tile before (rounded: the tensor
+//    cores truncate as they accumulate) to f32 sums in registers, half the dimensions each, while the tensor cores work
+//    on this tile's second and the next one's first product.
 //  - warps 8-11 turn the words into f16 operand tiles (the values transposed), and an item's queries into their parts.
-//  - warp 12 issues the products, warps 13 and 14 copy the words of 64 positions at a time from the pages into a ring
-//    (asynchronously, zeros for positions past the end), warp 15 deals out the items and prepares the scales.
+//  - warp 12 issues the products, warp 13 copies the words of 64 positions at a time from the pages into a ring (tensor
+//    copies of 16 rows, zeros for pages out of range), warp 15 deals out the items and prepares the scales.
 // Registers are moved from the last eight warps to the first eight (200 and 56 a thread).
+#include <cuda.h>
 #include <cuda_fp16.h>
 
 #include "paged_attn.cuh"
@@ -33,8 +34,9 @@ constexpr int PT_THREADS = 512;
 constexpr int PT_HALF = 64;                // positions a copied stage
 constexpr int PT_STAGES = 3;
 constexpr int PT_ITEMS = 4;                // items dealt out ahead
-constexpr int PT_READERS = 15;             // warps that read an item
-constexpr unsigned PT_WAIT = 1u << 18;      // polls before a wait gives up
+constexpr int PT_READERS = 14;             // warps that read an item
+constexpr unsigned PT_WAIT = 1u << 13;      // polls before a wait gives up, each up to PT_POLL_NS long
+constexpr unsigned PT_POLL_NS = 20000;
 constexpr int PT_PEXP = 14;                // weights are split as values of up to 2^(PT_PEXP + 1)
 
 // One item's piece as the roles read it.
@@ -52,23 +54,34 @@ template <int HD>
 struct PtShared {
     static constexpr uint32_t SBO_Q = HD / 8 * 128;        // bytes between 8-row groups of queries and keys
     static constexpr uint32_t SBO_V = PT_P / 8 * 128 + 16; // and of transposed values (the pad spreads the writes' banks)
+    unsigned char raw[PT_STAGES][PT_HALF * HD];
     unsigned char qh[PT_M * HD * 2], ql[PT_M * HD * 2];
     unsigned char k[2][PT_P * HD * 2];
     unsigned char v[2][HD / 8 * SBO_V];
-    unsigned char raw[PT_STAGES][PT_HALF * HD];
     float ks[2][PT_P], vs[2][PT_P];
     float qf[4][PT_M];
-    float mg_m[PT_M], mg_l[PT_M];
+    float trade[2][2][PT_M];
     float ce[2];
     unsigned groups[2];    // which 16-position groups of a tile are there
     PtItem item[PT_ITEMS];
     uint64_t d_full[PT_ITEMS], d_empty[PT_ITEMS], raw_full[PT_STAGES], raw_empty[PT_STAGES];
     uint64_t sc_full[2], sc_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t s_full[2], p_full[2], t_full[2], t_empty[2], q_full, q_empty, mg_full, met, drained;
+    uint64_t s_full[2], p_full[2], t_full[2], t_empty[2], q_full, q_empty, pair[4], met, drained;
     uint32_t tmem;
     int dead;              // a wait gave up: every role leaves
     int last;
 };
+
+// One poll of a barrier's phase; the hardware may hold the warp for up to PT_POLL_NS, issuing nothing meanwhile (polls
+// that return at once took about half of the SM's issue slots).
+__device__ __forceinline__ bool try_wait(uint64_t* bar, unsigned parity) {
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok)
+                 : "r"(smem_addr(bar)), "r"(parity), "r"(PT_POLL_NS)
+                 : "memory");
+    return ok != 0;
+}
 
 __device__ __forceinline__ uint64_t pk2(float a, float b) {
     uint64_t r;
@@ -98,33 +111,51 @@ __device__ __forceinline__ void tc_mma_f16_ta(uint32_t d, uint32_t a, uint64_t b
                  ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc));
 }
 
-// 32 columns of this warp's 32 lanes written; complete after tc_wait_st().
-__device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-          "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
-          "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
+// 16 columns of this warp's 32 lanes, one 32-bit value each: issued by tc_ld16, there after tc_wait16 on the same
+// registers (which keeps their use behind the wait), and written by tc_st16 (complete after tc_wait_st).
+__device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tc_wait16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                   "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+// N columns (a multiple of 32) from taddr into r, all of them asked for before the wait.
+template <int N>
+__device__ __forceinline__ void tc_load(uint32_t taddr, uint32_t (&r)[N]) {
+    uint32_t(&x)[N / 16][16] = reinterpret_cast<uint32_t(&)[N / 16][16]>(r);
+#pragma unroll
+    for (int i = 0; i < N / 16; ++i) tc_ld16(taddr + 16 * i, x[i]);
+#pragma unroll
+    for (int i = 0; i < N / 16; ++i) tc_wait16(x[i]);
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// 16 bytes from global into shared memory (zeros where !there), counted by async_arrive.
-__device__ __forceinline__ void async_copy16(void* dst, const void* src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-// This thread arrives on bar when the copies it issued so far are complete.
-__device__ __forceinline__ void async_arrive(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+// A tensor copy of one page's 16 rows from `row` of its [heads * page_size] rows into shared memory (zeros for a page out
+// of range), counted on bar's transaction bytes.
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int row, int page, uint64_t* bar) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                 ::"r"(smem_addr(dst)), "l"(map), "r"(0), "r"(row), "r"(page), "r"(smem_addr(bar))
+                 : "memory");
 }
 
 // sum_{i<n} floor((a i + b) / m), n, a, b >= 0, m > 0 (Euclid's steps on (a, m)).
-__device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+__device__ __noinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
     int64_t sum = 0;
     while (n > 0) {
         sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
@@ -190,8 +221,8 @@ __device__ __forceinline__ uint32_t words_flip(uint32_t w) {
     return WORDS == Q8_KV_INT8 ? w ^ 0x80808080u : w;
 }
 
-// Byte offset of 16-byte chunk c of row r in a copied stage: chunks are permuted within 128 bytes so that eight rows'
-// equal chunks lie in different banks.
+// Byte offset of 16-byte chunk c of row r in a copied stage, as the tensor copies' 128- or 64-byte swizzle places it:
+// eight rows' equal chunks lie in different banks.
 template <int HD>
 __device__ __forceinline__ uint32_t raw_off(int r, int c) {
     return HD == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
@@ -203,12 +234,13 @@ struct Flag {
 };
 
 template <int HD, int WORDS>
-__global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedParams pk) {
+__global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedParams pk, const __grid_constant__ CUtensorMap map_k,
+                                                                   const __grid_constant__ CUtensorMap map_v) {
     using Sh = PtShared<HD>;
     constexpr uint32_t SBO_Q = Sh::SBO_Q, SBO_V = Sh::SBO_V;
     constexpr int SLOT = PT_M * (HD + 2);
-    extern __shared__ __align__(128) unsigned char smem[];
-    Sh& sh = *reinterpret_cast<Sh*>(smem);
+    extern __shared__ unsigned char smem[];
+    Sh& sh = *reinterpret_cast<Sh*>(smem + (1024u - smem_addr(smem) % 1024u) % 1024u);  // (the swizzle goes by the address)
     const KvView& kv = pk.view;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, wg = wid >> 2;
     const int G = pk.group;
@@ -220,15 +252,16 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
 
     if (tid == 0) {
         for (int i = 0; i < PT_ITEMS; ++i) mbar_init(&sh.d_full[i], 1), mbar_init(&sh.d_empty[i], PT_READERS);
-        for (int i = 0; i < PT_STAGES; ++i) mbar_init(&sh.raw_full[i], 64), mbar_init(&sh.raw_empty[i], 4);
+        for (int i = 0; i < PT_STAGES; ++i) mbar_init(&sh.raw_full[i], 1), mbar_init(&sh.raw_empty[i], 4);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.sc_full[i], 1), mbar_init(&sh.sc_empty[i], 4);
+            mbar_init(&sh.sc_full[i], 1), mbar_init(&sh.sc_empty[i], 8);
             mbar_init(&sh.k_full[i], 4), mbar_init(&sh.k_empty[i], 1);
             mbar_init(&sh.v_full[i], 4), mbar_init(&sh.v_empty[i], 1);
-            mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 4);
-            mbar_init(&sh.t_full[i], 1), mbar_init(&sh.t_empty[i], 4);
+            mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 8);
+            mbar_init(&sh.t_full[i], 1), mbar_init(&sh.t_empty[i], 8);
         }
-        mbar_init(&sh.q_full, 4), mbar_init(&sh.q_empty, 1), mbar_init(&sh.mg_full, 4), mbar_init(&sh.met, 4);
+        mbar_init(&sh.q_full, 4), mbar_init(&sh.q_empty, 1), mbar_init(&sh.met, 8);
+        for (int i = 0; i < 4; ++i) mbar_init(&sh.pair[i], 2);
         mbar_init(&sh.drained, 1);
         sh.dead = 0;
         fence_barrier_init();
@@ -245,12 +278,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
     // A bounded wait, the same answer in every lane of the warp; false once any role's wait has given up.
     auto wait = [&](uint64_t* bar, unsigned parity) -> bool {
         bool got = false;
-        for (unsigned i = 0; i < PT_WAIT && !(got = mbar_try_wait(bar, parity & 1u)); ++i) {
-            if ((i & 63u) == 63u) {
-                if (*(volatile int*)&sh.dead) break;
-                if (i > 2048u) __nanosleep(32);
-            }
-        }
+#pragma unroll 1
+        for (unsigned i = 0; i < PT_WAIT && !(got = try_wait(bar, parity & 1u)); ++i)
+            if (*(volatile int*)&sh.dead) break;
         if (__all_sync(0xffffffffu, got)) return true;
         *(volatile int*)&sh.dead = 1;
         kv_flag(kv, Q8_KV_ERR_WAIT);
@@ -269,246 +299,225 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
 
     if (wg < 2) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        // ================ scores, weights and output sums: thread = query vector
-        const int m = 32 * (wid & 3) + lane;
-        const uint32_t lanes = (uint32_t)(32 * (wid & 3)) << 16;
-        const uint32_t s_at = tmem + lanes + 128 * wg, t_at = tmem + lanes + 256 + 128 * wg;
-        int tau = 0, merges = 0, meets = 0;
+        // ================ scores, weights and output sums: thread = half of a query vector's positions and dimensions
+        constexpr int HP = PT_P / 2, HV = HD / 2;
+        const int quarter = wid & 3, m = 32 * quarter + lane;
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+        int tau = 0, pairs = 0, meets = 0;
         PtItem d;
         bool ok = true;
+        // This row's value of the thread that holds its other half (the two warps of a quarter trade one a lane).
+        auto trade = [&](float mine, float& other) -> bool {
+            float(&x)[2][PT_M] = sh.trade[pairs & 1];
+            x[wg][m] = mine;
+            arrive(&sh.pair[quarter]);
+            if (!wait(&sh.pair[quarter], pairs++)) return false;
+            other = x[wg ^ 1][m];
+            return true;
+        };
+#pragma unroll 1
         for (int it = 0; ok && next_item(it, d); ++it) {
-            const int tiles = d.t1 - d.t0;
             const bool valid = m < d.tokens * G;
             const int token = m / G;
             const int lim = !valid ? INT_MAX : d.end ? d.pos + token : -1;
-            const bool active = 32 * (wid & 3) < d.tokens * G;  // (warp-uniform)
-            float mr = -INFINITY, l = 0.f, qf = 0.f;
-            uint64_t o[HD / 2];
+            const bool active = 32 * quarter < d.tokens * G;  // (uniform in both warps of the quarter)
+            float mr = -INFINITY, l = 0.f, qf = 0.f, alpha = 1.f, ce = 1.f;
+            uint64_t o[HV / 2];
 #pragma unroll
-            for (int i = 0; i < HD / 2; ++i) o[i] = 0ull;
-            int mine = 0;
-            for (int x = (tau + wg) & 1; x < tiles; x += 2, ++mine) {
-                const int tl = d.t0 + x, n = (tau + x) >> 1, p0 = tl * PT_P;
-                const bool last_odd = wg == 1 && x + 2 >= tiles;
-                if (!(ok = wait(&sh.s_full[wg], n) && wait(&sh.sc_full[wg], n))) break;
+            for (int i = 0; i < HV / 2; ++i) o[i] = 0ull;
+            auto fold = [&](int t) -> bool {  // adds tile t's product, whose alpha and ce are at hand
+                if (!wait(&sh.t_full[t & 1], t >> 1)) return false;
                 tc_fence_after();
-                float alpha = 1.f, ce = 1.f;
                 if (active) {
-                    if (mine == 0) qf = sh.qf[it & 3][m];
-                    ce = sh.ce[wg];
-                    const unsigned groups = sh.groups[wg];
-                    const float4* ks4 = reinterpret_cast<const float4*>(sh.ks[wg]);
-                    const float4* vs4 = reinterpret_cast<const float4*>(sh.vs[wg]);
-                    const bool masked = __any_sync(0xffffffffu, lim < p0 + PT_P - 1) || groups != 0xffu;
-                    const int rel = lim - p0;
-                    auto seen = [&](int c) { return c <= rel && ((groups >> (c >> 4)) & 1u); };
-                    auto softmax = [&](auto with_mask) {
+                    const uint64_t al2 = pk2(alpha, alpha), ce2 = pk2(ce, ce);
+                    uint32_t r[HV];
+                    tc_load<HV>(tmem + lanes + 256 + 128 * (t & 1) + HV * wg, r);
+                    if (!__all_sync(0xffffffffu, alpha == 1.f)) {  // (a maximum moved)
+#pragma unroll
+                        for (int i = 0; i < HV / 2; ++i) o[i] = mul2(o[i], al2);
+                    }
+#pragma unroll
+                    for (int i = 0; i < HV / 2; ++i)
+                        o[i] = fma2(pk2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), ce2, o[i]);
+                }
+                tc_fence_before();
+                arrive(&sh.t_empty[t & 1]);
+                return true;
+            };
+            const int first = tau;
+#pragma unroll 1
+            for (int tl = d.t0; tl < d.t1; ++tl, ++tau) {
+                const int b = tau & 1, n = tau >> 1, p0 = tl * PT_P + HP * wg;
+                const uint32_t s_at = tmem + lanes + 128 * b + HP * wg;
+                if (!(ok = wait(&sh.s_full[b], n) && wait(&sh.sc_full[b], n))) break;
+                tc_fence_after();
+                float alpha_new = 1.f, ce_new = 1.f;
+                if (active) {
+                    if (tau == first) qf = sh.qf[it & 3][m];
+                    ce_new = sh.ce[b];
+                    const unsigned groups = sh.groups[b] >> (4 * wg) & 15u;
+                    const float4* ks4 = reinterpret_cast<const float4*>(sh.ks[b] + HP * wg);
+                    const float4* vs4 = reinterpret_cast<const float4*>(sh.vs[b] + HP * wg);
+                    const bool masked = __any_sync(0xffffffffu, lim < p0 + HP - 1) || groups != 15u;
+                    uint32_t s[HP];
+                    tc_load<HP>(s_at, s);
+                    // scores without the query's factor, which is positive; what is masked is -infinity
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < HP / 4; ++i) {
+                        const float4 k4 = ks4[i];
+                        float a[4];
+                        upk2(mul2(pk2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), pk2(k4.x, k4.y)), a[0], a[1]);
+                        upk2(mul2(pk2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), pk2(k4.z, k4.w)), a[2], a[3]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s[4 * i + j] = __float_as_uint(a[j]);
+                    }
+                    uint64_t seen = ~0ull;
+                    if (masked) {
+                        const int count = lim - p0 + 1;  // positions of this half that the row attends
+                        seen = count >= HP ? ~0ull : count <= 0 ? 0ull : (1ull << count) - 1;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (!((groups >> j) & 1u)) seen &= ~(0xffffull << (16 * j));
+#pragma unroll
+                        for (int i = 0; i < HP; ++i)
+                            if (!((seen >> i) & 1ull)) s[i] = 0xff800000u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < HP; i += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
+                    float other;
+                    if (!(ok = trade(mx, other))) break;
+                    mx = fmaxf(mx, other);
+                    // (rounded up, so that no weight exceeds 1; and a factor of 0, an invalid vector's, must not meet the
+                    // masks' infinity)
+                    const float mn = fmaxf(mr, mx == -INFINITY ? -INFINITY : __fmul_ru(mx, qf));
+                    const float ms = mn == -INFINITY ? 0.f : mn;
+                    alpha_new = ex2(mr - ms);
+                    mr = mn;
+                    uint64_t sum = 0ull;
+                    const uint64_t qf2 = pk2(qf, qf), nm2 = pk2(-ms, -ms);
+                    auto weights = [&](auto with_mask) {
                         constexpr bool MASK = decltype(with_mask)::value;
-                        float mx = -INFINITY;
+                        const uint64_t less = pk2(-1.f, -1.f);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t s[32];
-                            tc_ld32(s_at + 32 * c, s);
-                            tc_wait_ld();
+                        for (int c = 0; c < HP / 16; ++c) {
+                            uint32_t w[16];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 k4 = ks4[8 * c + i];
-                                float a[4];
-                                upk2(mul2(pk2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), pk2(k4.x, k4.y)), a[0], a[1]);
-                                upk2(mul2(pk2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), pk2(k4.z, k4.w)), a[2], a[3]);
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    if (MASK) a[j] = seen(32 * c + 4 * i + j) ? a[j] : -INFINITY;
-                                    mx = fmaxf(mx, a[j]);
-                                }
-                            }
-                        }
-                        // (rounded up, so that no weight exceeds 1; and a factor of 0, an invalid vector's, must not
-                        // meet the masks' infinity)
-                        const float mn = fmaxf(mr, mx == -INFINITY ? -INFINITY : __fmul_ru(mx, qf));
-                        const float ms = mn == -INFINITY ? 0.f : mn;
-                        alpha = ex2(mr - ms);
-                        mr = mn;
-                        uint64_t sum = 0ull;
-                        const uint64_t qf2 = pk2(qf, qf), nm2 = pk2(-ms, -ms);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t s[32], w[32];
-                            tc_ld32(s_at + 32 * c, s);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 k4 = ks4[8 * c + i], v4 = vs4[8 * c + i];
+                            for (int i = 0; i < 4; ++i) {
+                                const float4 v4 = vs4[4 * c + i];
 #pragma unroll
                                 for (int j = 0; j < 2; ++j) {
-                                    const int e = 4 * i + 2 * j;
-                                    const uint64_t ks2 = j ? pk2(k4.z, k4.w) : pk2(k4.x, k4.y);
-                                    const uint64_t vs2 = j ? pk2(v4.z, v4.w) : pk2(v4.x, v4.y);
-                                    const uint64_t t2 = fma2(mul2(pk2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), ks2), qf2, nm2);
+                                    const int e = 4 * i + 2 * j, x = 16 * c + e;
                                     float a, b;
-                                    upk2(t2, a, b);
-                                    a = ex2(a), b = ex2(b);
-                                    if (MASK) a = seen(32 * c + e) ? a : 0.f, b = seen(32 * c + e + 1) ? b : 0.f;
-                                    const uint64_t p2 = pk2(a, b);
+                                    upk2(fma2(pk2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), qf2, nm2), a, b);
+                                    const uint64_t p2 = pk2(ex2(a), ex2(b));
                                     sum = add2(sum, p2);
-                                    uint64_t w2 = mul2(p2, vs2);
+                                    uint64_t w2 = mul2(p2, j ? pk2(v4.z, v4.w) : pk2(v4.x, v4.y));
                                     float wa, wb;
                                     upk2(w2, wa, wb);
                                     if (MASK) {  // (a value scale that is not a number stays behind the mask)
-                                        wa = seen(32 * c + e) ? wa : 0.f, wb = seen(32 * c + e + 1) ? wb : 0.f;
+                                        if (!((seen >> x) & 1ull)) wa = 0.f;
+                                        if (!((seen >> (x + 1)) & 1ull)) wb = 0.f;
                                         w2 = pk2(wa, wb);
                                     }
                                     const uint32_t hi = f16_pack(wa, wb);
                                     const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hi));
                                     float la, lb;
-                                    upk2(add2(w2, pk2(-hf.x, -hf.y)), la, lb);
-                                    w[2 * i + j] = hi;
-                                    w[16 + 2 * i + j] = f16_pack(la, lb);
+                                    upk2(fma2(pk2(hf.x, hf.y), less, w2), la, lb);
+                                    w[e / 2] = hi;
+                                    w[8 + e / 2] = f16_pack(la, lb);
                                 }
                             }
-                            tc_st32(s_at + 32 * c, w);
+                            tc_st16(s_at + 16 * c, w);
                         }
-                        float sa, sb;
-                        upk2(sum, sa, sb);
-                        l = l * alpha + (sa + sb);
                     };
-                    if (masked) softmax(Flag<true>());
-                    else softmax(Flag<false>());
+                    if (masked) weights(Flag<true>());
+                    else weights(Flag<false>());
+                    float sa, sb;
+                    upk2(sum, sa, sb);
+                    l = l * alpha_new + (sa + sb);
                     tc_wait_st();
                 }
                 tc_fence_before();
-                arrive(&sh.p_full[wg]);
-                if (lane == 0) mbar_arrive(&sh.sc_empty[wg]);
-                if (!(ok = wait(&sh.t_full[wg], n))) break;
-                tc_fence_after();
-                if (active) {
-                    const uint64_t al2 = pk2(alpha, alpha), ce2 = pk2(ce, ce);
-#pragma unroll
-                    for (int c = 0; c < HD / 32; ++c) {
-                        uint32_t r[32];
-                        tc_ld32(t_at + 32 * c, r);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            o[16 * c + i] = fma2(pk2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), ce2,
-                                                 mul2(o[16 * c + i], al2));
-                    }
-                }
-                tc_fence_before();
-                if (!last_odd) arrive(&sh.t_empty[wg]);
+                arrive(&sh.p_full[b]);
+                if (lane == 0) mbar_arrive(&sh.sc_empty[b]);
+                // the tile before is added while the tensor cores weigh this one
+                if (tau > first && !(ok = fold(tau - 1))) break;
+                alpha = alpha_new;
+                ce = ce_new;
             }
-            if (!ok) break;
-            const int odd = ((tau + 1) & 1) ? tiles / 2 : (tiles + 1) / 2;  // tiles of the second group
-            tau += tiles;
-            if (wg == 1) {
-                if (odd == 0) continue;
-                if (active) {  // its sums go to the first group over the last product, read by now
-#pragma unroll
-                    for (int c = 0; c < HD / 32; ++c) {
-                        uint32_t r[32];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float a, b;
-                            upk2(o[16 * c + i], a, b);
-                            r[2 * i] = __float_as_uint(a), r[2 * i + 1] = __float_as_uint(b);
-                        }
-                        tc_st32(t_at + 32 * c, r);
-                    }
-                    sh.mg_m[m] = mr;
-                    sh.mg_l[m] = l;
-                    tc_wait_st();
-                }
-                tc_fence_before();
-                arrive(&sh.mg_full);
-                continue;
-            }
-            if (odd) {
-                if (!(ok = wait(&sh.mg_full, merges++))) break;
-                tc_fence_after();
-                if (active) {
-                    const float m1 = sh.mg_m[m], mx = fmaxf(mr, m1), ms = mx == -INFINITY ? 0.f : mx;
-                    const float f0 = ex2(mr - ms), f1 = ex2(m1 - ms);
-                    l = l * f0 + sh.mg_l[m] * f1;
-                    mr = mx;
-                    const uint64_t f02 = pk2(f0, f0), f12 = pk2(f1, f1);
-#pragma unroll
-                    for (int c = 0; c < HD / 32; ++c) {
-                        uint32_t r[32];
-                        tc_ld32(t_at + 128 + 32 * c, r);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            o[16 * c + i] = fma2(pk2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f12,
-                                                 mul2(o[16 * c + i], f02));
-                    }
-                }
-                tc_fence_before();
-                arrive(&sh.t_empty[1]);
+            if (!ok || !(ok = fold(tau - 1))) break;
+            if (active) {
+                float other;
+                if (!(ok = trade(l, other))) break;
+                l += other;
             }
             // ---- the item's output, or its part of it
             const int64_t row = d.row0 + token;
             const int head = d.head * G + (m - token * G);
             auto write_out = [&]() {
-                if (!valid) return;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                float4* dst = reinterpret_cast<float4*>(pk.out + row * pk.out_stride + (int64_t)head * HD);
+                float4* dst = reinterpret_cast<float4*>(pk.out + row * pk.out_stride + (int64_t)head * HD + HV * wg);
 #pragma unroll
-                for (int i = 0; i < HD / 4; ++i) {
+                for (int i = 0; i < HV / 4; ++i) {
                     float4 v;
                     upk2(o[2 * i], v.x, v.y), upk2(o[2 * i + 1], v.z, v.w);
                     dst[i] = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
                 }
-                if (pk.lse) pk.lse[row * pk.heads + head] = l == 0.f ? -INFINITY : (mr + log2f(l)) * 0.693147180559945f;
+                if (pk.lse && wg == 0) pk.lse[row * pk.heads + head] = l == 0.f ? -INFINITY : (mr + log2f(l)) * 0.693147180559945f;
             };
-            if (d.t0 == 0 && d.t1 == d.units) {
-                write_out();
-                continue;
-            }
-            float* slot = pk.part + (int64_t)(2 * blockIdx.x + (d.opens ? 0 : 1)) * SLOT;
-            if (valid) {
+            bool write = valid;
+            if (d.t0 != 0 || d.t1 != d.units) {
+                float* slot = pk.part + (int64_t)(2 * blockIdx.x + (d.opens ? 0 : 1)) * SLOT;
+                if (valid) {
 #pragma unroll
-                for (int i = 0; i < HD / 4; ++i) {
-                    float4 v;
-                    upk2(o[2 * i], v.x, v.y), upk2(o[2 * i + 1], v.z, v.w);
-                    __stcg(reinterpret_cast<float4*>(slot) + i * PT_M + m, v);
-                }
-                __stcg(slot + PT_M * HD + m, mr);
-                __stcg(slot + PT_M * (HD + 1) + m, l);
-            }
-            const int c0 = run.owner(d.at), c1 = run.owner(d.at + d.units - 1);
-            arrive(&sh.met);
-            if (!(ok = wait(&sh.met, meets++))) break;
-            if (tid == 0) {
-                sh.last = atomic_add_acq_rel_gpu(pk.counters + c0, 1) == c1 - c0;
-                if (sh.last) pk.counters[c0] = 0;
-            }
-            arrive(&sh.met);
-            if (!(ok = wait(&sh.met, meets++))) break;
-            if (sh.last && valid) {
-                auto slot_of = [&](int c) {
-                    return pk.part + (int64_t)(2 * c + (run.start(c) >= d.at ? 0 : 1)) * SLOT;
-                };
-                float mx = -INFINITY;
-                for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, __ldcg(slot_of(c) + PT_M * HD + m));
-                const float ms = mx == -INFINITY ? 0.f : mx;
-#pragma unroll
-                for (int i = 0; i < HD / 2; ++i) o[i] = 0ull;
-                l = 0.f;
-                for (int c = c0; c <= c1; ++c) {
-                    const float* sl = slot_of(c);
-                    const float f = ex2(__ldcg(sl + PT_M * HD + m) - ms);
-                    l += __ldcg(sl + PT_M * (HD + 1) + m) * f;
-                    const uint64_t f2 = pk2(f, f);
-#pragma unroll
-                    for (int i = 0; i < HD / 4; ++i) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(sl) + i * PT_M + m);
-                        o[2 * i] = fma2(pk2(v.x, v.y), f2, o[2 * i]);
-                        o[2 * i + 1] = fma2(pk2(v.z, v.w), f2, o[2 * i + 1]);
+                    for (int i = 0; i < HV / 4; ++i) {
+                        float4 v;
+                        upk2(o[2 * i], v.x, v.y), upk2(o[2 * i + 1], v.z, v.w);
+                        __stcg(reinterpret_cast<float4*>(slot) + (i + HV / 4 * wg) * PT_M + m, v);
+                    }
+                    if (wg == 0) {
+                        __stcg(slot + PT_M * HD + m, mr);
+                        __stcg(slot + PT_M * (HD + 1) + m, l);
                     }
                 }
-                mr = mx;
-                write_out();
+                const int c0 = run.owner(d.at), c1 = run.owner(d.at + d.units - 1);
+                arrive(&sh.met);
+                if (!(ok = wait(&sh.met, meets++))) break;
+                if (tid == 0) {
+                    sh.last = atomic_add_acq_rel_gpu(pk.counters + c0, 1) == c1 - c0;
+                    if (sh.last) pk.counters[c0] = 0;
+                }
+                arrive(&sh.met);
+                if (!(ok = wait(&sh.met, meets++))) break;
+                write = valid && sh.last;
+                if (write) {  // the last CTA to arrive folds the item's pieces in order
+                    auto slot_of = [&](int c) {
+                        return pk.part + (int64_t)(2 * c + (run.start(c) >= d.at ? 0 : 1)) * SLOT;
+                    };
+                    float mx = -INFINITY;
+                    for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, __ldcg(slot_of(c) + PT_M * HD + m));
+                    const float ms = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+                    for (int i = 0; i < HV / 2; ++i) o[i] = 0ull;
+                    l = 0.f;
+#pragma unroll 1
+                    for (int c = c0; c <= c1; ++c) {
+                        const float* sl = slot_of(c);
+                        const float f = ex2(__ldcg(sl + PT_M * HD + m) - ms);
+                        l += __ldcg(sl + PT_M * (HD + 1) + m) * f;
+                        const uint64_t f2 = pk2(f, f);
+#pragma unroll
+                        for (int i = 0; i < HV / 4; ++i) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(sl) + (i + HV / 4 * wg) * PT_M + m);
+                            o[2 * i] = fma2(pk2(v.x, v.y), f2, o[2 * i]);
+                            o[2 * i + 1] = fma2(pk2(v.z, v.w), f2, o[2 * i + 1]);
+                        }
+                    }
+                    mr = mx;
+                }
             }
+            if (write) write_out();
         }
     } else if (wg == 2) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -517,9 +526,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
         int tau = 0, stage = 0, uses = 0;  // uses: stages taken so far
         PtItem d;
         bool ok = true;
+#pragma unroll 1
         for (int it = 0; ok && next_item(it, d); ++it) {
             if (!(ok = wait(&sh.q_empty, it + 1))) break;
             const int r = lane & 7, cc = lane >> 3;
+#pragma unroll 1
             for (int i = 0; i < 4; ++i) {  // 8 query vectors at a time, a lane HD / 32 chunks of 8 dimensions
                 const int m = 32 * w + 8 * i + r;
                 const int64_t row = d.row0 + m / G;
@@ -561,10 +572,12 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
             }
             fence_async();
             arrive(&sh.q_full);
+#pragma unroll 1
             for (int x = 0; ok && x < d.t1 - d.t0; ++x, ++tau) {
                 const int b = tau & 1, n = tau >> 1;
                 // keys: rows as they are; a lane 16 dimensions (one 16-byte chunk of words) of a position
                 if (!(ok = wait(&sh.k_empty[b], n + 1))) break;
+#pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     if (!(ok = wait(&sh.raw_full[stage], uses / PT_STAGES))) break;
                     const unsigned char* src = sh.raw[stage];
@@ -591,9 +604,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                 arrive(&sh.k_full[b]);
                 // values: transposed; a lane 4 dimensions of 8 positions
                 if (!(ok = wait(&sh.v_empty[b], n + 1))) break;
+#pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     if (!(ok = wait(&sh.raw_full[stage], uses / PT_STAGES))) break;
                     const unsigned char* src = sh.raw[stage];
+                    const int past = d.end - (d.t0 + x) * PT_P - PT_HALF * half;  // positions of the half before the end
 #pragma unroll
                     for (int i = 0; i < HD / 64; ++i) {
                         const int task = (i * 128 + 32 * w + lane);
@@ -602,6 +617,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             in[j] = *reinterpret_cast<const uint32_t*>(src + raw_off<HD>(8 * p8 + j, d4 >> 2) + 4 * (d4 & 3));
+                        if (WORDS == Q8_KV_E4M3 && past < 8 * p8 + 8) {  // (words past the end may stand for NaN)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (8 * p8 + j >= past) in[j] = 0u;
+                        }
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const uint32_t a = words_flip<WORDS>(__byte_perm(in[2 * j], in[2 * j + 1], 0x5140));
@@ -641,7 +661,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                     for (int part = 1; part >= 0; --part)  // the small parts first
 #pragma unroll
                         for (int j = 0; j < PT_P / 16; ++j)  // 16 positions: 8 columns of weights, two core matrices
-                            tc_mma_f16_ta(t_at, p_at + 32 * (j >> 1) + 8 * (j & 1) + 16 * part, dv + j * (256 >> 4), id_o,
+                            tc_mma_f16_ta(t_at, p_at + 16 * j + 8 * part, dv + j * (256 >> 4), id_o,
                                           part == 1 && j == 0 ? 0u : 1u);
                     tc_commit(&sh.t_full[b]);
                     tc_commit(&sh.v_empty[b]);
@@ -651,12 +671,14 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
             };
             int tau = 0;
             bool pending = false;  // whether tile tau - 1's second product is still to be issued
-            for (int it = 0; ok && next_item(it, d); ++it) {
+    #pragma unroll 1
+        for (int it = 0; ok && next_item(it, d); ++it) {
                 if (pending) {
                     if (!(ok = weigh(tau - 1))) break;
                     pending = false;
                 }
                 if (!(ok = wait(&sh.q_full, it))) break;
+#pragma unroll 1
                 for (int x = 0; x < d.t1 - d.t0; ++x, ++tau) {
                     const int b = tau & 1, n = tau >> 1;
                     // the scores overwrite tile tau - 2's weights: its second product has to be done
@@ -681,50 +703,47 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
             }
             if (ok && pending) weigh(tau - 1);
             if (lane == 0) tc_commit(&sh.drained);  // nothing is in flight when the CTA gives its tensor memory back
-            for (unsigned i = 0; i < PT_WAIT && !mbar_try_wait(&sh.drained, 0); ++i)
-                if (i > 2048u) __nanosleep(32);
-        } else if (wid < 15) {
-            // ================ copies of the words
-            constexpr int CH = HD / 16, ROWS = 64 / CH;  // 16-byte chunks a row, rows a pass of the two warps
-            const int c = (wid - 13) * 32 + lane, chunk = c % CH, r0 = c / CH;
+#pragma unroll 1
+            for (unsigned i = 0; i < PT_WAIT && !try_wait(&sh.drained, 0); ++i) {}
+        } else if (wid == 13) {
+            // ================ copies of the words: 16 positions of the head a box, a lane a box
             int stage = 0, uses = 0;
+#pragma unroll 1
             for (int it = 0; ok && next_item(it, d); ++it) {
+                auto page_at = [&](int tl) {  // the page of this lane's 16 positions; past the end or none: one past the
+                    const int p = tl * PT_P + 16 * lane;  // last, which reads as zeros
+                    if (lane >= PT_P / 16 || tl >= d.t1 || p >= d.end) return kv.pages;
+                    const int id = kv_page(kv, d.seq, p);
+                    if (id < 0) kv_flag(kv, Q8_KV_ERR_PAGE);
+                    return id < 0 ? kv.pages : id;
+                };
+                int next = page_at(d.t0);
+#pragma unroll 1
                 for (int tl = d.t0; ok && tl < d.t1; ++tl) {
-                    int page[2][PT_HALF / ROWS];
-#pragma unroll
-                    for (int i = 0; i < 2 * PT_HALF / ROWS; ++i) {
-                        const int p = tl * PT_P + i * ROWS + r0;
-                        int& pg = page[i / (PT_HALF / ROWS)][i % (PT_HALF / ROWS)];
-                        pg = -1;
-                        if (p < d.end) {
-                            pg = kv_page(kv, d.seq, p);
-                            if (pg < 0) kv_flag(kv, Q8_KV_ERR_PAGE);
-                        }
-                    }
-#pragma unroll
+                    const int page = next, row = (d.head << kv.page_log2) + ((tl * PT_P + 16 * lane) & ((1 << kv.page_log2) - 1));
+                    next = page_at(tl + 1);
+#pragma unroll 1
                     for (int part = 0; part < 4; ++part) {  // the keys' halves, then the values'
-                        const int half = part & 1;
-                        const int8_t* from = part < 2 ? kv.k : kv.v;
                         if (!(ok = wait(&sh.raw_empty[stage], uses / PT_STAGES + 1))) break;
-#pragma unroll
-                        for (int i = 0; i < PT_HALF / ROWS; ++i) {
-                            const int r = i * ROWS + r0, pg = page[half][i];
-                            const int64_t row = kv_row(kv, max(pg, 0), d.head, tl * PT_P + half * PT_HALF + r);
-                            async_copy16(sh.raw[stage] + raw_off<HD>(r, chunk), from + row * HD + 16 * chunk, pg >= 0);
-                        }
-                        async_arrive(&sh.raw_full[stage]);
+                        if (lane == 0) mbar_arrive_expect_tx(&sh.raw_full[stage], PT_HALF * HD);
+                        __syncwarp();
+                        if (lane < PT_P / 16 && lane / 4 == (part & 1))
+                            tma_box(sh.raw[stage] + (lane & 3) * 16 * HD, part < 2 ? &map_k : &map_v, row, page, &sh.raw_full[stage]);
                         stage = stage + 1 == PT_STAGES ? 0 : stage + 1;
                         ++uses;
                     }
                 }
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-        } else {
+            for (int u = max(0, uses - PT_STAGES); u < uses; ++u)  // no copy is in flight when the CTA leaves
+#pragma unroll 1
+                for (unsigned i = 0; i < PT_WAIT && !try_wait(&sh.raw_full[u % PT_STAGES], (u / PT_STAGES) & 1); ++i) {}
+        } else if (wid == 15) {
             // ================ items and scales
             int b = run.seq;
             int64_t b_at = run.seq_at, i = 0, h = 0, cur = run.lo;
             bool found = false;
             int tau = 0, it = 0;
+#pragma unroll 1
             for (; ok; ++it) {
                 PtItem& e = sh.item[it % PT_ITEMS];
                 if (!(ok = wait(&sh.d_empty[it % PT_ITEMS], it / PT_ITEMS + 1))) break;
@@ -777,6 +796,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                 if (lane == 0) e = d;
                 arrive(&sh.d_full[it % PT_ITEMS]);
                 if (!more) break;
+#pragma unroll 1
                 for (int tl = d.t0; tl < d.t1; ++tl, ++tau) {
                     const int bf = tau & 1, p = tl * PT_P + 4 * lane;
                     float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f), v4 = k4;
@@ -813,14 +833,46 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
     if (wid == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The CUDA driver API's tensor-map encoder, found once through the runtime's entry-point query.
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return (EncodeTiled) nullptr;
+        return reinterpret_cast<EncodeTiled>(f);
+    }();
+    return fn;
+}
+
+// Words [pages][kv * page_size][hd], read 16 rows of a page at a time.
+bool words_map(CUtensorMap* m, const void* words, const KvView& v, int hd) {
+    const EncodeTiled enc = encode_tiled();
+    if (!enc) return false;
+    const cuuint64_t rows = (cuuint64_t)v.kv << v.page_log2;
+    const cuuint64_t dims[3] = {(cuuint64_t)hd, rows, (cuuint64_t)v.pages};
+    const cuuint64_t strides[2] = {(cuuint64_t)hd, rows * hd};
+    const cuuint32_t box[3] = {(cuuint32_t)hd, 16, 1}, step[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(words), dims, strides, box, step,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int HD, int WORDS>
 cudaError_t tiles_launch(const PagedParams& p, cudaStream_t st) {
     auto kernel = paged_tiles_kernel<HD, WORDS>;
-    constexpr size_t smem = sizeof(PtShared<HD>);
-    static_assert(smem + 2048 <= 232448, "dynamic plus static shared memory within the 227 KB a CTA may hold");
+    constexpr size_t smem = sizeof(PtShared<HD>) + 1024;
+    static_assert(smem + 1024 <= 232448, "dynamic plus static shared memory within the 227 KB a CTA may hold");
+    CUtensorMap mk, mv;
+    if (!words_map(&mk, p.view.k, p.view, HD) || !words_map(&mv, p.view.v, p.view, HD)) return cudaErrorNotSupported;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<device_info().sms, PT_THREADS, smem, st>>>(p);
+    kernel<<<device_info().sms, PT_THREADS, smem, st>>>(p, mk, mv);
     return cudaGetLastError();
 }
 
