@@ -9,12 +9,11 @@
 // so each is two tensor-core products (4 x 128 x 128 x hd multiply-adds a tile pair, twice the formula's): those bound it.
 // One CTA an SM works through an equal run of tile pairs; its warps divide the work and meet only at barriers in shared
 // memory:
-//  - warps 0-3 and 4-7 (a thread half a query vector: one group the first, the other the last 64 positions of a tile)
-//    take the scores out of tensor memory once, trade maxima, and put the weights' parts back over the scores, where the
-//    second product reads them as its first operand; then they add the product of the tile before (rounded: the tensor
-//    cores truncate as they accumulate) to f32 sums in registers, half the dimensions each, while the tensor cores work
-//    on this tile's second and the next one's first product.
-//  - warps 8-11 turn the words into f16 operand tiles (the values transposed), and an item's queries into their parts.
+//  - warps 0-3 (a thread a query vector) take a tile's scores out of tensor memory, form its weights against the running
+//    maximum, and put their parts back over the scores, where the second product reads them as its first operand.
+//  - warps 4-7 turn the values' words into f16 operand tiles, transposed, and add each tile's product (rounded: the tensor
+//    cores truncate as they accumulate) to the f32 output sums in their registers; at an item's end they write it.
+//  - warps 8-11 turn the keys' words into operand tiles, and an item's queries into their parts.
 //  - warp 12 issues the products, warp 13 copies the words of 64 positions at a time from the pages into a ring (tensor
 //    copies of 16 rows, zeros for pages out of range), warp 15 deals out the items and prepares the scales.
 // Registers are moved from the last eight warps to the first eight (200 and 56 a thread).
@@ -35,8 +34,8 @@ constexpr int PT_HALF = 64;                // positions a copied stage
 constexpr int PT_STAGES = 3;
 constexpr int PT_ITEMS = 4;                // items dealt out ahead
 constexpr int PT_READERS = 14;             // warps that read an item
-constexpr unsigned PT_WAIT = 1u << 13;      // polls before a wait gives up, each up to PT_POLL_NS long
-constexpr unsigned PT_POLL_NS = 20000;
+constexpr unsigned PT_POLL_NS = 20000;     // the longest the hardware may hold a warp at a poll
+constexpr unsigned long long PT_WAIT_NS = 2000000000ull;  // a wait gives up after two seconds
 constexpr int PT_PEXP = 14;                // weights are split as values of up to 2^(PT_PEXP + 1)
 
 // One item's piece as the roles read it.
@@ -60,13 +59,14 @@ struct PtShared {
     unsigned char v[2][HD / 8 * SBO_V];
     float ks[2][PT_P], vs[2][PT_P];
     float qf[4][PT_M];
-    float trade[2][2][PT_M];
+    float alpha[4][PT_M], back[4];   // a tile's rescaling of the sums, and what scales its product back
+    float fin_m[PT_M], fin_l[PT_M];  // an item's maxima and sums
     float ce[2];
     unsigned groups[2];    // which 16-position groups of a tile are there
     PtItem item[PT_ITEMS];
     uint64_t d_full[PT_ITEMS], d_empty[PT_ITEMS], raw_full[PT_STAGES], raw_empty[PT_STAGES];
     uint64_t sc_full[2], sc_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t s_full[2], p_full[2], t_full[2], t_empty[2], q_full, q_empty, pair[4], met, drained;
+    uint64_t s_full[2], p_full[2], t_full[2], t_empty[2], q_full, q_empty, fin_full, fin_empty, met, drained;
     uint32_t tmem;
     int dead;              // a wait gave up: every role leaves
     int last;
@@ -81,6 +81,19 @@ __device__ __forceinline__ bool try_wait(uint64_t* bar, unsigned parity) {
                  : "r"(smem_addr(bar)), "r"(parity), "r"(PT_POLL_NS)
                  : "memory");
     return ok != 0;
+}
+
+__device__ __forceinline__ unsigned long long nanoseconds() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+
+// Waits for a phase, for two seconds at most, whatever the other roles do.
+__device__ __forceinline__ void drain(uint64_t* bar, unsigned parity) {
+    const unsigned long long from = nanoseconds();
+#pragma unroll 1
+    while (!try_wait(bar, parity) && nanoseconds() - from < PT_WAIT_NS) {}
 }
 
 __device__ __forceinline__ uint64_t pk2(float a, float b) {
@@ -112,7 +125,8 @@ __device__ __forceinline__ void tc_mma_f16_ta(uint32_t d, uint32_t a, uint64_t b
 }
 
 // 16 columns of this warp's 32 lanes, one 32-bit value each: issued by tc_ld16, there after tc_wait16 on the same
-// registers (which keeps their use behind the wait), and written by tc_st16 (complete after tc_wait_st).
+// registers (which keeps their use behind the wait), and written by tc_st16 (complete after tc_wait_st).  None of them
+// touches other memory, so loads from shared memory move freely across them.
 __device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
@@ -123,14 +137,12 @@ __device__ __forceinline__ void tc_wait16(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
+                 :);
 }
 __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
                  ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-                   "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-                 : "memory");
+                   "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
 }
 // N columns (a multiple of 32) from taddr into r, all of them asked for before the wait.
 template <int N>
@@ -140,6 +152,29 @@ __device__ __forceinline__ void tc_load(uint32_t taddr, uint32_t (&r)[N]) {
     for (int i = 0; i < N / 16; ++i) tc_ld16(taddr + 16 * i, x[i]);
 #pragma unroll
     for (int i = 0; i < N / 16; ++i) tc_wait16(x[i]);
+}
+__device__ __forceinline__ void tc_issue32(uint32_t taddr, uint32_t (&r)[2][16]) {
+    tc_ld16(taddr, r[0]);
+    tc_ld16(taddr + 16, r[1]);
+}
+// Calls f(i, r) for the columns 32 i .. of 128 columns from taddr (r: two times sixteen), the next ones on their way
+// meanwhile.  A loop, not straight code: what the warps of the roles run has to stay within the SM's instruction cache
+// together (with the softmax unrolled the warps waited for instructions most of the time).
+template <typename F>
+__device__ __forceinline__ void tc_columns(uint32_t taddr, F f) {
+    uint32_t r0[2][16], r1[2][16];
+    tc_issue32(taddr, r0);
+#pragma unroll 1
+    for (int i = 0; i < 4; i += 2) {
+        tc_wait16(r0[0]);
+        tc_wait16(r0[1]);
+        tc_issue32(taddr + 32 * (i + 1), r1);
+        f(i, r0);
+        tc_wait16(r1[0]);
+        tc_wait16(r1[1]);
+        if (i == 0) tc_issue32(taddr + 64, r0);
+        f(i + 1, r1);
+    }
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -254,14 +289,14 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
         for (int i = 0; i < PT_ITEMS; ++i) mbar_init(&sh.d_full[i], 1), mbar_init(&sh.d_empty[i], PT_READERS);
         for (int i = 0; i < PT_STAGES; ++i) mbar_init(&sh.raw_full[i], 1), mbar_init(&sh.raw_empty[i], 4);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.sc_full[i], 1), mbar_init(&sh.sc_empty[i], 8);
+            mbar_init(&sh.sc_full[i], 1), mbar_init(&sh.sc_empty[i], 4);
             mbar_init(&sh.k_full[i], 4), mbar_init(&sh.k_empty[i], 1);
             mbar_init(&sh.v_full[i], 4), mbar_init(&sh.v_empty[i], 1);
-            mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 8);
-            mbar_init(&sh.t_full[i], 1), mbar_init(&sh.t_empty[i], 8);
+            mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 4);
+            mbar_init(&sh.t_full[i], 1), mbar_init(&sh.t_empty[i], 4);
         }
-        mbar_init(&sh.q_full, 4), mbar_init(&sh.q_empty, 1), mbar_init(&sh.met, 8);
-        for (int i = 0; i < 4; ++i) mbar_init(&sh.pair[i], 2);
+        mbar_init(&sh.q_full, 4), mbar_init(&sh.q_empty, 1), mbar_init(&sh.met, 4);
+        mbar_init(&sh.fin_full, 4), mbar_init(&sh.fin_empty, 4);
         mbar_init(&sh.drained, 1);
         sh.dead = 0;
         fence_barrier_init();
@@ -277,10 +312,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
 
     // A bounded wait, the same answer in every lane of the warp; false once any role's wait has given up.
     auto wait = [&](uint64_t* bar, unsigned parity) -> bool {
-        bool got = false;
+        bool got = try_wait(bar, parity & 1u);
+        if (!got) {
+            const unsigned long long from = nanoseconds();
 #pragma unroll 1
-        for (unsigned i = 0; i < PT_WAIT && !(got = try_wait(bar, parity & 1u)); ++i)
-            if (*(volatile int*)&sh.dead) break;
+            while (!(got = try_wait(bar, parity & 1u)))
+                if (*(volatile int*)&sh.dead || nanoseconds() - from > PT_WAIT_NS) break;
+        }
         if (__all_sync(0xffffffffu, got)) return true;
         *(volatile int*)&sh.dead = 1;
         kv_flag(kv, Q8_KV_ERR_WAIT);
@@ -297,194 +335,242 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
         return d.t1 > d.t0;
     };
 
-    if (wg < 2) {
+    // Turns copied stage `idx` (64 positions of values) into half of a transposed operand tile; a lane 4 dimensions of 8
+    // positions.  `past`: the half's positions before the sequence's end.
+    auto values_half = [&](int idx, unsigned char* tile, int half, int past) -> bool {
+        const int stage = idx % PT_STAGES;
+        if (!wait(&sh.raw_full[stage], idx / PT_STAGES)) return false;
+        const unsigned char* src = sh.raw[stage];
+#pragma unroll
+        for (int i = 0; i < HD / 64; ++i) {
+            const int task = i * 128 + (tid & 127);
+            const int d4 = task % (HD / 4), p8 = task / (HD / 4);  // of 8 groups of 8 positions
+            uint32_t in[8], h[4][4];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                in[j] = *reinterpret_cast<const uint32_t*>(src + raw_off<HD>(8 * p8 + j, d4 >> 2) + 4 * (d4 & 3));
+            if (WORDS == Q8_KV_E4M3 && past < 8 * p8 + 8) {  // (words past the end may stand for NaN)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (8 * p8 + j >= past) in[j] = 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t a = words_flip<WORDS>(__byte_perm(in[2 * j], in[2 * j + 1], 0x5140));
+                const uint32_t c = words_flip<WORDS>(__byte_perm(in[2 * j], in[2 * j + 1], 0x7362));
+                h[0][j] = words2_f16<WORDS, 0>(a), h[1][j] = words2_f16<WORDS, 1>(a);
+                h[2][j] = words2_f16<WORDS, 0>(c), h[3][j] = words2_f16<WORDS, 1>(c);
+            }
+            unsigned char* dst = tile + (uint32_t)(d4 >> 1) * SBO_V + (uint32_t)(p8 + 8 * half) * 128 + (uint32_t)(d4 & 1) * 64;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(dst + 16 * j) = make_uint4(h[j][0], h[j][1], h[j][2], h[j][3]);
+        }
+        arrive(&sh.raw_empty[stage]);
+        return true;
+    };
+
+    if (wg == 0) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        // ================ scores, weights and output sums: thread = half of a query vector's positions and dimensions
-        constexpr int HP = PT_P / 2, HV = HD / 2;
-        const int quarter = wid & 3, m = 32 * quarter + lane;
-        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-        int tau = 0, pairs = 0, meets = 0;
+        // ================ scores to weights: thread = query vector
+        const int m = tid;
+        const uint32_t lanes = (uint32_t)(32 * wid) << 16;
+        int tau = 0;
         PtItem d;
         bool ok = true;
-        // This row's value of the thread that holds its other half (the two warps of a quarter trade one a lane).
-        auto trade = [&](float mine, float& other) -> bool {
-            float(&x)[2][PT_M] = sh.trade[pairs & 1];
-            x[wg][m] = mine;
-            arrive(&sh.pair[quarter]);
-            if (!wait(&sh.pair[quarter], pairs++)) return false;
-            other = x[wg ^ 1][m];
-            return true;
-        };
 #pragma unroll 1
         for (int it = 0; ok && next_item(it, d); ++it) {
             const bool valid = m < d.tokens * G;
-            const int token = m / G;
-            const int lim = !valid ? INT_MAX : d.end ? d.pos + token : -1;
-            const bool active = 32 * quarter < d.tokens * G;  // (uniform in both warps of the quarter)
-            float mr = -INFINITY, l = 0.f, qf = 0.f, alpha = 1.f, ce = 1.f;
-            uint64_t o[HV / 2];
-#pragma unroll
-            for (int i = 0; i < HV / 2; ++i) o[i] = 0ull;
-            auto fold = [&](int t) -> bool {  // adds tile t's product, whose alpha and ce are at hand
-                if (!wait(&sh.t_full[t & 1], t >> 1)) return false;
-                tc_fence_after();
-                if (active) {
-                    const uint64_t al2 = pk2(alpha, alpha), ce2 = pk2(ce, ce);
-                    uint32_t r[HV];
-                    tc_load<HV>(tmem + lanes + 256 + 128 * (t & 1) + HV * wg, r);
-                    if (!__all_sync(0xffffffffu, alpha == 1.f)) {  // (a maximum moved)
-#pragma unroll
-                        for (int i = 0; i < HV / 2; ++i) o[i] = mul2(o[i], al2);
-                    }
-#pragma unroll
-                    for (int i = 0; i < HV / 2; ++i)
-                        o[i] = fma2(pk2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), ce2, o[i]);
-                }
-                tc_fence_before();
-                arrive(&sh.t_empty[t & 1]);
-                return true;
-            };
+            const int lim = !valid ? INT_MAX : d.end ? d.pos + m / G : -1;
+            const bool active = 32 * wid < d.tokens * G;  // (warp-uniform)
+            float mr = -INFINITY, l = 0.f, qf = 0.f;
             const int first = tau;
 #pragma unroll 1
             for (int tl = d.t0; tl < d.t1; ++tl, ++tau) {
-                const int b = tau & 1, n = tau >> 1, p0 = tl * PT_P + HP * wg;
-                const uint32_t s_at = tmem + lanes + 128 * b + HP * wg;
+                const int b = tau & 1, n = tau >> 1, p0 = tl * PT_P;
+                const uint32_t s_at = tmem + lanes + 128 * b;
                 if (!(ok = wait(&sh.s_full[b], n) && wait(&sh.sc_full[b], n))) break;
                 tc_fence_after();
-                float alpha_new = 1.f, ce_new = 1.f;
                 if (active) {
                     if (tau == first) qf = sh.qf[it & 3][m];
-                    ce_new = sh.ce[b];
-                    const unsigned groups = sh.groups[b] >> (4 * wg) & 15u;
-                    const float4* ks4 = reinterpret_cast<const float4*>(sh.ks[b] + HP * wg);
-                    const float4* vs4 = reinterpret_cast<const float4*>(sh.vs[b] + HP * wg);
-                    const bool masked = __any_sync(0xffffffffu, lim < p0 + HP - 1) || groups != 15u;
-                    uint32_t s[HP];
-                    tc_load<HP>(s_at, s);
-                    // scores without the query's factor, which is positive; what is masked is -infinity
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int i = 0; i < HP / 4; ++i) {
-                        const float4 k4 = ks4[i];
-                        float a[4];
-                        upk2(mul2(pk2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), pk2(k4.x, k4.y)), a[0], a[1]);
-                        upk2(mul2(pk2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), pk2(k4.z, k4.w)), a[2], a[3]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) s[4 * i + j] = __float_as_uint(a[j]);
-                    }
-                    uint64_t seen = ~0ull;
-                    if (masked) {
-                        const int count = lim - p0 + 1;  // positions of this half that the row attends
-                        seen = count >= HP ? ~0ull : count <= 0 ? 0ull : (1ull << count) - 1;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (!((groups >> j) & 1u)) seen &= ~(0xffffull << (16 * j));
-#pragma unroll
-                        for (int i = 0; i < HP; ++i)
-                            if (!((seen >> i) & 1ull)) s[i] = 0xff800000u;
-                    }
-#pragma unroll
-                    for (int i = 0; i < HP; i += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
-                    float other;
-                    if (!(ok = trade(mx, other))) break;
-                    mx = fmaxf(mx, other);
-                    // (rounded up, so that no weight exceeds 1; and a factor of 0, an invalid vector's, must not meet the
-                    // masks' infinity)
-                    const float mn = fmaxf(mr, mx == -INFINITY ? -INFINITY : __fmul_ru(mx, qf));
-                    const float ms = mn == -INFINITY ? 0.f : mn;
-                    alpha_new = ex2(mr - ms);
-                    mr = mn;
-                    uint64_t sum = 0ull;
-                    const uint64_t qf2 = pk2(qf, qf), nm2 = pk2(-ms, -ms);
-                    auto weights = [&](auto with_mask) {
-                        constexpr bool MASK = decltype(with_mask)::value;
-                        const uint64_t less = pk2(-1.f, -1.f);
-#pragma unroll
-                        for (int c = 0; c < HP / 16; ++c) {
-                            uint32_t w[16];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float4 v4 = vs4[4 * c + i];
-#pragma unroll
-                                for (int j = 0; j < 2; ++j) {
-                                    const int e = 4 * i + 2 * j, x = 16 * c + e;
-                                    float a, b;
-                                    upk2(fma2(pk2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), qf2, nm2), a, b);
-                                    const uint64_t p2 = pk2(ex2(a), ex2(b));
-                                    sum = add2(sum, p2);
-                                    uint64_t w2 = mul2(p2, j ? pk2(v4.z, v4.w) : pk2(v4.x, v4.y));
-                                    float wa, wb;
-                                    upk2(w2, wa, wb);
-                                    if (MASK) {  // (a value scale that is not a number stays behind the mask)
-                                        if (!((seen >> x) & 1ull)) wa = 0.f;
-                                        if (!((seen >> (x + 1)) & 1ull)) wb = 0.f;
-                                        w2 = pk2(wa, wb);
-                                    }
-                                    const uint32_t hi = f16_pack(wa, wb);
-                                    const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-                                    float la, lb;
-                                    upk2(fma2(pk2(hf.x, hf.y), less, w2), la, lb);
-                                    w[e / 2] = hi;
-                                    w[8 + e / 2] = f16_pack(la, lb);
-                                }
-                            }
-                            tc_st16(s_at + 16 * c, w);
-                        }
+                    const unsigned groups = sh.groups[b];
+                    const float4* ks4 = reinterpret_cast<const float4*>(sh.ks[b]);
+                    const float4* vs4 = reinterpret_cast<const float4*>(sh.vs[b]);
+                    const bool masked = __any_sync(0xffffffffu, lim < p0 + PT_P - 1) || groups != 0xffu;
+                    const int count = lim - p0 + 1;  // positions of the tile that the row attends
+                    auto bits = [&](int c) -> unsigned {  // those of its columns 32 c .. that are seen
+                        const int n = count - 32 * c;
+                        unsigned seen = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
+                        if (!((groups >> (2 * c)) & 1u)) seen &= 0xffff0000u;
+                        if (!((groups >> (2 * c + 1)) & 1u)) seen &= 0xffffu;
+                        return seen;
                     };
-                    if (masked) weights(Flag<true>());
-                    else weights(Flag<false>());
-                    float sa, sb;
-                    upk2(sum, sa, sb);
-                    l = l * alpha_new + (sa + sb);
+                    auto softmax = [&](auto with_mask) {
+                        constexpr bool MASK = decltype(with_mask)::value;
+                        float mx = -INFINITY;  // scores without the query's factor, which is positive
+                        tc_columns(s_at, [&](int c, const uint32_t (&s)[2][16]) {
+                            unsigned seen = MASK ? bits(c) : 0u;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 k4 = ks4[8 * c + i];
+                                const uint32_t* x = &s[i / 4][4 * (i % 4)];
+                                float a[4];
+                                upk2(mul2(pk2(__uint_as_float(x[0]), __uint_as_float(x[1])), pk2(k4.x, k4.y)), a[0], a[1]);
+                                upk2(mul2(pk2(__uint_as_float(x[2]), __uint_as_float(x[3])), pk2(k4.z, k4.w)), a[2], a[3]);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    if (MASK && !((seen >> (4 * i + j)) & 1u)) a[j] = -INFINITY;
+                                mx = fmaxf(mx, fmaxf(a[0], a[1]));
+                                mx = fmaxf(mx, fmaxf(a[2], a[3]));
+                            }
+                        });
+                        // (rounded up, so that no weight exceeds 1; and a factor of 0, an invalid vector's, must not meet
+                        // the masks' infinity)
+                        const float mn = fmaxf(mr, mx == -INFINITY ? -INFINITY : __fmul_ru(mx, qf));
+                        const float ms = mn == -INFINITY ? 0.f : mn;
+                        const float alpha = ex2(mr - ms);
+                        mr = mn;
+                        sh.alpha[tau & 3][m] = alpha;
+                        if (m == 0) sh.back[tau & 3] = sh.ce[b];
+                        uint64_t sum = 0ull;
+                        const uint64_t qf2 = pk2(qf, qf), nm2 = pk2(-ms, -ms), less = pk2(-1.f, -1.f);
+                        tc_columns(s_at, [&](int c, const uint32_t (&s)[2][16]) {
+                            unsigned seen = MASK ? bits(c) : 0u;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t w[16];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const float4 k4 = ks4[8 * c + 4 * h + i], v4 = vs4[8 * c + 4 * h + i];
+#pragma unroll
+                                    for (int j = 0; j < 2; ++j) {
+                                        const int e = 4 * i + 2 * j;
+                                        uint64_t t2 = mul2(pk2(__uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1])),
+                                                           j ? pk2(k4.z, k4.w) : pk2(k4.x, k4.y));
+                                        t2 = fma2(t2, qf2, nm2);
+                                        float a, b;
+                                        upk2(t2, a, b);
+                                        a = ex2(a), b = ex2(b);
+                                        if (MASK) {
+                                            if (!((seen >> (16 * h + e)) & 1u)) a = 0.f;
+                                            if (!((seen >> (16 * h + e + 1)) & 1u)) b = 0.f;
+                                        }
+                                        const uint64_t p2 = pk2(a, b);
+                                        sum = add2(sum, p2);
+                                        uint64_t w2 = mul2(p2, j ? pk2(v4.z, v4.w) : pk2(v4.x, v4.y));
+                                        float wa, wb;
+                                        upk2(w2, wa, wb);
+                                        if (MASK) {  // (a value scale that is not a number stays behind the mask)
+                                            if (!((seen >> (16 * h + e)) & 1u)) wa = 0.f;
+                                            if (!((seen >> (16 * h + e + 1)) & 1u)) wb = 0.f;
+                                            w2 = pk2(wa, wb);
+                                        }
+                                        const uint32_t hi = f16_pack(wa, wb);
+                                        const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                                        float la, lb;
+                                        upk2(fma2(pk2(hf.x, hf.y), less, w2), la, lb);
+                                        w[e / 2] = hi;
+                                        w[8 + e / 2] = f16_pack(la, lb);
+                                    }
+                                }
+                                tc_st16(s_at + 32 * c + 16 * h, w);
+                            }
+                        });
+                        float sa, sb;
+                        upk2(sum, sa, sb);
+                        l = l * alpha + (sa + sb);
+                    };
+                    if (masked) softmax(Flag<true>());
+                    else softmax(Flag<false>());
                     tc_wait_st();
                 }
                 tc_fence_before();
                 arrive(&sh.p_full[b]);
                 if (lane == 0) mbar_arrive(&sh.sc_empty[b]);
-                // the tile before is added while the tensor cores weigh this one
-                if (tau > first && !(ok = fold(tau - 1))) break;
-                alpha = alpha_new;
-                ce = ce_new;
             }
-            if (!ok || !(ok = fold(tau - 1))) break;
-            if (active) {
-                float other;
-                if (!(ok = trade(l, other))) break;
-                l += other;
+            if (!ok || !(ok = wait(&sh.fin_empty, it + 1))) break;
+            sh.fin_m[m] = mr;
+            sh.fin_l[m] = l;
+            arrive(&sh.fin_full);
+        }
+    } else if (wg == 1) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        // ================ transposed values, output sums and results: thread = query vector
+        const int m = tid - 128;
+        const uint32_t lanes = (uint32_t)(32 * (wid - 4)) << 16;
+        int tau = 0, meets = 0;
+        PtItem d;
+        bool ok = true;
+#pragma unroll 1
+        for (int it = 0; ok && next_item(it, d); ++it) {
+            const bool valid = m < d.tokens * G;
+            const bool active = 32 * (wid - 4) < d.tokens * G;  // (warp-uniform)
+            uint64_t o[HD / 2];
+#pragma unroll
+            for (int i = 0; i < HD / 2; ++i) o[i] = 0ull;
+            const int tiles = d.t1 - d.t0;
+            // One step past the last tile: step x turns the values of tile x as soon as tile x - 2's product has left the
+            // buffer, and adds the product of tile x - 1.
+#pragma unroll 1
+            for (int x = 0; x <= tiles; ++x, ++tau) {
+                if (x < tiles) {
+                    const int b = tau & 1, past = d.end - (d.t0 + x) * PT_P;
+                    ok = wait(&sh.v_empty[b], (tau >> 1) + 1);
+#pragma unroll 1
+                    for (int half = 0; ok && half < 2; ++half)
+                        ok = values_half(4 * tau + 2 + half, sh.v[b], half, past - PT_HALF * half);
+                    if (!ok) break;
+                    fence_async();
+                    arrive(&sh.v_full[b]);
+                }
+                if (x == 0) continue;
+                const int t = tau - 1, b = t & 1;
+                if (!(ok = wait(&sh.t_full[b], t >> 1))) break;
+                tc_fence_after();
+                if (active) {
+                    const float alpha = sh.alpha[t & 3][m], back = sh.back[t & 3];
+                    const uint64_t al2 = pk2(alpha, alpha), back2 = pk2(back, back);
+                    if (!__all_sync(0xffffffffu, alpha == 1.f)) {  // (a maximum moved)
+#pragma unroll
+                        for (int i = 0; i < HD / 2; ++i) o[i] = mul2(o[i], al2);
+                    }
+#pragma unroll
+                    for (int c = 0; c < HD / 32; ++c) {
+                        uint32_t r[32];
+                        tc_load<32>(tmem + lanes + 256 + 128 * b + 32 * c, r);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            o[16 * c + i] = fma2(pk2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), back2, o[16 * c + i]);
+                    }
+                }
+                tc_fence_before();
+                arrive(&sh.t_empty[b]);
             }
+            if (!ok) break;
+            --tau;  // (the step past the last tile is no tile)
+            if (!(ok = wait(&sh.fin_full, it))) break;
+            float mr = sh.fin_m[m], l = sh.fin_l[m];
+            arrive(&sh.fin_empty);
             // ---- the item's output, or its part of it
+            const int token = m / G;
             const int64_t row = d.row0 + token;
             const int head = d.head * G + (m - token * G);
-            auto write_out = [&]() {
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                float4* dst = reinterpret_cast<float4*>(pk.out + row * pk.out_stride + (int64_t)head * HD + HV * wg);
-#pragma unroll
-                for (int i = 0; i < HV / 4; ++i) {
-                    float4 v;
-                    upk2(o[2 * i], v.x, v.y), upk2(o[2 * i + 1], v.z, v.w);
-                    dst[i] = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-                }
-                if (pk.lse && wg == 0) pk.lse[row * pk.heads + head] = l == 0.f ? -INFINITY : (mr + log2f(l)) * 0.693147180559945f;
-            };
             bool write = valid;
             if (d.t0 != 0 || d.t1 != d.units) {
                 float* slot = pk.part + (int64_t)(2 * blockIdx.x + (d.opens ? 0 : 1)) * SLOT;
                 if (valid) {
 #pragma unroll
-                    for (int i = 0; i < HV / 4; ++i) {
+                    for (int i = 0; i < HD / 4; ++i) {
                         float4 v;
                         upk2(o[2 * i], v.x, v.y), upk2(o[2 * i + 1], v.z, v.w);
-                        __stcg(reinterpret_cast<float4*>(slot) + (i + HV / 4 * wg) * PT_M + m, v);
+                        __stcg(reinterpret_cast<float4*>(slot) + i * PT_M + m, v);
                     }
-                    if (wg == 0) {
-                        __stcg(slot + PT_M * HD + m, mr);
-                        __stcg(slot + PT_M * (HD + 1) + m, l);
-                    }
+                    __stcg(slot + PT_M * HD + m, mr);
+                    __stcg(slot + PT_M * (HD + 1) + m, l);
                 }
                 const int c0 = run.owner(d.at), c1 = run.owner(d.at + d.units - 1);
                 arrive(&sh.met);
                 if (!(ok = wait(&sh.met, meets++))) break;
-                if (tid == 0) {
+                if (m == 0) {
                     sh.last = atomic_add_acq_rel_gpu(pk.counters + c0, 1) == c1 - c0;
                     if (sh.last) pk.counters[c0] = 0;
                 }
@@ -496,10 +582,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                         return pk.part + (int64_t)(2 * c + (run.start(c) >= d.at ? 0 : 1)) * SLOT;
                     };
                     float mx = -INFINITY;
+#pragma unroll 1
                     for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, __ldcg(slot_of(c) + PT_M * HD + m));
                     const float ms = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-                    for (int i = 0; i < HV / 2; ++i) o[i] = 0ull;
+                    for (int i = 0; i < HD / 2; ++i) o[i] = 0ull;
                     l = 0.f;
 #pragma unroll 1
                     for (int c = c0; c <= c1; ++c) {
@@ -508,8 +595,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                         l += __ldcg(sl + PT_M * (HD + 1) + m) * f;
                         const uint64_t f2 = pk2(f, f);
 #pragma unroll
-                        for (int i = 0; i < HV / 4; ++i) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4*>(sl) + (i + HV / 4 * wg) * PT_M + m);
+                        for (int i = 0; i < HD / 4; ++i) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(sl) + i * PT_M + m);
                             o[2 * i] = fma2(pk2(v.x, v.y), f2, o[2 * i]);
                             o[2 * i + 1] = fma2(pk2(v.z, v.w), f2, o[2 * i + 1]);
                         }
@@ -517,13 +604,23 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                     mr = mx;
                 }
             }
-            if (write) write_out();
+            if (write) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                float4* dst = reinterpret_cast<float4*>(pk.out + row * pk.out_stride + (int64_t)head * HD);
+#pragma unroll
+                for (int i = 0; i < HD / 4; ++i) {
+                    float4 v;
+                    upk2(o[2 * i], v.x, v.y), upk2(o[2 * i + 1], v.z, v.w);
+                    dst[i] = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                }
+                if (pk.lse) pk.lse[row * pk.heads + head] = l == 0.f ? -INFINITY : (mr + log2f(l)) * 0.693147180559945f;
+            }
         }
     } else if (wg == 2) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         // ================ operand tiles in f16
         const int w = wid - 8;
-        int tau = 0, stage = 0, uses = 0;  // uses: stages taken so far
+        int tau = 0;
         PtItem d;
         bool ok = true;
 #pragma unroll 1
@@ -579,7 +676,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                 if (!(ok = wait(&sh.k_empty[b], n + 1))) break;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
-                    if (!(ok = wait(&sh.raw_full[stage], uses / PT_STAGES))) break;
+                    const int idx = 4 * tau + half, stage = idx % PT_STAGES;
+                    if (!(ok = wait(&sh.raw_full[stage], idx / PT_STAGES))) break;
                     const unsigned char* src = sh.raw[stage];
 #pragma unroll
                     for (int i = 0; i < HD / 32; ++i) {  // (HD / 16 chunks) x 8 groups of 8 rows, 4 warps x 4 chunks at a time
@@ -596,51 +694,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                         *reinterpret_cast<uint4*>(dst + 128) = make_uint4(h[4], h[5], h[6], h[7]);
                     }
                     arrive(&sh.raw_empty[stage]);
-                    stage = stage + 1 == PT_STAGES ? 0 : stage + 1;
-                    ++uses;
                 }
                 if (!ok) break;
                 fence_async();
                 arrive(&sh.k_full[b]);
-                // values: transposed; a lane 4 dimensions of 8 positions
-                if (!(ok = wait(&sh.v_empty[b], n + 1))) break;
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    if (!(ok = wait(&sh.raw_full[stage], uses / PT_STAGES))) break;
-                    const unsigned char* src = sh.raw[stage];
-                    const int past = d.end - (d.t0 + x) * PT_P - PT_HALF * half;  // positions of the half before the end
-#pragma unroll
-                    for (int i = 0; i < HD / 64; ++i) {
-                        const int task = (i * 128 + 32 * w + lane);
-                        const int d4 = task % (HD / 4), p8 = task / (HD / 4);  // of 8 groups of 8 positions
-                        uint32_t in[8], h[4][4];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            in[j] = *reinterpret_cast<const uint32_t*>(src + raw_off<HD>(8 * p8 + j, d4 >> 2) + 4 * (d4 & 3));
-                        if (WORDS == Q8_KV_E4M3 && past < 8 * p8 + 8) {  // (words past the end may stand for NaN)
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (8 * p8 + j >= past) in[j] = 0u;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t a = words_flip<WORDS>(__byte_perm(in[2 * j], in[2 * j + 1], 0x5140));
-                            const uint32_t c = words_flip<WORDS>(__byte_perm(in[2 * j], in[2 * j + 1], 0x7362));
-                            h[0][j] = words2_f16<WORDS, 0>(a), h[1][j] = words2_f16<WORDS, 1>(a);
-                            h[2][j] = words2_f16<WORDS, 0>(c), h[3][j] = words2_f16<WORDS, 1>(c);
-                        }
-                        unsigned char* dst = sh.v[b] + (uint32_t)(d4 >> 1) * SBO_V + (uint32_t)(p8 + 8 * half) * 128 + (uint32_t)(d4 & 1) * 64;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            *reinterpret_cast<uint4*>(dst + 16 * j) = make_uint4(h[j][0], h[j][1], h[j][2], h[j][3]);
-                    }
-                    arrive(&sh.raw_empty[stage]);
-                    stage = stage + 1 == PT_STAGES ? 0 : stage + 1;
-                    ++uses;
-                }
-                if (!ok) break;
-                fence_async();
-                arrive(&sh.v_full[b]);
             }
         }
     } else {
@@ -657,9 +714,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                 if (lane == 0) {
                     const uint32_t p_at = tmem + 128 * b, t_at = tmem + 256 + 128 * b;
                     const uint64_t dv = tc_desc(sh.v[b], SBO_V);
-#pragma unroll
+#pragma unroll 1
                     for (int part = 1; part >= 0; --part)  // the small parts first
-#pragma unroll
+#pragma unroll 2
                         for (int j = 0; j < PT_P / 16; ++j)  // 16 positions: 8 columns of weights, two core matrices
                             tc_mma_f16_ta(t_at, p_at + 16 * j + 8 * part, dv + j * (256 >> 4), id_o,
                                           part == 1 && j == 0 ? 0u : 1u);
@@ -686,9 +743,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                     tc_fence_after();
                     if (lane == 0) {
                         const uint64_t dh = tc_desc(sh.qh, SBO_Q), dl = tc_desc(sh.ql, SBO_Q), dk = tc_desc(sh.k[b], SBO_Q);
-#pragma unroll
+#pragma unroll 1
                         for (int part = 1; part >= 0; --part)
-#pragma unroll
+#pragma unroll 2
                             for (int j = 0; j < HD / 16; ++j)
                                 tc_mma_f16(tmem + 128 * b, (part ? dl : dh) + j * (256 >> 4), dk + j * (256 >> 4), id_s,
                                            part == 1 && j == 0 ? 0u : 1u);
@@ -703,8 +760,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
             }
             if (ok && pending) weigh(tau - 1);
             if (lane == 0) tc_commit(&sh.drained);  // nothing is in flight when the CTA gives its tensor memory back
-#pragma unroll 1
-            for (unsigned i = 0; i < PT_WAIT && !try_wait(&sh.drained, 0); ++i) {}
+            drain(&sh.drained, 0);
         } else if (wid == 13) {
             // ================ copies of the words: 16 positions of the head a box, a lane a box
             int stage = 0, uses = 0;
@@ -735,8 +791,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                 }
             }
             for (int u = max(0, uses - PT_STAGES); u < uses; ++u)  // no copy is in flight when the CTA leaves
-#pragma unroll 1
-                for (unsigned i = 0; i < PT_WAIT && !try_wait(&sh.raw_full[u % PT_STAGES], (u / PT_STAGES) & 1); ++i) {}
+                drain(&sh.raw_full[u % PT_STAGES], (u / PT_STAGES) & 1);
         } else if (wid == 15) {
             // ================ items and scales
             int b = run.seq;
