@@ -293,49 +293,87 @@ def moe_down_combine(dq, ds, d, mode, k, ids, gates, y, h=None, hq=None, hs=None
                                 ws.handle if ws else None, _stream(stream)))
 
 
-def _refuse(cond, msg):
-    if cond:
-        raise Q8Error(-1, msg)
+_torch = None
 
 
-def _elsewhere(t):
-    """Whether t is not on the current device."""
-    import torch
+def _lazy_torch():
+    """torch, imported on first use (the calls below run once a layer: they look a module up once)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _refuse(msg):
+    raise Q8Error(-1, msg)
+
+
+def _device(t, name):
+    """The device of tensor t, which has to be the current one."""
     d = t.get_device()
-    return d < 0 or d != torch.cuda.current_device()
+    if d < 0 or d != _lazy_torch().cuda.current_device():
+        _refuse(f"{name}: not on the current device")
+    return d
 
 
-def _rows(t, heads, hd, name):
+_raw_stream = None
+
+
+def _stream_of(stream, device):
+    """The stream of a call on `device`: the one given, or torch's current one (by the handle alone where this torch has
+    a call for it: building a Stream object takes longer than the launch)."""
+    global _raw_stream
+    if stream is not None:
+        return int(stream)
+    if _raw_stream is None:
+        _raw_stream = getattr(_torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda d: _torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(device)
+
+
+def _rows(t, heads, hd, device, name):
     """The address and row stride of f32 rows [rows, heads, hd] whose heads are consecutive."""
-    import torch
-    _refuse(t.dtype != torch.float32 or _elsewhere(t), f"{name}: not an f32 tensor of the current device")
+    if t.dtype is not _torch.float32 or t.get_device() != device:
+        _refuse(f"{name}: not an f32 tensor of the current device")
     shape, stride = t.shape, t.stride()
-    _refuse(len(shape) != 3 or shape[1] != heads or shape[2] != hd, f"{name}: {tuple(shape)}, expected [rows, {heads}, {hd}]")
-    _refuse(stride[2] != 1 or (heads > 1 and stride[1] != hd), f"{name}: the heads of a row are not consecutive")
+    if len(shape) != 3 or shape[1] != heads or shape[2] != hd:
+        _refuse(f"{name}: {tuple(shape)}, expected [rows, {heads}, {hd}]")
+    if stride[2] != 1 or (heads > 1 and stride[1] != hd):
+        _refuse(f"{name}: the heads of a row are not consecutive")
     return t.data_ptr(), stride[0] if shape[0] > 1 else heads * hd
 
 
-def _vec(t, n, name):
+def _vec(t, n, device, name):
     """The address of a contiguous device f32 tensor of n values (None: NULL)."""
     if t is None:
         return None
-    import torch
-    _refuse(t.dtype != torch.float32 or _elsewhere(t) or not t.is_contiguous() or t.numel() != n,
-            f"{name}: not a contiguous f32 tensor of {n} values on the current device")
+    if t.dtype is not _torch.float32 or t.get_device() != device or t.numel() != n or not t.is_contiguous():
+        _refuse(f"{name}: not a contiguous f32 tensor of {n} values on the current device")
     return t.data_ptr()
 
 
 def kv_pages(k, ks, v, vs) -> q8_kv_pages:
     """Pages over device tensors: words k and v [pages, kv_heads, page_size, head_dim] (int8 or float8_e4m3fn), scales ks
     and vs f32 [pages, kv_heads, page_size].  The tensors must outlive the struct."""
-    import torch
-    words = {torch.int8: KV_INT8, torch.float8_e4m3fn: KV_E4M3}.get(k.dtype)
-    shape = k.shape
-    _refuse(words is None or len(shape) != 4, "k: not int8 or e4m3 words [pages, kv_heads, page_size, head_dim]")
-    for t, kind, want, name in ((k, k.dtype, shape, "k"), (v, k.dtype, shape, "v"), (ks, torch.float32, shape[:3], "ks"),
-                                (vs, torch.float32, shape[:3], "vs")):
-        _refuse(t.dtype != kind or t.shape != want or not t.is_contiguous() or _elsewhere(t),
-                f"{name}: not a contiguous {kind} tensor {tuple(want)} on the current device")
+    torch = _lazy_torch()
+    kind, shape = k.dtype, k.shape
+    if kind is torch.int8:
+        words = KV_INT8
+    elif kind is torch.float8_e4m3fn:
+        words = KV_E4M3
+    else:
+        _refuse("k: not int8 or e4m3 words")
+    if len(shape) != 4 or v.dtype is not kind or v.shape != shape:
+        _refuse("k, v: not words [pages, kv_heads, page_size, head_dim] of one type")
+    scales = shape[:3]
+    if ks.dtype is not torch.float32 or vs.dtype is not torch.float32 or ks.shape != scales or vs.shape != scales:
+        _refuse(f"ks, vs: not f32 {tuple(scales)}")
+    if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
+        _refuse("pages: not contiguous")
+    d = _device(k, "k")
+    if v.get_device() != d or ks.get_device() != d or vs.get_device() != d:
+        _refuse("pages: not all on the current device")
     return q8_kv_pages(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape[0], shape[2], shape[1], shape[3],
                        words)
 
@@ -343,77 +381,90 @@ def kv_pages(k, ks, v, vs) -> q8_kv_pages:
 def kv_batch(row_start, kv_len, table, error=None) -> q8_kv_batch:
     """A batch of sequences over pages (q8moe.h, q8_kv_batch): device int32 row_start [seqs + 1], kv_len [seqs] and table
     [seqs, pages], and optionally an int32 error word.  The tensors must outlive the struct."""
-    import torch
-    seqs = kv_len.shape[0]
-    _refuse(kv_len.dim() != 1 or row_start.shape != (seqs + 1,) or table.dim() != 2 or table.shape[0] != seqs,
-            "batch: expected row_start [seqs + 1], kv_len [seqs], table [seqs, pages]")
-    for t, name in ((row_start, "row_start"), (kv_len, "kv_len"), (table, "table"), (error, "error")):
-        if t is not None:
-            _refuse(t.dtype != torch.int32 or _elsewhere(t) or (t.numel() > 1 and t.shape[-1] > 1 and t.stride(-1) != 1),
-                    f"{name}: not an int32 tensor of consecutive values on the current device")
-    _refuse(error is not None and error.numel() != 1, "error: not one value")
-    pages = table.shape[1]
+    i32 = _lazy_torch().int32
+    shape = table.shape
+    if len(shape) != 2 or kv_len.dim() != 1 or row_start.dim() != 1:
+        _refuse("batch: expected row_start [seqs + 1], kv_len [seqs], table [seqs, pages]")
+    seqs, pages = shape
+    if kv_len.shape[0] != seqs or row_start.shape[0] != seqs + 1:
+        _refuse("batch: expected row_start [seqs + 1], kv_len [seqs], table [seqs, pages]")
+    if table.dtype is not i32 or kv_len.dtype is not i32 or row_start.dtype is not i32:
+        _refuse("batch: not int32")
+    strides = table.stride()
+    if not (kv_len.is_contiguous() and row_start.is_contiguous() and (pages <= 1 or strides[1] == 1)):
+        _refuse("batch: values not consecutive")
+    d = _device(table, "table")
+    if kv_len.get_device() != d or row_start.get_device() != d:
+        _refuse("batch: not all on the current device")
+    e = None
+    if error is not None:
+        if error.dtype is not i32 or error.numel() != 1 or error.get_device() != d:
+            _refuse("error: not one int32 value on the current device")
+        e = error.data_ptr()
     return q8_kv_batch(row_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), seqs, pages,
-                       table.stride(0) if seqs > 1 else pages, error.data_ptr() if error is not None else None)
+                       strides[0] if seqs > 1 else pages, e)
 
 
 def q8_rope_table(theta, cos, sin, stream=None):
     """Fills cos and sin (device f32 [positions, head_dim/2]) with the rotation tables of base theta."""
     n, half = cos.shape
-    _check(lib.q8_rope_table(float(theta), n, 2 * half, _vec(cos, n * half, "cos"), _vec(sin, n * half, "sin"),
-                             _stream(stream)))
+    d = _device(cos, "cos")
+    _check(lib.q8_rope_table(float(theta), n, 2 * half, _vec(cos, n * half, d, "cos"), _vec(sin, n * half, d, "sin"),
+                             _stream_of(stream, d)))
 
 
 def q8_kv_append(pages, batch, q, k, v, q_out, q_norm=None, k_norm=None, eps=1e-6, cos=None, sin=None, stream=None):
     """Norms and rotates the rows' query and key heads (q [rows, heads, hd] into q_out; k, v [rows, kv_heads, hd]) and
     quantizes the keys and values into their page slots.  q and q_out may be None (keys and values only)."""
     kv, hd = pages.kv_heads, pages.head_dim
-    rows = k.shape[0]
-    _refuse(v.shape[0] != rows or (q is None) != (q_out is None), "q, k, v, q_out: rows differ")
+    rows, d = k.shape[0], _device(k, "k")
+    if v.shape[0] != rows or (q is None) != (q_out is None):
+        _refuse("q, k, v, q_out: rows differ")
     heads, qa, qs, oa, os_ = 0, None, 0, None, 0
     if q is not None:
         heads = q.shape[1]
-        _refuse(q.shape[0] != rows or q_out.shape[0] != rows, "q, k, v, q_out: rows differ")
-        qa, qs = _rows(q, heads, hd, "q")
-        oa, os_ = _rows(q_out, heads, hd, "q_out")
-    ka, ks = _rows(k, kv, hd, "k")
-    va, vs = _rows(v, kv, hd, "v")
+        if q.shape[0] != rows or q_out.shape[0] != rows:
+            _refuse("q, k, v, q_out: rows differ")
+        qa, qs = _rows(q, heads, hd, d, "q")
+        oa, os_ = _rows(q_out, heads, hd, d, "q_out")
+    ka, ks = _rows(k, kv, hd, d, "k")
+    va, vs = _rows(v, kv, hd, d, "v")
     positions = cos.shape[0] if cos is not None else 0
-    _check(lib.q8_kv_append(ctypes.byref(pages), ctypes.byref(batch), rows, heads, qa, qs, ka, ks, va, vs,
-                            _vec(q_norm, hd, "q_norm"), _vec(k_norm, hd, "k_norm"), eps,
-                            _vec(cos, positions * hd // 2, "cos"), _vec(sin, positions * hd // 2, "sin"), positions, oa, os_,
-                            _stream(stream)))
+    _check(lib.q8_kv_append(pages, batch, rows, heads, qa, qs, ka, ks, va, vs, _vec(q_norm, hd, d, "q_norm"),
+                            _vec(k_norm, hd, d, "k_norm"), eps, _vec(cos, positions * hd // 2, d, "cos"),
+                            _vec(sin, positions * hd // 2, d, "sin"), positions, oa, os_, _stream_of(stream, d)))
 
 
 def q8_kv_read(pages, batch, k_out=None, v_out=None, stream=None):
     """The values of the batch's rows into k_out and v_out [rows, kv_heads, hd] (either may be None; rows and heads any
     multiple of 8 values apart, as in the transposed view of a dense cache [kv_heads, ctx, hd])."""
-    import torch
     kv, hd = pages.kv_heads, pages.head_dim
     one = k_out if k_out is not None else v_out
-    _refuse(one is None, "k_out and v_out: both None")
-    rows = one.shape[0]
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is not None:
-            _refuse(t.dtype != torch.float32 or _elsewhere(t) or t.shape != (rows, kv, hd) or t.stride(2) != 1 or
-                    t.stride() != one.stride(),
-                    f"{name}: not f32 [rows, {kv}, {hd}] on the current device, laid out as the other")
-    rs, hs = one.stride(0) if rows > 1 else kv * hd, one.stride(1) if kv > 1 else hd
-    _check(lib.q8_kv_read(ctypes.byref(pages), ctypes.byref(batch), rows, _ptr(k_out), _ptr(v_out), rs, hs,
-                          _stream(stream)))
+    if one is None:
+        _refuse("k_out and v_out: both None")
+    d, shape, strides, f32 = _device(one, "k_out, v_out"), one.shape, one.stride(), _torch.float32
+    if len(shape) != 3 or shape[1] != kv or shape[2] != hd or strides[2] != 1 or one.dtype is not f32:
+        _refuse(f"k_out, v_out: not f32 [rows, {kv}, {hd}] with consecutive values")
+    if one is k_out and v_out is not None:
+        if v_out.dtype is not f32 or v_out.get_device() != d or v_out.shape != shape or v_out.stride() != strides:
+            _refuse("v_out: not laid out as k_out")
+    rows = shape[0]
+    _check(lib.q8_kv_read(pages, batch, rows, k_out.data_ptr() if k_out is not None else None,
+                          v_out.data_ptr() if v_out is not None else None, strides[0] if rows > 1 else kv * hd,
+                          strides[1] if kv > 1 else hd, _stream_of(stream, d)))
 
 
 def q8_paged_attention(pages, batch, q, out, scale=None, lse=None, ws=None, stream=None):
     """Causal attention of the rows q [rows, heads, hd] over their sequences' cached positions, into out; scale defaults
     to hd^-1/2, lse (optional) is f32 [rows, heads]."""
-    hd = pages.head_dim
+    hd, d = pages.head_dim, _device(q, "q")
     rows, heads = q.shape[0], q.shape[1]
-    qa, qs = _rows(q, heads, hd, "q")
-    oa, os_ = _rows(out, heads, hd, "out")
-    _refuse(out.shape[0] != rows, "out: rows differ")
-    _check(lib.q8_paged_attention(ctypes.byref(pages), ctypes.byref(batch), rows, heads, qa, qs,
-                                  hd ** -0.5 if scale is None else scale, oa, os_, _vec(lse, rows * heads, "lse"),
-                                  ws.handle if ws else None, _stream(stream)))
+    qa, qs = _rows(q, heads, hd, d, "q")
+    oa, os_ = _rows(out, heads, hd, d, "out")
+    if out.shape[0] != rows:
+        _refuse("out: rows differ")
+    _check(lib.q8_paged_attention(pages, batch, rows, heads, qa, qs, hd ** -0.5 if scale is None else scale, oa, os_,
+                                  _vec(lse, rows * heads, d, "lse"), ws.handle if ws else None, _stream_of(stream, d)))
 
 
 class Model:
