@@ -32,7 +32,8 @@ constexpr int PR_WARPS = 16, PR_THREADS = PR_WARPS * 32;
 constexpr int PR_UNIT = 128;   // positions a unit
 constexpr int PR_STEP = 16;    // positions a warp takes at a time
 constexpr int PR_FLUSH = 8;    // steps between additions to the totals
-constexpr int PR_PEXP = 14;    // weights are split as values of up to 2^(PR_PEXP + 1)
+// Weights times value scales are split as values of up to 65472 (f16 holds 65504): PR_TOP times a scale below 2.
+constexpr float PR_TOP = 32736.f;
 
 // The bytes of w (flipped by 0x80 each for int8) that `SEL` picks, two of them, as two f16 values.
 template <int WORDS, int HALF>
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedPa
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
     const int G = pk.group;
 
-    auto tiles_of = [&](const KvSeq& s) { return (s.n * G + MT - 1) / MT; };
+    auto tiles_of = [&](const KvSeq& s) { return (s.n * G + MT - 1) / MT; };  // (MT is a power of two)
     auto span_of = [&](const KvSeq& s) -> int64_t {  // units of one item
         return s.len_ok ? (s.len + PR_UNIT - 1) / PR_UNIT : 1;
     };
@@ -150,63 +151,15 @@ __global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedPa
             b_at += n_units;
             s = kv_seq(kv, ++b);
         }
-        const int64_t U = span_of(s), tiles = tiles_of(s), item = (cur - b_at) / U;
-        const int h = (int)(item / tiles);
-        const int64_t m0 = item % tiles * MT;  // the item's first vector
+        const int64_t U = span_of(s), tiles = tiles_of(s), item = div_small(cur - b_at, U);
+        const int h = (int)div_small(item, tiles);
+        const int64_t m0 = (item - h * tiles) * MT;  // the item's first vector
         const int64_t item_at = b_at + item * U;
         const int64_t u0 = cur - item_at, u1 = min(U, u0 + (run.hi - cur));
         const int end = s.len_ok ? (int)min((int64_t)s.len, u1 * PR_UNIT) : 0;  // positions before which the piece ends
         const int begin = (int)(u0 * PR_UNIT);
 
-        // ---- the item's queries: a warp a vector, split into two f16 parts after a scaling by a power of two
-        if (wid < MT) {
-            const int64_t m = m0 + wid;
-            const bool valid = m < s.n * G;
-            const int64_t row = s.first + m / G;
-            const int head = h * G + (int)(m % G);
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (valid && lane < HD / 4)
-                x = *reinterpret_cast<const float4*>(pk.q + row * pk.q_stride + (int64_t)head * HD + 4 * lane);
-            const unsigned big = __reduce_max_sync(
-                0xffffffffu, max(max(__float_as_uint(fabsf(x.x)), __float_as_uint(fabsf(x.y))),
-                                 max(__float_as_uint(fabsf(x.z)), __float_as_uint(fabsf(x.w)))));
-            const int e = big == 0u ? 0 : 14 - exponent_of(big);
-            const float f = pow2i(e);
-            uint4 r;
-            split2(x.x * f, x.y * f, r.x, r.z);
-            split2(x.z * f, x.w * f, r.y, r.w);
-            if (lane < HD / 4) sh.q[wid / 8][lane % KS][(wid % 8) * 4 + lane / KS] = r;
-            if (lane == 0) {
-                sh.qf[wid] = pow2i(-e) * pk.scale;
-                sh.lim[wid] = valid && s.len_ok ? (int)(s.len - s.n + m / G) : -1;
-                sh.at[wid] = valid ? row * pk.out_stride + (int64_t)head * HD : -1;
-                sh.lse_at[wid] = row * pk.heads + head;
-            }
-        }
-        __syncthreads();
-
-        // ---- this warp's positions
-        float m_run[NT][2], l_run[NT][2], fac[NT][2], qf[NT][2];
-        int lim[NT][2];
-        float acc[NT][HD / 16][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                m_run[n][c] = -INFINITY;
-                l_run[n][c] = 0.f;
-                fac[n][c] = 1.f;
-                qf[n][c] = sh.qf[8 * n + 2 * t + c];
-                lim[n][c] = sh.lim[8 * n + 2 * t + c];
-            }
-#pragma unroll
-            for (int i = 0; i < HD / 16; ++i) {
-                sh.o[wid][n * (HD / 16) + i][lane] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) acc[n][i][c] = 0.f;
-            }
-        }
-        int exp_run = -100, exp_top = -100;  // the weights' scaling, and the largest it has been
+        // ---- this warp's first positions are on their way while the queries are prepared
         const int steps = end > begin ? (end - begin + PR_STEP - 1) / PR_STEP : 0;  // of all warps
         Bytes<KB> kw[2];
         Bytes<DPG> vw[4];
@@ -237,6 +190,14 @@ __global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedPa
 #pragma unroll
             for (int j = 0; j < 2; ++j) vs[j] = ld_scale_stream(kv.vs + row + g + 8 * j);
         };
+        auto fetch = [&](int i) {  // brings step i's words towards L2 (16 rows of a page are consecutive), i <= 31 of its batch
+            int pg;
+            const int64_t row = row_of(i, pg);
+            if (lane == 0 && pg >= 0) {
+                l2_prefetch_piece((const char*)(kv.k + row * HD), PR_STEP * HD);
+                l2_prefetch_piece((const char*)(kv.v + row * HD), PR_STEP * HD);
+            }
+        };
         const int mine = steps > wid ? (steps - wid + PR_WARPS - 1) / PR_WARPS : 0;
         int page = -1, page_next = -1;
         int64_t row_next = 0;
@@ -245,7 +206,58 @@ __global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedPa
             row_next = row_of(0, page_next);
             load_k(row_next);
             load_v(row_next);
+            if (mine > 1) fetch(1);
         }
+        // ---- the item's queries: a warp a vector, split into two f16 parts after a scaling by a power of two
+        if (wid < MT) {
+            const int64_t m = m0 + wid;
+            const bool valid = m < s.n * G;
+            const int token = (int)div_small(m, G);
+            const int64_t row = s.first + token;
+            const int head = h * G + (int)(m - (int64_t)token * G);
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (valid && lane < HD / 4)
+                x = *reinterpret_cast<const float4*>(pk.q + row * pk.q_stride + (int64_t)head * HD + 4 * lane);
+            const unsigned big = __reduce_max_sync(
+                0xffffffffu, max(max(__float_as_uint(fabsf(x.x)), __float_as_uint(fabsf(x.y))),
+                                 max(__float_as_uint(fabsf(x.z)), __float_as_uint(fabsf(x.w)))));
+            const int e = big == 0u ? 0 : 14 - exponent_of(big);
+            const float f = pow2i(e);
+            uint4 r;
+            split2(x.x * f, x.y * f, r.x, r.z);
+            split2(x.z * f, x.w * f, r.y, r.w);
+            if (lane < HD / 4) sh.q[wid / 8][lane % KS][(wid % 8) * 4 + lane / KS] = r;
+            if (lane == 0) {
+                sh.qf[wid] = pow2i(-e) * pk.scale;
+                sh.lim[wid] = valid && s.len_ok ? (int)(s.len - s.n + token) : -1;
+                sh.at[wid] = valid ? row * pk.out_stride + (int64_t)head * HD : -1;
+                sh.lse_at[wid] = row * pk.heads + head;
+            }
+        }
+        __syncthreads();
+
+        // ---- this warp's positions
+        float m_run[NT][2], l_run[NT][2], fac[NT][2], qf[NT][2];
+        int lim[NT][2];
+        float acc[NT][HD / 16][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                m_run[n][c] = -INFINITY;
+                l_run[n][c] = 0.f;
+                fac[n][c] = 1.f;
+                qf[n][c] = sh.qf[8 * n + 2 * t + c];
+                lim[n][c] = sh.lim[8 * n + 2 * t + c];
+            }
+#pragma unroll
+            for (int i = 0; i < HD / 16; ++i) {
+                sh.o[wid][n * (HD / 16) + i][lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[n][i][c] = 0.f;
+            }
+        }
+        int exp_run = -100, exp_top = -100;  // the weights' scaling, and the largest it has been
 #pragma unroll 1
         for (int i = 0; i < mine; ++i) {
             page = page_next;
@@ -253,6 +265,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedPa
             if (i + 1 < mine) {
                 if (((i + 1) & 31) == 0) look_up(i + 1);
                 row_next = row_of(i + 1, page_next);
+                if (i + 2 < mine && ((i + 2) & 31) != 0) fetch(i + 2);
             }
             // scores: positions g, g + 8 by vectors 2t, 2t + 1 of each tile
             float sh_hi[NT][4], sh_lo[NT][4];
@@ -288,9 +301,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedPa
             if (vtop != 0u) {
                 const int e = exponent_of(vtop);
                 exp_top = max(exp_top, e);
-                exp_run = max(e, exp_top - 40);  // (so that rescaling the sums never overflows)
+                // (kept while the tile's largest scale is within its octave or the one below: fewer rescalings; and not
+                // far below what it was, so that rescaling the sums never overflows)
+                if (e > exp_run || e < exp_run - 1) exp_run = max(e, exp_top - 40);
             }
-            const float wscale = pow2i(PR_PEXP - exp_run);
+            const float wscale = pow2i(-exp_run) * PR_TOP;
             const float eshift = exp_old - exp_run <= -126 ? 0.f : pow2i(exp_old - exp_run);
             uint32_t ph[NT][2], pl[NT][2];
             bool same = true;
@@ -389,7 +404,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedPa
                 if (g == 0) {
                     sh.m[wid][8 * n + 2 * t + c] = m_run[n][c];
                     sh.l[wid][8 * n + 2 * t + c] = l;
-                    sh.f[wid][8 * n + 2 * t + c] = pow2i(exp_run - PR_PEXP);
+                    sh.f[wid][8 * n + 2 * t + c] = pow2i(exp_run) * (1.f / PR_TOP);
                 }
             }
         __syncthreads();
@@ -441,9 +456,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedPa
             __syncthreads();
             if (sh.last) {
                 if (tid == 0) pk.counters[c0] = 0;
-                auto slot_of = [&](int c) {  // (the first CTA's piece may be the last of its run, the others' open theirs)
-                    return pk.part + (int64_t)(2 * c + (run.start(c) >= item_at ? 0 : 1)) * SLOT;
-                };
+                const bool opens = run.start(c0) == item_at;
+                auto slot_of = [&](int c) { return pk.part + (int64_t)paged_slot(c, c0, opens) * SLOT; };
                 if (tid < MT) {
                     float Mx = -INFINITY, Lx = 0.f;
                     for (int c = c0; c <= c1; ++c) Mx = fmaxf(Mx, __ldcg(slot_of(c) + FR * 128 + tid));

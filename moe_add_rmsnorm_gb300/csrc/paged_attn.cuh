@@ -32,6 +32,11 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// a / b for a, b >= 0, in 32 bits where both fit (a 64-bit division is about a hundred instructions).
+__device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // The launch's units in one line, sequence by sequence, cut into equal runs: CTA c takes units c*T/C .. (c+1)*T/C - 1 of
 // T, so ragged batches load every SM alike, whatever the device arrays hold when the launch runs.  C is the launch's
 // CTAs, or T when there are fewer units (the other CTAs leave), so every CTA below C has a unit.
@@ -40,8 +45,8 @@ struct PagedRun {
     int ctas = 0;
     int seq = 0;          // the sequence of unit lo
     int64_t seq_at = 0;   // its first unit
-    __device__ int64_t start(int64_t c) const { return c * total / ctas; }
-    __device__ int owner(int64_t unit) const { return (int)(((unit + 1) * ctas - 1) / total); }
+    __device__ int64_t start(int64_t c) const { return div_small(c * total, ctas); }
+    __device__ int owner(int64_t unit) const { return (int)div_small((unit + 1) * ctas - 1, total); }
 };
 
 // Forms the run; `units(s)` is a sequence's unit count (0: not this kernel's).  Every thread of the CTA calls it.  Each
@@ -102,6 +107,10 @@ __device__ __forceinline__ PagedRun paged_run(const PagedParams& pk, Units units
     r.seq_at = found_at;
     return r;
 }
+
+// The slot of the partial results where CTA c leaves its piece of the item whose first unit is `item_at`: its first when
+// the piece opens its run.  (Only the item's first CTA, c0, may have units before the item's.)
+__device__ __forceinline__ int paged_slot(int c, int c0, bool c0_opens) { return 2 * c + (c == c0 && !c0_opens ? 1 : 0); }
 
 // Whether a sequence is one of this launch's.
 __device__ __forceinline__ bool paged_takes(const PagedParams& pk, const KvSeq& s) {

@@ -31,7 +31,6 @@ namespace {
 constexpr int PT_M = 128, PT_P = 128;      // query vectors and positions a tile
 constexpr int PT_THREADS = 512;
 constexpr int PT_HALF = 64;                // positions a copied stage
-constexpr int PT_STAGES = 3;
 constexpr int PT_ITEMS = 4;                // items dealt out ahead
 constexpr int PT_READERS = 14;             // warps that read an item
 constexpr unsigned PT_POLL_NS = 20000;     // the longest the hardware may hold a warp at a poll
@@ -53,7 +52,7 @@ template <int HD>
 struct PtShared {
     static constexpr uint32_t SBO_Q = HD / 8 * 128;        // bytes between 8-row groups of queries and keys
     static constexpr uint32_t SBO_V = PT_P / 8 * 128 + 16; // and of transposed values (the pad spreads the writes' banks)
-    unsigned char raw[PT_STAGES][PT_HALF * HD];
+    unsigned char raw_k[2][PT_HALF * HD], raw_v[PT_HALF * HD];  // copied words: a tile's keys, half a tile's values
     unsigned char qh[PT_M * HD * 2], ql[PT_M * HD * 2];
     unsigned char k[2][PT_P * HD * 2];
     unsigned char v[2][HD / 8 * SBO_V];
@@ -64,7 +63,7 @@ struct PtShared {
     float ce[2];
     unsigned groups[2];    // which 16-position groups of a tile are there
     PtItem item[PT_ITEMS];
-    uint64_t d_full[PT_ITEMS], d_empty[PT_ITEMS], raw_full[PT_STAGES], raw_empty[PT_STAGES];
+    uint64_t d_full[PT_ITEMS], d_empty[PT_ITEMS], rk_full[2], rk_empty[2], rv_full, rv_empty;
     uint64_t sc_full[2], sc_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t s_full[2], p_full[2], t_full[2], t_empty[2], q_full, q_empty, fin_full, fin_empty, met, drained;
     uint32_t tmem;
@@ -287,8 +286,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
 
     if (tid == 0) {
         for (int i = 0; i < PT_ITEMS; ++i) mbar_init(&sh.d_full[i], 1), mbar_init(&sh.d_empty[i], PT_READERS);
-        for (int i = 0; i < PT_STAGES; ++i) mbar_init(&sh.raw_full[i], 1), mbar_init(&sh.raw_empty[i], 4);
+        mbar_init(&sh.rv_full, 1), mbar_init(&sh.rv_empty, 4);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.rk_full[i], 1), mbar_init(&sh.rk_empty[i], 4);
             mbar_init(&sh.sc_full[i], 1), mbar_init(&sh.sc_empty[i], 4);
             mbar_init(&sh.k_full[i], 4), mbar_init(&sh.k_empty[i], 1);
             mbar_init(&sh.v_full[i], 4), mbar_init(&sh.v_empty[i], 1);
@@ -335,12 +335,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
         return d.t1 > d.t0;
     };
 
-    // Turns copied stage `idx` (64 positions of values) into half of a transposed operand tile; a lane 4 dimensions of 8
-    // positions.  `past`: the half's positions before the sequence's end.
-    auto values_half = [&](int idx, unsigned char* tile, int half, int past) -> bool {
-        const int stage = idx % PT_STAGES;
-        if (!wait(&sh.raw_full[stage], idx / PT_STAGES)) return false;
-        const unsigned char* src = sh.raw[stage];
+    // Turns 64 copied positions of values (a tile's first or second half) into that half of a transposed operand tile; a lane 4
+    // dimensions of 8 positions.  `past`: the half's positions before the sequence's end.
+    auto values_half = [&](unsigned char* tile, int half, int past) -> bool {
+        if (!wait(&sh.rv_full, half)) return false;  // (two copies a tile)
+        const unsigned char* src = sh.raw_v;
 #pragma unroll
         for (int i = 0; i < HD / 64; ++i) {
             const int task = i * 128 + (tid & 127);
@@ -365,7 +364,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
 #pragma unroll
             for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(dst + 16 * j) = make_uint4(h[j][0], h[j][1], h[j][2], h[j][3]);
         }
-        arrive(&sh.raw_empty[stage]);
+        arrive(&sh.rv_empty);
         return true;
     };
 
@@ -508,45 +507,44 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
 #pragma unroll
             for (int i = 0; i < HD / 2; ++i) o[i] = 0ull;
             const int tiles = d.t1 - d.t0;
-            // One step past the last tile: step x turns the values of tile x as soon as tile x - 2's product has left the
-            // buffer, and adds the product of tile x - 1.
+            // Step x, as soon as tile x - 2's product is done (its values' buffer is free then): the values of tile x, and
+            // between their halves, while the second one is copied, tile x - 2's product onto the sums.
 #pragma unroll 1
-            for (int x = 0; x <= tiles; ++x, ++tau) {
+            for (int x = 0; x < tiles + 2; ++x) {
+                const int tx = tau + x, bx = tx & 1, past = d.end - (d.t0 + x) * PT_P;
+                if (x < tiles)
+                    if (!(ok = wait(&sh.v_empty[bx], (tx >> 1) + 1) && values_half(sh.v[bx], 0, past))) break;
+                if (x >= 2) {
+                    const int t = tx - 2;
+                    if (!(ok = wait(&sh.t_full[bx], t >> 1))) break;
+                    tc_fence_after();
+                    if (active) {
+                        const float alpha = sh.alpha[t & 3][m], back = sh.back[t & 3];
+                        const uint64_t al2 = pk2(alpha, alpha), back2 = pk2(back, back);
+                        if (!__all_sync(0xffffffffu, alpha == 1.f)) {  // (a maximum moved)
+#pragma unroll
+                            for (int i = 0; i < HD / 2; ++i) o[i] = mul2(o[i], al2);
+                        }
+#pragma unroll
+                        for (int c = 0; c < HD / 32; ++c) {
+                            uint32_t r[32];
+                            tc_load<32>(tmem + lanes + 256 + 128 * bx + 32 * c, r);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                o[16 * c + i] = fma2(pk2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), back2, o[16 * c + i]);
+                        }
+                    }
+                    tc_fence_before();
+                    arrive(&sh.t_empty[bx]);
+                }
                 if (x < tiles) {
-                    const int b = tau & 1, past = d.end - (d.t0 + x) * PT_P;
-                    ok = wait(&sh.v_empty[b], (tau >> 1) + 1);
-#pragma unroll 1
-                    for (int half = 0; ok && half < 2; ++half)
-                        ok = values_half(4 * tau + 2 + half, sh.v[b], half, past - PT_HALF * half);
-                    if (!ok) break;
+                    if (!(ok = values_half(sh.v[bx], 1, past - PT_HALF))) break;
                     fence_async();
-                    arrive(&sh.v_full[b]);
+                    arrive(&sh.v_full[bx]);
                 }
-                if (x == 0) continue;
-                const int t = tau - 1, b = t & 1;
-                if (!(ok = wait(&sh.t_full[b], t >> 1))) break;
-                tc_fence_after();
-                if (active) {
-                    const float alpha = sh.alpha[t & 3][m], back = sh.back[t & 3];
-                    const uint64_t al2 = pk2(alpha, alpha), back2 = pk2(back, back);
-                    if (!__all_sync(0xffffffffu, alpha == 1.f)) {  // (a maximum moved)
-#pragma unroll
-                        for (int i = 0; i < HD / 2; ++i) o[i] = mul2(o[i], al2);
-                    }
-#pragma unroll
-                    for (int c = 0; c < HD / 32; ++c) {
-                        uint32_t r[32];
-                        tc_load<32>(tmem + lanes + 256 + 128 * b + 32 * c, r);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            o[16 * c + i] = fma2(pk2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), back2, o[16 * c + i]);
-                    }
-                }
-                tc_fence_before();
-                arrive(&sh.t_empty[b]);
             }
             if (!ok) break;
-            --tau;  // (the step past the last tile is no tile)
+            tau += tiles;
             if (!(ok = wait(&sh.fin_full, it))) break;
             float mr = sh.fin_m[m], l = sh.fin_l[m];
             arrive(&sh.fin_empty);
@@ -578,9 +576,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                 if (!(ok = wait(&sh.met, meets++))) break;
                 write = valid && sh.last;
                 if (write) {  // the last CTA to arrive folds the item's pieces in order
-                    auto slot_of = [&](int c) {
-                        return pk.part + (int64_t)(2 * c + (run.start(c) >= d.at ? 0 : 1)) * SLOT;
-                    };
+                    const bool opens = run.start(c0) == d.at;
+                    auto slot_of = [&](int c) { return pk.part + (int64_t)paged_slot(c, c0, opens) * SLOT; };
                     float mx = -INFINITY;
 #pragma unroll 1
                     for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, __ldcg(slot_of(c) + PT_M * HD + m));
@@ -676,9 +673,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                 if (!(ok = wait(&sh.k_empty[b], n + 1))) break;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
-                    const int idx = 4 * tau + half, stage = idx % PT_STAGES;
-                    if (!(ok = wait(&sh.raw_full[stage], idx / PT_STAGES))) break;
-                    const unsigned char* src = sh.raw[stage];
+                    if (!(ok = wait(&sh.rk_full[half], tau))) break;
+                    const unsigned char* src = sh.raw_k[half];
 #pragma unroll
                     for (int i = 0; i < HD / 32; ++i) {  // (HD / 16 chunks) x 8 groups of 8 rows, 4 warps x 4 chunks at a time
                         const int task = i * 4 + w;
@@ -693,7 +689,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                         *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
                         *reinterpret_cast<uint4*>(dst + 128) = make_uint4(h[4], h[5], h[6], h[7]);
                     }
-                    arrive(&sh.raw_empty[stage]);
+                    arrive(&sh.rk_empty[half]);
                 }
                 if (!ok) break;
                 fence_async();
@@ -763,7 +759,24 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
             drain(&sh.drained, 0);
         } else if (wid == 13) {
             // ================ copies of the words: 16 positions of the head a box, a lane a box
-            int stage = 0, uses = 0;
+            // (Keys run a tile ahead of the values, which wait for the tile's turn: in one queue the values would hold the
+            // next tile's keys up.)
+            unsigned nk0 = 0, nk1 = 0, nv = 0;  // copies issued so far
+            auto copy = [&](uint64_t* full, uint64_t* empty, unsigned& issued, unsigned char* to, const CUtensorMap* map,
+                            int half, int row, int page) -> bool {
+                if (!wait(empty, issued + 1)) return false;
+                if (lane == 0) mbar_arrive_expect_tx(full, PT_HALF * HD);
+                __syncwarp();
+                if (lane < PT_P / 16 && lane / 4 == half) tma_box(to + (lane & 3) * 16 * HD, map, row, page, full);
+                ++issued;
+                return true;
+            };
+            int row_v = 0, page_v = 0;
+            bool values = false;  // whether the tile before's values are still to be copied
+            auto copy_values = [&]() -> bool {
+                return copy(&sh.rv_full, &sh.rv_empty, nv, sh.raw_v, &map_v, 0, row_v, page_v) &&
+                       copy(&sh.rv_full, &sh.rv_empty, nv, sh.raw_v, &map_v, 1, row_v, page_v);
+            };
 #pragma unroll 1
             for (int it = 0; ok && next_item(it, d); ++it) {
                 auto page_at = [&](int tl) {  // the page of this lane's 16 positions; past the end or none: one past the
@@ -778,20 +791,18 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                 for (int tl = d.t0; ok && tl < d.t1; ++tl) {
                     const int page = next, row = (d.head << kv.page_log2) + ((tl * PT_P + 16 * lane) & ((1 << kv.page_log2) - 1));
                     next = page_at(tl + 1);
-#pragma unroll 1
-                    for (int part = 0; part < 4; ++part) {  // the keys' halves, then the values'
-                        if (!(ok = wait(&sh.raw_empty[stage], uses / PT_STAGES + 1))) break;
-                        if (lane == 0) mbar_arrive_expect_tx(&sh.raw_full[stage], PT_HALF * HD);
-                        __syncwarp();
-                        if (lane < PT_P / 16 && lane / 4 == (part & 1))
-                            tma_box(sh.raw[stage] + (lane & 3) * 16 * HD, part < 2 ? &map_k : &map_v, row, page, &sh.raw_full[stage]);
-                        stage = stage + 1 == PT_STAGES ? 0 : stage + 1;
-                        ++uses;
-                    }
+                    ok = copy(&sh.rk_full[0], &sh.rk_empty[0], nk0, sh.raw_k[0], &map_k, 0, row, page) &&
+                         copy(&sh.rk_full[1], &sh.rk_empty[1], nk1, sh.raw_k[1], &map_k, 1, row, page);
+                    if (ok && values) ok = copy_values();
+                    values = true;
+                    row_v = row;
+                    page_v = page;
                 }
             }
-            for (int u = max(0, uses - PT_STAGES); u < uses; ++u)  // no copy is in flight when the CTA leaves
-                drain(&sh.raw_full[u % PT_STAGES], (u / PT_STAGES) & 1);
+            if (ok && values) copy_values();
+            if (nk0) drain(&sh.rk_full[0], (nk0 - 1) & 1);  // no copy is in flight when the CTA leaves
+            if (nk1) drain(&sh.rk_full[1], (nk1 - 1) & 1);
+            if (nv) drain(&sh.rv_full, (nv - 1) & 1);
         } else if (wid == 15) {
             // ================ items and scales
             int b = run.seq;

@@ -353,6 +353,27 @@ def test_attention(q8, ws, new, length, heads, kv, hd, page, words):
     assert torch.equal(again[:rows], out[:rows, :heads])
 
 
+@pytest.mark.parametrize("new,length,heads,kv,hd,words", [([1] * 40, [300 + 41 * i for i in range(40)], 32, 4, 128, "int8"),
+                                                          ([700, 1, 90], [700, 3000, 1500], 24, 8, 128, "int8"),
+                                                          ([400, 300], [400, 900], 14, 2, 64, "e4m3"),
+                                                          ([3], [20000], 32, 2, 128, "e4m3")])
+def test_attention_back_to_back(q8, ws, new, length, heads, kv, hd, words):
+    """Many launches in a row, on two batches in turn: every one gives the first one's bits (the order in which CTAs meet
+    decides nothing, and no launch leaves anything behind for the next)."""
+    import torch
+    caches = [Cache(q8, new, length, kv, hd, 16, words, seed) for seed in (31, 32)]
+    q = torch.randn(sum(new), heads, hd, generator=gen(33), device="cuda")
+    first = []
+    for c in caches:
+        first.append(torch.empty_like(q))
+        q8.q8_paged_attention(c.pages(), c.batch(), q, first[-1], ws=ws)
+    outs = [torch.empty_like(q) for _ in range(60)]
+    for i, o in enumerate(outs):
+        q8.q8_paged_attention(caches[i % 2].pages(), caches[i % 2].batch(), q, o, ws=ws)
+    assert all(torch.equal(o, first[i % 2]) for i, o in enumerate(outs))
+    assert caches[0].error.item() == 0 and caches[1].error.item() == 0
+
+
 @pytest.mark.parametrize("new,length,words", [([1, 1], [400, 70], "int8"), ([150, 1], [600, 200], "e4m3")])
 @pytest.mark.parametrize("factor", [0.01, 30.0])
 def test_attention_flat_and_sharp(q8, ws, new, length, words, factor):
