@@ -152,26 +152,20 @@ __device__ __forceinline__ void tc_load(uint32_t taddr, uint32_t (&r)[N]) {
 #pragma unroll
     for (int i = 0; i < N / 16; ++i) tc_wait16(x[i]);
 }
-__device__ __forceinline__ void tc_issue32(uint32_t taddr, uint32_t (&r)[2][16]) {
-    tc_ld16(taddr, r[0]);
-    tc_ld16(taddr + 16, r[1]);
-}
-// Calls f(i, r) for the columns 32 i .. of 128 columns from taddr (r: two times sixteen), the next ones on their way
-// meanwhile.  A loop, not straight code: what the warps of the roles run has to stay within the SM's instruction cache
-// together (with the softmax unrolled the warps waited for instructions most of the time).
+// Calls f(i, r) for the columns 16 i .. of 128 columns from taddr, the next ones on their way meanwhile.  A loop, not
+// straight code: what the warps of the roles run has to stay within the SM's instruction cache together (with the softmax
+// unrolled the warps waited for instructions most of the time).
 template <typename F>
 __device__ __forceinline__ void tc_columns(uint32_t taddr, F f) {
-    uint32_t r0[2][16], r1[2][16];
-    tc_issue32(taddr, r0);
+    uint32_t r0[16], r1[16];
+    tc_ld16(taddr, r0);
 #pragma unroll 1
-    for (int i = 0; i < 4; i += 2) {
-        tc_wait16(r0[0]);
-        tc_wait16(r0[1]);
-        tc_issue32(taddr + 32 * (i + 1), r1);
+    for (int i = 0; i < 8; i += 2) {
+        tc_wait16(r0);
+        tc_ld16(taddr + 16 * (i + 1), r1);
         f(i, r0);
-        tc_wait16(r1[0]);
-        tc_wait16(r1[1]);
-        if (i == 0) tc_issue32(taddr + 64, r0);
+        tc_wait16(r1);
+        if (i < 6) tc_ld16(taddr + 16 * (i + 2), r0);
         f(i + 1, r1);
     }
 }
@@ -313,13 +307,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
     // A bounded wait, the same answer in every lane of the warp; false once any role's wait has given up.
     auto wait = [&](uint64_t* bar, unsigned parity) -> bool {
         bool got = try_wait(bar, parity & 1u);
-        if (!got) {
+        if (__builtin_expect(!got, 0)) {
             const unsigned long long from = nanoseconds();
 #pragma unroll 1
             while (!(got = try_wait(bar, parity & 1u)))
                 if (*(volatile int*)&sh.dead || nanoseconds() - from > PT_WAIT_NS) break;
         }
-        if (__all_sync(0xffffffffu, got)) return true;
+        if (__builtin_expect(__all_sync(0xffffffffu, got), 1)) return true;
         *(volatile int*)&sh.dead = 1;
         kv_flag(kv, Q8_KV_ERR_WAIT);
         return false;
@@ -396,25 +390,21 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                     const float4* vs4 = reinterpret_cast<const float4*>(sh.vs[b]);
                     const bool masked = __any_sync(0xffffffffu, lim < p0 + PT_P - 1) || groups != 0xffu;
                     const int count = lim - p0 + 1;  // positions of the tile that the row attends
-                    auto bits = [&](int c) -> unsigned {  // those of its columns 32 c .. that are seen
-                        const int n = count - 32 * c;
-                        unsigned seen = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
-                        if (!((groups >> (2 * c)) & 1u)) seen &= 0xffff0000u;
-                        if (!((groups >> (2 * c + 1)) & 1u)) seen &= 0xffffu;
-                        return seen;
+                    auto bits = [&](int c) -> unsigned {  // those of its columns 16 c .. that are seen
+                        const int n = count - 16 * c;
+                        return ((groups >> c) & 1u) && n > 0 ? (n >= 16 ? 0xffffu : (1u << n) - 1) : 0u;
                     };
                     auto softmax = [&](auto with_mask) {
                         constexpr bool MASK = decltype(with_mask)::value;
                         float mx = -INFINITY;  // scores without the query's factor, which is positive
-                        tc_columns(s_at, [&](int c, const uint32_t (&s)[2][16]) {
-                            unsigned seen = MASK ? bits(c) : 0u;
+                        tc_columns(s_at, [&](int c, const uint32_t (&s)[16]) {
+                            const unsigned seen = MASK ? bits(c) : 0u;
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 k4 = ks4[8 * c + i];
-                                const uint32_t* x = &s[i / 4][4 * (i % 4)];
+                            for (int i = 0; i < 4; ++i) {
+                                const float4 k4 = ks4[4 * c + i];
                                 float a[4];
-                                upk2(mul2(pk2(__uint_as_float(x[0]), __uint_as_float(x[1])), pk2(k4.x, k4.y)), a[0], a[1]);
-                                upk2(mul2(pk2(__uint_as_float(x[2]), __uint_as_float(x[3])), pk2(k4.z, k4.w)), a[2], a[3]);
+                                upk2(mul2(pk2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), pk2(k4.x, k4.y)), a[0], a[1]);
+                                upk2(mul2(pk2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), pk2(k4.z, k4.w)), a[2], a[3]);
 #pragma unroll
                                 for (int j = 0; j < 4; ++j)
                                     if (MASK && !((seen >> (4 * i + j)) & 1u)) a[j] = -INFINITY;
@@ -432,47 +422,44 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                         if (m == 0) sh.back[tau & 3] = sh.ce[b];
                         uint64_t sum = 0ull;
                         const uint64_t qf2 = pk2(qf, qf), nm2 = pk2(-ms, -ms), less = pk2(-1.f, -1.f);
-                        tc_columns(s_at, [&](int c, const uint32_t (&s)[2][16]) {
-                            unsigned seen = MASK ? bits(c) : 0u;
+                        tc_columns(s_at, [&](int c, const uint32_t (&s)[16]) {
+                            const unsigned seen = MASK ? bits(c) : 0u;
+                            uint32_t w[16];
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                uint32_t w[16];
+                            for (int i = 0; i < 4; ++i) {
+                                const float4 k4 = ks4[4 * c + i], v4 = vs4[4 * c + i];
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const float4 k4 = ks4[8 * c + 4 * h + i], v4 = vs4[8 * c + 4 * h + i];
-#pragma unroll
-                                    for (int j = 0; j < 2; ++j) {
-                                        const int e = 4 * i + 2 * j;
-                                        uint64_t t2 = mul2(pk2(__uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1])),
-                                                           j ? pk2(k4.z, k4.w) : pk2(k4.x, k4.y));
-                                        t2 = fma2(t2, qf2, nm2);
-                                        float a, b;
-                                        upk2(t2, a, b);
-                                        a = ex2(a), b = ex2(b);
-                                        if (MASK) {
-                                            if (!((seen >> (16 * h + e)) & 1u)) a = 0.f;
-                                            if (!((seen >> (16 * h + e + 1)) & 1u)) b = 0.f;
-                                        }
-                                        const uint64_t p2 = pk2(a, b);
-                                        sum = add2(sum, p2);
-                                        uint64_t w2 = mul2(p2, j ? pk2(v4.z, v4.w) : pk2(v4.x, v4.y));
-                                        float wa, wb;
-                                        upk2(w2, wa, wb);
-                                        if (MASK) {  // (a value scale that is not a number stays behind the mask)
-                                            if (!((seen >> (16 * h + e)) & 1u)) wa = 0.f;
-                                            if (!((seen >> (16 * h + e + 1)) & 1u)) wb = 0.f;
-                                            w2 = pk2(wa, wb);
-                                        }
-                                        const uint32_t hi = f16_pack(wa, wb);
-                                        const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-                                        float la, lb;
-                                        upk2(fma2(pk2(hf.x, hf.y), less, w2), la, lb);
-                                        w[e / 2] = hi;
-                                        w[8 + e / 2] = f16_pack(la, lb);
+                                for (int j = 0; j < 2; ++j) {
+                                    const int e = 4 * i + 2 * j;
+                                    uint64_t t2 = mul2(pk2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])),
+                                                       j ? pk2(k4.z, k4.w) : pk2(k4.x, k4.y));
+                                    t2 = fma2(t2, qf2, nm2);
+                                    float a, b;
+                                    upk2(t2, a, b);
+                                    a = ex2(a), b = ex2(b);
+                                    if (MASK) {
+                                        if (!((seen >> e) & 1u)) a = 0.f;
+                                        if (!((seen >> (e + 1)) & 1u)) b = 0.f;
                                     }
+                                    const uint64_t p2 = pk2(a, b);
+                                    sum = add2(sum, p2);
+                                    uint64_t w2 = mul2(p2, j ? pk2(v4.z, v4.w) : pk2(v4.x, v4.y));
+                                    float wa, wb;
+                                    upk2(w2, wa, wb);
+                                    if (MASK) {  // (a value scale that is not a number stays behind the mask)
+                                        if (!((seen >> e) & 1u)) wa = 0.f;
+                                        if (!((seen >> (e + 1)) & 1u)) wb = 0.f;
+                                        w2 = pk2(wa, wb);
+                                    }
+                                    const uint32_t hi = f16_pack(wa, wb);
+                                    const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                                    float la, lb;
+                                    upk2(fma2(pk2(hf.x, hf.y), less, w2), la, lb);
+                                    w[e / 2] = hi;
+                                    w[8 + e / 2] = f16_pack(la, lb);
                                 }
-                                tc_st16(s_at + 32 * c + 16 * h, w);
                             }
+                            tc_st16(s_at + 16 * c, w);
                         });
                         float sa, sb;
                         upk2(sum, sa, sb);
@@ -512,9 +499,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
 #pragma unroll 1
             for (int x = 0; x < tiles + 2; ++x) {
                 const int tx = tau + x, bx = tx & 1, past = d.end - (d.t0 + x) * PT_P;
-                if (x < tiles)
-                    if (!(ok = wait(&sh.v_empty[bx], (tx >> 1) + 1) && values_half(sh.v[bx], 0, past))) break;
-                if (x >= 2) {
+                if (x < tiles && !(ok = wait(&sh.v_empty[bx], (tx >> 1) + 1))) break;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    if (x < tiles && !(ok = values_half(sh.v[bx], half, past - PT_HALF * half))) break;
+                    if (half == 1 || x < 2) continue;
                     const int t = tx - 2;
                     if (!(ok = wait(&sh.t_full[bx], t >> 1))) break;
                     tc_fence_after();
@@ -537,8 +526,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                     tc_fence_before();
                     arrive(&sh.t_empty[bx]);
                 }
+                if (!ok) break;
                 if (x < tiles) {
-                    if (!(ok = values_half(sh.v[bx], 1, past - PT_HALF))) break;
                     fence_async();
                     arrive(&sh.v_full[bx]);
                 }
