@@ -9,14 +9,16 @@
 // so each is two tensor-core products (4 x 128 x 128 x hd multiply-adds a tile pair, twice the formula's): those bound it.
 // One CTA an SM works through an equal run of tile pairs; its warps divide the work and meet only at barriers in shared
 // memory:
-//  - warps 0-3 (a thread a query vector) take a tile's scores out of tensor memory, form its weights against the running
-//    maximum, and put their parts back over the scores, where the second product reads them as its first operand.
-//  - warps 4-7 turn the values' words into f16 operand tiles, transposed, and add each tile's product (rounded: the tensor
-//    cores truncate as they accumulate) to the f32 output sums in their registers; at an item's end they write it.
-//  - warps 8-11 turn the keys' words into operand tiles, and an item's queries into their parts.
-//  - warp 12 issues the products, warp 13 copies the words of 64 positions at a time from the pages into a ring (tensor
-//    copies of 16 rows, zeros for pages out of range), warp 15 deals out the items and prepares the scales.
-// Registers are moved from the last eight warps to the first eight (200 and 56 a thread).
+//  - warps 0-3 and 4-7 (a thread a query vector) take the even and the odd tiles: scores out of tensor memory, the running
+//    maximum (handed from tile to tile: one group forms its weights while the other looks for its maximum), and the
+//    weights' parts back over the scores, where the second product reads them as its first operand.
+//  - warps 8-11 add each tile's product (rounded: the tensor cores truncate as they accumulate) to the f32 output sums in
+//    their registers, and write them at an item's end; and they turn the first half of each tile's values into f16
+//    operands, transposed.
+//  - warps 12-15 turn an item's queries into their parts, the keys into operands, and the values' second half.
+//  - warp 16 issues the products, warp 17 copies the words of 64 positions at a time from the pages (tensor copies of 16
+//    rows, zeros for pages out of range), warp 19 deals out the items and prepares the scales.
+// Registers are moved to the warps that hold the output sums (88, 88, 184, 64 and 56 a thread).
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -29,10 +31,10 @@ namespace q8 {
 namespace {
 
 constexpr int PT_M = 128, PT_P = 128;      // query vectors and positions a tile
-constexpr int PT_THREADS = 512;
+constexpr int PT_THREADS = 640;
 constexpr int PT_HALF = 64;                // positions a copied stage
 constexpr int PT_ITEMS = 4;                // items dealt out ahead
-constexpr int PT_READERS = 14;             // warps that read an item
+constexpr int PT_READERS = 18;             // warps that read an item
 constexpr unsigned PT_POLL_NS = 20000;     // the longest the hardware may hold a warp at a poll
 constexpr unsigned long long PT_WAIT_NS = 2000000000ull;  // a wait gives up after two seconds
 constexpr int PT_PEXP = 14;                // weights are split as values of up to 2^(PT_PEXP + 1)
@@ -58,14 +60,14 @@ struct PtShared {
     unsigned char v[2][HD / 8 * SBO_V];
     float ks[2][PT_P], vs[2][PT_P];
     float qf[4][PT_M];
-    float alpha[4][PT_M], back[4];   // a tile's rescaling of the sums, and what scales its product back
-    float fin_m[PT_M], fin_l[PT_M];  // an item's maxima and sums
+    float m_now[4][PT_M], back[4];   // the vectors' running maxima after a tile, and what scales its product back
+    float fin_l[2][PT_M];            // an item's sums, of the even and of the odd tiles
     float ce[2];
     unsigned groups[2];    // which 16-position groups of a tile are there
     PtItem item[PT_ITEMS];
-    uint64_t d_full[PT_ITEMS], d_empty[PT_ITEMS], rk_full[2], rk_empty[2], rv_full, rv_empty;
+    uint64_t d_full[PT_ITEMS], d_empty[PT_ITEMS], rk_full[2], rk_empty[2], rv_full[2], rv_empty;
     uint64_t sc_full[2], sc_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t s_full[2], p_full[2], t_full[2], t_empty[2], q_full, q_empty, fin_full, fin_empty, met, drained;
+    uint64_t s_full[2], p_full[2], t_full[2], t_empty[2], q_full, q_empty, m_full[2][4], fin_full, fin_empty, met, drained;
     uint32_t tmem;
     int dead;              // a wait gave up: every role leaves
     int last;
@@ -280,22 +282,23 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
 
     if (tid == 0) {
         for (int i = 0; i < PT_ITEMS; ++i) mbar_init(&sh.d_full[i], 1), mbar_init(&sh.d_empty[i], PT_READERS);
-        mbar_init(&sh.rv_full, 1), mbar_init(&sh.rv_empty, 4);
+        mbar_init(&sh.rv_full[0], 1), mbar_init(&sh.rv_full[1], 1), mbar_init(&sh.rv_empty, 4);
+        for (int i = 0; i < 8; ++i) mbar_init(&sh.m_full[i / 4][i % 4], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.rk_full[i], 1), mbar_init(&sh.rk_empty[i], 4);
             mbar_init(&sh.sc_full[i], 1), mbar_init(&sh.sc_empty[i], 4);
             mbar_init(&sh.k_full[i], 4), mbar_init(&sh.k_empty[i], 1);
-            mbar_init(&sh.v_full[i], 4), mbar_init(&sh.v_empty[i], 1);
+            mbar_init(&sh.v_full[i], 8), mbar_init(&sh.v_empty[i], 1);
             mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 4);
             mbar_init(&sh.t_full[i], 1), mbar_init(&sh.t_empty[i], 4);
         }
         mbar_init(&sh.q_full, 4), mbar_init(&sh.q_empty, 1), mbar_init(&sh.met, 4);
-        mbar_init(&sh.fin_full, 4), mbar_init(&sh.fin_empty, 4);
+        mbar_init(&sh.fin_full, 8), mbar_init(&sh.fin_empty, 4);
         mbar_init(&sh.drained, 1);
         sh.dead = 0;
         fence_barrier_init();
     }
-    if (wid == 12) {
+    if (wid == 16) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc_smem(&sh.tmem)), "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
@@ -331,8 +334,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
 
     // Turns 64 copied positions of values (a tile's first or second half) into that half of a transposed operand tile; a lane 4
     // dimensions of 8 positions.  `past`: the half's positions before the sequence's end.
-    auto values_half = [&](unsigned char* tile, int half, int past) -> bool {
-        if (!wait(&sh.rv_full, half)) return false;  // (two copies a tile)
+    auto values_half = [&](unsigned tau, unsigned char* tile, int half, int past) -> bool {
+        if (!wait(&sh.rv_full[half], tau)) return false;
         const unsigned char* src = sh.raw_v;
 #pragma unroll
         for (int i = 0; i < HD / 64; ++i) {
@@ -362,29 +365,31 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
         return true;
     };
 
-    if (wg == 0) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        // ================ scores to weights: thread = query vector
-        const int m = tid;
-        const uint32_t lanes = (uint32_t)(32 * wid) << 16;
-        int tau = 0;
+    if (wg < 2) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        // ================ scores to weights of the even (group 0) or odd tiles: thread = query vector
+        const int quarter = wid & 3, m = 32 * quarter + lane;
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+        int tau0 = 0;
         PtItem d;
         bool ok = true;
 #pragma unroll 1
         for (int it = 0; ok && next_item(it, d); ++it) {
             const bool valid = m < d.tokens * G;
             const int lim = !valid ? INT_MAX : d.end ? d.pos + m / G : -1;
-            const bool active = 32 * wid < d.tokens * G;  // (warp-uniform)
-            float mr = -INFINITY, l = 0.f, qf = 0.f;
-            const int first = tau;
+            const bool active = 32 * quarter < d.tokens * G;  // (uniform in the quarter's warps)
+            float mr = -INFINITY, l = 0.f, qf = 0.f;           // the maximum that l's terms are relative to
+            const int tiles = d.t1 - d.t0;
+            bool fresh = true;
 #pragma unroll 1
-            for (int tl = d.t0; tl < d.t1; ++tl, ++tau) {
-                const int b = tau & 1, n = tau >> 1, p0 = tl * PT_P;
+            for (int x = (tau0 + wg) & 1; x < tiles; x += 2) {
+                const int tau = tau0 + x, b = wg, n = tau >> 1, p0 = (d.t0 + x) * PT_P;
                 const uint32_t s_at = tmem + lanes + 128 * b;
                 if (!(ok = wait(&sh.s_full[b], n) && wait(&sh.sc_full[b], n))) break;
                 tc_fence_after();
                 if (active) {
-                    if (tau == first) qf = sh.qf[it & 3][m];
+                    if (fresh) qf = sh.qf[it & 3][m];
+                    fresh = false;
                     const unsigned groups = sh.groups[b];
                     const float4* ks4 = reinterpret_cast<const float4*>(sh.ks[b]);
                     const float4* vs4 = reinterpret_cast<const float4*>(sh.vs[b]);
@@ -414,11 +419,17 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                         });
                         // (rounded up, so that no weight exceeds 1; and a factor of 0, an invalid vector's, must not meet
                         // the masks' infinity)
-                        const float mn = fmaxf(mr, mx == -INFINITY ? -INFINITY : __fmul_ru(mx, qf));
+                        float before = -INFINITY;  // the maximum after the tile before, the other group's
+                        if (x > 0) {
+                            if (!(ok = wait(&sh.m_full[b ^ 1][quarter], (tau - 1) >> 1))) return;
+                            before = sh.m_now[(tau - 1) & 3][m];
+                        }
+                        const float mn = fmaxf(before, mx == -INFINITY ? -INFINITY : __fmul_ru(mx, qf));
                         const float ms = mn == -INFINITY ? 0.f : mn;
+                        sh.m_now[tau & 3][m] = mn;
+                        arrive(&sh.m_full[b][quarter]);
                         const float alpha = ex2(mr - ms);
                         mr = mn;
-                        sh.alpha[tau & 3][m] = alpha;
                         if (m == 0) sh.back[tau & 3] = sh.ce[b];
                         uint64_t sum = 0ull;
                         const uint64_t qf2 = pk2(qf, qf), nm2 = pk2(-ms, -ms), less = pk2(-1.f, -1.f);
@@ -467,75 +478,78 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                     };
                     if (masked) softmax(Flag<true>());
                     else softmax(Flag<false>());
+                    if (!ok) break;
                     tc_wait_st();
+                } else {
+                    arrive(&sh.m_full[b][quarter]);  // (a phase a tile, whether the quarter holds vectors or not)
                 }
                 tc_fence_before();
                 arrive(&sh.p_full[b]);
                 if (lane == 0) mbar_arrive(&sh.sc_empty[b]);
             }
+            tau0 += tiles;
             if (!ok || !(ok = wait(&sh.fin_empty, it + 1))) break;
-            sh.fin_m[m] = mr;
-            sh.fin_l[m] = l;
+            sh.fin_l[wg][m] = l;
             arrive(&sh.fin_full);
         }
-    } else if (wg == 1) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        // ================ transposed values, output sums and results: thread = query vector
-        const int m = tid - 128;
-        const uint32_t lanes = (uint32_t)(32 * (wid - 4)) << 16;
+    } else if (wg == 2) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        // ================ output sums and results, and the first half of each tile's values: thread = query vector
+        const int m = tid - 256;
+        const uint32_t lanes = (uint32_t)(32 * (wid - 8)) << 16;
         int tau = 0, meets = 0;
         PtItem d;
         bool ok = true;
 #pragma unroll 1
         for (int it = 0; ok && next_item(it, d); ++it) {
             const bool valid = m < d.tokens * G;
-            const bool active = 32 * (wid - 4) < d.tokens * G;  // (warp-uniform)
+            const bool active = 32 * (wid - 8) < d.tokens * G;  // (warp-uniform)
             uint64_t o[HD / 2];
 #pragma unroll
             for (int i = 0; i < HD / 2; ++i) o[i] = 0ull;
             const int tiles = d.t1 - d.t0;
-            // Step x, as soon as tile x - 2's product is done (its values' buffer is free then): the values of tile x, and
-            // between their halves, while the second one is copied, tile x - 2's product onto the sums.
+            float mr = -INFINITY, alpha = 0.f;
+            // Step x, as soon as tile x - 2's product is done (its values' buffer is free then): the first half of tile x's
+            // values, and tile x - 2's product onto the sums.
 #pragma unroll 1
             for (int x = 0; x < tiles + 2; ++x) {
-                const int tx = tau + x, bx = tx & 1, past = d.end - (d.t0 + x) * PT_P;
-                if (x < tiles && !(ok = wait(&sh.v_empty[bx], (tx >> 1) + 1))) break;
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    if (x < tiles && !(ok = values_half(sh.v[bx], half, past - PT_HALF * half))) break;
-                    if (half == 1 || x < 2) continue;
-                    const int t = tx - 2;
-                    if (!(ok = wait(&sh.t_full[bx], t >> 1))) break;
-                    tc_fence_after();
-                    if (active) {
-                        const float alpha = sh.alpha[t & 3][m], back = sh.back[t & 3];
-                        const uint64_t al2 = pk2(alpha, alpha), back2 = pk2(back, back);
-                        if (!__all_sync(0xffffffffu, alpha == 1.f)) {  // (a maximum moved)
-#pragma unroll
-                            for (int i = 0; i < HD / 2; ++i) o[i] = mul2(o[i], al2);
-                        }
-#pragma unroll
-                        for (int c = 0; c < HD / 32; ++c) {
-                            uint32_t r[32];
-                            tc_load<32>(tmem + lanes + 256 + 128 * bx + 32 * c, r);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                o[16 * c + i] = fma2(pk2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), back2, o[16 * c + i]);
-                        }
-                    }
-                    tc_fence_before();
-                    arrive(&sh.t_empty[bx]);
-                }
-                if (!ok) break;
+                const int tx = tau + x, bx = tx & 1;
                 if (x < tiles) {
+                    if (!(ok = wait(&sh.v_empty[bx], (tx >> 1) + 1) && values_half(tx, sh.v[bx], 0, d.end - (d.t0 + x) * PT_P))) break;
                     fence_async();
                     arrive(&sh.v_full[bx]);
                 }
+                if (x < 2) continue;
+                const int t = tx - 2;
+                if (!(ok = wait(&sh.t_full[bx], t >> 1))) break;
+                tc_fence_after();
+                if (active) {
+                    const float back = sh.back[t & 3], now = sh.m_now[t & 3][m];
+                    alpha = ex2(mr - (now == -INFINITY ? 0.f : now));
+                    mr = now;
+                    const uint64_t al2 = pk2(alpha, alpha), back2 = pk2(back, back);
+                    if (!__all_sync(0xffffffffu, alpha == 1.f)) {  // (a maximum moved)
+#pragma unroll
+                        for (int i = 0; i < HD / 2; ++i) o[i] = mul2(o[i], al2);
+                    }
+#pragma unroll
+                    for (int c = 0; c < HD / 32; ++c) {
+                        uint32_t r[32];
+                        tc_load<32>(tmem + lanes + 256 + 128 * bx + 32 * c, r);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            o[16 * c + i] = fma2(pk2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), back2, o[16 * c + i]);
+                    }
+                }
+                tc_fence_before();
+                arrive(&sh.t_empty[bx]);
             }
             if (!ok) break;
             tau += tiles;
             if (!(ok = wait(&sh.fin_full, it))) break;
-            float mr = sh.fin_m[m], l = sh.fin_l[m];
+            // (the sum of the tiles that end the item is relative to its maximum, the others' to the one before)
+            float l = sh.fin_l[(tau - 1) & 1][m];
+            if (tiles > 1) l = fmaf(sh.fin_l[tau & 1][m], alpha, l);
             arrive(&sh.fin_empty);
             // ---- the item's output, or its part of it
             const int token = m / G;
@@ -602,10 +616,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                 if (pk.lse) pk.lse[row * pk.heads + head] = l == 0.f ? -INFINITY : (mr + log2f(l)) * 0.693147180559945f;
             }
         }
-    } else if (wg == 2) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        // ================ operand tiles in f16
-        const int w = wid - 8;
+    } else if (wg == 3) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        // ================ operand tiles in f16: queries, keys, and the second half of each tile's values
+        const int w = wid - 12;
         int tau = 0;
         PtItem d;
         bool ok = true;
@@ -655,14 +669,17 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
             }
             fence_async();
             arrive(&sh.q_full);
+            const int tiles = d.t1 - d.t0;
+            // (tile x's keys go before tile x - 1's values: the products need them in that order)
 #pragma unroll 1
-            for (int x = 0; ok && x < d.t1 - d.t0; ++x, ++tau) {
-                const int b = tau & 1, n = tau >> 1;
+            for (int x = 0; x <= tiles; ++x) {
+                const int tx = tau + x, b = tx & 1, n = tx >> 1;
+                if (x < tiles) {
                 // keys: rows as they are; a lane 16 dimensions (one 16-byte chunk of words) of a position
                 if (!(ok = wait(&sh.k_empty[b], n + 1))) break;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
-                    if (!(ok = wait(&sh.rk_full[half], tau))) break;
+                    if (!(ok = wait(&sh.rk_full[half], tx))) break;
                     const unsigned char* src = sh.raw_k[half];
 #pragma unroll
                     for (int i = 0; i < HD / 32; ++i) {  // (HD / 16 chunks) x 8 groups of 8 rows, 4 warps x 4 chunks at a time
@@ -683,13 +700,21 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                 if (!ok) break;
                 fence_async();
                 arrive(&sh.k_full[b]);
+                }
+                if (x == 0) continue;
+                if (!(ok = wait(&sh.v_empty[b ^ 1], ((tx - 1) >> 1) + 1) &&
+                           values_half(tx - 1, sh.v[b ^ 1], 1, d.end - (d.t0 + x - 1) * PT_P - PT_HALF)))
+                    break;
+                fence_async();
+                arrive(&sh.v_full[b ^ 1]);
             }
+            tau += tiles;
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         PtItem d;
         bool ok = true;
-        if (wid == 12) {
+        if (wid == 16) {
             // ================ the products
             const uint32_t id_s = tc_idesc_f16(PT_M, PT_P), id_o = tc_idesc_f16(PT_M, HD);
             auto weigh = [&](int tau) -> bool {  // the second product of tile tau
@@ -746,7 +771,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
             if (ok && pending) weigh(tau - 1);
             if (lane == 0) tc_commit(&sh.drained);  // nothing is in flight when the CTA gives its tensor memory back
             drain(&sh.drained, 0);
-        } else if (wid == 13) {
+        } else if (wid == 17) {
             // ================ copies of the words: 16 positions of the head a box, a lane a box
             // (Keys run a tile ahead of the values, which wait for the tile's turn: in one queue the values would hold the
             // next tile's keys up.)
@@ -763,8 +788,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
             int row_v = 0, page_v = 0;
             bool values = false;  // whether the tile before's values are still to be copied
             auto copy_values = [&]() -> bool {
-                return copy(&sh.rv_full, &sh.rv_empty, nv, sh.raw_v, &map_v, 0, row_v, page_v) &&
-                       copy(&sh.rv_full, &sh.rv_empty, nv, sh.raw_v, &map_v, 1, row_v, page_v);
+                return copy(&sh.rv_full[0], &sh.rv_empty, nv, sh.raw_v, &map_v, 0, row_v, page_v) &&
+                       copy(&sh.rv_full[1], &sh.rv_empty, nv, sh.raw_v, &map_v, 1, row_v, page_v);
             };
 #pragma unroll 1
             for (int it = 0; ok && next_item(it, d); ++it) {
@@ -791,8 +816,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
             if (ok && values) copy_values();
             if (nk0) drain(&sh.rk_full[0], (nk0 - 1) & 1);  // no copy is in flight when the CTA leaves
             if (nk1) drain(&sh.rk_full[1], (nk1 - 1) & 1);
-            if (nv) drain(&sh.rv_full, (nv - 1) & 1);
-        } else if (wid == 15) {
+            if (nv) drain(&sh.rv_full[(nv - 1) & 1], ((nv - 1) >> 1) & 1);
+        } else if (wid == 19) {
             // ================ items and scales
             int b = run.seq;
             int64_t b_at = run.seq_at, i = 0, h = 0, cur = run.lo;
@@ -885,7 +910,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (wid == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    if (wid == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
