@@ -36,7 +36,7 @@ constexpr int PT_HALF = 64;                // positions a copied stage
 constexpr int PT_ITEMS = 4;                // items dealt out ahead
 constexpr int PT_READERS = 18;             // warps that read an item
 constexpr unsigned PT_POLL_NS = 20000;     // the longest the hardware may hold a warp at a poll
-constexpr unsigned long long PT_WAIT_NS = 2000000000ull;  // a wait gives up after two seconds
+constexpr unsigned PT_POLLS = 1u << 20;    // polls before a wait gives up (seconds)
 constexpr int PT_PEXP = 14;                // weights are split as values of up to 2^(PT_PEXP + 1)
 
 // One item's piece as the roles read it.
@@ -54,9 +54,9 @@ template <int HD>
 struct PtShared {
     static constexpr uint32_t SBO_Q = HD / 8 * 128;        // bytes between 8-row groups of queries and keys
     static constexpr uint32_t SBO_V = PT_P / 8 * 128 + 16; // and of transposed values (the pad spreads the writes' banks)
-    unsigned char raw_k[2][PT_HALF * HD], raw_v[PT_HALF * HD];  // copied words: a tile's keys, half a tile's values
+    unsigned char raw[4][PT_HALF * HD];  // copied words: the halves of a tile's keys, then of its values
     unsigned char qh[PT_M * HD * 2], ql[PT_M * HD * 2];
-    unsigned char k[2][PT_P * HD * 2];
+    unsigned char k[PT_P * HD * 2];
     unsigned char v[2][HD / 8 * SBO_V];
     float ks[2][PT_P], vs[2][PT_P];
     float qf[4][PT_M];
@@ -65,9 +65,9 @@ struct PtShared {
     float ce[2];
     unsigned groups[2];    // which 16-position groups of a tile are there
     PtItem item[PT_ITEMS];
-    uint64_t d_full[PT_ITEMS], d_empty[PT_ITEMS], rk_full[2], rk_empty[2], rv_full[2], rv_empty;
-    uint64_t sc_full[2], sc_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t s_full[2], p_full[2], t_full[2], t_empty[2], q_full, q_empty, m_full[2][4], fin_full, fin_empty, met, drained;
+    uint64_t d_full[PT_ITEMS], d_empty[PT_ITEMS], raw_full[4], raw_empty[4];
+    uint64_t sc_full[2], sc_empty[2], k_full, k_empty, v_full[2], v_empty[2];
+    uint64_t s_full[3], p_full[3], t_full, t_empty, q_full, q_empty, m_full[2][4], fin_full, fin_empty, met, drained;
     uint32_t tmem;
     int dead;              // a wait gave up: every role leaves
     int last;
@@ -84,17 +84,10 @@ __device__ __forceinline__ bool try_wait(uint64_t* bar, unsigned parity) {
     return ok != 0;
 }
 
-__device__ __forceinline__ unsigned long long nanoseconds() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
-}
-
-// Waits for a phase, for two seconds at most, whatever the other roles do.
+// Waits for a phase, whatever the other roles do.
 __device__ __forceinline__ void drain(uint64_t* bar, unsigned parity) {
-    const unsigned long long from = nanoseconds();
 #pragma unroll 1
-    while (!try_wait(bar, parity) && nanoseconds() - from < PT_WAIT_NS) {}
+    for (unsigned i = 0; i < PT_POLLS && !try_wait(bar, parity); ++i) {}
 }
 
 __device__ __forceinline__ uint64_t pk2(float a, float b) {
@@ -119,10 +112,38 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return r;
 }
 
-// D[tmem] (+)= A * B^T for one K = 16 slice, A in tensor memory.
-__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
-                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc));
+// D[tmem] (+)= A * B^T over 4 slices of K = 16, A in shared memory (tc_mma4) or in tensor memory (tc_mma4_ta: a slice every
+// 16 columns); slices of shared operands are 256 bytes apart.  Issued by one lane of the converged warp, so that the
+// operands stay in uniform registers (from one lane's branch every operand of every product took moves of its own).
+__device__ __forceinline__ void tc_mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{ .reg .pred q, p, t; .reg .b64 a1, a2, a3, b1, b2, b3;\n"
+        "elect.sync _|q, 0xffffffff; setp.ne.u32 p, %4, 0; setp.eq.u32 t, 0, 0;\n"
+        "add.s64 a1, %1, 16; add.s64 a2, %1, 32; add.s64 a3, %1, 48;\n"
+        "add.s64 b1, %2, 16; add.s64 b2, %2, 32; add.s64 b3, %2, 48;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t; }"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void tc_mma4_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{ .reg .pred q, p, t; .reg .b32 a1, a2, a3; .reg .b64 b1, b2, b3;\n"
+        "elect.sync _|q, 0xffffffff; setp.ne.u32 p, %4, 0; setp.eq.u32 t, 0, 0;\n"
+        "add.s32 a1, %1, 16; add.s32 a2, %1, 32; add.s32 a3, %1, 48;\n"
+        "add.s64 b1, %2, 16; add.s64 b2, %2, 32; add.s64 b3, %2, 48;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t; }"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+// The products issued so far arrive on bar when they complete (from one lane of the converged warp).
+__device__ __forceinline__ void tc_commit_one(uint64_t* bar) {
+    asm volatile("{ .reg .pred q; elect.sync _|q, 0xffffffff;\n"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(tc_smem(bar))
+                 : "memory");
 }
 
 // 16 columns of this warp's 32 lanes, one 32-bit value each: issued by tc_ld16, there after tc_wait16 on the same
@@ -282,16 +303,15 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
 
     if (tid == 0) {
         for (int i = 0; i < PT_ITEMS; ++i) mbar_init(&sh.d_full[i], 1), mbar_init(&sh.d_empty[i], PT_READERS);
-        mbar_init(&sh.rv_full[0], 1), mbar_init(&sh.rv_full[1], 1), mbar_init(&sh.rv_empty, 4);
         for (int i = 0; i < 8; ++i) mbar_init(&sh.m_full[i / 4][i % 4], 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.rk_full[i], 1), mbar_init(&sh.rk_empty[i], 4);
             mbar_init(&sh.sc_full[i], 1), mbar_init(&sh.sc_empty[i], 4);
-            mbar_init(&sh.k_full[i], 4), mbar_init(&sh.k_empty[i], 1);
             mbar_init(&sh.v_full[i], 8), mbar_init(&sh.v_empty[i], 1);
-            mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 4);
-            mbar_init(&sh.t_full[i], 1), mbar_init(&sh.t_empty[i], 4);
         }
+        for (int i = 0; i < 4; ++i) mbar_init(&sh.raw_full[i], 1), mbar_init(&sh.raw_empty[i], 4);
+        for (int i = 0; i < 3; ++i) mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 4);
+        mbar_init(&sh.t_full, 1), mbar_init(&sh.t_empty, 4);
+        mbar_init(&sh.k_full, 4), mbar_init(&sh.k_empty, 1);
         mbar_init(&sh.q_full, 4), mbar_init(&sh.q_empty, 1), mbar_init(&sh.met, 4);
         mbar_init(&sh.fin_full, 8), mbar_init(&sh.fin_empty, 4);
         mbar_init(&sh.drained, 1);
@@ -305,17 +325,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;  // columns: scores and weights of the even and odd tiles, then their products
+    const uint32_t tmem = sh.tmem;  // columns: scores and weights of three tiles in turn, then the latest product
 
     // A bounded wait, the same answer in every lane of the warp; false once any role's wait has given up.
     auto wait = [&](uint64_t* bar, unsigned parity) -> bool {
         bool got = try_wait(bar, parity & 1u);
-        if (__builtin_expect(!got, 0)) {
-            const unsigned long long from = nanoseconds();
 #pragma unroll 1
-            while (!(got = try_wait(bar, parity & 1u)))
-                if (*(volatile int*)&sh.dead || nanoseconds() - from > PT_WAIT_NS) break;
-        }
+        for (unsigned i = 0; !got && i < PT_POLLS && !*(volatile int*)&sh.dead; ++i) got = try_wait(bar, parity & 1u);
         if (__builtin_expect(__all_sync(0xffffffffu, got), 1)) return true;
         *(volatile int*)&sh.dead = 1;
         kv_flag(kv, Q8_KV_ERR_WAIT);
@@ -335,8 +351,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
     // Turns 64 copied positions of values (a tile's first or second half) into that half of a transposed operand tile; a lane 4
     // dimensions of 8 positions.  `past`: the half's positions before the sequence's end.
     auto values_half = [&](unsigned tau, unsigned char* tile, int half, int past) -> bool {
-        if (!wait(&sh.rv_full[half], tau)) return false;
-        const unsigned char* src = sh.raw_v;
+        if (!wait(&sh.raw_full[2 + half], tau)) return false;
+        const unsigned char* src = sh.raw[2 + half];
 #pragma unroll
         for (int i = 0; i < HD / 64; ++i) {
             const int task = i * 128 + (tid & 127);
@@ -361,7 +377,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
 #pragma unroll
             for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(dst + 16 * j) = make_uint4(h[j][0], h[j][1], h[j][2], h[j][3]);
         }
-        arrive(&sh.rv_empty);
+        arrive(&sh.raw_empty[2 + half]);
         return true;
     };
 
@@ -383,9 +399,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
             bool fresh = true;
 #pragma unroll 1
             for (int x = (tau0 + wg) & 1; x < tiles; x += 2) {
-                const int tau = tau0 + x, b = wg, n = tau >> 1, p0 = (d.t0 + x) * PT_P;
-                const uint32_t s_at = tmem + lanes + 128 * b;
-                if (!(ok = wait(&sh.s_full[b], n) && wait(&sh.sc_full[b], n))) break;
+                const int tau = tau0 + x, b = wg, n = tau >> 1, p0 = (d.t0 + x) * PT_P, place = tau % 3;
+                const uint32_t s_at = tmem + lanes + 128 * place;
+                if (!(ok = wait(&sh.s_full[place], tau / 3) && wait(&sh.sc_full[b], n))) break;
                 tc_fence_after();
                 if (active) {
                     if (fresh) qf = sh.qf[it & 3][m];
@@ -484,7 +500,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                     arrive(&sh.m_full[b][quarter]);  // (a phase a tile, whether the quarter holds vectors or not)
                 }
                 tc_fence_before();
-                arrive(&sh.p_full[b]);
+                arrive(&sh.p_full[place]);
                 if (lane == 0) mbar_arrive(&sh.sc_empty[b]);
             }
             tau0 += tiles;
@@ -509,40 +525,42 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
             for (int i = 0; i < HD / 2; ++i) o[i] = 0ull;
             const int tiles = d.t1 - d.t0;
             float mr = -INFINITY, alpha = 0.f;
-            // Step x, as soon as tile x - 2's product is done (its values' buffer is free then): the first half of tile x's
-            // values, and tile x - 2's product onto the sums.
+            // Step x, as soon as tile x - 2's product is done: it goes onto the sums (the next product waits for its place),
+            // then the first half of tile x's values (whose buffer it has left).
 #pragma unroll 1
             for (int x = 0; x < tiles + 2; ++x) {
-                const int tx = tau + x, bx = tx & 1;
+                const int tx = tau + x;
+                if (x >= 2) {
+                    const int t = tx - 2;
+                    if (!(ok = wait(&sh.t_full, t))) break;
+                    tc_fence_after();
+                    if (active) {
+                        const float back = sh.back[t & 3], now = sh.m_now[t & 3][m];
+                        alpha = ex2(mr - (now == -INFINITY ? 0.f : now));
+                        mr = now;
+                        const uint64_t al2 = pk2(alpha, alpha), back2 = pk2(back, back);
+                        if (!__all_sync(0xffffffffu, alpha == 1.f)) {  // (a maximum moved)
+#pragma unroll
+                            for (int i = 0; i < HD / 2; ++i) o[i] = mul2(o[i], al2);
+                        }
+#pragma unroll
+                        for (int c = 0; c < HD / 32; ++c) {
+                            uint32_t r[32];
+                            tc_load<32>(tmem + lanes + 384 + 32 * c, r);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                o[16 * c + i] = fma2(pk2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), back2, o[16 * c + i]);
+                        }
+                    }
+                    tc_fence_before();
+                    arrive(&sh.t_empty);
+                }
                 if (x < tiles) {
-                    if (!(ok = wait(&sh.v_empty[bx], (tx >> 1) + 1) && values_half(tx, sh.v[bx], 0, d.end - (d.t0 + x) * PT_P))) break;
+                    unsigned char* to = sh.v[tx & 1];
+                    if (!(ok = wait(&sh.v_empty[tx & 1], (tx >> 1) + 1) && values_half(tx, to, 0, d.end - (d.t0 + x) * PT_P))) break;
                     fence_async();
-                    arrive(&sh.v_full[bx]);
+                    arrive(&sh.v_full[tx & 1]);
                 }
-                if (x < 2) continue;
-                const int t = tx - 2;
-                if (!(ok = wait(&sh.t_full[bx], t >> 1))) break;
-                tc_fence_after();
-                if (active) {
-                    const float back = sh.back[t & 3], now = sh.m_now[t & 3][m];
-                    alpha = ex2(mr - (now == -INFINITY ? 0.f : now));
-                    mr = now;
-                    const uint64_t al2 = pk2(alpha, alpha), back2 = pk2(back, back);
-                    if (!__all_sync(0xffffffffu, alpha == 1.f)) {  // (a maximum moved)
-#pragma unroll
-                        for (int i = 0; i < HD / 2; ++i) o[i] = mul2(o[i], al2);
-                    }
-#pragma unroll
-                    for (int c = 0; c < HD / 32; ++c) {
-                        uint32_t r[32];
-                        tc_load<32>(tmem + lanes + 256 + 128 * bx + 32 * c, r);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            o[16 * c + i] = fma2(pk2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), back2, o[16 * c + i]);
-                    }
-                }
-                tc_fence_before();
-                arrive(&sh.t_empty[bx]);
             }
             if (!ok) break;
             tau += tiles;
@@ -673,14 +691,14 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
             // (tile x's keys go before tile x - 1's values: the products need them in that order)
 #pragma unroll 1
             for (int x = 0; x <= tiles; ++x) {
-                const int tx = tau + x, b = tx & 1, n = tx >> 1;
+                const int tx = tau + x, b = tx & 1;
                 if (x < tiles) {
                 // keys: rows as they are; a lane 16 dimensions (one 16-byte chunk of words) of a position
-                if (!(ok = wait(&sh.k_empty[b], n + 1))) break;
+                if (!(ok = wait(&sh.k_empty, tx + 1))) break;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
-                    if (!(ok = wait(&sh.rk_full[half], tx))) break;
-                    const unsigned char* src = sh.raw_k[half];
+                    if (!(ok = wait(&sh.raw_full[half], tx))) break;
+                    const unsigned char* src = sh.raw[half];
 #pragma unroll
                     for (int i = 0; i < HD / 32; ++i) {  // (HD / 16 chunks) x 8 groups of 8 rows, 4 warps x 4 chunks at a time
                         const int task = i * 4 + w;
@@ -691,15 +709,15 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
 #pragma unroll
                         for (int j = 0; j < 4; ++j) h[2 * j] = words2_f16<WORDS, 0>(in[j]), h[2 * j + 1] = words2_f16<WORDS, 1>(in[j]);
                         const int pp = PT_HALF * half + p;
-                        unsigned char* dst = sh.k[b] + (uint32_t)(pp >> 3) * SBO_Q + (uint32_t)c * 256 + (uint32_t)(pp & 7) * 16;
+                        unsigned char* dst = sh.k + (uint32_t)(pp >> 3) * SBO_Q + (uint32_t)c * 256 + (uint32_t)(pp & 7) * 16;
                         *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
                         *reinterpret_cast<uint4*>(dst + 128) = make_uint4(h[4], h[5], h[6], h[7]);
                     }
-                    arrive(&sh.rk_empty[half]);
+                    arrive(&sh.raw_empty[half]);
                 }
                 if (!ok) break;
                 fence_async();
-                arrive(&sh.k_full[b]);
+                arrive(&sh.k_full);
                 }
                 if (x == 0) continue;
                 if (!(ok = wait(&sh.v_empty[b ^ 1], ((tx - 1) >> 1) + 1) &&
@@ -717,106 +735,101 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
         if (wid == 16) {
             // ================ the products
             const uint32_t id_s = tc_idesc_f16(PT_M, PT_P), id_o = tc_idesc_f16(PT_M, HD);
-            auto weigh = [&](int tau) -> bool {  // the second product of tile tau
-                const int b = tau & 1, n = tau >> 1;
-                if (!wait(&sh.p_full[b], n) || !wait(&sh.v_full[b], n) || !wait(&sh.t_empty[b], n + 1)) return false;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t p_at = tmem + 128 * b, t_at = tmem + 256 + 128 * b;
-                    const uint64_t dv = tc_desc(sh.v[b], SBO_V);
+            const uint64_t dh = tc_desc(sh.qh, SBO_Q), dl = tc_desc(sh.ql, SBO_Q), dk = tc_desc(sh.k, SBO_Q);
+            const uint64_t dv = tc_desc(sh.v[0], SBO_V);
+            constexpr uint32_t V_STEP = sizeof(sh.v[0]) >> 4;  // between the two buffers of values
+            int tau = 0, next = 0;  // tiles whose first, and whose second product is issued
 #pragma unroll 1
-                    for (int part = 1; part >= 0; --part)  // the small parts first
-#pragma unroll 2
-                        for (int j = 0; j < PT_P / 16; ++j)  // 16 positions: 8 columns of weights, two core matrices
-                            tc_mma_f16_ta(t_at, p_at + 16 * j + 8 * part, dv + j * (256 >> 4), id_o,
-                                          part == 1 && j == 0 ? 0u : 1u);
-                    tc_commit(&sh.t_full[b]);
-                    tc_commit(&sh.v_empty[b]);
-                }
-                __syncwarp();
-                return true;
-            };
-            int tau = 0;
-            bool pending = false;  // whether tile tau - 1's second product is still to be issued
-    #pragma unroll 1
-        for (int it = 0; ok && next_item(it, d); ++it) {
-                if (pending) {
-                    if (!(ok = weigh(tau - 1))) break;
-                    pending = false;
-                }
-                if (!(ok = wait(&sh.q_full, it))) break;
+            for (int it = 0; ok; ++it) {
+                bool more = next_item(it, d);
+                const int last = more ? tau + (d.t1 - d.t0) : tau;
+                if (sh.dead) break;
+                // Scores run two tiles ahead of the sums within an item, so that both softmax groups have a tile to work on;
+                // the next item's queries wait for all of them.
 #pragma unroll 1
-                for (int x = 0; x < d.t1 - d.t0; ++x, ++tau) {
-                    const int b = tau & 1, n = tau >> 1;
-                    // the scores overwrite tile tau - 2's weights: its second product has to be done
-                    if (!(ok = wait(&sh.k_full[b], n) && wait(&sh.t_full[b], n + 1))) break;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint64_t dh = tc_desc(sh.qh, SBO_Q), dl = tc_desc(sh.ql, SBO_Q), dk = tc_desc(sh.k[b], SBO_Q);
+                for (bool fresh = true; ok && (next < tau || tau < last);) {
+                    if (tau < last && tau - next < 3 && !(fresh && next < tau)) {
+                        if (fresh && !(ok = wait(&sh.q_full, it))) break;
+                        fresh = false;
+                        // The scores overwrite tile tau - 3's weights, so its second product has to be done: the latest
+                        // one issued, or one before it (whose sums the latest one waited for).
+                        if (!(ok = wait(&sh.k_full, tau))) break;
+                        if (next > 0 && next == tau - 2 && !(ok = wait(&sh.t_full, next - 1))) break;
+                        tc_fence_after();
+                        const uint32_t s_at = tmem + 128 * (tau % 3);
 #pragma unroll 1
-                        for (int part = 1; part >= 0; --part)
-#pragma unroll 2
-                            for (int j = 0; j < HD / 16; ++j)
-                                tc_mma_f16(tmem + 128 * b, (part ? dl : dh) + j * (256 >> 4), dk + j * (256 >> 4), id_s,
-                                           part == 1 && j == 0 ? 0u : 1u);
-                        tc_commit(&sh.s_full[b]);
-                        tc_commit(&sh.k_empty[b]);
-                        if (x + 1 == d.t1 - d.t0) tc_commit(&sh.q_empty);
+                        for (int j = 0; j < 2 * HD / 64; ++j)  // the small parts first
+                            tc_mma4(s_at, (j < HD / 64 ? dl : dh) + (j % (HD / 64)) * 64, dk + (j % (HD / 64)) * 64, id_s, j > 0);
+                        tc_commit_one(&sh.s_full[tau % 3]);
+                        tc_commit_one(&sh.k_empty);
+                        if (++tau == last) tc_commit_one(&sh.q_empty);
+                        if (tau < last && tau - next < 3) continue;
                     }
-                    __syncwarp();
-                    if (pending && !(ok = weigh(tau - 1))) break;
-                    pending = true;
+                    if (next == tau) break;
+                    const int b = next & 1, place = next % 3;
+                    if (!(ok = wait(&sh.p_full[place], next / 3) && wait(&sh.v_full[b], next >> 1) && wait(&sh.t_empty, next + 1))) break;
+                    tc_fence_after();
+                    const uint32_t p_at = tmem + 128 * place;
+#pragma unroll 1
+                    for (int j = 0; j < 4; ++j)  // 64 positions: 4 slices of 8 columns of weights, two core matrices each
+                        tc_mma4_ta(tmem + 384, p_at + 64 * (j & 1) + (j < 2 ? 8 : 0), dv + b * V_STEP + (j & 1) * 64, id_o, j > 0);
+                    tc_commit_one(&sh.t_full);
+                    tc_commit_one(&sh.v_empty[b]);
+                    ++next;
                 }
+                if (!more) break;
             }
-            if (ok && pending) weigh(tau - 1);
-            if (lane == 0) tc_commit(&sh.drained);  // nothing is in flight when the CTA gives its tensor memory back
+            tc_commit_one(&sh.drained);  // nothing is in flight when the CTA gives its tensor memory back
             drain(&sh.drained, 0);
         } else if (wid == 17) {
             // ================ copies of the words: 16 positions of the head a box, a lane a box
-            // (Keys run a tile ahead of the values, which wait for the tile's turn: in one queue the values would hold the
-            // next tile's keys up.)
-            unsigned nk0 = 0, nk1 = 0, nv = 0;  // copies issued so far
-            auto copy = [&](uint64_t* full, uint64_t* empty, unsigned& issued, unsigned char* to, const CUtensorMap* map,
-                            int half, int row, int page) -> bool {
-                if (!wait(empty, issued + 1)) return false;
-                if (lane == 0) mbar_arrive_expect_tx(full, PT_HALF * HD);
-                __syncwarp();
-                if (lane < PT_P / 16 && lane / 4 == half) tma_box(to + (lane & 3) * 16 * HD, map, row, page, full);
-                ++issued;
-                return true;
-            };
+            // Keys run a tile ahead of the values, which wait for the tile's turn: in one queue the values would hold the
+            // next tile's keys up.
+            unsigned keys = 0, values = 0;  // tiles whose keys, and whose values are on their way
             int row_v = 0, page_v = 0;
-            bool values = false;  // whether the tile before's values are still to be copied
-            auto copy_values = [&]() -> bool {
-                return copy(&sh.rv_full[0], &sh.rv_empty, nv, sh.raw_v, &map_v, 0, row_v, page_v) &&
-                       copy(&sh.rv_full[1], &sh.rv_empty, nv, sh.raw_v, &map_v, 1, row_v, page_v);
+            auto copy = [&](int part, unsigned n, int row, int page) -> bool {  // half `part & 1` of a tile
+                if (!wait(&sh.raw_empty[part], n + 1)) return false;
+                if (lane == 0) mbar_arrive_expect_tx(&sh.raw_full[part], PT_HALF * HD);
+                __syncwarp();
+                if (lane < PT_P / 16 && lane / 4 == (part & 1))
+                    tma_box(sh.raw[part] + (lane & 3) * 16 * HD, part < 2 ? &map_k : &map_v, row, page, &sh.raw_full[part]);
+                return true;
             };
 #pragma unroll 1
             for (int it = 0; ok && next_item(it, d); ++it) {
-                auto page_at = [&](int tl) {  // the page of this lane's 16 positions; past the end or none: one past the
-                    const int p = tl * PT_P + 16 * lane;  // last, which reads as zeros
-                    if (lane >= PT_P / 16 || tl >= d.t1 || p >= d.end) return kv.pages;
-                    const int id = kv_page(kv, d.seq, p);
-                    if (id < 0) kv_flag(kv, Q8_KV_ERR_PAGE);
-                    return id < 0 ? kv.pages : id;
-                };
-                int next = page_at(d.t0);
+                int next = kv.pages;
 #pragma unroll 1
-                for (int tl = d.t0; ok && tl < d.t1; ++tl) {
-                    const int page = next, row = (d.head << kv.page_log2) + ((tl * PT_P + 16 * lane) & ((1 << kv.page_log2) - 1));
-                    next = page_at(tl + 1);
-                    ok = copy(&sh.rk_full[0], &sh.rk_empty[0], nk0, sh.raw_k[0], &map_k, 0, row, page) &&
-                         copy(&sh.rk_full[1], &sh.rk_empty[1], nk1, sh.raw_k[1], &map_k, 1, row, page);
-                    if (ok && values) ok = copy_values();
-                    values = true;
+                for (int tl = d.t0 - 1; ok && tl < d.t1; ++tl) {
+                    // the page of this lane's 16 positions of the next tile; past the end or none: one past the last, which
+                    // reads as zeros
+                    const int page = next, p = (tl + 1) * PT_P + 16 * lane;
+                    next = kv.pages;
+                    if (tl + 1 < d.t1 && lane < PT_P / 16 && p < d.end) {
+                        const int id = kv_page(kv, d.seq, p);
+                        if (id < 0) kv_flag(kv, Q8_KV_ERR_PAGE);
+                        else next = id;
+                    }
+                    if (tl < d.t0) continue;  // (the first tile's page)
+                    const int row = (d.head << kv.page_log2) + ((tl * PT_P + 16 * lane) & ((1 << kv.page_log2) - 1));
+#pragma unroll 1
+                    for (int part = 0; ok && part < 4; ++part) {
+                        if (part < 2) ok = copy(part, keys, row, page);
+                        else if (keys > 0) ok = copy(part, values, row_v, page_v);
+                        if (ok && part == 3 && keys > 0) ++values;
+                        if (ok && part == 3) ++keys;
+                    }
                     row_v = row;
                     page_v = page;
                 }
             }
-            if (ok && values) copy_values();
-            if (nk0) drain(&sh.rk_full[0], (nk0 - 1) & 1);  // no copy is in flight when the CTA leaves
-            if (nk1) drain(&sh.rk_full[1], (nk1 - 1) & 1);
-            if (nv) drain(&sh.rv_full[(nv - 1) & 1], ((nv - 1) >> 1) & 1);
+#pragma unroll 1
+            for (int part = 2; ok && part < 4 && keys > 0; ++part) ok = copy(part, values, row_v, page_v);  // the last values
+            if (keys > 0 && ok) ++values;
+#pragma unroll 1
+            for (int part = 0; part < 4; ++part) {  // no copy is in flight when the CTA leaves
+                const unsigned n = part < 2 ? keys : values;
+                if (n) drain(&sh.raw_full[part], (n - 1) & 1);
+            }
         } else if (wid == 19) {
             // ================ items and scales
             int b = run.seq;
