@@ -28,7 +28,7 @@ namespace q8 {
 
 namespace {
 
-constexpr int PR_WARPS = 16, PR_THREADS = PR_WARPS * 32;
+constexpr int PR_WARPS = 8, PR_THREADS = PR_WARPS * 32, PR_CTAS = 2;  // two CTAs an SM
 constexpr int PR_UNIT = 128;   // positions a unit
 constexpr int PR_STEP = 16;    // positions a warp takes at a time
 constexpr int PR_FLUSH = 8;    // steps between additions to the totals
@@ -119,11 +119,13 @@ struct RowsShared {
     int lim[MT];                       // the last position a vector attends (-1: none)
     int64_t at[MT];                    // where a vector's output starts (-1: no such vector)
     int64_t lse_at[MT];
-    int last;
+    // What the walk over the items keeps between them (in shared memory: the registers are the inner loop's).
+    int64_t cur, lo, hi, seq_at, item_at, units, total;
+    int seq, ctas, last;
 };
 
 template <int HD, int WORDS, int NT>
-__global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedParams pk) {
+__global__ void __launch_bounds__(PR_THREADS, PR_CTAS) paged_rows_kernel(const PagedParams pk) {
     constexpr int MT = 8 * NT, KB = HD / 4, KS = HD / 16, DPG = HD / 8, FR = HD / 16 * NT;
     constexpr int SLOT = FR * 32 * 4 + 2 * MT;  // floats of a partial result
     extern __shared__ __align__(16) unsigned char raw[];
@@ -139,25 +141,45 @@ __global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedPa
     auto units = [&](const KvSeq& s) -> int64_t {
         return paged_takes(pk, s) ? kv.kv * tiles_of(s) * span_of(s) : 0;
     };
-    const PagedRun run = paged_run<PR_THREADS>(pk, units);
-    if ((int)blockIdx.x >= run.ctas) return;
-
-    int b = run.seq;
-    int64_t b_at = run.seq_at;
-    KvSeq s = kv_seq(kv, b);
-    for (int64_t cur = run.lo; cur < run.hi;) {
-        int64_t n_units;
-        while (cur >= b_at + (n_units = units(s))) {  // the sequence of unit `cur`
-            b_at += n_units;
-            s = kv_seq(kv, ++b);
+    {
+        const PagedRun run = paged_run<PR_THREADS>(pk, units);
+        if ((int)blockIdx.x >= run.ctas) return;
+        if (tid == 0) {
+            sh.cur = sh.lo = run.lo, sh.hi = run.hi;
+            sh.seq = run.seq, sh.seq_at = run.seq_at;
+            sh.total = run.total, sh.ctas = run.ctas;
         }
-        const int64_t U = span_of(s), tiles = tiles_of(s), item = div_small(cur - b_at, U);
-        const int h = (int)div_small(item, tiles);
-        const int64_t m0 = (item - h * tiles) * MT;  // the item's first vector
-        const int64_t item_at = b_at + item * U;
-        const int64_t u0 = cur - item_at, u1 = min(U, u0 + (run.hi - cur));
-        const int end = s.len_ok ? (int)min((int64_t)s.len, u1 * PR_UNIT) : 0;  // positions before which the piece ends
-        const int begin = (int)(u0 * PR_UNIT);
+    }
+    __syncthreads();
+
+    for (;;) {
+        int b, begin, end, h;
+        KvSeq s;
+        int64_t m0;
+        {
+            const int64_t cur = sh.cur, hi = sh.hi;
+            if (cur >= hi) break;
+            b = sh.seq;
+            int64_t at = sh.seq_at, n_units;
+            s = kv_seq(kv, b);
+            while (cur >= at + (n_units = units(s))) {  // the sequence of unit `cur`
+                at += n_units;
+                s = kv_seq(kv, ++b);
+            }
+            const int64_t U = span_of(s), tiles = tiles_of(s), item = div_small(cur - at, U);
+            h = (int)div_small(item, tiles);
+            m0 = (item - h * tiles) * MT;  // the item's first vector
+            const int64_t item_at = at + item * U, u0 = cur - item_at, u1 = min(U, u0 + (hi - cur));
+            begin = (int)(u0 * PR_UNIT);
+            end = s.len_ok ? (int)min((int64_t)s.len, u1 * PR_UNIT) : 0;  // positions before which the piece ends
+            __syncthreads();  // every thread has read the walk's state
+            if (tid == 0) {
+                sh.cur = cur + (u1 - u0);
+                sh.seq = b, sh.seq_at = at;
+                sh.item_at = item_at, sh.units = U;
+                sh.last = u0 == 0 && u1 == U ? 1 : 0;  // whether the piece is the whole item
+            }
+        }
 
         // ---- this warp's first positions are on their way while the queries are prepared
         const int steps = end > begin ? (end - begin + PR_STEP - 1) / PR_STEP : 0;  // of all warps
@@ -190,14 +212,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedPa
 #pragma unroll
             for (int j = 0; j < 2; ++j) vs[j] = ld_scale_stream(kv.vs + row + g + 8 * j);
         };
-        auto fetch = [&](int i) {  // brings step i's words towards L2 (16 rows of a page are consecutive), i <= 31 of its batch
-            int pg;
-            const int64_t row = row_of(i, pg);
-            if (lane == 0 && pg >= 0) {
-                l2_prefetch_piece((const char*)(kv.k + row * HD), PR_STEP * HD);
-                l2_prefetch_piece((const char*)(kv.v + row * HD), PR_STEP * HD);
-            }
-        };
         const int mine = steps > wid ? (steps - wid + PR_WARPS - 1) / PR_WARPS : 0;
         int page = -1, page_next = -1;
         int64_t row_next = 0;
@@ -206,7 +220,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedPa
             row_next = row_of(0, page_next);
             load_k(row_next);
             load_v(row_next);
-            if (mine > 1) fetch(1);
         }
         // ---- the item's queries: a warp a vector, split into two f16 parts after a scaling by a power of two
         if (wid < MT) {
@@ -238,7 +251,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedPa
 
         // ---- this warp's positions
         float m_run[NT][2], l_run[NT][2], fac[NT][2], qf[NT][2];
-        int lim[NT][2];
         float acc[NT][HD / 16][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -248,7 +260,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedPa
                 l_run[n][c] = 0.f;
                 fac[n][c] = 1.f;
                 qf[n][c] = sh.qf[8 * n + 2 * t + c];
-                lim[n][c] = sh.lim[8 * n + 2 * t + c];
             }
 #pragma unroll
             for (int i = 0; i < HD / 16; ++i) {
@@ -257,6 +268,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedPa
                 for (int c = 0; c < 4; ++c) acc[n][i][c] = 0.f;
             }
         }
+        int low = INT_MAX;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) low = min(low, sh.at[i] >= 0 ? sh.lim[i] : INT_MAX);
         int exp_run = -100, exp_top = -100;  // the weights' scaling, and the largest it has been
 #pragma unroll 1
         for (int i = 0; i < mine; ++i) {
@@ -265,7 +279,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedPa
             if (i + 1 < mine) {
                 if (((i + 1) & 31) == 0) look_up(i + 1);
                 row_next = row_of(i + 1, page_next);
-                if (i + 2 < mine && ((i + 2) & 31) != 0) fetch(i + 2);
             }
             // scores: positions g, g + 8 by vectors 2t, 2t + 1 of each tile
             float sh_hi[NT][4], sh_lo[NT][4];
@@ -297,57 +310,80 @@ __global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedPa
                 vtop = max(vtop, __float_as_uint(fabsf(vscale[j])));
             }
             vtop = __reduce_max_sync(0xffffffffu, vtop);
-            const int exp_old = exp_run;
-            if (vtop != 0u) {
-                const int e = exponent_of(vtop);
-                exp_top = max(exp_top, e);
-                // (kept while the tile's largest scale is within its octave or the one below: fewer rescalings; and not
-                // far below what it was, so that rescaling the sums never overflows)
-                if (e > exp_run || e < exp_run - 1) exp_run = max(e, exp_top - 40);
-            }
-            const float wscale = pow2i(-exp_run) * PR_TOP;
-            const float eshift = exp_old - exp_run <= -126 ? 0.f : pow2i(exp_old - exp_run);
-            uint32_t ph[NT][2], pl[NT][2];
-            bool same = true;
-            float alpha[NT][2];
+            float sc[NT][4];
+            bool moved = false;  // whether a maximum or the weights' scaling changes: the sums are rescaled then
+            const bool all = here && p0 + PR_STEP <= low + 1;  // (low: the smallest of the vectors' last positions)
+            unsigned seen = 0xffffffffu;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float sc[4];
-                bool seen[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    seen[c] = here && p0 + g + 8 * (c >> 1) <= lim[n][c & 1];
-                    sc[c] = seen[c] ? (sh_hi[n][c] + sh_lo[n][c]) * kscale[c >> 1] * qf[n][c & 1] : -INFINITY;
+                    sc[n][c] = (sh_hi[n][c] + sh_lo[n][c]) * (kscale[c >> 1] * qf[n][c & 1]);
+                    if (!all && !(here && p0 + g + 8 * (c >> 1) <= sh.lim[8 * n + 2 * t + (c & 1)])) {
+                        sc[n][c] = -INFINITY;
+                        seen &= ~(1u << (4 * n + c));
+                    }
                 }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) moved |= fmaxf(sc[n][c], sc[n][c + 2]) > m_run[n][c];
+            }
+            if (vtop != 0u) {
+                const int e = exponent_of(vtop);
+                // (kept while the tile's largest scale is within its octave or the one below: fewer rescalings)
+                moved |= e > exp_run || e < exp_run - 1;
+            }
+            if (__any_sync(0xffffffffu, moved)) {
+                const int exp_old = exp_run;
+                if (vtop != 0u) {
+                    const int e = exponent_of(vtop);
+                    exp_top = max(exp_top, e);
+                    // (not far below what it was, so that rescaling the sums never overflows)
+                    if (e > exp_run || e < exp_run - 1) exp_run = max(e, exp_top - 40);
+                }
+                const float eshift = exp_old - exp_run <= -126 ? 0.f : pow2i(exp_old - exp_run);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float alpha[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float mx = fmaxf(sc[n][c], sc[n][c + 2]);
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        const float mn = fmaxf(m_run[n][c], mx), ms = mn == -INFINITY ? 0.f : mn;
+                        alpha[c] = ex2(m_run[n][c] - ms);
+                        m_run[n][c] = mn;
+                        l_run[n][c] *= alpha[c];
+                        alpha[c] *= eshift;
+                        fac[n][c] *= alpha[c];
+                    }
+#pragma unroll
+                    for (int j = 0; j < HD / 16; ++j)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) acc[n][j][c] *= alpha[c & 1];
+                }
+            }
+            const float wscale = pow2i(-exp_run) * PR_TOP;
+            uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
                 float wt[4];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    float mx = fmaxf(sc[c], sc[c + 2]);
+                    const float ms = m_run[n][c] == -INFINITY ? 0.f : m_run[n][c];
+                    const float e0 = ex2(sc[n][c] - ms), e1 = ex2(sc[n][c + 2] - ms);
+                    l_run[n][c] += e0 + e1;
+                    wt[c] = e0 * (vscale[0] * wscale);
+                    wt[c + 2] = e1 * (vscale[1] * wscale);
+                }
+                if (!all) {  // (a value scale that is not a number stays behind the mask)
 #pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    const float mn = fmaxf(m_run[n][c], mx), ms = mn == -INFINITY ? 0.f : mn;
-                    alpha[n][c] = ex2(m_run[n][c] - ms);
-                    m_run[n][c] = mn;
-                    const float e0 = ex2(sc[c] - ms), e1 = ex2(sc[c + 2] - ms);
-                    l_run[n][c] = l_run[n][c] * alpha[n][c] + (e0 + e1);
-                    wt[c] = seen[c] ? e0 * (vscale[0] * wscale) : 0.f;
-                    wt[c + 2] = seen[c + 2] ? e1 * (vscale[1] * wscale) : 0.f;
-                    alpha[n][c] *= eshift;
-                    fac[n][c] *= alpha[n][c];
-                    same = same && alpha[n][c] == 1.f;
+                    for (int c = 0; c < 4; ++c)
+                        if (!((seen >> (4 * n + c)) & 1u)) wt[c] = 0.f;
                 }
                 split2(wt[0], wt[1], ph[n][0], pl[n][0]);
                 split2(wt[2], wt[3], ph[n][1], pl[n][1]);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) ph[n][j] = transpose8x8(ph[n][j]), pl[n][j] = transpose8x8(pl[n][j]);
-            }
-            if (!__all_sync(0xffffffffu, same)) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int j = 0; j < HD / 16; ++j)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) acc[n][j][c] *= alpha[n][c & 1];
             }
             if (p0 + PR_STEP > end || !here) {  // words past the end are whatever the page holds: left out
 #pragma unroll
@@ -420,8 +456,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedPa
             sh.l[0][tid] = L;
         }
         __syncthreads();
-        const bool whole = u0 == 0 && u1 == U;
-        float* slot = pk.part + (int64_t)(2 * blockIdx.x + (cur == run.lo ? 0 : 1)) * SLOT;
+        const bool whole = sh.last != 0;
+        const int64_t item_at = sh.item_at;
+        float* slot = pk.part + (int64_t)(2 * blockIdx.x + (item_at + begin / PR_UNIT == sh.lo ? 0 : 1)) * SLOT;
         auto write_out = [&](int i, int ln, float4 v, const float* m, const float* l) {
             const int n = i / (HD / 16), dim = DPG * (ln >> 2) + 2 * (i % (HD / 16)), c = 8 * n + 2 * (ln & 3);
             const float x0 = l[c] == 0.f ? 0.f : 1.f / l[c], x1 = l[c + 1] == 0.f ? 0.f : 1.f / l[c + 1];
@@ -450,7 +487,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedPa
                 __stcg(slot + FR * 128 + tid, M);
                 __stcg(slot + FR * 128 + MT + tid, L);
             }
-            const int c0 = run.owner(item_at), c1 = run.owner(item_at + U - 1);
+            PagedRun run;
+            run.total = sh.total, run.ctas = sh.ctas;
+            const int c0 = run.owner(item_at), c1 = run.owner(item_at + sh.units - 1);
             __syncthreads();
             if (tid == 0) sh.last = atomic_add_acq_rel_gpu(pk.counters + c0, 1) == c1 - c0;
             __syncthreads();
@@ -484,7 +523,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1) paged_rows_kernel(const PagedPa
             }
         }
         __syncthreads();  // the shared arrays are the next item's
-        cur += u1 - u0;
     }
 }
 
@@ -494,7 +532,7 @@ cudaError_t rows_launch(const PagedParams& p, cudaStream_t st) {
     constexpr size_t smem = sizeof(RowsShared<HD, NT>);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<device_info().sms, PR_THREADS, smem, st>>>(p);
+    kernel<<<PR_CTAS * device_info().sms, PR_THREADS, smem, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -533,18 +571,18 @@ cudaError_t launch_paged_attention(const PagedAttnCall& c, Carve& ws, cudaStream
     const bool tiles = most > kRowsMost;
     const int sms = device_info().sms;
     PagedParams t = p;
-    auto scratch = [&](PagedParams& x, size_t slot) {
-        x.part = ws.take<float>(2 * (size_t)sms * slot / sizeof(float));
-        x.counters = ws.take_counters(sms);
+    auto scratch = [&](PagedParams& x, int ctas, size_t slot) {
+        x.part = ws.take<float>(2 * (size_t)ctas * slot / sizeof(float));
+        x.counters = ws.take_counters(ctas);
     };
-    if (rows) scratch(p, paged_rows_slot(c.hd));
-    if (tiles) scratch(t, paged_tiles_slot(c.hd));
+    if (rows) scratch(p, PR_CTAS * sms, paged_rows_slot(c.hd));
+    if (tiles) scratch(t, sms, paged_tiles_slot(c.hd));
     if (ws.overflow) return cudaSuccess;  // refused by the caller; nothing is launched
     p.upto = tiles ? kRowsMost : INT64_MAX;
     t.above = rows ? kRowsMost : 0;
     t.upto = INT64_MAX;
     cudaError_t e = cudaSuccess;
-    if (rows) e = launch_paged_rows(p, c.hd, c.words, most <= 8 ? 1 : 2, st);
+    if (rows) e = launch_paged_rows(p, c.hd, c.words, p.group <= 8 ? 1 : 2, st);
     if (tiles && e == cudaSuccess) e = launch_paged_tiles(t, c.hd, c.words, st);
     return e;
 }
