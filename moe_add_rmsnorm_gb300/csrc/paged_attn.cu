@@ -195,22 +195,30 @@ __global__ void __launch_bounds__(PR_THREADS, PR_CTAS) paged_rows_kernel(const P
                 if (page_l < 0) kv_flag(kv, Q8_KV_ERR_PAGE);
             }
         };
-        auto row_of = [&](int i, int& page) -> int64_t {  // the cached row of step i's first position
+        // This lane's places in the page of step i, as byte offsets from page 0: keys of row g, 32 dimensions from KB t;
+        // values of row 2t, dimensions from DPG g.
+        const uint32_t page_rows = (uint32_t)kv.kv << kv.page_log2;
+        const int8_t* k_at = kv.k + (((int64_t)h << kv.page_log2) + g) * HD + KB * t;
+        const int8_t* v_at = kv.v + (((int64_t)h << kv.page_log2) + 2 * t) * HD + DPG * g;
+        const float* ks_at = kv.ks + ((int64_t)h << kv.page_log2) + g;
+        const float* vs_at = kv.vs + ((int64_t)h << kv.page_log2) + g;
+        auto row_of = [&](int i, int& page) -> int64_t {  // the cached row of step i's first position, heads before h left out
             page = __shfl_sync(0xffffffffu, page_l, i & 31);
-            return kv_row(kv, max(page, 0), h, begin + (wid + i * PR_WARPS) * PR_STEP);
+            const uint32_t slot = (uint32_t)(begin + (wid + i * PR_WARPS) * PR_STEP) & ((1u << kv.page_log2) - 1);
+            return (int64_t)((uint64_t)(uint32_t)max(page, 0) * page_rows + slot);
         };
         auto load_k = [&](int64_t row) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                load_words<KB>(kv.k + (row + g + 8 * j) * HD + KB * t, kw[j]);
-                ks[j] = ld_scale_stream(kv.ks + row + g + 8 * j);
+                load_words<KB>(k_at + row * HD + 8 * j * HD, kw[j]);
+                ks[j] = ld_scale_stream(ks_at + row + 8 * j);
             }
         };
         auto load_v = [&](int64_t row) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) load_words<DPG>(kv.v + (row + 2 * t + (j & 1) + 8 * (j >> 1)) * HD + DPG * g, vw[j]);
+            for (int j = 0; j < 4; ++j) load_words<DPG>(v_at + row * HD + ((j & 1) + 8 * (j >> 1)) * HD, vw[j]);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) vs[j] = ld_scale_stream(kv.vs + row + g + 8 * j);
+            for (int j = 0; j < 2; ++j) vs[j] = ld_scale_stream(vs_at + row + 8 * j);
         };
         const int mine = steps > wid ? (steps - wid + PR_WARPS - 1) / PR_WARPS : 0;
         int page = -1, page_next = -1;
@@ -315,18 +323,23 @@ __global__ void __launch_bounds__(PR_THREADS, PR_CTAS) paged_rows_kernel(const P
             const bool all = here && p0 + PR_STEP <= low + 1;  // (low: the smallest of the vectors' last positions)
             unsigned seen = 0xffffffffu;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    sc[n][c] = (sh_hi[n][c] + sh_lo[n][c]) * (kscale[c >> 1] * qf[n][c & 1]);
-                    if (!all && !(here && p0 + g + 8 * (c >> 1) <= sh.lim[8 * n + 2 * t + (c & 1)])) {
-                        sc[n][c] = -INFINITY;
-                        seen &= ~(1u << (4 * n + c));
-                    }
-                }
+                for (int c = 0; c < 4; ++c) sc[n][c] = (sh_hi[n][c] + sh_lo[n][c]) * (kscale[c >> 1] * qf[n][c & 1]);
+            if (!all) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (!(here && p0 + g + 8 * (c >> 1) <= sh.lim[8 * n + 2 * t + (c & 1)])) {
+                            sc[n][c] = -INFINITY;
+                            seen &= ~(1u << (4 * n + c));
+                        }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) moved |= fmaxf(sc[n][c], sc[n][c + 2]) > m_run[n][c];
-            }
             if (vtop != 0u) {
                 const int e = exponent_of(vtop);
                 // (kept while the tile's largest scale is within its octave or the one below: fewer rescalings)
@@ -364,24 +377,29 @@ __global__ void __launch_bounds__(PR_THREADS, PR_CTAS) paged_rows_kernel(const P
             }
             const float wscale = pow2i(-exp_run) * PR_TOP;
             uint32_t ph[NT][2], pl[NT][2];
+            float wt[NT][4];
+            const float vw0 = vscale[0] * wscale, vw1 = vscale[1] * wscale;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float wt[4];
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const float ms = m_run[n][c] == -INFINITY ? 0.f : m_run[n][c];
                     const float e0 = ex2(sc[n][c] - ms), e1 = ex2(sc[n][c + 2] - ms);
                     l_run[n][c] += e0 + e1;
-                    wt[c] = e0 * (vscale[0] * wscale);
-                    wt[c + 2] = e1 * (vscale[1] * wscale);
+                    wt[n][c] = e0 * vw0;
+                    wt[n][c + 2] = e1 * vw1;
                 }
-                if (!all) {  // (a value scale that is not a number stays behind the mask)
+            if (!all) {  // (a value scale that is not a number stays behind the mask)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        if (!((seen >> (4 * n + c)) & 1u)) wt[c] = 0.f;
-                }
-                split2(wt[0], wt[1], ph[n][0], pl[n][0]);
-                split2(wt[2], wt[3], ph[n][1], pl[n][1]);
+                        if (!((seen >> (4 * n + c)) & 1u)) wt[n][c] = 0.f;
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                split2(wt[n][0], wt[n][1], ph[n][0], pl[n][0]);
+                split2(wt[n][2], wt[n][3], ph[n][1], pl[n][1]);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) ph[n][j] = transpose8x8(ph[n][j]), pl[n][j] = transpose8x8(pl[n][j]);
             }
@@ -497,25 +515,37 @@ __global__ void __launch_bounds__(PR_THREADS, PR_CTAS) paged_rows_kernel(const P
                 if (tid == 0) pk.counters[c0] = 0;
                 const bool opens = run.start(c0) == item_at;
                 auto slot_of = [&](int c) { return pk.part + (int64_t)paged_slot(c, c0, opens) * SLOT; };
+                // every piece's weight for every vector, then the sums with many pieces' loads in flight
+                const int pieces = c1 - c0 + 1;
+                float* wf = reinterpret_cast<float*>(sh.o);  // [pieces][MT]: the warps' totals are used up
+                for (int i = tid; i < pieces * MT; i += PR_THREADS) wf[i] = __ldcg(slot_of(c0 + i / MT) + FR * 128 + i % MT);
+                __syncthreads();
                 if (tid < MT) {
-                    float Mx = -INFINITY, Lx = 0.f;
-                    for (int c = c0; c <= c1; ++c) Mx = fmaxf(Mx, __ldcg(slot_of(c) + FR * 128 + tid));
-                    for (int c = c0; c <= c1; ++c) {
-                        const float mc = __ldcg(slot_of(c) + FR * 128 + tid);
-                        if (mc != -INFINITY) Lx += __ldcg(slot_of(c) + FR * 128 + MT + tid) * ex2(mc - Mx);
-                    }
+                    float Mx = -INFINITY;
+                    for (int p = 0; p < pieces; ++p) Mx = fmaxf(Mx, wf[p * MT + tid]);
                     sh.m[0][tid] = Mx;
+                    sh.l[0][tid] = 0.f;
+                }
+                __syncthreads();
+                for (int i = tid; i < pieces * MT; i += PR_THREADS) {
+                    const float mx = sh.m[0][i % MT];
+                    wf[i] = ex2(wf[i] - (mx == -INFINITY ? 0.f : mx));
+                }
+                __syncthreads();
+                if (tid < MT) {
+                    float Lx = 0.f;
+#pragma unroll 8
+                    for (int p = 0; p < pieces; ++p) Lx = fmaf(__ldcg(slot_of(c0 + p) + FR * 128 + MT + tid), wf[p * MT + tid], Lx);
                     sh.l[0][tid] = Lx;
                 }
                 __syncthreads();
                 for (int i = tid; i < FR * 32; i += PR_THREADS) {
                     const int fr = i >> 5, ln = i & 31, c = 8 * (fr / (HD / 16)) + 2 * (ln & 3);
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int p = c0; p <= c1; ++p) {
-                        const float* sl = slot_of(p);
-                        const float4 o = __ldcg(reinterpret_cast<const float4*>(sl) + i);
-                        const float f0 = sh.m[0][c] == -INFINITY ? 0.f : ex2(__ldcg(sl + FR * 128 + c) - sh.m[0][c]);
-                        const float f1 = sh.m[0][c + 1] == -INFINITY ? 0.f : ex2(__ldcg(sl + FR * 128 + c + 1) - sh.m[0][c + 1]);
+#pragma unroll 8
+                    for (int p = 0; p < pieces; ++p) {
+                        const float4 o = __ldcg(reinterpret_cast<const float4*>(slot_of(c0 + p)) + i);
+                        const float f0 = wf[p * MT + c], f1 = wf[p * MT + c + 1];
                         v.x = fmaf(o.x, f0, v.x), v.y = fmaf(o.y, f1, v.y), v.z = fmaf(o.z, f0, v.z), v.w = fmaf(o.w, f1, v.w);
                     }
                     write_out(fr, ln, v, sh.m[0], sh.l[0]);
@@ -526,13 +556,19 @@ __global__ void __launch_bounds__(PR_THREADS, PR_CTAS) paged_rows_kernel(const P
     }
 }
 
+// The launch's CTAs: what the GPU holds at once, and no more pieces of an item than the fold's weights have room for.
+int rows_ctas() { return device_info().sms < 256 ? PR_CTAS * device_info().sms : 2 * 255; }
+static_assert(2 * 255 * 8 * sizeof(float) <= sizeof(RowsShared<64, 1>::o) && 2 * 255 * 16 * sizeof(float) <= sizeof(RowsShared<64, 2>::o),
+              "the fold's weights over the warps' totals");
+
 template <int HD, int WORDS, int NT>
 cudaError_t rows_launch(const PagedParams& p, cudaStream_t st) {
     auto kernel = paged_rows_kernel<HD, WORDS, NT>;
     constexpr size_t smem = sizeof(RowsShared<HD, NT>);
+    static_assert(PR_CTAS * (smem + 2048) <= 233472, "the CTAs of an SM within its shared memory");
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<PR_CTAS * device_info().sms, PR_THREADS, smem, st>>>(p);
+    kernel<<<rows_ctas(), PR_THREADS, smem, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -575,7 +611,7 @@ cudaError_t launch_paged_attention(const PagedAttnCall& c, Carve& ws, cudaStream
         x.part = ws.take<float>(2 * (size_t)ctas * slot / sizeof(float));
         x.counters = ws.take_counters(ctas);
     };
-    if (rows) scratch(p, PR_CTAS * sms, paged_rows_slot(c.hd));
+    if (rows) scratch(p, rows_ctas(), paged_rows_slot(c.hd));
     if (tiles) scratch(t, sms, paged_tiles_slot(c.hd));
     if (ws.overflow) return cudaSuccess;  // refused by the caller; nothing is launched
     p.upto = tiles ? kRowsMost : INT64_MAX;
