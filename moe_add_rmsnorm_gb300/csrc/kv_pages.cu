@@ -32,22 +32,43 @@ struct AppendParams {
     float* q_out;
 };
 
-// The words of 8 values with the scale d: rounded halves away from zero (int8) or to nearest even (e4m3).
+// The int8 words of 4 values with the scale d > 0, packed: the IEEE quotients rounded halves away from zero and clamped.
+__device__ __forceinline__ uint32_t kv_words4_exact(const float* x, float d) {
+    uint32_t u = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        u |= ((uint32_t)(int)fminf(fmaxf(roundf(__fdiv_rn(x[i], d)), -127.f), 127.f) & 0xffu) << (8 * i);
+    return u;
+}
+
+// The words of 8 values with the scale d > 0: rounded halves away from zero (int8) or to nearest even (e4m3).  An int8 word
+// needs only the integer that the quotient rounds to: x times the approximate inverse is within 5e-5 of the quotient (of at
+// most 127), so it rounds to the same one unless it lies within 1e-4 of a half; there, and where d is so small that its
+// inverse is not normal, the IEEE quotients decide (half of the instructions of dividing always).
 template <int WORDS>
 __device__ __forceinline__ uint2 kv_words8(const float (&x)[8], float d) {
     uint32_t w[2];
+    if (WORDS == Q8_KV_INT8) {
+        const float inv = __fdividef(1.f, d);
+        bool near = !(d >= 1e-30f);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float t[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t[i] = __fdiv_rn(x[4 * h + i], d);
-        if (WORDS == Q8_KV_INT8) {
+        for (int h = 0; h < 2; ++h) {
             uint32_t u = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                u |= ((uint32_t)(int)fminf(fmaxf(roundf(t[i]), -127.f), 127.f) & 0xffu) << (8 * i);
+            for (int i = 0; i < 4; ++i) {
+                const float v = x[4 * h + i], a = fmaf(fabsf(v), inv, 0.5f), k = floorf(a);
+                near |= fabsf((a - k) - 0.5f) > 0.4999f;
+                u |= ((uint32_t)(int)copysignf(k, v) & 0xffu) << (8 * i);
+            }
             w[h] = u;
-        } else {
+        }
+        if (near) w[0] = kv_words4_exact(x, d), w[1] = kv_words4_exact(x + 4, d);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float t[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[i] = __fdiv_rn(x[4 * h + i], d);
             uint16_t a, b;
             asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(t[1]), "f"(t[0]));
             asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(t[3]), "f"(t[2]));
@@ -84,11 +105,14 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams pk) {
     const int64_t warp = (int64_t)blockIdx.x * Q8_WARPS + (threadIdx.x >> 5);
     const int64_t r = warp / pk.groups;
     if (r >= kv.rows) return;
-    const int v0 = (int)(warp % pk.groups) * (KV_ITERS * VPW) + sub, nvec = pk.heads + 2 * kv.kv;
+    // A row's warps take its vectors in turn, so that each has its share of the keys and values, whose words cost several
+    // times a query's work (a warp of keys alone held its CTA: with the rounding above, 2318 rows
+    // of 24 + 8 + 8 heads went from 35.8 to 25.0 us).
+    const int v0 = (int)(warp % pk.groups) * VPW + sub, step = pk.groups * VPW, nvec = pk.heads + 2 * kv.kv;
     float x[KV_ITERS][8];
 #pragma unroll
     for (int it = 0; it < KV_ITERS; ++it) {
-        const int vec = v0 + it * VPW;
+        const int vec = v0 + it * step;
         const float* src = nullptr;
         if (vec < pk.heads) src = pk.q + r * pk.q_stride + (int64_t)vec * HD;
         else if (vec < pk.heads + kv.kv) src = pk.k + r * pk.k_stride + (int64_t)(vec - pk.heads) * HD;
@@ -124,7 +148,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams pk) {
     if (page < 0 && lane == 0) kv_flag(kv, Q8_KV_ERR_PAGE);
 #pragma unroll
     for (int it = 0; it < KV_ITERS; ++it) {
-        const int vec = v0 + it * VPW;
+        const int vec = v0 + it * step;
         const int first = vec - sub;  // the iteration's first vector: the warp's branches go by it
         if (first >= nvec) break;
         if (first < pk.heads) {  // queries, in f32 (their last bits decide no word)
@@ -132,7 +156,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams pk) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss = fmaf(x[it][i], x[it][i], ss);
             ss = group_sum<LPV>(ss);
-            const float inv = pk.q_norm ? 1.0f / sqrtf(ss / (float)HD + pk.eps) : 1.0f;
+            const float inv = pk.q_norm ? rsqrtf(ss / (float)HD + pk.eps) : 1.0f;
             if (vec < pk.heads) {
                 float z[8];
 #pragma unroll
@@ -196,67 +220,90 @@ struct ReadParams {
     int64_t row_stride, head_stride;
 };
 
-// LPV lanes a vector, a lane 8 words (8 bytes in, 32 bytes out).
-template <int HD, int WORDS>
+__device__ __forceinline__ void store8(float* p, const float (&y)[8]) {
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]),
+                 "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7])
+                 : "memory");
+}
+
+// LPV lanes a vector, a lane 8 words (8 bytes in, 32 bytes out).  A warp takes ROWS consecutive rows' group of vectors:
+// where there are rows enough to fill the GPU, four, whose lookups and loads are then in flight together.
+template <int HD, int WORDS, int ROWS>
 __global__ void __launch_bounds__(256) kv_read_kernel(const ReadParams pk) {
     constexpr int LPV = HD / 8, VPW = 32 / LPV;
     const KvView& kv = pk.view;
     const int lane = threadIdx.x & 31, sub = lane / LPV, l = lane % LPV;
     const int64_t warp = (int64_t)blockIdx.x * Q8_WARPS + (threadIdx.x >> 5);
-    const int64_t r = warp / pk.groups;
-    if (r >= kv.rows) return;
-    const int b = kv_find_seq(kv, r);
-    if (b < 0) return;
-    const KvSeq s = kv_seq(kv, b);
-    if (!s.rows_ok || !s.len_ok) {
-        if (lane == 0) kv_flag(kv, Q8_KV_ERR_LENGTH);
-        return;
-    }
-    const int pos = (int)(s.len - s.n + (r - s.first));
-    const int page = kv_page(kv, b, pos);
-    if (page < 0) {
-        if (lane == 0) kv_flag(kv, Q8_KV_ERR_PAGE);
-        return;
-    }
+    const int64_t r0 = warp / pk.groups * ROWS;
+    if (r0 >= kv.rows) return;
     const int v0 = (int)(warp % pk.groups) * (KV_ITERS * VPW) + sub;
-    uint2 w[KV_ITERS];
-    float d[KV_ITERS];
+    int b = kv_find_seq(kv, r0);
+    KvSeq s;
+    if (b >= 0) s = kv_seq(kv, b);
+    int pos[ROWS], page[ROWS];
 #pragma unroll
-    for (int it = 0; it < KV_ITERS; ++it) {
-        const int vec = v0 + it * VPW;
-        if (vec < 2 * kv.kv) {
-            const bool key = vec < kv.kv;
-            const int64_t row = kv_row(kv, page, key ? vec : vec - kv.kv, pos);
-            w[it] = *reinterpret_cast<const uint2*>((key ? kv.k : kv.v) + row * HD + 8 * l);
-            d[it] = (key ? kv.ks : kv.vs)[row];
+    for (int i = 0; i < ROWS; ++i) {
+        const int64_t r = r0 + i;
+        pos[i] = page[i] = -1;
+        if (i > 0 && (b < 0 || r >= s.first + s.n) && r < kv.rows) {  // (warp-uniform) another sequence's row
+            b = kv_find_seq(kv, r);
+            if (b >= 0) s = kv_seq(kv, b);
         }
+        if (b < 0 || r >= kv.rows) continue;
+        if (!s.rows_ok || !s.len_ok) {
+            if (lane == 0) kv_flag(kv, Q8_KV_ERR_LENGTH);
+            continue;
+        }
+        pos[i] = (int)(s.len - s.n + (r - s.first));
+        page[i] = __ldg(kv.table + b * kv.table_stride + (pos[i] >> kv.page_log2));
     }
+    bool bad = false;
 #pragma unroll
-    for (int it = 0; it < KV_ITERS; ++it) {
-        const int vec = v0 + it * VPW;
-        float* out = vec < kv.kv ? pk.k_out : pk.v_out;
-        if (vec >= 2 * kv.kv || !out) continue;
-        float y[8];
+    for (int i = 0; i < ROWS; ++i)
+        if (pos[i] >= 0 && (page[i] < 0 || page[i] >= kv.pages)) bad = true, pos[i] = -1;
+    if (bad && lane == 0) kv_flag(kv, Q8_KV_ERR_PAGE);
+    uint2 w[ROWS][KV_ITERS];
+    float d[ROWS][KV_ITERS];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t u = h ? w[it].y : w[it].x;
-            if (WORDS == Q8_KV_INT8) {
-                const uint32_t f = u ^ 0x80808080u;
-                y[4 * h] = i8_to_f32<0>(f), y[4 * h + 1] = i8_to_f32<1>(f);
-                y[4 * h + 2] = i8_to_f32<2>(f), y[4 * h + 3] = i8_to_f32<3>(f);
-            } else {
+    for (int i = 0; i < ROWS; ++i)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)(u >> (16 * i)));
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-                    y[4 * h + 2 * i] = f.x, y[4 * h + 2 * i + 1] = f.y;
-                }
+        for (int it = 0; it < KV_ITERS; ++it) {
+            const int vec = v0 + it * VPW;
+            if (vec < 2 * kv.kv && pos[i] >= 0) {
+                const bool key = vec < kv.kv;
+                const int64_t row = kv_row(kv, page[i], key ? vec : vec - kv.kv, pos[i]);
+                w[i][it] = *reinterpret_cast<const uint2*>((key ? kv.k : kv.v) + row * HD + 8 * l);
+                d[i][it] = (key ? kv.ks : kv.vs)[row];
             }
         }
-        float4* dst = reinterpret_cast<float4*>(out + r * pk.row_stride + (vec < kv.kv ? vec : vec - kv.kv) * pk.head_stride) + 2 * l;
-        dst[0] = make_float4(y[0] * d[it], y[1] * d[it], y[2] * d[it], y[3] * d[it]);
-        dst[1] = make_float4(y[4] * d[it], y[5] * d[it], y[6] * d[it], y[7] * d[it]);
-    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+        for (int it = 0; it < KV_ITERS; ++it) {
+            const int vec = v0 + it * VPW;
+            float* out = vec < kv.kv ? pk.k_out : pk.v_out;
+            if (vec >= 2 * kv.kv || !out || pos[i] < 0) continue;
+            float y[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t u = h ? w[i][it].y : w[i][it].x;
+                if (WORDS == Q8_KV_INT8) {
+                    const uint32_t f = u ^ 0x80808080u;
+                    y[4 * h] = i8_to_f32<0>(f), y[4 * h + 1] = i8_to_f32<1>(f);
+                    y[4 * h + 2] = i8_to_f32<2>(f), y[4 * h + 3] = i8_to_f32<3>(f);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)(u >> (16 * j)));
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+                        y[4 * h + 2 * j] = f.x, y[4 * h + 2 * j + 1] = f.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] *= d[i][it];
+            store8(out + (r0 + i) * pk.row_stride + (vec < kv.kv ? vec : vec - kv.kv) * pk.head_stride + 8 * l, y);
+        }
 }
 
 // Warps a row for `vectors` head vectors of hd values, and the CTAs of `rows` rows.
@@ -266,6 +313,12 @@ int warps_a_row(int vectors, int hd) {
 }
 
 unsigned ctas(int64_t rows, int groups) { return (unsigned)((rows * groups + Q8_WARPS - 1) / Q8_WARPS); }
+
+template <int HD, int WORDS>
+void read_launch(const ReadParams& p, bool many, cudaStream_t st) {
+    if (many) kv_read_kernel<HD, WORDS, 4><<<ctas((p.view.rows + 3) / 4, p.groups), Q8_THREADS, 0, st>>>(p);
+    else kv_read_kernel<HD, WORDS, 1><<<ctas(p.view.rows, p.groups), Q8_THREADS, 0, st>>>(p);
+}
 
 }  // namespace
 
@@ -295,11 +348,14 @@ cudaError_t launch_kv_read(const KvReadCall& c, cudaStream_t st) {
     p.groups = warps_a_row(2 * c.view.kv, c.hd);
     p.k_out = c.k_out, p.v_out = c.v_out;
     p.row_stride = c.row_stride, p.head_stride = c.head_stride;
-    const unsigned grid = ctas(c.view.rows, p.groups);
-    if (c.hd == 128 && c.words == Q8_KV_INT8) kv_read_kernel<128, Q8_KV_INT8><<<grid, Q8_THREADS, 0, st>>>(p);
-    else if (c.hd == 128) kv_read_kernel<128, Q8_KV_E4M3><<<grid, Q8_THREADS, 0, st>>>(p);
-    else if (c.words == Q8_KV_INT8) kv_read_kernel<64, Q8_KV_INT8><<<grid, Q8_THREADS, 0, st>>>(p);
-    else kv_read_kernel<64, Q8_KV_E4M3><<<grid, Q8_THREADS, 0, st>>>(p);
+    const bool many = (int64_t)c.view.rows * p.groups >= 4 * 32 * (int64_t)device_info().sms;  // (four rows a warp leave 32
+    if (c.hd == 128) {                                                                         // warps an SM)
+        if (c.words == Q8_KV_INT8) read_launch<128, Q8_KV_INT8>(p, many, st);
+        else read_launch<128, Q8_KV_E4M3>(p, many, st);
+    } else {
+        if (c.words == Q8_KV_INT8) read_launch<64, Q8_KV_INT8>(p, many, st);
+        else read_launch<64, Q8_KV_E4M3>(p, many, st);
+    }
     return cudaGetLastError();
 }
 
