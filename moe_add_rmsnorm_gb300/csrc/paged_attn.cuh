@@ -32,9 +32,10 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// a / b for a, b >= 0, in 32 bits where both fit (a 64-bit division is about a hundred instructions).
+// a / b for a, b >= 0, in 32 bits where both fit (a 64-bit division is about a hundred instructions, kept out of line).
+static __device__ __noinline__ int64_t div_large(int64_t a, int64_t b) { return a / b; }
 __device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) {
-    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : div_large(a, b);
 }
 
 // The launch's units in one line, sequence by sequence, cut into equal runs: CTA c takes units c*T/C .. (c+1)*T/C - 1 of

@@ -18,7 +18,7 @@
 //  - warps 12-15 turn an item's queries into their parts, the keys into operands, and the values' second half.
 //  - warp 16 issues the products, warp 17 copies the words of 64 positions at a time from the pages (tensor copies of 16
 //    rows, zeros for pages out of range), warp 19 deals out the items and prepares the scales.
-// Registers are moved to the warps that hold the output sums (88, 88, 184, 64 and 56 a thread).
+// Registers are moved to the warps that hold the output sums (80, 80, 184, 80 and 56 a thread).
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -48,6 +48,7 @@ struct PtItem {
     int end;               // positions before which the sequence ends (0: a length out of range)
     int t0, t1;            // the piece's tiles of positions (t0 == t1: no more items)
     int opens;             // whether the piece opens the CTA's run
+    int c0, c1, c0_opens;  // the CTAs that share the item, and whether it opens the first one's run
 };
 
 template <int HD>
@@ -61,6 +62,7 @@ struct PtShared {
     float ks[2][PT_P], vs[2][PT_P];
     float qf[4][PT_M];
     float m_now[4][PT_M], back[4];   // the vectors' running maxima after a tile, and what scales its product back
+    float fold_m[PT_M], fold_i[PT_M]; // a fold's maxima, and the inverses of its sums
     float fin_l[2][PT_M];            // an item's sums, of the even and of the odd tiles
     float ce[2];
     unsigned groups[2];    // which 16-position groups of a tile are there
@@ -178,9 +180,18 @@ __device__ __forceinline__ void tc_load(uint32_t taddr, uint32_t (&r)[N]) {
 // Calls f(i, r) for the columns 16 i .. of 128 columns from taddr, the next ones on their way meanwhile.  A loop, not
 // straight code: what the warps of the roles run has to stay within the SM's instruction cache together (with the softmax
 // unrolled the warps waited for instructions most of the time).
-template <typename F>
+template <bool AHEAD, typename F>
 __device__ __forceinline__ void tc_columns(uint32_t taddr, F f) {
     uint32_t r0[16], r1[16];
+    if (!AHEAD) {  // (half the code, for what runs once an item: fetching code that is not in the cache takes longer)
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+            tc_ld16(taddr + 16 * i, r0);
+            tc_wait16(r0);
+            f(i, r0);
+        }
+        return;
+    }
     tc_ld16(taddr, r0);
 #pragma unroll 1
     for (int i = 0; i < 8; i += 2) {
@@ -205,18 +216,22 @@ __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int r
                  : "memory");
 }
 
-// sum_{i<n} floor((a i + b) / m), n, a, b >= 0, m > 0 (Euclid's steps on (a, m)).
-__device__ __noinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+// sum_{i<n} floor((a i + b) / m) for a < 2^8, n <= 2^24, b < 2^31 and m = 128 (Euclid's steps on (a, m); what is divided stays
+// within 32 bits).
+__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t a, uint32_t b) {
     int64_t sum = 0;
+    uint32_t m = PT_P;
+#pragma unroll 1
     while (n > 0) {
-        sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
-        a %= m;
-        b %= m;
-        const int64_t top = a * n + b;
+        const uint32_t qa = a / m, qb = b / m;
+        sum += (int64_t)n * (n - 1) / 2 * qa + (int64_t)n * qb;
+        a -= qa * m;
+        b -= qb * m;
+        const uint32_t top = a * n + b;
         if (top < m) break;
         n = top / m;
-        b = top % m;
-        const int64_t x = m;
+        b = top - n * m;
+        const uint32_t x = m;
         m = a;
         a = x;
     }
@@ -226,22 +241,21 @@ __device__ __noinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64
 // A sequence's tiles of query vectors: `per` whole tokens each, tile i attending the positions before len - n +
 // min((i + 1) per, n), in units of 128.
 struct PtTiles {
-    int64_t n, per, count, base;
-    int len;
+    int n, per, count, base, len;
     __device__ PtTiles(const KvSeq& s, int group) {
-        n = s.n;
+        n = (int)s.n;
         per = PT_M / group;
         count = (n + per - 1) / per;
         len = s.len_ok ? s.len : 0;
-        base = s.len - s.n;
+        base = s.len - n;
     }
-    __device__ int64_t units(int64_t i) const {
+    __device__ int units(int i) const {
         if (len == 0) return 1;  // a length out of range: zeros to write
-        const int64_t ends = i + 1 < count ? base + (i + 1) * per : len;
+        const int ends = i + 1 < count ? base + (i + 1) * per : len;
         return (ends + PT_P - 1) / PT_P;
     }
-    __device__ int64_t before(int64_t i) const {  // units of the tiles before i (i < count)
-        return len == 0 ? i : floor_sum(i, PT_P, per, base + per + PT_P - 1);
+    __device__ int64_t before(int i) const {  // units of the tiles before i (i < count)
+        return len == 0 ? i : floor_sum(i, per, base + per + PT_P - 1);
     }
     __device__ int64_t all() const { return before(count - 1) + units(count - 1); }
 };
@@ -296,12 +310,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, wg = wid >> 2;
     const int G = pk.group;
 
-    const PagedRun run = paged_run<PT_THREADS>(pk, [&](const KvSeq& s) -> int64_t {
-        return paged_takes(pk, s) ? kv.kv * PtTiles(s, G).all() : 0;
-    });
-    if ((int)blockIdx.x >= run.ctas) return;
-
-    if (tid == 0) {
+    if (tid == 512) {  // (warps 16 and 17 make ready while the others read the batch)
         for (int i = 0; i < PT_ITEMS; ++i) mbar_init(&sh.d_full[i], 1), mbar_init(&sh.d_empty[i], PT_READERS);
         for (int i = 0; i < 8; ++i) mbar_init(&sh.m_full[i / 4][i % 4], 1);
         for (int i = 0; i < 2; ++i) {
@@ -318,14 +327,22 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
         sh.dead = 0;
         fence_barrier_init();
     }
-    if (wid == 16) {
+    if (wid == 17) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc_smem(&sh.tmem)), "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
+    const PagedRun run = paged_run<PT_THREADS>(pk, [&](const KvSeq& s) -> int64_t {
+        return paged_takes(pk, s) ? kv.kv * PtTiles(s, G).all() : 0;
+    });
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;  // columns: scores and weights of three tiles in turn, then the latest product
+
+    if ((int)blockIdx.x >= run.ctas) {
+        if (wid == 17) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+        return;
+    }
 
     // A bounded wait, the same answer in every lane of the warp; false once any role's wait has given up.
     auto wait = [&](uint64_t* bar, unsigned parity) -> bool {
@@ -382,7 +399,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
     };
 
     if (wg < 2) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         // ================ scores to weights of the even (group 0) or odd tiles: thread = query vector
         const int quarter = wid & 3, m = 32 * quarter + lane;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
@@ -418,7 +435,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                     auto softmax = [&](auto with_mask) {
                         constexpr bool MASK = decltype(with_mask)::value;
                         float mx = -INFINITY;  // scores without the query's factor, which is positive
-                        tc_columns(s_at, [&](int c, const uint32_t (&s)[16]) {
+                        tc_columns<!MASK>(s_at, [&](int c, const uint32_t (&s)[16]) {
                             const unsigned seen = MASK ? bits(c) : 0u;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
@@ -449,7 +466,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                         if (m == 0) sh.back[tau & 3] = sh.ce[b];
                         uint64_t sum = 0ull;
                         const uint64_t qf2 = pk2(qf, qf), nm2 = pk2(-ms, -ms), less = pk2(-1.f, -1.f);
-                        tc_columns(s_at, [&](int c, const uint32_t (&s)[16]) {
+                        tc_columns<!MASK>(s_at, [&](int c, const uint32_t (&s)[16]) {
                             const unsigned seen = MASK ? bits(c) : 0u;
                             uint32_t w[16];
 #pragma unroll
@@ -552,8 +569,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                                 o[16 * c + i] = fma2(pk2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), back2, o[16 * c + i]);
                         }
                     }
-                    tc_fence_before();
-                    arrive(&sh.t_empty);
+                    if (x < tiles + 1) {  // (the last product's place takes the sums first)
+                        tc_fence_before();
+                        arrive(&sh.t_empty);
+                    }
                 }
                 if (x < tiles) {
                     unsigned char* to = sh.v[tx & 1];
@@ -573,69 +592,111 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
             const int token = m / G;
             const int64_t row = d.row0 + token;
             const int head = d.head * G + (m - token * G);
-            bool write = valid;
-            if (d.t0 != 0 || d.t1 != d.units) {
-                float* slot = pk.part + (int64_t)(2 * blockIdx.x + (d.opens ? 0 : 1)) * SLOT;
-                if (valid) {
+            // The sums go back to tensor memory (the product's place), from where loops take them sixteen at a time: indexed
+            // registers would make straight code of every one of these loops, and an item's end runs once an item, out of
+            // the instruction cache.
+            const uint32_t o_at = tmem + lanes + 384;
+            if (active) {
 #pragma unroll
-                    for (int i = 0; i < HD / 4; ++i) {
-                        float4 v;
-                        upk2(o[2 * i], v.x, v.y), upk2(o[2 * i + 1], v.z, v.w);
-                        __stcg(reinterpret_cast<float4*>(slot) + i * PT_M + m, v);
+                for (int c = 0; c < HD / 16; ++c) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float x, y;
+                        upk2(o[8 * c + i], x, y);
+                        r[2 * i] = __float_as_uint(x), r[2 * i + 1] = __float_as_uint(y);
                     }
-                    __stcg(slot + PT_M * HD + m, mr);
-                    __stcg(slot + PT_M * (HD + 1) + m, l);
+                    tc_st16(o_at + 16 * c, r);
                 }
-                const int c0 = run.owner(d.at), c1 = run.owner(d.at + d.units - 1);
-                arrive(&sh.met);
-                if (!(ok = wait(&sh.met, meets++))) break;
-                if (m == 0) {
-                    sh.last = atomic_add_acq_rel_gpu(pk.counters + c0, 1) == c1 - c0;
-                    if (sh.last) pk.counters[c0] = 0;
-                }
-                arrive(&sh.met);
-                if (!(ok = wait(&sh.met, meets++))) break;
-                write = valid && sh.last;
-                if (write) {  // the last CTA to arrive folds the item's pieces in order
-                    const bool opens = run.start(c0) == d.at;
-                    auto slot_of = [&](int c) { return pk.part + (int64_t)paged_slot(c, c0, opens) * SLOT; };
-                    float mx = -INFINITY;
+                tc_wait_st();
+            }
+            const bool whole = d.t0 == 0 && d.t1 == d.units;
+            float* slot = pk.part + (int64_t)(2 * blockIdx.x + (d.opens ? 0 : 1)) * SLOT;
+            const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            float* dst = whole ? pk.out + row * pk.out_stride + (int64_t)head * HD : slot + 4 * m;
+            const int step = whole ? 4 : 4 * PT_M;  // a partial result's float4 i of vector m at 4 (PT_M i + m)
+            if (active) {
 #pragma unroll 1
-                    for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, __ldcg(slot_of(c) + PT_M * HD + m));
-                    const float ms = mx == -INFINITY ? 0.f : mx;
+                for (int c = 0; c < HD / 32; ++c) {
+                    uint32_t r[32];
+                    tc_load<32>(o_at + 32 * c, r);
+                    if (!valid) continue;
 #pragma unroll
-                    for (int i = 0; i < HD / 2; ++i) o[i] = 0ull;
-                    l = 0.f;
+                    for (int i = 0; i < 8; ++i)
+                        __stcg(reinterpret_cast<float4*>(dst + (8 * c + i) * step),
+                               make_float4(__uint_as_float(r[4 * i]) * inv, __uint_as_float(r[4 * i + 1]) * inv,
+                                           __uint_as_float(r[4 * i + 2]) * inv, __uint_as_float(r[4 * i + 3]) * inv));
+                }
+            }
+            tc_fence_before();
+            arrive(&sh.t_empty);  // (the last tile's: its place is free now)
+            if (whole) {
+                if (valid && pk.lse) pk.lse[row * pk.heads + head] = l == 0.f ? -INFINITY : (mr + log2f(l)) * 0.693147180559945f;
+                continue;
+            }
+            if (valid) {
+                __stcg(slot + PT_M * HD + m, mr);
+                __stcg(slot + PT_M * (HD + 1) + m, l);
+            }
+            arrive(&sh.met);
+            if (!(ok = wait(&sh.met, meets++))) break;
+            if (m == 0) {
+                sh.last = atomic_add_acq_rel_gpu(pk.counters + d.c0, 1) == d.c1 - d.c0;
+                if (sh.last) pk.counters[d.c0] = 0;
+            }
+            arrive(&sh.met);
+            if (!(ok = wait(&sh.met, meets++))) break;
+            if (!sh.last) continue;
+            // The last CTA to arrive folds the item's pieces in order: every vector's maximum and sum, then its values, the
+            // threads spread over vectors and float4s, four of these a thread at a time.
+            auto slot_of = [&](int c) { return pk.part + (int64_t)paged_slot(c, d.c0, d.c0_opens) * SLOT; };
+            if (valid) {
+                float mx = -INFINITY, sum = 0.f;
+#pragma unroll 2
+                for (int c = d.c0; c <= d.c1; ++c) mx = fmaxf(mx, __ldcg(slot_of(c) + PT_M * HD + m));
+                const float ms = mx == -INFINITY ? 0.f : mx;
+#pragma unroll 2
+                for (int c = d.c0; c <= d.c1; ++c)
+                    sum = fmaf(__ldcg(slot_of(c) + PT_M * (HD + 1) + m), ex2(__ldcg(slot_of(c) + PT_M * HD + m) - ms), sum);
+                sh.fold_m[m] = ms;
+                sh.fold_i[m] = sum == 0.f ? 0.f : 1.f / sum;
+                if (pk.lse) pk.lse[row * pk.heads + head] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.693147180559945f;
+            }
+            arrive(&sh.met);
+            if (!(ok = wait(&sh.met, meets++))) break;
+            const int vectors = d.tokens * G, log2 = vectors > 1 ? 32 - __clz(vectors - 1) : 0;
+            const int vec = m & ((1 << log2) - 1), groups = PT_M >> log2;
+            if (vec < vectors) {
+                const int tk = vec / G;
+                const float ms = sh.fold_m[vec], f = sh.fold_i[vec];
+                float4* to = reinterpret_cast<float4*>(pk.out + (d.row0 + tk) * pk.out_stride + (int64_t)(d.head * G + vec - tk * G) * HD);
 #pragma unroll 1
-                    for (int c = c0; c <= c1; ++c) {
+                for (int i0 = m >> log2; i0 < HD / 4; i0 += 4 * groups) {
+                    float4 v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                    for (int c = d.c0; c <= d.c1; ++c) {
                         const float* sl = slot_of(c);
-                        const float f = ex2(__ldcg(sl + PT_M * HD + m) - ms);
-                        l += __ldcg(sl + PT_M * (HD + 1) + m) * f;
-                        const uint64_t f2 = pk2(f, f);
+                        const float w = ex2(__ldcg(sl + PT_M * HD + vec) - ms);
 #pragma unroll
-                        for (int i = 0; i < HD / 4; ++i) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4*>(sl) + i * PT_M + m);
-                            o[2 * i] = fma2(pk2(v.x, v.y), f2, o[2 * i]);
-                            o[2 * i + 1] = fma2(pk2(v.z, v.w), f2, o[2 * i + 1]);
+                        for (int i = 0; i < 4; ++i) {
+                            if (i0 + i * groups >= HD / 4) break;
+                            const float4 p = __ldcg(reinterpret_cast<const float4*>(sl) + (i0 + i * groups) * PT_M + vec);
+                            v[i].x = fmaf(p.x, w, v[i].x), v[i].y = fmaf(p.y, w, v[i].y);
+                            v[i].z = fmaf(p.z, w, v[i].z), v[i].w = fmaf(p.w, w, v[i].w);
                         }
                     }
-                    mr = mx;
-                }
-            }
-            if (write) {
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                float4* dst = reinterpret_cast<float4*>(pk.out + row * pk.out_stride + (int64_t)head * HD);
 #pragma unroll
-                for (int i = 0; i < HD / 4; ++i) {
-                    float4 v;
-                    upk2(o[2 * i], v.x, v.y), upk2(o[2 * i + 1], v.z, v.w);
-                    dst[i] = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                    for (int i = 0; i < 4; ++i)
+                        if (i0 + i * groups < HD / 4) to[i0 + i * groups] = make_float4(v[i].x * f, v[i].y * f, v[i].z * f, v[i].w * f);
                 }
-                if (pk.lse) pk.lse[row * pk.heads + head] = l == 0.f ? -INFINITY : (mr + log2f(l)) * 0.693147180559945f;
             }
+            arrive(&sh.met);  // (the fold's arrays are the next one's)
+            if (!(ok = wait(&sh.met, meets++))) break;
         }
     } else if (wg == 3) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         // ================ operand tiles in f16: queries, keys, and the second half of each tile's values
         const int w = wid - 12;
         int tau = 0;
@@ -643,22 +704,33 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
         bool ok = true;
 #pragma unroll 1
         for (int it = 0; ok && next_item(it, d); ++it) {
-            if (!(ok = wait(&sh.q_empty, it + 1))) break;
             const int r = lane & 7, cc = lane >> 3;
+            auto source = [&](int i) -> const float* {  // this lane's row of the i-th 8 query vectors, or null
+                const int m = 32 * w + 8 * i + r, token = m / G;
+                if (m >= d.tokens * G) return nullptr;
+                return pk.q + (d.row0 + token) * pk.q_stride + (int64_t)(d.head * G + m - token * G) * HD + 8 * cc;
+            };
+            auto fetch = [&](const float* p) {  // towards L1, a lane its 32 bytes of each chunk
+                if (!p) return;
+#pragma unroll
+                for (int c = 0; c < HD / 32; ++c) asm volatile("prefetch.global.L1 [%0];" ::"l"(p + 32 * c));
+            };
+            const float* src = source(0);
+            fetch(src);
+            if (!(ok = wait(&sh.q_empty, it + 1))) break;
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) {  // 8 query vectors at a time, a lane HD / 32 chunks of 8 dimensions
                 const int m = 32 * w + 8 * i + r;
-                const int64_t row = d.row0 + m / G;
-                const bool valid = m < d.tokens * G;
-                const float* src = pk.q + (valid ? row * pk.q_stride + (int64_t)(d.head * G + m % G) * HD : 0);
+                const float* ahead = i < 3 ? source(i + 1) : nullptr;
+                fetch(ahead);
                 float x[HD / 32][8];
                 unsigned big = 0u;
 #pragma unroll
                 for (int c = 0; c < HD / 32; ++c) {
                     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-                    if (valid) {
-                        a = *reinterpret_cast<const float4*>(src + 8 * (cc + 4 * c));
-                        b = *reinterpret_cast<const float4*>(src + 8 * (cc + 4 * c) + 4);
+                    if (src) {
+                        a = *reinterpret_cast<const float4*>(src + 32 * c);
+                        b = *reinterpret_cast<const float4*>(src + 32 * c + 4);
                     }
                     x[c][0] = a.x, x[c][1] = a.y, x[c][2] = a.z, x[c][3] = a.w;
                     x[c][4] = b.x, x[c][5] = b.y, x[c][6] = b.z, x[c][7] = b.w;
@@ -669,7 +741,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                 big = max(big, __shfl_xor_sync(0xffffffffu, big, 16));
                 const int e = big == 0u ? 0 : 14 - exponent_of(big);
                 const float f = pow2i(e);
-                if (cc == 0) sh.qf[it & 3][m] = valid ? pow2i(-e) * pk.scale : 0.f;
+                if (cc == 0) sh.qf[it & 3][m] = src ? pow2i(-e) * pk.scale : 0.f;
+                src = ahead;
 #pragma unroll
                 for (int c = 0; c < HD / 32; ++c) {
                     uint32_t h[4], lo[4];
@@ -833,7 +906,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
         } else if (wid == 19) {
             // ================ items and scales
             int b = run.seq;
-            int64_t b_at = run.seq_at, i = 0, h = 0, cur = run.lo;
+            int64_t b_at = run.seq_at, h = 0, cur = run.lo;
+            int i = 0;
             bool found = false;
             int tau = 0, it = 0;
 #pragma unroll 1
@@ -846,11 +920,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                     if (!found) {  // the run's first item: the head and the tile of unit run.lo
                         const PtTiles t(s, G);
                         const int64_t all = t.all();
-                        h = (cur - b_at) / all;
+                        h = div_small(cur - b_at, all);
                         b_at += h * all;  // from here on the first unit of the head
-                        int64_t lo = 0, hi = t.count - 1;
+                        int lo = 0, hi = t.count - 1;
                         while (lo < hi) {
-                            const int64_t mid = (lo + hi + 1) / 2;
+                            const int mid = (lo + hi + 1) / 2;
                             if (t.before(mid) <= cur - b_at) lo = mid;
                             else hi = mid - 1;
                         }
@@ -862,15 +936,17 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                     const int64_t U = t.units(i), u0 = cur - b_at;
                     d.at = b_at;
                     d.units = U;
-                    d.row0 = s.first + i * t.per;
+                    d.row0 = s.first + (int64_t)i * t.per;
                     d.seq = b;
                     d.head = (int)h;
-                    d.tokens = (int)min(t.per, t.n - i * t.per);
-                    d.pos = (int)(t.base + i * t.per);
+                    d.tokens = min(t.per, t.n - i * t.per);
+                    d.pos = t.base + i * t.per;
                     d.end = t.len;
                     d.t0 = (int)u0;
                     d.t1 = (int)min(U, u0 + (run.hi - cur));
                     d.opens = cur == run.lo;
+                    d.c0 = run.owner(d.at), d.c1 = run.owner(d.at + U - 1);
+                    d.c0_opens = run.start(d.c0) == d.at;
                     cur += d.t1 - d.t0;
                     if (d.t1 == U) {  // on to the next item: the next tile, head or sequence
                         b_at += U;
@@ -923,7 +999,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (wid == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    if (wid == 17) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
