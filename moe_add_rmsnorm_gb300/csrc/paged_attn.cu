@@ -11,15 +11,23 @@
 // form, m16n8k16: 16 positions (or dimensions) by 8 vectors.  Words are exact in f16.  The f32 operand (query, or weight
 // times value scale) is scaled by a power of two and split into two f16 parts, x = hi + lo to 2^-22, both products
 // accumulated in f32.
-//  - A warp takes 16 positions at a time straight from the pages into registers (no shared memory: a position's words are
-//    used by one warp).  The order of a contraction's index is free, so each lane loads 32 (hd 128) consecutive bytes of
-//    a key row as its share of the scores' dimensions, and 16 of four value rows as its share of the output's.
+//  - A warp takes 16 positions at a time from a ring of its own: two stages in shared memory, filled by tensor copies of
+//    a page's 16 rows that are issued as a stage is read out, waited for by that warp alone.  (Loads straight into
+//    registers could be issued only half a step ahead within 128 registers: 64 sequences of up to 4096, 32 heads over 4,
+//    took 52.9 us for 49.2, one of 100003 took 41.0 for 39.2.)  The order of a contraction's index is free, so each
+//    lane reads 32 (hd 128) consecutive bytes of a key row as its share of the scores' dimensions, and 16 of four value
+//    rows as its share of the output's; the copies' swizzle keeps those reads apart.
 //  - Scores come out as positions by vectors and go back in as the second product's operand after an 8 x 8 transpose of
 //    their f16 parts across the warp.
-//  - Every warp keeps its own running maximum and sums.  The tensor cores truncate as they accumulate, so every 8 steps
-//    the products are added (rounded) to the warp's f32 totals in shared memory.
-//  - 16 warps a CTA, one CTA an SM, each CTA an equal run of 128-position units over the whole batch.  The warps' results
-//    meet in shared memory; an item that several CTAs share meets in the workspace, folded in order by the last to arrive.
+//  - Every warp keeps its own running maximum and sums, rescaled only when one moves.  The tensor cores truncate as they
+//    accumulate, so every 8 steps the products are added (rounded) to the warp's f32 totals in shared memory.
+//  - 8 warps a CTA, two CTAs an SM (one for more than 8 vectors, whose sums take the registers), each CTA an equal run of
+//    128-position units over the whole batch.  The warps' results meet in shared memory; an item that several CTAs share
+//    meets in the workspace, folded in order by the last to arrive.
+//
+// What bounds it: instruction issue.  A step is 580 warp instructions on 4224 bytes (over a third turn bytes into pairs of
+// f16, the rest are the products, the softmax and the splits); 64 sequences of 4096 issue 0.55 a clock with the memory at 56% of
+// its rate.
 #include <cuda_fp16.h>
 
 #include "paged_attn.cuh"
@@ -28,7 +36,7 @@ namespace q8 {
 
 namespace {
 
-constexpr int PR_WARPS = 8, PR_THREADS = PR_WARPS * 32, PR_CTAS = 2;  // two CTAs an SM
+constexpr int PR_WARPS = 8, PR_THREADS = PR_WARPS * 32;
 constexpr int PR_UNIT = 128;   // positions a unit
 constexpr int PR_STEP = 16;    // positions a warp takes at a time
 constexpr int PR_FLUSH = 8;    // steps between additions to the totals
@@ -86,31 +94,17 @@ __device__ __forceinline__ int exponent_of(unsigned bits) {
     return bits >= 0x7f800000u ? 0 : max((int)(bits >> 23) - 127, -100);
 }
 
-
 template <int BYTES>
 struct Bytes {
     uint32_t w[BYTES / 4];
 };
 
-template <int BYTES>
-__device__ __forceinline__ void load_words(const int8_t* p, Bytes<BYTES>& b) {
-    if constexpr (BYTES == 32) {
-        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=r"(b.w[0]), "=r"(b.w[1]), "=r"(b.w[2]), "=r"(b.w[3]), "=r"(b.w[4]), "=r"(b.w[5]), "=r"(b.w[6]),
-                       "=r"(b.w[7])
-                     : "l"(p));
-    } else if constexpr (BYTES == 16) {
-        asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(b.w[0]), "=r"(b.w[1]), "=r"(b.w[2]), "=r"(b.w[3])
-                     : "l"(p));
-    } else {
-        asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0,%1}, [%2];" : "=r"(b.w[0]), "=r"(b.w[1]) : "l"(p));
-    }
-}
-
 // NT: 8-vector tiles an item (1 or 2).
 template <int HD, int NT>
 struct RowsShared {
+    static constexpr int CTAS = NT == 1 ? 2 : 1;           // of an SM
+    unsigned char ring[PR_WARPS][2][2][PR_STEP * HD];      // each warp's next steps: two stages of keys and values
+    uint64_t full[PR_WARPS][2];
     static constexpr int MT = 8 * NT, FR = HD / 16 * NT;   // vectors an item; float4 totals a lane
     uint4 q[NT][HD / 16][32];          // the queries' parts in the scores' operand order: hi (2 registers), lo
     float4 o[PR_WARPS][FR][32];        // the warps' totals, in the accumulators' order
@@ -125,11 +119,13 @@ struct RowsShared {
 };
 
 template <int HD, int WORDS, int NT>
-__global__ void __launch_bounds__(PR_THREADS, PR_CTAS) paged_rows_kernel(const PagedParams pk) {
+__global__ void __launch_bounds__(PR_THREADS, RowsShared<HD, NT>::CTAS)
+    paged_rows_kernel(const PagedParams pk, const __grid_constant__ CUtensorMap map_k,
+                      const __grid_constant__ CUtensorMap map_v) {
     constexpr int MT = 8 * NT, KB = HD / 4, KS = HD / 16, DPG = HD / 8, FR = HD / 16 * NT;
     constexpr int SLOT = FR * 32 * 4 + 2 * MT;  // floats of a partial result
-    extern __shared__ __align__(16) unsigned char raw[];
-    RowsShared<HD, NT>& sh = *reinterpret_cast<RowsShared<HD, NT>*>(raw);
+    extern __shared__ unsigned char raw[];
+    RowsShared<HD, NT>& sh = *reinterpret_cast<RowsShared<HD, NT>*>(raw + (1024u - smem_addr(raw) % 1024u) % 1024u);
     const KvView& kv = pk.view;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
     const int G = pk.group;
@@ -148,9 +144,20 @@ __global__ void __launch_bounds__(PR_THREADS, PR_CTAS) paged_rows_kernel(const P
             sh.cur = sh.lo = run.lo, sh.hi = run.hi;
             sh.seq = run.seq, sh.seq_at = run.seq_at;
             sh.total = run.total, sh.ctas = run.ctas;
+            for (int i = 0; i < 2 * PR_WARPS; ++i) mbar_init(&sh.full[0][i], 1);
+            fence_barrier_init();
         }
     }
     __syncthreads();
+
+    // Where this lane reads a stage: keys of rows g, g + 8, 32 dimensions from KB t (two 16-byte chunks; hd 64: one);
+    // values of rows 2t, 2t + 1, 2t + 8, 2t + 9, dimensions from DPG g; as the tensor copies' swizzle places them (a
+    // quarter warp's reads lie in different banks).
+    const uint32_t k_lane = HD == 128 ? g * 128 + (((2 * t) ^ g) << 4) : g * 64 + ((t ^ ((g >> 1) & 3)) << 4);
+    const uint32_t k_next = g * 128 + (((2 * t + 1) ^ g) << 4);  // (hd 128)
+    const uint32_t v_lane = HD == 128 ? 2 * t * 128 + ((g ^ (2 * t)) << 4) : 2 * t * 64 + (((g >> 1) ^ t) << 4) + (g & 1) * 8;
+    const uint32_t v_odd = HD == 128 ? (2 * t + 1) * 128 + ((g ^ (2 * t + 1)) << 4) : v_lane + 64;
+    unsigned used = 0;  // steps this warp has taken
 
     for (;;) {
         int b, begin, end, h;
@@ -183,9 +190,6 @@ __global__ void __launch_bounds__(PR_THREADS, PR_CTAS) paged_rows_kernel(const P
 
         // ---- this warp's first positions are on their way while the queries are prepared
         const int steps = end > begin ? (end - begin + PR_STEP - 1) / PR_STEP : 0;  // of all warps
-        Bytes<KB> kw[2];
-        Bytes<DPG> vw[4];
-        float ks[2], vs[2];
         int page_l = -1;  // this lane's: the page of the warp's step (batch of 32 steps)
         auto look_up = [&](int i) {  // the pages of the warp's steps i .. i + 31
             const int step = wid + (i + lane) * PR_WARPS;
@@ -195,43 +199,40 @@ __global__ void __launch_bounds__(PR_THREADS, PR_CTAS) paged_rows_kernel(const P
                 if (page_l < 0) kv_flag(kv, Q8_KV_ERR_PAGE);
             }
         };
-        // This lane's places in the page of step i, as byte offsets from page 0: keys of row g, 32 dimensions from KB t;
-        // values of row 2t, dimensions from DPG g.
-        const uint32_t page_rows = (uint32_t)kv.kv << kv.page_log2;
-        const int8_t* k_at = kv.k + (((int64_t)h << kv.page_log2) + g) * HD + KB * t;
-        const int8_t* v_at = kv.v + (((int64_t)h << kv.page_log2) + 2 * t) * HD + DPG * g;
-        const float* ks_at = kv.ks + ((int64_t)h << kv.page_log2) + g;
-        const float* vs_at = kv.vs + ((int64_t)h << kv.page_log2) + g;
-        auto row_of = [&](int i, int& page) -> int64_t {  // the cached row of step i's first position, heads before h left out
-            page = __shfl_sync(0xffffffffu, page_l, i & 31);
-            const uint32_t slot = (uint32_t)(begin + (wid + i * PR_WARPS) * PR_STEP) & ((1u << kv.page_log2) - 1);
-            return (int64_t)((uint64_t)(uint32_t)max(page, 0) * page_rows + slot);
+        auto page_of = [&](int i) { return __shfl_sync(0xffffffffu, page_l, i & 31); };
+        auto slot_of_step = [&](int i) {  // the row of step i's first position in its page
+            return (h << kv.page_log2) + ((begin + (wid + i * PR_WARPS) * PR_STEP) & ((1 << kv.page_log2) - 1));
         };
-        auto load_k = [&](int64_t row) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                load_words<KB>(k_at + row * HD + 8 * j * HD, kw[j]);
-                ks[j] = ld_scale_stream(ks_at + row + 8 * j);
+        auto issue = [&](int i, int page) {  // step i's words on their way
+            if (lane == 0) {
+                const unsigned stage = (used + i) & 1;
+                mbar_arrive_expect_tx(&sh.full[wid][stage], 2 * PR_STEP * HD);
+                tma_box(sh.ring[wid][stage][0], &map_k, slot_of_step(i), page < 0 ? kv.pages : page, &sh.full[wid][stage]);
+                tma_box(sh.ring[wid][stage][1], &map_v, slot_of_step(i), page < 0 ? kv.pages : page, &sh.full[wid][stage]);
             }
         };
-        auto load_v = [&](int64_t row) {
+        const uint32_t page_rows = (uint32_t)kv.kv << kv.page_log2;
+        float ks[2], vs[2];
+        auto load_scales = [&](int i, int page) {
+            const uint64_t row = (uint64_t)(uint32_t)max(page, 0) * page_rows + slot_of_step(i) + g;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) load_words<DPG>(v_at + row * HD + ((j & 1) + 8 * (j >> 1)) * HD, vw[j]);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) vs[j] = ld_scale_stream(vs_at + row + 8 * j);
+            for (int j = 0; j < 2; ++j) ks[j] = ld_scale_stream(kv.ks + row + 8 * j), vs[j] = ld_scale_stream(kv.vs + row + 8 * j);
         };
         const int mine = steps > wid ? (steps - wid + PR_WARPS - 1) / PR_WARPS : 0;
-        int page = -1, page_next = -1;
-        int64_t row_next = 0;
+        int page_next = -1, page_after = -1;
         if (mine > 0) {
             look_up(0);
-            row_next = row_of(0, page_next);
-            load_k(row_next);
-            load_v(row_next);
+            page_next = page_of(0);
+            issue(0, page_next);
+            load_scales(0, page_next);
+            if (mine > 1) {
+                page_after = page_of(1);
+                issue(1, page_after);
+            }
         }
         // ---- the item's queries: a warp a vector, split into two f16 parts after a scaling by a power of two
-        if (wid < MT) {
-            const int64_t m = m0 + wid;
+        for (int vec = wid; vec < MT; vec += PR_WARPS) {
+            const int64_t m = m0 + vec;
             const bool valid = m < s.n * G;
             const int token = (int)div_small(m, G);
             const int64_t row = s.first + token;
@@ -247,12 +248,12 @@ __global__ void __launch_bounds__(PR_THREADS, PR_CTAS) paged_rows_kernel(const P
             uint4 r;
             split2(x.x * f, x.y * f, r.x, r.z);
             split2(x.z * f, x.w * f, r.y, r.w);
-            if (lane < HD / 4) sh.q[wid / 8][lane % KS][(wid % 8) * 4 + lane / KS] = r;
+            if (lane < HD / 4) sh.q[vec / 8][lane % KS][(vec % 8) * 4 + lane / KS] = r;
             if (lane == 0) {
-                sh.qf[wid] = pow2i(-e) * pk.scale;
-                sh.lim[wid] = valid && s.len_ok ? (int)(s.len - s.n + token) : -1;
-                sh.at[wid] = valid ? row * pk.out_stride + (int64_t)head * HD : -1;
-                sh.lse_at[wid] = row * pk.heads + head;
+                sh.qf[vec] = pow2i(-e) * pk.scale;
+                sh.lim[vec] = valid && s.len_ok ? (int)(s.len - s.n + token) : -1;
+                sh.at[vec] = valid ? row * pk.out_stride + (int64_t)head * HD : -1;
+                sh.lse_at[vec] = row * pk.heads + head;
             }
         }
         __syncthreads();
@@ -282,11 +283,24 @@ __global__ void __launch_bounds__(PR_THREADS, PR_CTAS) paged_rows_kernel(const P
         int exp_run = -100, exp_top = -100;  // the weights' scaling, and the largest it has been
 #pragma unroll 1
         for (int i = 0; i < mine; ++i) {
-            page = page_next;
+            const int page = page_next;
             const int p0 = begin + (wid + i * PR_WARPS) * PR_STEP;
-            if (i + 1 < mine) {
-                if (((i + 1) & 31) == 0) look_up(i + 1);
-                row_next = row_of(i + 1, page_next);
+            const unsigned stage = (used + i) & 1;
+            const float kscale[2] = {ks[0], ks[1]}, vraw[2] = {vs[0], vs[1]};
+            if (i + 1 < mine) load_scales(i + 1, page_after);
+            bool got = try_wait(&sh.full[wid][stage], ((used + i) >> 1) & 1);
+#pragma unroll 1
+            for (unsigned poll = 0; !got && poll < PA_POLLS; ++poll) got = try_wait(&sh.full[wid][stage], ((used + i) >> 1) & 1);
+            if (!got) kv_flag(kv, Q8_KV_ERR_WAIT);
+            Bytes<KB> kw[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const unsigned char* from = sh.ring[wid][stage][0] + 8 * HD * j;
+#pragma unroll
+                for (int x = 0; x < KB / 16; ++x) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(from + (x ? k_next : k_lane));
+                    kw[j].w[4 * x] = w.x, kw[j].w[4 * x + 1] = w.y, kw[j].w[4 * x + 2] = w.z, kw[j].w[4 * x + 3] = w.w;
+                }
             }
             // scores: positions g, g + 8 by vectors 2t, 2t + 1 of each tile
             float sh_hi[NT][4], sh_lo[NT][4];
@@ -306,15 +320,13 @@ __global__ void __launch_bounds__(PR_THREADS, PR_CTAS) paged_rows_kernel(const P
                     mma16816(sh_lo[n], a0, a1, a2, a3, q.z, q.w);
                 }
             }
-            const float kscale[2] = {ks[0], ks[1]};
-            if (i + 1 < mine) load_k(row_next);
             // the softmax's running maximum and sums, and the weights' parts
             const bool here = page >= 0;
             float vscale[2];
             unsigned vtop = 0u;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                vscale[j] = here && p0 + g + 8 * j < end ? vs[j] : 0.f;
+                vscale[j] = here && p0 + g + 8 * j < end ? vraw[j] : 0.f;
                 vtop = max(vtop, __float_as_uint(fabsf(vscale[j])));
             }
             vtop = __reduce_max_sync(0xffffffffu, vtop);
@@ -403,6 +415,18 @@ __global__ void __launch_bounds__(PR_THREADS, PR_CTAS) paged_rows_kernel(const P
 #pragma unroll
                 for (int j = 0; j < 2; ++j) ph[n][j] = transpose8x8(ph[n][j]), pl[n][j] = transpose8x8(pl[n][j]);
             }
+            Bytes<DPG> vw[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const unsigned char* from = sh.ring[wid][stage][1] + 8 * HD * (j >> 1) + (j & 1 ? v_odd : v_lane);
+                if constexpr (DPG == 16) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(from);
+                    vw[j].w[0] = w.x, vw[j].w[1] = w.y, vw[j].w[2] = w.z, vw[j].w[3] = w.w;
+                } else {
+                    const uint2 w = *reinterpret_cast<const uint2*>(from);
+                    vw[j].w[0] = w.x, vw[j].w[1] = w.y;
+                }
+            }
             if (p0 + PR_STEP > end || !here) {  // words past the end are whatever the page holds: left out
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -429,7 +453,13 @@ __global__ void __launch_bounds__(PR_THREADS, PR_CTAS) paged_rows_kernel(const P
                         mma16816(acc[n][2 * x + y], a[0][2 * y], a[0][2 * y + 1], a[1][2 * y], a[1][2 * y + 1], ph[n][0], ph[n][1]);
                     }
             }
-            if (i + 1 < mine) load_v(row_next);
+            __syncwarp();  // every lane has read the stage
+            page_next = page_after;
+            if (i + 2 < mine) {
+                if (((i + 2) & 31) == 0) look_up(i + 2);
+                page_after = page_of(i + 2);
+                issue(i + 2, page_after);
+            }
             if (i % PR_FLUSH == PR_FLUSH - 1 || i + 1 == mine) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -447,6 +477,7 @@ __global__ void __launch_bounds__(PR_THREADS, PR_CTAS) paged_rows_kernel(const P
                 }
             }
         }
+        used += mine;
         // ---- the warps meet: every vector's maximum and sum, then the totals with each warp's factor
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -556,19 +587,19 @@ __global__ void __launch_bounds__(PR_THREADS, PR_CTAS) paged_rows_kernel(const P
     }
 }
 
-// The launch's CTAs: what the GPU holds at once, and no more pieces of an item than the fold's weights have room for.
-int rows_ctas() { return device_info().sms < 256 ? PR_CTAS * device_info().sms : 2 * 255; }
-static_assert(2 * 255 * 8 * sizeof(float) <= sizeof(RowsShared<64, 1>::o) && 2 * 255 * 16 * sizeof(float) <= sizeof(RowsShared<64, 2>::o),
+static_assert(2 * 255 * 8 * sizeof(float) <= sizeof(RowsShared<64, 1>::o) && 255 * 16 * sizeof(float) <= sizeof(RowsShared<64, 2>::o),
               "the fold's weights over the warps' totals");
 
 template <int HD, int WORDS, int NT>
 cudaError_t rows_launch(const PagedParams& p, cudaStream_t st) {
     auto kernel = paged_rows_kernel<HD, WORDS, NT>;
-    constexpr size_t smem = sizeof(RowsShared<HD, NT>);
-    static_assert(PR_CTAS * (smem + 2048) <= 233472, "the CTAs of an SM within its shared memory");
+    constexpr size_t smem = sizeof(RowsShared<HD, NT>) + 1024;
+    static_assert(RowsShared<HD, NT>::CTAS * (smem + 2048) <= 233472, "the CTAs of an SM within its shared memory");
+    CUtensorMap mk, mv;
+    if (!paged_words_map(&mk, p.view.k, p.view, HD) || !paged_words_map(&mv, p.view.v, p.view, HD)) return cudaErrorNotSupported;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<rows_ctas(), PR_THREADS, smem, st>>>(p);
+    kernel<<<paged_rows_ctas(NT), PR_THREADS, smem, st>>>(p, mk, mv);
     return cudaGetLastError();
 }
 
@@ -580,6 +611,12 @@ cudaError_t rows_launch_nt(const PagedParams& p, int tiles, cudaStream_t st) {
 constexpr int kRowsMost = 16;  // query vectors a key/value head that this kernel's item holds
 
 }  // namespace
+
+// What the GPU holds at once, and no more pieces of an item than the fold's weights have room for.
+int paged_rows_ctas(int tiles) {
+    const int sms = device_info().sms < 255 ? device_info().sms : 255;
+    return tiles == 1 ? RowsShared<64, 1>::CTAS * sms : RowsShared<64, 2>::CTAS * sms;
+}
 
 size_t paged_rows_slot(int hd) { return (size_t)kRowsMost * (hd + 2) * sizeof(float); }
 
@@ -611,7 +648,7 @@ cudaError_t launch_paged_attention(const PagedAttnCall& c, Carve& ws, cudaStream
         x.part = ws.take<float>(2 * (size_t)ctas * slot / sizeof(float));
         x.counters = ws.take_counters(ctas);
     };
-    if (rows) scratch(p, rows_ctas(), paged_rows_slot(c.hd));
+    if (rows) scratch(p, paged_rows_ctas(p.group <= 8 ? 1 : 2), paged_rows_slot(c.hd));
     if (tiles) scratch(t, sms, paged_tiles_slot(c.hd));
     if (ws.overflow) return cudaSuccess;  // refused by the caller; nothing is launched
     p.upto = tiles ? kRowsMost : INT64_MAX;

@@ -1,6 +1,7 @@
 // What the two kernels of the paged attention share: the call as they read it, and the division of a batch's work over
 // the CTAs of one launch.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <limits.h>
 #include <math.h>
@@ -8,6 +9,7 @@
 
 #include "common.cuh"
 #include "kv_pages.cuh"
+#include "stream.cuh"
 
 namespace q8 {
 
@@ -119,7 +121,35 @@ __device__ __forceinline__ bool paged_takes(const PagedParams& pk, const KvSeq& 
     return s.rows_ok && s.n > 0 && vectors > pk.above && vectors <= pk.upto;
 }
 
+// ---- the pages' words by tensor copies -----------------------------------------------------------------------------
+// A map of words [pages][kv * page_size][hd], read 16 rows of a page at a time with the 128- or 64-byte swizzle
+// (paged_attn_tc.cu); false where the driver has no encoder.
+bool paged_words_map(CUtensorMap* m, const void* words, const KvView& v, int hd);
+
+// A tensor copy of one page's 16 rows from `row` of its [heads * page_size] rows into shared memory (zeros for a page out
+// of range), counted on bar's transaction bytes.
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int row, int page, uint64_t* bar) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                 ::"r"(smem_addr(dst)), "l"(map), "r"(0), "r"(row), "r"(page), "r"(smem_addr(bar))
+                 : "memory");
+}
+
+constexpr unsigned PA_POLL_NS = 20000;   // the longest the hardware may hold a warp at a poll
+constexpr unsigned PA_POLLS = 1u << 20;  // polls before a wait gives up (seconds)
+
+// One poll of a barrier's phase; the hardware may hold the warp for up to PA_POLL_NS, issuing nothing meanwhile (polls
+// that return at once took about half of the SM's issue slots).
+__device__ __forceinline__ bool try_wait(uint64_t* bar, unsigned parity) {
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok)
+                 : "r"(smem_addr(bar)), "r"(parity), "r"(PA_POLL_NS)
+                 : "memory");
+    return ok != 0;
+}
+
 cudaError_t launch_paged_rows(const PagedParams& p, int hd, int words, int tiles, cudaStream_t st);
+int paged_rows_ctas(int tiles);   // the launch's CTAs
 size_t paged_rows_slot(int hd);   // bytes of one partial result
 cudaError_t launch_paged_tiles(const PagedParams& p, int hd, int words, cudaStream_t st);
 size_t paged_tiles_slot(int hd);

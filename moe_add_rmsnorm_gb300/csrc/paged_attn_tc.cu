@@ -19,11 +19,9 @@
 //  - warp 16 issues the products, warp 17 copies the words of 64 positions at a time from the pages (tensor copies of 16
 //    rows, zeros for pages out of range), warp 19 deals out the items and prepares the scales.
 // Registers are moved to the warps that hold the output sums (80, 80, 184, 80 and 56 a thread).
-#include <cuda.h>
 #include <cuda_fp16.h>
 
 #include "paged_attn.cuh"
-#include "stream.cuh"
 #include "tcgen05.cuh"
 
 namespace q8 {
@@ -35,8 +33,6 @@ constexpr int PT_THREADS = 640;
 constexpr int PT_HALF = 64;                // positions a copied stage
 constexpr int PT_ITEMS = 4;                // items dealt out ahead
 constexpr int PT_READERS = 18;             // warps that read an item
-constexpr unsigned PT_POLL_NS = 20000;     // the longest the hardware may hold a warp at a poll
-constexpr unsigned PT_POLLS = 1u << 20;    // polls before a wait gives up (seconds)
 constexpr int PT_PEXP = 14;                // weights are split as values of up to 2^(PT_PEXP + 1)
 
 // One item's piece as the roles read it.
@@ -75,21 +71,10 @@ struct PtShared {
     int last;
 };
 
-// One poll of a barrier's phase; the hardware may hold the warp for up to PT_POLL_NS, issuing nothing meanwhile (polls
-// that return at once took about half of the SM's issue slots).
-__device__ __forceinline__ bool try_wait(uint64_t* bar, unsigned parity) {
-    uint32_t ok;
-    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(ok)
-                 : "r"(smem_addr(bar)), "r"(parity), "r"(PT_POLL_NS)
-                 : "memory");
-    return ok != 0;
-}
-
 // Waits for a phase, whatever the other roles do.
 __device__ __forceinline__ void drain(uint64_t* bar, unsigned parity) {
 #pragma unroll 1
-    for (unsigned i = 0; i < PT_POLLS && !try_wait(bar, parity); ++i) {}
+    for (unsigned i = 0; i < PA_POLLS && !try_wait(bar, parity); ++i) {}
 }
 
 __device__ __forceinline__ uint64_t pk2(float a, float b) {
@@ -207,14 +192,6 @@ __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sy
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// A tensor copy of one page's 16 rows from `row` of its [heads * page_size] rows into shared memory (zeros for a page out
-// of range), counted on bar's transaction bytes.
-__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int row, int page, uint64_t* bar) {
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-                 ::"r"(smem_addr(dst)), "l"(map), "r"(0), "r"(row), "r"(page), "r"(smem_addr(bar))
-                 : "memory");
-}
 
 // sum_{i<n} floor((a i + b) / m) for a < 2^8, n <= 2^24, b < 2^31 and m = 128 (Euclid's steps on (a, m); what is divided stays
 // within 32 bits).
@@ -348,7 +325,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
     auto wait = [&](uint64_t* bar, unsigned parity) -> bool {
         bool got = try_wait(bar, parity & 1u);
 #pragma unroll 1
-        for (unsigned i = 0; !got && i < PT_POLLS && !*(volatile int*)&sh.dead; ++i) got = try_wait(bar, parity & 1u);
+        for (unsigned i = 0; !got && i < PA_POLLS && !*(volatile int*)&sh.dead; ++i) got = try_wait(bar, parity & 1u);
         if (__builtin_expect(__all_sync(0xffffffffu, got), 1)) return true;
         *(volatile int*)&sh.dead = 1;
         kv_flag(kv, Q8_KV_ERR_WAIT);
@@ -1019,8 +996,22 @@ EncodeTiled encode_tiled() {
     return fn;
 }
 
-// Words [pages][kv * page_size][hd], read 16 rows of a page at a time.
-bool words_map(CUtensorMap* m, const void* words, const KvView& v, int hd) {
+template <int HD, int WORDS>
+cudaError_t tiles_launch(const PagedParams& p, cudaStream_t st) {
+    auto kernel = paged_tiles_kernel<HD, WORDS>;
+    constexpr size_t smem = sizeof(PtShared<HD>) + 1024;
+    static_assert(smem + 1024 <= 232448, "dynamic plus static shared memory within the 227 KB a CTA may hold");
+    CUtensorMap mk, mv;
+    if (!paged_words_map(&mk, p.view.k, p.view, HD) || !paged_words_map(&mv, p.view.v, p.view, HD)) return cudaErrorNotSupported;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<device_info().sms, PT_THREADS, smem, st>>>(p, mk, mv);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool paged_words_map(CUtensorMap* m, const void* words, const KvView& v, int hd) {
     const EncodeTiled enc = encode_tiled();
     if (!enc) return false;
     const cuuint64_t rows = (cuuint64_t)v.kv << v.page_log2;
@@ -1031,21 +1022,6 @@ bool words_map(CUtensorMap* m, const void* words, const KvView& v, int hd) {
                CU_TENSOR_MAP_INTERLEAVE_NONE, hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-template <int HD, int WORDS>
-cudaError_t tiles_launch(const PagedParams& p, cudaStream_t st) {
-    auto kernel = paged_tiles_kernel<HD, WORDS>;
-    constexpr size_t smem = sizeof(PtShared<HD>) + 1024;
-    static_assert(smem + 1024 <= 232448, "dynamic plus static shared memory within the 227 KB a CTA may hold");
-    CUtensorMap mk, mv;
-    if (!words_map(&mk, p.view.k, p.view, HD) || !words_map(&mv, p.view.v, p.view, HD)) return cudaErrorNotSupported;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    kernel<<<device_info().sms, PT_THREADS, smem, st>>>(p, mk, mv);
-    return cudaGetLastError();
-}
-
-}  // namespace
 
 size_t paged_tiles_slot(int hd) { return (size_t)PT_M * (hd + 2) * sizeof(float); }
 

@@ -332,6 +332,11 @@ ATTEND = [
     ([33], [333], 48, 1, 64, 1024, "e4m3"),
     ([1], [700], 64, 1, 128, 16, "int8"),
     ([2], [100], 23, 1, 128, 16, "int8"),
+    ([1], [3000], 16, 1, 128, 16, "int8"),
+    ([1, 1, 1], [33, 2500, 700], 24, 2, 64, 32, "e4m3"),
+    ([1] * 30, [100 + 61 * i for i in range(30)], 22, 2, 128, 16, "e4m3"),
+    ([1, 300, 1], [900, 400, 77], 12, 1, 128, 16, "int8"),
+    ([2, 2, 1, 40], [700, 2, 1300, 40], 8, 1, 128, 64, "int8"),
 ]
 
 
