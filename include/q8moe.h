@@ -368,7 +368,7 @@ typedef struct {
 #define Q8_KV_ERR_LENGTH 1  /* rows outside the call's, or a kv_len below the sequence's rows or past the table's end */
 #define Q8_KV_ERR_PAGE 2    /* a page id outside [0, pages) */
 #define Q8_KV_ERR_ROPE 4    /* a position past the rotation tables */
-#define Q8_KV_ERR_WAIT 8    /* a bounded device-side wait gave up (the call's outputs are incomplete) */
+#define Q8_KV_ERR_WAIT 8    /* a bounded device-side wait gave up (the call's outputs are incomplete, and its workspace is done with) */
 
 /* A batch of sequences over pages, all of it device memory that is read when the call runs (a captured graph replays with
  * what the arrays hold then).  Sequence b owns the activation rows row_start[b] .. row_start[b+1]-1 (row_start does not
@@ -377,7 +377,8 @@ typedef struct {
  * row_start[b]) + i.  Position p lives in page table[b*table_stride + p/page_size], slot p % page_size.
  * What the host cannot check is checked on the device, and recorded in *error (or-ed into it) when error is not NULL:
  *   - a sequence whose rows are not within the call's, or whose kv_len is out of range, is skipped by q8_kv_append and
- *     q8_kv_read; q8_paged_attention skips the former and gives the latter's rows zeros (and an lse of -infinity);
+ *     q8_kv_read, as is a row that a decreasing row_start leads to no sequence of its own; q8_paged_attention skips the
+ *     first and gives the second's rows zeros (and an lse of -infinity);
  *   - nothing is written to, or read from, a page id out of range: q8_kv_append drops the row's keys and values (its
  *     queries are written), q8_kv_read leaves the row as it was, q8_paged_attention leaves the page's positions out. */
 typedef struct {

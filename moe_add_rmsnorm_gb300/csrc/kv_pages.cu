@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams pk) {
     const int b = kv_find_seq(kv, r);
     if (b < 0) return;
     const KvSeq s = kv_seq(kv, b);
-    if (!s.rows_ok || !s.len_ok) {
+    if (!s.holds(r)) {
         if (lane == 0) kv_flag(kv, Q8_KV_ERR_LENGTH);
         return;
     }
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const ReadParams pk) {
             if (b >= 0) s = kv_seq(kv, b);
         }
         if (b < 0 || r >= kv.rows) continue;
-        if (!s.rows_ok || !s.len_ok) {
+        if (!s.holds(r)) {
             if (lane == 0) kv_flag(kv, Q8_KV_ERR_LENGTH);
             continue;
         }

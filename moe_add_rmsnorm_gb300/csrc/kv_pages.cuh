@@ -15,6 +15,8 @@ struct KvSeq {
     int64_t first = 0, n = 0;
     int len = 0;
     bool rows_ok = false, len_ok = false;
+    // Whether row r is the sequence's and has a position (a row_start that decreases leads rows to sequences not theirs).
+    __device__ bool holds(int64_t r) const { return rows_ok && len_ok && r >= first && r < first + n; }
 };
 
 __device__ __forceinline__ KvSeq kv_seq(const KvView& p, int b) {

@@ -487,6 +487,38 @@ def test_bad_pages_and_lengths_are_left_out(q8, ws, new, length):
     assert (q_out[new[0] - 1] == 7.5).all() and (q_out[new[0]:] != 7.5).any() and c.error.item() == q8.KV_ERR_ROPE
 
 
+@pytest.mark.parametrize("starts", [[7, 0, 1, 9], [0, 9, 3, 9], [5, 5, 0, 9], [-4, 0, -9, 2 ** 31 - 1]])
+def test_decreasing_row_starts(q8, ws, starts):
+    """Rows that no sequence owns are left as they were, whatever a search among the starts lands on; nothing is read or
+    written past a table's row or outside the sequences' pages."""
+    import torch
+    rows, page = 9, 16
+    c = Cache(q8, [3, 3, 3], [48, 48, 48], 2, 128, page, "int8", 31)
+    c.row_start.copy_(torch.tensor(starts, dtype=torch.int64).to(torch.int32))
+    table = c.table[:, :3].contiguous()  # (positions 48 on are past its row: another sequence's pages, or the end)
+    owned = torch.zeros(rows, dtype=torch.bool)
+    slots = torch.zeros(c.kw.shape[0], page, dtype=torch.bool, device="cuda")
+    for b in range(3):
+        first, n = starts[b], starts[b + 1] - starts[b]
+        if first >= 0 and 0 <= n <= 48 and first + n <= rows:
+            owned[first:first + n] = True
+            for p in range(48 - n, 48):
+                slots[table[b, p // page].long(), p % page] = True
+    batch = q8.kv_batch(c.row_start, c.kv_len, table, c.error)
+    back = torch.full((rows, 2, 128), 7.5, device="cuda")
+    q8.q8_kv_read(c.pages(), batch, back)
+    assert (back[~owned.cuda()] == 7.5).all() and c.error.item() == q8.KV_ERR_LENGTH
+    before = c.kw.clone()
+    x = torch.randn(rows, 2, 128, generator=gen(32), device="cuda")
+    q_out = torch.full_like(x, 7.5)
+    q8.q8_kv_append(c.pages(), batch, x, x, x, q_out)
+    assert (q_out[~owned.cuda()] == 7.5).all()
+    assert torch.equal(c.kw.transpose(1, 2)[~slots], before.transpose(1, 2)[~slots])
+    out = torch.full((rows, 4, 128), 7.5, device="cuda")
+    q8.q8_paged_attention(c.pages(), batch, torch.randn(rows, 4, 128, generator=gen(33), device="cuda"), out, ws=ws)
+    assert (out[~owned.cuda()] == 7.5).all()
+
+
 def test_addresses_past_32_bits(q8, ws):
     """Words behind 2^32 bytes and scales behind 2^27 values."""
     import torch
