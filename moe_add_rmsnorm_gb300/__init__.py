@@ -54,11 +54,13 @@ KV_ERR_LENGTH, KV_ERR_PAGE, KV_ERR_ROPE, KV_ERR_WAIT = 1, 2, 4, 8  # bits of a b
 
 
 class q8_kv_pages(ctypes.Structure):
+    device = None  # the tensors' (kv_pages sets it; None: the caller's business)
     _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "ks", "vs")] + [
         (n, ctypes.c_int64) for n in ("pages", "page_size", "kv_heads", "head_dim")] + [("words", ctypes.c_int)]
 
 
 class q8_kv_batch(ctypes.Structure):
+    device = None
     _fields_ = [(n, ctypes.c_void_p) for n in ("row_start", "kv_len", "table")] + [
         (n, ctypes.c_int64) for n in ("seqs", "table_pages", "table_stride")] + [("error", ctypes.c_void_p)]
 
@@ -374,8 +376,10 @@ def kv_pages(k, ks, v, vs) -> q8_kv_pages:
     d = _device(k, "k")
     if v.get_device() != d or ks.get_device() != d or vs.get_device() != d:
         _refuse("pages: not all on the current device")
-    return q8_kv_pages(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape[0], shape[2], shape[1], shape[3],
-                       words)
+    p = q8_kv_pages(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape[0], shape[2], shape[1], shape[3],
+                    words)
+    p.device = d
+    return p
 
 
 def kv_batch(row_start, kv_len, table, error=None) -> q8_kv_batch:
@@ -401,8 +405,18 @@ def kv_batch(row_start, kv_len, table, error=None) -> q8_kv_batch:
         if error.dtype is not i32 or error.numel() != 1 or error.get_device() != d:
             _refuse("error: not one int32 value on the current device")
         e = error.data_ptr()
-    return q8_kv_batch(row_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), seqs, pages,
-                       strides[0] if seqs > 1 else pages, e)
+    b = q8_kv_batch(row_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), seqs, pages,
+                    strides[0] if seqs > 1 else pages, e)
+    b.device = d
+    return b
+
+
+def _paged_device(pages, batch, t, name):
+    """The device of a call's tensor t, which has to be the current one, the pages' and the batch's."""
+    d = _device(t, name)
+    if (pages.device not in (d, None)) or (batch.device not in (d, None)):
+        _refuse("pages, batch: not on the current device")
+    return d
 
 
 def q8_rope_table(theta, cos, sin, stream=None):
@@ -417,7 +431,7 @@ def q8_kv_append(pages, batch, q, k, v, q_out, q_norm=None, k_norm=None, eps=1e-
     """Norms and rotates the rows' query and key heads (q [rows, heads, hd] into q_out; k, v [rows, kv_heads, hd]) and
     quantizes the keys and values into their page slots.  q and q_out may be None (keys and values only)."""
     kv, hd = pages.kv_heads, pages.head_dim
-    rows, d = k.shape[0], _device(k, "k")
+    rows, d = k.shape[0], _paged_device(pages, batch, k, "k")
     if v.shape[0] != rows or (q is None) != (q_out is None):
         _refuse("q, k, v, q_out: rows differ")
     heads, qa, qs, oa, os_ = 0, None, 0, None, 0
@@ -442,7 +456,7 @@ def q8_kv_read(pages, batch, k_out=None, v_out=None, stream=None):
     one = k_out if k_out is not None else v_out
     if one is None:
         _refuse("k_out and v_out: both None")
-    d, shape, strides, f32 = _device(one, "k_out, v_out"), one.shape, one.stride(), _torch.float32
+    d, shape, strides, f32 = _paged_device(pages, batch, one, "k_out, v_out"), one.shape, one.stride(), _torch.float32
     if len(shape) != 3 or shape[1] != kv or shape[2] != hd or strides[2] != 1 or one.dtype is not f32:
         _refuse(f"k_out, v_out: not f32 [rows, {kv}, {hd}] with consecutive values")
     if one is k_out and v_out is not None:
@@ -457,7 +471,7 @@ def q8_kv_read(pages, batch, k_out=None, v_out=None, stream=None):
 def q8_paged_attention(pages, batch, q, out, scale=None, lse=None, ws=None, stream=None):
     """Causal attention of the rows q [rows, heads, hd] over their sequences' cached positions, into out; scale defaults
     to hd^-1/2, lse (optional) is f32 [rows, heads]."""
-    hd, d = pages.head_dim, _device(q, "q")
+    hd, d = pages.head_dim, _paged_device(pages, batch, q, "q")
     rows, heads = q.shape[0], q.shape[1]
     qa, qs = _rows(q, heads, hd, d, "q")
     oa, os_ = _rows(out, heads, hd, d, "out")

@@ -519,6 +519,19 @@ def test_decreasing_row_starts(q8, ws, starts):
     assert (out[~owned.cuda()] == 7.5).all()
 
 
+def test_pages_and_batches_of_another_device_are_refused(q8, ws):
+    import torch
+    c = Cache(q8, [1], [5], 1, 64, 16, "int8", 34)
+    x = torch.ones(1, 1, 64, device="cuda")
+    for which in range(2):
+        both = [c.pages(), c.batch()]
+        both[which].device += 1
+        for call in (lambda: q8.q8_kv_append(*both, x, x, x, x), lambda: q8.q8_kv_read(*both, x),
+                     lambda: q8.q8_paged_attention(*both, x, torch.empty_like(x), ws=ws)):
+            with pytest.raises(q8.Q8Error, match="current device"):
+                call()
+
+
 def test_addresses_past_32_bits(q8, ws):
     """Words behind 2^32 bytes and scales behind 2^27 values."""
     import torch
