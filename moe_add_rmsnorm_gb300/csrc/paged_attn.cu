@@ -116,6 +116,7 @@ struct RowsShared {
     // What the walk over the items keeps between them (in shared memory: the registers are the inner loop's).
     int64_t cur, lo, hi, seq_at, item_at, units, total;
     int seq, ctas, last;
+    unsigned polls;                    // a wait's limit
 };
 
 template <int HD, int WORDS, int NT>
@@ -145,6 +146,7 @@ __global__ void __launch_bounds__(PR_THREADS, RowsShared<HD, NT>::CTAS)
             sh.seq = run.seq, sh.seq_at = run.seq_at;
             sh.total = run.total, sh.ctas = run.ctas;
             for (int i = 0; i < 2 * PR_WARPS; ++i) mbar_init(&sh.full[0][i], 1);
+            sh.polls = PA_POLLS;
             fence_barrier_init();
         }
     }
@@ -290,8 +292,11 @@ __global__ void __launch_bounds__(PR_THREADS, RowsShared<HD, NT>::CTAS)
             if (i + 1 < mine) load_scales(i + 1, page_after);
             bool got = try_wait(&sh.full[wid][stage], ((used + i) >> 1) & 1);
 #pragma unroll 1
-            for (unsigned poll = 0; !got && poll < PA_POLLS; ++poll) got = try_wait(&sh.full[wid][stage], ((used + i) >> 1) & 1);
-            if (!got) kv_flag(kv, Q8_KV_ERR_WAIT);
+            for (unsigned poll = 0; !got && poll < *(volatile unsigned*)&sh.polls; ++poll) got = try_wait(&sh.full[wid][stage], ((used + i) >> 1) & 1);
+            if (!got) {  // (the CTA's later waits are short)
+                *(volatile unsigned*)&sh.polls = 64;
+                kv_flag(kv, Q8_KV_ERR_WAIT);
+            }
             Bytes<KB> kw[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {

@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
 #pragma unroll 1
         for (int it = 0; ok && next_item(it, d); ++it) {
             const bool valid = m < d.tokens * G;
-            const int lim = !valid ? INT_MAX : d.end ? d.pos + m / G : -1;
+            const int lim = !valid ? INT_MAX - 1 : d.end ? d.pos + m / G : -1;
             const bool active = 32 * quarter < d.tokens * G;  // (uniform in the quarter's warps)
             float mr = -INFINITY, l = 0.f, qf = 0.f;           // the maximum that l's terms are relative to
             const int tiles = d.t1 - d.t0;
@@ -597,12 +597,14 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                 for (int c = 0; c < HD / 32; ++c) {
                     uint32_t r[32];
                     tc_load<32>(o_at + 32 * c, r);
-                    if (!valid) continue;
+                    if (valid) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        __stcg(reinterpret_cast<float4*>(dst + (8 * c + i) * step),
-                               make_float4(__uint_as_float(r[4 * i]) * inv, __uint_as_float(r[4 * i + 1]) * inv,
-                                           __uint_as_float(r[4 * i + 2]) * inv, __uint_as_float(r[4 * i + 3]) * inv));
+                        for (int i = 0; i < 8; ++i)
+                            __stcg(reinterpret_cast<float4*>(dst + (8 * c + i) * step),
+                                   make_float4(__uint_as_float(r[4 * i]) * inv, __uint_as_float(r[4 * i + 1]) * inv,
+                                               __uint_as_float(r[4 * i + 2]) * inv, __uint_as_float(r[4 * i + 3]) * inv));
+                    }
+                    __syncwarp();  // (the next load is the whole warp's)
                 }
             }
             tc_fence_before();
@@ -743,31 +745,31 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
             for (int x = 0; x <= tiles; ++x) {
                 const int tx = tau + x, b = tx & 1;
                 if (x < tiles) {
-                // keys: rows as they are; a lane 16 dimensions (one 16-byte chunk of words) of a position
-                if (!(ok = wait(&sh.k_empty, tx + 1))) break;
+                    // keys: rows as they are; a lane 16 dimensions (one 16-byte chunk of words) of a position
+                    if (!(ok = wait(&sh.k_empty, tx + 1))) break;
 #pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    if (!(ok = wait(&sh.raw_full[half], tx))) break;
-                    const unsigned char* src = sh.raw[half];
+                    for (int half = 0; half < 2; ++half) {
+                        if (!(ok = wait(&sh.raw_full[half], tx))) break;
+                        const unsigned char* src = sh.raw[half];
 #pragma unroll
-                    for (int i = 0; i < HD / 32; ++i) {  // (HD / 16 chunks) x 8 groups of 8 rows, 4 warps x 4 chunks at a time
-                        const int task = i * 4 + w;
-                        const int c = (lane >> 3) + 4 * (task & (HD / 64 - 1)), p = 8 * (task / (HD / 64)) + (lane & 7);
-                        const uint4 u = *reinterpret_cast<const uint4*>(src + raw_off<HD>(p, c));
-                        const uint32_t in[4] = {words_flip<WORDS>(u.x), words_flip<WORDS>(u.y), words_flip<WORDS>(u.z), words_flip<WORDS>(u.w)};
-                        uint32_t h[8];
+                        for (int i = 0; i < HD / 32; ++i) {  // (HD / 16 chunks) x 8 groups of 8 rows, 4 warps x 4 chunks at a time
+                            const int task = i * 4 + w;
+                            const int c = (lane >> 3) + 4 * (task & (HD / 64 - 1)), p = 8 * (task / (HD / 64)) + (lane & 7);
+                            const uint4 u = *reinterpret_cast<const uint4*>(src + raw_off<HD>(p, c));
+                            const uint32_t in[4] = {words_flip<WORDS>(u.x), words_flip<WORDS>(u.y), words_flip<WORDS>(u.z), words_flip<WORDS>(u.w)};
+                            uint32_t h[8];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) h[2 * j] = words2_f16<WORDS, 0>(in[j]), h[2 * j + 1] = words2_f16<WORDS, 1>(in[j]);
-                        const int pp = PT_HALF * half + p;
-                        unsigned char* dst = sh.k + (uint32_t)(pp >> 3) * SBO_Q + (uint32_t)c * 256 + (uint32_t)(pp & 7) * 16;
-                        *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
-                        *reinterpret_cast<uint4*>(dst + 128) = make_uint4(h[4], h[5], h[6], h[7]);
+                            for (int j = 0; j < 4; ++j) h[2 * j] = words2_f16<WORDS, 0>(in[j]), h[2 * j + 1] = words2_f16<WORDS, 1>(in[j]);
+                            const int pp = PT_HALF * half + p;
+                            unsigned char* dst = sh.k + (uint32_t)(pp >> 3) * SBO_Q + (uint32_t)c * 256 + (uint32_t)(pp & 7) * 16;
+                            *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+                            *reinterpret_cast<uint4*>(dst + 128) = make_uint4(h[4], h[5], h[6], h[7]);
+                        }
+                        arrive(&sh.raw_empty[half]);
                     }
-                    arrive(&sh.raw_empty[half]);
-                }
-                if (!ok) break;
-                fence_async();
-                arrive(&sh.k_full);
+                    if (!ok) break;
+                    fence_async();
+                    arrive(&sh.k_full);
                 }
                 if (x == 0) continue;
                 if (!(ok = wait(&sh.v_empty[b ^ 1], ((tx - 1) >> 1) + 1) &&
@@ -879,6 +881,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
             for (int part = 0; part < 4; ++part) {  // no copy is in flight when the CTA leaves
                 const unsigned n = part < 2 ? keys : values;
                 if (n) drain(&sh.raw_full[part], (n - 1) & 1);
+                // (a wait gave up: there may be one copy more, or none; a millisecond is many times a copy's latency)
+#pragma unroll 1
+                for (int i = 0; sh.dead && i < 64 && !try_wait(&sh.raw_full[part], n & 1); ++i) {}
             }
         } else if (wid == 19) {
             // ================ items and scales
