@@ -613,7 +613,12 @@ cudaError_t rows_launch_nt(const PagedParams& p, int tiles, cudaStream_t st) {
     return tiles == 1 ? rows_launch<HD, WORDS, 1>(p, st) : rows_launch<HD, WORDS, 2>(p, st);
 }
 
-constexpr int kRowsMost = 16;  // query vectors a key/value head that this kernel's item holds
+constexpr int kRowsItem = 16;  // query vectors an item holds at most
+// Query vectors a key/value head up to which a sequence is this kernel's (two to four items of it, each reading the
+// positions).  Measured, this kernel and the tiles': 16 vectors of 64 sequences of 4096 113 and 194 us, of one of 100003 50
+// and 110; 32 vectors 206 and 200 us, 80 and 129, of 64 sequences of 500 51 and 63, of 33 of 9000 with heads of 64 228 and
+// 275; 64 vectors 392 and 214 us, 147 and 182.
+constexpr int kRowsMost = 32;
 
 }  // namespace
 
@@ -623,7 +628,7 @@ int paged_rows_ctas(int tiles) {
     return tiles == 1 ? RowsShared<64, 1>::CTAS * sms : RowsShared<64, 2>::CTAS * sms;
 }
 
-size_t paged_rows_slot(int hd) { return (size_t)kRowsMost * (hd + 2) * sizeof(float); }
+size_t paged_rows_slot(int hd) { return (size_t)kRowsItem * (hd + 2) * sizeof(float); }
 
 cudaError_t launch_paged_rows(const PagedParams& p, int hd, int words, int tiles, cudaStream_t st) {
     if (hd == 128)
@@ -648,19 +653,22 @@ cudaError_t launch_paged_attention(const PagedAttnCall& c, Carve& ws, cudaStream
     const bool rows = p.group <= kRowsMost && (c.view.seqs > 1 || most <= kRowsMost);
     const bool tiles = most > kRowsMost;
     const int sms = device_info().sms;
+    // 8-vector tiles an item: two where one row has more vectors than one holds.  (One row of 8 vectors, 64 sequences of
+    // 4096: 62 us with one and 96 with two; two rows, 16 vectors: 113 and 104.)
+    const int nt = p.group <= 8 ? 1 : 2;
     PagedParams t = p;
     auto scratch = [&](PagedParams& x, int ctas, size_t slot) {
         x.part = ws.take<float>(2 * (size_t)ctas * slot / sizeof(float));
         x.counters = ws.take_counters(ctas);
     };
-    if (rows) scratch(p, paged_rows_ctas(p.group <= 8 ? 1 : 2), paged_rows_slot(c.hd));
+    if (rows) scratch(p, paged_rows_ctas(nt), paged_rows_slot(c.hd));
     if (tiles) scratch(t, sms, paged_tiles_slot(c.hd));
     if (ws.overflow) return cudaSuccess;  // refused by the caller; nothing is launched
     p.upto = tiles ? kRowsMost : INT64_MAX;
     t.above = rows ? kRowsMost : 0;
     t.upto = INT64_MAX;
     cudaError_t e = cudaSuccess;
-    if (rows) e = launch_paged_rows(p, c.hd, c.words, p.group <= 8 ? 1 : 2, st);
+    if (rows) e = launch_paged_rows(p, c.hd, c.words, nt, st);
     if (tiles && e == cudaSuccess) e = launch_paged_tiles(t, c.hd, c.words, st);
     return e;
 }
