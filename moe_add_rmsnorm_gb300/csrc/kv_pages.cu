@@ -4,11 +4,13 @@
 // What it computes: qwen_emit docs, emit_qwen30b_generate (per-head QK-norm, then RoPE on pairs (i, i + head_dim/2), then
 // the key/value append), for ragged batches over pages of 8-bit words (q8moe.h, q8_kv_pages).
 //
-// How: both are streams, bound by the bytes of the f32 rows (a row of 32 + 4 + 4 heads of 128 is 20 KiB in and 16 KiB of
+// How: both are streams, with floors set by the bytes of the f32 rows (a row of 32 + 4 + 4 heads of 128 is 20 KiB in and 16 KiB of
 // queries and 1 KiB of words out).  A warp takes one row's group of head vectors; LPV lanes hold a vector, each lane two
 // float4 (dims 4l.. of either half), so both elements of every rotation pair sit in one lane and the row's sums are
 // shuffles among LPV lanes.  All of a warp's loads are issued before the row's sequence and page are looked up (a chain
-// of three dependent loads), which hides that chain behind them.
+// of three dependent loads), which hides that chain behind them.  Measured: 2318 rows of 24 + 8 + 8 heads of 128 in 23.9 us
+// (3.4 TB/s; the exact keys and the words' rounding issue more than the bytes cost), 34182 rows of 8 heads of 64 read back
+// in 32.7 us (5.4 TB/s, the memory's: a copy runs at 6.8).
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -18,7 +20,8 @@ namespace q8 {
 
 namespace {
 
-constexpr int KV_ITERS = 4;  // vectors a lane group holds: 8 float4 loads in flight a lane
+constexpr int KV_ITERS = 4;  // vectors a lane group of the writing kernel holds: 8 float4 loads in flight a lane
+constexpr int KV_READ = 2;   // and of the reading one
 
 struct AppendParams {
     KvView view;
@@ -98,7 +101,7 @@ __device__ __forceinline__ float f2_turn(float a, float wa, float ca, float b, f
 }
 
 template <int HD, int WORDS>
-__global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams pk) {
+__global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendParams pk) {
     constexpr int LPV = HD / 8, VPW = 32 / LPV, HALF = HD / 2;
     const KvView& kv = pk.view;
     const int lane = threadIdx.x & 31, sub = lane / LPV, l = lane % LPV;
@@ -106,8 +109,8 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams pk) {
     const int64_t r = warp / pk.groups;
     if (r >= kv.rows) return;
     // A row's warps take its vectors in turn, so that each has its share of the keys and values, whose words cost several
-    // times a query's work (a warp of keys alone held its CTA: with the rounding above, 2318 rows
-    // of 24 + 8 + 8 heads went from 35.8 to 25.0 us).
+    // times a query's work (a warp of keys alone held its CTA: with the rounding above, 2318 rows of 24 + 8 + 8 heads went from
+    // 35.8 to 25.0 us; four CTAs an SM, by 64 registers for 76, to 23.9).
     const int v0 = (int)(warp % pk.groups) * VPW + sub, step = pk.groups * VPW, nvec = pk.heads + 2 * kv.kv;
     float x[KV_ITERS][8];
 #pragma unroll
@@ -226,99 +229,79 @@ __device__ __forceinline__ void store8(float* p, const float (&y)[8]) {
                  : "memory");
 }
 
-// LPV lanes a vector, a lane 8 words (8 bytes in, 32 bytes out).  A warp takes ROWS consecutive rows' group of vectors:
-// where there are rows enough to fill the GPU, four, whose lookups and loads are then in flight together.
-template <int HD, int WORDS, int ROWS>
+// LPV lanes a vector, a lane 8 words (8 bytes in, 32 bytes out), a warp a group of one row's vectors, all of its loads in
+// flight together.  Many warps hide the chain sequence, page, words best: 38912 rows of 4 heads of 128 take 36.4 us in int8
+// words and 33.4 in e4m3 (4096 rows 5.5 and 5.4) with two vectors a lane group, 39.7 and 33.0 (5.7 and 5.5) with four, and
+// 54 and 35 (10.2 and 6.5) with four rows a warp.
+template <int HD, int WORDS>
 __global__ void __launch_bounds__(256) kv_read_kernel(const ReadParams pk) {
     constexpr int LPV = HD / 8, VPW = 32 / LPV;
     const KvView& kv = pk.view;
     const int lane = threadIdx.x & 31, sub = lane / LPV, l = lane % LPV;
     const int64_t warp = (int64_t)blockIdx.x * Q8_WARPS + (threadIdx.x >> 5);
-    const int64_t r0 = warp / pk.groups * ROWS;
-    if (r0 >= kv.rows) return;
-    const int v0 = (int)(warp % pk.groups) * (KV_ITERS * VPW) + sub;
-    int b = kv_find_seq(kv, r0);
-    KvSeq s;
-    if (b >= 0) s = kv_seq(kv, b);
-    int pos[ROWS], page[ROWS];
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-        const int64_t r = r0 + i;
-        pos[i] = page[i] = -1;
-        if (i > 0 && (b < 0 || r >= s.first + s.n) && r < kv.rows) {  // (warp-uniform) another sequence's row
-            b = kv_find_seq(kv, r);
-            if (b >= 0) s = kv_seq(kv, b);
-        }
-        if (b < 0 || r >= kv.rows) continue;
-        if (!s.holds(r)) {
-            if (lane == 0) kv_flag(kv, Q8_KV_ERR_LENGTH);
-            continue;
-        }
-        pos[i] = (int)(s.len - s.n + (r - s.first));
-        page[i] = __ldg(kv.table + b * kv.table_stride + (pos[i] >> kv.page_log2));
+    const int64_t r = warp / pk.groups;
+    if (r >= kv.rows) return;
+    const int v0 = (int)(warp % pk.groups) * (KV_READ * VPW) + sub;
+    const int b = kv_find_seq(kv, r);
+    if (b < 0) return;
+    const KvSeq s = kv_seq(kv, b);
+    if (!s.holds(r)) {
+        if (lane == 0) kv_flag(kv, Q8_KV_ERR_LENGTH);
+        return;
     }
-    bool bad = false;
+    const int pos = (int)(s.len - s.n + (r - s.first));
+    const int page = kv_page(kv, b, pos);
+    if (page < 0) {
+        if (lane == 0) kv_flag(kv, Q8_KV_ERR_PAGE);
+        return;
+    }
+    uint2 w[KV_READ];
+    float d[KV_READ];
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i)
-        if (pos[i] >= 0 && (page[i] < 0 || page[i] >= kv.pages)) bad = true, pos[i] = -1;
-    if (bad && lane == 0) kv_flag(kv, Q8_KV_ERR_PAGE);
-    uint2 w[ROWS][KV_ITERS];
-    float d[ROWS][KV_ITERS];
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i)
-#pragma unroll
-        for (int it = 0; it < KV_ITERS; ++it) {
-            const int vec = v0 + it * VPW;
-            if (vec < 2 * kv.kv && pos[i] >= 0) {
-                const bool key = vec < kv.kv;
-                const int64_t row = kv_row(kv, page[i], key ? vec : vec - kv.kv, pos[i]);
-                w[i][it] = *reinterpret_cast<const uint2*>((key ? kv.k : kv.v) + row * HD + 8 * l);
-                d[i][it] = (key ? kv.ks : kv.vs)[row];
-            }
+    for (int it = 0; it < KV_READ; ++it) {
+        const int vec = v0 + it * VPW;
+        if (vec < 2 * kv.kv) {
+            const bool key = vec < kv.kv;
+            const int64_t row = kv_row(kv, page, key ? vec : vec - kv.kv, pos);
+            w[it] = *reinterpret_cast<const uint2*>((key ? kv.k : kv.v) + row * HD + 8 * l);
+            d[it] = (key ? kv.ks : kv.vs)[row];
         }
+    }
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i)
+    for (int it = 0; it < KV_READ; ++it) {
+        const int vec = v0 + it * VPW;
+        float* out = vec < kv.kv ? pk.k_out : pk.v_out;
+        if (vec >= 2 * kv.kv || !out) continue;
+        float y[8];
 #pragma unroll
-        for (int it = 0; it < KV_ITERS; ++it) {
-            const int vec = v0 + it * VPW;
-            float* out = vec < kv.kv ? pk.k_out : pk.v_out;
-            if (vec >= 2 * kv.kv || !out || pos[i] < 0) continue;
-            float y[8];
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t u = h ? w[it].y : w[it].x;
+            if (WORDS == Q8_KV_INT8) {
+                const uint32_t f = u ^ 0x80808080u;
+                y[4 * h] = i8_to_f32<0>(f), y[4 * h + 1] = i8_to_f32<1>(f);
+                y[4 * h + 2] = i8_to_f32<2>(f), y[4 * h + 3] = i8_to_f32<3>(f);
+            } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t u = h ? w[i][it].y : w[i][it].x;
-                if (WORDS == Q8_KV_INT8) {
-                    const uint32_t f = u ^ 0x80808080u;
-                    y[4 * h] = i8_to_f32<0>(f), y[4 * h + 1] = i8_to_f32<1>(f);
-                    y[4 * h + 2] = i8_to_f32<2>(f), y[4 * h + 3] = i8_to_f32<3>(f);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)(u >> (16 * j)));
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-                        y[4 * h + 2 * j] = f.x, y[4 * h + 2 * j + 1] = f.y;
-                    }
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)(u >> (16 * j)));
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+                    y[4 * h + 2 * j] = f.x, y[4 * h + 2 * j + 1] = f.y;
                 }
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] *= d[i][it];
-            store8(out + (r0 + i) * pk.row_stride + (vec < kv.kv ? vec : vec - kv.kv) * pk.head_stride + 8 * l, y);
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] *= d[it];
+        store8(out + r * pk.row_stride + (vec < kv.kv ? vec : vec - kv.kv) * pk.head_stride + 8 * l, y);
+    }
 }
 
-// Warps a row for `vectors` head vectors of hd values, and the CTAs of `rows` rows.
-int warps_a_row(int vectors, int hd) {
-    const int each = KV_ITERS * (32 / (hd / 8));
+// Warps a row for `vectors` head vectors of hd values, `held` a lane group, and the CTAs of `rows` rows.
+int warps_a_row(int vectors, int hd, int held) {
+    const int each = held * (32 / (hd / 8));
     return (vectors + each - 1) / each;
 }
 
 unsigned ctas(int64_t rows, int groups) { return (unsigned)((rows * groups + Q8_WARPS - 1) / Q8_WARPS); }
-
-template <int HD, int WORDS>
-void read_launch(const ReadParams& p, bool many, cudaStream_t st) {
-    if (many) kv_read_kernel<HD, WORDS, 4><<<ctas((p.view.rows + 3) / 4, p.groups), Q8_THREADS, 0, st>>>(p);
-    else kv_read_kernel<HD, WORDS, 1><<<ctas(p.view.rows, p.groups), Q8_THREADS, 0, st>>>(p);
-}
 
 }  // namespace
 
@@ -326,7 +309,7 @@ cudaError_t launch_kv_append(const KvAppendCall& c, cudaStream_t st) {
     AppendParams p;
     p.view = c.view;
     p.heads = c.heads;
-    p.groups = warps_a_row(c.heads + 2 * c.view.kv, c.hd);
+    p.groups = warps_a_row(c.heads + 2 * c.view.kv, c.hd, KV_ITERS);
     p.q = c.q, p.k = c.k, p.v = c.v;
     p.q_stride = c.q_stride, p.k_stride = c.k_stride, p.v_stride = c.v_stride, p.q_out_stride = c.q_out_stride;
     p.q_norm = c.q_norm, p.k_norm = c.k_norm;
@@ -345,17 +328,14 @@ cudaError_t launch_kv_append(const KvAppendCall& c, cudaStream_t st) {
 cudaError_t launch_kv_read(const KvReadCall& c, cudaStream_t st) {
     ReadParams p;
     p.view = c.view;
-    p.groups = warps_a_row(2 * c.view.kv, c.hd);
+    p.groups = warps_a_row(2 * c.view.kv, c.hd, KV_READ);
     p.k_out = c.k_out, p.v_out = c.v_out;
     p.row_stride = c.row_stride, p.head_stride = c.head_stride;
-    const bool many = (int64_t)c.view.rows * p.groups >= 4 * 32 * (int64_t)device_info().sms;  // (four rows a warp leave 32
-    if (c.hd == 128) {                                                                         // warps an SM)
-        if (c.words == Q8_KV_INT8) read_launch<128, Q8_KV_INT8>(p, many, st);
-        else read_launch<128, Q8_KV_E4M3>(p, many, st);
-    } else {
-        if (c.words == Q8_KV_INT8) read_launch<64, Q8_KV_INT8>(p, many, st);
-        else read_launch<64, Q8_KV_E4M3>(p, many, st);
-    }
+    const unsigned grid = ctas(c.view.rows, p.groups);
+    if (c.hd == 128 && c.words == Q8_KV_INT8) kv_read_kernel<128, Q8_KV_INT8><<<grid, Q8_THREADS, 0, st>>>(p);
+    else if (c.hd == 128) kv_read_kernel<128, Q8_KV_E4M3><<<grid, Q8_THREADS, 0, st>>>(p);
+    else if (c.words == Q8_KV_INT8) kv_read_kernel<64, Q8_KV_INT8><<<grid, Q8_THREADS, 0, st>>>(p);
+    else kv_read_kernel<64, Q8_KV_E4M3><<<grid, Q8_THREADS, 0, st>>>(p);
     return cudaGetLastError();
 }
 
