@@ -38,6 +38,9 @@ namespace {
 
 constexpr int PR_WARPS = 8, PR_THREADS = PR_WARPS * 32;
 constexpr int PR_UNIT = 128;   // positions a unit
+// What an item's start and end cost, in units (64 ragged sequences of up to 4096, one row each: 49.3 us with 0, 47.1 with 1,
+// 45.0 with 2, 45.4 with 4, 50.8 with 8; 33 of up to 8885, 3 rows of heads of 64: 61.4, 59.2, 57.4, 55.2, 56.5).
+constexpr int PR_START = 3;
 constexpr int PR_STEP = 16;    // positions a warp takes at a time
 constexpr int PR_FLUSH = 8;    // steps between additions to the totals
 // Weights times value scales are split as values of up to 65472 (f16 holds 65504): PR_TOP times a scale below 2.
@@ -136,7 +139,7 @@ __global__ void __launch_bounds__(PR_THREADS, RowsShared<HD, NT>::CTAS)
         return s.len_ok ? (s.len + PR_UNIT - 1) / PR_UNIT : 1;
     };
     auto units = [&](const KvSeq& s) -> int64_t {
-        return paged_takes(pk, s) ? kv.kv * tiles_of(s) * span_of(s) : 0;
+        return paged_takes(pk, s) ? kv.kv * tiles_of(s) * (PR_START + span_of(s)) : 0;
     };
     {
         const PagedRun run = paged_run<PR_THREADS>(pk, units);
@@ -175,15 +178,17 @@ __global__ void __launch_bounds__(PR_THREADS, RowsShared<HD, NT>::CTAS)
                 at += n_units;
                 s = kv_seq(kv, ++b);
             }
-            const int64_t U = span_of(s), tiles = tiles_of(s), item = div_small(cur - at, U);
+            const int64_t U = span_of(s), tiles = tiles_of(s), item = div_small(cur - at, PR_START + U);
             h = (int)div_small(item, tiles);
             m0 = (item - h * tiles) * MT;  // the item's first vector
-            const int64_t item_at = at + item * U, u0 = cur - item_at, u1 = min(U, u0 + (hi - cur));
+            const int64_t item_at = at + item * (PR_START + U), first = item_at + PR_START;
+            const int64_t u0 = max(int64_t(0), cur - first), u1 = min(U, hi - first);
+            if (u1 <= u0) break;  // the run ends in the item's start: nothing of it is this CTA's
             begin = (int)(u0 * PR_UNIT);
             end = s.len_ok ? (int)min((int64_t)s.len, u1 * PR_UNIT) : 0;  // positions before which the piece ends
             __syncthreads();  // every thread has read the walk's state
             if (tid == 0) {
-                sh.cur = cur + (u1 - u0);
+                sh.cur = u1 == U ? first + U : hi;
                 sh.seq = b, sh.seq_at = at;
                 sh.item_at = item_at, sh.units = U;
                 sh.last = u0 == 0 && u1 == U ? 1 : 0;  // whether the piece is the whole item
@@ -512,7 +517,7 @@ __global__ void __launch_bounds__(PR_THREADS, RowsShared<HD, NT>::CTAS)
         __syncthreads();
         const bool whole = sh.last != 0;
         const int64_t item_at = sh.item_at;
-        float* slot = pk.part + (int64_t)(2 * blockIdx.x + (item_at + begin / PR_UNIT == sh.lo ? 0 : 1)) * SLOT;
+        float* slot = pk.part + (int64_t)(2 * blockIdx.x + (sh.lo >= item_at ? 0 : 1)) * SLOT;
         auto write_out = [&](int i, int ln, float4 v, const float* m, const float* l) {
             const int n = i / (HD / 16), dim = DPG * (ln >> 2) + 2 * (i % (HD / 16)), c = 8 * n + 2 * (ln & 3);
             const float x0 = l[c] == 0.f ? 0.f : 1.f / l[c], x1 = l[c + 1] == 0.f ? 0.f : 1.f / l[c + 1];
@@ -543,13 +548,13 @@ __global__ void __launch_bounds__(PR_THREADS, RowsShared<HD, NT>::CTAS)
             }
             PagedRun run;
             run.total = sh.total, run.ctas = sh.ctas;
-            const int c0 = run.owner(item_at), c1 = run.owner(item_at + sh.units - 1);
+            const int c0 = run.owner(item_at + PR_START), c1 = run.owner(item_at + PR_START + sh.units - 1);
             __syncthreads();
             if (tid == 0) sh.last = atomic_add_acq_rel_gpu(pk.counters + c0, 1) == c1 - c0;
             __syncthreads();
             if (sh.last) {
                 if (tid == 0) pk.counters[c0] = 0;
-                const bool opens = run.start(c0) == item_at;
+                const bool opens = run.start(c0) >= item_at;
                 auto slot_of = [&](int c) { return pk.part + (int64_t)paged_slot(c, c0, opens) * SLOT; };
                 // every piece's weight for every vector, then the sums with many pieces' loads in flight
                 const int pieces = c1 - c0 + 1;

@@ -41,7 +41,8 @@ __device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) {
 }
 
 // The launch's units in one line, sequence by sequence, cut into equal runs: CTA c takes units c*T/C .. (c+1)*T/C - 1 of
-// T, so ragged batches load every SM alike, whatever the device arrays hold when the launch runs.  C is the launch's
+// T, so ragged batches load every SM alike, whatever the device arrays hold when the launch runs.  An item's first units
+// stand for what its start and end cost and are nobody's work; the others are its tiles of positions.  C is the launch's
 // CTAs, or T when there are fewer units (the other CTAs leave), so every CTA below C has a unit.
 struct PagedRun {
     int64_t total = 0, lo = 0, hi = 0;
@@ -111,8 +112,8 @@ __device__ __forceinline__ PagedRun paged_run(const PagedParams& pk, Units units
     return r;
 }
 
-// The slot of the partial results where CTA c leaves its piece of the item whose first unit is `item_at`: its first when
-// the piece opens its run.  (Only the item's first CTA, c0, may have units before the item's.)
+// The slot of the partial results where CTA c leaves its piece of an item: its first when its run begins in the item.
+// (Only the item's first CTA, c0, may have a run that begins before it.)
 __device__ __forceinline__ int paged_slot(int c, int c0, bool c0_opens) { return 2 * c + (c == c0 && !c0_opens ? 1 : 0); }
 
 // Whether a sequence is one of this launch's.

@@ -19,6 +19,13 @@
 //  - warp 16 issues the products, warp 17 copies the words of 64 positions at a time from the pages (tensor copies of 16
 //    rows, zeros for pages out of range), warp 19 deals out the items and prepares the scales.
 // Registers are moved to the warps that hold the output sums (80, 80, 184, 80 and 56 a thread).
+//
+// What bounds it: 2048 rows over 32768 positions (32 heads over 4 of 128) take 2.06 ms, 516 TFLOP/s of the formula and 1032
+// issued (a library bf16 product: 1932).  The weights' arithmetic takes half of the issue slots and the tensor pipe
+// works 40 to 50% of the time.  An item's start and end (queries into parts, masks, the sums written out or folded) are
+// 18 to 26 us of a CTA's time, most of it instruction fetch of code that runs once an item, so the roles' code is kept in
+// loops; prompts of 483 to 1749 rows (4465 in all) take 342 us.  Queries in tensor memory and a tile's weights in halves
+// by two groups at once took 0.315 ms where this form took 0.295 (512 rows over 16384), and 597 us where it took 368.
 #include <cuda_fp16.h>
 
 #include "paged_attn.cuh"
@@ -33,18 +40,22 @@ constexpr int PT_THREADS = 640;
 constexpr int PT_HALF = 64;                // positions a copied stage
 constexpr int PT_ITEMS = 4;                // items dealt out ahead
 constexpr int PT_READERS = 18;             // warps that read an item
+// What an item's start and end cost, in tiles (12 us or so, mostly instruction fetch): runs that leave it out give a CTA of
+// short items several times the work of one of long ones (4465 rows of 4 prompts 341 us with 0, 260 with 2, 251 with 4, 262
+// with 6, 267 with 8; 24 sequences of 1 to 300 rows 128, 112, 113, 114, 114).
+constexpr int PT_START = 4;
 constexpr int PT_PEXP = 14;                // weights are split as values of up to 2^(PT_PEXP + 1)
 
 // One item's piece as the roles read it.
 struct PtItem {
-    int64_t at, units;     // the item's first unit and its units
+    int64_t units;         // the item's tiles of positions
     int64_t row0;          // activation row of its first token
     int seq, head, tokens; // key/value head; tokens of the tile
     int pos;               // position of the first token
     int end;               // positions before which the sequence ends (0: a length out of range)
     int t0, t1;            // the piece's tiles of positions (t0 == t1: no more items)
-    int opens;             // whether the piece opens the CTA's run
-    int c0, c1, c0_opens;  // the CTAs that share the item, and whether it opens the first one's run
+    int opens;             // whether the CTA's run begins in the item
+    int c0, c1, c0_opens;  // the CTAs that share the item, and whether the first one's run begins in it
 };
 
 template <int HD>
@@ -231,10 +242,10 @@ struct PtTiles {
         const int ends = i + 1 < count ? base + (i + 1) * per : len;
         return (ends + PT_P - 1) / PT_P;
     }
-    __device__ int64_t before(int i) const {  // units of the tiles before i (i < count)
-        return len == 0 ? i : floor_sum(i, per, base + per + PT_P - 1);
+    __device__ int64_t before(int i) const {  // the cost of the tiles before i (i < count)
+        return (int64_t)i * PT_START + (len == 0 ? i : floor_sum(i, per, base + per + PT_P - 1));
     }
-    __device__ int64_t all() const { return before(count - 1) + units(count - 1); }
+    __device__ int64_t all() const { return before(count - 1) + PT_START + units(count - 1); }
 };
 
 __device__ __forceinline__ uint32_t f16_pack(float lo, float hi) {
@@ -896,7 +907,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
             for (; ok; ++it) {
                 PtItem& e = sh.item[it % PT_ITEMS];
                 if (!(ok = wait(&sh.d_empty[it % PT_ITEMS], it / PT_ITEMS + 1))) break;
-                const bool more = cur < run.hi;
+                bool more = cur < run.hi;
                 if (more) {
                     KvSeq s = kv_seq(kv, b);
                     if (!found) {  // the run's first item: the head and the tile of unit run.lo
@@ -915,8 +926,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                         found = true;
                     }
                     const PtTiles t(s, G);
-                    const int64_t U = t.units(i), u0 = cur - b_at;
-                    d.at = b_at;
+                    const int64_t U = t.units(i), first = b_at + PT_START;
                     d.units = U;
                     d.row0 = s.first + (int64_t)i * t.per;
                     d.seq = b;
@@ -924,14 +934,15 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                     d.tokens = min(t.per, t.n - i * t.per);
                     d.pos = t.base + i * t.per;
                     d.end = t.len;
-                    d.t0 = (int)u0;
-                    d.t1 = (int)min(U, u0 + (run.hi - cur));
-                    d.opens = cur == run.lo;
-                    d.c0 = run.owner(d.at), d.c1 = run.owner(d.at + U - 1);
-                    d.c0_opens = run.start(d.c0) == d.at;
-                    cur += d.t1 - d.t0;
+                    d.t0 = (int)max(int64_t(0), cur - first);
+                    d.t1 = (int)min(U, run.hi - first);
+                    d.opens = run.lo >= b_at;
+                    d.c0 = run.owner(first), d.c1 = run.owner(first + U - 1);
+                    d.c0_opens = run.start(d.c0) >= b_at;
+                    more = d.t1 > d.t0;  // (a run may end in an item's start: nothing of it is this CTA's)
+                    cur = run.hi;
                     if (d.t1 == U) {  // on to the next item: the next tile, head or sequence
-                        b_at += U;
+                        cur = b_at = first + U;
                         if (++i == t.count) {
                             i = 0;
                             if (++h == kv.kv) {
@@ -941,9 +952,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                             }
                         }
                     }
-                } else {
-                    d.t0 = d.t1 = 0;
                 }
+                if (!more) d.t0 = d.t1 = 0;
                 if (lane == 0) e = d;
                 arrive(&sh.d_full[it % PT_ITEMS]);
                 if (!more) break;
