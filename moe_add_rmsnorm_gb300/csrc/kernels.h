@@ -320,7 +320,7 @@ cudaError_t launch_pos_add(int32_t* pos, int add, const int* err, cudaStream_t s
 // The scratch and counters of a caller's workspace, for the launches of one call (the C ABI's q8_ws).
 Carve workspace_carve(const q8_ws* ws);
 
-// ---- the paged, quantized key/value cache (kv_pages.cu, paged_attn.cu) --------------------------------------------
+// ---- the paged, quantized key/value cache (kv_pages.cu, paged_attn.cu, paged_attn_tc.cu) --------------------------------------------
 // A batch over pages as the kernels read it (q8_kv_pages and q8_kv_batch, checked).
 struct KvView {
     int8_t* k = nullptr;               // [pages][kv][page][hd] words (8 bits of either type)

@@ -14,7 +14,7 @@
 //  - A warp takes 16 positions at a time from a ring of its own: two stages in shared memory, filled by tensor copies of
 //    a page's 16 rows that are issued as a stage is read out, waited for by that warp alone.  (Loads straight into
 //    registers could be issued only half a step ahead within 128 registers: 64 sequences of up to 4096, 32 heads over 4,
-//    took 52.9 us for 49.2, one of 100003 took 41.0 for 39.2.)  The order of a contraction's index is free, so each
+//    took 8% more, one of 100003 5%.)  The order of a contraction's index is free, so each
 //    lane reads 32 (hd 128) consecutive bytes of a key row as its share of the scores' dimensions, and 16 of four value
 //    rows as its share of the output's; the copies' swizzle keeps those reads apart.
 //  - Scores come out as positions by vectors and go back in as the second product's operand after an 8 x 8 transpose of
@@ -26,8 +26,8 @@
 //    meets in the workspace, folded in order by the last to arrive.
 //
 // What bounds it: instruction issue.  A step is 580 warp instructions on 4224 bytes (over a third turn bytes into pairs of
-// f16, the rest are the products, the softmax and the splits); 64 sequences of 4096 issue 0.55 a clock with the memory at 56% of
-// its rate.
+// f16, the rest are the products, the softmax and the splits); 64 sequences of 4096 (62 us, 4.5 TB/s) issue 0.55 a clock.
+// 64 ragged ones of up to 4096 take 45.0 us (3.4 TB/s), one of 100003 39.2 (2.7 TB/s).
 #include <cuda_fp16.h>
 
 #include "paged_attn.cuh"

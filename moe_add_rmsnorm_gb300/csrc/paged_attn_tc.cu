@@ -20,12 +20,12 @@
 //    rows, zeros for pages out of range), warp 19 deals out the items and prepares the scales.
 // Registers are moved to the warps that hold the output sums (80, 80, 184, 80 and 56 a thread).
 //
-// What bounds it: 2048 rows over 32768 positions (32 heads over 4 of 128) take 2.06 ms, 516 TFLOP/s of the formula and 1032
+// What bounds it: 2048 rows over 32768 positions (32 heads over 4 of 128) take 2.05 ms, 519 TFLOP/s of the formula and 1038
 // issued (a library bf16 product: 1932).  The weights' arithmetic takes half of the issue slots and the tensor pipe
 // works 40 to 50% of the time.  An item's start and end (queries into parts, masks, the sums written out or folded) are
-// 18 to 26 us of a CTA's time, most of it instruction fetch of code that runs once an item, so the roles' code is kept in
-// loops; prompts of 483 to 1749 rows (4465 in all) take 342 us.  Queries in tensor memory and a tile's weights in halves
-// by two groups at once took 0.315 ms where this form took 0.295 (512 rows over 16384), and 597 us where it took 368.
+// 12 us or so of a CTA's time, most of it instruction fetch of code that runs once an item, so the roles' code is kept in
+// loops; prompts of 483 to 1749 rows (4465 in all) take 252 us.  Queries in tensor memory and a tile's weights in halves
+// by two groups at once took 7% more over long caches and 60% more for prompts.
 #include <cuda_fp16.h>
 
 #include "paged_attn.cuh"
