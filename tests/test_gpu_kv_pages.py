@@ -337,6 +337,12 @@ ATTEND = [
     ([1] * 30, [100 + 61 * i for i in range(30)], 22, 2, 128, 16, "e4m3"),
     ([1, 300, 1], [900, 400, 77], 12, 1, 128, 16, "int8"),
     ([2, 2, 1, 40], [700, 2, 1300, 40], 8, 1, 128, 64, "int8"),
+    ([1], [3000], 32, 1, 128, 16, "int8"),
+    ([1, 1], [2000, 9], 30, 1, 64, 1024, "e4m3"),
+    ([2, 3, 4, 5, 1], [900, 500, 64, 3000, 7], 8, 1, 128, 16, "int8"),
+    ([20] + [0] * 19, [900] + [0] * 19, 32, 4, 128, 16, "e4m3"),
+    ([1, 0, 33, 4] * 200, [(i * 53) % 200 + 40 for i in range(800)], 8, 2, 128, 16, "int8"),
+    ([16, 1, 700, 17, 2], [16, 1, 700, 2500, 1100], 8, 1, 64, 16, "e4m3"),
 ]
 
 
@@ -361,7 +367,8 @@ def test_attention(q8, ws, new, length, heads, kv, hd, page, words):
 @pytest.mark.parametrize("new,length,heads,kv,hd,words", [([1] * 40, [300 + 41 * i for i in range(40)], 32, 4, 128, "int8"),
                                                           ([700, 1, 90], [700, 3000, 1500], 24, 8, 128, "int8"),
                                                           ([400, 300], [400, 900], 14, 2, 64, "e4m3"),
-                                                          ([3], [20000], 32, 2, 128, "e4m3")])
+                                                          ([3], [20000], 32, 2, 128, "e4m3"),
+                                                          ([5, 40, 17, 1] * 9, [60 + 31 * i for i in range(36)], 16, 2, 64, "int8")])
 def test_attention_back_to_back(q8, ws, new, length, heads, kv, hd, words):
     """Many launches in a row, on two batches in turn: every one gives the first one's bits (the order in which CTAs meet
     decides nothing, and no launch leaves anything behind for the next)."""
