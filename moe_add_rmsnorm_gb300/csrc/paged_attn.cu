@@ -46,23 +46,6 @@ constexpr int PR_FLUSH = 8;    // steps between additions to the totals
 // Weights times value scales are split as values of up to 65472 (f16 holds 65504): PR_TOP times a scale below 2.
 constexpr float PR_TOP = 32736.f;
 
-// The bytes of w (flipped by 0x80 each for int8) that `SEL` picks, two of them, as two f16 values.
-template <int WORDS, int HALF>
-__device__ __forceinline__ uint32_t words2_f16(uint32_t w) {
-    if (WORDS == Q8_KV_INT8) {
-        // byte + 128 in the low mantissa byte of 1024.0, less 1152: exact
-        const uint32_t u = __byte_perm(w, 0x64646464u, HALF ? 0x4342 : 0x4140);
-        const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return e4m3x2_to_f16x2((uint16_t)(HALF ? w >> 16 : w & 0xffffu));
-}
-
-template <int WORDS>
-__device__ __forceinline__ uint32_t words_flip(uint32_t w) {
-    return WORDS == Q8_KV_INT8 ? w ^ 0x80808080u : w;
-}
-
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -76,25 +59,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return y;
 }
 
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // Two f32 values as two f16 parts each.
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
     hi = pack_f16(a, b);
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
     lo = pack_f16(a - f.x, b - f.y);
-}
-
-__device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }  // e in [-126, 127]
-
-// The unbiased exponent of a non-negative float's bits, at least -100 (so that scalings by its inverse and by 2^14 stay
-// finite); infinities and NaN: 0 (whatever they scale stays not finite).
-__device__ __forceinline__ int exponent_of(unsigned bits) {
-    return bits >= 0x7f800000u ? 0 : max((int)(bits >> 23) - 127, -100);
 }
 
 template <int BYTES>

@@ -2,6 +2,7 @@
 // the CTAs of one launch.
 #pragma once
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <limits.h>
 #include <math.h>
@@ -147,6 +148,38 @@ __device__ __forceinline__ bool try_wait(uint64_t* bar, unsigned parity) {
                  : "r"(smem_addr(bar)), "r"(parity), "r"(PA_POLL_NS)
                  : "memory");
     return ok != 0;
+}
+
+// ---- words and parts -------------------------------------------------------------------------------------------------
+// Bytes 0 and 1 (HALF 1: 2 and 3) of w, flipped by words_flip, as two f16 values (exact).
+template <int WORDS, int HALF>
+__device__ __forceinline__ uint32_t words2_f16(uint32_t w) {
+    if (WORDS == Q8_KV_INT8) {
+        // byte + 128 in the low mantissa byte of 1024.0, less 1152: exact
+        const uint32_t u = __byte_perm(w, 0x64646464u, HALF ? 0x4342 : 0x4140);
+        const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return e4m3x2_to_f16x2((uint16_t)(HALF ? w >> 16 : w & 0xffffu));
+}
+
+template <int WORDS>
+__device__ __forceinline__ uint32_t words_flip(uint32_t w) {
+    return WORDS == Q8_KV_INT8 ? w ^ 0x80808080u : w;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }  // e in [-126, 127]
+
+// The unbiased exponent of a non-negative float's bits, at least -100 (so that scalings by its inverse and by 2^14 stay
+// finite); infinities and NaN: 0 (whatever they scale stays not finite).
+__device__ __forceinline__ int exponent_of(unsigned bits) {
+    return bits >= 0x7f800000u ? 0 : max((int)(bits >> 23) - 127, -100);
 }
 
 cudaError_t launch_paged_rows(const PagedParams& p, int hd, int words, int tiles, cudaStream_t st);

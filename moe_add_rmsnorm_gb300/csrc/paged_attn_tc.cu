@@ -248,32 +248,6 @@ struct PtTiles {
     __device__ int64_t all() const { return before(count - 1) + PT_START + units(count - 1); }
 };
 
-__device__ __forceinline__ uint32_t f16_pack(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }  // e in [-126, 127]
-// (as in paged_attn.cu)
-__device__ __forceinline__ int exponent_of(unsigned bits) {
-    return bits >= 0x7f800000u ? 0 : max((int)(bits >> 23) - 127, -100);
-}
-
-template <int WORDS, int HALF>
-__device__ __forceinline__ uint32_t words2_f16(uint32_t w) {
-    if (WORDS == Q8_KV_INT8) {
-        const uint32_t u = __byte_perm(w, 0x64646464u, HALF ? 0x4342 : 0x4140);
-        const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return e4m3x2_to_f16x2((uint16_t)(HALF ? w >> 16 : w & 0xffffu));
-}
-template <int WORDS>
-__device__ __forceinline__ uint32_t words_flip(uint32_t w) {
-    return WORDS == Q8_KV_INT8 ? w ^ 0x80808080u : w;
-}
-
 // Byte offset of 16-byte chunk c of row r in a copied stage, as the tensor copies' 128- or 64-byte swizzle places it:
 // eight rows' equal chunks lie in different banks.
 template <int HD>
@@ -483,12 +457,12 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                                         if (!((seen >> (e + 1)) & 1u)) wb = 0.f;
                                         w2 = pk2(wa, wb);
                                     }
-                                    const uint32_t hi = f16_pack(wa, wb);
+                                    const uint32_t hi = pack_f16(wa, wb);
                                     const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hi));
                                     float la, lb;
                                     upk2(fma2(pk2(hf.x, hf.y), less, w2), la, lb);
                                     w[e / 2] = hi;
-                                    w[8 + e / 2] = f16_pack(la, lb);
+                                    w[8 + e / 2] = pack_f16(la, lb);
                                 }
                             }
                             tc_st16(s_at + 16 * c, w);
@@ -739,9 +713,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float a = x[c][2 * j] * f, b = x[c][2 * j + 1] * f;
-                        h[j] = f16_pack(a, b);
+                        h[j] = pack_f16(a, b);
                         const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-                        lo[j] = f16_pack(a - hf.x, b - hf.y);
+                        lo[j] = pack_f16(a - hf.x, b - hf.y);
                     }
                     const uint32_t off = (uint32_t)(m >> 3) * SBO_Q + (uint32_t)(cc + 4 * c) * 128 + (uint32_t)(m & 7) * 16;
                     *reinterpret_cast<uint4*>(sh.qh + off) = make_uint4(h[0], h[1], h[2], h[3]);
