@@ -616,6 +616,23 @@ def test_captured_step_follows_the_device_arrays(q8, new):
     w.close()
 
 
+@pytest.mark.parametrize("nbytes,new", [(1 << 20, [1, 1]), (1 << 20, [90]), (8 << 20, [1, 90])])
+def test_a_small_workspace_is_refused(q8, ws, nbytes, new):
+    """Nothing of the call is launched, not the half that would have had room either; the next call is as ever."""
+    import torch
+    c = Cache(q8, new, [200] * len(new), 2, 128, 16, "int8", 35)
+    q = torch.randn(sum(new), 8, 128, generator=gen(36), device="cuda")
+    out, want = torch.full_like(q, 7.5), torch.empty_like(q)
+    small = q8.Workspace(nbytes)
+    with pytest.raises(q8.Q8Error, match="workspace too small"):
+        q8.q8_paged_attention(c.pages(), c.batch(), q, out, ws=small)
+    torch.cuda.synchronize()
+    assert (out == 7.5).all()
+    q8.q8_paged_attention(c.pages(), c.batch(), q, want, ws=ws)
+    close(want, None, attention64(c, q, 128 ** -0.5))
+    small.close()
+
+
 def test_two_streams_with_their_own_workspaces(q8):
     import torch
     c = Cache(q8, [1] * 20 + [60], [500] * 21, 4, 128, 16, "int8", 27)
