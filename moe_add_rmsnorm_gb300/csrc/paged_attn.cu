@@ -306,13 +306,14 @@ __global__ void __launch_bounds__(PR_THREADS, RowsShared<HD, NT>::CTAS)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 vscale[j] = here && p0 + g + 8 * j < end ? vraw[j] : 0.f;
-                vtop = max(vtop, __float_as_uint(fabsf(vscale[j])));
+                vtop = max(vtop, finite_bits(vscale[j]));
             }
             vtop = __reduce_max_sync(0xffffffffu, vtop);
             float sc[NT][4];
             bool moved = false;  // whether a maximum or the weights' scaling changes: the sums are rescaled then
             const bool all = here && p0 + PR_STEP <= low + 1;  // (low: the smallest of the vectors' last positions)
             unsigned seen = 0xffffffffu;
+            bool apart = false;  // whether some of a masked step's value scales lie far below the weights' scaling
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(PR_THREADS, RowsShared<HD, NT>::CTAS)
                         for (int c = 0; c < 4; ++c) acc[n][j][c] *= alpha[c & 1];
                 }
             }
-            const float wscale = pow2i(-exp_run) * PR_TOP;
+            const float wscale = pow2i(14 - exp_run) * (PR_TOP / 16384.f);
             uint32_t ph[NT][2], pl[NT][2];
             float wt[NT][4];
             const float vw0 = vscale[0] * wscale, vw1 = vscale[1] * wscale;
@@ -386,6 +387,29 @@ __global__ void __launch_bounds__(PR_THREADS, RowsShared<HD, NT>::CTAS)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         if (!((seen >> (4 * n + c)) & 1u)) wt[n][c] = 0.f;
+                const unsigned bits[2] = {finite_bits(vscale[0]), finite_bits(vscale[1])};
+#pragma unroll
+                for (int j = 0; j < 2; ++j) apart |= bits[j] != 0u && exp_run - exponent_of(bits[j]) > PA_SPREAD;
+                apart = __any_sync(0xffffffffu, apart);
+                if (__builtin_expect(apart, 0)) {
+                    // The weights of a vector that sees only such scales, and its products so far, go up by a power of two
+                    // for this step, and down after it.  (The products so far are fewer than 2^7 of values below 2^16 times
+                    // words below 2^9, in terms of exp_top: what they go up by keeps them below 2^122.)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            unsigned own = max((seen >> (4 * n + c)) & 1u ? bits[0] : 0u, (seen >> (4 * n + c + 2)) & 1u ? bits[1] : 0u);
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) own = max(own, __shfl_xor_sync(0xffffffffu, own, o));
+                            const int d = own == 0u ? 0 : min(max(exp_run - exponent_of(own), 0), 90 - (exp_top - exp_run));
+                            wt[n][c] *= pow2i(d), wt[n][c + 2] *= pow2i(d);
+#pragma unroll
+                            for (int j = 0; j < HD / 16; ++j) acc[n][j][c] *= pow2i(d), acc[n][j][c + 2] *= pow2i(d);
+                            if (g == 0) sh.f[wid][8 * n + 2 * t + c] = pow2i(-d);
+                        }
+                    __syncwarp();
+                }
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -432,7 +456,17 @@ __global__ void __launch_bounds__(PR_THREADS, RowsShared<HD, NT>::CTAS)
                         mma16816(acc[n][2 * x + y], a[0][2 * y], a[0][2 * y + 1], a[1][2 * y], a[1][2 * y + 1], ph[n][0], ph[n][1]);
                     }
             }
-            __syncwarp();  // every lane has read the stage
+            if (__builtin_expect(apart, 0)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float f = sh.f[wid][8 * n + 2 * t + c];
+#pragma unroll
+                        for (int j = 0; j < HD / 16; ++j) acc[n][j][c] *= f, acc[n][j][c + 2] *= f;
+                    }
+            }
+            __syncwarp();  // every lane has read the stage (and the factors)
             page_next = page_after;
             if (i + 2 < mine) {
                 if (((i + 2) & 31) == 0) look_up(i + 2);

@@ -182,6 +182,18 @@ __device__ __forceinline__ int exponent_of(unsigned bits) {
     return bits >= 0x7f800000u ? 0 : max((int)(bits >> 23) - 127, -100);
 }
 
+// The magnitude's bits of a value scale, or 0 where it is not finite: such a row makes a number of no sum that it enters, and
+// must not decide how the others are scaled, which are read by rows that do not see it.
+__device__ __forceinline__ unsigned finite_bits(float x) {
+    const unsigned b = __float_as_uint(x) & 0x7fffffffu;
+    return b < 0x7f800000u ? b : 0u;
+}
+
+// Weights are scaled by the largest value scale of the positions taken together, and split into two f16 parts.  A row of which
+// the mask hides that one, and which sees none within 2^PA_SPREAD of it, scales its own weights up further, so that what it
+// does not see costs it no bits.  (Within that spread its weights of 1 lie at 2^6 or above, and an f16 part resolves 2^-24.)
+constexpr int PA_SPREAD = 8;
+
 cudaError_t launch_paged_rows(const PagedParams& p, int hd, int words, int tiles, cudaStream_t st);
 int paged_rows_ctas(int tiles);   // the launch's CTAs
 size_t paged_rows_slot(int hd);   // bytes of one partial result

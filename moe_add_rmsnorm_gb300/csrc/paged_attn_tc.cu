@@ -45,6 +45,7 @@ constexpr int PT_READERS = 18;             // warps that read an item
 // with 6, 267 with 8; 24 sequences of 1 to 300 rows 128, 112, 113, 114, 114).
 constexpr int PT_START = 4;
 constexpr int PT_PEXP = 14;                // weights are split as values of up to 2^(PT_PEXP + 1)
+constexpr unsigned PT_APART = 0x100u;      // a tile's value scales lie further apart than 2^PA_SPREAD
 
 // One item's piece as the roles read it.
 struct PtItem {
@@ -68,11 +69,11 @@ struct PtShared {
     unsigned char v[2][HD / 8 * SBO_V];
     float ks[2][PT_P], vs[2][PT_P];
     float qf[4][PT_M];
-    float m_now[4][PT_M], back[4];   // the vectors' running maxima after a tile, and what scales its product back
+    float m_now[4][PT_M], back[4][PT_M];  // the vectors' running maxima after a tile, and what scales its product back
     float fold_m[PT_M], fold_i[PT_M]; // a fold's maxima, and the inverses of its sums
     float fin_l[2][PT_M];            // an item's sums, of the even and of the odd tiles
     float ce[2];
-    unsigned groups[2];    // which 16-position groups of a tile are there
+    unsigned groups[2];    // which 16-position groups of a tile are there, and PT_APART
     PtItem item[PT_ITEMS];
     uint64_t d_full[PT_ITEMS], d_empty[PT_ITEMS], raw_full[4], raw_empty[4];
     uint64_t sc_full[2], sc_empty[2], k_full, k_empty, v_full[2], v_empty[2];
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                     const unsigned groups = sh.groups[b];
                     const float4* ks4 = reinterpret_cast<const float4*>(sh.ks[b]);
                     const float4* vs4 = reinterpret_cast<const float4*>(sh.vs[b]);
-                    const bool masked = __any_sync(0xffffffffu, lim < p0 + PT_P - 1) || groups != 0xffu;
+                    const bool masked = __any_sync(0xffffffffu, lim < p0 + PT_P - 1) || (groups & 0xffu) != 0xffu;
                     const int count = lim - p0 + 1;  // positions of the tile that the row attends
                     auto bits = [&](int c) -> unsigned {  // those of its columns 16 c .. that are seen
                         const int n = count - 16 * c;
@@ -425,9 +426,18 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                         arrive(&sh.m_full[b][quarter]);
                         const float alpha = ex2(mr - ms);
                         mr = mn;
-                        if (m == 0) sh.back[tau & 3] = sh.ce[b];
+                        float boost = 1.f, back = sh.ce[b];
+                        if (MASK && __builtin_expect(groups & PT_APART, 0)) {  // from the tile's scaling of the weights to the row's own
+                            unsigned top = 0u;  // the largest finite value scale that it sees (as stored)
+#pragma unroll 1
+                            for (int p = 0; p < PT_P; ++p)
+                                if ((bits(p >> 4) >> (p & 15)) & 1u) top = max(top, finite_bits(sh.vs[b][p]));
+                            if (top != 0u) boost = pow2i(PT_PEXP - exponent_of(top));
+                            back *= 1.f / boost;
+                        }
+                        sh.back[tau & 3][m] = back;
                         uint64_t sum = 0ull;
-                        const uint64_t qf2 = pk2(qf, qf), nm2 = pk2(-ms, -ms), less = pk2(-1.f, -1.f);
+                        const uint64_t qf2 = pk2(qf, qf), nm2 = pk2(-ms, -ms), less = pk2(-1.f, -1.f), boost2 = pk2(boost, boost);
                         tc_columns<!MASK>(s_at, [&](int c, const uint32_t (&s)[16]) {
                             const unsigned seen = MASK ? bits(c) : 0u;
                             uint32_t w[16];
@@ -449,7 +459,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                                     }
                                     const uint64_t p2 = pk2(a, b);
                                     sum = add2(sum, p2);
-                                    uint64_t w2 = mul2(p2, j ? pk2(v4.z, v4.w) : pk2(v4.x, v4.y));
+                                    uint64_t w2 = mul2(MASK ? mul2(p2, boost2) : p2, j ? pk2(v4.z, v4.w) : pk2(v4.x, v4.y));
                                     float wa, wb;
                                     upk2(w2, wa, wb);
                                     if (MASK) {  // (a value scale that is not a number stays behind the mask)
@@ -514,7 +524,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                     if (!(ok = wait(&sh.t_full, t))) break;
                     tc_fence_after();
                     if (active) {
-                        const float back = sh.back[t & 3], now = sh.m_now[t & 3][m];
+                        const float back = sh.back[t & 3][m], now = sh.m_now[t & 3][m];
                         alpha = ex2(mr - (now == -INFINITY ? 0.f : now));
                         mr = now;
                         const uint64_t al2 = pk2(alpha, alpha), back2 = pk2(back, back);
@@ -948,10 +958,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                     unsigned groups = 0u;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) groups |= ((ballot >> (4 * j)) & 1u) << j;
-                    const unsigned top = __reduce_max_sync(
-                        0xffffffffu, max(max(__float_as_uint(fabsf(v4.x)), __float_as_uint(fabsf(v4.y))),
-                                         max(__float_as_uint(fabsf(v4.z)), __float_as_uint(fabsf(v4.w)))));
+                    const unsigned bits[4] = {finite_bits(v4.x), finite_bits(v4.y), finite_bits(v4.z), finite_bits(v4.w)};
+                    const unsigned top = __reduce_max_sync(0xffffffffu, max(max(bits[0], bits[1]), max(bits[2], bits[3])));
                     const int ex = top == 0u ? 0 : exponent_of(top);
+                    bool apart = false;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) apart |= bits[j] != 0u && ex - exponent_of(bits[j]) > PA_SPREAD;
+                    if (__any_sync(0xffffffffu, apart)) groups |= PT_APART;
                     const float f = pow2i(PT_PEXP - ex);
                     if (!(ok = wait(&sh.sc_empty[bf], (tau >> 1) + 1))) break;
                     reinterpret_cast<float4*>(sh.ks[bf])[lane] = k4;

@@ -1,0 +1,96 @@
+"""The paged key/value cache on the GPU where one row's numbers meet another's.
+
+Tolerances.  As in test_gpu_kv_pages.py, but every row's bound is formed from the positions which that row sees: a score is
+off by at most delta = 2^-18 of its products' magnitudes; the output by (2 delta + 2^-17) sum p |v|, and by what a split
+weight may lose, the smaller of the weight and 2^-28 times the largest value the row sees.  lse is off by delta, by the sum's
+rounding (an exponential of 2^-22 and, at the lengths here, fewer than 2^5 additions of 2^-24: 2^-18 in all), and by the
+scores' own rounding to f32 and that of the logarithm's result (2^-20 of the largest of them).
+"""
+import math
+
+import pytest
+
+from test_gpu_kv_pages import Cache, gen, ws  # noqa: F401  (ws: a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def attention_seen(c, q, scale):
+    """Output, lse and both bounds in f64, each row's from the positions that it sees alone."""
+    import torch
+    rows, heads, hd = q.shape
+    group = heads // c.kv
+    out, lim = (torch.zeros(rows, heads, hd, dtype=torch.float64, device="cuda") for _ in range(2))
+    lse, off = (torch.zeros(rows, heads, dtype=torch.float64, device="cuda") for _ in range(2))
+    r = 0
+    for b, (n, L) in enumerate(zip(c.new, c.length)):
+        for i in range(n if n else 0):
+            k, v = (c.values(name, b)[:L - n + i + 1].transpose(0, 1) for name in "kv")  # [kv, seen, hd]
+            x = q[r].double().unflatten(0, (c.kv, group))
+            s = torch.einsum("kgd,ktd->kgt", x, k) * scale
+            delta = torch.einsum("kgd,ktd->kgt", x.abs(), k.abs()).amax(-1, keepdim=True) * scale * 2 ** -18
+            m = s.amax(-1, keepdim=True)
+            e = (s - m).exp()
+            total = e.sum(-1, keepdim=True)
+            o = torch.einsum("kgt,ktd->kgd", e / total, v)
+            near = torch.einsum("kgt,ktd->kgd", e / total, v.abs()) * (2 * delta + 2 ** -17)
+            near = near + (e.clamp_max(2 ** -28).sum(-1, keepdim=True) / total) * v.abs().amax((1, 2))[:, None, None]
+            out[r], lim[r] = o.flatten(0, 1), near.flatten(0, 1)
+            lse[r] = (m + total.log()).flatten()
+            off[r] = (delta + 2 ** -18 + 2 ** -20 * (s.abs().amax(-1, keepdim=True) + total.log().abs())).flatten()
+            r += 1
+    return out, lim, lse, off
+
+
+def near(out, lse, ref, rows, heads):
+    """Rows `rows` (an index) and heads `heads` of out and lse against the reference; the others are another check's."""
+    o, lim, l, off = (t[rows][:, heads] for t in ref)
+    d = (out[rows][:, heads].double() - o).abs()
+    assert (d <= lim).all(), f"off by {d.nan_to_num(math.inf).max():.3e}, allowed up to {lim.max():.3e}"
+    assert ((lse[rows][:, heads].double() - l).abs() <= off).all()
+
+
+# A sequence of a few rows and one of many (the two kernels), and one of many beside places that hold none (which the first
+# kernel takes): the bad position is one that the last rows see.
+MASKED = [([3], [300], 299), ([4], [290], 288), ([140], [300], 270), ([257], [257], 130),
+          ([40] + [0] * 39, [300] + [0] * 39, 281)]
+
+
+@pytest.mark.parametrize("new,length,at", MASKED)
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("size", [8.0, 1000.0, 2.0 ** -40])
+@pytest.mark.parametrize("words", ["int8", "e4m3"])
+def test_a_value_row_that_is_not_finite_stays_behind_the_mask(q8, ws, new, length, at, bad, size, words):  # noqa: F811
+    """Rows before it are as if it were not there, whatever the size of the values that they see."""
+    import torch
+    c = Cache(q8, new, length, 2, 128, 16, words, 41)
+    n, L = new[0], length[0]
+    c.vs.copy_(c.vs * 0 + size * (1 + torch.rand(c.vs.shape, generator=gen(42), device="cuda")))
+    q = torch.randn(n, 8, 128, generator=gen(43), device="cuda")
+    ref = attention_seen(c, q, 128 ** -0.5)
+    a, o = c.where(0, torch.tensor([at], device="cuda"))
+    c.vs[a, 0, o] = bad
+    out, lse = torch.empty_like(q), torch.empty(n, 8, device="cuda")
+    q8.q8_paged_attention(c.pages(), c.batch(), q, out, lse=lse, ws=ws)
+    first = at - (L - n)  # the first row that sees it
+    assert c.error.item() == 0
+    near(out, lse, ref, slice(0, first), slice(0, 8))
+    near(out, lse, ref, slice(first, n), slice(4, 8))  # (the other key/value head)
+    assert not out[first:, :4].isfinite().any()
+
+
+@pytest.mark.parametrize("new,length,at", MASKED)
+@pytest.mark.parametrize("power", [20, 45, 90])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -20])
+def test_a_large_value_row_costs_the_rows_before_it_no_bits(q8, ws, new, length, at, power, size):  # noqa: F811
+    import torch
+    c = Cache(q8, new, length, 2, 128, 16, "int8", 44)
+    n, L = new[0], length[0]
+    c.vs.mul_(size)
+    a, o = c.where(0, torch.arange(at, L, device="cuda"))
+    c.vs[a, :, o] = c.vs[a, :, o] * 2.0 ** power
+    q = torch.randn(n, 8, 128, generator=gen(45), device="cuda")
+    ref = attention_seen(c, q, 128 ** -0.5)
+    out, lse = torch.empty_like(q), torch.empty(n, 8, device="cuda")
+    q8.q8_paged_attention(c.pages(), c.batch(), q, out, lse=lse, ws=ws)
+    near(out, lse, ref, slice(0, n), slice(0, 8))
