@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(PR_THREADS, RowsShared<HD, NT>::CTAS)
             for (int w = 0; w < PR_WARPS; ++w) M = fmaxf(M, sh.m[w][tid]);
             for (int w = 0; w < PR_WARPS; ++w) {
                 const float f = M == -INFINITY ? 0.f : ex2(sh.m[w][tid] - M);
-                if (sh.m[w][tid] != -INFINITY) L += sh.l[w][tid] * f;
+                L = fmaf(sh.l[w][tid], f, L);  // (no number where a warp saw scores that are none, though its maximum is -infinity)
                 sh.f[w][tid] *= f;
             }
             sh.m[0][tid] = M;

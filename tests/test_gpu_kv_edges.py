@@ -94,3 +94,41 @@ def test_a_large_value_row_costs_the_rows_before_it_no_bits(q8, ws, new, length,
     out, lse = torch.empty_like(q), torch.empty(n, 8, device="cuda")
     q8.q8_paged_attention(c.pages(), c.batch(), q, out, lse=lse, ws=ws)
     near(out, lse, ref, slice(0, n), slice(0, 8))
+
+
+@pytest.mark.parametrize("new,length,keys", [
+    ([1], [1], [0]), ([1], [17], [16]), ([1], [300], range(32, 48)), ([1], [4097], range(1024, 1040)),
+    ([1], [4097], range(4097)), ([1] * 3, [900, 1, 33], range(900)), ([2], [130], [128]), ([140], [300], [160, 299]),
+    ([140], [300], range(300))])
+def test_lse_beside_keys_that_are_not_numbers(q8, ws, new, length, keys):  # noqa: F811
+    """A row that sees such a key has no lse, whichever positions are looked at together; others keep theirs."""
+    import torch
+    c = Cache(q8, new, length, 2, 128, 16, "int8", 48)
+    rows = sum(new)
+    q = torch.randn(rows, 8, 128, generator=gen(49), device="cuda")
+    ref = attention_seen(c, q, 128 ** -0.5)
+    a, o = c.where(0, torch.tensor(list(keys), device="cuda"))
+    c.ks[a, 1, o] = math.nan
+    out, lse = torch.empty_like(q), torch.empty(rows, 8, device="cuda")
+    q8.q8_paged_attention(c.pages(), c.batch(), q, out, lse=lse, ws=ws)
+    first = max(0, min(keys) - (length[0] - new[0]))
+    assert out[first:new[0], 4:].isnan().all() and lse[first:new[0], 4:].isnan().all()
+    near(out, lse, ref, slice(0, rows), slice(0, 4))
+    near(out, lse, ref, slice(0, first), slice(4, 8))
+    near(out, lse, ref, slice(new[0], rows), slice(4, 8))
+
+
+@pytest.mark.parametrize("new,length", [([1], [1]), ([1], [5000]), ([3], [700]), ([140], [300])])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_lse_of_a_query_that_is_not_finite(q8, ws, new, length, bad):  # noqa: F811
+    import torch
+    c = Cache(q8, new, length, 2, 128, 16, "int8", 50)
+    n = new[0]
+    q = torch.randn(n, 8, 128, generator=gen(51), device="cuda")
+    ref = attention_seen(c, q, 128 ** -0.5)
+    q[n - 1, 3, 7] = bad
+    out, lse = torch.empty_like(q), torch.empty(n, 8, device="cuda")
+    q8.q8_paged_attention(c.pages(), c.batch(), q, out, lse=lse, ws=ws)
+    assert out[n - 1, 3].isnan().all() and lse[n - 1, 3].isnan()
+    out[n - 1, 3], lse[n - 1, 3] = ref[0][n - 1, 3].float(), ref[2][n - 1, 3].float()
+    near(out, lse, ref, slice(0, n), slice(0, 8))
