@@ -375,6 +375,7 @@ typedef struct {
  * decrease; a sequence may own none; rows outside every sequence are left as they were) and has kv_len[b] cached
  * positions, its own rows the last of them: row row_start[b] + i is position kv_len[b] - (row_start[b+1] -
  * row_start[b]) + i.  Position p lives in page table[b*table_stride + p/page_size], slot p % page_size.
+ * A call with no rows or no sequences does nothing; the addresses of what is empty then may be NULL.
  * What the host cannot check is checked on the device, and recorded in *error (or-ed into it) when error is not NULL:
  *   - a sequence whose rows are not within the call's, or whose kv_len is out of range, is skipped by q8_kv_append and
  *     q8_kv_read, as is a row that a decreasing row_start leads to no sequence of its own; q8_paged_attention skips the

@@ -35,14 +35,15 @@ int check_view(const q8_kv_pages* pages, const q8_kv_batch* batch, int64_t rows,
         return model_fail(Q8_EUNSUPPORTED, "pages: page_size %lld: a power of two from 16 to 1024", (long long)ps);
     if (!aligned(pages->k, 32) || !aligned(pages->v, 32)) return model_fail(Q8_EINVAL, "pages: words not 32-byte aligned");
     if (!aligned(pages->ks, 16) || !aligned(pages->vs, 16)) return model_fail(Q8_EINVAL, "pages: scales not 16-byte aligned");
-    if (!batch->row_start || !batch->kv_len || !batch->table)
+    // (a batch without sequences has no arrays: an empty tensor's address is null)
+    if (batch->seqs != 0 && (!batch->row_start || !batch->kv_len || !batch->table))
         return model_fail(Q8_EINVAL, "batch: null row_start, kv_len or table");
     if (!aligned(batch->row_start, 4) || !aligned(batch->kv_len, 4) || !aligned(batch->table, 4) || !aligned(batch->error, 4))
         return model_fail(Q8_EINVAL, "batch: an array not 4-byte aligned");
     if (batch->seqs < 0 || rows < 0) return model_fail(Q8_EINVAL, "batch: seqs or rows negative");
     if (batch->seqs > 65536) return model_fail(Q8_EUNSUPPORTED, "batch: %lld sequences: at most 65536", (long long)batch->seqs);
     if (rows > (1 << 24)) return model_fail(Q8_EUNSUPPORTED, "rows %lld: at most 2^24", (long long)rows);
-    if (batch->table_pages < 1 || batch->table_stride < batch->table_pages)
+    if (batch->seqs != 0 && (batch->table_pages < 1 || batch->table_stride < batch->table_pages))
         return model_fail(Q8_EINVAL, "batch: %lld pages a table row, rows %lld apart", (long long)batch->table_pages,
                           (long long)batch->table_stride);
     if (batch->table_pages > kMost / ps || batch->table_stride > kMost)
@@ -67,9 +68,9 @@ int check_view(const q8_kv_pages* pages, const q8_kv_batch* batch, int64_t rows,
     return Q8_OK;
 }
 
-// f32 rows of `width` values, `stride` apart.
+// f32 rows of `width` values, `stride` apart (none: any address, that of an empty tensor among them).
 int check_rows(const float* x, int64_t stride, int64_t width, int64_t rows, const char* name) {
-    if (!x) return model_fail(Q8_EINVAL, "%s: null", name);
+    if (!x && rows != 0) return model_fail(Q8_EINVAL, "%s: null", name);
     if (!aligned(x, 16) || stride % 4) return model_fail(Q8_EINVAL, "%s: address or stride not 16-byte aligned", name);
     if (rows > 1 && stride < width)
         return model_fail(Q8_EINVAL, "%s: rows %lld apart, %lld values wide", name, (long long)stride, (long long)width);
@@ -139,7 +140,7 @@ int q8_kv_read(const q8_kv_pages* pages, const q8_kv_batch* batch, int64_t rows,
                int64_t row_stride, int64_t head_stride, q8_stream stream) {
     KvReadCall c;
     if (int r = check_view(pages, batch, rows, &c.view)) return r;
-    if (!k_out && !v_out) return model_fail(Q8_EINVAL, "k_out and v_out: both null");
+    if (!k_out && !v_out && rows != 0) return model_fail(Q8_EINVAL, "k_out and v_out: both null");
     if (!aligned(k_out, 32) || !aligned(v_out, 32) || row_stride % 8 || head_stride % 8)
         return model_fail(Q8_EINVAL, "k_out, v_out: an address or stride not 32-byte aligned");
     const int64_t hd = pages->head_dim;
@@ -167,7 +168,7 @@ int q8_paged_attention(const q8_kv_pages* pages, const q8_kv_batch* batch, int64
     if (heads / kv > 64) return model_fail(Q8_EUNSUPPORTED, "heads %lld: more than 64 a key/value head", (long long)heads);
     if (int r = check_rows(q, q_stride, heads * pages->head_dim, rows, "q")) return r;
     if (int r = check_rows(out, out_stride, heads * pages->head_dim, rows, "out")) return r;
-    if (q == out) return model_fail(Q8_EINVAL, "out: q itself");
+    if (q == out && rows != 0) return model_fail(Q8_EINVAL, "out: q itself");
     if (!aligned(lse, 4)) return model_fail(Q8_EINVAL, "lse: not 4-byte aligned");
     if (!(scale > 0.f) || scale > 1e30f) return model_fail(Q8_EINVAL, "scale: not positive and finite");
     if (!ws) return model_fail(Q8_EINVAL, "ws: null");

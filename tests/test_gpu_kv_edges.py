@@ -132,3 +132,22 @@ def test_lse_of_a_query_that_is_not_finite(q8, ws, new, length, bad):  # noqa: F
     assert out[n - 1, 3].isnan().all() and lse[n - 1, 3].isnan()
     out[n - 1, 3], lse[n - 1, 3] = ref[0][n - 1, 3].float(), ref[2][n - 1, 3].float()
     near(out, lse, ref, slice(0, n), slice(0, 8))
+
+
+def test_a_batch_without_rows_or_sequences(q8, ws):  # noqa: F811
+    """Empty tensors, whose address is none, are a batch with nothing to do."""
+    import torch
+    c = Cache(q8, [1, 1], [5, 9], 2, 128, 16, "int8", 52)
+    words = c.kw.clone()
+    none = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for rows, batch in ((0, c.batch()), (0, q8.kv_batch(none, none[:0], c.table[:0, :1], c.error)),
+                        (2, q8.kv_batch(none, none[:0], c.table[:0, :0], c.error))):
+        q, k = torch.ones(rows, 8, 128, device="cuda"), torch.ones(rows, 2, 128, device="cuda")
+        out = torch.full_like(q, 7.5)
+        q8.q8_kv_append(c.pages(), batch, q, k, k, out)
+        q8.q8_kv_append(c.pages(), batch, None, k, k, None)
+        q8.q8_kv_read(c.pages(), batch, k, torch.empty_like(k))
+        q8.q8_kv_read(c.pages(), batch, None, k)
+        q8.q8_paged_attention(c.pages(), batch, q, out, lse=torch.empty(rows, 8, device="cuda"), ws=ws)
+        assert (out == 7.5).all() and (k == 1).all()
+    assert torch.equal(c.kw, words) and c.error.item() == 0
