@@ -514,6 +514,9 @@ __global__ void __launch_bounds__(PR_THREADS, RowsShared<HD, NT>::CTAS)
                 L = fmaf(sh.l[w][tid], f, L);  // (no number where a warp saw scores that are none, though its maximum is -infinity)
                 sh.f[w][tid] *= f;
             }
+            // (the totals are divided by the sum as they are added up, so that no sum of large values overflows)
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            for (int w = 0; w < PR_WARPS; ++w) sh.f[w][tid] *= inv;
             sh.m[0][tid] = M;
             sh.l[0][tid] = L;
         }
@@ -523,10 +526,8 @@ __global__ void __launch_bounds__(PR_THREADS, RowsShared<HD, NT>::CTAS)
         float* slot = pk.part + (int64_t)(2 * blockIdx.x + (sh.lo >= item_at ? 0 : 1)) * SLOT;
         auto write_out = [&](int i, int ln, float4 v, const float* m, const float* l) {
             const int n = i / (HD / 16), dim = DPG * (ln >> 2) + 2 * (i % (HD / 16)), c = 8 * n + 2 * (ln & 3);
-            const float x0 = l[c] == 0.f ? 0.f : 1.f / l[c], x1 = l[c + 1] == 0.f ? 0.f : 1.f / l[c + 1];
-            if (sh.at[c] >= 0) *reinterpret_cast<float2*>(pk.out + sh.at[c] + dim) = make_float2(v.x * x0, v.z * x0);
-            if (sh.at[c + 1] >= 0)
-                *reinterpret_cast<float2*>(pk.out + sh.at[c + 1] + dim) = make_float2(v.y * x1, v.w * x1);
+            if (sh.at[c] >= 0) *reinterpret_cast<float2*>(pk.out + sh.at[c] + dim) = make_float2(v.x, v.z);
+            if (sh.at[c + 1] >= 0) *reinterpret_cast<float2*>(pk.out + sh.at[c + 1] + dim) = make_float2(v.y, v.w);
             if (pk.lse && i % (HD / 16) == 0 && (ln >> 2) == 0)
                 for (int j = 0; j < 2; ++j)
                     if (sh.at[c + j] >= 0)
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(PR_THREADS, RowsShared<HD, NT>::CTAS)
                 if (tid == 0) pk.counters[c0] = 0;
                 const bool opens = run.start(c0) >= item_at;
                 auto slot_of = [&](int c) { return pk.part + (int64_t)paged_slot(c, c0, opens) * SLOT; };
-                // every piece's weight for every vector, then the sums with many pieces' loads in flight
+                // every piece's share of every vector's sum, then the results with many pieces' loads in flight
                 const int pieces = c1 - c0 + 1;
                 float* wf = reinterpret_cast<float*>(sh.o);  // [pieces][MT]: the warps' totals are used up
                 for (int i = tid; i < pieces * MT; i += PR_THREADS) wf[i] = __ldcg(slot_of(c0 + i / MT) + FR * 128 + i % MT);
@@ -568,28 +569,28 @@ __global__ void __launch_bounds__(PR_THREADS, RowsShared<HD, NT>::CTAS)
                     float Mx = -INFINITY;
                     for (int p = 0; p < pieces; ++p) Mx = fmaxf(Mx, wf[p * MT + tid]);
                     sh.m[0][tid] = Mx;
-                    sh.l[0][tid] = 0.f;
                 }
                 __syncthreads();
                 for (int i = tid; i < pieces * MT; i += PR_THREADS) {
-                    const float mx = sh.m[0][i % MT];
-                    wf[i] = ex2(wf[i] - (mx == -INFINITY ? 0.f : mx));
+                    const float mx = sh.m[0][i % MT], l = __ldcg(slot_of(c0 + i / MT) + FR * 128 + MT + i % MT);
+                    wf[i] = ex2(wf[i] - (mx == -INFINITY ? 0.f : mx)) * l;
                 }
                 __syncthreads();
                 if (tid < MT) {
                     float Lx = 0.f;
-#pragma unroll 8
-                    for (int p = 0; p < pieces; ++p) Lx = fmaf(__ldcg(slot_of(c0 + p) + FR * 128 + MT + tid), wf[p * MT + tid], Lx);
+                    for (int p = 0; p < pieces; ++p) Lx += wf[p * MT + tid];
                     sh.l[0][tid] = Lx;
+                    sh.f[0][tid] = Lx == 0.f ? 0.f : 1.f / Lx;
                 }
                 __syncthreads();
                 for (int i = tid; i < FR * 32; i += PR_THREADS) {
                     const int fr = i >> 5, ln = i & 31, c = 8 * (fr / (HD / 16)) + 2 * (ln & 3);
+                    const float x0 = sh.f[0][c], x1 = sh.f[0][c + 1];
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
                     for (int p = 0; p < pieces; ++p) {
                         const float4 o = __ldcg(reinterpret_cast<const float4*>(slot_of(c0 + p)) + i);
-                        const float f0 = wf[p * MT + c], f1 = wf[p * MT + c + 1];
+                        const float f0 = wf[p * MT + c] * x0, f1 = wf[p * MT + c + 1] * x1;
                         v.x = fmaf(o.x, f0, v.x), v.y = fmaf(o.y, f1, v.y), v.z = fmaf(o.z, f0, v.z), v.w = fmaf(o.w, f1, v.w);
                     }
                     write_out(fr, ln, v, sh.m[0], sh.l[0]);

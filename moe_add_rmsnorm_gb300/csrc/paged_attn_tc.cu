@@ -45,6 +45,9 @@ constexpr int PT_READERS = 18;             // warps that read an item
 // with 6, 267 with 8; 24 sequences of 1 to 300 rows 128, 112, 113, 114, 114).
 constexpr int PT_START = 4;
 constexpr int PT_PEXP = 14;                // weights are split as values of up to 2^(PT_PEXP + 1)
+// The output sums are kept 2^-PT_DOWN of what they stand for: those of 2^30 positions of the largest values stay finite
+// (and values down to 2^-96 keep their bits).
+constexpr int PT_DOWN = 30;
 constexpr unsigned PT_APART = 0x100u;      // a tile's value scales lie further apart than 2^PA_SPREAD
 
 // One item's piece as the roles read it.
@@ -584,7 +587,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
             }
             const bool whole = d.t0 == 0 && d.t1 == d.units;
             float* slot = pk.part + (int64_t)(2 * blockIdx.x + (d.opens ? 0 : 1)) * SLOT;
-            const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            const float inv = !whole ? 1.f : l == 0.f ? 0.f : (float)(1 << PT_DOWN) / l;
             float* dst = whole ? pk.out + row * pk.out_stride + (int64_t)head * HD : slot + 4 * m;
             const int step = whole ? 4 : 4 * PT_M;  // a partial result's float4 i of vector m at 4 (PT_M i + m)
             if (active) {
@@ -633,7 +636,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                 for (int c = d.c0; c <= d.c1; ++c)
                     sum = fmaf(__ldcg(slot_of(c) + PT_M * (HD + 1) + m), ex2(__ldcg(slot_of(c) + PT_M * HD + m) - ms), sum);
                 sh.fold_m[m] = ms;
-                sh.fold_i[m] = sum == 0.f ? 0.f : 1.f / sum;
+                sh.fold_i[m] = sum == 0.f ? 0.f : (float)(1 << PT_DOWN) / sum;
                 if (pk.lse) pk.lse[row * pk.heads + head] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.693147180559945f;
             }
             arrive(&sh.met);
@@ -960,7 +963,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                     for (int j = 0; j < 8; ++j) groups |= ((ballot >> (4 * j)) & 1u) << j;
                     const unsigned bits[4] = {finite_bits(v4.x), finite_bits(v4.y), finite_bits(v4.z), finite_bits(v4.w)};
                     const unsigned top = __reduce_max_sync(0xffffffffu, max(max(bits[0], bits[1]), max(bits[2], bits[3])));
-                    const int ex = top == 0u ? 0 : exponent_of(top);
+                    const int ex = top == 0u ? 0 : max(exponent_of(top), PT_PEXP + PT_DOWN - 126);
                     bool apart = false;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) apart |= bits[j] != 0u && ex - exponent_of(bits[j]) > PA_SPREAD;
@@ -969,7 +972,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
                     if (!(ok = wait(&sh.sc_empty[bf], (tau >> 1) + 1))) break;
                     reinterpret_cast<float4*>(sh.ks[bf])[lane] = k4;
                     reinterpret_cast<float4*>(sh.vs[bf])[lane] = make_float4(v4.x * f, v4.y * f, v4.z * f, v4.w * f);
-                    if (lane == 0) sh.ce[bf] = pow2i(ex - PT_PEXP), sh.groups[bf] = groups;
+                    if (lane == 0) sh.ce[bf] = pow2i(ex - PT_PEXP - PT_DOWN), sh.groups[bf] = groups;
                     arrive(&sh.sc_full[bf]);
                 }
             }

@@ -151,3 +151,16 @@ def test_a_batch_without_rows_or_sequences(q8, ws):  # noqa: F811
         q8.q8_paged_attention(c.pages(), batch, q, out, lse=torch.empty(rows, 8, device="cuda"), ws=ws)
         assert (out == 7.5).all() and (k == 1).all()
     assert torch.equal(c.kw, words) and c.error.item() == 0
+
+
+def test_the_largest_scales(q8, ws):  # noqa: F811
+    """Value scales up to the largest that the pages can hold."""
+    import torch
+    for new, length in (([2], [40]), ([60], [200])):
+        c = Cache(q8, new, length, 2, 128, 16, "int8", 46)
+        c.vs.copy_(c.vs * 0 + 2.6e36)  # words of up to 127: values up to 3.3e38
+        q = torch.randn(new[0], 8, 128, generator=gen(47), device="cuda")
+        ref = attention_seen(c, q, 128 ** -0.5)
+        out, lse = torch.empty_like(q), torch.empty(new[0], 8, device="cuda")
+        q8.q8_paged_attention(c.pages(), c.batch(), q, out, lse=lse, ws=ws)
+        near(out, lse, ref, slice(0, new[0]), slice(0, 8))
