@@ -428,6 +428,13 @@ Q8_API int q8_paged_attention(const q8_kv_pages *pages, const q8_kv_batch *batch
                               const float *q, int64_t q_stride, float scale, float *out, int64_t out_stride, float *lse,
                               q8_ws *ws, q8_stream stream);
 
+/* Self-test of the bounded waits: q8_paged_attention's launches with every copy of cached words waited for 16 bytes longer
+ * than it brings, so that the first waits of every CTA run out after `polls` polls (1 to 2^12) and the launches end as they
+ * do when a copy is lost: no result is written, and Q8_KV_ERR_WAIT is recorded. */
+Q8_API int q8_paged_wait_selftest(const q8_kv_pages *pages, const q8_kv_batch *batch, int64_t rows, int64_t heads,
+                                  const float *q, int64_t q_stride, float scale, float *out, int64_t out_stride, q8_ws *ws,
+                                  unsigned polls, q8_stream stream);
+
 /* ---- errors --------------------------------------------------------------------------------------------------- */
 /* The text of the calling thread's last error (empty when none); valid until the thread's next call. */
 Q8_API const char *q8_last_error(void);

@@ -107,6 +107,8 @@ _SIGS = {
                      _vp, _i64, _vp, _i64, _vp],
     "q8_kv_read": [_P(q8_kv_pages), _P(q8_kv_batch), _i64, _vp, _vp, _i64, _i64, _vp],
     "q8_paged_attention": [_P(q8_kv_pages), _P(q8_kv_batch), _i64, _i64, _vp, _i64, _f32, _vp, _i64, _vp, _vp, _vp],
+    "q8_paged_wait_selftest": [_P(q8_kv_pages), _P(q8_kv_batch), _i64, _i64, _vp, _i64, _f32, _vp, _i64, _vp, ctypes.c_uint,
+                               _vp],
     "q8_model_create": [_P(q8_model_desc), _P(_vp)],
     "q8_model_destroy": [_vp],
     "decode_step": [_vp, _vp],
@@ -479,6 +481,16 @@ def q8_paged_attention(pages, batch, q, out, scale=None, lse=None, ws=None, stre
         _refuse("out: rows differ")
     _check(lib.q8_paged_attention(pages, batch, rows, heads, qa, qs, hd ** -0.5 if scale is None else scale, oa, os_,
                                   _vec(lse, rows * heads, d, "lse"), ws.handle if ws else None, _stream_of(stream, d)))
+
+
+def q8_paged_wait_selftest(pages, batch, q, out, polls, ws, stream=None):
+    """q8_paged_attention's launches with waits that run out after `polls` polls."""
+    hd, d = pages.head_dim, _paged_device(pages, batch, q, "q")
+    rows, heads = q.shape[0], q.shape[1]
+    qa, qs = _rows(q, heads, hd, d, "q")
+    oa, os_ = _rows(out, heads, hd, d, "out")
+    _check(lib.q8_paged_wait_selftest(pages, batch, rows, heads, qa, qs, hd ** -0.5, oa, os_, ws.handle, int(polls),
+                                      _stream_of(stream, d)))
 
 
 class Model:

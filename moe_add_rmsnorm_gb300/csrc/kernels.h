@@ -367,6 +367,8 @@ struct PagedAttnCall {
     float scale = 0.f;
     float* out = nullptr;
     float* lse = nullptr;
+    unsigned polls = 0;    // of a bounded wait (0: the kernels' own limit)
+    unsigned missing = 0;  // bytes that every copy is waited for beyond what it brings (the self-test's: 16)
 };
 cudaError_t launch_paged_attention(const PagedAttnCall& c, Carve& ws, cudaStream_t st);
 

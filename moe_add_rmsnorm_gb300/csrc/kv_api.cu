@@ -157,10 +157,9 @@ int q8_kv_read(const q8_kv_pages* pages, const q8_kv_batch* batch, int64_t rows,
     return done(launch_kv_read(c, (cudaStream_t)stream), "q8_kv_read");
 }
 
-int q8_paged_attention(const q8_kv_pages* pages, const q8_kv_batch* batch, int64_t rows, int64_t heads, const float* q,
-                       int64_t q_stride, float scale, float* out, int64_t out_stride, float* lse, q8_ws* ws,
-                       q8_stream stream) {
-    PagedAttnCall c;
+static int attention(PagedAttnCall& c, const q8_kv_pages* pages, const q8_kv_batch* batch, int64_t rows, int64_t heads,
+                     const float* q, int64_t q_stride, float scale, float* out, int64_t out_stride, float* lse, q8_ws* ws,
+                     q8_stream stream) {
     if (int r = check_view(pages, batch, rows, &c.view)) return r;
     const int64_t kv = pages->kv_heads;
     if (heads < 1 || heads % kv) return model_fail(Q8_EINVAL, "heads %lld: not a multiple of the %lld key/value heads",
@@ -185,6 +184,24 @@ int q8_paged_attention(const q8_kv_pages* pages, const q8_kv_batch* batch, int64
     cudaError_t e = launch_paged_attention(c, cv, (cudaStream_t)stream);
     if (cv.overflow) return model_fail(Q8_ENOSPACE, "q8_paged_attention: workspace too small for the partial results");
     return done(e, "q8_paged_attention");
+}
+
+int q8_paged_attention(const q8_kv_pages* pages, const q8_kv_batch* batch, int64_t rows, int64_t heads, const float* q,
+                       int64_t q_stride, float scale, float* out, int64_t out_stride, float* lse, q8_ws* ws,
+                       q8_stream stream) {
+    PagedAttnCall c;
+    return attention(c, pages, batch, rows, heads, q, q_stride, scale, out, out_stride, lse, ws, stream);
+}
+
+int q8_paged_wait_selftest(const q8_kv_pages* pages, const q8_kv_batch* batch, int64_t rows, int64_t heads, const float* q,
+                           int64_t q_stride, float scale, float* out, int64_t out_stride, q8_ws* ws, unsigned polls,
+                           q8_stream stream) {
+    model_fail(Q8_OK, "%s", "");
+    if (polls < 1 || polls > (1u << 12)) return model_fail(Q8_EINVAL, "polls %u: 1 to 2^12", polls);
+    PagedAttnCall c;
+    c.polls = polls;
+    c.missing = 16;
+    return attention(c, pages, batch, rows, heads, q, q_stride, scale, out, out_stride, nullptr, ws, stream);
 }
 
 }  // extern "C"

@@ -88,7 +88,7 @@ struct RowsShared {
     // What the walk over the items keeps between them (in shared memory: the registers are the inner loop's).
     int64_t cur, lo, hi, seq_at, item_at, units, total;
     int seq, ctas, last;
-    unsigned polls;                    // a wait's limit
+    int dead;                          // a wait gave up: the CTA leaves
 };
 
 template <int HD, int WORDS, int NT>
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(PR_THREADS, RowsShared<HD, NT>::CTAS)
             sh.seq = run.seq, sh.seq_at = run.seq_at;
             sh.total = run.total, sh.ctas = run.ctas;
             for (int i = 0; i < 2 * PR_WARPS; ++i) mbar_init(&sh.full[0][i], 1);
-            sh.polls = PA_POLLS;
+            sh.dead = 0;
             fence_barrier_init();
         }
     }
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(PR_THREADS, RowsShared<HD, NT>::CTAS)
         auto issue = [&](int i, int page) {  // step i's words on their way
             if (lane == 0) {
                 const unsigned stage = (used + i) & 1;
-                mbar_arrive_expect_tx(&sh.full[wid][stage], 2 * PR_STEP * HD);
+                mbar_arrive_expect_tx(&sh.full[wid][stage], 2 * PR_STEP * HD + pk.missing);
                 tma_box(sh.ring[wid][stage][0], &map_k, slot_of_step(i), page < 0 ? kv.pages : page, &sh.full[wid][stage]);
                 tma_box(sh.ring[wid][stage][1], &map_v, slot_of_step(i), page < 0 ? kv.pages : page, &sh.full[wid][stage]);
             }
@@ -266,10 +266,15 @@ __global__ void __launch_bounds__(PR_THREADS, RowsShared<HD, NT>::CTAS)
             if (i + 1 < mine) load_scales(i + 1, page_after);
             bool got = try_wait(&sh.full[wid][stage], ((used + i) >> 1) & 1);
 #pragma unroll 1
-            for (unsigned poll = 0; !got && poll < *(volatile unsigned*)&sh.polls; ++poll) got = try_wait(&sh.full[wid][stage], ((used + i) >> 1) & 1);
-            if (!got) {  // (the CTA's later waits are short)
-                *(volatile unsigned*)&sh.polls = 64;
-                kv_flag(kv, Q8_KV_ERR_WAIT);
+            for (unsigned poll = 0; !got && poll < pk.polls && !*(volatile int*)&sh.dead; ++poll)
+                got = try_wait(&sh.full[wid][stage], ((used + i) >> 1) & 1);
+            if (__builtin_expect(!__all_sync(0xffffffffu, got), 0)) {
+                // Nothing of what the ring holds is used and nothing more is copied; this step's copies and the next one's
+                // may be on their way, and none is in flight when the CTA leaves.
+                *(volatile int*)&sh.dead = 1;
+#pragma unroll 1
+                for (int j = i; j < mine && j < i + 2; ++j) drain(&sh.full[wid][(used + j) & 1], ((used + j) >> 1) & 1);
+                break;
             }
             Bytes<KB> kw[2];
 #pragma unroll
@@ -506,6 +511,10 @@ __global__ void __launch_bounds__(PR_THREADS, RowsShared<HD, NT>::CTAS)
                 }
             }
         __syncthreads();
+        if (sh.dead) {  // (every warp's copies have arrived, and no result of this item is written)
+            if (tid == 0) wait_gave_up(pk);
+            return;
+        }
         float M = -INFINITY, L = 0.f;
         if (tid < MT) {
             for (int w = 0; w < PR_WARPS; ++w) M = fmaxf(M, sh.m[w][tid]);
@@ -655,6 +664,8 @@ cudaError_t launch_paged_attention(const PagedAttnCall& c, Carve& ws, cudaStream
     p.scale = (float)((double)c.scale * 1.4426950408889634);
     p.out = c.out;
     p.lse = c.lse;
+    p.polls = c.polls ? c.polls : PA_POLLS;
+    p.missing = c.missing;
     // Which kernel takes a sequence goes by its vectors a key/value head, which the device holds: up to kRowsMost the
     // rows kernel.  A launch that could find no sequence is left out: a batch of no more rows than sequences is taken as
     // decoding (whatever its sequences turn out to hold, the rows kernel takes all of it), one sequence by its rows.

@@ -27,6 +27,8 @@ struct PagedParams {
     int64_t above = 0, upto = 0;    // the sequences taken: above < vectors a key/value head <= upto
     float* part = nullptr;          // partial results: two slots a CTA
     int* counters = nullptr;        // one a CTA, zero between launches
+    unsigned polls = 0;             // of a wait, before it gives up
+    unsigned missing = 0;           // bytes that the copies are waited for beyond what they bring (the self-test's)
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -138,6 +140,7 @@ __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int r
 
 constexpr unsigned PA_POLL_NS = 20000;   // the longest the hardware may hold a warp at a poll
 constexpr unsigned PA_POLLS = 1u << 20;  // polls before a wait gives up (seconds)
+constexpr unsigned PA_DRAIN = 1u << 10;  // polls of a wait for what is in flight when a CTA leaves (many times its latency)
 
 // One poll of a barrier's phase; the hardware may hold the warp for up to PA_POLL_NS, issuing nothing meanwhile (polls
 // that return at once took about half of the SM's issue slots).
@@ -148,6 +151,18 @@ __device__ __forceinline__ bool try_wait(uint64_t* bar, unsigned parity) {
                  : "r"(smem_addr(bar)), "r"(parity), "r"(PA_POLL_NS)
                  : "memory");
     return ok != 0;
+}
+
+// Waits for a phase, whatever else has given up.
+__device__ __forceinline__ void drain(uint64_t* bar, unsigned parity) {
+#pragma unroll 1
+    for (unsigned i = 0; i < PA_DRAIN && !try_wait(bar, parity); ++i) {}
+}
+
+// Records a wait that gave up.  (One thread calls it as the CTA leaves: in every wait it would be code beside the loops that have to stay in the
+// instruction cache, 2309 us for 2057 over 32768 positions.)
+__device__ __forceinline__ void wait_gave_up(const PagedParams& pk) {
+    kv_flag(pk.view, Q8_KV_ERR_WAIT);
 }
 
 // ---- words and parts -------------------------------------------------------------------------------------------------

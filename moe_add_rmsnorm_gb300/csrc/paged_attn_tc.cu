@@ -86,12 +86,6 @@ struct PtShared {
     int last;
 };
 
-// Waits for a phase, whatever the other roles do.
-__device__ __forceinline__ void drain(uint64_t* bar, unsigned parity) {
-#pragma unroll 1
-    for (unsigned i = 0; i < PA_POLLS && !try_wait(bar, parity); ++i) {}
-}
-
 __device__ __forceinline__ uint64_t pk2(float a, float b) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -314,10 +308,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
     auto wait = [&](uint64_t* bar, unsigned parity) -> bool {
         bool got = try_wait(bar, parity & 1u);
 #pragma unroll 1
-        for (unsigned i = 0; !got && i < PA_POLLS && !*(volatile int*)&sh.dead; ++i) got = try_wait(bar, parity & 1u);
+        for (unsigned i = 0; !got && i < pk.polls && !*(volatile int*)&sh.dead; ++i) got = try_wait(bar, parity & 1u);
         if (__builtin_expect(__all_sync(0xffffffffu, got), 1)) return true;
         *(volatile int*)&sh.dead = 1;
-        kv_flag(kv, Q8_KV_ERR_WAIT);
         return false;
     };
     auto arrive = [&](uint64_t* bar) {  // one arrival a warp, after all its lanes
@@ -839,7 +832,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
             int row_v = 0, page_v = 0;
             auto copy = [&](int part, unsigned n, int row, int page) -> bool {  // half `part & 1` of a tile
                 if (!wait(&sh.raw_empty[part], n + 1)) return false;
-                if (lane == 0) mbar_arrive_expect_tx(&sh.raw_full[part], PT_HALF * HD);
+                if (lane == 0) mbar_arrive_expect_tx(&sh.raw_full[part], PT_HALF * HD + pk.missing);
                 __syncwarp();
                 if (lane < PT_P / 16 && lane / 4 == (part & 1))
                     tma_box(sh.raw[part] + (lane & 3) * 16 * HD, part < 2 ? &map_k : &map_v, row, page, &sh.raw_full[part]);
@@ -879,9 +872,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
             for (int part = 0; part < 4; ++part) {  // no copy is in flight when the CTA leaves
                 const unsigned n = part < 2 ? keys : values;
                 if (n) drain(&sh.raw_full[part], (n - 1) & 1);
-                // (a wait gave up: there may be one copy more, or none; a millisecond is many times a copy's latency)
-#pragma unroll 1
-                for (int i = 0; sh.dead && i < 64 && !try_wait(&sh.raw_full[part], n & 1); ++i) {}
+                if (sh.dead) drain(&sh.raw_full[part], n & 1);  // (a wait gave up: there may be one copy more, or none)
             }
         } else if (wid == 19) {
             // ================ items and scales
@@ -982,6 +973,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_tiles_kernel(const PagedP
     __syncthreads();
     tc_fence_after();
     if (wid == 17) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    if (tid == 0 && sh.dead) wait_gave_up(pk);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
