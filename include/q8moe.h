@@ -31,9 +31,9 @@
  *   - Arguments are checked before any launch.  A bad argument returns Q8_EINVAL (Q8_EUNSUPPORTED for a shape the
  *     kernels refuse, as kernel_refusal does in forward_shim.rs) and launches nothing; q8_last_error() names the
  *     argument.  A CUDA launch error returns Q8_ECUDA.  Errors raised later on the device surface at the caller's next
- *     synchronization as CUDA errors.  A bounded device-side wait that gives up (Q8_ETIMEOUT) is reported only for the
- *     decode model, by q8_model_check; a standalone call whose wait gave up leaves its outputs incomplete and reports
- *     nothing.
+ *     synchronization as CUDA errors.  A bounded device-side wait that gives up (Q8_ETIMEOUT) is reported for the
+ *     decode model by q8_model_check and for q8_paged_attention by q8_workspace_check; any other standalone call whose
+ *     wait gave up leaves its outputs incomplete and reports nothing.
  *   - Calls that take a workspace use its scratch and its arrival counters.  Calls sharing one workspace must be
  *     ordered (one stream, or events); two calls that overlap on the device through one workspace race.
  */
@@ -60,7 +60,7 @@ typedef enum {
     Q8_EINVAL = -1,       /* a null, misaligned or out-of-range argument */
     Q8_EUNSUPPORTED = -2, /* a shape the kernels refuse (cols % 32, K outside [1,32], more than 8192 experts, ...) */
     Q8_ECUDA = -3,        /* a CUDA runtime error (launch, capture, allocation at create time) */
-    Q8_ETIMEOUT = -4,     /* a bounded device-side wait gave up (reported by q8_model_check) */
+    Q8_ETIMEOUT = -4,     /* a bounded device-side wait gave up (q8_model_check, q8_workspace_check) */
     Q8_ENOSPACE = -5      /* the workspace is too small for the call */
 } q8_status;
 
@@ -98,6 +98,11 @@ typedef struct q8_ws q8_ws;
 Q8_API int q8_workspace_create(size_t bytes, q8_ws **ws);
 Q8_API void q8_workspace_destroy(q8_ws *ws);
 Q8_API size_t q8_workspace_bytes(const q8_ws *ws);
+/* Waits for `stream` and returns Q8_ETIMEOUT when a bounded wait of a q8_paged_attention on this workspace gave up: that
+ * call's outputs are incomplete, and later ones on the workspace wrote nothing, because its counters may not have been
+ * zero.  The counters are zeroed and the failure cleared, so that the workspace can be used again; no other call on it may
+ * be in flight. */
+Q8_API int q8_workspace_check(q8_ws *ws, q8_stream stream);
 
 /* ---- a1 / K4: quantisation and the residual add + RMSNorm -------------------------------------------------------- */
 
@@ -368,7 +373,8 @@ typedef struct {
 #define Q8_KV_ERR_LENGTH 1  /* rows outside the call's, or a kv_len below the sequence's rows or past the table's end */
 #define Q8_KV_ERR_PAGE 2    /* a page id outside [0, pages) */
 #define Q8_KV_ERR_ROPE 4    /* a position past the rotation tables */
-#define Q8_KV_ERR_WAIT 8    /* a bounded device-side wait gave up (the call's outputs are incomplete, and its workspace is done with) */
+#define Q8_KV_ERR_WAIT 8    /* a bounded device-side wait gave up, in this call or in an earlier one on its workspace: the outputs
+                             * are incomplete, and the workspace takes no such call until q8_workspace_check has been made */
 
 /* A batch of sequences over pages, all of it device memory that is read when the call runs (a captured graph replays with
  * what the arrays hold then).  Sequence b owns the activation rows row_start[b] .. row_start[b+1]-1 (row_start does not
@@ -430,7 +436,8 @@ Q8_API int q8_paged_attention(const q8_kv_pages *pages, const q8_kv_batch *batch
 
 /* Self-test of the bounded waits: q8_paged_attention's launches with every copy of cached words waited for 16 bytes longer
  * than it brings, so that the first waits of every CTA run out after `polls` polls (1 to 2^12) and the launches end as they
- * do when a copy is lost: no result is written, and Q8_KV_ERR_WAIT is recorded. */
+ * do when a copy is lost: no result is written, Q8_KV_ERR_WAIT is recorded, and the workspace takes no further
+ * q8_paged_attention until q8_workspace_check, which reports Q8_ETIMEOUT. */
 Q8_API int q8_paged_wait_selftest(const q8_kv_pages *pages, const q8_kv_batch *batch, int64_t rows, int64_t heads,
                                   const float *q, int64_t q_stride, float scale, float *out, int64_t out_stride, q8_ws *ws,
                                   unsigned polls, q8_stream stream);

@@ -85,6 +85,7 @@ _SIGS = {
     "q8_workspace_create": [_sz, _P(_vp)],
     "q8_workspace_destroy": [_vp],
     "q8_workspace_bytes": [_vp],
+    "q8_workspace_check": [_vp, _vp],
     "q8_quantize": [_vp, _i64, _i64, _P(q8_act), _vp],
     "add_rmsnorm_q8": [_vp, _vp, _vp, _i64, _i64, _f32, _vp, _vp, _P(q8_act), _vp],
     "q8_gemv": [_P(q8_mat), _i32, _vp, _P(q8_act), _i64, _vp, _vp, _vp],
@@ -176,6 +177,11 @@ class Workspace:
     @property
     def nbytes(self):
         return lib.q8_workspace_bytes(self.handle)
+
+    def check(self, stream=None):
+        """Waits for the stream; raises Q8_ETIMEOUT, and makes the workspace usable again, when a bounded wait of a
+        q8_paged_attention on it gave up."""
+        _check(lib.q8_workspace_check(self.handle, _stream(stream)))
 
     def close(self):
         if self.handle:
@@ -484,7 +490,7 @@ def q8_paged_attention(pages, batch, q, out, scale=None, lse=None, ws=None, stre
 
 
 def q8_paged_wait_selftest(pages, batch, q, out, polls, ws, stream=None):
-    """q8_paged_attention's launches with waits that run out after `polls` polls."""
+    """q8_paged_attention's launches with waits that run out after `polls` polls; the next ws.check() raises Q8_ETIMEOUT."""
     hd, d = pages.head_dim, _paged_device(pages, batch, q, "q")
     rows, heads = q.shape[0], q.shape[1]
     qa, qs = _rows(q, heads, hd, d, "q")

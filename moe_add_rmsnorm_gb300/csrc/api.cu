@@ -99,6 +99,7 @@ struct q8_ws {
         c.size = bytes;
         c.counters = counters;
         c.n_counters = n_counters;
+        c.failed = counters + n_counters;
         return c;
     }
 };
@@ -118,8 +119,8 @@ int q8_workspace_create(size_t bytes, q8_ws** ws) {
     w->bytes = bytes ? bytes : kDefaultScratch;
     w->n_counters = kCounters;
     cudaError_t e = cudaMalloc(&w->scratch, w->bytes);
-    if (e == cudaSuccess) e = cudaMalloc(&w->counters, w->n_counters * sizeof(int));
-    if (e == cudaSuccess) e = cudaMemset(w->counters, 0, w->n_counters * sizeof(int));
+    if (e == cudaSuccess) e = cudaMalloc(&w->counters, (w->n_counters + 1) * sizeof(int));  // (and the failure word)
+    if (e == cudaSuccess) e = cudaMemset(w->counters, 0, (w->n_counters + 1) * sizeof(int));
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
         cudaFree(w->scratch);
@@ -139,6 +140,21 @@ void q8_workspace_destroy(q8_ws* ws) {
 }
 
 size_t q8_workspace_bytes(const q8_ws* ws) { return ws ? ws->bytes : 0; }
+
+int q8_workspace_check(q8_ws* ws, q8_stream stream) {
+    g_err[0] = 0;
+    if (!ws) return fail(Q8_EINVAL, "ws: null");
+    const cudaStream_t st = (cudaStream_t)stream;
+    int v = 0;
+    cudaError_t e = cudaMemcpyAsync(&v, ws->counters + ws->n_counters, sizeof(int), cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess && v) {
+        e = cudaMemsetAsync(ws->counters, 0, (ws->n_counters + 1) * sizeof(int), st);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "q8_workspace_check");
+    return v ? fail(Q8_ETIMEOUT, "a bounded wait of a call on this workspace gave up (its outputs are incomplete)") : Q8_OK;
+}
 
 int q8_quantize(const float* x, int64_t rows, int64_t cols, const q8_act* out, q8_stream stream) {
     g_err[0] = 0;

@@ -22,6 +22,7 @@ struct Carve {
     size_t size = 0, used = 0;
     int* counters = nullptr;
     size_t n_counters = 0, used_counters = 0;
+    int* failed = nullptr;  // a workspace's: set by a launch of which a bounded wait gave up (its counters may not be zero)
     bool overflow = false;
     template <typename T>
     T* take(size_t n) {

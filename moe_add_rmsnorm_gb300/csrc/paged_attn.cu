@@ -664,6 +664,7 @@ cudaError_t launch_paged_attention(const PagedAttnCall& c, Carve& ws, cudaStream
     p.scale = (float)((double)c.scale * 1.4426950408889634);
     p.out = c.out;
     p.lse = c.lse;
+    p.failed = ws.failed;
     p.polls = c.polls ? c.polls : PA_POLLS;
     p.missing = c.missing;
     // Which kernel takes a sequence goes by its vectors a key/value head, which the device holds: up to kRowsMost the

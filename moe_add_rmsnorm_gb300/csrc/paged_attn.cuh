@@ -27,6 +27,7 @@ struct PagedParams {
     int64_t above = 0, upto = 0;    // the sequences taken: above < vectors a key/value head <= upto
     float* part = nullptr;          // partial results: two slots a CTA
     int* counters = nullptr;        // one a CTA, zero between launches
+    int* failed = nullptr;          // the workspace's failure word: a launch that finds it set does nothing
     unsigned polls = 0;             // of a wait, before it gives up
     unsigned missing = 0;           // bytes that the copies are waited for beyond what they bring (the self-test's)
 };
@@ -62,9 +63,10 @@ template <int THREADS, typename Units>
 __device__ __forceinline__ PagedRun paged_run(const PagedParams& pk, Units units) {
     __shared__ int64_t warp_sum[THREADS / 32];
     __shared__ int64_t found_at;
-    __shared__ int found;
+    __shared__ int found, failed;
     const KvView& kv = pk.view;
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+    const int was_failed = t == 0 ? *(volatile int*)pk.failed : 0;
     const int each = (kv.seqs + THREADS - 1) / THREADS;
     const int b0 = min(kv.seqs, t * each), b1 = min(kv.seqs, b0 + each);
     int64_t sum = 0;
@@ -81,7 +83,10 @@ __device__ __forceinline__ PagedRun paged_run(const PagedParams& pk, Units units
         if (lane >= o) pre += up;
     }
     if (lane == 31) warp_sum[w] = pre;
-    if (t == 0) found = 0, found_at = 0;
+    if (t == 0) {
+        found = 0, found_at = 0, failed = was_failed;
+        if (was_failed && blockIdx.x == 0) kv_flag(kv, Q8_KV_ERR_WAIT);
+    }
     __syncthreads();
     int64_t before = 0, total = 0;
 #pragma unroll 1
@@ -90,6 +95,7 @@ __device__ __forceinline__ PagedRun paged_run(const PagedParams& pk, Units units
         total += warp_sum[i];
     }
     PagedRun r;
+    if (failed) total = 0;  // (a workspace whose counters may not be zero)
     r.total = total;
     r.ctas = (int)(total < gridDim.x ? total : gridDim.x);
     if (r.ctas > 0 && (int)blockIdx.x < r.ctas) {
@@ -159,10 +165,13 @@ __device__ __forceinline__ void drain(uint64_t* bar, unsigned parity) {
     for (unsigned i = 0; i < PA_DRAIN && !try_wait(bar, parity); ++i) {}
 }
 
-// Records a wait that gave up.  (One thread calls it as the CTA leaves: in every wait it would be code beside the loops that have to stay in the
+// What a wait that gave up leaves behind, whether the caller has an error word or not: later launches on this workspace do
+// nothing (an item that several CTAs share may have been left part-way) until q8_workspace_check has cleared it.
+// (One thread calls it as the CTA leaves: in every wait it would be code beside the loops that have to stay in the
 // instruction cache, 2309 us for 2057 over 32768 positions.)
 __device__ __forceinline__ void wait_gave_up(const PagedParams& pk) {
     kv_flag(pk.view, Q8_KV_ERR_WAIT);
+    atomicOr(pk.failed, 1);
 }
 
 // ---- words and parts -------------------------------------------------------------------------------------------------

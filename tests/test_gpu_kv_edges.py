@@ -171,17 +171,29 @@ def test_the_largest_scales(q8, ws):  # noqa: F811
     ([1, 1], [900, 70], 12, 1, 128, "e4m3"), ([140], [300], 8, 2, 64, "int8"), ([2000], [4000], 32, 4, 128, "e4m3"),
     ([1, 90, 3, 1], [400, 900, 77, 3000], 8, 2, 128, "int8")])
 @pytest.mark.parametrize("polls", [1, 64])
-def test_waits_that_give_up(q8, ws, new, length, heads, kv, hd, words, polls):  # noqa: F811
-    """Copies that never complete, as far as their barriers know: the launches end, write nothing and say so."""
+def test_waits_that_give_up(q8, new, length, heads, kv, hd, words, polls):
+    """Copies that never complete, as far as their barriers know: the launches end, write nothing and say so; the workspace
+    takes no further call until it has been checked, and works as before then."""
     import torch
     c = Cache(q8, new, length, kv, hd, 16, words, 59)
     w, q = q8.Workspace(), torch.randn(sum(new), heads, hd, generator=gen(60), device="cuda")
     want, out = torch.empty_like(q), torch.full_like(q, 7.5)
-    q8.q8_paged_attention(c.pages(), c.batch(), q, want, ws=ws)
+    q8.q8_paged_attention(c.pages(), c.batch(), q, want, ws=w)
+    w.check()
     q8.q8_paged_wait_selftest(c.pages(), c.batch(), q, out, polls, w)
     torch.cuda.synchronize()
     assert (out == 7.5).all() and c.error.item() == q8.KV_ERR_WAIT
     c.error.zero_()
-    q8.q8_paged_attention(c.pages(), c.batch(), q, out, ws=ws)  # (a workspace of its own is as ever)
-    assert torch.equal(out, want) and c.error.item() == 0
+    q8.q8_paged_attention(c.pages(), c.batch(), q, out, ws=w)
+    assert (out == 7.5).all() and c.error.item() == q8.KV_ERR_WAIT
+    q8.q8_paged_attention(c.pages(), q8.kv_batch(c.row_start, c.kv_len, c.table), q, out, ws=w)  # (no error word)
+    assert (out == 7.5).all()
+    with pytest.raises(q8.Q8Error, match="Q8_ETIMEOUT"):
+        w.check()
+    w.check()  # cleared
+    c.error.zero_()
+    for _ in range(3):
+        q8.q8_paged_attention(c.pages(), c.batch(), q, out, ws=w)
+        assert torch.equal(out, want) and c.error.item() == 0
+    w.check()
     w.close()
