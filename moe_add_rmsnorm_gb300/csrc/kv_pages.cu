@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendParams pk
     const int lane = threadIdx.x & 31, sub = lane / LPV, l = lane % LPV;
     const int64_t warp = (int64_t)blockIdx.x * Q8_WARPS + (threadIdx.x >> 5);
     const int64_t r = warp / pk.groups;
+    if (kv.error && blockIdx.x == gridDim.x - 1) return kv_check(kv);
     if (r >= kv.rows) return;
     // A row's warps take its vectors in turn, so that each has its share of the keys and values, whose words cost several
     // times a query's work (a warp of keys alone held its CTA: with the rounding above, 2318 rows of 24 + 8 + 8 heads went from
@@ -131,10 +132,7 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendParams pk
     const int b = kv_find_seq(kv, r);
     if (b < 0) return;
     const KvSeq s = kv_seq(kv, b);
-    if (!s.holds(r)) {
-        if (lane == 0) kv_flag(kv, Q8_KV_ERR_LENGTH);
-        return;
-    }
+    if (!s.holds(r)) return;
     const int pos = (int)(s.len - s.n + (r - s.first));
     float c[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
     if (pk.cos_t) {
@@ -240,15 +238,13 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const ReadParams pk) {
     const int lane = threadIdx.x & 31, sub = lane / LPV, l = lane % LPV;
     const int64_t warp = (int64_t)blockIdx.x * Q8_WARPS + (threadIdx.x >> 5);
     const int64_t r = warp / pk.groups;
+    if (kv.error && blockIdx.x == gridDim.x - 1) return kv_check(kv);
     if (r >= kv.rows) return;
     const int v0 = (int)(warp % pk.groups) * (KV_READ * VPW) + sub;
     const int b = kv_find_seq(kv, r);
     if (b < 0) return;
     const KvSeq s = kv_seq(kv, b);
-    if (!s.holds(r)) {
-        if (lane == 0) kv_flag(kv, Q8_KV_ERR_LENGTH);
-        return;
-    }
+    if (!s.holds(r)) return;
     const int pos = (int)(s.len - s.n + (r - s.first));
     const int page = kv_page(kv, b, pos);
     if (page < 0) {
@@ -295,13 +291,16 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const ReadParams pk) {
     }
 }
 
-// Warps a row for `vectors` head vectors of hd values, `held` a lane group, and the CTAs of `rows` rows.
+// Warps a row for `vectors` head vectors of hd values, `held` a lane group, and the CTAs of the view's rows (and the one that
+// checks the batch).
 int warps_a_row(int vectors, int hd, int held) {
     const int each = held * (32 / (hd / 8));
     return (vectors + each - 1) / each;
 }
 
-unsigned ctas(int64_t rows, int groups) { return (unsigned)((rows * groups + Q8_WARPS - 1) / Q8_WARPS); }
+unsigned ctas(const KvView& v, int groups) {
+    return (unsigned)(((int64_t)v.rows * groups + Q8_WARPS - 1) / Q8_WARPS) + (v.error ? 1 : 0);
+}
 
 }  // namespace
 
@@ -317,7 +316,7 @@ cudaError_t launch_kv_append(const KvAppendCall& c, cudaStream_t st) {
     p.cos_t = c.cos_t, p.sin_t = c.sin_t;
     p.rope_positions = c.rope_positions;
     p.q_out = c.q_out;
-    const unsigned grid = ctas(c.view.rows, p.groups);
+    const unsigned grid = ctas(c.view, p.groups);
     if (c.hd == 128 && c.words == Q8_KV_INT8) kv_append_kernel<128, Q8_KV_INT8><<<grid, Q8_THREADS, 0, st>>>(p);
     else if (c.hd == 128) kv_append_kernel<128, Q8_KV_E4M3><<<grid, Q8_THREADS, 0, st>>>(p);
     else if (c.words == Q8_KV_INT8) kv_append_kernel<64, Q8_KV_INT8><<<grid, Q8_THREADS, 0, st>>>(p);
@@ -331,7 +330,7 @@ cudaError_t launch_kv_read(const KvReadCall& c, cudaStream_t st) {
     p.groups = warps_a_row(2 * c.view.kv, c.hd, KV_READ);
     p.k_out = c.k_out, p.v_out = c.v_out;
     p.row_stride = c.row_stride, p.head_stride = c.head_stride;
-    const unsigned grid = ctas(c.view.rows, p.groups);
+    const unsigned grid = ctas(c.view, p.groups);
     if (c.hd == 128 && c.words == Q8_KV_INT8) kv_read_kernel<128, Q8_KV_INT8><<<grid, Q8_THREADS, 0, st>>>(p);
     else if (c.hd == 128) kv_read_kernel<128, Q8_KV_E4M3><<<grid, Q8_THREADS, 0, st>>>(p);
     else if (c.words == Q8_KV_INT8) kv_read_kernel<64, Q8_KV_INT8><<<grid, Q8_THREADS, 0, st>>>(p);

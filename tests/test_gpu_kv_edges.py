@@ -197,3 +197,21 @@ def test_waits_that_give_up(q8, new, length, heads, kv, hd, words, polls):
         assert torch.equal(out, want) and c.error.item() == 0
     w.check()
     w.close()
+
+
+@pytest.mark.parametrize("starts,lens", [([0, 9, 20], [9, 30]), ([0, 9, 9, 30], [9, 0, 30]), ([0, 9, 12], [9, 30]),
+                                         ([-3, 0, 9], [9, 30]), ([0, 9] + [9] * 300 + [20], [9] + [5] * 300 + [30])])
+def test_a_sequence_with_no_row_of_the_call_is_recorded(q8, ws, starts, lens):  # noqa: F811
+    """Its rows are skipped by every call, and the error word says so, although no row of the call leads to it."""
+    import torch
+    rows, seqs = 9, len(lens)
+    c = Cache(q8, [0] * seqs, lens, 2, 128, 16, "int8", 53)
+    c.row_start.copy_(torch.tensor(starts, dtype=torch.int32))
+    k = torch.randn(rows, 2, 128, generator=gen(54), device="cuda")
+    q = torch.randn(rows, 8, 128, generator=gen(55), device="cuda")
+    back, out = torch.empty_like(k), torch.empty_like(q)
+    for call in (lambda: q8.q8_kv_append(c.pages(), c.batch(), q, k, k, out), lambda: q8.q8_kv_read(c.pages(), c.batch(), back),
+                 lambda: q8.q8_paged_attention(c.pages(), c.batch(), q, out, ws=ws)):
+        c.error.zero_()
+        call()
+        assert c.error.item() == q8.KV_ERR_LENGTH
