@@ -54,13 +54,13 @@ KV_ERR_LENGTH, KV_ERR_PAGE, KV_ERR_ROPE, KV_ERR_WAIT = 1, 2, 4, 8  # bits of a b
 
 
 class q8_kv_pages(ctypes.Structure):
-    device = None  # the tensors' (kv_pages sets it; None: the caller's business)
+    device = tensors = None  # the tensors behind it (kv_pages sets them; None: the caller's business)
     _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "ks", "vs")] + [
         (n, ctypes.c_int64) for n in ("pages", "page_size", "kv_heads", "head_dim")] + [("words", ctypes.c_int)]
 
 
 class q8_kv_batch(ctypes.Structure):
-    device = None
+    device = tensors = None
     _fields_ = [(n, ctypes.c_void_p) for n in ("row_start", "kv_len", "table")] + [
         (n, ctypes.c_int64) for n in ("seqs", "table_pages", "table_stride")] + [("error", ctypes.c_void_p)]
 
@@ -365,7 +365,7 @@ def _vec(t, n, device, name):
 
 def kv_pages(k, ks, v, vs) -> q8_kv_pages:
     """Pages over device tensors: words k and v [pages, kv_heads, page_size, head_dim] (int8 or float8_e4m3fn), scales ks
-    and vs f32 [pages, kv_heads, page_size].  The tensors must outlive the struct."""
+    and vs f32 [pages, kv_heads, page_size].  The struct keeps the tensors."""
     torch = _lazy_torch()
     kind, shape = k.dtype, k.shape
     if kind is torch.int8:
@@ -386,13 +386,13 @@ def kv_pages(k, ks, v, vs) -> q8_kv_pages:
         _refuse("pages: not all on the current device")
     p = q8_kv_pages(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape[0], shape[2], shape[1], shape[3],
                     words)
-    p.device = d
+    p.device, p.tensors = d, (k, ks, v, vs)
     return p
 
 
 def kv_batch(row_start, kv_len, table, error=None) -> q8_kv_batch:
     """A batch of sequences over pages (q8moe.h, q8_kv_batch): device int32 row_start [seqs + 1], kv_len [seqs] and table
-    [seqs, pages], and optionally an int32 error word.  The tensors must outlive the struct."""
+    [seqs, pages], and optionally an int32 error word.  The struct keeps the tensors."""
     i32 = _lazy_torch().int32
     shape = table.shape
     if len(shape) != 2 or kv_len.dim() != 1 or row_start.dim() != 1:
@@ -415,7 +415,7 @@ def kv_batch(row_start, kv_len, table, error=None) -> q8_kv_batch:
         e = error.data_ptr()
     b = q8_kv_batch(row_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), seqs, pages,
                     strides[0] if seqs > 1 else pages, e)
-    b.device = d
+    b.device, b.tensors = d, (row_start, kv_len, table, error)
     return b
 
 

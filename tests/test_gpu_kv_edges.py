@@ -215,3 +215,19 @@ def test_a_sequence_with_no_row_of_the_call_is_recorded(q8, ws, starts, lens):  
         c.error.zero_()
         call()
         assert c.error.item() == q8.KV_ERR_LENGTH
+
+
+def test_pages_and_batches_keep_their_tensors(q8):
+    """The structs hold addresses: the tensors behind them live as long as they do."""
+    import gc
+    import weakref
+    c = Cache(q8, [1], [5], 1, 64, 16, "int8", 56)
+    made = [t.clone() for t in (c.kw, c.ks, c.vw, c.vs, c.row_start, c.kv_len, c.table, c.error)]
+    refs = [weakref.ref(t) for t in made]
+    pages, batch = q8.kv_pages(*made[:4]), q8.kv_batch(*made[4:])
+    del made
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    del pages, batch
+    gc.collect()
+    assert all(r() is None for r in refs)
