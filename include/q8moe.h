@@ -427,7 +427,8 @@ Q8_API int q8_kv_read(const q8_kv_pages *pages, const q8_kv_batch *batch, int64_
  *     out = sum_{t<=p} e^{scale q.k_t - m} v_t / sum_{t<=p} e^{scale q.k_t - m}     (m the largest score)
  *     lse = m + log sum_{t<=p} e^{scale q.k_t - m}                                (device f32 [rows][heads], or NULL)
  * q and out are device f32, rows q_stride and out_stride values apart, heads of a row consecutive, 16-byte aligned,
- * strides multiples of 4; out must not overlap q.  Sequences of one row and of many run in the same call, and the work
+ * strides multiples of 4; out's rows must not overlap q's (columns of one buffer are fine where its rows are equally far apart
+ * in both).  Sequences of one row and of many run in the same call, and the work
  * is divided over the GPU by what the device arrays hold.  A row with no position left gets zeros and an lse of
  * -infinity.  ws holds the partial results of sequences that several CTAs share (at most 26 MiB). */
 Q8_API int q8_paged_attention(const q8_kv_pages *pages, const q8_kv_batch *batch, int64_t rows, int64_t heads,

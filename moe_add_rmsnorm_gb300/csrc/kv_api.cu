@@ -78,6 +78,21 @@ int check_rows(const float* x, int64_t stride, int64_t width, int64_t rows, cons
     return Q8_OK;
 }
 
+// Rows of one buffer written while those of another are read: q8_paged_attention's out and q.  Columns of one buffer, the same
+// distance apart, are rows that lie between one another's.
+int check_apart(const float* x, int64_t x_stride, int64_t x_width, const char* x_name, const float* y, int64_t y_stride,
+                int64_t y_width, const char* y_name, int64_t rows) {
+    if (rows == 0) return Q8_OK;
+    const int64_t xs = (rows - 1) * x_stride + x_width, ys = (rows - 1) * y_stride + y_width;
+    const uintptr_t xa = (uintptr_t)x, ya = (uintptr_t)y;
+    if (xa + 4 * (uint64_t)xs <= ya || ya + 4 * (uint64_t)ys <= xa) return Q8_OK;
+    if (rows > 1 && x_stride == y_stride) {  // (both addresses are multiples of 16)
+        const int64_t d = ((int64_t)(ya - xa) / 4 % x_stride + x_stride) % x_stride;
+        if (d >= x_width && d + y_width <= x_stride) return Q8_OK;
+    }
+    return model_fail(Q8_EINVAL, "%s: overlaps %s", x_name, y_name);
+}
+
 int done(cudaError_t e, const char* what) {
     return e == cudaSuccess ? Q8_OK : model_fail(Q8_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
@@ -168,6 +183,8 @@ static int attention(PagedAttnCall& c, const q8_kv_pages* pages, const q8_kv_bat
     if (int r = check_rows(q, q_stride, heads * pages->head_dim, rows, "q")) return r;
     if (int r = check_rows(out, out_stride, heads * pages->head_dim, rows, "out")) return r;
     if (q == out && rows != 0) return model_fail(Q8_EINVAL, "out: q itself");
+    const int64_t width = heads * pages->head_dim;
+    if (int r = check_apart(out, out_stride, width, "out", q, q_stride, width, "q", rows)) return r;
     if (!aligned(lse, 4)) return model_fail(Q8_EINVAL, "lse: not 4-byte aligned");
     if (!(scale > 0.f) || scale > 1e30f) return model_fail(Q8_EINVAL, "scale: not positive and finite");
     if (!ws) return model_fail(Q8_EINVAL, "ws: null");
