@@ -406,7 +406,8 @@ Q8_API int q8_rope_table(double theta, int64_t positions, int64_t head_dim, floa
  *     y = x / sqrt(mean(x^2) + eps) * w          (w = q_norm or k_norm, device f32 [head_dim]; NULL: y = x)
  *     z_i = y_i c_i - y_{i+h} s_i,  z_{i+h} = y_i s_i + y_{i+h} c_i    (h = head_dim/2; c, s the row's position's table
  *                                                 rows, rope_positions of them; both tables NULL: z = y)
- * Queries go to q_out (device f32, rows q_out_stride apart; may be q itself); keys z and values v are quantized into
+ * Queries go to q_out (device f32, rows q_out_stride apart; may be q itself, equally far apart; its rows must not overlap
+ * q's, k's or v's otherwise, columns of one buffer whose rows are equally far apart aside); keys z and values v are quantized into
  * their page slots.  The keys' z is formed to about 2^-44 and rounded to f32 once, so that the words follow the formula.
  * A row past the rotation tables is skipped (Q8_KV_ERR_ROPE).  Two rows must not share a slot.  Addresses are 16-byte
  * aligned and strides multiples of 4. */

@@ -78,7 +78,8 @@ int check_rows(const float* x, int64_t stride, int64_t width, int64_t rows, cons
     return Q8_OK;
 }
 
-// Rows of one buffer written while those of another are read: q8_paged_attention's out and q.  Columns of one buffer, the same
+// Rows of one buffer written while those of another are read: q8_paged_attention's out and q, q8_kv_append's q_out and what
+// it reads.  Columns of one buffer, the same
 // distance apart, are rows that lie between one another's.
 int check_apart(const float* x, int64_t x_stride, int64_t x_width, const char* x_name, const float* y, int64_t y_stride,
                 int64_t y_width, const char* y_name, int64_t rows) {
@@ -138,6 +139,13 @@ int q8_kv_append(const q8_kv_pages* pages, const q8_kv_batch* batch, int64_t row
     if (!aligned(cos, 16) || !aligned(sin, 16)) return model_fail(Q8_EINVAL, "cos or sin: not 16-byte aligned");
     if (cos && rope_positions < 1) return model_fail(Q8_EINVAL, "rope_positions %lld", (long long)rope_positions);
     if (rows == 0 || batch->seqs == 0) return Q8_OK;
+    if (heads) {
+        const int64_t qw = heads * hd, kw = kv * hd;
+        if (q_out != q || (rows > 1 && q_out_stride != q_stride))
+            if (int r = check_apart(q_out, q_out_stride, qw, "q_out", q, q_stride, qw, "q", rows)) return r;
+        if (int r = check_apart(q_out, q_out_stride, qw, "q_out", k, k_stride, kw, "k", rows)) return r;
+        if (int r = check_apart(q_out, q_out_stride, qw, "q_out", v, v_stride, kw, "v", rows)) return r;
+    }
     c.hd = (int)hd;
     c.heads = (int)heads;
     c.words = (int)pages->words;

@@ -10,7 +10,7 @@ import math
 
 import pytest
 
-from test_gpu_kv_pages import Cache, gen, ws  # noqa: F401  (ws: a fixture)
+from test_gpu_kv_pages import Cache, gen, rope, ws  # noqa: F401  (ws: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -231,3 +231,21 @@ def test_pages_and_batches_keep_their_tensors(q8):
     del pages, batch
     gc.collect()
     assert all(r() is None for r in refs)
+
+
+def test_append_into_columns_of_one_buffer(q8):
+    """The queries' places among what is read: q itself, and columns beside q, k and v in one buffer."""
+    import torch
+    c = Cache(q8, [3, 2], [20, 2], 2, 128, 16, "int8", 61, fill=False)
+    cos, sin = rope(q8, 32, 128)
+    wide = torch.randn(5, 12 + 8, 128, generator=gen(62), device="cuda")
+    want = torch.empty(5, 8, 128, device="cuda")
+    q, k, v, beside = wide[:, :8], wide[:, 8:10], wide[:, 10:12], wide[:, 12:]
+    q8.q8_kv_append(c.pages(), c.batch(), q, k, v, want, cos=cos, sin=sin)
+    q8.q8_kv_append(c.pages(), c.batch(), q, k, v, beside, cos=cos, sin=sin)
+    assert torch.equal(beside, want)
+    q8.q8_kv_append(c.pages(), c.batch(), q, k, v, q, cos=cos, sin=sin)
+    assert torch.equal(q, want)
+    for bad in (wide[:, 4:12], wide[:, 9:17], wide[:, 3:11]):
+        with pytest.raises(q8.Q8Error, match="q_out: overlaps"):
+            q8.q8_kv_append(c.pages(), c.batch(), q, k, v, bad, cos=cos, sin=sin)

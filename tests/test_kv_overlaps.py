@@ -27,3 +27,17 @@ def test_attention_out_over_q(q8, change):  # noqa: F811
     dict(rows=1, qs=0, os=4, out=A + 512 * 4), dict(qs=2048, os=1024, out=B)])
 def test_attention_out_beside_q(q8, change):  # noqa: F811
     assert ok(attend, q8, **change)
+
+
+# one merged projection of rows 1024 values apart: 4 query heads, 2 key and 2 value heads of 128
+MERGED = dict(qs=1024, ks=1024, vs=1024, q=A, k=A + 512 * 4, v=A + 768 * 4)
+
+
+@pytest.mark.parametrize("change,name", [
+    (dict(out=A, os=1024), "q"), (dict(out=A + 16), "q"), (dict(qs=520, out=A), "q"), (dict(k=B, out=B), "k"),
+    (dict(v=B, out=B + 1024), "v"), (dict(MERGED, out=A + 256 * 4, os=1024), "q"), (dict(MERGED, out=A + 512 * 4, os=1024), "k"),
+    (dict(MERGED, k=B, out=A + 512 * 4, os=1024), "v"), (dict(MERGED, out=A, os=512), "q"), (dict(rows=1, out=A + 16), "q")])
+def test_append_q_out_over_its_inputs(q8, change, name):  # noqa: F811
+    change = dict(dict(q=A, k=4 * B, v=5 * B, out=6 * B), **change)
+    assert append(q8, **change) == -1
+    assert f"q_out: overlaps {name}" in q8.last_error()
