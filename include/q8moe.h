@@ -418,7 +418,8 @@ Q8_API int q8_kv_append(const q8_kv_pages *pages, const q8_kv_batch *batch, int6
 
 /* The inverse: word * d of the keys and values of the batch's rows (the last row_start[b+1] - row_start[b] positions of
  * sequence b; all of them where it owns kv_len[b] rows), into k_out and v_out (device f32, either may be NULL, 32-byte
- * aligned), value i of head g of row r at r*row_stride + g*head_stride + i (strides multiples of 8).  A dense cache
+ * aligned), value i of head g of row r at r*row_stride + g*head_stride + i (strides multiples of 8).  No two of those
+ * vectors may overlap.  A dense cache
  * [kv_heads][ctx][head_dim] is row_stride head_dim and head_stride ctx*head_dim. */
 Q8_API int q8_kv_read(const q8_kv_pages *pages, const q8_kv_batch *batch, int64_t rows, float *k_out, float *v_out,
                       int64_t row_stride, int64_t head_stride, q8_stream stream);

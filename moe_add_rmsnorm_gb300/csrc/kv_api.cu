@@ -94,6 +94,21 @@ int check_apart(const float* x, int64_t x_stride, int64_t x_width, const char* x
     return model_fail(Q8_EINVAL, "%s: overlaps %s", x_name, y_name);
 }
 
+// Whether two vectors of hd values lie over one another among rows x heads of them at r*rs + h*hs and the same ones `at` values
+// on (at 0: any two different ones).  Exact: for each distance between heads only the two nearest between rows can do it.
+bool vectors_meet(int64_t at, int64_t rows, int64_t rs, int64_t heads, int64_t hs, int64_t hd) {
+    for (int64_t dh = 1 - heads; dh < heads; ++dh) {
+        const int64_t d = at + dh * hs;  // to be undone by -dr * rs, to within hd - 1
+        const int64_t near = rows > 1 ? d / rs : 0;
+        for (int64_t dr = near - 1; dr <= near + 1; ++dr) {
+            if (dr <= -rows || dr >= rows || (at == 0 && dh == 0 && dr == 0)) continue;
+            const int64_t left = d - dr * rs;
+            if (left > -hd && left < hd) return true;
+        }
+    }
+    return false;
+}
+
 int done(cudaError_t e, const char* what) {
     return e == cudaSuccess ? Q8_OK : model_fail(Q8_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
@@ -172,6 +187,20 @@ int q8_kv_read(const q8_kv_pages* pages, const q8_kv_batch* batch, int64_t rows,
                           (long long)head_stride, (long long)hd);
     if (row_stride > (int64_t(1) << 36) || head_stride > (int64_t(1) << 36))
         return model_fail(Q8_EUNSUPPORTED, "k_out, v_out: strides of more than 2^36");
+    if (rows > 0) {
+        // Rows within heads or heads within rows, as dense layouts are, is the quick answer.
+        const int64_t kv = pages->kv_heads, span = (rows - 1) * row_stride + (kv - 1) * head_stride + hd;
+        const bool nested = (rows == 1 || row_stride >= (kv - 1) * head_stride + hd) || (kv == 1 || head_stride >= (rows - 1) * row_stride + hd);
+        if (!nested && vectors_meet(0, rows, row_stride, kv, head_stride, hd))
+            return model_fail(Q8_EINVAL, "k_out, v_out: rows %lld and heads %lld apart overlap", (long long)row_stride,
+                              (long long)head_stride);
+        if (k_out && v_out && batch->seqs > 0) {
+            const uintptr_t a = (uintptr_t)k_out, b = (uintptr_t)v_out;
+            if (a < b + 4 * (uint64_t)span && b < a + 4 * (uint64_t)span &&
+                (a == b || vectors_meet((int64_t)(b - a) / 4, rows, row_stride, kv, head_stride, hd)))
+                return model_fail(Q8_EINVAL, "v_out: overlaps k_out");
+        }
+    }
     if (rows == 0 || batch->seqs == 0) return Q8_OK;
     c.hd = (int)hd;
     c.words = (int)pages->words;

@@ -249,3 +249,32 @@ def test_append_into_columns_of_one_buffer(q8):
     for bad in (wide[:, 4:12], wide[:, 9:17], wide[:, 3:11]):
         with pytest.raises(q8.Q8Error, match="q_out: overlaps"):
             q8.q8_kv_append(c.pages(), c.batch(), q, k, v, bad, cos=cos, sin=sin)
+
+
+@pytest.mark.parametrize("kv,hd", [(1, 64), (3, 64), (2, 128)])
+def test_read_into_layouts_of_one_buffer(q8, kv, hd):
+    """Keys and values side by side in one buffer, in several orders, and layouts that overlap."""
+    import torch
+    n = 21
+    c = Cache(q8, [n], [40], kv, hd, 16, "int8", 63)
+    k, v = (torch.empty(n, kv, hd, device="cuda") for _ in range(2))
+    q8.q8_kv_read(c.pages(), c.batch(), k, v)
+    for shape, at in (((n, 2, kv, hd), lambda t, i: t[:, i]), ((2, n, kv, hd), lambda t, i: t[i]),
+                      ((kv, 2, n + 3, hd), lambda t, i: t[:, i, :n].transpose(0, 1)),
+                      ((kv, n, 2, hd), lambda t, i: t[:, :, i].transpose(0, 1)),
+                      ((n, kv, 2 * hd + 8), lambda t, i: t[:, :, i * hd:(i + 1) * hd]),
+                      ((2, kv, n + 5, hd + 8), lambda t, i: t[i, :, 5:, 8:].transpose(0, 1))):
+        t = torch.full(shape, 7.5, device="cuda")
+        kept = torch.ones(shape, dtype=torch.bool, device="cuda")
+        at(kept, 0)[:] = False
+        at(kept, 1)[:] = False
+        q8.q8_kv_read(c.pages(), c.batch(), at(t, 0), at(t, 1))
+        assert torch.equal(at(t, 0), k) and torch.equal(at(t, 1), v) and (t[kept] == 7.5).all()
+    t = torch.zeros(4 * n * kv * hd, device="cuda")
+    with pytest.raises(q8.Q8Error, match="overlap"):
+        q8.q8_kv_read(c.pages(), c.batch(), k, k)
+    with pytest.raises(q8.Q8Error, match="overlap"):
+        q8.q8_kv_read(c.pages(), c.batch(), t[:n * kv * hd].view(n, kv, hd), t[hd - 8:n * kv * hd + hd - 8].view(n, kv, hd))
+    if kv > 1:
+        with pytest.raises(q8.Q8Error, match="overlap"):  # heads within one another's rows
+            q8.q8_kv_read(c.pages(), c.batch(), t.as_strided((n, kv, hd), (hd, hd, 1)))

@@ -3,7 +3,7 @@ call that would go on to a launch has no sequences)."""
 import pytest
 
 from test_kv_empty import NONE
-from test_kv_refusals import A, append, attend, batch, q8, read  # noqa: F401  (q8: a fixture)
+from test_kv_refusals import A, append, attend, batch, pages, q8, read  # noqa: F401  (q8: a fixture)
 
 B = 1 << 20  # far from A
 
@@ -41,3 +41,30 @@ def test_append_q_out_over_its_inputs(q8, change, name):  # noqa: F811
     change = dict(dict(q=A, k=4 * B, v=5 * B, out=6 * B), **change)
     assert append(q8, **change) == -1
     assert f"q_out: overlaps {name}" in q8.last_error()
+
+
+def meet(at, rows, rs, heads, hs, hd):
+    """Whether two of the vectors of hd values at r rs + h hs, and (with `at` given) those `at` values on, share a value."""
+    a = sorted(r * rs + h * hs for r in range(rows) for h in range(heads))
+    if at is None:
+        return any(y - x < hd for x, y in zip(a, a[1:]))
+    return any(abs(x - y - at) < hd for x in a for y in a)
+
+
+@pytest.mark.parametrize("hd,kv", [(64, 1), (64, 3), (128, 2), (128, 5)])
+def test_read_outputs(q8, hd, kv):  # noqa: F811
+    """A layout of rows and heads whose vectors share a value is refused, and no other; so is a v_out over k_out."""
+    pg = pages(q8, head_dim=hd, kv_heads=kv)
+    for rows in (1, 2, 5):
+        for rs in {hd, hd + 8, 2 * hd, 3 * hd, kv * hd, kv * hd + 8, 2 * kv * hd}:
+            for hs in {hd, hd + 8, 2 * hd, 3 * hd + 16, rows * hd, rows * hd + 8, rows * rs, 2 * rows * hd}:
+                bad = meet(None, rows, rs, kv, hs, hd)
+                assert read(q8, pg=pg, bt=batch(q8, **NONE), rows=rows, k=B, v=None, rs=rs, hs=hs) == (-1 if bad else 0)
+                if bad:
+                    assert "overlap" in q8.last_error()
+                    continue
+                for at in {0, 8, hd - 8, hd, hd + 8, 2 * hd, kv * hd, rows * hd, rows * rs, rows * rs + kv * hs}:
+                    for sign in (1, -1):  # (the other layouts go on to a launch: taken on real tensors, on a GPU)
+                        if meet(sign * at, rows, rs, kv, hs, hd):
+                            assert read(q8, pg=pg, rows=rows, k=B, v=B + 4 * sign * at, rs=rs, hs=hs) == -1
+                            assert "overlap" in q8.last_error()
