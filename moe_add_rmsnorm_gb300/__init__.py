@@ -173,6 +173,7 @@ class Workspace:
         h = ctypes.c_void_p()
         _check(lib.q8_workspace_create(nbytes, ctypes.byref(h)))
         self.handle = h
+        self.device = _lazy_torch().cuda.current_device()
 
     @property
     def nbytes(self):
@@ -427,6 +428,15 @@ def _paged_device(pages, batch, t, name):
     return d
 
 
+def _ws_of(ws, device):
+    """The handle of a call's workspace, which has to be of its device."""
+    if ws is None:
+        return None
+    if ws.device != device:
+        _refuse("ws: not on the current device")
+    return ws.handle
+
+
 def q8_rope_table(theta, cos, sin, stream=None):
     """Fills cos and sin (device f32 [positions, head_dim/2]) with the rotation tables of base theta."""
     n, half = cos.shape
@@ -486,7 +496,7 @@ def q8_paged_attention(pages, batch, q, out, scale=None, lse=None, ws=None, stre
     if out.shape[0] != rows:
         _refuse("out: rows differ")
     _check(lib.q8_paged_attention(pages, batch, rows, heads, qa, qs, hd ** -0.5 if scale is None else scale, oa, os_,
-                                  _vec(lse, rows * heads, d, "lse"), ws.handle if ws else None, _stream_of(stream, d)))
+                                  _vec(lse, rows * heads, d, "lse"), _ws_of(ws, d), _stream_of(stream, d)))
 
 
 def q8_paged_wait_selftest(pages, batch, q, out, polls, ws, stream=None):
@@ -495,7 +505,7 @@ def q8_paged_wait_selftest(pages, batch, q, out, polls, ws, stream=None):
     rows, heads = q.shape[0], q.shape[1]
     qa, qs = _rows(q, heads, hd, d, "q")
     oa, os_ = _rows(out, heads, hd, d, "out")
-    _check(lib.q8_paged_wait_selftest(pages, batch, rows, heads, qa, qs, hd ** -0.5, oa, os_, ws.handle, int(polls),
+    _check(lib.q8_paged_wait_selftest(pages, batch, rows, heads, qa, qs, hd ** -0.5, oa, os_, _ws_of(ws, d), int(polls),
                                       _stream_of(stream, d)))
 
 

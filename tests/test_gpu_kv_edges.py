@@ -278,3 +278,22 @@ def test_read_into_layouts_of_one_buffer(q8, kv, hd):
     if kv > 1:
         with pytest.raises(q8.Q8Error, match="overlap"):  # heads within one another's rows
             q8.q8_kv_read(c.pages(), c.batch(), t.as_strided((n, kv, hd), (hd, hd, 1)))
+
+
+def test_a_workspace_of_another_device_is_refused(q8):
+    import torch
+    c = Cache(q8, [1], [5], 1, 64, 16, "int8", 64)
+    q = torch.ones(1, 1, 64, device="cuda")
+    w = q8.Workspace()
+    assert w.device == torch.cuda.current_device()
+    w.device += 1
+    for call in (lambda: q8.q8_paged_attention(c.pages(), c.batch(), q, torch.empty_like(q), ws=w),
+                 lambda: q8.q8_paged_wait_selftest(c.pages(), c.batch(), q, torch.empty_like(q), 64, w)):
+        with pytest.raises(q8.Q8Error, match="ws: not on the current device"):
+            call()
+    w.close()
+    with pytest.raises(q8.Q8Error, match="ws: null"):
+        q8.q8_paged_attention(c.pages(), c.batch(), q, torch.empty_like(q))
+    with pytest.raises(q8.Q8Error, match="ws: null"):  # closed
+        w.device -= 1
+        q8.q8_paged_attention(c.pages(), c.batch(), q, torch.empty_like(q), ws=w)
