@@ -406,9 +406,11 @@ Q8_API int q8_rope_table(double theta, int64_t positions, int64_t head_dim, floa
  *     y = x / sqrt(mean(x^2) + eps) * w          (w = q_norm or k_norm, device f32 [head_dim]; NULL: y = x)
  *     z_i = y_i c_i - y_{i+h} s_i,  z_{i+h} = y_i s_i + y_{i+h} c_i    (h = head_dim/2; c, s the row's position's table
  *                                                 rows, rope_positions of them; both tables NULL: z = y)
- * Queries go to q_out (device f32, rows q_out_stride apart; may be q itself, equally far apart; its rows must not overlap
- * q's, k's or v's otherwise, columns of one buffer whose rows are equally far apart aside); keys z and values v are quantized into
+ * Queries go to q_out (device f32, rows q_out_stride apart): q itself with q's stride, or rows that overlap none of q's, k's
+ * and v's (columns of one buffer are fine where its rows are equally far apart); keys z and values v are quantized into
  * their page slots.  The keys' z is formed to about 2^-44 and rounded to f32 once, so that the words follow the formula.
+ * The squares are added up in f32's range, as in add_rmsnorm_q8: a normed head has to keep them below 2^127 (values of
+ * 10^18), beyond which its queries come out as zeros and its keys as not finite, and above 2^-80 where eps is smaller still.
  * A row past the rotation tables is skipped (Q8_KV_ERR_ROPE).  Two rows must not share a slot.  Addresses are 16-byte
  * aligned and strides multiples of 4. */
 Q8_API int q8_kv_append(const q8_kv_pages *pages, const q8_kv_batch *batch, int64_t rows, int64_t heads, const float *q,

@@ -10,7 +10,7 @@ import math
 
 import pytest
 
-from test_gpu_kv_pages import Cache, gen, rope, ws  # noqa: F401  (ws: a fixture)
+from test_gpu_kv_pages import Cache, gen, quantize, rope, ws  # noqa: F401  (ws: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -297,3 +297,37 @@ def test_a_workspace_of_another_device_is_refused(q8):
     with pytest.raises(q8.Q8Error, match="ws: null"):  # closed
         w.device -= 1
         q8.q8_paged_attention(c.pages(), c.batch(), q, torch.empty_like(q), ws=w)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("words", ["int8", "e4m3"])
+@pytest.mark.parametrize("eps", [1e-6, 0.0])
+def test_rows_at_the_ends_of_the_norms_range(q8, hd, words, eps):
+    """Rows whose squares add up to little less than f32's largest number, and, without eps, to 2^-72."""
+    import torch
+    n = 4
+    c = Cache(q8, [n], [n], 2, hd, 16, words, 57, fill=False)
+    g = gen(58)
+    size = torch.tensor([1.0, 1e12, 1e18, 1e-3 if eps else 1e-12], device="cuda")[:, None, None]
+    q, k = (torch.randn(n, h, hd, generator=g, device="cuda") * size for h in (4, 2))
+    w = 1 + 0.1 * torch.randn(hd, generator=g, device="cuda")
+    cos, sin = rope(q8, n, hd)
+    out = torch.empty_like(q)
+    q8.q8_kv_append(c.pages(), c.batch(), q, k, torch.ones_like(k), out, q_norm=w, k_norm=w, eps=eps, cos=cos, sin=sin)
+
+    eps32 = torch.tensor(eps, dtype=torch.float32).item()  # (what the call takes: 2.5e-9 from 1e-6, which turns last bits of f32)
+
+    def turned(x):
+        x = x.double()
+        x = x * torch.rsqrt(x.square().mean(-1, keepdim=True) + eps32) * w.double()
+        a, b = x.chunk(2, -1)
+        cs, sn = cos.double()[:, None], sin.double()[:, None]
+        return torch.cat((a * cs - b * sn, a * sn + b * cs), -1)
+
+    z = turned(q)
+    lim = z.abs() + z.roll(hd // 2, -1).abs()
+    assert ((out.double() - z).abs() <= 20 * 2 ** -24 * lim).all()
+    qx, d = quantize(turned(k).float(), words)
+    a, o = c.where(0, torch.arange(n, device="cuda"))
+    assert torch.equal(c.ks[a, :, o], d)
+    assert torch.equal(c.kw.view(torch.int8)[a, :, o].view(c.kw.dtype).float(), qx.float())
