@@ -355,6 +355,20 @@ def _rows(t, heads, hd, device, name):
     return t.data_ptr(), stride[0] if shape[0] > 1 else heads * hd
 
 
+def _matrix(t, name):
+    """A table of two dimensions (its values are checked by _vec)."""
+    if t.dim() != 2:
+        _refuse(f"{name}: {tuple(t.shape)}, expected [positions, head_dim/2]")
+    return t.shape
+
+
+def _heads_of(t, name):
+    """The heads of rows [rows, heads, hd] (the rest of them is checked by _rows)."""
+    if t.dim() != 3:
+        _refuse(f"{name}: {tuple(t.shape)}, expected [rows, heads, head_dim]")
+    return t.shape[1]
+
+
 def _vec(t, n, device, name):
     """The address of a contiguous device f32 tensor of n values (None: NULL)."""
     if t is None:
@@ -439,7 +453,7 @@ def _ws_of(ws, device):
 
 def q8_rope_table(theta, cos, sin, stream=None):
     """Fills cos and sin (device f32 [positions, head_dim/2]) with the rotation tables of base theta."""
-    n, half = cos.shape
+    n, half = _matrix(cos, "cos")
     d = _device(cos, "cos")
     _check(lib.q8_rope_table(float(theta), n, 2 * half, _vec(cos, n * half, d, "cos"), _vec(sin, n * half, d, "sin"),
                              _stream_of(stream, d)))
@@ -449,19 +463,20 @@ def q8_kv_append(pages, batch, q, k, v, q_out, q_norm=None, k_norm=None, eps=1e-
     """Norms and rotates the rows' query and key heads (q [rows, heads, hd] into q_out; k, v [rows, kv_heads, hd]) and
     quantizes the keys and values into their page slots.  q and q_out may be None (keys and values only)."""
     kv, hd = pages.kv_heads, pages.head_dim
-    rows, d = k.shape[0], _paged_device(pages, batch, k, "k")
+    d = _paged_device(pages, batch, k, "k")
+    ka, ks = _rows(k, kv, hd, d, "k")
+    va, vs = _rows(v, kv, hd, d, "v")
+    rows = k.shape[0]
     if v.shape[0] != rows or (q is None) != (q_out is None):
         _refuse("q, k, v, q_out: rows differ")
     heads, qa, qs, oa, os_ = 0, None, 0, None, 0
     if q is not None:
-        heads = q.shape[1]
-        if q.shape[0] != rows or q_out.shape[0] != rows:
-            _refuse("q, k, v, q_out: rows differ")
+        heads = _heads_of(q, "q")
         qa, qs = _rows(q, heads, hd, d, "q")
         oa, os_ = _rows(q_out, heads, hd, d, "q_out")
-    ka, ks = _rows(k, kv, hd, d, "k")
-    va, vs = _rows(v, kv, hd, d, "v")
-    positions = cos.shape[0] if cos is not None else 0
+        if q.shape[0] != rows or q_out.shape[0] != rows:
+            _refuse("q, k, v, q_out: rows differ")
+    positions = _matrix(cos, "cos")[0] if cos is not None else 0
     _check(lib.q8_kv_append(pages, batch, rows, heads, qa, qs, ka, ks, va, vs, _vec(q_norm, hd, d, "q_norm"),
                             _vec(k_norm, hd, d, "k_norm"), eps, _vec(cos, positions * hd // 2, d, "cos"),
                             _vec(sin, positions * hd // 2, d, "sin"), positions, oa, os_, _stream_of(stream, d)))
@@ -490,7 +505,7 @@ def q8_paged_attention(pages, batch, q, out, scale=None, lse=None, ws=None, stre
     """Causal attention of the rows q [rows, heads, hd] over their sequences' cached positions, into out; scale defaults
     to hd^-1/2, lse (optional) is f32 [rows, heads]."""
     hd, d = pages.head_dim, _paged_device(pages, batch, q, "q")
-    rows, heads = q.shape[0], q.shape[1]
+    heads, rows = _heads_of(q, "q"), q.shape[0]
     qa, qs = _rows(q, heads, hd, d, "q")
     oa, os_ = _rows(out, heads, hd, d, "out")
     if out.shape[0] != rows:
@@ -502,9 +517,11 @@ def q8_paged_attention(pages, batch, q, out, scale=None, lse=None, ws=None, stre
 def q8_paged_wait_selftest(pages, batch, q, out, polls, ws, stream=None):
     """q8_paged_attention's launches with waits that run out after `polls` polls; the next ws.check() raises Q8_ETIMEOUT."""
     hd, d = pages.head_dim, _paged_device(pages, batch, q, "q")
-    rows, heads = q.shape[0], q.shape[1]
+    heads, rows = _heads_of(q, "q"), q.shape[0]
     qa, qs = _rows(q, heads, hd, d, "q")
     oa, os_ = _rows(out, heads, hd, d, "out")
+    if out.shape[0] != rows:
+        _refuse("out: rows differ")
     _check(lib.q8_paged_wait_selftest(pages, batch, rows, heads, qa, qs, hd ** -0.5, oa, os_, _ws_of(ws, d), int(polls),
                                       _stream_of(stream, d)))
 

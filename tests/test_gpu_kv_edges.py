@@ -331,3 +331,32 @@ def test_rows_at_the_ends_of_the_norms_range(q8, hd, words, eps):
     a, o = c.where(0, torch.arange(n, device="cuda"))
     assert torch.equal(c.ks[a, :, o], d)
     assert torch.equal(c.kw.view(torch.int8)[a, :, o].view(c.kw.dtype).float(), qx.float())
+
+
+def test_binding_refuses_tensors_of_other_dimensions(q8, ws):  # noqa: F811
+    """With a Q8Error that names the tensor, whatever its number of dimensions."""
+    import torch
+    c = Cache(q8, [2], [5], 2, 64, 16, "int8", 65)
+    p, b, x = c.pages(), c.batch(), torch.ones(2, 2, 64, device="cuda")
+    o, t = torch.empty_like(x), torch.ones(8, 32, device="cuda")
+    for bad in (x.view(-1), x.view(2, 128), x[0, 0, 0], x.view(1, 2, 2, 64), x.view(2, 4, 32), x[:, :, ::2], x.double(),
+                x.cpu(), x[:1].expand(2, 2, 64)):
+        for call, name in ((lambda: q8.q8_kv_append(p, b, bad, x, x, o), "q"), (lambda: q8.q8_kv_append(p, b, x, bad, x, o), "k"),
+                           (lambda: q8.q8_kv_append(p, b, x, x, bad, o), "v"), (lambda: q8.q8_kv_append(p, b, x, x, x, bad), "q_out"),
+                           (lambda: q8.q8_paged_attention(p, b, bad, o, ws=ws), "q"),
+                           (lambda: q8.q8_paged_attention(p, b, x, bad, ws=ws), "out"),
+                           (lambda: q8.q8_paged_wait_selftest(p, b, x, bad, 64, ws), "out"),
+                           (lambda: q8.q8_kv_read(p, b, bad), "k_out")):
+            with pytest.raises(q8.Q8Error, match=rf"\b{name}\b"):
+                call()
+    for bad in (t.view(-1), t[0, 0], t.view(8, 1, 32), t[:, :16]):
+        with pytest.raises(q8.Q8Error):
+            q8.q8_kv_append(p, b, x, x, x, o, cos=bad, sin=t)
+        with pytest.raises(q8.Q8Error):
+            q8.q8_rope_table(1e6, bad, t)
+    with pytest.raises(q8.Q8Error):
+        q8.q8_kv_append(p, b, x, x, x, o, cos=t, sin=None)
+    for rows in (1, 3):
+        with pytest.raises(q8.Q8Error, match="rows differ"):
+            q8.q8_paged_wait_selftest(p, b, x, torch.empty(rows, 2, 64, device="cuda"), 64, ws)
+    assert c.error.item() == 0
