@@ -320,10 +320,17 @@ def _refuse(msg):
     raise Q8Error(-1, msg)
 
 
+_current_device = None
+
+
 def _device(t, name):
-    """The device of tensor t, which has to be the current one."""
+    """The device of tensor t, which has to be the current one (a CUDA tensor's torch has been initialised: the device is
+    asked for without that check where this torch has a call for it)."""
+    global _current_device
+    if _current_device is None:
+        _current_device = getattr(_lazy_torch()._C, "_cuda_getDevice", None) or _lazy_torch().cuda.current_device
     d = t.get_device()
-    if d < 0 or d != _lazy_torch().cuda.current_device():
+    if d < 0 or d != _current_device():
         _refuse(f"{name}: not on the current device")
     return d
 
