@@ -37,10 +37,13 @@ __device__ __forceinline__ void kv_flag(const KvView& p, int bit) {
 // Records a batch's sequences whose rows are not the call's or whose length is out of range, whether a row of the call leads
 // to them or not: for a CTA of 256 threads of its own, beside those that take the rows (launched where there is an error word).
 __device__ __forceinline__ void kv_check(const KvView& p) {
-    for (int b = threadIdx.x; b < p.seqs; b += Q8_THREADS) {
+    bool bad = false;
+#pragma unroll 4
+    for (int b = threadIdx.x; b < p.seqs; b += Q8_THREADS) {  // (without the flag inside: several loads at once)
         const KvSeq s = kv_seq(p, b);
-        if (!s.rows_ok || (s.n > 0 && !s.len_ok)) kv_flag(p, Q8_KV_ERR_LENGTH);
+        bad |= !s.rows_ok || (s.n > 0 && !s.len_ok);
     }
+    if (bad) kv_flag(p, Q8_KV_ERR_LENGTH);
 }
 
 // The sequence row r belongs to, or -1 (all lanes of a warp call it with the same r).  A 32-way search for the last b

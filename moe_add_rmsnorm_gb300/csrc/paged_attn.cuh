@@ -215,7 +215,8 @@ __device__ __forceinline__ unsigned finite_bits(float x) {
 
 // Weights are scaled by the largest value scale of the positions taken together, and split into two f16 parts.  A row of which
 // the mask hides that one, and which sees none within 2^PA_SPREAD of it, scales its own weights up further, so that what it
-// does not see costs it no bits.  (Within that spread its weights of 1 lie at 2^6 or above, and an f16 part resolves 2^-24.)
+// does not see, up to 2^100 times what it does, costs it no bits.  (Within that spread its weights of 1 lie at 2^6 or above,
+// and an f16 part resolves 2^-24.)
 constexpr int PA_SPREAD = 8;
 
 cudaError_t launch_paged_rows(const PagedParams& p, int hd, int words, int tiles, cudaStream_t st);
