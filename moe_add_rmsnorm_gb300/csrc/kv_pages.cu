@@ -8,8 +8,8 @@
 // queries and 1 KiB of words out).  A warp takes one row's group of head vectors; LPV lanes hold a vector, each lane two
 // float4 (dims 4l.. of either half), so both elements of every rotation pair sit in one lane and the row's sums are
 // shuffles among LPV lanes.  All of a warp's loads are issued before the row's sequence and page are looked up (a chain
-// of three dependent loads), which hides that chain behind them.  Measured: 2318 rows of 24 + 8 + 8 heads of 128 in 23.9 us
-// (3.4 TB/s; the exact keys and the words' rounding issue more than the bytes cost), 34182 rows of 8 heads of 64 read back
+// of three dependent loads), which hides that chain behind them.  Measured: 2318 rows of 24 + 8 + 8 heads of 128 in 24.3 us
+// (3.4 TB/s at 60% of the issue slots: all keys are turned in pairs of f32, though the words next to a border alone need it), 34182 rows of 8 heads of 64 read back
 // in 32.7 us (5.4 TB/s, the memory's: a copy runs at 6.8).
 #include <cuda_fp16.h>
 
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendParams pk
     if (r >= kv.rows) return;
     // A row's warps take its vectors in turn, so that each has its share of the keys and values, whose words cost several
     // times a query's work (a warp of keys alone held its CTA: with the rounding above, 2318 rows of 24 + 8 + 8 heads went from
-    // 35.8 to 25.0 us; four CTAs an SM, by 64 registers for 76, to 23.9).
+    // 35.8 to 25.0 us; four CTAs an SM, by 64 registers for 76, to 23.9, now 24.3).
     const int v0 = (int)(warp % pk.groups) * VPW + sub, step = pk.groups * VPW, nvec = pk.heads + 2 * kv.kv;
     float x[KV_ITERS][8];
 #pragma unroll

@@ -25,9 +25,11 @@
 //    128-position units over the whole batch.  The warps' results meet in shared memory; an item that several CTAs share
 //    meets in the workspace, folded in order by the last to arrive.
 //
-// What bounds it: instruction issue.  A step is 580 warp instructions on 4224 bytes (over a third turn bytes into pairs of
-// f16, the rest are the products, the softmax and the splits); 64 sequences of 4096 (62 us, 4.5 TB/s) issue 0.55 a clock.
-// 64 ragged ones of up to 4096 take 45.0 us (3.4 TB/s), one of 100003 39.2 (2.7 TB/s).
+// What holds it back: a step's own chain (words, scores, maximum, exponentials, transposes, products), which 16 warps an SM
+// do not hide.  A step is 610 warp instructions on 4224 bytes (over a third turn bytes into pairs of f16, the rest are the
+// products, the softmax and the splits); 64 sequences of 4096 (66 us, 4.2 TB/s) use 57% of the issue slots and 55% of the
+// memory's rate, and the stalls that lead are fixed latencies (wait) and other warps' turns (not selected).  64 ragged
+// ones of up to 4096 take 45.2 us (3.4 TB/s), one of 100003 38.6 (2.7 TB/s).
 #include <cuda_fp16.h>
 
 #include "paged_attn.cuh"
@@ -39,7 +41,8 @@ namespace {
 constexpr int PR_WARPS = 8, PR_THREADS = PR_WARPS * 32;
 constexpr int PR_UNIT = 128;   // positions a unit
 // What an item's start and end cost, in units (64 ragged sequences of up to 4096, one row each: 49.3 us with 0, 47.1 with 1,
-// 45.0 with 2, 45.4 with 4, 50.8 with 8; 33 of up to 8885, 3 rows of heads of 64: 61.4, 59.2, 57.4, 55.2, 56.5).
+// 45.0 with 2, 45.4 with 4, 50.8 with 8; 33 of up to 8885, 3 rows of heads of 64: 61.4, 59.2, 57.4, 55.2, 56.5; in the
+// present form, with 2, 3 and 4, 45.8, 45.2 and 47.1, and 58.2, 56.8 and 55.4).
 constexpr int PR_START = 3;
 constexpr int PR_STEP = 16;    // positions a warp takes at a time
 constexpr int PR_FLUSH = 8;    // steps between additions to the totals
@@ -669,7 +672,9 @@ cudaError_t launch_paged_attention(const PagedAttnCall& c, Carve& ws, cudaStream
     p.missing = c.missing;
     // Which kernel takes a sequence goes by its vectors a key/value head, which the device holds: up to kRowsMost the
     // rows kernel.  A launch that could find no sequence is left out: a batch of no more rows than sequences is taken as
-    // decoding (whatever its sequences turn out to hold, the rows kernel takes all of it), one sequence by its rows.
+    // decoding (whatever its sequences turn out to hold, the rows kernel takes all of it), one sequence by its rows.  (A
+    // prompt in a batch of mostly empty sequences, 32 heads over 4: 60 rows over 1000 positions in a batch of 60 27 us, and
+    // 62 as the only sequence, by the tiles kernel; 500 rows over 4000 in a batch of 500 386, and 115.)
     const int64_t most = c.view.seqs == 1 ? (int64_t)c.view.rows * p.group : c.view.rows > c.view.seqs ? INT64_MAX : p.group;
     const bool rows = p.group <= kRowsMost && (c.view.seqs > 1 || most <= kRowsMost);
     const bool tiles = most > kRowsMost;

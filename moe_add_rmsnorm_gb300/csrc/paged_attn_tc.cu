@@ -20,12 +20,14 @@
 //    rows, zeros for pages out of range), warp 19 deals out the items and prepares the scales.
 // Registers are moved to the warps that hold the output sums (80, 80, 184, 80 and 56 a thread).
 //
-// What bounds it: 2048 rows over 32768 positions (32 heads over 4 of 128) take 2.05 ms, 519 TFLOP/s of the formula and 1038
-// issued (a library bf16 product: 1932).  The weights' arithmetic takes half of the issue slots and the tensor pipe
-// works 40 to 50% of the time.  An item's start and end (queries into parts, masks, the sums written out or folded) are
-// 12 us or so of a CTA's time, most of it instruction fetch of code that runs once an item, so the roles' code is kept in
-// loops; prompts of 483 to 1749 rows (4465 in all) take 252 us.  Queries in tensor memory and a tile's weights in halves
-// by two groups at once took 7% more over long caches and 60% more for prompts.
+// What holds it back: 2048 rows over 32768 positions (32 heads over 4 of 128) take 1.97 ms, 542 TFLOP/s of the formula and
+// 1084 issued (a library bf16 product: 1932).  Neither the tensor pipe (39% of the time, 512 rows over 16384) nor the issue
+// slots (52%) are full: the two softmax groups hand the maximum from tile to tile, and each score is read from tensor memory
+// twice.  Between items the pipeline drains: the next item's scores wait until the last product is issued, and the next
+// product until the sums have gone through tensor memory and out.  Prompts of 483 to 1749 rows (4465 in all, 42 tile pairs
+// and 7.4 items a CTA) take 255 us, of which the pairs, at the long cache's 2.35 us, are 99; the tensor pipe works 21% of it.
+// The roles' code is kept in loops, because it has to stay within the instruction cache.  Queries in tensor memory and a
+// tile's weights in halves by two groups at once took 7% more over long caches and 60% more for prompts.
 #include <cuda_fp16.h>
 
 #include "paged_attn.cuh"
@@ -40,7 +42,7 @@ constexpr int PT_THREADS = 640;
 constexpr int PT_HALF = 64;                // positions a copied stage
 constexpr int PT_ITEMS = 4;                // items dealt out ahead
 constexpr int PT_READERS = 18;             // warps that read an item
-// What an item's start and end cost, in tiles (12 us or so, mostly instruction fetch): runs that leave it out give a CTA of
+// What an item's start and end cost, in tiles (the pipeline drains and fills): runs that leave it out give a CTA of
 // short items several times the work of one of long ones (4465 rows of 4 prompts 341 us with 0, 260 with 2, 251 with 4, 262
 // with 6, 267 with 8; 24 sequences of 1 to 300 rows 128, 112, 113, 114, 114).
 constexpr int PT_START = 4;
