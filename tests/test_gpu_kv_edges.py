@@ -360,3 +360,18 @@ def test_binding_refuses_tensors_of_other_dimensions(q8, ws):  # noqa: F811
         with pytest.raises(q8.Q8Error, match="rows differ"):
             q8.q8_paged_wait_selftest(p, b, x, torch.empty(rows, 2, 64, device="cuda"), 64, ws)
     assert c.error.item() == 0
+
+
+@pytest.mark.parametrize("new,length", [([1, 1], [400, 70]), ([60, 1], [200, 33])])
+def test_attention_into_columns_beside_the_queries(q8, ws, new, length):  # noqa: F811
+    import torch
+    c = Cache(q8, new, length, 2, 128, 16, "int8", 66)
+    wide = torch.randn(sum(new), 20, 128, generator=gen(67), device="cuda")
+    q, want = wide[:, 4:12], torch.empty(sum(new), 8, 128, device="cuda")
+    q8.q8_paged_attention(c.pages(), c.batch(), q, want, ws=ws)
+    kept = wide.clone()
+    q8.q8_paged_attention(c.pages(), c.batch(), q, wide[:, 12:], ws=ws)
+    assert torch.equal(wide[:, 12:], want) and torch.equal(wide[:, :12], kept[:, :12])
+    for bad in (wide[:, 5:13], wide[:, 11:19], q):
+        with pytest.raises(q8.Q8Error, match="out"):
+            q8.q8_paged_attention(c.pages(), c.batch(), q, bad, ws=ws)

@@ -1,5 +1,5 @@
-"""Host-side refusals of overlapping buffers in the paged key/value cache's calls (no GPU: the addresses are never used; a
-call that would go on to a launch has no sequences)."""
+"""Host-side refusals of overlapping buffers in the paged key/value cache's calls (no GPU: the addresses are never used, for
+every call is refused or has no sequences; layouts that are taken run on real tensors in test_gpu_kv_edges.py)."""
 import pytest
 
 from test_kv_empty import NONE
