@@ -447,6 +447,86 @@ Q8_API int q8_paged_wait_selftest(const q8_kv_pages *pages, const q8_kv_batch *b
                                   const float *q, int64_t q_stride, float scale, float *out, int64_t out_stride, q8_ws *ws,
                                   unsigned polls, q8_stream stream);
 
+/* ---- a feed-forward block with 4-bit weights --------------------------------------------------------------------------
+ * The pages' mixture keeps Q8_0 weights, one softmax router and one norm a block (kernel_refusal's Moe arms refuse the
+ * rest), so the format and the calls below are this library's, in the order a layer makes them: the norms around the block,
+ * the scored router, projections and the experts' products with 4-bit weights.  A call with no rows does nothing. */
+
+/* Norm after a block, its gate and residual scale, the residual add, and the norm before the next block, in one pass.  For
+ * each of `rows` rows of d values (device f32; d at most 16384):
+ *     p = b / sqrt(mean(b^2) + eps) * w_post              (w_post NULL: p = b)
+ *     s = a + scale * g p                                 (one rounding)                        -> sum_out (or NULL)
+ *     y = s / sqrt(mean(s^2) + eps) * w_pre               (of the rounded s; one rounding)      -> y_out (or NULL)
+ *     yq = quantize(y)                                                                          -> yq (or NULL)
+ * a is the residual, b the block's output, w_post and w_pre device f32 [d].  gate (device f32, or NULL for g = 1) is read at
+ * gate[r * gate_row_stride + i * gate_stride] for value i of row r: [d] is (0, 1), [rows] is (1, 0), [rows][d] is (d, 1).
+ * yq as in add_rmsnorm_q8 (d % 32 == 0; the two-word form when yq->lo is not NULL).  At least one output must be given;
+ * sum_out and y_out may each be a or b itself, but no output may otherwise overlap an input or another output.  Norms and
+ * products are carried to about 2^-44 up to the stated roundings, the squares added up in f32's range, as in q8_kv_append. */
+Q8_API int postnorm_add_rmsnorm_q8(const float *a, const float *b, const float *w_post, const float *w_pre, const float *gate,
+                                   int64_t gate_row_stride, int64_t gate_stride, float scale, int64_t rows, int64_t d,
+                                   float eps, float *sum_out, float *y_out, const q8_act *yq, q8_stream stream);
+
+typedef enum { Q8_SCORE_SOFTMAX = 0, Q8_SCORE_SIGMOID = 1 } q8_score;
+
+/* How moe_route_scored chooses and weighs. */
+typedef struct {
+    q8_score score;      /* p = softmax of the row's logits, or the sigmoid of each */
+    const float *bias;   /* device f32 [experts], added to p for the choice alone, or NULL */
+    int groups;          /* experts stand in `groups` equal groups of consecutive ones (1: no groups; at most 32) */
+    int keep_groups;     /* the groups that experts are chosen from (1 to groups) */
+    int group_top;       /* a group's mark: the sum of its 1 or 2 largest p + bias */
+    int renorm;          /* 1: the kept p are divided by their sum; 0: they are not */
+    float scale;         /* multiplies the gates */
+} q8_route_rule;
+
+/* Router scores to experts: for each row of logits (device f32, `experts` values, rows `stride` values apart):
+ *     c = p + bias; the keep_groups groups of the largest marks; among their experts the k of the largest c, in descending
+ *     order -> ids [rows][k];  gates[j] = scale * p_j (/ sum of the kept p when renorm) -> gates [rows][k]
+ * Equal marks or c take the lower index first.  The order is that of p + bias in 64 bits (of the logits themselves without a
+ * bias).  A logit of -infinity or NaN takes its expert out of service for the row, as does a bias of -infinity or NaN: it is
+ * chosen only when no other is left in the kept groups (the lowest index first), has a gate of 0, and adds nothing to a
+ * group's mark; a group of none but such ranks last.  +infinity counts as f32's largest value.  A row without an expert in
+ * service has gates of 0.  experts at most 1024, k at most 32 and at most the experts of keep_groups groups.  plan (or
+ * NULL) is filled as by moe_route_topk (rows * k at most 2^24); ws is needed with it. */
+Q8_API int moe_route_scored(const float *logits, int64_t stride, int64_t rows, int64_t experts, const q8_route_rule *rule,
+                            int k, int32_t *ids, float *gates, const q8_moe_plan *plan, q8_ws *ws, q8_stream stream);
+
+typedef enum { Q4_SCALE_F16 = 0, Q4_SCALE_BF16 = 1 } q4_scale;
+
+/* A device matrix of 4-bit words, with a 16-bit scale and (or not) a zero point for every `group` consecutive columns:
+ *     W[o][t] = s[o*(cols/group) + t/group] * (word(o, t) - z[o*(cols/group) + t/group])       (z NULL: 8 everywhere)
+ * q is [rows][cols/2] bytes, 16-byte aligned, byte i of a row holding value 2i in its low half and 2i + 1 in its high one;
+ * s is 2-byte aligned.  group is 32, 64 or 128 and divides cols; cols at most 32768. */
+typedef struct {
+    const uint8_t *q;
+    const void *s;    /* [rows][cols/group] of scale_type */
+    const uint8_t *z; /* [rows][cols/group] or NULL */
+    int64_t rows, cols, group;
+    q4_scale scale_type;
+} q4_mat;
+
+/* y[r][o] = sum_t W[o][t] x[r][t] for `rows` activation rows, x either f32 (rows x_stride values apart, 16-byte aligned, the
+ * stride a multiple of 4) or, with x NULL, the quantized form xq (dense; the two-word form when xq->lo is not NULL).  y is
+ * device f32, rows y_stride values apart, and overlaps no input.  Sums are f32: of f32 activations in two f16 parts, which
+ * carry 2^-22 of each 32-value block's largest value, and of exact integer block sums for quantized ones.  Calls of one row
+ * need no workspace. */
+Q8_API int q4_gemv(const q4_mat *W, const float *x, int64_t x_stride, const q8_act *xq, int64_t rows, float *y,
+                   int64_t y_stride, q8_ws *ws, q8_stream stream);
+
+/* moe_gate_up with 4-bit weights: h[r][j][i] = silu(Wg[e*dff+i] . x_r) * (Wu[e*dff+i] . x_r), e = ids[r][j], gate and up
+ * stacked [E*dff, d] alike, x or xq as in q4_gemv (dense rows).  plan (from moe_route_scored or moe_route_topk over the same
+ * ids) is required when rows > 1.  The hidden row of an id outside [0, E) is left as it was. */
+Q8_API int moe_gate_up_q4(const q4_mat *gate, const q4_mat *up, int64_t dff, const float *x, const q8_act *xq, int64_t rows,
+                          int k, const int32_t *ids, const q8_moe_plan *plan, float *h, q8_ws *ws, q8_stream stream);
+
+/* moe_down_combine with 4-bit weights: y[r] = residual[r] + sum_j gates[r][j] (Wd[e*d .. e*d+d) . h[r][j]), the sum over j
+ * in order, down stacked [E*d, dff], the hidden rows h ([rows*k][dff]) or hq.  residual may be NULL, and may be y itself.
+ * plan as above.  An id outside [0, E) adds nothing.  ws holds the choices' outputs of several rows. */
+Q8_API int moe_down_combine_q4(const q4_mat *down, int64_t d, const float *h, const q8_act *hq, int64_t rows, int k,
+                               const int32_t *ids, const float *gates, const q8_moe_plan *plan, const float *residual,
+                               float *y, q8_ws *ws, q8_stream stream);
+
 /* ---- errors --------------------------------------------------------------------------------------------------- */
 /* The text of the calling thread's last error (empty when none); valid until the thread's next call. */
 Q8_API const char *q8_last_error(void);

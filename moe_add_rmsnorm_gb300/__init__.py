@@ -65,6 +65,21 @@ class q8_kv_batch(ctypes.Structure):
         (n, ctypes.c_int64) for n in ("seqs", "table_pages", "table_stride")] + [("error", ctypes.c_void_p)]
 
 
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1  # moe_route_scored: how logits become scores
+Q4_F16, Q4_BF16 = 0, 1  # a 4-bit matrix's scales
+
+
+class q8_route_rule(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int), ("bias", ctypes.c_void_p)] + [
+        (n, ctypes.c_int) for n in ("groups", "keep_groups", "group_top", "renorm")] + [("scale", ctypes.c_float)]
+
+
+class q4_matrix(ctypes.Structure):  # q4_mat in q8moe.h; built by q4_mat()
+    device = tensors = None
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "s", "z")] + [
+        (n, ctypes.c_int64) for n in ("rows", "cols", "group")] + [("scale_type", ctypes.c_int)]
+
+
 class q8_model_desc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("layers", "d", "heads", "kv_heads", "head_dim", "experts", "k", "dff",
                                                 "vocab", "ctx")] + [
@@ -110,6 +125,11 @@ _SIGS = {
     "q8_paged_attention": [_P(q8_kv_pages), _P(q8_kv_batch), _i64, _i64, _vp, _i64, _f32, _vp, _i64, _vp, _vp, _vp],
     "q8_paged_wait_selftest": [_P(q8_kv_pages), _P(q8_kv_batch), _i64, _i64, _vp, _i64, _f32, _vp, _i64, _vp, ctypes.c_uint,
                                _vp],
+    "postnorm_add_rmsnorm_q8": [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _f32, _i64, _i64, _f32, _vp, _vp, _P(q8_act), _vp],
+    "moe_route_scored": [_vp, _i64, _i64, _i64, _P(q8_route_rule), _i32, _vp, _vp, _P(q8_moe_plan), _vp, _vp],
+    "q4_gemv": [_P(q4_matrix), _vp, _i64, _P(q8_act), _i64, _vp, _i64, _vp, _vp],
+    "moe_gate_up_q4": [_P(q4_matrix), _P(q4_matrix), _i64, _vp, _P(q8_act), _i64, _i32, _vp, _P(q8_moe_plan), _vp, _vp, _vp],
+    "moe_down_combine_q4": [_P(q4_matrix), _i64, _vp, _P(q8_act), _i64, _i32, _vp, _vp, _P(q8_moe_plan), _vp, _vp, _vp, _vp],
     "q8_model_create": [_P(q8_model_desc), _P(_vp)],
     "q8_model_destroy": [_vp],
     "decode_step": [_vp, _vp],
@@ -531,6 +551,181 @@ def q8_paged_wait_selftest(pages, batch, q, out, polls, ws, stream=None):
         _refuse("out: rows differ")
     _check(lib.q8_paged_wait_selftest(pages, batch, rows, heads, qa, qs, hd ** -0.5, oa, os_, _ws_of(ws, d), int(polls),
                                       _stream_of(stream, d)))
+
+
+def _tensor(t, kind, shape, device, name):
+    """The address of a contiguous tensor of this type, shape and device (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not kind or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        _refuse(f"{name}: not a contiguous {kind} tensor {tuple(shape)} on the current device")
+    return t.data_ptr()
+
+
+def _words(q, s, lo, rows, cols, device, name):
+    """A quantized activation of rows x cols values."""
+    i8 = _torch.int8
+    if q is None or s is None:
+        _refuse(f"{name}: words without scales, or scales without words")
+    if cols % 32:
+        _refuse(f"{name}: {cols} values a row, not whole 32-value blocks")
+    for t, kind, n in ((q, i8, rows * cols), (lo, i8, rows * cols), (s, _torch.float32, rows * cols // 32)):
+        if t is not None and (t.dtype is not kind or t.numel() != n or t.get_device() != device or not t.is_contiguous()):
+            _refuse(f"{name}: not contiguous int8 words [{rows}, {cols}] and f32 scales of every 32 on the current device")
+    return q8_act(q.data_ptr(), s.data_ptr(), lo.data_ptr() if lo is not None else None)
+
+
+def _matrix_rows(t, cols, device, name):
+    """The address, rows and row stride of f32 rows [rows, cols] (or one row [cols]) whose values are consecutive."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not _torch.float32 or t.get_device() != device:
+        _refuse(f"{name}: not an f32 tensor of the current device")
+    if len(shape) not in (1, 2) or shape[-1] != cols or (cols > 1 and stride[-1] != 1):
+        _refuse(f"{name}: {tuple(shape)}, expected [rows, {cols}] with consecutive values")
+    if len(shape) == 1:
+        return t.data_ptr(), 1, cols
+    return t.data_ptr(), shape[0], stride[0] if shape[0] > 1 else cols
+
+
+def postnorm_add_rmsnorm_q8(a, b, w_post, w_pre, eps, gate=None, scale=1.0, sum_out=None, y_out=None, yq=None, ys=None,
+                            yl=None, stream=None):
+    """s = a + scale * gate * norm(b) * w_post into sum_out; y = norm(s) * w_pre into y_out and, quantized, into yq, ys (and
+    yl).  a and b are [rows, d]; gate is [d], [rows, 1] or [rows, d], or None; w_post may be None (b as it is)."""
+    dev, shape = _device(a, "a"), a.shape
+    f32, d = _torch.float32, shape[-1] if a.dim() else 0
+    if len(shape) not in (1, 2):
+        _refuse(f"a: {tuple(shape)}, expected [rows, d]")
+    rows = shape[0] if len(shape) == 2 else 1
+    ga, gr, gc = None, 0, 0
+    if gate is not None:
+        if gate.dtype is not f32 or gate.get_device() != dev:
+            _refuse("gate: not an f32 tensor of the current device")
+        g = gate.shape
+        if len(g) == 1 and g[0] == d:
+            gc = gate.stride(0) if d > 1 else 0
+        elif len(g) == 2 and g[0] in (1, rows) and g[1] in (1, d):
+            gr, gc = (st if n > 1 else 0 for n, st in zip(g, gate.stride()))
+        else:
+            _refuse(f"gate: {tuple(g)}, expected [{d}], [{rows}, 1] or [{rows}, {d}]")
+        ga = gate.data_ptr()
+    act_ = ctypes.byref(_words(yq, ys, yl, rows, d, dev, "yq")) if yq is not None or ys is not None else None
+    _check(lib.postnorm_add_rmsnorm_q8(
+        _tensor(a, f32, shape, dev, "a"), _tensor(b, f32, shape, dev, "b"), _vec(w_post, d, dev, "w_post"),
+        _vec(w_pre, d, dev, "w_pre"), ga, gr, gc, scale, rows, d, eps, _tensor(sum_out, f32, shape, dev, "sum_out"),
+        _tensor(y_out, f32, shape, dev, "y_out"), act_, _stream_of(stream, dev)))
+
+
+def _plan_ref(plan):
+    return ctypes.byref(plan) if plan is not None else None
+
+
+def _choices(ids, device):
+    """The rows and choices a row of ids int32 [rows, k] (or [k])."""
+    shape = ids.shape
+    if len(shape) not in (1, 2) or ids.dtype is not _torch.int32 or ids.get_device() != device or not ids.is_contiguous():
+        _refuse("ids: not contiguous int32 [rows, k] on the current device")
+    return (shape[0] if len(shape) == 2 else 1), shape[-1]
+
+
+def moe_route_scored(logits, ids, gates, score=SCORE_SOFTMAX, bias=None, groups=1, keep_groups=1, group_top=2, renorm=True,
+                     scale=1.0, plan=None, ws=None, stream=None):
+    """Scores (SCORE_SOFTMAX or SCORE_SIGMOID) of logits [rows, experts], the choice of ids.shape[-1] experts a row by score
+    + bias among the keep_groups best groups, into ids (int32) and gates, and the grouping by expert into plan."""
+    d = _device(logits, "logits")
+    E = logits.shape[-1] if logits.dim() else 0
+    la, rows, stride = _matrix_rows(logits, E, d, "logits")
+    n, k = _choices(ids, d)
+    if n != rows:
+        _refuse("ids: rows differ")
+    rule = q8_route_rule(score, _vec(bias, E, d, "bias"), groups, keep_groups, group_top, 1 if renorm else 0, scale)
+    _check(lib.moe_route_scored(la, stride, rows, E, rule, k, ids.data_ptr(),
+                                _tensor(gates, _torch.float32, ids.shape, d, "gates"), _plan_ref(plan), _ws_of(ws, d),
+                                _stream_of(stream, d)))
+
+
+def q4_mat(q, s, z=None) -> q4_matrix:
+    """A matrix of 4-bit words: q uint8 [rows, cols / 2], scales s float16 or bfloat16 [rows, cols / group], zero points z
+    uint8 of s's shape (None: 8).  The struct keeps the tensors."""
+    torch = _lazy_torch()
+    if q.dim() != 2 or s.dim() != 2 or q.dtype is not torch.uint8:
+        _refuse("q, s: expected uint8 [rows, cols / 2] and scales [rows, cols / group]")
+    if s.dtype is not torch.float16 and s.dtype is not torch.bfloat16:
+        _refuse("s: not float16 or bfloat16")
+    rows, cols, groups = q.shape[0], 2 * q.shape[1], s.shape[1]
+    if s.shape[0] != rows or groups < 1 or cols % groups:
+        _refuse(f"s: {tuple(s.shape)} scales for {rows} x {cols} values")
+    if z is not None and (z.dtype is not torch.uint8 or z.shape != s.shape):
+        _refuse("z: not uint8 of the scales' shape")
+    d = _device(q, "q")
+    for t in (q, s, z):
+        if t is not None and (t.get_device() != d or not t.is_contiguous()):
+            _refuse("q, s, z: not contiguous, or not all on the current device")
+    m = q4_matrix(q.data_ptr(), s.data_ptr(), z.data_ptr() if z is not None else None, rows, cols, cols // groups,
+                  Q4_F16 if s.dtype is torch.float16 else Q4_BF16)
+    m.device, m.tensors = d, (q, s, z)
+    return m
+
+
+def _q4_device(t, name, *mats):
+    """The device of a call's tensor t, which has to be the current one and the matrices'."""
+    d = _device(t, name)
+    for m in mats:
+        if m.device not in (d, None):
+            _refuse("matrix: not on the current device")
+    return d
+
+
+def _q4_act(x, xq, xs, xl, rows, cols, device, name):
+    """A product's activation: the address and row stride of f32 rows, or the quantized form."""
+    if x is not None:
+        if xq is not None or xs is not None or xl is not None:
+            _refuse(f"{name}: given as values and as words")
+        xa, n, stride = _matrix_rows(x, cols, device, name)
+        if n != rows:
+            _refuse(f"{name}: rows differ")
+        return xa, stride, None
+    return None, 0, ctypes.byref(_words(xq, xs, xl, rows, cols, device, name))
+
+
+def q4_gemv(W, y, x=None, xq=None, xs=None, xl=None, ws=None, stream=None):
+    """y [rows, W.rows] = W x for x f32 [rows, W.cols], or its quantized form xq, xs (and xl)."""
+    d = _q4_device(y, "y", W)
+    ya, rows, y_stride = _matrix_rows(y, W.rows, d, "y")
+    xa, stride, qa = _q4_act(x, xq, xs, xl, rows, W.cols, d, "x")
+    _check(lib.q4_gemv(W, xa, stride, qa, rows, ya, y_stride, _ws_of(ws, d), _stream_of(stream, d)))
+
+
+def moe_gate_up_q4(gate, up, ids, h, x=None, xq=None, xs=None, xl=None, plan=None, ws=None, stream=None):
+    """h [rows, k, dff] = silu(gate x) * (up x) of the experts ids [rows, k], x f32 [rows, d] or its quantized form."""
+    d = _q4_device(h, "h", gate, up)
+    rows, k = _choices(ids, d)
+    dff = h.shape[-1] if h.dim() else 0
+    if h.dtype is not _torch.float32 or h.numel() != rows * k * dff or not h.is_contiguous():
+        _refuse(f"h: not contiguous f32 [{rows}, {k}, dff]")
+    xa, stride, qa = _q4_act(x, xq, xs, xl, rows, gate.cols, d, "x")
+    if rows > 1 and stride not in (0, gate.cols):
+        _refuse("x: not contiguous")
+    _check(lib.moe_gate_up_q4(gate, up, dff, xa, qa, rows, k, ids.data_ptr(), _plan_ref(plan), h.data_ptr(), _ws_of(ws, d),
+                              _stream_of(stream, d)))
+
+
+def moe_down_combine_q4(down, ids, gates, y, h=None, hq=None, hs=None, hl=None, plan=None, residual=None, ws=None,
+                        stream=None):
+    """y [rows, d] = residual + sum_j gates[:, j] * (down h_j) of the experts ids [rows, k], h f32 [rows, k, dff] or its
+    quantized form."""
+    dev, f32 = _q4_device(y, "y", down), _torch.float32
+    rows, k = _choices(ids, dev)
+    d = y.shape[-1] if y.dim() else 0
+    if y.dtype is not f32 or y.numel() != rows * d or not y.is_contiguous():
+        _refuse(f"y: not contiguous f32 [{rows}, d]")
+    if h is not None and not h.is_contiguous():
+        _refuse("h: not contiguous")
+    if h is not None and h.numel() == rows * k * down.cols:
+        h = h.view(rows * k, down.cols)
+    xa, _, qa = _q4_act(h, hq, hs, hl, rows * k, down.cols, dev, "h")
+    _check(lib.moe_down_combine_q4(down, d, xa, qa, rows, k, ids.data_ptr(), _tensor(gates, f32, ids.shape, dev, "gates"),
+                                   _plan_ref(plan), _tensor(residual, f32, y.shape, dev, "residual"), y.data_ptr(),
+                                   _ws_of(ws, dev), _stream_of(stream, dev)))
 
 
 class Model:

@@ -1,0 +1,413 @@
+// Router scores to experts (q8moe.h, moe_route_scored): scores, groups, the k best, gates, and the grouping by expert.
+//
+// A warp takes a row: lane L holds experts L, L + 32, ...; the k best come from k rounds of one warp-wide maximum over
+// order-preserving integer keys and one warp-wide minimum over the indices that hold it.  Scores are formed in f32, whose
+// errors can exchange two experts that 64 bits would order: the choice is taken again in 64 bits for a row in which two
+// neighbours of the order (or a kept and a left group) are closer than those errors reach.
+#include <math.h>
+
+#include "common.cuh"
+#include "ffn4.h"
+
+namespace q8 {
+namespace {
+
+constexpr unsigned FULL = 0xffffffffu;
+constexpr int kPlaceThreads = 1024;
+
+struct RouteParams {
+    const float* logits;
+    int64_t stride;
+    int rows, E, K;
+    const float* bias;
+    int sigmoid, groups, keep, top, renorm;
+    float scale;
+    int32_t* ids;
+    float* gates;
+    PlanPtrs plan;
+    int32_t* hist;  // [CTAs][E] when other CTAs group the choices
+    int per;        // rows a CTA (0: rows are dealt out warp by warp)
+};
+
+// f32 -> an unsigned integer of the same order (both zeros alike).
+__device__ __forceinline__ unsigned order_key(float x) {
+    const unsigned u = __float_as_uint(x + 0.f);
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float key_value(unsigned k) {
+    return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+}
+constexpr unsigned kHidden = 0u, kOff = 1u;  // below every number's key: of another group or taken; out of service
+
+template <typename T>
+__device__ __forceinline__ T minus_inf();
+template <>
+__device__ __forceinline__ float minus_inf<float>() { return -INFINITY; }
+template <>
+__device__ __forceinline__ double minus_inf<double>() { return -INFINITY; }
+
+// The kept groups as a bit mask, from the marks c [E] of the warp's row in shared memory (-infinity: out of service).
+// `close`: whether a kept and a left group are within `tol` of one another.
+template <typename T>
+__device__ __forceinline__ unsigned kept_groups(const T* c, int E, int groups, int keep, int top, T tol, bool& close) {
+    const int lane = threadIdx.x & 31, S = E / groups;
+    int lpg = 32;  // lanes a group: a power of two
+    while (lpg * groups > 32) lpg >>= 1;
+    const int g = lane / lpg;
+    const T none = minus_inf<T>();
+    T t1 = none, t2 = none;
+    if (g < groups)
+        for (int i = lane % lpg; i < S; i += lpg) {
+            const T v = c[g * S + i];
+            t2 = max(t2, min(t1, v));
+            t1 = max(t1, v);
+        }
+    for (int o = lpg >> 1; o > 0; o >>= 1) {
+        const T o1 = __shfl_xor_sync(FULL, t1, o), o2 = __shfl_xor_sync(FULL, t2, o);
+        t2 = max(min(t1, o1), max(t2, o2));
+        t1 = max(t1, o1);
+    }
+    const T sum = top == 2 && t2 > none ? t1 + t2 : t1;
+    const T mark = __shfl_sync(FULL, sum, (lane < groups ? lane : 0) * lpg);  // lane j: group j's
+    int rank = 0;
+    for (int j = 0; j < groups; ++j) {
+        const T m = __shfl_sync(FULL, mark, j);
+        rank += m > mark || (m == mark && j < lane);
+    }
+    const bool kept = lane < groups && rank < keep;
+    T least = kept ? mark : -none, most = lane < groups && !kept ? mark : none;
+    for (int o = 16; o > 0; o >>= 1) {
+        least = min(least, __shfl_xor_sync(FULL, least, o));
+        most = max(most, __shfl_xor_sync(FULL, most, o));
+    }
+    close = most > none && !(least - most > tol);
+    return __ballot_sync(FULL, kept);
+}
+
+// The choice of the warp's row in 64 bits: lane j gets the j-th expert, and whether it is in service.  l holds the row's
+// logits, c is scratch, both [E] of the warp in shared memory.
+__device__ __noinline__ void choose_exactly(const RouteParams& p, const float* l, double* c, int& id, bool& on) {
+    const int lane = threadIdx.x & 31;
+    double m = -INFINITY, z = 0;
+    if (!p.sigmoid) {
+        for (int e = lane; e < p.E; e += 32) m = max(m, (double)l[e]);
+        for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(FULL, m, o));
+        for (int e = lane; e < p.E; e += 32)
+            if (l[e] != -INFINITY) z += exp((double)l[e] - m);
+        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(FULL, z, o);
+    }
+    for (int e = lane; e < p.E; e += 32) {
+        double v = -INFINITY;
+        if (l[e] != -INFINITY) {
+            v = p.sigmoid ? 1 / (1 + exp(-(double)l[e])) : exp((double)l[e] - m) / z;
+            if (p.bias) v += p.bias[e];
+            if (isnan(v)) v = -INFINITY;
+        }
+        c[e] = v;
+    }
+    __syncwarp();
+    unsigned kept = FULL;
+    bool close;
+    const int S = p.E / p.groups;
+    if (p.groups > 1) kept = kept_groups<double>(c, p.E, p.groups, p.keep, p.top, 0, close);
+    __syncwarp();
+    // what is out of service goes below every number, what is hidden or taken below that
+    for (int e = lane; e < p.E; e += 32) {
+        if (p.groups > 1 && !((kept >> (e / S)) & 1u)) c[e] = -INFINITY;
+        else if (c[e] == -INFINITY) c[e] = -1.7e308;
+        else if (!p.bias) c[e] = l[e];
+    }
+    __syncwarp();
+    for (int j = 0; j < p.K; ++j) {
+        double best = -INFINITY;
+        int at = p.E;
+        for (int e = lane; e < p.E; e += 32)
+            if (c[e] > best) best = c[e], at = e;
+        for (int o = 16; o > 0; o >>= 1) {
+            const double ob = __shfl_xor_sync(FULL, best, o);
+            const int oa = __shfl_xor_sync(FULL, at, o);
+            if (ob > best || (ob == best && oa < at)) best = ob, at = oa;
+        }
+        at = min(at, p.E - 1);
+        if (lane == j) id = at, on = best > -1.6e308;
+        if ((at & 31) == lane) c[at] = -INFINITY;
+        __syncwarp();
+    }
+}
+
+// Adds the CTA's choices [first, first + n) (their experts in ids) to the lists, in ascending order: next[e] is expert e's
+// first free place.  wh is [warps][E] of shared memory.
+__device__ __forceinline__ void place_choices(const int32_t* ids, int first, int n, int E, int* wh, int* next, int32_t* lists) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, W = blockDim.x >> 5;
+    const int seg = ((n + W - 1) / W + 31) & ~31;
+    const int lo = min(w * seg, n), hi = min(lo + seg, n);
+    for (int i = threadIdx.x; i < W * E; i += blockDim.x) wh[i] = 0;
+    __syncthreads();
+    for (int i = lo + lane; i < hi; i += 32) atomicAdd(&wh[w * E + ids[first + i]], 1);
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        int run = next[e];
+        for (int v = 0; v < W; ++v) {
+            const int n_v = wh[v * E + e];
+            wh[v * E + e] = run;
+            run += n_v;
+        }
+    }
+    __syncthreads();
+    for (int i = lo; i < hi; i += 32) {
+        const bool in = i + lane < hi;
+        const int e = in ? ids[first + i + lane] : E;  // (lanes past the end stand together)
+        const unsigned same = __match_any_sync(FULL, e);
+        const int before = __popc(same & ((1u << lane) - 1));
+        if (in) lists[wh[w * E + e] + before] = first + i + lane;
+        __syncwarp();
+        if (in && before == 0) wh[w * E + e] += __popc(same);
+        __syncwarp();
+    }
+}
+
+// From total[e] (shared memory): offsets into `off` (shared) and, when `write`, counts, offsets and the experts with
+// choices to the plan.  E <= 1024; tmp is 64 ints.
+__device__ __forceinline__ void scan_totals(const int* total, int E, int* off, int* tmp, const PlanPtrs& plan, bool write) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    int base = 0, hits = 0;  // of the experts before this round's (a CTA of fewer threads than experts takes rounds)
+    for (int e0 = 0; e0 < E; e0 += blockDim.x) {
+        const int e = e0 + threadIdx.x;
+        const int n = e < E ? total[e] : 0;
+        int run = n;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(FULL, run, o);
+            if (lane >= o) run += v;
+        }
+        const unsigned some = __ballot_sync(FULL, n > 0);
+        if (lane == 31) tmp[w] = run, tmp[32 + w] = __popc(some);
+        __syncthreads();
+        int before = base, hit = hits, all = 0, all_hits = 0;
+        for (int v = 0; v < (int)(blockDim.x >> 5); ++v) {
+            if (v < w) before += tmp[v], hit += tmp[32 + v];
+            all += tmp[v], all_hits += tmp[32 + v];
+        }
+        base += all, hits += all_hits;
+        if (e < E) {
+            off[e] = before + run - n;
+            if (write) {
+                plan.counts[e] = n;
+                plan.offsets[e] = before + run - n;
+                if (n > 0) plan.active[1 + hit + __popc(some & ((1u << lane) - 1))] = e;
+            }
+        }
+        __syncthreads();
+    }
+    if (write && threadIdx.x == 0) plan.offsets[E] = base, plan.active[0] = hits;
+}
+
+template <int NL>
+__global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_kernel(const RouteParams p) {
+    extern __shared__ char smem[];
+    __shared__ int tmp[64];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, W = blockDim.x >> 5;
+    double* c64 = reinterpret_cast<double*>(smem) + w * p.E;  // a warp's marks (f32 in the same place)
+    float* cs = reinterpret_cast<float*>(c64);
+    float* ls = reinterpret_cast<float*>(smem + (size_t)W * p.E * 8) + w * p.E;
+    const int S = p.E / p.groups;
+    float b[NL], bmax = 0.f;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const int e = lane + 32 * i;
+        b[i] = p.bias && e < p.E ? p.bias[e] : 0.f;
+        if (isfinite(b[i])) bmax = fmaxf(bmax, fabsf(b[i]));
+    }
+    bmax = warp_max(bmax);
+    const int first = p.per ? blockIdx.x * p.per : 0;
+    const int end = p.per ? min(first + p.per, p.rows) : p.rows;
+    const int step = p.per ? W : W * gridDim.x;
+    for (int r = first + (p.per ? w : blockIdx.x * W + w); r < end; r += step) {
+        const float* row = p.logits + r * p.stride;
+        float l[NL];
+        unsigned key[NL];
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int e = lane + 32 * i;
+            const float v = e < p.E ? row[e] : -INFINITY;
+            l[i] = isnan(v) ? -INFINITY : fminf(v, 3.402823466e38f);
+            m = fmaxf(m, l[i]);
+        }
+        m = warp_max(m);
+        const float m0 = m == -INFINITY ? 0.f : m;
+        float z = 0.f, zi = 0.f;
+        const bool scores = p.bias || p.groups > 1 || !p.renorm;
+        if (!p.sigmoid && scores) {
+#pragma unroll
+            for (int i = 0; i < NL; ++i) z += expf(l[i] - m0);
+            z = group_sum<32>(z);
+            zi = z > 0.f ? 1.f / z : 0.f;
+        }
+        // How far two f32 scores can be out against one another: a few roundings of p <= pmax and of p + b, and for the
+        // softmax its sum's, which all scores share (up to NL + 5 roundings of a sum).
+        const float pmax = p.sigmoid ? 1.f : zi;
+        const float tol = 6e-7f * (pmax + bmax) + (p.sigmoid ? 0.f : 1.2e-7f * (NL + 5) * pmax);
+        bool slow = false;
+        unsigned kept = FULL;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int e = lane + 32 * i;
+            float c = l[i];
+            if (p.bias || p.groups > 1) {
+                c = p.sigmoid ? 1.f / (1.f + expf(-l[i])) : expf(l[i] - m0) * zi;
+                if (p.bias) c += b[i];
+            }
+            const bool on = e < p.E && l[i] > -INFINITY && c > -INFINITY;  // (a c that is no number fails too)
+            if (e < p.E) {
+                ls[e] = l[i];  // (an expert that its bias takes out of service still counts in the softmax)
+                if (p.groups > 1) cs[e] = on ? c : -INFINITY;
+            }
+            key[i] = e >= p.E ? kHidden : !on ? kOff : order_key(p.bias ? c : l[i]);
+        }
+        __syncwarp();
+        if (p.groups > 1) {
+            kept = kept_groups<float>(cs, p.E, p.groups, p.keep, p.top, 2.5f * tol, slow);
+#pragma unroll
+            for (int i = 0; i < NL; ++i)
+                if (!((kept >> min((lane + 32 * i) / S, 31)) & 1u)) key[i] = kHidden;
+        }
+        int id = 0;
+        bool on = false;
+        unsigned mine = kHidden, mine_at = 0;  // this lane's largest key and its expert
+        auto rescan = [&]() {
+            mine = key[0], mine_at = lane;
+#pragma unroll
+            for (int i = 1; i < NL; ++i)
+                if (key[i] > mine) mine = key[i], mine_at = lane + 32 * i;
+        };
+        rescan();
+        unsigned last = kHidden;
+        const int rounds = p.bias ? p.K + 1 : p.K;  // (the order by logits is exact)
+        for (int j = 0; j < rounds; ++j) {
+            const unsigned best = __reduce_max_sync(FULL, mine);
+            const unsigned at = __reduce_min_sync(FULL, mine == best ? mine_at : FULL);
+            if (p.bias && last > kOff && best > kOff) slow |= !(key_value(last) - key_value(best) > tol);
+            last = best;
+            if (lane == j) id = at, on = best > kOff;
+            if ((at & 31) == lane) {
+#pragma unroll
+                for (int i = 0; i < NL; ++i)
+                    if (at == lane + 32 * i) key[i] = kHidden;
+                rescan();
+            }
+        }
+        if (slow) choose_exactly(p, ls, c64, id, on);
+        // gates: lane j the j-th
+        const bool kth = lane < p.K;
+        id = kth ? min(max(id, 0), p.E - 1) : 0;
+        float gate = 0.f;
+        const float v = kth && on ? ls[id] : -INFINITY;
+        if (p.renorm) {  // relative to the largest: below -20 a sigmoid is e^l to less than f32's rounding
+            const float most = warp_max(v);
+            if (v > -INFINITY) gate = p.sigmoid && most >= -20.f ? 1.f / (1.f + expf(-v)) : expf(v - most);
+            const float sum = group_sum<32>(gate);
+            gate = sum > 0.f ? gate / sum : 0.f;
+        } else if (v > -INFINITY) {
+            gate = p.sigmoid ? (v < -80.f ? expf(v) : 1.f / (1.f + expf(-v))) : expf(v - m0) * zi;
+        }
+        if (kth) {
+            p.ids[(int64_t)r * p.K + lane] = id;
+            p.gates[(int64_t)r * p.K + lane] = gate * p.scale;
+        }
+        __syncwarp();
+    }
+    if (!p.per || !p.plan.counts) return;
+    // The grouping: all of it here when this CTA has all rows, else this CTA's counts for the CTAs that place the choices.
+    __syncthreads();
+    int* wh = reinterpret_cast<int*>(smem);
+    int* total = reinterpret_cast<int*>(smem + (size_t)W * p.E * 8);
+    int* off = total + p.E;
+    const int n = (end - first) * p.K;
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) total[e] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) atomicAdd(&total[p.ids[(int64_t)first * p.K + i]], 1);
+    __syncthreads();
+    if (p.hist) {
+        for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.hist[(int64_t)blockIdx.x * p.E + e] = total[e];
+        return;
+    }
+    scan_totals(total, p.E, off, tmp, p.plan, true);
+    __syncthreads();
+    place_choices(p.ids, 0, n, p.E, wh, off, p.plan.lists);
+}
+
+// CTA b places the choices of route_kernel's CTA b: the counts of all CTAs give every expert's total and where CTA b's
+// choices start.
+__global__ void __launch_bounds__(kPlaceThreads) place_kernel(const RouteParams p) {
+    extern __shared__ char smem[];
+    __shared__ int tmp[64];
+    int* total = reinterpret_cast<int*>(smem);
+    int* off = total + p.E;
+    int* before = off + p.E;
+    int* wh = before + p.E;
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) total[e] = before[e] = 0;
+    __syncthreads();
+    const int parts = max(1, (int)blockDim.x / p.E), mine = blockIdx.x;
+    for (int i = threadIdx.x; i < parts * p.E; i += blockDim.x) {
+        const int e = i % p.E;
+        int all = 0, pre = 0;
+#pragma unroll 8
+        for (int b = i / p.E; b < (int)gridDim.x; b += parts) {
+            const int n = p.hist[(int64_t)b * p.E + e];
+            all += n;
+            if (b < mine) pre += n;
+        }
+        atomicAdd(&total[e], all);
+        atomicAdd(&before[e], pre);
+    }
+    __syncthreads();
+    scan_totals(total, p.E, off, tmp, p.plan, mine == 0);
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) off[e] += before[e];
+    __syncthreads();
+    const int first = mine * p.per, end = min(first + p.per, p.rows);
+    place_choices(p.ids, first * p.K, max(end - first, 0) * p.K, p.E, wh, off, p.plan.lists);
+}
+
+template <int NL>
+cudaError_t run(RouteParams p, Carve& ws, cudaStream_t st) {
+    constexpr int most = (NL <= 8 ? 1024 : NL == 16 ? 512 : 256) / 32;  // warps
+    static_assert(most * NL * 32 * 12 <= 98304, "a CTA's rows in shared memory");
+    const int sms = device_info().sms;
+    cudaError_t e = cudaFuncSetAttribute(route_kernel<NL>, cudaFuncAttributeMaxDynamicSharedMemorySize, 98304);
+    if (e != cudaSuccess) return e;
+    if (!p.plan.counts) {
+        const int W = 4;
+        const int64_t grid = min((int64_t)(p.rows + W - 1) / W, (int64_t)sms * 8);
+        return launch(route_kernel<NL>, dim3((unsigned)grid), dim3(32 * W), (size_t)W * p.E * 12, st, 0, p);
+    }
+    // With a plan: one CTA up to a few rows a warp, whose grouping needs no second launch; else a CTA an SM.
+    const int grid = p.rows <= 4 * most ? 1 : min(sms, (p.rows + most - 1) / most);
+    p.per = (p.rows + grid - 1) / grid;
+    const size_t smem = (size_t)most * p.E * 12;
+    if (grid == 1) return launch(route_kernel<NL>, dim3(1), dim3(32 * most), max(smem, (size_t)p.E * (8 * most + 8)), st, 0, p);
+    p.hist = ws.take<int32_t>((size_t)grid * p.E);
+    if (ws.overflow) return cudaSuccess;
+    e = launch(route_kernel<NL>, dim3(grid), dim3(32 * most), max(smem, (size_t)p.E * (8 * most + 8)), st, 0, p);
+    if (e != cudaSuccess) return e;
+    const size_t place = (size_t)p.E * 4 * (3 + kPlaceThreads / 32);
+    e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 * 4 * (3 + kPlaceThreads / 32));
+    if (e != cudaSuccess) return e;
+    return launch(place_kernel, dim3(grid), dim3(kPlaceThreads), place, st, 0, p);
+}
+
+}  // namespace
+
+cudaError_t launch_route_scored(const RouteScoredCall& c, Carve& ws, cudaStream_t st) {
+    RouteParams p = {c.logits, c.stride, (int)c.rows, c.E, c.K, c.rule.bias, c.rule.score == Q8_SCORE_SIGMOID,
+                     c.rule.groups, c.rule.keep_groups, c.rule.group_top, c.rule.renorm, c.rule.scale, c.ids, c.gates, c.plan,
+                     nullptr, 0};
+    if (p.E <= 32) return run<1>(p, ws, st);
+    if (p.E <= 64) return run<2>(p, ws, st);
+    if (p.E <= 128) return run<4>(p, ws, st);
+    if (p.E <= 256) return run<8>(p, ws, st);
+    if (p.E <= 512) return run<16>(p, ws, st);
+    return run<32>(p, ws, st);
+}
+
+}  // namespace q8
