@@ -60,6 +60,8 @@ Q4View view_of(const q4_mat* W) {
 
 // The activation of a product: f32 rows or quantized ones, `cols` values each.
 int check_q4_act(const float* x, int64_t stride, const q8_act* xq, int64_t rows, int64_t cols, const char* name, Q4Act* out) {
+    if (rows * cols > (int64_t(1) << 33))
+        return model_fail(Q8_EUNSUPPORTED, "%s: %lld rows of %lld values: at most 2^33", name, (long long)rows, (long long)cols);
     if (!x && !xq) return model_fail(Q8_EINVAL, "%s: null, as is its quantized form", name);
     if (x && xq) return model_fail(Q8_EINVAL, "%s: given as values and as words", name);
     if (x) {
