@@ -54,21 +54,24 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Eight consecutive values of an activation row as f16 parts, in the order words_f16 gives the weights; four lanes (a quad)
-// hold a 32-value block and share its scale.  All lanes of the warp call it.
+// Eight consecutive values of an activation row as f16 parts, in the order words_f16 gives the weights.
 struct ActParts {
     uint4 hi, lo;
     float scale;
 };
 
-__device__ __forceinline__ ActParts split_values(const float (&x)[8]) {
+// The largest finite magnitude of eight values.
+__device__ __forceinline__ float finite_max(const float (&x)[8]) {
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]) <= 3.402823466e38f ? fabsf(x[i]) : 0.f);  // of the finite ones
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    // The block's unit 2^(e - 141) brings its largest value into [2^14, 2^15): well inside f16, and a value's second part
-    // leaves f16's normal range only 2^18 below that.  e is held where both the unit and its inverse are normal numbers.
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]) <= 3.402823466e38f ? fabsf(x[i]) : 0.f);
+    return m;
+}
+
+// The parts of eight values that share a unit with others of which m is the largest magnitude.  The unit, 2^(e - 141), brings
+// m into [2^14, 2^15): well inside f16, and a value's second part leaves f16's normal range only 2^18 below that.  e is held
+// where both the unit and its inverse are normal numbers.
+__device__ __forceinline__ ActParts split_values(const float (&x)[8], float m) {
     const unsigned e = max(__float_as_uint(m) >> 23, 15u);
     const float up = __uint_as_float((268u - e) << 23);
     float v[8], r[8];
@@ -93,20 +96,20 @@ __device__ __forceinline__ uint4 words_parts(uint2 w, float unit) {
     return make_uint4(pack_f16(v[0], v[4]), pack_f16(v[1], v[5]), pack_f16(v[2], v[6]), pack_f16(v[3], v[7]));
 }
 
-// Values 8 i .. 8 i + 7 of activation row r (i < cols / 8, else zeros).
-__device__ __forceinline__ ActParts act_parts(const Q4Act& a, int64_t r, int i, int cols) {
-    const bool in = 8 * i < cols;
-    if (a.x) {
-        float x[8] = {};
-        if (in) {
-            const float4* p = reinterpret_cast<const float4*>(a.x + r * a.stride + 8 * i);
-            const float4 u = p[0], v = p[1];
-            x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
-        }
-        return split_values(x);
+// Values 8 i .. 8 i + 7 of f32 activation row r (zeros from `cols` on).
+__device__ __forceinline__ void act_values(const Q4Act& a, int64_t r, int i, int cols, float (&x)[8]) {
+    float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+    if (8 * i < cols) {
+        const float4* p = reinterpret_cast<const float4*>(a.x + r * a.stride + 8 * i);
+        u = p[0], v = p[1];
     }
+    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+}
+
+// Values 8 i .. 8 i + 7 of quantized activation row r (zeros from `cols` on).
+__device__ __forceinline__ ActParts act_words(const Q4Act& a, int64_t r, int i, int cols) {
     ActParts p = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0), 0.f};
-    if (in) {
+    if (8 * i < cols) {
         const int64_t at = r * cols + 8 * i;
         p.hi = words_parts(*reinterpret_cast<const uint2*>(a.q + at), 1.f);
         if (a.lo) p.lo = words_parts(*reinterpret_cast<const uint2*>(a.lo + at), 0.0078125f);

@@ -85,7 +85,17 @@ __device__ __forceinline__ void stage_rows(const RowParams& p, char* vecs, int f
     const int octets = 4 * 4 * p.chunks, cols = p.w0.cols;  // eight values each, up to whole chunks
     for (int i = threadIdx.x; i < ((n * octets + 31) & ~31); i += blockDim.x) {  // whole warps: quads share a block
         const int v = i / octets, o = i - v * octets, b = o >> 2;
-        const ActParts a = act_parts(p.act, first + min(v, n - 1), v < n ? o : octets, cols);
+        ActParts a;
+        if (p.act.x) {  // a block's four lanes share its unit
+            float x[8];
+            act_values(p.act, first + min(v, n - 1), v < n ? o : octets, cols, x);
+            float m = finite_max(x);
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            a = split_values(x, m);
+        } else {
+            a = act_words(p.act, first + min(v, n - 1), o, cols);
+        }
         if (v >= n) continue;
         char* at = vecs + v * p.vec + b * kBlockBytes + (o & 3) * 16;
         *reinterpret_cast<uint4*>(at) = a.hi;

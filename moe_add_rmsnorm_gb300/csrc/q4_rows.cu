@@ -3,56 +3,89 @@
 //
 // A first launch lays the activation rows out as f16 parts (q4.cuh) in the order of the products' operands; a second one
 // multiplies.  There a warp takes two tiles of 16 weight rows (gate-up: 16 gate rows and the 16 up rows beside them) by up
-// to NT tiles of eight columns, a column being one part of one activation row.  The weights come through a ring of
-// asynchronous 16-byte copies of the warp's own in shared memory, from where one matrix load gives each lane the words it
-// multiplies; a block's dots are scaled by the weights' and the activation's scales into f32 sums.  What bounds it is the
-// weights' bytes with few columns and the warp-wide products with many.
+// to NT tiles of eight columns, a column being one part of one activation row.  Weights and activation parts come through
+// rings of asynchronous 16-byte copies: the weights' is the warp's own, from where one matrix load gives each lane the words
+// it multiplies; the activation's is the CTA's, whose warps read the same columns.  A block's dots are scaled, two sums an
+// instruction, by the weights' scale (and a quantized activation's; an f32 row has one unit, taken out at the end).
 #include "ffn4.h"
 #include "q4.cuh"
 
 namespace q8 {
 namespace {
 
-constexpr int kWarps = 4;   // a CTA
-constexpr int kStages = 6;  // of a warp's ring: chunks of four blocks of its 32 rows
-constexpr int kStageBytes = 2 * 16 * 64;
+constexpr int kWarps = 8;    // a CTA
+constexpr int kStages = 4;   // of the rings: a stage is a chunk of four blocks for each of the warps that share a tile
+constexpr int kTileBytes = 2 * 16 * 64;
+
+enum { FORM_F32 = 0, FORM_ONE = 1, FORM_TWO = 2 };
 
 struct RowsParams {
     Q4View w0, w1;
     Q4Act act;
+    int kind;
     int64_t E, out_rows;
     int R, K;            // activation rows of the call and choices a row
     int64_t act_rows;    // rows that are laid out
     PlanPtrs plan;
     const int32_t* ids;
     const float *gates, *residual;
-    uint4* parts;        // [act_rows][4 * chunks][PARTS][4]
-    float* scales;       // [act_rows][4 * chunks]
+    uint4* parts;        // [act_rows][4 * chunks][parts][4]
+    float* scales;       // f32: [act_rows], a row's unit; else [act_rows][4 * chunks] (two words: each twice)
     float* y;
     int64_t y_stride;
     float* out;          // down: [R * K][out_rows]
     int chunks, wk, row_tiles;
 };
 
-template <int PARTS>
+// A CTA lays one activation row out at a time.
+template <int FORM>
 __global__ void __launch_bounds__(256) q4_parts_kernel(const RowsParams p) {
+    constexpr int PARTS = FORM == FORM_ONE ? 1 : 2;
+    __shared__ float most[2][8];
     griddep_launch();
-    const int octets = 16 * p.chunks;
-    const int64_t n = p.act_rows * octets, step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < ((n + 31) & ~int64_t(31)); i += step) {
-        const int64_t r = min(i / octets, p.act_rows - 1);
-        const int o = i < n ? (int)(i - r * octets) : octets;  // (past the end: whole warps take part)
-        const ActParts a = act_parts(p.act, r, o, p.w0.cols);
-        if (i >= n) continue;
-        uint4* at = p.parts + (r * octets + (o & ~3)) * PARTS + (o & 3);
-        at[0] = a.hi;
-        if (PARTS == 2) at[4] = a.lo;
-        if ((o & 3) == 0) p.scales[r * (octets / 4) + (o >> 2)] = a.scale;
+    const int octets = 16 * p.chunks, cols = p.w0.cols, lane = threadIdx.x & 31;
+    int buf = 0;
+    for (int64_t r = blockIdx.x; r < p.act_rows; r += gridDim.x, buf ^= 1) {
+        float m = 0.f;
+        if (FORM == FORM_F32) {
+            for (int o = threadIdx.x; o < octets; o += blockDim.x) {
+                float x[8];
+                act_values(p.act, r, o, cols, x);
+                m = fmaxf(m, finite_max(x));
+            }
+            m = warp_max(m);
+            if (lane == 0) most[buf][threadIdx.x >> 5] = m;
+            __syncthreads();
+            for (int i = 0; i < 8; ++i) m = fmaxf(m, most[buf][i]);
+        }
+        for (int o = threadIdx.x; o < octets; o += blockDim.x) {
+            ActParts a;
+            if (FORM == FORM_F32) {
+                float x[8];
+                act_values(p.act, r, o, cols, x);
+                a = split_values(x, m);
+                if (o == 0) p.scales[r] = a.scale;
+            } else {
+                a = act_words(p.act, r, o, cols);
+                const int64_t b = r * (octets / 4) + (o >> 2);
+                if ((o & 3) == 0) {
+                    if (FORM == FORM_ONE) p.scales[b] = a.scale;
+                    else reinterpret_cast<float2*>(p.scales)[b] = make_float2(a.scale, a.scale);
+                }
+            }
+            uint4* at = p.parts + (r * octets + (o & ~3)) * PARTS + (o & 3);
+            at[0] = a.hi;
+            if (PARTS == 2) at[4] = a.lo;
+        }
     }
 }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_small(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
 }
 
 __device__ __forceinline__ void load_matrices(uint32_t (&m)[4], uint32_t at) {
@@ -68,122 +101,160 @@ __device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-template <int KIND, int PARTS, int NT>
-__global__ void __launch_bounds__(32 * kWarps, 4) q4_rows_kernel(const RowsParams p) {
+// Pairs of f32, two operations an instruction.
+__device__ __forceinline__ float2 pair_mul(float2 a, float2 b) {
+    float2 d;
+    asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z;}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ void pair_fma(float2& acc, float2 a, float bx, float by) {
+    asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%0, %1}; fma.rn.f32x2 z, x, y, z; mov.b64 {%0, %1}, z;}"
+        : "+f"(acc.x), "+f"(acc.y) : "f"(a.x), "f"(a.y), "f"(bx), "f"(by));
+}
+
+template <int FORM, int NT>
+__global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1) q4_rows_kernel(const RowsParams p) {
+    constexpr int PARTS = FORM == FORM_ONE ? 1 : 2;
     constexpr int COLS = 8 / PARTS;  // activation rows a tile of columns
     constexpr int NC = NT * COLS;
-    constexpr int AC = 4 / PARTS;    // sums a lane keeps of a tile: of rows g and g + 8, for its one or two activation rows
+    constexpr int BCHUNK = NT * 8 * 4 * 64;                          // a chunk's columns: [block][column][4 x 16 bytes]
+    constexpr int SCHUNK = FORM == FORM_F32 ? 0 : 4 * NT * 8 * 4;    // and scales: [block][column] (two words: a row's twice)
     extern __shared__ __align__(128) char smem[];
-    __shared__ int cols[NC];  // the choices (dense: activation rows) of the columns, -1: none
+    __shared__ int cols[NC];           // the choices (dense: activation rows) of the columns, -1: none
+    __shared__ uint32_t rowat[NC];     // their activation rows
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int side = kWarps / p.wk, tile = blockIdx.x * side + w / p.wk;
+    const int side = kWarps / p.wk, tile = blockIdx.x * side + w / p.wk, part_of = w % p.wk;
     const int nb = p.w0.cols >> 5, ngroups = p.w0.cols >> p.w0.group_log2;
-    const int mine = (p.chunks + p.wk - 1) / p.wk, c0 = (w % p.wk) * mine, c1 = min(c0 + mine, p.chunks);
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + w * kStages * kStageBytes;
+    const int steps = (p.chunks + p.wk - 1) / p.wk;
+    const uint32_t base_a = (uint32_t)__cvta_generic_to_shared(smem) + w * (kStages * kTileBytes);
+    const uint32_t base_b = (uint32_t)__cvta_generic_to_shared(smem) + kWarps * kStages * kTileBytes;
+    const uint32_t stage_b = p.wk * (BCHUNK + SCHUNK);
     const int total = p.R * p.K;
+    const bool gate_up = p.kind == Q4_GATE_UP;
+    const Q4View& second = gate_up ? p.w1 : p.w0;
     bool ready = false;
-    griddep_launch();
     int groups = 1;
-    if (KIND != Q4_DENSE) groups = min(max(p.plan.active[0], 0), (int)min(p.E, (int64_t)total));
+    if (p.kind != Q4_DENSE) groups = min(max(p.plan.active[0], 0), (int)min(p.E, (int64_t)total));
+    griddep_launch();
     for (int a = blockIdx.y; a < groups; a += gridDim.y) {
         int e = 0, first = 0, count = p.R;
-        if (KIND != Q4_DENSE) {
+        if (p.kind != Q4_DENSE) {
             e = p.plan.active[1 + a];
             if (e < 0 || e >= p.E) continue;
             first = max(p.plan.offsets[e], 0);
             count = min(p.plan.offsets[e + 1], total) - first;
         }
-        // the lane's rows of the two weight tiles: m-tile 0 and 1, rows g and g + 8; copies clamp to the group's last row
+        // the lane's rows of the two weight tiles: rows g and g + 8 of each; they clamp to the group's last row
         const int64_t base = (int64_t)e * p.out_rows;
-        const int r0 = (KIND == Q4_GATE_UP ? 16 : 32) * tile;
-        const int last = (int)p.out_rows - 1;
+        const int r0 = (gate_up ? 16 : 32) * tile, last = (int)p.out_rows - 1;
         const uint8_t* src[2][2];
         int64_t sg[2][2];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int r = min(r0 + (KIND == Q4_GATE_UP ? 0 : 16 * m) + g + 8 * i, last);
-                const Q4View& v = KIND == Q4_GATE_UP && m == 1 ? p.w1 : p.w0;
-                src[m][i] = v.q + (base + r) * (p.w0.cols >> 1) + 16 * t;
-                sg[m][i] = (base + r) * ngroups;
+                const int64_t r = base + min(r0 + (gate_up ? 0 : 16 * m) + g + 8 * i, last);
+                src[m][i] = (m == 0 ? p.w0.q : second.q) + r * (p.w0.cols >> 1) + 16 * t;
+                sg[m][i] = r * ngroups;
             }
         for (int ct = blockIdx.z; ct * NC < count; ct += gridDim.z) {
-            uint32_t into = ring;
-            auto fetch = [&](int c) {  // the warp's chunk c into the next stage
-                if (c < c1) {
-                    const uint32_t at = into;
-                    const bool in = 4 * c + t < nb;
-#pragma unroll
-                    for (int m = 0; m < 2; ++m)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int r = g + 8 * i;
-                            copy16(at + m * 1024 + r * 64 + ((t ^ ((r >> 1) & 3)) << 4), in ? src[m][i] + 64 * c : p.w0.q, in);
-                        }
-                }
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                into += kStageBytes;
-                if (into == ring + kStages * kStageBytes) into = ring;
-            };
+            const int tiles = min((count - ct * NC + COLS - 1) / COLS, NT);
             uint32_t s[2][2], z[2][2];  // the next chunk's scales and zero points: lane t block t's
             auto scales = [&](int c) {
                 const int b = 4 * c + t;
+                const bool in = b < nb;
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const Q4View& v = KIND == Q4_GATE_UP && m == 1 ? p.w1 : p.w0;
                         const int64_t at = sg[m][i] + ((32 * b) >> p.w0.group_log2);
-                        const bool in = c < c1 && b < nb;
-                        s[m][i] = in ? __ldg(v.s + at) : 0u;
-                        z[m][i] = in && v.z ? __ldg(v.z + at) : 8u;
+                        s[m][i] = in ? __ldg((m == 0 ? p.w0.s : second.s) + at) : 0u;
+                        z[m][i] = in && p.w0.z ? __ldg((m == 0 ? p.w0.z : second.z) + at) : 8u;
                     }
             };
+            auto fetch_weights = [&](int step) {
+                const int c = step * p.wk + part_of;
+                if (step >= steps || c >= p.chunks) return;
+                const uint32_t at = base_a + (step % kStages) * kTileBytes;
+                const bool in = 4 * c + t < nb;
 #pragma unroll
-            for (int i = 0; i < kStages - 1; ++i) fetch(c0 + i);
-            scales(c0);
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = g + 8 * i;
+                        copy16(at + m * 1024 + r * 64 + ((t ^ ((r >> 1) & 3)) << 4), in ? src[m][i] + 64 * c : p.w0.q, in);
+                    }
+            };
+            auto fetch_columns = [&](int step) {  // all warps: the stage's chunks of the columns
+                if (step >= steps) return;
+                const uint32_t at = base_b + (step % kStages) * stage_b;
+                const int rows = tiles * COLS, units = rows * 16 * PARTS;
+                for (int j = 0; j < p.wk; ++j) {
+                    const int c = step * p.wk + j;
+                    if (c >= p.chunks) break;
+                    const uint32_t to = at + j * (BCHUNK + SCHUNK);
+                    for (int u = threadIdx.x; u < units; u += 32 * kWarps) {
+                        const int row = u / (16 * PARTS), v = u % (16 * PARTS);  // v = (block, part, word)
+                        const int b = v / (4 * PARTS), part = (v >> 2) % PARTS;
+                        copy16(to + (((b * NT * 8 + row * PARTS + part) << 2) + (v & 3)) * 16,
+                               p.parts + rowat[row] * (size_t)(16 * PARTS) * p.chunks + c * (16 * PARTS) + v, true);
+                    }
+                    if (FORM != FORM_F32)
+                        for (int u = threadIdx.x; u < rows * 4; u += 32 * kWarps) {
+                            const int row = u >> 2, b = u & 3;
+                            const size_t from = rowat[row] * (size_t)(4 * p.chunks) + 4 * c + b;
+                            if (FORM == FORM_ONE) copy_small<4>(to + BCHUNK + (b * NT * 8 + row) * 4, p.scales + from);
+                            else copy_small<8>(to + BCHUNK + (b * NT * 8 + 2 * row) * 4, p.scales + 2 * from);
+                        }
+                }
+            };
+            // weights first: they depend on no launch before
+            scales(part_of);
+            fetch_weights(0);
             __syncthreads();  // (the columns before these have been used)
             if (threadIdx.x < NC) {
                 const int i = ct * NC + threadIdx.x;
-                int c = i < count ? (KIND == Q4_DENSE ? i : p.plan.lists[first + i]) : -1;
+                int c = i < count ? (p.kind == Q4_DENSE ? i : p.plan.lists[first + i]) : -1;
                 if (c < 0 || c >= total) c = -1;
                 cols[threadIdx.x] = c;
+                rowat[threadIdx.x] = gate_up ? max(c, 0) / p.K : max(c, 0);
             }
             __syncthreads();
             if (!ready) griddep_wait(), ready = true;  // the activation parts
-            const int tiles = min((count - ct * NC + COLS - 1) / COLS, NT);
-            // operands: column g of tile n is part g % PARTS of row g / PARTS; scales: of the rows whose sums the lane keeps
-            uint32_t boff[NT], soff[NT][2 / PARTS];
+            fetch_columns(0);
+            asm volatile("cp.async.commit_group;" ::: "memory");
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int c = max(cols[n * COLS + g / PARTS], 0);
-                const uint32_t row = KIND == Q4_GATE_UP ? c / p.K : c;
-                boff[n] = row * (uint32_t)(16 * p.chunks * PARTS) + (PARTS == 2 ? (g & 1) * 4 : 0) + t;
-#pragma unroll
-                for (int j = 0; j < 2 / PARTS; ++j) {
-                    const int c2 = max(cols[n * COLS + (2 / PARTS) * t + j], 0);
-                    soff[n][j] = (KIND == Q4_GATE_UP ? c2 / p.K : c2) * (uint32_t)(4 * p.chunks);
-                }
+            for (int i = 1; i < kStages - 1; ++i) {
+                fetch_weights(i);
+                fetch_columns(i);
+                asm volatile("cp.async.commit_group;" ::: "memory");
             }
-            float acc[2][NT][AC] = {};
-            uint32_t at = ring;
-            for (int c = c0; c < c1; ++c, at = at + kStageBytes == ring + kStages * kStageBytes ? ring : at + kStageBytes) {
+            float2 acc[2][NT][2] = {};  // [tile][columns][row g, g + 8]: columns 2 t and 2 t + 1
+            for (int step = 0; step < steps; ++step) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-                __syncwarp();
-                fetch(c + kStages - 1);
+                __syncthreads();
+                fetch_weights(step + kStages - 1);
+                fetch_columns(step + kStages - 1);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                const int c = step * p.wk + part_of;
+                if (c >= p.chunks) continue;
                 uint32_t sz[2][2];
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) sz[m][i] = s[m][i] | z[m][i] << 16;
-                scales(c + 1);
+                scales(c + p.wk);
+                const uint32_t at = base_a + (step % kStages) * kTileBytes;
+                const char* bt = smem + kWarps * kStages * kTileBytes + (step % kStages) * stage_b + part_of * (BCHUNK + SCHUNK);
+                const uint4* bcol = reinterpret_cast<const uint4*>(bt) + lane;
+                const float2* bscale = reinterpret_cast<const float2*>(bt + BCHUNK) + t;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    uint32_t words[2][4];  // [m][block 2 half, rows g; rows g + 8; block 2 half + 1, rows g; rows g + 8]
+                    uint32_t words[2][4];  // [m][block 2 half: rows g, rows g + 8; block 2 half + 1: the same]
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
-                        const int r = (lane & 7) + (lane & 8), b = 2 * half + (lane >> 4);
+                        const int r = lane & 15, b = 2 * half + (lane >> 4);
                         load_matrices(words[m], at + m * 1024 + r * 64 + ((b ^ ((r >> 1) & 3)) << 4));
                     }
 #pragma unroll
@@ -204,22 +275,19 @@ __global__ void __launch_bounds__(32 * kWarps, 4) q4_rows_kernel(const RowsParam
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             if (n < tiles) {
-                                const uint4 x = __ldca(p.parts + boff[n] + (uint32_t)(4 * c + b) * (4 * PARTS));
-                                float sx[2 / PARTS];
-#pragma unroll
-                                for (int j = 0; j < 2 / PARTS; ++j) sx[j] = __ldca(p.scales + soff[n][j] + 4 * c + b);
+                                const uint4 x = bcol[(b * NT + n) * 32];
+                                float2 sx = make_float2(1.f, 1.f);
+                                if (FORM != FORM_F32) sx = bscale[(b * NT + n) * 4];
 #pragma unroll
                                 for (int m = 0; m < 2; ++m) {
                                     float d[4];
                                     mma16_first(d, h[m][0][0], h[m][1][0], h[m][0][1], h[m][1][1], x.x, x.y);
                                     mma16(d, h[m][0][2], h[m][1][2], h[m][0][3], h[m][1][3], x.z, x.w);
-                                    if (PARTS == 2) {
-                                        acc[m][n][0] = fmaf(sw[m][0] * sx[0], d[0] + d[1], acc[m][n][0]);
-                                        acc[m][n][1] = fmaf(sw[m][1] * sx[0], d[2] + d[3], acc[m][n][1]);
-                                    } else {
 #pragma unroll
-                                        for (int j = 0; j < 4; ++j)
-                                            acc[m][n][j % AC] = fmaf(sw[m][j >> 1] * sx[(j & 1) % (2 / PARTS)], d[j], acc[m][n][j % AC]);
+                                    for (int i = 0; i < 2; ++i) {
+                                        float2 sc = make_float2(sw[m][i], sw[m][i]);
+                                        if (FORM != FORM_F32) sc = pair_mul(sc, sx);
+                                        pair_fma(acc[m][n][i], sc, d[2 * i], d[2 * i + 1]);
                                     }
                                 }
                             }
@@ -228,49 +296,57 @@ __global__ void __launch_bounds__(32 * kWarps, 4) q4_rows_kernel(const RowsParam
                 }
             }
             asm volatile("cp.async.wait_group 0;" ::: "memory");
-            if (p.wk > 1) {  // the warps' sums of the tile's columns, in their order
+            if (p.wk > 1) {  // the warps' sums of the tile, in the order of their parts
                 __syncthreads();
-                float* red = reinterpret_cast<float*>(smem);
-                if (w % p.wk) {
+                float2* red = reinterpret_cast<float2*>(smem);
+                if (part_of) {
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
 #pragma unroll
-                            for (int j = 0; j < AC; ++j) red[(w * (2 * NT * AC) + (m * NT + n) * AC + j) * 32 + lane] = acc[m][n][j];
+                            for (int i = 0; i < 2; ++i) red[(w * 4 * NT + (m * NT + n) * 2 + i) * 32 + lane] = acc[m][n][i];
                 }
                 __syncthreads();
-                if (w % p.wk == 0) {
+                if (part_of == 0) {
                     for (int k = 1; k < p.wk; ++k)
 #pragma unroll
                         for (int m = 0; m < 2; ++m)
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                                for (int j = 0; j < AC; ++j)
-                                    acc[m][n][j] += red[((w + k) * (2 * NT * AC) + (m * NT + n) * AC + j) * 32 + lane];
+                                for (int i = 0; i < 2; ++i) {
+                                    const float2 v = red[((w + k) * 4 * NT + (m * NT + n) * 2 + i) * 32 + lane];
+                                    acc[m][n][i].x += v.x, acc[m][n][i].y += v.y;
+                                }
                 }
             }
-            if (w % p.wk == 0 && tile < p.row_tiles) {
+            if (part_of == 0 && tile < p.row_tiles) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int j = 0; j < AC; ++j) {
-                        // PARTS 2: j is the row half; PARTS 1: j is row half * 2 + activation row
-                        const int i = PARTS == 2 ? j : j >> 1;
-                        const int c = cols[n * COLS + (2 / PARTS) * t + (PARTS == 2 ? 0 : j & 1)];
-                        if (c < 0) continue;
-                        const int r = r0 + g + 8 * i;
-                        if (KIND == Q4_GATE_UP) {
-                            if (r <= last) p.y[c * p.y_stride + r] = silu_f32(acc[0][n][j]) * acc[1][n][j];
-                        } else {
-                            float* to = KIND == Q4_DENSE ? p.y + c * p.y_stride : p.out + c * p.out_rows;
-                            if (r <= last) to[r] = acc[0][n][j];
-                            if (r + 16 <= last) to[r + 16] = acc[1][n][j];
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2 / PARTS; ++j) {
+                            const int at = n * COLS + (2 / PARTS) * t + j, c = cols[at];
+                            if (n >= tiles || c < 0) continue;
+                            float v[2];
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) {
+                                v[m] = PARTS == 2 ? acc[m][n][i].x + acc[m][n][i].y : j ? acc[m][n][i].y : acc[m][n][i].x;
+                                if (FORM == FORM_F32) v[m] *= p.scales[rowat[at]];
+                            }
+                            const int r = r0 + g + 8 * i;
+                            if (gate_up) {
+                                if (r <= last) p.y[c * p.y_stride + r] = silu_f32(v[0]) * v[1];
+                            } else {
+                                float* to = p.kind == Q4_DENSE ? p.y + c * p.y_stride : p.out + c * p.out_rows;
+                                if (r <= last) to[r] = v[0];
+                                if (r + 16 <= last) to[r + 16] = v[1];
+                            }
                         }
-                    }
             }
-            if (p.wk > 1) __syncthreads();  // (the ring takes the next columns' weights)
+            __syncthreads();  // (the rings take the next columns)
         }
     }
     if (!ready) griddep_wait();  // (a grid ends after the launch before it, whatever its CTAs had to do)
@@ -292,20 +368,36 @@ __global__ void __launch_bounds__(256) q4_combine_kernel(const RowsParams p) {
     }
 }
 
-template <int KIND, int PARTS, int NT>
-cudaError_t run(const RowsParams& p, dim3 grid, cudaStream_t st) {
-    constexpr size_t smem = (size_t)kWarps * kStages * kStageBytes;
-    static_assert(smem >= (size_t)kWarps * 2 * NT * (4 / PARTS) * 128, "the warps' sums fit the ring");
-    const cudaError_t e = cudaFuncSetAttribute(q4_rows_kernel<KIND, PARTS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+constexpr size_t kRowsSmem = 220 << 10;
+
+template <int FORM, int NT>
+cudaError_t run(RowsParams p, int64_t groups, cudaStream_t st) {
+    constexpr int NC = NT * 8 / (FORM == FORM_ONE ? 1 : 2);
+    const int sms = device_info().sms;
+    auto smem = [&](int wk) {
+        return (size_t)kStages * (kWarps * kTileBytes + wk * (NT * 2048 + (FORM == FORM_F32 ? 0 : NT * 128)));
+    };
+    const int64_t zs = p.kind == Q4_DENSE ? min((int64_t)(p.R + NC - 1) / NC, (int64_t)65535) : 1;
+    // Warps that share a tile: as many as it takes to give every SM its CTAs, while their columns fit.
+    p.wk = 1;
+    while (p.wk < kWarps && p.wk * 2 <= p.chunks && smem(p.wk * 2) <= kRowsSmem &&
+           p.row_tiles * groups * zs * p.wk < (int64_t)sms * kWarps)
+        p.wk *= 2;
+    const int side = kWarps / p.wk;
+    const dim3 grid((unsigned)((p.row_tiles + side - 1) / side), (unsigned)min(groups, (int64_t)65535), (unsigned)zs);
+    const cudaError_t e = cudaFuncSetAttribute(q4_rows_kernel<FORM, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmem);
     if (e != cudaSuccess) return e;
-    return launch(q4_rows_kernel<KIND, PARTS, NT>, grid, dim3(32 * kWarps), smem, st, 1, p);
+    return launch(q4_rows_kernel<FORM, NT>, grid, dim3(32 * kWarps), smem(p.wk), st, 1, p);
 }
 
-template <int PARTS, int NT>
-cudaError_t run_kind(int kind, const RowsParams& p, dim3 grid, cudaStream_t st) {
-    if (kind == Q4_DENSE) return run<Q4_DENSE, PARTS, NT>(p, grid, st);
-    if (kind == Q4_GATE_UP) return run<Q4_GATE_UP, PARTS, NT>(p, grid, st);
-    return run<Q4_DOWN, PARTS, NT>(p, grid, st);
+template <int FORM>
+cudaError_t run_columns(const RowsParams& p, int64_t groups, cudaStream_t st) {
+    // Tiles of columns a pass: those that twice an expert's average rows fill.
+    const int64_t rows = p.kind == Q4_DENSE ? p.R : 2 * ((int64_t)p.R * p.K / groups);
+    const int tile = FORM == FORM_ONE ? 8 : 4;
+    if (rows <= 2 * tile) return run<FORM, 2>(p, groups, st);
+    if (rows <= 4 * tile) return run<FORM, 4>(p, groups, st);
+    return run<FORM, 8>(p, groups, st);
 }
 
 }  // namespace
@@ -314,11 +406,12 @@ cudaError_t launch_q4_row(const Q4Call& c, cudaStream_t st);
 
 cudaError_t launch_q4(const Q4Call& c, Carve& ws, cudaStream_t st) {
     if (c.R == 1) return launch_q4_row(c, st);
-    const int parts = c.act.x || c.act.lo ? 2 : 1;
+    const int form = c.act.x ? FORM_F32 : c.act.lo ? FORM_TWO : FORM_ONE;
     RowsParams p = {};
     p.w0 = c.w0;
     p.w1 = c.w1;
     p.act = c.act;
+    p.kind = c.kind;
     p.E = c.E;
     p.out_rows = c.out_rows;
     p.R = (int)c.R;
@@ -331,26 +424,21 @@ cudaError_t launch_q4(const Q4Call& c, Carve& ws, cudaStream_t st) {
     p.y = c.y;
     p.y_stride = c.y_stride;
     p.chunks = (c.w0.cols + 127) / 128;
-    p.parts = ws.take<uint4>((size_t)p.act_rows * p.chunks * 16 * parts);
-    p.scales = ws.take<float>((size_t)p.act_rows * p.chunks * 4);
+    p.row_tiles = (int)((c.out_rows + (c.kind == Q4_GATE_UP ? 15 : 31)) / (c.kind == Q4_GATE_UP ? 16 : 32));
+    p.parts = ws.take<uint4>((size_t)p.act_rows * p.chunks * 16 * (form == FORM_ONE ? 1 : 2));
+    p.scales = ws.take<float>((size_t)p.act_rows * (form == FORM_F32 ? 1 : p.chunks * 4 * form));
     if (c.kind == Q4_DOWN) p.out = ws.take<float>((size_t)c.R * c.K * c.out_rows);
     if (ws.overflow) return cudaSuccess;
     const int sms = device_info().sms;
-    const int64_t octets = p.act_rows * p.chunks * 16;
-    const dim3 lay((unsigned)min((octets + 255) / 256, (int64_t)sms * 8));
-    cudaError_t e = parts == 2 ? launch(q4_parts_kernel<2>, lay, dim3(256), 0, st, 0, p)
-                               : launch(q4_parts_kernel<1>, lay, dim3(256), 0, st, 0, p);
+    const dim3 lay((unsigned)min(p.act_rows, (int64_t)sms * 8));
+    cudaError_t e = form == FORM_F32 ? launch(q4_parts_kernel<FORM_F32>, lay, dim3(256), 0, st, 0, p)
+                    : form == FORM_ONE ? launch(q4_parts_kernel<FORM_ONE>, lay, dim3(256), 0, st, 0, p)
+                                       : launch(q4_parts_kernel<FORM_TWO>, lay, dim3(256), 0, st, 0, p);
     if (e != cudaSuccess) return e;
-    p.row_tiles = (int)((c.out_rows + (c.kind == Q4_GATE_UP ? 15 : 31)) / (c.kind == Q4_GATE_UP ? 16 : 32));
     const int64_t groups = c.kind == Q4_DENSE ? 1 : min(c.E, c.R * c.K);
-    const int nc = 32;
-    const int64_t zs = c.kind == Q4_DENSE ? min((c.R + nc - 1) / nc, (int64_t)65535) : 1;
-    // Warps that share a tile: as many as it takes for 16 warps an SM.
-    p.wk = 1;
-    while (p.wk < kWarps && p.wk * 2 <= p.chunks && p.row_tiles * groups * zs * p.wk < (int64_t)sms * 16) p.wk *= 2;
-    const int side = kWarps / p.wk;
-    const dim3 grid((unsigned)((p.row_tiles + side - 1) / side), (unsigned)min(groups, (int64_t)65535), (unsigned)zs);
-    e = parts == 2 ? run_kind<2, 8>(c.kind, p, grid, st) : run_kind<1, 4>(c.kind, p, grid, st);
+    e = form == FORM_F32   ? run_columns<FORM_F32>(p, groups, st)
+        : form == FORM_ONE ? run_columns<FORM_ONE>(p, groups, st)
+                           : run_columns<FORM_TWO>(p, groups, st);
     if (e != cudaSuccess || c.kind != Q4_DOWN) return e;
     const int64_t n = c.R * c.out_rows;
     return launch(q4_combine_kernel, dim3((unsigned)min((n + 255) / 256, (int64_t)sms * 16)), dim3(256), 0, st, 1, p);
