@@ -12,6 +12,8 @@
 
 namespace q8 {
 
+enum { FORM_F32 = 0, FORM_ONE = 1, FORM_TWO = 2 };  // activations: f32, int8 words, words and low words
+
 // The eight words of w less their zero point, as pairs of f16: values (0, 4), (1, 5), (2, 6), (3, 7).  A word placed in the
 // low mantissa bits of 1024 is 1024 + word, one placed four bits higher 1024 + 16 word = 16 (64 + word): both exact.
 // zc: 1024 + z twice; zf: -(64 + z) twice.
@@ -44,7 +46,7 @@ __device__ __forceinline__ float scale_f32(uint32_t bits, int bf16) {
 
 // d += a b over 16 rows, 8 columns and 16 values (f16 in, f32 sums).
 __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }

@@ -1,12 +1,16 @@
 // Products of 4-bit weights with one activation row: the projection, and a row's experts (gate-up with SwiGLU, and
 // down-and-combine).
 //
-// The work is bound by the weights' bytes, which lanes read straight into registers, 16 bytes (a whole 32-value block of one
-// row) a load.  A warp takes 16 rows by chunks of four blocks: lane (g, t) holds block t of rows g and g + 8, which
-// is an A operand of the warp-wide f16 product if the product's sum over t is kept apart.  Its eight columns do that: column
-// (j, p) holds part p of the activation's block j, and zeros where the lanes with t != j read.  Lane (g, t) then receives the
-// two parts' dots of its own block of its own rows, and scales them by the scales it loaded.  So no weight passes through
-// shared memory or a shuffle, and every group size costs the same.
+// The work is bound by the weights' bytes and, close behind, by the instructions that unpack them.  A warp takes 16 rows by
+// steps of eight 32-value blocks (128 bytes a row), which come through a ring of asynchronous copies of its own; lane (g, t)
+// reads whole blocks of rows g and g + 8 from it, block t of each half step.
+//   - Quantized activations: integer dot products of four bytes, the zero point taken out of the block's sum by the sum of
+//     the activation's words; exact.
+//   - f32 activations: warp-wide f16 products (q4.cuh).  A lane's block is an A operand if the product's sum over t is kept
+//     apart, which its eight columns do: column (j, p) holds part p of the activation's block j, and zeros where the lanes
+//     with t != j read.  Lane (g, t) then receives the two parts' dots of its own block of its own rows.
+// Either way a block's dot meets its scales in the lane that loaded them: nothing is shuffled until a tile ends, and every
+// group size costs the same.
 #include "ffn4.h"
 #include "q4.cuh"
 
@@ -14,111 +18,123 @@ namespace q8 {
 namespace {
 
 constexpr int kRowWarps = 8;
-constexpr int kBlockBytes = 144;  // a block's two parts of 64 bytes, 16 more so that four blocks lie in different banks
+constexpr int kRowStages = 4;       // of a warp's ring
+constexpr int kStepBytes = 16 * 128;  // a step of one tile's rows
+
+// A block of the activation in shared memory.  f32: two parts of 64 bytes, and 16 more so that four blocks lie in different
+// banks (its unit stands in the array behind).  Words: 32 bytes (and 32 of low words), then scale and sum.
+template <int FORM>
+constexpr int block_bytes() { return FORM == FORM_F32 ? 144 : FORM == FORM_ONE ? 48 : 80; }
 
 struct RowParams {
     Q4View w0, w1;
     Q4Act act;
+    int kind;
     int64_t E, out_rows;  // rows a group
     int K;
     const int32_t* ids;
     const float *gates, *residual;
     float* y;
-    int chunks;      // of four blocks, a row
-    int wk;          // warps that share a tile's columns
-    int tiles;       // of 16 * MT rows (all groups')
-    int row_tiles;   // a group's
-    int batch;       // down: hidden rows in shared memory at a time
-    int slices;      // down: warps' tasks a hidden row
-    uint32_t vec;    // bytes of a row's parts in shared memory
+    int steps;            // of a row
+    int parts;            // warps' parts of a row's steps
+    int segs, spw, side;  // a tile's segments (parts, or experts times parts), those a warp takes, tiles side by side
+    int tiles, row_tiles; // of 16 rows: all, a group's
+    int vecs;             // activation rows
+    uint32_t vec;         // bytes of one in shared memory
 };
 
-// The four-block chunk `c` of rows r and r + 8 (while below `rows`) of w.
-struct Chunk {
-    uint4 w[2];
-    uint32_t s[2], z[2];
-};
-
-__device__ __forceinline__ void fetch(Chunk& q, const Q4View& w, int64_t row0, int r, int64_t rows, int c, int nb) {
-    const int t = threadIdx.x & 3, b = 4 * c + t;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (r + 8 * i < rows && b < nb) {
-            const int64_t row = row0 + r + 8 * i;
-            const uint8_t* p = w.q + row * (w.cols >> 1) + 16 * b;
-            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(q.w[i].x), "=r"(q.w[i].y), "=r"(q.w[i].z), "=r"(q.w[i].w)
-                         : "l"(p));
-            const int64_t g = row * (w.cols >> w.group_log2) + ((32 * b) >> w.group_log2);
-            q.s[i] = __ldg(w.s + g);
-            q.z[i] = w.z ? __ldg(w.z + g) : 8u;
-        } else {
-            q.w[i] = make_uint4(0, 0, 0, 0);
-            q.s[i] = 0u;
-            q.z[i] = 8u;
-        }
-    }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// acc[i] += the chunk's block t of row g + 8 i times the activation's.
-__device__ __forceinline__ void multiply(const Chunk& q, const uint4 (&b)[4], float sx, int bf16, float (&acc)[2]) {
-    float d[4] = {0.f, 0.f, 0.f, 0.f};
-    uint32_t zc[2], zf[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) zero_forms(q.z[i], zc[i], zf[i]);
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-        const uint32_t w0 = m == 0 ? q.w[0].x : m == 1 ? q.w[0].y : m == 2 ? q.w[0].z : q.w[0].w;
-        const uint32_t w1 = m == 0 ? q.w[1].x : m == 1 ? q.w[1].y : m == 2 ? q.w[1].z : q.w[1].w;
-        uint32_t h0[4], h1[4];
-        words_f16(w0, zc[0], zf[0], h0);
-        words_f16(w1, zc[1], zf[1], h1);
-        mma16(d, h0[0], h1[0], h0[1], h1[1], b[m].x, b[m].y);
-        mma16(d, h0[2], h1[2], h0[3], h1[3], b[m].z, b[m].w);
-    }
-    acc[0] = fmaf(scale_f32(q.s[0], bf16) * sx, d[0] + d[1], acc[0]);
-    acc[1] = fmaf(scale_f32(q.s[1], bf16) * sx, d[2] + d[3], acc[1]);
-}
-
-// Rows first .. first + n of the activation as parts in shared memory.
-__device__ __forceinline__ void stage_rows(const RowParams& p, char* vecs, int first, int n) {
-    const int octets = 4 * 4 * p.chunks, cols = p.w0.cols;  // eight values each, up to whole chunks
-    for (int i = threadIdx.x; i < ((n * octets + 31) & ~31); i += blockDim.x) {  // whole warps: quads share a block
+// The activation's rows in shared memory, zeros up to whole steps.
+template <int FORM>
+__device__ __forceinline__ void stage_rows(const RowParams& p, char* vecs) {
+    const int octets = 32 * p.steps, cols = p.w0.cols;  // eight values each
+    for (int i = threadIdx.x; i < p.vecs * octets; i += blockDim.x) {  // whole warps, a block's four lanes together
         const int v = i / octets, o = i - v * octets, b = o >> 2;
-        ActParts a;
-        if (p.act.x) {  // a block's four lanes share its unit
+        char* at = vecs + v * p.vec + b * block_bytes<FORM>();
+        if (FORM == FORM_F32) {
             float x[8];
-            act_values(p.act, first + min(v, n - 1), v < n ? o : octets, cols, x);
+            act_values(p.act, v, o, cols, x);
             float m = finite_max(x);
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            a = split_values(x, m);
+            const ActParts a = split_values(x, m);
+            *reinterpret_cast<uint4*>(at + (o & 3) * 16) = a.hi;
+            *reinterpret_cast<uint4*>(at + 64 + (o & 3) * 16) = a.lo;
+            if ((o & 3) == 0) *reinterpret_cast<float*>(vecs + v * p.vec + 8 * p.steps * 144 + 4 * b) = a.scale;
         } else {
-            a = act_words(p.act, first + min(v, n - 1), o, cols);
+            const int64_t from = (int64_t)v * cols + 8 * o;
+            const bool in = 8 * o < cols;
+            int sum = 0;
+#pragma unroll
+            for (int k = 0; k < (FORM == FORM_TWO ? 2 : 1); ++k) {
+                const uint2 x = in ? *reinterpret_cast<const uint2*>((k ? p.act.lo : p.act.q) + from) : make_uint2(0, 0);
+                sum = sum * 128 + __dp4a((int)x.x, 0x01010101, __dp4a((int)x.y, 0x01010101, 0));
+                *reinterpret_cast<uint2*>(at + 32 * k + (o & 3) * 8) =
+                    make_uint2(__byte_perm(x.x, x.y, 0x6420), __byte_perm(x.x, x.y, 0x7531));  // even values, odd values
+            }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            if ((o & 3) == 0) {
+                float scale = in ? p.act.s[from >> 5] : 0.f;
+                if (FORM == FORM_TWO) scale *= 0.0078125f;
+                *reinterpret_cast<float2*>(at + (FORM == FORM_TWO ? 64 : 32)) = make_float2(scale, __int_as_float(sum));
+            }
         }
-        if (v >= n) continue;
-        char* at = vecs + v * p.vec + b * kBlockBytes + (o & 3) * 16;
-        *reinterpret_cast<uint4*>(at) = a.hi;
-        *reinterpret_cast<uint4*>(at + 64) = a.lo;
-        if ((o & 3) == 0) *reinterpret_cast<float*>(vecs + v * p.vec + 4 * p.chunks * kBlockBytes + 4 * b) = a.scale;
     }
 }
 
-// A lane's operand of the product: part g & 1 of block t for the lanes that hold a column of their own block, else zeros.
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int m) { return m == 0 ? v.x : m == 1 ? v.y : m == 2 ? v.z : v.w; }
+
+// An activation block as the lane multiplies it.
+template <int FORM>
 struct Operand {
-    const char *at, *scale;
-    uint32_t step;
+    uint4 v[FORM == FORM_F32 || FORM == FORM_TWO ? 4 : 2];
+    float scale;
+    int sum;
 };
-__device__ __forceinline__ Operand operand(const RowParams& p, const char* vec, const char* zeros) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const bool own = (g >> 1) == t;
-    return Operand{own ? vec + t * kBlockBytes + (g & 1) * 64 : zeros, vec + 4 * p.chunks * kBlockBytes + 4 * t,
-                   own ? 4u * kBlockBytes : 0u};
-}
-__device__ __forceinline__ void load_operand(const Operand& o, int c, uint4 (&b)[4], float& sx) {
+
+// acc[i] += block t of row g + 8 i (words w[i], scale sw[i], zero point z[i]) times the activation's.
+template <int FORM>
+__device__ __forceinline__ void multiply(const uint4 (&w)[2], const float (&sw)[2], const uint32_t (&z)[2], const Operand<FORM>& x,
+                                         float (&acc)[2]) {
+    if (FORM == FORM_F32) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t zc[2], zf[2];
 #pragma unroll
-    for (int m = 0; m < 4; ++m) b[m] = *reinterpret_cast<const uint4*>(o.at + c * o.step + 16 * m);
-    sx = *reinterpret_cast<const float*>(o.scale + 16 * c);
+        for (int i = 0; i < 2; ++i) zero_forms(z[i], zc[i], zf[i]);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            uint32_t h0[4], h1[4];
+            words_f16(word_of(w[0], m), zc[0], zf[0], h0);
+            words_f16(word_of(w[1], m), zc[1], zf[1], h1);
+            mma16(d, h0[0], h1[0], h0[1], h1[1], x.v[m].x, x.v[m].y);
+            mma16(d, h0[2], h1[2], h0[3], h1[3], x.v[m].z, x.v[m].w);
+        }
+        acc[0] = fmaf(sw[0] * x.scale, d[0] + d[1], acc[0]);
+        acc[1] = fmaf(sw[1] * x.scale, d[2] + d[3], acc[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            int hi = 0, lo = 0;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const uint32_t u = word_of(w[i], m);
+                const int even = u & 0x0f0f0f0f, odd = (u >> 4) & 0x0f0f0f0f;
+                const uint4 v = x.v[m >> 1];
+                hi = __dp4a(odd, (int)(m & 1 ? v.w : v.y), __dp4a(even, (int)(m & 1 ? v.z : v.x), hi));
+                if (FORM == FORM_TWO) {
+                    const uint4 l = x.v[(FORM == FORM_TWO ? 2 : 0) + (m >> 1)];
+                    lo = __dp4a(odd, (int)(m & 1 ? l.w : l.y), __dp4a(even, (int)(m & 1 ? l.z : l.x), lo));
+                }
+            }
+            if (FORM == FORM_TWO) hi = hi * 128 + lo;
+            hi -= (int)z[i] * x.sum;
+            acc[i] = fmaf(sw[i] * x.scale, (float)hi, acc[i]);
+        }
+    }
 }
 
 __device__ __forceinline__ float quad_sum(float v) {
@@ -126,202 +142,240 @@ __device__ __forceinline__ float quad_sum(float v) {
     return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
-// The projection (MT = 1: a tile is 16 rows) and the gate-up (MT = 2: a tile is 16 gate rows and the up rows beside them).
-// wk warps share a tile, each `mine` chunks of its columns; a warp's chunks follow one another over all its tiles, DEPTH of
-// them on their way.
-template <int MT, int DEPTH>
+// A CTA takes `side` tiles at a time (all of a tile's segments), its warps their segments' steps one after another over all
+// their tiles.  MT = 2 (gate-up): a tile is 16 gate rows and the 16 up rows beside them.
+template <int FORM, int MT>
 __global__ void __launch_bounds__(32 * kRowWarps, 2) q4_row_kernel(const RowParams p) {
-    extern __shared__ __align__(16) char smem[];
-    __shared__ float part[2][kRowWarps][MT][16];
+    extern __shared__ __align__(128) char smem[];
     __shared__ uint4 zeros[4];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int nb = p.w0.cols >> 5, side = kRowWarps / p.wk;  // tiles that the CTA's warps take side by side
-    const int mine = (p.chunks + p.wk - 1) / p.wk, c0 = (w % p.wk) * mine;
-    const int stride = gridDim.x * side, first = blockIdx.x * side + w / p.wk;
-    const int rounds = (p.tiles - (int)blockIdx.x * side + stride - 1) / stride;  // the CTA's, alike in all its warps
-    // the chunk that is fetched next: its tile, place, group's first row and rows
-    int tile = first, at = 0, r0 = 0;
-    int64_t base = 0, rows = 0;
-    auto locate = [&]() {
-        rows = 0;
-        if (tile >= p.tiles) return;
-        const int group = tile / p.row_tiles, e = p.ids ? p.ids[group] : 0;
-        r0 = 16 * (tile - group * p.row_tiles);
-        if (e >= 0 && e < p.E) base = e * p.out_rows, rows = p.out_rows;
+    const int nb = p.w0.cols >> 5, last = (int)p.out_rows - 1;
+    const int64_t row_bytes = p.w0.cols >> 1, row_groups = p.w0.cols >> p.w0.group_log2;
+    const int mine = (p.steps + p.parts - 1) / p.parts;
+    const int own_seg = p.side > 1 ? w % p.segs : w, off_tile = p.side > 1 ? w / p.segs : 0;
+    const int stride = gridDim.x * p.side, first = off_tile < p.side ? (int)blockIdx.x * p.side + off_tile : p.tiles;
+    const int rounds = (p.tiles - (int)blockIdx.x * p.side + stride - 1) / stride;  // the CTA's, alike in all its warps
+    char* ring = smem + w * (kRowStages * MT * kStepBytes);
+    char* vecs = smem + kRowWarps * kRowStages * MT * kStepBytes;
+    float* part = reinterpret_cast<float*>(vecs + p.vecs * p.vec);  // [2][side * segs][MT][16]
+    const int slots = p.side * p.segs;
+
+    // A place in the warp's run of (tile, segment, step).
+    struct Place {
+        int tile, seg, at, step;  // step: the first of the segment, then the next one
+        int64_t row;              // the lane's row g (less where the tile ends), -1: none
+        int more;                 // rows from there to row g + 8
     };
-    Chunk q[DEPTH][MT];
-    auto next = [&](Chunk (&c)[MT]) {
-        fetch(c[0], p.w0, base, r0 + g, rows, c0 + at, nb);
-        if (MT == 2) fetch(c[MT - 1], p.w1, base, r0 + g, rows, c0 + at, nb);
-        if (++at == mine) {
-            at = 0;
-            tile += stride;
-            locate();
-        }
+    auto locate = [&](Place& l) {
+        l.at = 0;
+        l.row = -1;
+        l.step = l.seg % p.parts * mine;
+        if (l.tile >= p.tiles || l.seg >= p.segs) return;
+        const int group = p.kind == Q4_DOWN ? l.seg / p.parts : l.tile / p.row_tiles;
+        const int r0 = 16 * (p.kind == Q4_DOWN ? l.tile : l.tile - group * p.row_tiles) + g;
+        const int e = p.ids ? p.ids[group] : 0;
+        if (e < 0 || e >= p.E) return;
+        l.row = e * p.out_rows + min(r0, last);
+        l.more = min(r0 + 8, last) - min(r0, last);
     };
-    locate();
+    auto advance = [&](Place& l) {
+        ++l.step;
+        if (++l.at < mine) return;
+        l.seg += kRowWarps;
+        if (p.spw == 1 || l.seg >= p.spw * kRowWarps) l.seg = own_seg, l.tile += stride;
+        locate(l);
+    };
+    Place in = {first, own_seg}, sc = in;
+    locate(in);
+    sc = in;
+    // copies: 16-byte unit u of a row of the step stands at u ^ 4 (row & 1), so that two rows' units lie in different banks
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(ring) + g * 128 + ((t ^ (4 * (g & 1))) << 4);
+    uint32_t into = 0;
+    auto fetch = [&]() {
+        if (in.row >= 0 && in.step < p.steps) {
+            const int64_t from = in.row * row_bytes + 128 * in.step + 16 * t;
+            const bool one = 8 * in.step + t < nb, two = 8 * in.step + 4 + t < nb;
 #pragma unroll
-    for (int i = 0; i < DEPTH; ++i) next(q[i]);
-    if (threadIdx.x < 4) zeros[threadIdx.x] = make_uint4(0, 0, 0, 0);
-    stage_rows(p, smem, 0, 1);
-    __syncthreads();
-    const Operand o = operand(p, smem, reinterpret_cast<const char*>(zeros));
-    float acc[MT][2] = {};
-    int done = 0, own = first, buf = 0;
-    const int total = rounds * mine;
-    for (int it = 0; it < total; it += DEPTH) {
-#pragma unroll
-        for (int k = 0; k < DEPTH; ++k) {
-            if (it + k >= total) break;
-            if (c0 + done < p.chunks) {
-                uint4 b[4];
-                float sx;
-                load_operand(o, c0 + done, b, sx);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) multiply(q[k][m], b, sx, p.w0.bf16, acc[m]);
+            for (int m = 0; m < MT; ++m) {
+                const uint8_t* a = (m ? p.w1.q : p.w0.q) + from;
+                const uint8_t* b = a + in.more * row_bytes;
+                const uint32_t d = to + into + m * kStepBytes;
+                if (one) copy16(d, a), copy16(d + 1024, b);
+                if (two) copy16(d ^ 64, a + 64), copy16((d + 1024) ^ 64, b + 64);
             }
-            next(q[k]);
-            if (++done < mine) continue;
-            // the tile's end: the warps' sums in the order of their columns
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        into = into == (kRowStages - 1) * MT * kStepBytes ? 0 : into + MT * kStepBytes;
+        advance(in);
+    };
+    uint32_t s[MT][2][2], z[MT][2][2];  // the next step's scales and zero points: [half step][row g, g + 8]
+    auto scales = [&]() {
+        const bool ok = sc.row >= 0 && sc.step < p.steps;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int b = 8 * sc.step + 4 * k + t;
+            const bool here = ok && b < nb;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int64_t at = (sc.row + (i ? sc.more : 0)) * row_groups + ((32 * b) >> p.w0.group_log2);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    s[m][k][i] = here ? __ldg((m ? p.w1.s : p.w0.s) + at) : 0u;
+                    z[m][k][i] = here && p.w0.z ? __ldg((m ? p.w1.z : p.w0.z) + at) : 8u;
+                }
+            }
+        }
+        advance(sc);
+    };
+#pragma unroll
+    for (int i = 0; i < kRowStages - 1; ++i) fetch();
+    scales();
+    if (threadIdx.x < 4) zeros[threadIdx.x] = make_uint4(0, 0, 0, 0);
+    stage_rows<FORM>(p, vecs);
+    __syncthreads();
+    const bool own = (g >> 1) == t;  // f32: the lane holds a column of its own block
+    uint32_t from = 0;
+    int buf = 0;
+    for (int round = 0; round < rounds; ++round, buf ^= 1) {
+        const int tile = first + round * stride;
+        for (int k = 0; k < p.spw; ++k) {
+            const int seg = own_seg + k * kRowWarps;
+            const bool real = off_tile < p.side && seg < p.segs;
+            const int step0 = seg % p.parts * mine;
+            const char* vec = vecs + (p.kind == Q4_DOWN && real ? seg / p.parts : 0) * p.vec;
+            float acc[MT][2] = {};
+            for (int i = 0; i < mine; ++i) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kRowStages - 2) : "memory");
+                __syncwarp();
+                fetch();
+                const int step = step0 + i;
+                float sw[MT][2][2];
+                uint32_t zz[MT][2][2];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) sw[m][h][j] = scale_f32(s[m][h][j], p.w0.bf16), zz[m][h][j] = z[m][h][j];
+                scales();
+                if (real && step < p.steps) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int b = 8 * step + 4 * h + t;
+                        Operand<FORM> x;
+                        if (FORM == FORM_F32) {
+                            const char* at = own ? vec + b * 144 + (g & 1) * 64 : reinterpret_cast<const char*>(zeros);
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) x.v[m] = *reinterpret_cast<const uint4*>(at + 16 * m);
+                            x.scale = *reinterpret_cast<const float*>(vec + 8 * p.steps * 144 + 4 * b);
+                        } else {
+                            const char* at = vec + b * block_bytes<FORM>();
+#pragma unroll
+                            for (int m = 0; m < (FORM == FORM_TWO ? 4 : 2); ++m) x.v[m] = *reinterpret_cast<const uint4*>(at + 16 * m);
+                            const float2 f = *reinterpret_cast<const float2*>(at + (FORM == FORM_TWO ? 64 : 32));
+                            x.scale = f.x, x.sum = __float_as_int(f.y);
+                        }
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            const char* at = ring + from + m * kStepBytes + g * 128 + (((t + 4 * h) ^ (4 * (g & 1))) << 4);
+                            const uint4 words[2] = {*reinterpret_cast<const uint4*>(at), *reinterpret_cast<const uint4*>(at + 1024)};
+                            multiply<FORM>(words, sw[m][h], zz[m][h], x, acc[m]);
+                        }
+                    }
+                }
+                from = from == (kRowStages - 1) * MT * kStepBytes ? 0 : from + MT * kStepBytes;
+            }
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const float v = quad_sum(acc[m][i]);
-                    if (t == 0) part[buf][w][m][g + 8 * i] = v;
-                    acc[m][i] = 0.f;
+                    if (t == 0 && real) part[((buf * slots + off_tile * p.segs + seg) * MT + m) * 16 + g + 8 * i] = v;
                 }
-            if (p.wk > 1) __syncthreads();
-            else __syncwarp();
-            if (w % p.wk == 0 && lane < 16 && own < p.tiles) {
-                const int group = own / p.row_tiles, r = 16 * (own - group * p.row_tiles) + lane;
+        }
+        __syncthreads();  // (the next tiles' sums go to the other half: one barrier a round)
+        if (own_seg == 0 && lane < 16 && tile < p.tiles) {
+            const float* sums = part + (buf * slots + off_tile * p.segs) * MT * 16 + lane;
+            if (p.kind == Q4_DOWN) {
+                const int r = 16 * tile + lane;
+                float sum = 0.f;
+                for (int j = 0; j < p.K; ++j) {
+                    const int e = p.ids[j];
+                    if (e < 0 || e >= p.E) continue;
+                    float v = 0.f;
+                    for (int i = 0; i < p.parts; ++i) v += sums[(j * p.parts + i) * 16];
+                    sum = fmaf(p.gates[j], v, sum);
+                }
+                if (r <= last) p.y[r] = p.residual ? p.residual[r] + sum : sum;
+            } else {
+                const int group = tile / p.row_tiles, r = 16 * (tile - group * p.row_tiles) + lane;
+                const int e = p.ids ? p.ids[group] : 0;
                 float v[MT] = {};
-                for (int j = 0; j < p.wk; ++j)
+                for (int i = 0; i < p.segs; ++i)
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) v[m] += part[buf][w + j][m][lane];
-                bool ok = r < p.out_rows;
-                if (p.ids && ok) {
-                    const int e = p.ids[group];
-                    ok = e >= 0 && e < p.E;
-                }
-                if (ok) p.y[group * p.out_rows + r] = MT == 2 ? silu_f32(v[0]) * v[MT - 1] : v[0];
+                    for (int m = 0; m < MT; ++m) v[m] += sums[(i * MT + m) * 16];
+                if (r <= last && e >= 0 && e < p.E) p.y[group * p.out_rows + r] = MT == 2 ? silu_f32(v[0]) * v[MT - 1] : v[0];
             }
-            buf ^= 1;  // (the next tile's sums go to the other half: one barrier a tile)
-            done = 0;
-            own += stride;
         }
     }
 }
 
-// Down-and-combine: a CTA takes 16 output rows of all the row's experts, its warps (hidden row, part of its columns) tasks;
-// the sums meet in shared memory and are added up in the order of the experts.  Hidden rows come `batch` at a time.
-template <int DEPTH>
-__global__ void __launch_bounds__(32 * kRowWarps, 2) q4_down_row_kernel(const RowParams p) {
-    extern __shared__ __align__(16) char smem[];
-    __shared__ uint4 zeros[4];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int nb = p.w0.cols >> 5, r0 = 16 * blockIdx.x;
-    float* part = reinterpret_cast<float*>(smem + (size_t)p.batch * p.vec);  // [K * slices][16]
-    const int mine = (p.chunks + p.slices - 1) / p.slices;
-    const int per = (p.batch * p.slices + kRowWarps - 1) / kRowWarps;  // tasks a warp and batch
-    const int batches = (p.K + p.batch - 1) / p.batch;
-    // the chunk that is fetched next
-    int task = 0, batch = 0, at = 0, c0 = 0;
-    int64_t base = 0, rows = 0;
-    auto expert = [&](int j) {  // the hidden row's expert, or -1
-        const int e = j < p.K ? p.ids[j] : -1;
-        return e >= 0 && e < p.E ? e : -1;
-    };
-    auto place = [&](int b, int i, int& j, int& s) {  // task i of this warp in batch b: hidden row and part (j = K: none)
-        const int k = i * kRowWarps + w;
-        s = k % p.slices;
-        j = k / p.slices < p.batch && b < batches ? b * p.batch + k / p.slices : p.K;
-        j = min(j, p.K);
-    };
-    auto locate = [&]() {
-        int j, s;
-        place(batch, task, j, s);
-        const int e = expert(j);
-        c0 = s * mine;
-        rows = 0;
-        if (e >= 0) base = e * p.out_rows, rows = p.out_rows;
-    };
-    Chunk q[DEPTH];
-    auto next = [&](Chunk& c) {
-        fetch(c, p.w0, base, r0 + g, at < mine ? rows : 0, c0 + at, nb);
-        if (++at == mine) {
-            at = 0;
-            if (++task == per) task = 0, ++batch;
-            locate();
-        }
-    };
-    locate();
-#pragma unroll
-    for (int i = 0; i < DEPTH; ++i) next(q[i]);
-    if (threadIdx.x < 4) zeros[threadIdx.x] = make_uint4(0, 0, 0, 0);
-    float acc[2] = {};
-    int done = 0, my_task = 0, my_batch = 0, j, s;
-    Operand o = {};
-    const int total = batches * per * mine;
-    for (int it = 0; it < total; it += DEPTH) {
-#pragma unroll
-        for (int k = 0; k < DEPTH; ++k) {
-            if (it + k >= total) break;
-            if (done == 0) {
-                if (my_task == 0) {  // (all warps alike)
-                    if (my_batch > 0) __syncthreads();
-                    stage_rows(p, smem, my_batch * p.batch, min(p.batch, p.K - my_batch * p.batch));
-                    __syncthreads();
-                }
-                place(my_batch, my_task, j, s);
-                o = operand(p, smem + (size_t)(min(j, p.K - 1) - my_batch * p.batch) * p.vec, reinterpret_cast<const char*>(zeros));
-            }
-            if (j < p.K && s * mine + done < p.chunks) {
-                uint4 b[4];
-                float sx;
-                load_operand(o, s * mine + done, b, sx);
-                multiply(q[k], b, sx, p.w0.bf16, acc);
-            }
-            next(q[k]);
-            if (++done < mine) continue;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float v = quad_sum(acc[i]);
-                if (t == 0 && j < p.K) part[(j * p.slices + s) * 16 + g + 8 * i] = v;
-                acc[i] = 0.f;
-            }
-            done = 0;
-            if (++my_task == per) my_task = 0, ++my_batch;
-        }
-    }
-    __syncthreads();
-    const int r = r0 + threadIdx.x;
-    if (threadIdx.x >= 16 || r >= p.out_rows) return;
-    float sum = 0.f;
-    for (int k = 0; k < p.K; ++k) {
-        if (expert(k) < 0) continue;
-        float v = 0.f;
-        for (int i = 0; i < p.slices; ++i) v += part[(k * p.slices + i) * 16 + threadIdx.x];
-        sum = fmaf(p.gates[k], v, sum);
-    }
-    p.y[r] = p.residual ? p.residual[r] + sum : sum;
+constexpr size_t kRowSmem = 220 << 10;
+
+size_t row_smem(const RowParams& p, int mt) {
+    return (size_t)kRowWarps * kRowStages * mt * kStepBytes + (size_t)p.vecs * p.vec + 2 * (size_t)p.side * p.segs * mt * 64;
 }
 
-constexpr size_t kRowSmem = 200 << 10;
+// How a tile's steps are dealt to the warps: `parts` of a row each (of an expert's, for down).
+void deal(RowParams& p, int parts) {
+    p.parts = parts;
+    p.segs = p.kind == Q4_DOWN ? p.K * parts : parts;
+    p.spw = (p.segs + kRowWarps - 1) / kRowWarps;
+    p.side = p.spw > 1 ? 1 : kRowWarps / p.segs;
+}
 
-template <typename Kern>
-cudaError_t allow_smem(Kern kernel, size_t smem) {
-    return smem > (48 << 10) - 4096 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
-                                    : cudaSuccess;
+template <int FORM, int MT>
+cudaError_t run(const RowParams& p, cudaStream_t st) {
+    const size_t smem = row_smem(p, MT);
+    const cudaError_t e = cudaFuncSetAttribute(q4_row_kernel<FORM, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowSmem);
+    if (e != cudaSuccess) return e;
+    const int64_t ctas = (p.tiles + p.side - 1) / p.side, most = (int64_t)device_info().sms * 2;
+    return launch(q4_row_kernel<FORM, MT>, dim3((unsigned)min(ctas, most)), dim3(32 * kRowWarps), smem, st, 0, p);
+}
+
+template <int FORM>
+cudaError_t run_kind(RowParams p, cudaStream_t st) {
+    p.vec = (uint32_t)(8 * p.steps * (block_bytes<FORM>() + (FORM == FORM_F32 ? 4 : 0)));
+    // The parts that leave the warps of two CTAs an SM the fewest steps one after another.
+    int best = 1;
+    int64_t fewest = INT64_MAX;
+    for (int parts = 1; parts <= 8 && parts <= p.steps; ++parts) {
+        if (p.kind != Q4_DOWN && (parts & (parts - 1))) continue;
+        deal(p, parts);
+        const int64_t at_once = (int64_t)device_info().sms * 2 * p.side;
+        const int64_t steps = (p.tiles + at_once - 1) / at_once * p.spw * ((p.steps + parts - 1) / parts);
+        if (steps < fewest) fewest = steps, best = parts;
+    }
+    deal(p, best);
+    return p.kind == Q4_GATE_UP ? run<FORM, 2>(p, st) : run<FORM, 1>(p, st);
 }
 
 }  // namespace
+
+// Whether the row's activations fit a CTA (an expert's hidden rows may be many and long).
+bool q4_row_fits(const Q4Call& c) {
+    const size_t steps = (c.w0.cols + 255) / 256, vecs = c.kind == Q4_DOWN ? c.K : 1;
+    const size_t block = c.act.x ? 148 : c.act.lo ? 80 : 48;
+    const size_t mt = c.kind == Q4_GATE_UP ? 2 : 1, segs = 8 * vecs;
+    return (size_t)kRowWarps * kRowStages * mt * kStepBytes + vecs * steps * 8 * block + 2 * segs * mt * 64 <= kRowSmem;
+}
 
 cudaError_t launch_q4_row(const Q4Call& c, cudaStream_t st) {
     RowParams p = {};
     p.w0 = c.w0;
     p.w1 = c.w1;
     p.act = c.act;
+    p.kind = c.kind;
     p.E = c.E;
     p.out_rows = c.out_rows;
     p.K = c.K;
@@ -329,40 +383,12 @@ cudaError_t launch_q4_row(const Q4Call& c, cudaStream_t st) {
     p.gates = c.gates;
     p.residual = c.residual;
     p.y = c.y;
-    p.chunks = (c.w0.cols + 127) / 128;
-    p.vec = (uint32_t)p.chunks * (4 * kBlockBytes + 16);
+    p.steps = (c.w0.cols + 255) / 256;
+    p.vecs = c.kind == Q4_DOWN ? c.K : 1;
     p.row_tiles = (int)((c.out_rows + 15) / 16);
-    const int sms = device_info().sms;
-    if (c.kind == Q4_DOWN) {
-        p.batch = (int)min((size_t)c.K, kRowSmem / p.vec);
-        // parts of a hidden row: what leaves the warps the fewest chunks one after another
-        p.slices = 1;
-        auto steps = [&](int s) { return (p.batch * s + kRowWarps - 1) / kRowWarps * ((p.chunks + s - 1) / s); };
-        for (int s = 2; s <= 8 && s <= p.chunks; ++s)
-            if (steps(s) < steps(p.slices)) p.slices = s;
-        const size_t smem = (size_t)p.batch * p.vec + (size_t)c.K * p.slices * 64;
-        const cudaError_t e = allow_smem(q4_down_row_kernel<6>, smem);
-        if (e != cudaSuccess) return e;
-        return launch(q4_down_row_kernel<6>, dim3((unsigned)p.row_tiles), dim3(32 * kRowWarps), smem, st, 0, p);
-    }
     p.tiles = p.row_tiles * (c.kind == Q4_GATE_UP ? c.K : 1);
-    // Warps that share a tile: those that leave the fewest chunks one after another on two CTAs an SM.
-    auto steps = [&](int wk) {
-        const int64_t slots = (int64_t)sms * 2 * (kRowWarps / wk);
-        return (p.tiles + slots - 1) / slots * ((p.chunks + wk - 1) / wk);
-    };
-    p.wk = 1;
-    for (int wk = 2; wk <= kRowWarps; wk *= 2)
-        if (steps(wk) < steps(p.wk)) p.wk = wk;
-    const int side = kRowWarps / p.wk;
-    const int64_t grid = min((int64_t)(p.tiles + side - 1) / side, (int64_t)sms * 2);
-    cudaError_t e;
-    if (c.kind == Q4_GATE_UP) {
-        if ((e = allow_smem(q4_row_kernel<2, 2>, p.vec)) != cudaSuccess) return e;
-        return launch(q4_row_kernel<2, 2>, dim3((unsigned)grid), dim3(32 * kRowWarps), p.vec, st, 0, p);
-    }
-    if ((e = allow_smem(q4_row_kernel<1, 4>, p.vec)) != cudaSuccess) return e;
-    return launch(q4_row_kernel<1, 4>, dim3((unsigned)grid), dim3(32 * kRowWarps), p.vec, st, 0, p);
+    if (c.act.x) return run_kind<FORM_F32>(p, st);
+    return c.act.lo ? run_kind<FORM_TWO>(p, st) : run_kind<FORM_ONE>(p, st);
 }
 
 }  // namespace q8

@@ -17,8 +17,6 @@ constexpr int kWarps = 8;    // a CTA
 constexpr int kStages = 4;   // of the rings: a stage is a chunk of four blocks for each of the warps that share a tile
 constexpr int kTileBytes = 2 * 16 * 64;
 
-enum { FORM_F32 = 0, FORM_ONE = 1, FORM_TWO = 2 };
-
 struct RowsParams {
     Q4View w0, w1;
     Q4Act act;
@@ -96,7 +94,7 @@ __device__ __forceinline__ void load_matrices(uint32_t (&m)[4], uint32_t at) {
 // d = a b, without an addend.
 __device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                             uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
@@ -135,15 +133,15 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1) q4_rows_kernel(c
     const Q4View& second = gate_up ? p.w1 : p.w0;
     bool ready = false;
     int groups = 1;
-    if (p.kind != Q4_DENSE) groups = min(max(p.plan.active[0], 0), (int)min(p.E, (int64_t)total));
+    if (p.kind != Q4_DENSE) groups = p.plan.active ? min(max(p.plan.active[0], 0), (int)min(p.E, (int64_t)total)) : p.K;
     griddep_launch();
     for (int a = blockIdx.y; a < groups; a += gridDim.y) {
         int e = 0, first = 0, count = p.R;
         if (p.kind != Q4_DENSE) {
-            e = p.plan.active[1 + a];
+            e = p.plan.active ? p.plan.active[1 + a] : p.ids[a];  // (one row has no plan: every choice is a group)
             if (e < 0 || e >= p.E) continue;
-            first = max(p.plan.offsets[e], 0);
-            count = min(p.plan.offsets[e + 1], total) - first;
+            first = p.plan.active ? max(p.plan.offsets[e], 0) : a;
+            count = p.plan.active ? min(p.plan.offsets[e + 1], total) - first : 1;
         }
         // the lane's rows of the two weight tiles: rows g and g + 8 of each; they clamp to the group's last row
         const int64_t base = (int64_t)e * p.out_rows;
@@ -215,7 +213,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1) q4_rows_kernel(c
             __syncthreads();  // (the columns before these have been used)
             if (threadIdx.x < NC) {
                 const int i = ct * NC + threadIdx.x;
-                int c = i < count ? (p.kind == Q4_DENSE ? i : p.plan.lists[first + i]) : -1;
+                int c = i < count ? (p.kind == Q4_DENSE ? i : p.plan.active ? p.plan.lists[first + i] : first) : -1;
                 if (c < 0 || c >= total) c = -1;
                 cols[threadIdx.x] = c;
                 rowat[threadIdx.x] = gate_up ? max(c, 0) / p.K : max(c, 0);
@@ -402,10 +400,11 @@ cudaError_t run_columns(const RowsParams& p, int64_t groups, cudaStream_t st) {
 
 }  // namespace
 
+bool q4_row_fits(const Q4Call& c);
 cudaError_t launch_q4_row(const Q4Call& c, cudaStream_t st);
 
 cudaError_t launch_q4(const Q4Call& c, Carve& ws, cudaStream_t st) {
-    if (c.R == 1) return launch_q4_row(c, st);
+    if (c.R == 1 && q4_row_fits(c)) return launch_q4_row(c, st);
     const int form = c.act.x ? FORM_F32 : c.act.lo ? FORM_TWO : FORM_ONE;
     RowsParams p = {};
     p.w0 = c.w0;
@@ -435,7 +434,7 @@ cudaError_t launch_q4(const Q4Call& c, Carve& ws, cudaStream_t st) {
                     : form == FORM_ONE ? launch(q4_parts_kernel<FORM_ONE>, lay, dim3(256), 0, st, 0, p)
                                        : launch(q4_parts_kernel<FORM_TWO>, lay, dim3(256), 0, st, 0, p);
     if (e != cudaSuccess) return e;
-    const int64_t groups = c.kind == Q4_DENSE ? 1 : min(c.E, c.R * c.K);
+    const int64_t groups = c.kind == Q4_DENSE ? 1 : c.R == 1 ? c.K : min(c.E, c.R * c.K);
     e = form == FORM_F32   ? run_columns<FORM_F32>(p, groups, st)
         : form == FORM_ONE ? run_columns<FORM_ONE>(p, groups, st)
                            : run_columns<FORM_TWO>(p, groups, st);

@@ -493,6 +493,24 @@ def test_experts(q8, ws, rows, E, k, d, dff, group, kind, zeros, skew, form):
     del kept
 
 
+@pytest.mark.parametrize("E,k,d,dff", [(3, 2, 32768, 32), (4, 3, 64, 32768), (9, 8, 128, 8192)])
+def test_experts_of_a_row_longer_than_a_cta_holds(q8, ws, E, k, d, dff):
+    """One row whose activations do not fit a CTA, with the same expert chosen twice and one out of range."""
+    import torch
+    g = gen(d + dff)
+    gate, up, down = (matrix(torch, n, c, 32, "f16", True, g) for n, c in ((E * dff, d), (E * dff, d), (E * d, dff)))
+    ids = choices(torch, 1, E, k, g, False)
+    ids[0, 0] = ids[0, 1]
+    gates = torch.rand(1, k, generator=g, device="cuda")
+    x = torch.randn(1, d, generator=g, device="cuda") / 64
+    h = torch.full((1, k, dff), math.nan, device="cuda")
+    q8.moe_gate_up_q4(q8.q4_mat(*gate), q8.q4_mat(*up), ids, h, x=x, ws=ws)
+    check_hidden(torch, h, values(torch, gate), values(torch, up), x.double(), ids, dff, "f32")
+    y = torch.empty(1, d, device="cuda")
+    q8.moe_down_combine_q4(q8.q4_mat(*down), ids, gates, y, h=h, ws=ws)
+    check_combined(torch, y, values(torch, down), h.double(), ids, gates, None, d, "f32")
+
+
 def test_experts_out_of_range_and_the_same_expert_twice(q8, ws):
     import torch
     g = gen(1)
