@@ -33,11 +33,14 @@ __device__ __forceinline__ void words_f16(uint32_t w, uint32_t zc, uint32_t zf, 
     }
 }
 
-// The two forms of a zero point that words_f16 takes.
+// The two forms of a zero point that words_f16 takes, the second from the first.
+__device__ __forceinline__ uint32_t zero_less(uint32_t zc) {
+    const __half2 v = __hsub2(__float2half2_rn(960.f), *reinterpret_cast<__half2*>(&zc));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
 __device__ __forceinline__ void zero_forms(uint32_t z, uint32_t& zc, uint32_t& zf) {
     zc = 0x64006400u | (z * 0x10001u);
-    const __half2 v = __hsub2(__float2half2_rn(960.f), *reinterpret_cast<__half2*>(&zc));
-    zf = *reinterpret_cast<const uint32_t*>(&v);
+    zf = zero_less(zc);
 }
 
 __device__ __forceinline__ float scale_f32(uint32_t bits, int bf16) {

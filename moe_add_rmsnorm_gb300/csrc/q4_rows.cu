@@ -78,8 +78,11 @@ __global__ void __launch_bounds__(256) q4_parts_kernel(const RowsParams p) {
     }
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void zero16(uint32_t dst) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void copy_small(uint32_t dst, const void* src) {
@@ -123,11 +126,21 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1) q4_rows_kernel(c
     __shared__ uint32_t rowat[NC];     // their activation rows
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int side = kWarps / p.wk, tile = blockIdx.x * side + w / p.wk, part_of = w % p.wk;
-    const int nb = p.w0.cols >> 5, ngroups = p.w0.cols >> p.w0.group_log2;
+    const int nb = p.w0.cols >> 5, ngroups = p.w0.cols >> p.w0.group_log2, row_bytes = p.w0.cols >> 1;
     const int steps = (p.chunks + p.wk - 1) / p.wk;
+    // The rings.  Of a chunk of weights, block t of row r of 16 stands at 64 r + 16 (t ^ (r >> 1 & 3)), so that the eight rows
+    // of a matrix load lie in different banks.
+    char* columns = smem + kWarps * kStages * kTileBytes;
     const uint32_t base_a = (uint32_t)__cvta_generic_to_shared(smem) + w * (kStages * kTileBytes);
-    const uint32_t base_b = (uint32_t)__cvta_generic_to_shared(smem) + kWarps * kStages * kTileBytes;
-    const uint32_t stage_b = p.wk * (BCHUNK + SCHUNK);
+    const uint32_t base_b = (uint32_t)__cvta_generic_to_shared(columns), stage_b = p.wk * (BCHUNK + SCHUNK);
+    const uint32_t ring_at = base_a + g * 64 + ((t ^ ((g >> 1) & 3)) << 4);
+    const uint32_t matrix_at = base_a + (lane & 15) * 64 + (((lane >> 4) ^ ((lane >> 1) & 3)) << 4);
+    // Of a chunk of columns the thread copies unit (block, part, word) of rows unit_row, + 2 kWarps / PARTS, ...
+    constexpr int NU = NT * 8 * 16 / (32 * kWarps);
+    const int unit_of = threadIdx.x % (16 * PARTS), unit_row = threadIdx.x / (16 * PARTS);
+    const uint32_t unit_at = (((unit_of / (4 * PARTS)) * NT * 8 + unit_row * PARTS + (unit_of >> 2) % PARTS) * 4 + (unit_of & 3)) * 16;
+    const uint32_t scale_at = BCHUNK + ((threadIdx.x % 4) * NT * 8 + threadIdx.x / 4 * PARTS) * 4;
+    const bool has_z = p.w0.z != nullptr;
     const int total = p.R * p.K;
     const bool gate_up = p.kind == Q4_GATE_UP;
     const Q4View& second = gate_up ? p.w1 : p.w0;
@@ -143,73 +156,77 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1) q4_rows_kernel(c
             first = p.plan.active ? max(p.plan.offsets[e], 0) : a;
             count = p.plan.active ? min(p.plan.offsets[e + 1], total) - first : 1;
         }
-        // the lane's rows of the two weight tiles: rows g and g + 8 of each; they clamp to the group's last row
+        // The lane's rows of the two weight tiles, rows g and g + 8 of each (they clamp to the group's last row), as offsets
+        // from the first tile row's words and scales, which run on from chunk to chunk.
         const int64_t base = (int64_t)e * p.out_rows;
-        const int r0 = (gate_up ? 16 : 32) * tile, last = (int)p.out_rows - 1;
-        const uint8_t* src[2][2];
-        int64_t sg[2][2];
+        const int r0 = (gate_up ? 16 : 32) * tile, last = (int)p.out_rows - 1, top = min(r0, last);
+        const uint8_t *qa = p.w0.q + (base + top) * row_bytes, *qb = second.q + (base + top) * row_bytes;
+        const uint16_t *sa = p.w0.s + (base + top) * ngroups, *sb = second.s + (base + top) * ngroups;
+        const uint8_t *za = p.w0.z + (base + top) * ngroups, *zb = second.z + (base + top) * ngroups;
+        int row[2][2];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int64_t r = base + min(r0 + (gate_up ? 0 : 16 * m) + g + 8 * i, last);
-                src[m][i] = (m == 0 ? p.w0.q : second.q) + r * (p.w0.cols >> 1) + 16 * t;
-                sg[m][i] = r * ngroups;
-            }
+            for (int i = 0; i < 2; ++i) row[m][i] = min(r0 + (gate_up ? 0 : 16 * m) + g + 8 * i, last) - top;
         for (int ct = blockIdx.z; ct * NC < count; ct += gridDim.z) {
             const int tiles = min((count - ct * NC + COLS - 1) / COLS, NT);
             uint32_t s[2][2], z[2][2];  // the next chunk's scales and zero points: lane t block t's
-            auto scales = [&](int c) {
-                const int b = 4 * c + t;
+            int sc = part_of;           // that chunk
+            auto scales = [&]() {
+                const int b = 4 * sc + t, at = (32 * b) >> p.w0.group_log2;
                 const bool in = b < nb;
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int64_t at = sg[m][i] + ((32 * b) >> p.w0.group_log2);
-                        s[m][i] = in ? __ldg((m == 0 ? p.w0.s : second.s) + at) : 0u;
-                        z[m][i] = in && p.w0.z ? __ldg((m == 0 ? p.w0.z : second.z) + at) : 8u;
+                        const int k = row[m][i] * ngroups + at;
+                        s[m][i] = in ? __ldg((m == 0 ? sa : sb) + k) : 0u;
+                        if (has_z) z[m][i] = in ? __ldg((m == 0 ? za : zb) + k) : 8u;
                     }
+                sc += p.wk;
             };
-            auto fetch_weights = [&](int step) {
-                const int c = step * p.wk + part_of;
-                if (step >= steps || c >= p.chunks) return;
-                const uint32_t at = base_a + (step % kStages) * kTileBytes;
-                const bool in = 4 * c + t < nb;
+            int wc = part_of;  // the chunk of weights that is fetched next, its place in the ring, and of the columns'
+            uint32_t wat = 0, bat = 0;
+            int bc = 0;
+            auto fetch_weights = [&]() {
+                if (wc < p.chunks) {
+                    const uint32_t to = ring_at + wat;
+                    const int from = 64 * wc + 16 * t;
+                    if (4 * wc + t < nb) {
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+                        for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = g + 8 * i;
-                        copy16(at + m * 1024 + r * 64 + ((t ^ ((r >> 1) & 3)) << 4), in ? src[m][i] + 64 * c : p.w0.q, in);
+                            for (int i = 0; i < 2; ++i)
+                                copy16(to + m * 1024 + i * 512, (m == 0 ? qa : qb) + (row[m][i] * row_bytes + from));
+                    } else {  // (columns past the last: zeros in the activations, anything finite here)
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) zero16(to + m * 512);
                     }
-            };
-            auto fetch_columns = [&](int step) {  // all warps: the stage's chunks of the columns
-                if (step >= steps) return;
-                const uint32_t at = base_b + (step % kStages) * stage_b;
-                const int rows = tiles * COLS, units = rows * 16 * PARTS;
-                for (int j = 0; j < p.wk; ++j) {
-                    const int c = step * p.wk + j;
-                    if (c >= p.chunks) break;
-                    const uint32_t to = at + j * (BCHUNK + SCHUNK);
-                    for (int u = threadIdx.x; u < units; u += 32 * kWarps) {
-                        const int row = u / (16 * PARTS), v = u % (16 * PARTS);  // v = (block, part, word)
-                        const int b = v / (4 * PARTS), part = (v >> 2) % PARTS;
-                        copy16(to + (((b * NT * 8 + row * PARTS + part) << 2) + (v & 3)) * 16,
-                               p.parts + rowat[row] * (size_t)(16 * PARTS) * p.chunks + c * (16 * PARTS) + v, true);
-                    }
-                    if (FORM != FORM_F32)
-                        for (int u = threadIdx.x; u < rows * 4; u += 32 * kWarps) {
-                            const int row = u >> 2, b = u & 3;
-                            const size_t from = rowat[row] * (size_t)(4 * p.chunks) + 4 * c + b;
-                            if (FORM == FORM_ONE) copy_small<4>(to + BCHUNK + (b * NT * 8 + row) * 4, p.scales + from);
-                            else copy_small<8>(to + BCHUNK + (b * NT * 8 + 2 * row) * 4, p.scales + 2 * from);
-                        }
                 }
+                wc += p.wk;
+                wat = wat == (kStages - 1) * kTileBytes ? 0 : wat + kTileBytes;
+            };
+            uint32_t goff[NU];  // the thread's 16-byte units of a chunk of the columns
+            const float* sfrom = p.scales;  // and its scale (words: of block threadIdx.x % 4 of row threadIdx.x / 4)
+            const int rows_here = tiles * COLS;
+            auto fetch_columns = [&]() {  // all warps: the stage's chunks of the columns
+                for (int j = 0; j < p.wk && bc < p.chunks; ++j, ++bc) {
+                    const uint32_t to = base_b + bat + j * (BCHUNK + SCHUNK) + unit_at;
+#pragma unroll
+                    for (int k = 0; k < NU; ++k)
+                        if (unit_row + k * (kWarps * 2 / PARTS) < rows_here)
+                            copy16(to + k * 1024, p.parts + (goff[k] + (uint32_t)bc * (16 * PARTS)));
+                    if (FORM != FORM_F32 && (int)threadIdx.x < 4 * rows_here) {
+                        const uint32_t sto = base_b + bat + j * (BCHUNK + SCHUNK) + scale_at;
+                        if (FORM == FORM_ONE) copy_small<4>(sto, sfrom + 4 * bc);
+                        else copy_small<8>(sto, sfrom + 8 * bc);
+                    }
+                }
+                bat = bat == (kStages - 1) * stage_b ? 0 : bat + stage_b;
             };
             // weights first: they depend on no launch before
-            scales(part_of);
-            fetch_weights(0);
+            scales();
+            fetch_weights();
             __syncthreads();  // (the columns before these have been used)
             if (threadIdx.x < NC) {
                 const int i = ct * NC + threadIdx.x;
@@ -219,79 +236,86 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1) q4_rows_kernel(c
                 rowat[threadIdx.x] = gate_up ? max(c, 0) / p.K : max(c, 0);
             }
             __syncthreads();
+#pragma unroll
+            for (int k = 0; k < NU; ++k)
+                goff[k] = rowat[min(unit_row + k * (kWarps * 2 / PARTS), NC - 1)] * (uint32_t)(16 * PARTS * p.chunks) + unit_of;
+            if (FORM != FORM_F32)
+                sfrom = p.scales + ((size_t)rowat[min((int)threadIdx.x / 4, NC - 1)] * (4 * p.chunks) + threadIdx.x % 4) * PARTS;
             if (!ready) griddep_wait(), ready = true;  // the activation parts
-            fetch_columns(0);
+            fetch_columns();
             asm volatile("cp.async.commit_group;" ::: "memory");
 #pragma unroll
             for (int i = 1; i < kStages - 1; ++i) {
-                fetch_weights(i);
-                fetch_columns(i);
+                fetch_weights();
+                fetch_columns();
                 asm volatile("cp.async.commit_group;" ::: "memory");
             }
             float2 acc[2][NT][2] = {};  // [tile][columns][row g, g + 8]: columns 2 t and 2 t + 1
-            for (int step = 0; step < steps; ++step) {
+            uint32_t at = 0, bt = 0;
+            for (int c = part_of, step = 0; step < steps; ++step, c += p.wk) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
                 __syncthreads();
-                fetch_weights(step + kStages - 1);
-                fetch_columns(step + kStages - 1);
+                fetch_weights();
+                fetch_columns();
                 asm volatile("cp.async.commit_group;" ::: "memory");
-                const int c = step * p.wk + part_of;
-                if (c >= p.chunks) continue;
-                uint32_t sz[2][2];
+                float so[2][2];
+                uint32_t zo[2][2];
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) sz[m][i] = s[m][i] | z[m][i] << 16;
-                scales(c + p.wk);
-                const uint32_t at = base_a + (step % kStages) * kTileBytes;
-                const char* bt = smem + kWarps * kStages * kTileBytes + (step % kStages) * stage_b + part_of * (BCHUNK + SCHUNK);
-                const uint4* bcol = reinterpret_cast<const uint4*>(bt) + lane;
-                const float2* bscale = reinterpret_cast<const float2*>(bt + BCHUNK) + t;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t words[2][4];  // [m][block 2 half: rows g, rows g + 8; block 2 half + 1: the same]
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        const int r = lane & 15, b = 2 * half + (lane >> 4);
-                        load_matrices(words[m], at + m * 1024 + r * 64 + ((b ^ ((r >> 1) & 3)) << 4));
+                    for (int i = 0; i < 2; ++i) {
+                        so[m][i] = scale_f32(s[m][i], p.w0.bf16);
+                        zo[m][i] = has_z ? 0x64006400u | (z[m][i] * 0x10001u) : 0x64086408u;
                     }
+                scales();
+                if (c < p.chunks) {
+                    const uint32_t mat = matrix_at + at;
+                    const char* bs = columns + bt + part_of * (BCHUNK + SCHUNK);
+                    const uint4* bcol = reinterpret_cast<const uint4*>(bs) + lane;
+                    const float2* bscale = reinterpret_cast<const float2*>(bs + BCHUNK) + t;
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int b = 2 * half + k;
-                        uint32_t h[2][2][4];
-                        float sw[2][2];
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t words[2][4];  // [m][block 2 half: rows g, rows g + 8; block 2 half + 1: the same]
 #pragma unroll
-                        for (int m = 0; m < 2; ++m)
+                        for (int m = 0; m < 2; ++m) load_matrices(words[m], (mat + m * 1024) ^ (32 * half));
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const uint32_t v = __shfl_sync(0xffffffffu, sz[m][i], (lane & ~3) + b);
-                                uint32_t zc, zf;
-                                zero_forms(v >> 16, zc, zf);
-                                words_f16(words[m][2 * k + i], zc, zf, h[m][i]);
-                                sw[m][i] = scale_f32(v & 0xffffu, p.w0.bf16);
-                            }
+                        for (int k = 0; k < 2; ++k) {
+                            const int b = 2 * half + k;
+                            uint32_t h[2][2][4];
+                            float2 sw[2][2];
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            if (n < tiles) {
-                                const uint4 x = bcol[(b * NT + n) * 32];
-                                float2 sx = make_float2(1.f, 1.f);
-                                if (FORM != FORM_F32) sx = bscale[(b * NT + n) * 4];
+                            for (int m = 0; m < 2; ++m)
 #pragma unroll
-                                for (int m = 0; m < 2; ++m) {
-                                    float d[4];
-                                    mma16_first(d, h[m][0][0], h[m][1][0], h[m][0][1], h[m][1][1], x.x, x.y);
-                                    mma16(d, h[m][0][2], h[m][1][2], h[m][0][3], h[m][1][3], x.z, x.w);
+                                for (int i = 0; i < 2; ++i) {
+                                    const float v = __shfl_sync(0xffffffffu, so[m][i], (lane & ~3) + b);
+                                    sw[m][i] = make_float2(v, v);
+                                    uint32_t zc = zo[m][i];
+                                    if (has_z) zc = __shfl_sync(0xffffffffu, zc, (lane & ~3) + b);
+                                    words_f16(words[m][2 * k + i], zc, zero_less(zc), h[m][i]);
+                                }
 #pragma unroll
-                                    for (int i = 0; i < 2; ++i) {
-                                        float2 sc = make_float2(sw[m][i], sw[m][i]);
-                                        if (FORM != FORM_F32) sc = pair_mul(sc, sx);
-                                        pair_fma(acc[m][n][i], sc, d[2 * i], d[2 * i + 1]);
+                            for (int n = 0; n < NT; ++n) {
+                                if (n < tiles) {
+                                    const uint4 x = bcol[(b * NT + n) * 32];
+                                    float2 sx = make_float2(1.f, 1.f);
+                                    if (FORM != FORM_F32) sx = bscale[(b * NT + n) * 4];
+#pragma unroll
+                                    for (int m = 0; m < 2; ++m) {
+                                        float d[4];
+                                        mma16_first(d, h[m][0][0], h[m][1][0], h[m][0][1], h[m][1][1], x.x, x.y);
+                                        mma16(d, h[m][0][2], h[m][1][2], h[m][0][3], h[m][1][3], x.z, x.w);
+#pragma unroll
+                                        for (int i = 0; i < 2; ++i)
+                                            pair_fma(acc[m][n][i], FORM == FORM_F32 ? sw[m][i] : pair_mul(sw[m][i], sx),
+                                                     d[2 * i], d[2 * i + 1]);
                                     }
                                 }
                             }
                         }
                     }
                 }
+                at = at == (kStages - 1) * kTileBytes ? 0 : at + kTileBytes;
+                bt = bt == (kStages - 1) * stage_b ? 0 : bt + stage_b;
             }
             asm volatile("cp.async.wait_group 0;" ::: "memory");
             if (p.wk > 1) {  // the warps' sums of the tile, in the order of their parts
