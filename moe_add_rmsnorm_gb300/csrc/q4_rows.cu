@@ -1,378 +1,8 @@
-// Products of 4-bit weights with several activation rows: the projection, and a chunk's experts (each expert's weights with
-// the rows that chose it: gate-up with SwiGLU, and down-and-combine).
-//
-// A first launch lays the activation rows out as f16 parts (q4.cuh) in the order of the products' operands; a second one
-// multiplies.  There a warp takes two tiles of 16 weight rows (gate-up: 16 gate rows and the 16 up rows beside them) by up
-// to NT tiles of eight columns, a column being one part of one activation row.  Weights and activation parts come through
-// rings of asynchronous 16-byte copies: the weights' is the warp's own, from where one matrix load gives each lane the words
-// it multiplies; the activation's is the CTA's, whose warps read the same columns.  A block's dots are scaled, two sums an
-// instruction, by the weights' scale (and a quantized activation's; an f32 row has one unit, taken out at the end).
-#include "ffn4.h"
-#include "q4.cuh"
+// Products of 4-bit weights with several activation rows: the launches (q4_rows.cuh has the kernels).
+#include "q4_rows.cuh"
 
 namespace q8 {
 namespace {
-
-constexpr int kWarps = 8;    // a CTA
-constexpr int kStages = 4;   // of the rings: a stage is a chunk of four blocks for each of the warps that share a tile
-constexpr int kTileBytes = 2 * 16 * 64;
-
-struct RowsParams {
-    Q4View w0, w1;
-    Q4Act act;
-    int kind;
-    int64_t E, out_rows;
-    int R, K;            // activation rows of the call and choices a row
-    int64_t act_rows;    // rows that are laid out
-    PlanPtrs plan;
-    const int32_t* ids;
-    const float *gates, *residual;
-    uint4* parts;        // [act_rows][4 * chunks][parts][4]
-    float* scales;       // f32: [act_rows], a row's unit; else [act_rows][4 * chunks] (two words: each twice)
-    float* y;
-    int64_t y_stride;
-    float* out;          // down: [R * K][out_rows]
-    int chunks, wk, row_tiles;
-};
-
-// A CTA lays one activation row out at a time.
-template <int FORM>
-__global__ void __launch_bounds__(256) q4_parts_kernel(const RowsParams p) {
-    constexpr int PARTS = FORM == FORM_ONE ? 1 : 2;
-    __shared__ float most[2][8];
-    griddep_launch();
-    const int octets = 16 * p.chunks, cols = p.w0.cols, lane = threadIdx.x & 31;
-    int buf = 0;
-    for (int64_t r = blockIdx.x; r < p.act_rows; r += gridDim.x, buf ^= 1) {
-        float m = 0.f;
-        if (FORM == FORM_F32) {
-            for (int o = threadIdx.x; o < octets; o += blockDim.x) {
-                float x[8];
-                act_values(p.act, r, o, cols, x);
-                m = fmaxf(m, finite_max(x));
-            }
-            m = warp_max(m);
-            if (lane == 0) most[buf][threadIdx.x >> 5] = m;
-            __syncthreads();
-            for (int i = 0; i < 8; ++i) m = fmaxf(m, most[buf][i]);
-        }
-        for (int o = threadIdx.x; o < octets; o += blockDim.x) {
-            ActParts a;
-            if (FORM == FORM_F32) {
-                float x[8];
-                act_values(p.act, r, o, cols, x);
-                a = split_values(x, m);
-                if (o == 0) p.scales[r] = a.scale;
-            } else {
-                a = act_words(p.act, r, o, cols);
-                const int64_t b = r * (octets / 4) + (o >> 2);
-                if ((o & 3) == 0) {
-                    if (FORM == FORM_ONE) p.scales[b] = a.scale;
-                    else reinterpret_cast<float2*>(p.scales)[b] = make_float2(a.scale, a.scale);
-                }
-            }
-            uint4* at = p.parts + (r * octets + (o & ~3)) * PARTS + (o & 3);
-            at[0] = a.hi;
-            if (PARTS == 2) at[4] = a.lo;
-        }
-    }
-}
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void zero16(uint32_t dst) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void copy_small(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
-}
-
-__device__ __forceinline__ void load_matrices(uint32_t (&m)[4], uint32_t at) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(m[0]), "=r"(m[1]), "=r"(m[2]), "=r"(m[3]) : "r"(at) : "memory");
-}
-
-// d = a b, without an addend.
-__device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                            uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-
-// Pairs of f32, two operations an instruction.
-__device__ __forceinline__ float2 pair_mul(float2 a, float2 b) {
-    float2 d;
-    asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z;}"
-        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ void pair_fma(float2& acc, float2 a, float bx, float by) {
-    asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%0, %1}; fma.rn.f32x2 z, x, y, z; mov.b64 {%0, %1}, z;}"
-        : "+f"(acc.x), "+f"(acc.y) : "f"(a.x), "f"(a.y), "f"(bx), "f"(by));
-}
-
-template <int FORM, int NT>
-__global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1) q4_rows_kernel(const RowsParams p) {
-    constexpr int PARTS = FORM == FORM_ONE ? 1 : 2;
-    constexpr int COLS = 8 / PARTS;  // activation rows a tile of columns
-    constexpr int NC = NT * COLS;
-    constexpr int BCHUNK = NT * 8 * 4 * 64;                          // a chunk's columns: [block][column][4 x 16 bytes]
-    constexpr int SCHUNK = FORM == FORM_F32 ? 0 : 4 * NT * 8 * 4;    // and scales: [block][column] (two words: a row's twice)
-    extern __shared__ __align__(128) char smem[];
-    __shared__ int cols[NC];           // the choices (dense: activation rows) of the columns, -1: none
-    __shared__ uint32_t rowat[NC];     // their activation rows
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int side = kWarps / p.wk, tile = blockIdx.x * side + w / p.wk, part_of = w % p.wk;
-    const int nb = p.w0.cols >> 5, ngroups = p.w0.cols >> p.w0.group_log2, row_bytes = p.w0.cols >> 1;
-    const int steps = (p.chunks + p.wk - 1) / p.wk;
-    // The rings.  Of a chunk of weights, block t of row r of 16 stands at 64 r + 16 (t ^ (r >> 1 & 3)), so that the eight rows
-    // of a matrix load lie in different banks.
-    char* columns = smem + kWarps * kStages * kTileBytes;
-    const uint32_t base_a = (uint32_t)__cvta_generic_to_shared(smem) + w * (kStages * kTileBytes);
-    const uint32_t base_b = (uint32_t)__cvta_generic_to_shared(columns), stage_b = p.wk * (BCHUNK + SCHUNK);
-    const uint32_t ring_at = base_a + g * 64 + ((t ^ ((g >> 1) & 3)) << 4);
-    const uint32_t matrix_at = base_a + (lane & 15) * 64 + (((lane >> 4) ^ ((lane >> 1) & 3)) << 4);
-    // Of a chunk of columns the thread copies unit (block, part, word) of rows unit_row, + 2 kWarps / PARTS, ...
-    constexpr int NU = NT * 8 * 16 / (32 * kWarps);
-    const int unit_of = threadIdx.x % (16 * PARTS), unit_row = threadIdx.x / (16 * PARTS);
-    const uint32_t unit_at = (((unit_of / (4 * PARTS)) * NT * 8 + unit_row * PARTS + (unit_of >> 2) % PARTS) * 4 + (unit_of & 3)) * 16;
-    const uint32_t scale_at = BCHUNK + ((threadIdx.x % 4) * NT * 8 + threadIdx.x / 4 * PARTS) * 4;
-    const bool has_z = p.w0.z != nullptr;
-    const int total = p.R * p.K;
-    const bool gate_up = p.kind == Q4_GATE_UP;
-    const Q4View& second = gate_up ? p.w1 : p.w0;
-    bool ready = false;
-    int groups = 1;
-    if (p.kind != Q4_DENSE) groups = p.plan.active ? min(max(p.plan.active[0], 0), (int)min(p.E, (int64_t)total)) : p.K;
-    griddep_launch();
-    for (int a = blockIdx.y; a < groups; a += gridDim.y) {
-        int e = 0, first = 0, count = p.R;
-        if (p.kind != Q4_DENSE) {
-            e = p.plan.active ? p.plan.active[1 + a] : p.ids[a];  // (one row has no plan: every choice is a group)
-            if (e < 0 || e >= p.E) continue;
-            first = p.plan.active ? max(p.plan.offsets[e], 0) : a;
-            count = p.plan.active ? min(p.plan.offsets[e + 1], total) - first : 1;
-        }
-        // The lane's rows of the two weight tiles, rows g and g + 8 of each (they clamp to the group's last row), as offsets
-        // from the first tile row's words and scales, which run on from chunk to chunk.
-        const int64_t base = (int64_t)e * p.out_rows;
-        const int r0 = (gate_up ? 16 : 32) * tile, last = (int)p.out_rows - 1, top = min(r0, last);
-        const uint8_t *qa = p.w0.q + (base + top) * row_bytes, *qb = second.q + (base + top) * row_bytes;
-        const uint16_t *sa = p.w0.s + (base + top) * ngroups, *sb = second.s + (base + top) * ngroups;
-        const uint8_t *za = p.w0.z + (base + top) * ngroups, *zb = second.z + (base + top) * ngroups;
-        int row[2][2];
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) row[m][i] = min(r0 + (gate_up ? 0 : 16 * m) + g + 8 * i, last) - top;
-        for (int ct = blockIdx.z; ct * NC < count; ct += gridDim.z) {
-            const int tiles = min((count - ct * NC + COLS - 1) / COLS, NT);
-            uint32_t s[2][2], z[2][2];  // the next chunk's scales and zero points: lane t block t's
-            int sc = part_of;           // that chunk
-            auto scales = [&]() {
-                const int b = 4 * sc + t, at = (32 * b) >> p.w0.group_log2;
-                const bool in = b < nb;
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int k = row[m][i] * ngroups + at;
-                        s[m][i] = in ? __ldg((m == 0 ? sa : sb) + k) : 0u;
-                        if (has_z) z[m][i] = in ? __ldg((m == 0 ? za : zb) + k) : 8u;
-                    }
-                sc += p.wk;
-            };
-            int wc = part_of;  // the chunk of weights that is fetched next, its place in the ring, and of the columns'
-            uint32_t wat = 0, bat = 0;
-            int bc = 0;
-            auto fetch_weights = [&]() {
-                if (wc < p.chunks) {
-                    const uint32_t to = ring_at + wat;
-                    const int from = 64 * wc + 16 * t;
-                    if (4 * wc + t < nb) {
-#pragma unroll
-                        for (int m = 0; m < 2; ++m)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                copy16(to + m * 1024 + i * 512, (m == 0 ? qa : qb) + (row[m][i] * row_bytes + from));
-                    } else {  // (columns past the last: zeros in the activations, anything finite here)
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) zero16(to + m * 512);
-                    }
-                }
-                wc += p.wk;
-                wat = wat == (kStages - 1) * kTileBytes ? 0 : wat + kTileBytes;
-            };
-            uint32_t goff[NU];  // the thread's 16-byte units of a chunk of the columns
-            const float* sfrom = p.scales;  // and its scale (words: of block threadIdx.x % 4 of row threadIdx.x / 4)
-            const int rows_here = tiles * COLS;
-            auto fetch_columns = [&]() {  // all warps: the stage's chunks of the columns
-                for (int j = 0; j < p.wk && bc < p.chunks; ++j, ++bc) {
-                    const uint32_t to = base_b + bat + j * (BCHUNK + SCHUNK) + unit_at;
-#pragma unroll
-                    for (int k = 0; k < NU; ++k)
-                        if (unit_row + k * (kWarps * 2 / PARTS) < rows_here)
-                            copy16(to + k * 1024, p.parts + (goff[k] + (uint32_t)bc * (16 * PARTS)));
-                    if (FORM != FORM_F32 && (int)threadIdx.x < 4 * rows_here) {
-                        const uint32_t sto = base_b + bat + j * (BCHUNK + SCHUNK) + scale_at;
-                        if (FORM == FORM_ONE) copy_small<4>(sto, sfrom + 4 * bc);
-                        else copy_small<8>(sto, sfrom + 8 * bc);
-                    }
-                }
-                bat = bat == (kStages - 1) * stage_b ? 0 : bat + stage_b;
-            };
-            // weights first: they depend on no launch before
-            scales();
-            fetch_weights();
-            __syncthreads();  // (the columns before these have been used)
-            if (threadIdx.x < NC) {
-                const int i = ct * NC + threadIdx.x;
-                int c = i < count ? (p.kind == Q4_DENSE ? i : p.plan.active ? p.plan.lists[first + i] : first) : -1;
-                if (c < 0 || c >= total) c = -1;
-                cols[threadIdx.x] = c;
-                rowat[threadIdx.x] = gate_up ? max(c, 0) / p.K : max(c, 0);
-            }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < NU; ++k)
-                goff[k] = rowat[min(unit_row + k * (kWarps * 2 / PARTS), NC - 1)] * (uint32_t)(16 * PARTS * p.chunks) + unit_of;
-            if (FORM != FORM_F32)
-                sfrom = p.scales + ((size_t)rowat[min((int)threadIdx.x / 4, NC - 1)] * (4 * p.chunks) + threadIdx.x % 4) * PARTS;
-            if (!ready) griddep_wait(), ready = true;  // the activation parts
-            fetch_columns();
-            asm volatile("cp.async.commit_group;" ::: "memory");
-#pragma unroll
-            for (int i = 1; i < kStages - 1; ++i) {
-                fetch_weights();
-                fetch_columns();
-                asm volatile("cp.async.commit_group;" ::: "memory");
-            }
-            float2 acc[2][NT][2] = {};  // [tile][columns][row g, g + 8]: columns 2 t and 2 t + 1
-            uint32_t at = 0, bt = 0;
-            for (int c = part_of, step = 0; step < steps; ++step, c += p.wk) {
-                asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-                __syncthreads();
-                fetch_weights();
-                fetch_columns();
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                float so[2][2];
-                uint32_t zo[2][2];
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        so[m][i] = scale_f32(s[m][i], p.w0.bf16);
-                        zo[m][i] = has_z ? 0x64006400u | (z[m][i] * 0x10001u) : 0x64086408u;
-                    }
-                scales();
-                if (c < p.chunks) {
-                    const uint32_t mat = matrix_at + at;
-                    const char* bs = columns + bt + part_of * (BCHUNK + SCHUNK);
-                    const uint4* bcol = reinterpret_cast<const uint4*>(bs) + lane;
-                    const float2* bscale = reinterpret_cast<const float2*>(bs + BCHUNK) + t;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t words[2][4];  // [m][block 2 half: rows g, rows g + 8; block 2 half + 1: the same]
-#pragma unroll
-                        for (int m = 0; m < 2; ++m) load_matrices(words[m], (mat + m * 1024) ^ (32 * half));
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int b = 2 * half + k;
-                            uint32_t h[2][2][4];
-                            float2 sw[2][2];
-#pragma unroll
-                            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    const float v = __shfl_sync(0xffffffffu, so[m][i], (lane & ~3) + b);
-                                    sw[m][i] = make_float2(v, v);
-                                    uint32_t zc = zo[m][i];
-                                    if (has_z) zc = __shfl_sync(0xffffffffu, zc, (lane & ~3) + b);
-                                    words_f16(words[m][2 * k + i], zc, zero_less(zc), h[m][i]);
-                                }
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                if (n < tiles) {
-                                    const uint4 x = bcol[(b * NT + n) * 32];
-                                    float2 sx = make_float2(1.f, 1.f);
-                                    if (FORM != FORM_F32) sx = bscale[(b * NT + n) * 4];
-#pragma unroll
-                                    for (int m = 0; m < 2; ++m) {
-                                        float d[4];
-                                        mma16_first(d, h[m][0][0], h[m][1][0], h[m][0][1], h[m][1][1], x.x, x.y);
-                                        mma16(d, h[m][0][2], h[m][1][2], h[m][0][3], h[m][1][3], x.z, x.w);
-#pragma unroll
-                                        for (int i = 0; i < 2; ++i)
-                                            pair_fma(acc[m][n][i], FORM == FORM_F32 ? sw[m][i] : pair_mul(sw[m][i], sx),
-                                                     d[2 * i], d[2 * i + 1]);
-                                    }
-                                }
-                            }
-                        }
-                    }
-                }
-                at = at == (kStages - 1) * kTileBytes ? 0 : at + kTileBytes;
-                bt = bt == (kStages - 1) * stage_b ? 0 : bt + stage_b;
-            }
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            if (p.wk > 1) {  // the warps' sums of the tile, in the order of their parts
-                __syncthreads();
-                float2* red = reinterpret_cast<float2*>(smem);
-                if (part_of) {
-#pragma unroll
-                    for (int m = 0; m < 2; ++m)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) red[(w * 4 * NT + (m * NT + n) * 2 + i) * 32 + lane] = acc[m][n][i];
-                }
-                __syncthreads();
-                if (part_of == 0) {
-                    for (int k = 1; k < p.wk; ++k)
-#pragma unroll
-                        for (int m = 0; m < 2; ++m)
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    const float2 v = red[((w + k) * 4 * NT + (m * NT + n) * 2 + i) * 32 + lane];
-                                    acc[m][n][i].x += v.x, acc[m][n][i].y += v.y;
-                                }
-                }
-            }
-            if (part_of == 0 && tile < p.row_tiles) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int j = 0; j < 2 / PARTS; ++j) {
-                            const int at = n * COLS + (2 / PARTS) * t + j, c = cols[at];
-                            if (n >= tiles || c < 0) continue;
-                            float v[2];
-#pragma unroll
-                            for (int m = 0; m < 2; ++m) {
-                                v[m] = PARTS == 2 ? acc[m][n][i].x + acc[m][n][i].y : j ? acc[m][n][i].y : acc[m][n][i].x;
-                                if (FORM == FORM_F32) v[m] *= p.scales[rowat[at]];
-                            }
-                            const int r = r0 + g + 8 * i;
-                            if (gate_up) {
-                                if (r <= last) p.y[c * p.y_stride + r] = silu_f32(v[0]) * v[1];
-                            } else {
-                                float* to = p.kind == Q4_DENSE ? p.y + c * p.y_stride : p.out + c * p.out_rows;
-                                if (r <= last) to[r] = v[0];
-                                if (r + 16 <= last) to[r + 16] = v[1];
-                            }
-                        }
-            }
-            __syncthreads();  // (the rings take the next columns)
-        }
-    }
-    if (!ready) griddep_wait();  // (a grid ends after the launch before it, whatever its CTAs had to do)
-}
 
 // y[r] = residual[r] + sum_j gates[r][j] out[r][j], in the order of the choices.
 __global__ void __launch_bounds__(256) q4_combine_kernel(const RowsParams p) {
@@ -388,38 +18,6 @@ __global__ void __launch_bounds__(256) q4_combine_kernel(const RowsParams p) {
         }
         p.y[i] = p.residual ? p.residual[i] + sum : sum;
     }
-}
-
-constexpr size_t kRowsSmem = 220 << 10;
-
-template <int FORM, int NT>
-cudaError_t run(RowsParams p, int64_t groups, cudaStream_t st) {
-    constexpr int NC = NT * 8 / (FORM == FORM_ONE ? 1 : 2);
-    const int sms = device_info().sms;
-    auto smem = [&](int wk) {
-        return (size_t)kStages * (kWarps * kTileBytes + wk * (NT * 2048 + (FORM == FORM_F32 ? 0 : NT * 128)));
-    };
-    const int64_t zs = p.kind == Q4_DENSE ? min((int64_t)(p.R + NC - 1) / NC, (int64_t)65535) : 1;
-    // Warps that share a tile: as many as it takes to give every SM its CTAs, while their columns fit.
-    p.wk = 1;
-    while (p.wk < kWarps && p.wk * 2 <= p.chunks && smem(p.wk * 2) <= kRowsSmem &&
-           p.row_tiles * groups * zs * p.wk < (int64_t)sms * kWarps)
-        p.wk *= 2;
-    const int side = kWarps / p.wk;
-    const dim3 grid((unsigned)((p.row_tiles + side - 1) / side), (unsigned)min(groups, (int64_t)65535), (unsigned)zs);
-    const cudaError_t e = cudaFuncSetAttribute(q4_rows_kernel<FORM, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmem);
-    if (e != cudaSuccess) return e;
-    return launch(q4_rows_kernel<FORM, NT>, grid, dim3(32 * kWarps), smem(p.wk), st, 1, p);
-}
-
-template <int FORM>
-cudaError_t run_columns(const RowsParams& p, int64_t groups, cudaStream_t st) {
-    // Tiles of columns a pass: those that twice an expert's average rows fill.
-    const int64_t rows = p.kind == Q4_DENSE ? p.R : 2 * ((int64_t)p.R * p.K / groups);
-    const int tile = FORM == FORM_ONE ? 8 : 4;
-    if (rows <= 2 * tile) return run<FORM, 2>(p, groups, st);
-    if (rows <= 4 * tile) return run<FORM, 4>(p, groups, st);
-    return run<FORM, 8>(p, groups, st);
 }
 
 }  // namespace
@@ -452,19 +50,13 @@ cudaError_t launch_q4(const Q4Call& c, Carve& ws, cudaStream_t st) {
     p.scales = ws.take<float>((size_t)p.act_rows * (form == FORM_F32 ? 1 : p.chunks * 4 * form));
     if (c.kind == Q4_DOWN) p.out = ws.take<float>((size_t)c.R * c.K * c.out_rows);
     if (ws.overflow) return cudaSuccess;
-    const int sms = device_info().sms;
-    const dim3 lay((unsigned)min(p.act_rows, (int64_t)sms * 8));
-    cudaError_t e = form == FORM_F32 ? launch(q4_parts_kernel<FORM_F32>, lay, dim3(256), 0, st, 0, p)
-                    : form == FORM_ONE ? launch(q4_parts_kernel<FORM_ONE>, lay, dim3(256), 0, st, 0, p)
-                                       : launch(q4_parts_kernel<FORM_TWO>, lay, dim3(256), 0, st, 0, p);
-    if (e != cudaSuccess) return e;
     const int64_t groups = c.kind == Q4_DENSE ? 1 : c.R == 1 ? c.K : min(c.E, c.R * c.K);
-    e = form == FORM_F32   ? run_columns<FORM_F32>(p, groups, st)
-        : form == FORM_ONE ? run_columns<FORM_ONE>(p, groups, st)
-                           : run_columns<FORM_TWO>(p, groups, st);
+    const cudaError_t e = form == FORM_F32   ? launch_rows_f32(p, groups, st)
+                          : form == FORM_ONE ? launch_rows_one(p, groups, st)
+                                             : launch_rows_two(p, groups, st);
     if (e != cudaSuccess || c.kind != Q4_DOWN) return e;
     const int64_t n = c.R * c.out_rows;
-    return launch(q4_combine_kernel, dim3((unsigned)min((n + 255) / 256, (int64_t)sms * 16)), dim3(256), 0, st, 1, p);
+    return launch(q4_combine_kernel, dim3((unsigned)min((n + 255) / 256, (int64_t)device_info().sms * 16)), dim3(256), 0, st, 1, p);
 }
 
 }  // namespace q8

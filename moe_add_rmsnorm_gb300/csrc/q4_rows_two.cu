@@ -1,0 +1,8 @@
+// Products of 4-bit weights with several rows of activations of two int8 words a value (q4_rows.cuh).
+#include "q4_rows.cuh"
+
+namespace q8 {
+
+cudaError_t launch_rows_two(const RowsParams& p, int64_t groups, cudaStream_t st) { return launch_rows<FORM_TWO>(p, groups, st); }
+
+}  // namespace q8
