@@ -26,7 +26,6 @@ struct RowsParams {
     int64_t act_rows;    // rows that are laid out
     PlanPtrs plan;
     const int32_t* ids;
-    const float *gates, *residual;
     uint4* parts;        // [act_rows][4 * chunks][parts][4]
     float* scales;       // f32: [act_rows], a row's unit; else [act_rows][4 * chunks] (two words: each twice)
     float* y;
@@ -180,7 +179,7 @@ __device__ __forceinline__ void multiply_chunk(uint32_t mat, const char* bs, con
 }
 
 template <int FORM, int NT>
-__global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1) q4_rows_kernel(const RowsParams p) {
+__global__ void __launch_bounds__(32 * kWarps, 2) q4_rows_kernel(const RowsParams p) {
     constexpr int PARTS = FORM == FORM_ONE ? 1 : 2;
     constexpr int COLS = 8 / PARTS;  // activation rows a tile of columns
     constexpr int NC = NT * COLS;
@@ -341,9 +340,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1) q4_rows_kernel(c
                 if (c < p.chunks) {
                     const uint32_t mat = matrix_at + at;
                     const char* bs = columns + bt + part_of * (BCHUNK + SCHUNK);
-                    if (NT >= 8 && tiles > 6) multiply_chunk<FORM, NT, NT >= 8 ? 8 : 1>(mat, bs, so, zo, has_z, same, acc);
-                    else if (NT >= 8 && tiles > 4) multiply_chunk<FORM, NT, NT >= 8 ? 6 : 1>(mat, bs, so, zo, has_z, same, acc);
-                    else if (NT >= 4 && tiles > 2) multiply_chunk<FORM, NT, NT >= 4 ? 4 : 1>(mat, bs, so, zo, has_z, same, acc);
+                    if (NT >= 4 && tiles > 2) multiply_chunk<FORM, NT, NT >= 4 ? 4 : 1>(mat, bs, so, zo, has_z, same, acc);
                     else if (tiles > 1) multiply_chunk<FORM, NT, 2>(mat, bs, so, zo, has_z, same, acc);
                     else multiply_chunk<FORM, NT, 1>(mat, bs, so, zo, has_z, same, acc);
                 }
@@ -438,9 +435,7 @@ cudaError_t launch_rows(const RowsParams& p, int64_t groups, cudaStream_t st) {
     // Tiles of columns a pass: those that twice an expert's average rows fill.
     const int64_t rows = p.kind == Q4_DENSE ? p.R : 2 * ((int64_t)p.R * p.K / groups);
     const int tile = FORM == FORM_ONE ? 8 : 4;
-    if (rows <= 2 * tile) return run_rows<FORM, 2>(p, groups, st);
-    if (rows <= 4 * tile) return run_rows<FORM, 4>(p, groups, st);
-    return run_rows<FORM, 8>(p, groups, st);
+    return rows <= 2 * tile ? run_rows<FORM, 2>(p, groups, st) : run_rows<FORM, 4>(p, groups, st);
 }
 
 // One file each, so that they compile beside one another.

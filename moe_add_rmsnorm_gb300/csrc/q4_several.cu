@@ -1,0 +1,116 @@
+// Products of 4-bit weights with several activation rows: which kernel takes them (q4_rows.cuh, q4_mma.cuh), and the sum over
+// the choices.
+#include "q4_mma.cuh"
+
+namespace q8 {
+namespace {
+
+struct CombineParams {
+    int64_t E, d;
+    int R, K;
+    const int32_t* ids;
+    const float *gates, *residual, *out;
+    float* y;
+};
+
+// y[r] = residual[r] + sum_j gates[r][j] out[r][j], in the order of the choices.
+__global__ void __launch_bounds__(256) q4_combine_kernel(const CombineParams p) {
+    griddep_wait();
+    const int64_t n = (int64_t)p.R * p.d, step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) {
+        const int64_t r = i / p.d, o = i - r * p.d;
+        float sum = 0.f;
+        for (int j = 0; j < p.K; ++j) {
+            const int64_t c = r * p.K + j;
+            const int e = p.ids[c];
+            if (e >= 0 && e < p.E) sum = fmaf(p.gates[c], p.out[c * p.d + o], sum);
+        }
+        p.y[i] = p.residual ? p.residual[i] + sum : sum;
+    }
+}
+
+// The CUDA driver API's tensor-map encoder, found once through the runtime's entry-point lookup, so that the library does not
+// link against libcuda.
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+Encode encoder() {
+    static const Encode fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return (Encode) nullptr;
+        return reinterpret_cast<Encode>(f);
+    }();
+    return fn;
+}
+
+}  // namespace
+
+bool q4_map(CUtensorMap* map, const Q4View& w, int box_rows) {
+    const Encode encode = encoder();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)w.cols / 2, (cuuint64_t)w.rows}, stride[1] = {(cuuint64_t)w.cols / 2};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(w.q), dims, stride, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool q4_row_fits(const Q4Call& c);
+cudaError_t launch_q4_row(const Q4Call& c, cudaStream_t st);
+cudaError_t launch_q4_warps(const Q4Call& c, int64_t groups, int form, float* out, Carve& ws, cudaStream_t st);
+
+namespace {
+
+cudaError_t launch_q4_tensor(const Q4Call& c, int64_t groups, int form, float* out, Carve& ws, cudaStream_t st) {
+    MmaParams p = {};
+    p.w0 = c.w0;
+    p.w1 = c.w1;
+    p.act = c.act;
+    p.kind = c.kind;
+    p.E = c.E;
+    p.out_rows = c.out_rows;
+    p.R = (int)c.R;
+    p.K = c.K;
+    p.plan = c.plan;
+    p.ids = c.ids;
+    p.y = c.y;
+    p.y_stride = c.y_stride;
+    p.out = out;
+    p.failed = ws.failed;
+    p.chunks = (c.w0.cols + 127) / 128;
+    const int tile_rows = c.kind == Q4_GATE_UP ? 64 : 128;
+    p.row_tiles = (int)((c.out_rows + tile_rows - 1) / tile_rows);
+    p.slots = c.kind == Q4_DENSE ? (c.R + 7) & ~int64_t(7) : (c.R * c.K + 8 * groups + 15) & ~int64_t(7);
+    p.parts = ws.take<char>((size_t)p.slots / 8 * p.chunks * (form == FORM_ONE ? 2048 : 4096));
+    p.scales = ws.take<float>(form == FORM_F32 ? (size_t)p.slots : (size_t)p.slots / 8 * p.chunks * 32);
+    if (ws.overflow) return cudaSuccess;
+    return form == FORM_F32   ? launch_mma_f32(p, groups, ws, st)
+           : form == FORM_ONE ? launch_mma_one(p, groups, ws, st)
+                              : launch_mma_two(p, groups, ws, st);
+}
+
+}  // namespace
+
+cudaError_t launch_q4(const Q4Call& c, Carve& ws, cudaStream_t st) {
+    if (c.R == 1 && q4_row_fits(c)) return launch_q4_row(c, st);
+    const int form = c.act.x ? FORM_F32 : c.act.lo ? FORM_TWO : FORM_ONE;
+    const int64_t groups = c.kind == Q4_DENSE ? 1 : c.R == 1 ? c.K : min(c.E, c.R * c.K);
+    float* out = c.kind == Q4_DOWN ? ws.take<float>((size_t)c.R * c.K * c.out_rows) : nullptr;
+    if (ws.overflow) return cudaSuccess;
+    // Up to 16 columns (an activation's parts) a group on average, the warp-wide products are as fast or faster: they start
+    // sooner and unpack with all their warps.  From there on the tensor cores' rows share what was unpacked.  Measured, warps and
+    // tensor cores, us: 8192 x 4096, group 128, f32: 4 rows 14 and 16, 16 rows 19 and 17, 64 rows 40 and 25; 6 of 64 experts of
+    // 2048 x 1408, group 32, f32: 24 rows (2.3 an expert) 124 and 155, 100 (9.4) 215 and 198, 256 (24) 310 and 239.
+    const int64_t columns = c.R * c.K * (form == FORM_ONE ? 1 : 2);
+    const cudaError_t e = columns <= 16 * groups ? launch_q4_warps(c, groups, form, out, ws, st)
+                                                 : launch_q4_tensor(c, groups, form, out, ws, st);
+    if (e != cudaSuccess || ws.overflow || c.kind != Q4_DOWN) return e;
+    const CombineParams p = {c.E, c.out_rows, (int)c.R, c.K, c.ids, c.gates, c.residual, out, c.y};
+    const int64_t n = c.R * c.out_rows;
+    return launch(q4_combine_kernel, dim3((unsigned)min((n + 255) / 256, (int64_t)device_info().sms * 16)), dim3(256), 0, st, 1, p);
+}
+
+}  // namespace q8
