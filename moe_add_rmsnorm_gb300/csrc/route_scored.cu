@@ -1,9 +1,11 @@
 // Router scores to experts (q8moe.h, moe_route_scored): scores, groups, the k best, gates, and the grouping by expert.
 //
-// A warp takes a row: lane L holds experts L, L + 32, ...; the k best come from k rounds of one warp-wide maximum over
-// order-preserving integer keys and one warp-wide minimum over the indices that hold it.  Scores are formed in f32, whose
-// errors can exchange two experts that 64 bits would order: the choice is taken again in 64 bits for a row in which two
-// neighbours of the order (or a kept and a left group) are closer than those errors reach.
+// A warp takes a row: lane L holds experts L, L + 32, ... as order-preserving integer keys.  The K-th largest of the lanes' maxima
+// bounds the K-th largest key from below; the keys from there on, a few more than K, are gathered one a lane, and each counts
+// those before it.  Scores are formed in f32 by the fast exponential and quotient, whose errors can exchange two experts that
+// 64 bits would order: where two of the gathered ones are closer than those errors reach, all of them are formed again in 64
+// bits and counted by those; where kept and left groups are, or a softmax with a bias (whose sum all scores share) or more
+// candidates than lanes, the whole row is chosen again in 64 bits.  What bounds it is instructions, about 600 a row of 256.
 #include <math.h>
 
 #include "common.cuh"
@@ -25,7 +27,8 @@ struct RouteParams {
     int32_t* ids;
     float* gates;
     PlanPtrs plan;
-    int32_t* hist;  // [CTAs][E] when other CTAs group the choices
+    int32_t* hist;  // [CTAs][E] when a second launch groups the choices
+    int* arrived;   // else: the CTAs that are done, zero between calls; the last one groups the choices
     int per;        // rows a CTA (0: rows are dealt out warp by warp)
 };
 
@@ -143,7 +146,7 @@ __device__ __forceinline__ void place_choices(const int32_t* ids, int first, int
     const int lo = min(w * seg, n), hi = min(lo + seg, n);
     for (int i = threadIdx.x; i < W * E; i += blockDim.x) wh[i] = 0;
     __syncthreads();
-    for (int i = lo + lane; i < hi; i += 32) atomicAdd(&wh[w * E + ids[first + i]], 1);
+    for (int i = lo + lane; i < hi; i += 32) atomicAdd(&wh[w * E + __ldcg(ids + first + i)], 1);
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         int run = next[e];
@@ -156,7 +159,7 @@ __device__ __forceinline__ void place_choices(const int32_t* ids, int first, int
     __syncthreads();
     for (int i = lo; i < hi; i += 32) {
         const bool in = i + lane < hi;
-        const int e = in ? ids[first + i + lane] : E;  // (lanes past the end stand together)
+        const int e = in ? __ldcg(ids + first + i + lane) : E;  // (lanes past the end stand together)
         const unsigned same = __match_any_sync(FULL, e);
         const int before = __popc(same & ((1u << lane) - 1));
         if (in) lists[wh[w * E + e] + before] = first + i + lane;
@@ -201,14 +204,19 @@ __device__ __forceinline__ void scan_totals(const int* total, int E, int* off, i
     if (write && threadIdx.x == 0) plan.offsets[E] = base, plan.active[0] = hits;
 }
 
+// p of logit l by the fast exponential and quotient: within 8e-7 of a sigmoid, and of a softmax's largest score times that.
+__device__ __forceinline__ float fast_sigmoid(float l) { return __fdividef(1.f, 1.f + __expf(-l)); }
+
 template <int NL>
 __global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_kernel(const RouteParams p) {
     extern __shared__ char smem[];
     __shared__ int tmp[64];
+    __shared__ int last_cta;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, W = blockDim.x >> 5;
     double* c64 = reinterpret_cast<double*>(smem) + w * p.E;  // a warp's marks (f32 in the same place)
     float* cs = reinterpret_cast<float*>(c64);
     float* ls = reinterpret_cast<float*>(smem + (size_t)W * p.E * 8) + w * p.E;
+    unsigned* found = reinterpret_cast<unsigned*>(smem + (size_t)W * p.E * 12) + w * 64;  // [32] keys, [32] experts
     const int S = p.E / p.groups;
     float b[NL], bmax = 0.f;
 #pragma unroll
@@ -233,28 +241,29 @@ __global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_k
             l[i] = isnan(v) ? -INFINITY : fminf(v, 3.402823466e38f);
             m = fmaxf(m, l[i]);
         }
-        m = warp_max(m);
-        const float m0 = m == -INFINITY ? 0.f : m;
-        float z = 0.f, zi = 0.f;
-        const bool scores = p.bias || p.groups > 1 || !p.renorm;
-        if (!p.sigmoid && scores) {
+        float m0 = 0.f, z = 0.f, zi = 0.f;
+        const bool marks = p.bias || p.groups > 1;
+        if (!p.sigmoid) {
+            m = warp_max(m);
+            m0 = m == -INFINITY ? 0.f : m;
+            if (marks || !p.renorm) {
 #pragma unroll
-            for (int i = 0; i < NL; ++i) z += expf(l[i] - m0);
-            z = group_sum<32>(z);
-            zi = z > 0.f ? 1.f / z : 0.f;
+                for (int i = 0; i < NL; ++i) z += __expf(l[i] - m0);
+                z = group_sum<32>(z);
+                zi = z > 0.f ? 1.f / z : 0.f;
+            }
         }
-        // How far two f32 scores can be out against one another: a few roundings of p <= pmax and of p + b, and for the
-        // softmax its sum's, which all scores share (up to NL + 5 roundings of a sum).
+        // How far two f32 scores can be out against one another: fast_sigmoid's errors, or a softmax's, the exponential's
+        // argument (up to 3e-7 of the largest score) and its sum's NL + 5 roundings; and the sum p + b.
         const float pmax = p.sigmoid ? 1.f : zi;
-        const float tol = 6e-7f * (pmax + bmax) + (p.sigmoid ? 0.f : 1.2e-7f * (NL + 5) * pmax);
+        const float tol = 2e-6f * pmax + 2e-7f * bmax + (p.sigmoid ? 0.f : 1.2e-7f * (NL + 5) * pmax);
         bool slow = false;
-        unsigned kept = FULL;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
             const int e = lane + 32 * i;
             float c = l[i];
-            if (p.bias || p.groups > 1) {
-                c = p.sigmoid ? 1.f / (1.f + expf(-l[i])) : expf(l[i] - m0) * zi;
+            if (marks) {
+                c = p.sigmoid ? fast_sigmoid(l[i]) : __expf(l[i] - m0) * zi;
                 if (p.bias) c += b[i];
             }
             const bool on = e < p.E && l[i] > -INFINITY && c > -INFINITY;  // (a c that is no number fails too)
@@ -264,42 +273,73 @@ __global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_k
             }
             key[i] = e >= p.E ? kHidden : !on ? kOff : order_key(p.bias ? c : l[i]);
         }
-        __syncwarp();
         if (p.groups > 1) {
-            kept = kept_groups<float>(cs, p.E, p.groups, p.keep, p.top, 2.5f * tol, slow);
+            __syncwarp();
+            const unsigned kept = kept_groups<float>(cs, p.E, p.groups, p.keep, p.top, 2.5f * tol, slow);
 #pragma unroll
             for (int i = 0; i < NL; ++i)
                 if (!((kept >> min((lane + 32 * i) / S, 31)) & 1u)) key[i] = kHidden;
         }
-        int id = 0;
-        bool on = false;
-        unsigned mine = kHidden, mine_at = 0;  // this lane's largest key and its expert
-        auto rescan = [&]() {
-            mine = key[0], mine_at = lane;
+        // the keys that may be among the K largest: all from the K-th largest of the lanes' maxima on, and a biased order's
+        // error below it
+        unsigned mine = key[0], from = kHidden;
 #pragma unroll
-            for (int i = 1; i < NL; ++i)
-                if (key[i] > mine) mine = key[i], mine_at = lane + 32 * i;
-        };
-        rescan();
-        unsigned last = kHidden;
-        const int rounds = p.bias ? p.K + 1 : p.K;  // (the order by logits is exact)
-        for (int j = 0; j < rounds; ++j) {
-            const unsigned best = __reduce_max_sync(FULL, mine);
-            const unsigned at = __reduce_min_sync(FULL, mine == best ? mine_at : FULL);
-            if (p.bias && last > kOff && best > kOff) slow |= !(key_value(last) - key_value(best) > tol);
-            last = best;
-            if (lane == j) id = at, on = best > kOff;
-            if ((at & 31) == lane) {
+        for (int i = 1; i < NL; ++i) mine = max(mine, key[i]);
+        for (int j = 0; j < p.K; ++j) {
+            from = __reduce_max_sync(FULL, mine);
+            if (lane == __ffs(__ballot_sync(FULL, mine == from)) - 1) mine = kHidden;
+        }
+        if (from > kOff && p.bias) from = max(order_key(key_value(from) - tol), kOff + 1);
+        const unsigned least = max(from, kOff + 1);
+        int n = 0;
 #pragma unroll
-                for (int i = 0; i < NL; ++i)
-                    if (at == lane + 32 * i) key[i] = kHidden;
-                rescan();
+        for (int i = 0; i < NL; ++i) {
+            const unsigned here = __ballot_sync(FULL, key[i] >= least);
+            if (here == 0) continue;
+            const int at = n + __popc(here & ((1u << lane) - 1));
+            if (key[i] >= least && at < 32) found[at] = key[i], found[32 + at] = lane + 32 * i;
+            n += __popc(here);
+        }
+        if (from <= kOff && n <= 32) {  // too few in service: the first of the others behind them
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const unsigned here = __ballot_sync(FULL, key[i] == kOff);
+                const int at = n + __popc(here & ((1u << lane) - 1));
+                if (key[i] == kOff && at < 32) found[at] = kOff, found[32 + at] = lane + 32 * i;
+                n = min(n + __popc(here), 32);
             }
         }
-        if (slow) choose_exactly(p, ls, c64, id, on);
-        // gates: lane j the j-th
-        const bool kth = lane < p.K;
-        id = kth ? min(max(id, 0), p.E - 1) : 0;
+        __syncwarp();
+        // lane j: candidate j (they stand in the order of their experts), and how many come before it
+        unsigned k = kHidden;
+        int id = 0, rank = 32;
+        bool close = false;
+        if (n <= 32) {
+            if (lane < n) k = found[lane], id = found[32 + lane];
+            const float v = k > kOff ? key_value(k) : 0.f;
+            rank = lane < n ? 0 : 32;
+            for (int j = 0; j < n; ++j) {
+                const unsigned o = __shfl_sync(FULL, k, j);
+                rank += o > k || (o == k && j < lane);
+                close |= p.bias && j != lane && o > kOff && k > kOff && !(fabsf(key_value(o) - v) > tol);
+            }
+        }
+        close = __any_sync(FULL, close && rank < p.K);
+        bool on = k > kOff;
+        if (slow || n > 32 || (close && !p.sigmoid)) {
+            choose_exactly(p, ls, c64, id, on);
+            rank = lane;
+        } else if (close) {  // the candidates' marks in 64 bits
+            const double c = on ? 1 / (1 + exp(-(double)ls[id])) + (double)p.bias[id] : k == kOff ? -1.7e308 : -INFINITY;
+            rank = lane < n ? 0 : 32;
+            for (int j = 0; j < n; ++j) {
+                const double o = __shfl_sync(FULL, c, j);
+                rank += o > c || (o == c && j < lane);
+            }
+        }
+        // gates, of the lanes whose expert is chosen
+        const bool kth = rank < p.K;
+        id = min(max(id, 0), p.E - 1);
         float gate = 0.f;
         const float v = kth && on ? ls[id] : -INFINITY;
         if (p.renorm) {  // relative to the largest: below -20 a sigmoid is e^l to less than f32's rounding
@@ -307,25 +347,40 @@ __global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_k
             if (v > -INFINITY) gate = p.sigmoid && most >= -20.f ? 1.f / (1.f + expf(-v)) : expf(v - most);
             const float sum = group_sum<32>(gate);
             gate = sum > 0.f ? gate / sum : 0.f;
-        } else if (v > -INFINITY) {
-            gate = p.sigmoid ? (v < -80.f ? expf(v) : 1.f / (1.f + expf(-v))) : expf(v - m0) * zi;
+        } else if (p.sigmoid) {
+            if (v > -INFINITY) gate = v < -80.f ? expf(v) : 1.f / (1.f + expf(-v));
+        } else {  // (the sum again, by the exact exponential)
+            float zs = 0.f;
+#pragma unroll
+            for (int i = 0; i < NL; ++i) zs += expf(l[i] - m0);
+            zs = group_sum<32>(zs);
+            if (v > -INFINITY) gate = expf(v - m0) / zs;
         }
         if (kth) {
-            p.ids[(int64_t)r * p.K + lane] = id;
-            p.gates[(int64_t)r * p.K + lane] = gate * p.scale;
+            p.ids[(int64_t)r * p.K + rank] = id;
+            p.gates[(int64_t)r * p.K + rank] = gate * p.scale;
         }
         __syncwarp();
     }
     if (!p.per || !p.plan.counts) return;
-    // The grouping: all of it here when this CTA has all rows, else this CTA's counts for the CTAs that place the choices.
+    // The grouping: by the last CTA of few choices, else this CTA's counts for the CTAs that place the choices.
+    int from = first, n = (end - first) * p.K;
     __syncthreads();
+    if (!p.hist) {
+        if (gridDim.x > 1) {
+            if (threadIdx.x == 0) last_cta = atomic_add_acq_rel_gpu(p.arrived, 1) == (int)gridDim.x - 1;
+            __syncthreads();
+            if (!last_cta) return;
+            if (threadIdx.x == 0) *p.arrived = 0;
+        }
+        from = 0, n = p.rows * p.K;
+    }
     int* wh = reinterpret_cast<int*>(smem);
     int* total = reinterpret_cast<int*>(smem + (size_t)W * p.E * 8);
     int* off = total + p.E;
-    const int n = (end - first) * p.K;
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) total[e] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += blockDim.x) atomicAdd(&total[p.ids[(int64_t)first * p.K + i]], 1);
+    for (int i = threadIdx.x; i < n; i += blockDim.x) atomicAdd(&total[__ldcg(p.ids + (int64_t)from * p.K + i)], 1);
     __syncthreads();
     if (p.hist) {
         for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.hist[(int64_t)blockIdx.x * p.E + e] = total[e];
@@ -345,6 +400,7 @@ __global__ void __launch_bounds__(kPlaceThreads) place_kernel(const RouteParams 
     int* off = total + p.E;
     int* before = off + p.E;
     int* wh = before + p.E;
+    griddep_wait();
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) total[e] = before[e] = 0;
     __syncthreads();
     const int parts = max(1, (int)blockDim.x / p.E), mine = blockIdx.x;
@@ -372,28 +428,36 @@ __global__ void __launch_bounds__(kPlaceThreads) place_kernel(const RouteParams 
 template <int NL>
 cudaError_t run(RouteParams p, Carve& ws, cudaStream_t st) {
     constexpr int most = (NL <= 8 ? 1024 : NL == 16 ? 512 : 256) / 32;  // warps
+    constexpr size_t limit = 98304 + most * 256;
     static_assert(most * NL * 32 * 12 <= 98304, "a CTA's rows in shared memory");
     const int sms = device_info().sms;
-    cudaError_t e = cudaFuncSetAttribute(route_kernel<NL>, cudaFuncAttributeMaxDynamicSharedMemorySize, 98304);
-    if (e != cudaSuccess) return e;
+    auto bytes = [&](int W) { return (size_t)W * (p.E * 12 + 256); };
+    if (bytes(most) > (48 << 10)) {
+        const cudaError_t e = cudaFuncSetAttribute(route_kernel<NL>, cudaFuncAttributeMaxDynamicSharedMemorySize, limit);
+        if (e != cudaSuccess) return e;
+    }
     if (!p.plan.counts) {
         const int W = 4;
         const int64_t grid = min((int64_t)(p.rows + W - 1) / W, (int64_t)sms * 8);
-        return launch(route_kernel<NL>, dim3((unsigned)grid), dim3(32 * W), (size_t)W * p.E * 12, st, 0, p);
+        return launch(route_kernel<NL>, dim3((unsigned)grid), dim3(32 * W), bytes(W), st, 0, p);
     }
-    // With a plan: one CTA up to a few rows a warp, whose grouping needs no second launch; else a CTA an SM.
-    const int grid = p.rows <= 4 * most ? 1 : min(sms, (p.rows + most - 1) / most);
+    // With a plan: up to 4096 choices a row a warp and the grouping by the last CTA, which is one launch; from there on a CTA an
+    // SM, and a second launch.
+    const bool few = (int64_t)p.rows * p.K <= 4096;
+    const int W = few ? min(most, 8) : most;
+    const int grid = few ? (p.rows + W - 1) / W : min(sms, (p.rows + W - 1) / W);
     p.per = (p.rows + grid - 1) / grid;
-    const size_t smem = (size_t)most * p.E * 12;
-    if (grid == 1) return launch(route_kernel<NL>, dim3(1), dim3(32 * most), max(smem, (size_t)p.E * (8 * most + 8)), st, 0, p);
-    p.hist = ws.take<int32_t>((size_t)grid * p.E);
+    if (few && grid > 1) p.arrived = ws.take_counters(1);
+    if (!few) p.hist = ws.take<int32_t>((size_t)grid * p.E);
     if (ws.overflow) return cudaSuccess;
-    e = launch(route_kernel<NL>, dim3(grid), dim3(32 * most), max(smem, (size_t)p.E * (8 * most + 8)), st, 0, p);
-    if (e != cudaSuccess) return e;
+    cudaError_t e = launch(route_kernel<NL>, dim3(grid), dim3(32 * W), bytes(W), st, 0, p);
+    if (e != cudaSuccess || few) return e;
     const size_t place = (size_t)p.E * 4 * (3 + kPlaceThreads / 32);
-    e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 * 4 * (3 + kPlaceThreads / 32));
-    if (e != cudaSuccess) return e;
-    return launch(place_kernel, dim3(grid), dim3(kPlaceThreads), place, st, 0, p);
+    if (place > (48 << 10)) {
+        e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 * 4 * (3 + kPlaceThreads / 32));
+        if (e != cudaSuccess) return e;
+    }
+    return launch(place_kernel, dim3(grid), dim3(kPlaceThreads), place, st, 1, p);
 }
 
 }  // namespace
@@ -401,7 +465,7 @@ cudaError_t run(RouteParams p, Carve& ws, cudaStream_t st) {
 cudaError_t launch_route_scored(const RouteScoredCall& c, Carve& ws, cudaStream_t st) {
     RouteParams p = {c.logits, c.stride, (int)c.rows, c.E, c.K, c.rule.bias, c.rule.score == Q8_SCORE_SIGMOID,
                      c.rule.groups, c.rule.keep_groups, c.rule.group_top, c.rule.renorm, c.rule.scale, c.ids, c.gates, c.plan,
-                     nullptr, 0};
+                     nullptr, nullptr, 0};
     if (p.E <= 32) return run<1>(p, ws, st);
     if (p.E <= 64) return run<2>(p, ws, st);
     if (p.E <= 128) return run<4>(p, ws, st);
