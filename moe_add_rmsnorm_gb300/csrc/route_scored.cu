@@ -52,15 +52,15 @@ __device__ __forceinline__ double minus_inf<double>() { return -INFINITY; }
 // The kept groups as a bit mask, from the marks c [E] of the warp's row in shared memory (-infinity: out of service).
 // `close`: whether a kept and a left group are within `tol` of one another.
 template <typename T>
-__device__ __forceinline__ unsigned kept_groups(const T* c, int E, int groups, int keep, int top, T tol, bool& close) {
-    const int lane = threadIdx.x & 31, S = E / groups;
-    int lpg = 32;  // lanes a group: a power of two
-    while (lpg * groups > 32) lpg >>= 1;
-    const int g = lane / lpg;
+__device__ __forceinline__ unsigned kept_groups(const T* c, int S, int groups, int keep, int top, T tol, bool& close) {
+    const int lane = threadIdx.x & 31;
+    const int lpg_log2 = 31 - __clz(32 / groups), lpg = 1 << lpg_log2;  // lanes a group
+    const int g = lane >> lpg_log2;
     const T none = minus_inf<T>();
     T t1 = none, t2 = none;
     if (g < groups)
-        for (int i = lane % lpg; i < S; i += lpg) {
+#pragma unroll 4
+        for (int i = lane & (lpg - 1); i < S; i += lpg) {
             const T v = c[g * S + i];
             t2 = max(t2, min(t1, v));
             t1 = max(t1, v);
@@ -71,7 +71,7 @@ __device__ __forceinline__ unsigned kept_groups(const T* c, int E, int groups, i
         t1 = max(t1, o1);
     }
     const T sum = top == 2 && t2 > none ? t1 + t2 : t1;
-    const T mark = __shfl_sync(FULL, sum, (lane < groups ? lane : 0) * lpg);  // lane j: group j's
+    const T mark = __shfl_sync(FULL, sum, (lane < groups ? lane : 0) << lpg_log2);  // lane j: group j's
     int rank = 0;
     for (int j = 0; j < groups; ++j) {
         const T m = __shfl_sync(FULL, mark, j);
@@ -87,22 +87,26 @@ __device__ __forceinline__ unsigned kept_groups(const T* c, int E, int groups, i
     return __ballot_sync(FULL, kept);
 }
 
-// The choice of the warp's row in 64 bits: lane j gets the j-th expert, and whether it is in service.  l holds the row's
-// logits, c is scratch, both [E] of the warp in shared memory.
-__device__ __noinline__ void choose_exactly(const RouteParams& p, const float* l, double* c, int& id, bool& on) {
+// A logit as the rule takes it: what is no number is out of service, +infinity the largest value.
+__device__ __forceinline__ float logit_of(float v) { return isnan(v) ? -INFINITY : fminf(v, 3.402823466e38f); }
+
+// The choice of the warp's row in 64 bits: lane j gets the j-th expert, and whether it is in service.  c is scratch, [E] of the
+// warp in shared memory.
+__device__ __noinline__ void choose_exactly(const RouteParams& p, const float* row, double* c, int& id, bool& on) {
     const int lane = threadIdx.x & 31;
     double m = -INFINITY, z = 0;
     if (!p.sigmoid) {
-        for (int e = lane; e < p.E; e += 32) m = max(m, (double)l[e]);
+        for (int e = lane; e < p.E; e += 32) m = max(m, (double)logit_of(row[e]));
         for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(FULL, m, o));
         for (int e = lane; e < p.E; e += 32)
-            if (l[e] != -INFINITY) z += exp((double)l[e] - m);
+            if (logit_of(row[e]) != -INFINITY) z += exp((double)logit_of(row[e]) - m);
         for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(FULL, z, o);
     }
     for (int e = lane; e < p.E; e += 32) {
         double v = -INFINITY;
-        if (l[e] != -INFINITY) {
-            v = p.sigmoid ? 1 / (1 + exp(-(double)l[e])) : exp((double)l[e] - m) / z;
+        const float l = logit_of(row[e]);
+        if (l != -INFINITY) {
+            v = p.sigmoid ? 1 / (1 + exp(-(double)l)) : exp((double)l - m) / z;
             if (p.bias) v += p.bias[e];
             if (isnan(v)) v = -INFINITY;
         }
@@ -112,13 +116,13 @@ __device__ __noinline__ void choose_exactly(const RouteParams& p, const float* l
     unsigned kept = FULL;
     bool close;
     const int S = p.E / p.groups;
-    if (p.groups > 1) kept = kept_groups<double>(c, p.E, p.groups, p.keep, p.top, 0, close);
+    if (p.groups > 1) kept = kept_groups<double>(c, S, p.groups, p.keep, p.top, 0, close);
     __syncwarp();
     // what is out of service goes below every number, what is hidden or taken below that
     for (int e = lane; e < p.E; e += 32) {
         if (p.groups > 1 && !((kept >> (e / S)) & 1u)) c[e] = -INFINITY;
         else if (c[e] == -INFINITY) c[e] = -1.7e308;
-        else if (!p.bias) c[e] = l[e];
+        else if (!p.bias) c[e] = logit_of(row[e]);
     }
     __syncwarp();
     for (int j = 0; j < p.K; ++j) {
@@ -213,11 +217,15 @@ __global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_k
     __shared__ int tmp[64];
     __shared__ int last_cta;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, W = blockDim.x >> 5;
-    double* c64 = reinterpret_cast<double*>(smem) + w * p.E;  // a warp's marks (f32 in the same place)
+    double* c64 = reinterpret_cast<double*>(smem) + w * max(p.E, 32);  // a warp's marks (f32 in the same place)
     float* cs = reinterpret_cast<float*>(c64);
-    float* ls = reinterpret_cast<float*>(smem + (size_t)W * p.E * 8) + w * p.E;
-    unsigned* found = reinterpret_cast<unsigned*>(smem + (size_t)W * p.E * 12) + w * 64;  // [32] keys, [32] experts
+    uint2* found = reinterpret_cast<uint2*>(smem) + w * max(p.E, 32);  // candidates' keys and experts, in the marks' place
     const int S = p.E / p.groups;
+    uint32_t group[(NL + 3) / 4] = {};  // the group of expert lane + 32 i in byte i
+    if (p.groups > 1) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) group[i >> 2] |= (uint32_t)min((lane + 32 * i) / S, 31) << (8 * (i & 3));
+    }
     float b[NL], bmax = 0.f;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
@@ -237,8 +245,7 @@ __global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_k
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
             const int e = lane + 32 * i;
-            const float v = e < p.E ? row[e] : -INFINITY;
-            l[i] = isnan(v) ? -INFINITY : fminf(v, 3.402823466e38f);
+            l[i] = logit_of(e < p.E ? row[e] : -INFINITY);
             m = fmaxf(m, l[i]);
         }
         float m0 = 0.f, z = 0.f, zi = 0.f;
@@ -258,27 +265,42 @@ __global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_k
         const float pmax = p.sigmoid ? 1.f : zi;
         const float tol = 2e-6f * pmax + 2e-7f * bmax + (p.sigmoid ? 0.f : 1.2e-7f * (NL + 5) * pmax);
         bool slow = false;
+        // (a loop for each of the rule's choices: tests of the rule for every expert took a third of the kernel's instructions)
+        if (marks) {
+            float c[NL];
+            if (p.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int e = lane + 32 * i;
-            float c = l[i];
-            if (marks) {
-                c = p.sigmoid ? fast_sigmoid(l[i]) : __expf(l[i] - m0) * zi;
-                if (p.bias) c += b[i];
+                for (int i = 0; i < NL; ++i) c[i] = fast_sigmoid(l[i]) + b[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < NL; ++i) c[i] = fmaf(__expf(l[i] - m0), zi, b[i]);
             }
-            const bool on = e < p.E && l[i] > -INFINITY && c > -INFINITY;  // (a c that is no number fails too)
-            if (e < p.E) {
-                ls[e] = l[i];  // (an expert that its bias takes out of service still counts in the softmax)
-                if (p.groups > 1) cs[e] = on ? c : -INFINITY;
+#pragma unroll
+            for (int i = 0; i < NL; ++i)  // (a c that is no number is out of service too)
+                c[i] = l[i] > -INFINITY && c[i] > -INFINITY ? c[i] : -INFINITY;
+            if (p.groups > 1) {
+#pragma unroll
+                for (int i = 0; i < NL; ++i)
+                    if (lane + 32 * i < p.E) cs[lane + 32 * i] = c[i];
             }
-            key[i] = e >= p.E ? kHidden : !on ? kOff : order_key(p.bias ? c : l[i]);
+            if (p.bias) {
+#pragma unroll
+                for (int i = 0; i < NL; ++i) l[i] = c[i];  // what orders the experts
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NL; ++i) key[i] = l[i] > -INFINITY ? order_key(l[i]) : kOff;
+        if (p.E < 32 * NL) {
+#pragma unroll
+            for (int i = 0; i < NL; ++i)
+                if (lane + 32 * i >= p.E) key[i] = kHidden;
         }
         if (p.groups > 1) {
             __syncwarp();
-            const unsigned kept = kept_groups<float>(cs, p.E, p.groups, p.keep, p.top, 2.5f * tol, slow);
+            const unsigned kept = kept_groups<float>(cs, S, p.groups, p.keep, p.top, 2.5f * tol, slow);
 #pragma unroll
             for (int i = 0; i < NL; ++i)
-                if (!((kept >> min((lane + 32 * i) / S, 31)) & 1u)) key[i] = kHidden;
+                if (!((kept >> (group[i >> 2] >> (8 * (i & 3)) & 31u)) & 1u)) key[i] = kHidden;
         }
         // the keys that may be among the K largest: all from the K-th largest of the lanes' maxima on, and a biased order's
         // error below it
@@ -290,14 +312,14 @@ __global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_k
             if (lane == __ffs(__ballot_sync(FULL, mine == from)) - 1) mine = kHidden;
         }
         if (from > kOff && p.bias) from = max(order_key(key_value(from) - tol), kOff + 1);
+        __syncwarp();  // (the marks have been read)
         const unsigned least = max(from, kOff + 1);
         int n = 0;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
             const unsigned here = __ballot_sync(FULL, key[i] >= least);
             if (here == 0) continue;
-            const int at = n + __popc(here & ((1u << lane) - 1));
-            if (key[i] >= least && at < 32) found[at] = key[i], found[32 + at] = lane + 32 * i;
+            if (key[i] >= least) found[n + __popc(here & ((1u << lane) - 1))] = make_uint2(key[i], lane + 32 * i);
             n += __popc(here);
         }
         if (from <= kOff && n <= 32) {  // too few in service: the first of the others behind them
@@ -305,7 +327,7 @@ __global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_k
             for (int i = 0; i < NL; ++i) {
                 const unsigned here = __ballot_sync(FULL, key[i] == kOff);
                 const int at = n + __popc(here & ((1u << lane) - 1));
-                if (key[i] == kOff && at < 32) found[at] = kOff, found[32 + at] = lane + 32 * i;
+                if (key[i] == kOff && at < 32) found[at] = make_uint2(kOff, lane + 32 * i);
                 n = min(n + __popc(here), 32);
             }
         }
@@ -315,22 +337,31 @@ __global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_k
         int id = 0, rank = 32;
         bool close = false;
         if (n <= 32) {
-            if (lane < n) k = found[lane], id = found[32 + lane];
-            const float v = k > kOff ? key_value(k) : 0.f;
+            if (lane < n) k = found[lane].x, id = found[lane].y;
             rank = lane < n ? 0 : 32;
-            for (int j = 0; j < n; ++j) {
-                const unsigned o = __shfl_sync(FULL, k, j);
-                rank += o > k || (o == k && j < lane);
-                close |= p.bias && j != lane && o > kOff && k > kOff && !(fabsf(key_value(o) - v) > tol);
+            for (int j = 0; j < n; j += 4) {  // (lanes past the last hold what is before nothing)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const unsigned o = __shfl_sync(FULL, k, j + i);
+                    rank += o > k || (o == k && j + i < lane);
+                }
+            }
+            if (p.bias) {  // neighbours of the order that the errors reach across
+                __syncwarp();
+                if (lane < n) found[rank].x = k;
+                __syncwarp();
+                const unsigned here = found[lane].x, next = found[(lane + 1) & 31].x;
+                close = lane < p.K && lane + 1 < n && next > kOff && !(key_value(here) - key_value(next) > tol);
             }
         }
-        close = __any_sync(FULL, close && rank < p.K);
+        close = __any_sync(FULL, close);
         bool on = k > kOff;
         if (slow || n > 32 || (close && !p.sigmoid)) {
-            choose_exactly(p, ls, c64, id, on);
+            __syncwarp();
+            choose_exactly(p, row, c64, id, on);
             rank = lane;
         } else if (close) {  // the candidates' marks in 64 bits
-            const double c = on ? 1 / (1 + exp(-(double)ls[id])) + (double)p.bias[id] : k == kOff ? -1.7e308 : -INFINITY;
+            const double c = on ? 1 / (1 + exp(-(double)logit_of(row[id]))) + (double)p.bias[id] : k == kOff ? -1.7e308 : -INFINITY;
             rank = lane < n ? 0 : 32;
             for (int j = 0; j < n; ++j) {
                 const double o = __shfl_sync(FULL, c, j);
@@ -341,7 +372,7 @@ __global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_k
         const bool kth = rank < p.K;
         id = min(max(id, 0), p.E - 1);
         float gate = 0.f;
-        const float v = kth && on ? ls[id] : -INFINITY;
+        const float v = kth && on ? logit_of(row[id]) : -INFINITY;
         if (p.renorm) {  // relative to the largest: below -20 a sigmoid is e^l to less than f32's rounding
             const float most = warp_max(v);
             if (v > -INFINITY) gate = p.sigmoid && most >= -20.f ? 1.f / (1.f + expf(-v)) : expf(v - most);
@@ -352,7 +383,7 @@ __global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_k
         } else {  // (the sum again, by the exact exponential)
             float zs = 0.f;
 #pragma unroll
-            for (int i = 0; i < NL; ++i) zs += expf(l[i] - m0);
+            for (int i = 0; i < NL; ++i) zs += expf(logit_of(lane + 32 * i < p.E ? row[lane + 32 * i] : -INFINITY) - m0);
             zs = group_sum<32>(zs);
             if (v > -INFINITY) gate = expf(v - m0) / zs;
         }
@@ -376,7 +407,7 @@ __global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_k
         from = 0, n = p.rows * p.K;
     }
     int* wh = reinterpret_cast<int*>(smem);
-    int* total = reinterpret_cast<int*>(smem + (size_t)W * p.E * 8);
+    int* total = reinterpret_cast<int*>(smem + (size_t)W * p.E * 4);
     int* off = total + p.E;
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) total[e] = 0;
     __syncthreads();
@@ -403,18 +434,33 @@ __global__ void __launch_bounds__(kPlaceThreads) place_kernel(const RouteParams 
     griddep_wait();
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) total[e] = before[e] = 0;
     __syncthreads();
-    const int parts = max(1, (int)blockDim.x / p.E), mine = blockIdx.x;
-    for (int i = threadIdx.x; i < parts * p.E; i += blockDim.x) {
-        const int e = i % p.E;
-        int all = 0, pre = 0;
-#pragma unroll 8
-        for (int b = i / p.E; b < (int)gridDim.x; b += parts) {
-            const int n = p.hist[(int64_t)b * p.E + e];
-            all += n;
-            if (b < mine) pre += n;
+    const int mine = blockIdx.x;
+    if (p.E % 4 == 0) {  // four experts a thread
+        const int quads = p.E / 4, parts = max(1, (int)blockDim.x / quads);
+        for (int i = threadIdx.x; i < parts * quads; i += blockDim.x) {
+            const int q = i % quads;
+            int4 all = make_int4(0, 0, 0, 0), pre = all;
+#pragma unroll 10
+            for (int b = i / quads; b < (int)gridDim.x; b += parts) {
+                const int4 n = *reinterpret_cast<const int4*>(p.hist + (int64_t)b * p.E + 4 * q);
+                all.x += n.x, all.y += n.y, all.z += n.z, all.w += n.w;
+                if (b < mine) pre.x += n.x, pre.y += n.y, pre.z += n.z, pre.w += n.w;
+            }
+            atomicAdd(&total[4 * q], all.x), atomicAdd(&total[4 * q + 1], all.y), atomicAdd(&total[4 * q + 2], all.z);
+            atomicAdd(&total[4 * q + 3], all.w), atomicAdd(&before[4 * q], pre.x), atomicAdd(&before[4 * q + 1], pre.y);
+            atomicAdd(&before[4 * q + 2], pre.z), atomicAdd(&before[4 * q + 3], pre.w);
         }
-        atomicAdd(&total[e], all);
-        atomicAdd(&before[e], pre);
+    } else {
+        for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+            int all = 0, pre = 0;
+#pragma unroll 8
+            for (int b = 0; b < (int)gridDim.x; ++b) {
+                const int n = p.hist[(int64_t)b * p.E + e];
+                all += n;
+                if (b < mine) pre += n;
+            }
+            total[e] = all, before[e] = pre;
+        }
     }
     __syncthreads();
     scan_totals(total, p.E, off, tmp, p.plan, mine == 0);
@@ -428,10 +474,10 @@ __global__ void __launch_bounds__(kPlaceThreads) place_kernel(const RouteParams 
 template <int NL>
 cudaError_t run(RouteParams p, Carve& ws, cudaStream_t st) {
     constexpr int most = (NL <= 8 ? 1024 : NL == 16 ? 512 : 256) / 32;  // warps
-    constexpr size_t limit = 98304 + most * 256;
-    static_assert(most * NL * 32 * 12 <= 98304, "a CTA's rows in shared memory");
+    constexpr size_t limit = 65536;
+    static_assert(most * NL * 32 * 8 <= limit, "a CTA's rows in shared memory");
     const int sms = device_info().sms;
-    auto bytes = [&](int W) { return (size_t)W * (p.E * 12 + 256); };
+    auto bytes = [&](int W) { return (size_t)W * max(p.E, 32) * 8; };
     if (bytes(most) > (48 << 10)) {
         const cudaError_t e = cudaFuncSetAttribute(route_kernel<NL>, cudaFuncAttributeMaxDynamicSharedMemorySize, limit);
         if (e != cudaSuccess) return e;
