@@ -557,7 +557,7 @@ def _tensor(t, kind, shape, device, name):
     """The address of a contiguous tensor of this type, shape and device (None: NULL)."""
     if t is None:
         return None
-    if t.dtype is not kind or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+    if t.dtype is not kind or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
         _refuse(f"{name}: not a contiguous {kind} tensor {tuple(shape)} on the current device")
     return t.data_ptr()
 

@@ -1,8 +1,23 @@
 // Launch interface between the C ABI of the 4-bit feed-forward block (ffn4_api.cu) and its kernels.  Host code only.
 #pragma once
+#include <atomic>
+
 #include "kernels.h"
 
 namespace q8 {
+
+// Allows `kernel` `bytes` of dynamic shared memory, once a device (the call takes longer than the checks of a whole call).
+template <typename Kern>
+cudaError_t allow_smem(Kern kernel, size_t bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // ---- the norms around a block (postnorm.cu) ---------------------------------------------------------------------
 struct PostnormCall {

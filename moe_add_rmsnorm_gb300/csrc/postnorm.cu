@@ -88,6 +88,8 @@ __global__ void __launch_bounds__(T) postnorm_kernel(const PostnormParams p) {
     __shared__ F2 red[2][32];
     const int d = p.d, t = threadIdx.x;
     const int64_t row = blockIdx.x, at = row * d;
+    griddep_wait();  // (launches overlap up to here: nothing is read before the launch before has ended)
+    griddep_launch();
     float a[PER][4], b[PER][4];
 #pragma unroll
     for (int j = 0; j < PER; ++j) load4<VEC>(p.b + at, 4 * (j * T + t), d, b[j]);
@@ -184,13 +186,13 @@ cudaError_t launch_postnorm(const PostnormCall& c, cudaStream_t st) {
                           (const void*)c.y, c.gate_col == 1 ? (const void*)c.gate : nullptr})
         vec = vec && aligned16(q);
     const dim3 grid((unsigned)c.rows);
-    if (!vec) return launch(postnorm_kernel<512, 8, false>, grid, dim3(512), 0, st, 0, p);
+    if (!vec) return launch(postnorm_kernel<512, 8, false>, grid, dim3(512), 0, st, 1, p);
     // A row's time is its chain of reductions: with few rows as many threads as it has vectors; with many, the CTAs of an SM
     // hide one another's chains and 256 threads of several vectors spend less on the reductions.
     const int n4 = (int)((c.d + 3) / 4);
     const bool many = c.rows > 2 * device_info().sms;
 #define Q8_POSTNORM(T, PER) \
-    if (n4 <= (T) * (PER)) return launch(postnorm_kernel<T, PER, true>, grid, dim3(T), 0, st, 0, p);
+    if (n4 <= (T) * (PER)) return launch(postnorm_kernel<T, PER, true>, grid, dim3(T), 0, st, 1, p);
     if (many) {
         Q8_POSTNORM(128, 1)
         Q8_POSTNORM(256, 1)

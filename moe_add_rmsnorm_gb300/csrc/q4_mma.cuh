@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(256) q4_slots_kernel(const MmaParams p) {
     constexpr int PARTS = FORM == FORM_ONE ? 1 : 2;
     __shared__ float most[2][8];
     __shared__ int where[2];
+    griddep_wait();    // the launch before has ended, which the products' launch takes for granted from its start on
     griddep_launch();
     const int octets = 16 * p.chunks, cols = p.w0.cols, lane = threadIdx.x & 31;
     const int n = p.kind == Q4_DENSE ? p.R : p.R * p.K, groups = mma_groups(p);
@@ -728,11 +729,12 @@ cudaError_t run_mma(MmaParams p, int64_t groups, Carve& ws, cudaStream_t st) {
     const bool gate_up = p.kind == Q4_GATE_UP;
     if (!q4_map(&m0, p.w0, gate_up ? 64 : 128) || !q4_map(&m1, gate_up ? p.w1 : p.w0, gate_up ? 64 : 128)) return cudaErrorInvalidValue;
     const dim3 lay((unsigned)min(p.kind == Q4_DENSE ? (int64_t)p.R : (int64_t)p.R * p.K, (int64_t)sms * 8));
-    cudaError_t e = launch(q4_slots_kernel<FORM>, lay, dim3(256), 0, st, 0, p);
+    cudaError_t e = launch(q4_slots_kernel<FORM>, lay, dim3(256), 0, st, 1, p);
     if (e != cudaSuccess) return e;
     constexpr size_t smem = sizeof(MmaShared<FORM, TN>);
     static_assert(smem <= 232448, "a CTA's shared memory");
-    e = cudaFuncSetAttribute(q4_mma_kernel<FORM, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> done;
+    e = allow_smem(q4_mma_kernel<FORM, TN>, smem, done);
     if (e != cudaSuccess) return e;
     return launch(q4_mma_kernel<FORM, TN>, dim3((unsigned)min(items, (int64_t)sms)), dim3(kMmaThreads), smem, st, 1, p, m0, m1);
 }

@@ -148,6 +148,8 @@ template <int FORM, int MT>
 __global__ void __launch_bounds__(32 * kRowWarps, 2) q4_row_kernel(const RowParams p) {
     extern __shared__ __align__(128) char smem[];
     __shared__ uint4 zeros[4];
+    griddep_wait();  // (launches overlap up to here: nothing is read before the launch before has ended)
+    griddep_launch();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int nb = p.w0.cols >> 5, last = (int)p.out_rows - 1;
     const int64_t row_bytes = p.w0.cols >> 1, row_groups = p.w0.cols >> p.w0.group_log2;
@@ -337,10 +339,11 @@ void deal(RowParams& p, int parts) {
 template <int FORM, int MT>
 cudaError_t run(const RowParams& p, cudaStream_t st) {
     const size_t smem = row_smem(p, MT);
-    const cudaError_t e = cudaFuncSetAttribute(q4_row_kernel<FORM, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowSmem);
+    static std::atomic<uint64_t> done;
+    const cudaError_t e = allow_smem(q4_row_kernel<FORM, MT>, kRowSmem, done);
     if (e != cudaSuccess) return e;
     const int64_t ctas = (p.tiles + p.side - 1) / p.side, most = (int64_t)device_info().sms * 2;
-    return launch(q4_row_kernel<FORM, MT>, dim3((unsigned)min(ctas, most)), dim3(32 * kRowWarps), smem, st, 0, p);
+    return launch(q4_row_kernel<FORM, MT>, dim3((unsigned)min(ctas, most)), dim3(32 * kRowWarps), smem, st, 1, p);
 }
 
 template <int FORM>

@@ -39,6 +39,7 @@ template <int FORM>
 __global__ void __launch_bounds__(256) q4_parts_kernel(const RowsParams p) {
     constexpr int PARTS = FORM == FORM_ONE ? 1 : 2;
     __shared__ float most[2][8];
+    griddep_wait();    // the launch before has ended, which the products' launch takes for granted from its start on
     griddep_launch();
     const int octets = 16 * p.chunks, cols = p.w0.cols, lane = threadIdx.x & 31;
     int buf = 0;
@@ -421,7 +422,8 @@ cudaError_t run_rows(RowsParams p, int64_t groups, cudaStream_t st) {
         p.wk *= 2;
     const int side = kWarps / p.wk;
     const dim3 grid((unsigned)((p.row_tiles + side - 1) / side), (unsigned)min(groups, (int64_t)65535), (unsigned)zs);
-    const cudaError_t e = cudaFuncSetAttribute(q4_rows_kernel<FORM, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmem);
+    static std::atomic<uint64_t> done;
+    const cudaError_t e = allow_smem(q4_rows_kernel<FORM, NT>, kRowsSmem, done);
     if (e != cudaSuccess) return e;
     return launch(q4_rows_kernel<FORM, NT>, grid, dim3(32 * kWarps), smem(p.wk), st, 1, p);
 }
@@ -430,7 +432,7 @@ cudaError_t run_rows(RowsParams p, int64_t groups, cudaStream_t st) {
 template <int FORM>
 cudaError_t launch_rows(const RowsParams& p, int64_t groups, cudaStream_t st) {
     const dim3 lay((unsigned)min(p.act_rows, (int64_t)device_info().sms * 8));
-    const cudaError_t e = launch(q4_parts_kernel<FORM>, lay, dim3(256), 0, st, 0, p);
+    const cudaError_t e = launch(q4_parts_kernel<FORM>, lay, dim3(256), 0, st, 1, p);
     if (e != cudaSuccess) return e;
     // Tiles of columns a pass: those that twice an expert's average rows fill.
     const int64_t rows = p.kind == Q4_DENSE ? p.R : 2 * ((int64_t)p.R * p.K / groups);

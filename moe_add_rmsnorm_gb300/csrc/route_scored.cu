@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_k
     double* c64 = reinterpret_cast<double*>(smem) + w * max(p.E, 32);  // a warp's marks (f32 in the same place)
     float* cs = reinterpret_cast<float*>(c64);
     uint2* found = reinterpret_cast<uint2*>(smem) + w * max(p.E, 32);  // candidates' keys and experts, in the marks' place
+    griddep_wait();  // (launches overlap up to here: nothing is read before the launch before has ended)
     const int S = p.E / p.groups;
     uint32_t group[(NL + 3) / 4] = {};  // the group of expert lane + 32 i in byte i
     if (p.groups > 1) {
@@ -479,13 +480,14 @@ cudaError_t run(RouteParams p, Carve& ws, cudaStream_t st) {
     const int sms = device_info().sms;
     auto bytes = [&](int W) { return (size_t)W * max(p.E, 32) * 8; };
     if (bytes(most) > (48 << 10)) {
-        const cudaError_t e = cudaFuncSetAttribute(route_kernel<NL>, cudaFuncAttributeMaxDynamicSharedMemorySize, limit);
+        static std::atomic<uint64_t> done;
+        const cudaError_t e = allow_smem(route_kernel<NL>, limit, done);
         if (e != cudaSuccess) return e;
     }
     if (!p.plan.counts) {
         const int W = 4;
         const int64_t grid = min((int64_t)(p.rows + W - 1) / W, (int64_t)sms * 8);
-        return launch(route_kernel<NL>, dim3((unsigned)grid), dim3(32 * W), bytes(W), st, 0, p);
+        return launch(route_kernel<NL>, dim3((unsigned)grid), dim3(32 * W), bytes(W), st, 1, p);
     }
     // With a plan: up to 4096 choices a row a warp and the grouping by the last CTA, which is one launch; from there on a CTA an
     // SM, and a second launch.
@@ -496,11 +498,12 @@ cudaError_t run(RouteParams p, Carve& ws, cudaStream_t st) {
     if (few && grid > 1) p.arrived = ws.take_counters(1);
     if (!few) p.hist = ws.take<int32_t>((size_t)grid * p.E);
     if (ws.overflow) return cudaSuccess;
-    cudaError_t e = launch(route_kernel<NL>, dim3(grid), dim3(32 * W), bytes(W), st, 0, p);
+    cudaError_t e = launch(route_kernel<NL>, dim3(grid), dim3(32 * W), bytes(W), st, 1, p);
     if (e != cudaSuccess || few) return e;
     const size_t place = (size_t)p.E * 4 * (3 + kPlaceThreads / 32);
     if (place > (48 << 10)) {
-        e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 * 4 * (3 + kPlaceThreads / 32));
+        static std::atomic<uint64_t> done;
+        e = allow_smem(place_kernel, 1024 * 4 * (3 + kPlaceThreads / 32), done);
         if (e != cudaSuccess) return e;
     }
     return launch(place_kernel, dim3(grid), dim3(kPlaceThreads), place, st, 1, p);
