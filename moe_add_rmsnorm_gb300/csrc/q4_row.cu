@@ -36,9 +36,9 @@ struct RowParams {
     const float *gates, *residual;
     float* y;
     int steps;            // of a row
-    int parts;            // warps' parts of a row's steps
+    int parts_log2;       // warps' parts of a row's steps
     int segs, spw, side;  // a tile's segments (parts, or experts times parts), those a warp takes, tiles side by side
-    int tiles, row_tiles; // of 16 rows: all, a group's
+    int tiles;            // of 16 rows, of a choice's for gate-up
     int vecs;             // activation rows
     uint32_t vec;         // bytes of one in shared memory
 };
@@ -148,19 +148,24 @@ template <int FORM, int MT>
 __global__ void __launch_bounds__(32 * kRowWarps, 2) q4_row_kernel(const RowParams p) {
     extern __shared__ __align__(128) char smem[];
     __shared__ uint4 zeros[4];
+    const bool has_z = p.w0.z != nullptr;
     griddep_wait();  // (launches overlap up to here: nothing is read before the launch before has ended)
     griddep_launch();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int nb = p.w0.cols >> 5, last = (int)p.out_rows - 1;
-    const int64_t row_bytes = p.w0.cols >> 1, row_groups = p.w0.cols >> p.w0.group_log2;
-    const int mine = (p.steps + p.parts - 1) / p.parts;
-    const int own_seg = p.side > 1 ? w % p.segs : w, off_tile = p.side > 1 ? w / p.segs : 0;
+    const int nb = p.w0.cols >> 5, last = (int)p.out_rows - 1, choice = blockIdx.y;  // gate-up: the CTA's choice
+    const int64_t row_bytes = p.w0.cols >> 1;
+    const int row_groups = p.w0.cols >> p.w0.group_log2, mine = (p.steps + (1 << p.parts_log2) - 1) >> p.parts_log2;
+    const int own_seg = p.side > 1 ? w & (p.segs - 1) : w, off_tile = p.side > 1 ? w / p.segs : 0;
     const int stride = gridDim.x * p.side, first = off_tile < p.side ? (int)blockIdx.x * p.side + off_tile : p.tiles;
     const int rounds = (p.tiles - (int)blockIdx.x * p.side + stride - 1) / stride;  // the CTA's, alike in all its warps
     char* ring = smem + w * (kRowStages * MT * kStepBytes);
     char* vecs = smem + kRowWarps * kRowStages * MT * kStepBytes;
     float* part = reinterpret_cast<float*>(vecs + p.vecs * p.vec);  // [2][side * segs][MT][16]
     const int slots = p.side * p.segs;
+    auto expert = [&](int j) {  // of the row's choice j, or -1
+        const int e = p.ids ? p.ids[j] : 0;
+        return e >= 0 && e < p.E ? e : -1;
+    };
 
     // A place in the warp's run of (tile, segment, step).
     struct Place {
@@ -171,12 +176,10 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) q4_row_kernel(const RowPara
     auto locate = [&](Place& l) {
         l.at = 0;
         l.row = -1;
-        l.step = l.seg % p.parts * mine;
+        l.step = (l.seg & ((1 << p.parts_log2) - 1)) * mine;
         if (l.tile >= p.tiles || l.seg >= p.segs) return;
-        const int group = p.kind == Q4_DOWN ? l.seg / p.parts : l.tile / p.row_tiles;
-        const int r0 = 16 * (p.kind == Q4_DOWN ? l.tile : l.tile - group * p.row_tiles) + g;
-        const int e = p.ids ? p.ids[group] : 0;
-        if (e < 0 || e >= p.E) return;
+        const int e = expert(p.kind == Q4_DOWN ? l.seg >> p.parts_log2 : choice), r0 = 16 * l.tile + g;
+        if (e < 0) return;
         l.row = e * p.out_rows + min(r0, last);
         l.more = min(r0 + 8, last) - min(r0, last);
     };
@@ -195,15 +198,14 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) q4_row_kernel(const RowPara
     uint32_t into = 0;
     auto fetch = [&]() {
         if (in.row >= 0 && in.step < p.steps) {
-            const int64_t from = in.row * row_bytes + 128 * in.step + 16 * t;
+            const int64_t from = in.row * row_bytes + 128 * in.step + 16 * t, more = in.more * row_bytes;
             const bool one = 8 * in.step + t < nb, two = 8 * in.step + 4 + t < nb;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const uint8_t* a = (m ? p.w1.q : p.w0.q) + from;
-                const uint8_t* b = a + in.more * row_bytes;
                 const uint32_t d = to + into + m * kStepBytes;
-                if (one) copy16(d, a), copy16(d + 1024, b);
-                if (two) copy16(d ^ 64, a + 64), copy16((d + 1024) ^ 64, b + 64);
+                if (one) copy16(d, a), copy16(d + 1024, a + more);
+                if (two) copy16(d ^ 64, a + 64), copy16((d + 1024) ^ 64, a + more + 64);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -213,17 +215,19 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) q4_row_kernel(const RowPara
     uint32_t s[MT][2][2], z[MT][2][2];  // the next step's scales and zero points: [half step][row g, g + 8]
     auto scales = [&]() {
         const bool ok = sc.row >= 0 && sc.step < p.steps;
+        const int64_t row = sc.row * row_groups;
+        const int more = sc.more * row_groups;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int b = 8 * sc.step + 4 * k + t;
+            const int b = 8 * sc.step + 4 * k + t, col = (32 * b) >> p.w0.group_log2;
             const bool here = ok && b < nb;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int64_t at = (sc.row + (i ? sc.more : 0)) * row_groups + ((32 * b) >> p.w0.group_log2);
+                const int64_t at = row + (i ? col + more : col);
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     s[m][k][i] = here ? __ldg((m ? p.w1.s : p.w0.s) + at) : 0u;
-                    z[m][k][i] = here && p.w0.z ? __ldg((m ? p.w1.z : p.w0.z) + at) : 8u;
+                    if (has_z) z[m][k][i] = here ? __ldg((m ? p.w1.z : p.w0.z) + at) : 8u;
                 }
             }
         }
@@ -243,8 +247,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) q4_row_kernel(const RowPara
         for (int k = 0; k < p.spw; ++k) {
             const int seg = own_seg + k * kRowWarps;
             const bool real = off_tile < p.side && seg < p.segs;
-            const int step0 = seg % p.parts * mine;
-            const char* vec = vecs + (p.kind == Q4_DOWN && real ? seg / p.parts : 0) * p.vec;
+            const int step0 = (seg & ((1 << p.parts_log2) - 1)) * mine;
+            const char* vec = vecs + (p.kind == Q4_DOWN && real ? seg >> p.parts_log2 : 0) * p.vec;
             float acc[MT][2] = {};
             for (int i = 0; i < mine; ++i) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(kRowStages - 2) : "memory");
@@ -258,7 +262,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) q4_row_kernel(const RowPara
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) sw[m][h][j] = scale_f32(s[m][h][j], p.w0.bf16), zz[m][h][j] = z[m][h][j];
+                        for (int j = 0; j < 2; ++j) sw[m][h][j] = scale_f32(s[m][h][j], p.w0.bf16), zz[m][h][j] = has_z ? z[m][h][j] : 8u;
                 scales();
                 if (real && step < p.steps) {
 #pragma unroll
@@ -298,25 +302,22 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) q4_row_kernel(const RowPara
         __syncthreads();  // (the next tiles' sums go to the other half: one barrier a round)
         if (own_seg == 0 && lane < 16 && tile < p.tiles) {
             const float* sums = part + (buf * slots + off_tile * p.segs) * MT * 16 + lane;
+            const int r = 16 * tile + lane;
             if (p.kind == Q4_DOWN) {
-                const int r = 16 * tile + lane;
                 float sum = 0.f;
                 for (int j = 0; j < p.K; ++j) {
-                    const int e = p.ids[j];
-                    if (e < 0 || e >= p.E) continue;
+                    if (expert(j) < 0) continue;
                     float v = 0.f;
-                    for (int i = 0; i < p.parts; ++i) v += sums[(j * p.parts + i) * 16];
+                    for (int i = 0; i < 1 << p.parts_log2; ++i) v += sums[((j << p.parts_log2) + i) * 16];
                     sum = fmaf(p.gates[j], v, sum);
                 }
                 if (r <= last) p.y[r] = p.residual ? p.residual[r] + sum : sum;
             } else {
-                const int group = tile / p.row_tiles, r = 16 * (tile - group * p.row_tiles) + lane;
-                const int e = p.ids ? p.ids[group] : 0;
                 float v[MT] = {};
                 for (int i = 0; i < p.segs; ++i)
 #pragma unroll
                     for (int m = 0; m < MT; ++m) v[m] += sums[(i * MT + m) * 16];
-                if (r <= last && e >= 0 && e < p.E) p.y[group * p.out_rows + r] = MT == 2 ? silu_f32(v[0]) * v[MT - 1] : v[0];
+                if (r <= last && expert(choice) >= 0) p.y[choice * p.out_rows + r] = MT == 2 ? silu_f32(v[0]) * v[MT - 1] : v[0];
             }
         }
     }
@@ -328,12 +329,12 @@ size_t row_smem(const RowParams& p, int mt) {
     return (size_t)kRowWarps * kRowStages * mt * kStepBytes + (size_t)p.vecs * p.vec + 2 * (size_t)p.side * p.segs * mt * 64;
 }
 
-// How a tile's steps are dealt to the warps: `parts` of a row each (of an expert's, for down).
-void deal(RowParams& p, int parts) {
-    p.parts = parts;
-    p.segs = p.kind == Q4_DOWN ? p.K * parts : parts;
+// How a tile's steps are dealt to the warps: 2^parts_log2 parts of a row each (of an expert's, for down).
+void deal(RowParams& p, int parts_log2) {
+    p.parts_log2 = parts_log2;
+    p.segs = (p.kind == Q4_DOWN ? p.K : 1) << parts_log2;
     p.spw = (p.segs + kRowWarps - 1) / kRowWarps;
-    p.side = p.spw > 1 ? 1 : kRowWarps / p.segs;
+    p.side = p.spw > 1 || p.kind == Q4_DOWN ? 1 : kRowWarps / p.segs;
 }
 
 template <int FORM, int MT>
@@ -342,22 +343,22 @@ cudaError_t run(const RowParams& p, cudaStream_t st) {
     static std::atomic<uint64_t> done;
     const cudaError_t e = allow_smem(q4_row_kernel<FORM, MT>, kRowSmem, done);
     if (e != cudaSuccess) return e;
-    const int64_t ctas = (p.tiles + p.side - 1) / p.side, most = (int64_t)device_info().sms * 2;
-    return launch(q4_row_kernel<FORM, MT>, dim3((unsigned)min(ctas, most)), dim3(32 * kRowWarps), smem, st, 1, p);
+    const int choices = p.kind == Q4_GATE_UP ? p.K : 1;
+    const int64_t ctas = (p.tiles + p.side - 1) / p.side, most = max(device_info().sms * 2 / choices, 1);
+    return launch(q4_row_kernel<FORM, MT>, dim3((unsigned)min(ctas, most), choices), dim3(32 * kRowWarps), smem, st, 1, p);
 }
 
 template <int FORM>
 cudaError_t run_kind(RowParams p, cudaStream_t st) {
     p.vec = (uint32_t)(8 * p.steps * (block_bytes<FORM>() + (FORM == FORM_F32 ? 4 : 0)));
-    // The parts that leave the warps of two CTAs an SM the fewest steps one after another.
-    int best = 1;
+    // The parts that leave an SM the fewest steps, counting half a one for each tile's end.
+    int best = 0;
     int64_t fewest = INT64_MAX;
-    for (int parts = 1; parts <= 8 && parts <= p.steps; ++parts) {
-        if (p.kind != Q4_DOWN && (parts & (parts - 1))) continue;
-        deal(p, parts);
-        const int64_t at_once = (int64_t)device_info().sms * 2 * p.side;
-        const int64_t steps = (p.tiles + at_once - 1) / at_once * p.spw * ((p.steps + parts - 1) / parts);
-        if (steps < fewest) fewest = steps, best = parts;
+    for (int l = 0; l <= 3 && (1 << l) <= p.steps; ++l) {
+        deal(p, l);
+        const int64_t ctas = (int64_t)(p.tiles + p.side - 1) / p.side * (p.kind == Q4_GATE_UP ? p.K : 1), sms = device_info().sms;
+        const int64_t steps = (ctas + sms - 1) / sms * (2 * p.spw * ((p.steps + (1 << l) - 1) >> l) + 1);
+        if (steps < fewest) fewest = steps, best = l;
     }
     deal(p, best);
     return p.kind == Q4_GATE_UP ? run<FORM, 2>(p, st) : run<FORM, 1>(p, st);
@@ -388,8 +389,7 @@ cudaError_t launch_q4_row(const Q4Call& c, cudaStream_t st) {
     p.y = c.y;
     p.steps = (c.w0.cols + 255) / 256;
     p.vecs = c.kind == Q4_DOWN ? c.K : 1;
-    p.row_tiles = (int)((c.out_rows + 15) / 16);
-    p.tiles = p.row_tiles * (c.kind == Q4_GATE_UP ? c.K : 1);
+    p.tiles = (int)((c.out_rows + 15) / 16);
     if (c.act.x) return run_kind<FORM_F32>(p, st);
     return c.act.lo ? run_kind<FORM_TWO>(p, st) : run_kind<FORM_ONE>(p, st);
 }
