@@ -63,27 +63,29 @@ struct Group {
 
 __device__ __forceinline__ int mma_groups(const MmaParams& p) {
     if (p.kind == Q4_DENSE) return 1;
-    if (!p.plan.active) return p.K;  // (one row has no plan: every choice is a group)
     return min(max(p.plan.active[0], 0), (int)min(p.E, (int64_t)p.R * p.K));
 }
 
-// Group a.  Slots start at a multiple of eight behind those of the groups before: with at most seven lost a group, no two
-// groups meet.
+// Where expert e's slots start, its rows standing from place `first` of the lists on: a multiple of eight, and with at most seven
+// lost an expert no two experts' meet.
+__device__ __forceinline__ int mma_slot(int first, int e) { return (first + 7 * e + 7) & ~7; }
+
+// Group a.
 __device__ __forceinline__ Group mma_group(const MmaParams& p, int a) {
     if (p.kind == Q4_DENSE) return Group{0, 0, p.R, 0};
     Group g;
     const int total = p.R * p.K;
-    g.e = p.plan.active ? p.plan.active[1 + a] : p.ids[a];
+    g.e = p.plan.active[1 + a];
     if (g.e < 0 || g.e >= p.E) return Group{-1, 0, 0, 0};
-    g.first = p.plan.active ? min(max(p.plan.offsets[g.e], 0), total) : a;
-    g.count = p.plan.active ? max(min(p.plan.offsets[g.e + 1], total) - g.first, 0) : 1;
-    g.slot = (g.first + 7 * a + 7) & ~7;
+    g.first = min(max(p.plan.offsets[g.e], 0), total);
+    g.count = max(min(p.plan.offsets[g.e + 1], total) - g.first, 0);
+    g.slot = mma_slot(g.first, g.e);
     return g;
 }
 
 // The choice at place i of the lists (-1: none).
 __device__ __forceinline__ int mma_choice(const MmaParams& p, int i) {
-    if (p.kind == Q4_DENSE || !p.plan.active) return i;
+    if (p.kind == Q4_DENSE) return i;
     const int c = p.plan.lists[i];
     return c >= 0 && c < p.R * p.K ? c : -1;
 }
@@ -97,25 +99,18 @@ __global__ void __launch_bounds__(256) q4_slots_kernel(const MmaParams p) {
     griddep_wait();    // the launch before has ended, which the products' launch takes for granted from its start on
     griddep_launch();
     const int octets = 16 * p.chunks, cols = p.w0.cols, lane = threadIdx.x & 31;
-    const int n = p.kind == Q4_DENSE ? p.R : p.R * p.K, groups = mma_groups(p);
+    const int n = p.kind == Q4_DENSE ? p.R : p.R * p.K;
     int buf = 0;
     for (int i = blockIdx.x; i < n; i += gridDim.x, buf ^= 1) {
         int c = i, slot = i;
         if (p.kind != Q4_DENSE) {
-            if (threadIdx.x == 0) {  // the group whose places hold i: groups stand in the order of their places
+            if (threadIdx.x == 0) {
                 c = mma_choice(p, i);
-                int lo = 0, hi = groups - 1;
-                if (!p.plan.active) lo = hi = i;
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) >> 1;
-                    const Group g = mma_group(p, mid);
-                    if (g.e >= 0 && g.first > i) hi = mid - 1;
-                    else lo = mid;
-                }
                 slot = -1;
-                if (groups > 0 && c >= 0) {
-                    const Group g = mma_group(p, lo);
-                    if (g.e >= 0 && i >= g.first && i < g.first + g.count) slot = g.slot + i - g.first;
+                const int e = c >= 0 ? p.ids[c] : -1;
+                if (e >= 0 && e < p.E) {
+                    const int first = p.plan.offsets[e];
+                    if (first >= 0 && i >= first && i < p.plan.offsets[e + 1]) slot = mma_slot(first, e) + i - first;
                 }
                 if (slot >= p.slots) slot = -1;
                 where[0] = c, where[1] = slot;
@@ -590,11 +585,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1) q4_mma_kernel(const __grid_con
             if (it.c0 >= it.c1) continue;
             for (; it.ct < it.cts; ++it.ct) {
                 const int n = columns(it), place = it.g.first + it.ct * TN;
-                // thread j: column j's choice and unit, for the end
-                int choice = -1;
+                // thread j: column j's choice and unit, looked at only at the end (a wait for them here held up the first chunk)
+                int choice = place + r;
                 float column_unit = 1.f;
                 if (col0 == 0 && r < n) {
-                    choice = mma_choice(p, place + r);
+                    if (p.kind != Q4_DENSE) choice = p.plan.lists[place + r];
                     if (FORM == FORM_F32) column_unit = p.scales[it.g.slot + it.ct * TN + r];
                 }
                 float2 acc[HN / 2] = {};
@@ -674,7 +669,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1) q4_mma_kernel(const __grid_con
                 }
                 // The sums go through shared memory, so that short loops write them (unrolled over the columns this end took as
                 // long as ten chunks).
-                if (col0 == 0 && r < TN) sh.choice[r] = choice, sh.unit[r] = column_unit;
+                if (col0 == 0 && r < TN) {
+                    sh.choice[r] = r < n && choice >= 0 && choice < p.R * p.K ? choice : -1;
+                    sh.unit[r] = column_unit;
+                }
 #pragma unroll
                 for (int j = 0; j < HN; ++j) sh.sums[col0 + j][r] = j & 1 ? acc[j >> 1].y : acc[j >> 1].x;
                 sync();
@@ -682,6 +680,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) q4_mma_kernel(const __grid_con
                     const int id = threadIdx.x - 256;
                     if (gate_up) {  // 64 threads a column
                         const int row = it.row_tile * 64 + (id & 63);
+#pragma unroll 4
                         for (int j = id >> 6; j < n; j += 4) {
                             const int to = sh.choice[j];
                             const float u = sh.unit[j];
@@ -690,6 +689,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) q4_mma_kernel(const __grid_con
                         }
                     } else {
                         const int row = it.row_tile * 128 + r;
+#pragma unroll 4
                         for (int j = id >> 7; j < n; j += 2) {
                             const int to = sh.choice[j];
                             const float v = sh.sums[j][r] * sh.unit[j];

@@ -16,16 +16,18 @@ struct CombineParams {
 // y[r] = residual[r] + sum_j gates[r][j] out[r][j], in the order of the choices.
 __global__ void __launch_bounds__(256) q4_combine_kernel(const CombineParams p) {
     griddep_wait();
-    const int64_t n = (int64_t)p.R * p.d, step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) {
-        const int64_t r = i / p.d, o = i - r * p.d;
+    const int64_t o = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (o >= p.d) return;
+    for (int64_t r = blockIdx.y; r < p.R; r += gridDim.y) {
         float sum = 0.f;
-        for (int j = 0; j < p.K; ++j) {
+#pragma unroll 8
+        for (int j = 0; j < p.K; ++j) {  // (independent loads: eight of them on their way together)
             const int64_t c = r * p.K + j;
             const int e = p.ids[c];
-            if (e >= 0 && e < p.E) sum = fmaf(p.gates[c], p.out[c * p.d + o], sum);
+            const float g = p.gates[c], v = p.out[c * p.d + o];
+            if (e >= 0 && e < p.E) sum = fmaf(g, v, sum);
         }
-        p.y[i] = p.residual ? p.residual[i] + sum : sum;
+        p.y[r * p.d + o] = p.residual ? p.residual[r * p.d + o] + sum : sum;
     }
 }
 
@@ -109,8 +111,8 @@ cudaError_t launch_q4(const Q4Call& c, Carve& ws, cudaStream_t st) {
                                                  : launch_q4_tensor(c, groups, form, out, ws, st);
     if (e != cudaSuccess || ws.overflow || c.kind != Q4_DOWN) return e;
     const CombineParams p = {c.E, c.out_rows, (int)c.R, c.K, c.ids, c.gates, c.residual, out, c.y};
-    const int64_t n = c.R * c.out_rows;
-    return launch(q4_combine_kernel, dim3((unsigned)min((n + 255) / 256, (int64_t)device_info().sms * 16)), dim3(256), 0, st, 1, p);
+    const dim3 grid((unsigned)((c.out_rows + 127) / 128), (unsigned)min(c.R, (int64_t)65535));
+    return launch(q4_combine_kernel, grid, dim3(128), 0, st, 1, p);
 }
 
 }  // namespace q8
