@@ -32,8 +32,9 @@
  *     kernels refuse, as kernel_refusal does in forward_shim.rs) and launches nothing; q8_last_error() names the
  *     argument.  A CUDA launch error returns Q8_ECUDA.  Errors raised later on the device surface at the caller's next
  *     synchronization as CUDA errors.  A bounded device-side wait that gives up (Q8_ETIMEOUT) is reported for the
- *     decode model by q8_model_check and for q8_paged_attention by q8_workspace_check; any other standalone call whose
- *     wait gave up leaves its outputs incomplete and reports nothing.
+ *     decode model by q8_model_check and for q8_paged_attention and the products with 4-bit weights by
+ *     q8_workspace_check; any other standalone call whose wait gave up leaves its outputs incomplete and reports
+ *     nothing.
  *   - Calls that take a workspace use its scratch and its arrival counters.  Calls sharing one workspace must be
  *     ordered (one stream, or events); two calls that overlap on the device through one workspace race.
  */
@@ -98,7 +99,8 @@ typedef struct q8_ws q8_ws;
 Q8_API int q8_workspace_create(size_t bytes, q8_ws **ws);
 Q8_API void q8_workspace_destroy(q8_ws *ws);
 Q8_API size_t q8_workspace_bytes(const q8_ws *ws);
-/* Waits for `stream` and returns Q8_ETIMEOUT when a bounded wait of a q8_paged_attention on this workspace gave up: that
+/* Waits for `stream` and returns Q8_ETIMEOUT when a bounded wait of a q8_paged_attention, or of a product with 4-bit weights
+ * (q4_gemv, moe_gate_up_q4, moe_down_combine_q4), on this workspace gave up: that
  * call's outputs are incomplete, and later ones on the workspace wrote nothing, because its counters may not have been
  * zero.  The counters are zeroed and the failure cleared, so that the workspace can be used again; no other call on it may
  * be in flight. */
@@ -488,7 +490,7 @@ typedef struct {
  * chosen only when no other is left in the kept groups (the lowest index first), has a gate of 0, and adds nothing to a
  * group's mark; a group of none but such ranks last.  +infinity counts as f32's largest value.  A row without an expert in
  * service has gates of 0.  experts at most 1024, k at most 32 and at most the experts of keep_groups groups.  plan (or
- * NULL) is filled as by moe_route_topk (rows * k at most 2^24); ws is needed with it. */
+ * NULL) is filled as by moe_route_topk (rows * k at most 2^24); ws is needed with it.  No output overlaps an input or another. */
 Q8_API int moe_route_scored(const float *logits, int64_t stride, int64_t rows, int64_t experts, const q8_route_rule *rule,
                             int k, int32_t *ids, float *gates, const q8_moe_plan *plan, q8_ws *ws, q8_stream stream);
 
@@ -508,9 +510,11 @@ typedef struct {
 
 /* y[r][o] = sum_t W[o][t] x[r][t] for `rows` activation rows, x either f32 (rows x_stride values apart, 16-byte aligned, the
  * stride a multiple of 4) or, with x NULL, the quantized form xq (dense; the two-word form when xq->lo is not NULL).  y is
- * device f32, rows y_stride values apart, and overlaps no input.  Sums are f32: of f32 activations in two f16 parts, which
- * carry 2^-22 of each 32-value block's largest value, and of exact integer block sums for quantized ones.  Calls of one row
- * need no workspace. */
+ * device f32, rows y_stride values apart, and overlaps no input (columns beside x's of one buffer do not).  Every 32-value block's dot of a quantized activation is the
+ * exact integer, scaled and summed in f32; f32 activations enter as two f16 parts, which hold a value to 2^-22 of it or 2^-28
+ * of the largest magnitude of its block (one row) or of its row (several), whichever is more, and are summed in f32.  With
+ * several rows scales of magnitudes up to 2^80 leave the sums in range.  Calls of one row need no workspace; several take four
+ * bytes of it an activation value and some MiB, a projection as many rows at a time as it holds. */
 Q8_API int q4_gemv(const q4_mat *W, const float *x, int64_t x_stride, const q8_act *xq, int64_t rows, float *y,
                    int64_t y_stride, q8_ws *ws, q8_stream stream);
 

@@ -83,6 +83,14 @@ int check_q4_act(const float* x, int64_t stride, const q8_act* xq, int64_t rows,
     return Q8_OK;
 }
 
+// Whether two sets of `rows` rows, equally far apart, are columns beside one another.
+bool beside(const float* a, int64_t a_cols, const float* b, int64_t b_cols, int64_t stride, int64_t rows) {
+    if (rows < 2 || stride < 1 || ((uintptr_t)a - (uintptr_t)b) % 4) return false;
+    int64_t at = (int64_t)((intptr_t)b - (intptr_t)a) / 4 % stride;  // where b's columns start in a's rows
+    if (at < 0) at += stride;
+    return at >= a_cols && at + b_cols <= stride;
+}
+
 // Whether `out` meets the activation (its `rows` rows of cols values) or the matrix.
 bool meets_act(const Range& out, const Q4Act& a, int64_t rows, int64_t cols) {
     if (a.x) return out.meets(Range(a.x, 4 * ((rows - 1) * a.stride + cols)));
@@ -218,9 +226,20 @@ int moe_route_scored(const float* logits, int64_t stride, int64_t rows, int64_t 
         return model_fail(Q8_EINVAL, "logits, bias, ids or gates: not 4-byte aligned");
     if (rows > 1 && stride < experts)
         return model_fail(Q8_EINVAL, "logits: rows %lld apart, of %lld values", (long long)stride, (long long)experts);
+    const Range in(logits, 4 * ((rows - 1) * stride + experts)), biases(rule->bias, 4 * experts);
+    const Range out[] = {{ids, 4 * rows * k}, {gates, 4 * rows * k}};
+    if (out[0].meets(out[1]) || out[0].meets(in) || out[1].meets(in) || out[0].meets(biases) || out[1].meets(biases))
+        return model_fail(Q8_EINVAL, "ids or gates: overlaps the logits, the bias or the other");
     if (plan) {
         if (int r = check_plan4(plan)) return r;
         if (!ws) return model_fail(Q8_EINVAL, "ws: null (the choices are grouped)");
+        const Range made[] = {{plan->counts, 4 * experts}, {plan->offsets, 4 * (experts + 1)}, {plan->lists, 4 * rows * k},
+                              {plan->active, 4 * (experts + 1)}};
+        for (int i = 0; i < 4; ++i) {
+            bool bad = made[i].meets(in) || made[i].meets(biases) || made[i].meets(out[0]) || made[i].meets(out[1]);
+            for (int j = 0; j < i; ++j) bad = bad || made[i].meets(made[j]);
+            if (bad) return model_fail(Q8_EINVAL, "plan: overlaps the logits, the bias, ids, gates or itself");
+        }
     }
     RouteScoredCall c;
     c.logits = logits;
@@ -252,7 +271,10 @@ int q4_gemv(const q4_mat* W, const float* x, int64_t x_stride, const q8_act* xq,
         return model_fail(Q8_EINVAL, "y: rows %lld apart, of %lld values", (long long)y_stride, (long long)W->rows);
     if (rows > 1 && !ws) return model_fail(Q8_EINVAL, "ws: null (several rows)");
     const Range out(y, 4 * ((rows - 1) * y_stride + W->rows));
-    if (meets_act(out, c.act, rows, W->cols) || meets_mat(out, W)) return model_fail(Q8_EINVAL, "y: overlaps an input");
+    if (meets_mat(out, W) ||
+        (meets_act(out, c.act, rows, W->cols) &&
+         !(x && x_stride == y_stride && beside(x, W->cols, y, W->rows, y_stride, rows))))
+        return model_fail(Q8_EINVAL, "y: overlaps an input");
     c.kind = Q4_DENSE;
     c.w0 = view_of(W);
     c.out_rows = W->rows;

@@ -1,4 +1,4 @@
-// Device helpers of the products with 4-bit weights (q4_row.cu, q4_rows.cu).
+// Device helpers of the products with 4-bit weights (q4_row.cu, q4_rows.cuh, q4_mma.cuh).
 //
 // The arithmetic.  A 4-bit word less its zero point is a small integer, exact in f16, and so is an int8 activation word; an f32
 // activation is, in units of a power of two that its 32-value block shares, the sum of two f16 parts (22 significant bits
@@ -52,6 +52,19 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Pairs of f32, two operations an instruction.
+__device__ __forceinline__ float2 pair_mul(float2 a, float2 b) {
+    float2 d;
+    asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z;}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ void pair_fma(float2& acc, float2 a, float bx, float by) {
+    asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%0, %1}; fma.rn.f32x2 z, x, y, z; "
+        "mov.b64 {%0, %1}, z;}"
+        : "+f"(acc.x), "+f"(acc.y) : "f"(a.x), "f"(a.y), "f"(bx), "f"(by));
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {

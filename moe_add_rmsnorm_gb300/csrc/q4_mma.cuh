@@ -209,18 +209,6 @@ __device__ __forceinline__ void tile_g2s(void* dst, const CUtensorMap* map, int 
                  : "memory");
 }
 
-// Pairs of f32, two operations an instruction.
-__device__ __forceinline__ float2 pair_mul(float2 a, float2 b) {
-    float2 d;
-    asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z;}"
-        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ void pair_fma(float2& acc, float2 a, float bx, float by) {
-    asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%0, %1}; fma.rn.f32x2 z, x, y, z; mov.b64 {%0, %1}, z;}"
-        : "+f"(acc.x), "+f"(acc.y) : "f"(a.x), "f"(a.y), "f"(bx), "f"(by));
-}
-
 // The rest of a wait whose first poll found its phase open, by one lane or a whole warp: false when it gave up, or when another of
 // the CTA's did.
 static __device__ __noinline__ bool mma_wait_on(uint64_t* bar, unsigned parity, int* dead, int* failed) {

@@ -102,18 +102,6 @@ __device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Pairs of f32, two operations an instruction.
-__device__ __forceinline__ float2 pair_mul(float2 a, float2 b) {
-    float2 d;
-    asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z;}"
-        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ void pair_fma(float2& acc, float2 a, float bx, float by) {
-    asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%0, %1}; fma.rn.f32x2 z, x, y, z; mov.b64 {%0, %1}, z;}"
-        : "+f"(acc.x), "+f"(acc.y) : "f"(a.x), "f"(a.y), "f"(bx), "f"(by));
-}
-
 // A warp's chunk: the four blocks of its 32 rows (matrix tiles from `mat` on) by the first TN tiles of columns (at `bs`).  Without a
 // branch for every tile of columns, so that the products of one hide the scaling of another.  so, zo: lane t's
 // scales and zero points are block t's; `same` + 1 blocks share one.

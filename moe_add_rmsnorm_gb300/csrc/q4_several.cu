@@ -94,11 +94,9 @@ cudaError_t launch_q4_tensor(const Q4Call& c, int64_t groups, int form, float* o
                               : launch_mma_two(p, groups, ws, st);
 }
 
-}  // namespace
-
-cudaError_t launch_q4(const Q4Call& c, Carve& ws, cudaStream_t st) {
+// A call whose rows fit the workspace.
+cudaError_t launch_q4_rows(const Q4Call& c, int form, Carve& ws, cudaStream_t st) {
     if (c.R == 1 && q4_row_fits(c)) return launch_q4_row(c, st);
-    const int form = c.act.x ? FORM_F32 : c.act.lo ? FORM_TWO : FORM_ONE;
     const int64_t groups = c.kind == Q4_DENSE ? 1 : c.R == 1 ? c.K : min(c.E, c.R * c.K);
     float* out = c.kind == Q4_DOWN ? ws.take<float>((size_t)c.R * c.K * c.out_rows) : nullptr;
     if (ws.overflow) return cudaSuccess;
@@ -113,6 +111,35 @@ cudaError_t launch_q4(const Q4Call& c, Carve& ws, cudaStream_t st) {
     const CombineParams p = {c.E, c.out_rows, (int)c.R, c.K, c.ids, c.gates, c.residual, out, c.y};
     const dim3 grid((unsigned)((c.out_rows + 127) / 128), (unsigned)min(c.R, (int64_t)65535));
     return launch(q4_combine_kernel, grid, dim3(128), 0, st, 1, p);
+}
+
+}  // namespace
+
+cudaError_t launch_q4(const Q4Call& call, Carve& ws, cudaStream_t st) {
+    const int form = call.act.x ? FORM_F32 : call.act.lo ? FORM_TWO : FORM_ONE;
+    if (call.kind != Q4_DENSE || call.R == 1) return launch_q4_rows(call, form, ws, st);
+    // A projection of more rows than the workspace holds operands of takes them so many at a time.
+    const size_t row = (size_t)((call.w0.cols + 127) / 128) * (form == FORM_ONE ? 256 + 16 : 512 + 16) + 8;
+    const size_t joins = size_t(6) << 20;  // the sums of weights that are cut (a tile of 64 rows by 128 an SM), and edges
+    const size_t room = ws.size > ws.used + joins ? (ws.size - ws.used - joins) / row : 0;
+    if (room < 64 || (size_t)call.R <= room) return launch_q4_rows(call, form, ws, st);
+    Q4Call c = call;
+    for (int64_t left = call.R; left > 0; left -= c.R) {
+        c.R = min(left, (int64_t)(room & ~size_t(63)));
+        Carve own = ws;  // (the blocks' launches follow one another)
+        const cudaError_t e = launch_q4_rows(c, form, own, st);
+        ws.overflow = own.overflow;
+        if (e != cudaSuccess || ws.overflow) return e;
+        c.y += c.R * c.y_stride;
+        if (form == FORM_F32) {
+            c.act.x += c.R * c.act.stride;
+        } else {
+            c.act.q += c.R * c.w0.cols;
+            if (form == FORM_TWO) c.act.lo += c.R * c.w0.cols;
+            c.act.s += c.R * (c.w0.cols / 32);
+        }
+    }
+    return cudaSuccess;
 }
 
 }  // namespace q8

@@ -39,6 +39,9 @@ def test_norm(q8, change, code, word):
     assert word in q8.last_error()
 
 
+PLAN = (9 * A, 10 * A, 11 * A, 12 * A)
+
+
 def route(q8, logits=A, stride=64, rows=3, experts=64, rule=True, k=4, ids=2 * A, gates=3 * A, plan=None, ws=A, **other):
     f = dict(score=0, bias=None, groups=4, keep_groups=2, group_top=2, renorm=1, scale=1.0)
     r = ctypes.byref(q8.q8_route_rule(**{**f, **other})) if rule else None
@@ -55,7 +58,10 @@ def route(q8, logits=A, stride=64, rows=3, experts=64, rule=True, k=4, ids=2 * A
     (dict(keep_groups=1, k=17), -1, "k 17 above the 16"), (dict(rows=1 << 23), -2, "2^24"), (dict(logits=None), -1, "null"),
     (dict(ids=None), -1, "null"), (dict(gates=3 * A + 2), -1, "4-byte"), (dict(bias=A + 1), -1, "4-byte"),
     (dict(stride=63), -1, "63 apart"), (dict(plan=(A, A, A, None)), -1, "plan: null"),
-    (dict(plan=(A, A, A, A + 2)), -1, "plan: not 4-byte"), (dict(plan=(A, A, A, A), ws=None), -1, "ws: null")])
+    (dict(plan=(A, A, A, A + 2)), -1, "plan: not 4-byte"), (dict(plan=PLAN, ws=None), -1, "ws: null"),
+    (dict(ids=A + 128), -1, "ids or gates: overlaps"), (dict(gates=2 * A + 16), -1, "ids or gates: overlaps"),
+    (dict(bias=3 * A + 8), -1, "ids or gates: overlaps"), (dict(plan=(A, *PLAN[1:])), -1, "plan: overlaps"),
+    (dict(plan=(*PLAN[:3], 9 * A + 4)), -1, "plan: overlaps"), (dict(plan=(*PLAN[:2], 2 * A, PLAN[3])), -1, "plan: overlaps")])
 def test_route(q8, change, code, word):
     assert route(q8, **change) == code
     assert word in q8.last_error()

@@ -408,6 +408,69 @@ def test_projection_of_values_that_are_not_finite_and_of_extremes(q8, ws, rows):
     assert not y.any()
 
 
+def test_projection_into_columns_beside_its_rows(q8, ws):
+    import torch
+    g = gen(11)
+    m = matrix(torch, 100, 128, 32, "f16", False, g)
+    for rows in (3, 40):
+        wide = torch.randn(rows, 300, generator=g, device="cuda")
+        kept = wide.clone()
+        q8.q4_gemv(q8.q4_mat(*m), wide[:, 160:260], x=wide[:, 16:144], ws=ws)
+        x, W = kept[:, 16:144].double(), values(torch, m)
+        assert ((wide[:, 160:260].double() - x @ W.T).abs() <= product_error(torch, W, x, "f32")).all()
+        assert torch.equal(wide[:, :160], kept[:, :160]) and torch.equal(wide[:, 260:], kept[:, 260:])
+        with pytest.raises(q8.Q8Error):
+            q8.q4_gemv(q8.q4_mat(*m), wide[:, 140:240], x=wide[:, 16:144], ws=ws)
+
+
+@pytest.mark.parametrize("form", ["f32", "one", "two"])
+def test_projection_of_more_rows_than_the_workspace_holds(q8, form):
+    """Rows taken so many at a time, and a workspace that holds none."""
+    import torch
+    rows, n, cols = 2113, 200, 512
+    g = gen(7)
+    m = matrix(torch, n, cols, 64, "f16", True, g)
+    call, x = activation(torch, rows, cols, form, g)
+    y = torch.full((rows, n), math.nan, device="cuda")
+    small = q8.Workspace(8 << 20)
+    q8.q4_gemv(q8.q4_mat(*m), y, **call, ws=small)
+    W = values(torch, m)
+    assert ((y.double() - x @ W.T).abs() <= product_error(torch, W, x, form)).all()
+    small.check()
+    small.close()
+    tiny = q8.Workspace(4096)
+    with pytest.raises(q8.Q8Error) as e:
+        q8.q4_gemv(q8.q4_mat(*m), y, **call, ws=tiny)
+    assert e.value.code == -5
+    tiny.close()
+
+
+def test_projection_on_a_workspace_of_which_a_wait_gave_up(q8):
+    """Nothing is written until the workspace has been checked."""
+    import torch
+    ws = q8.Workspace()
+    words = [torch.zeros(4, 2, 16, 64, dtype=torch.int8, device="cuda") for _ in range(2)]
+    scales = [torch.zeros(4, 2, 16, device="cuda") for _ in range(2)]
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    pages = q8.kv_pages(words[0], scales[0], words[1], scales[1])
+    q = torch.zeros(1, 4, 64, device="cuda")
+    q8.q8_paged_wait_selftest(pages, q8.kv_batch(i32(0, 1), i32(40), i32(0, 1, 2).view(1, 3)), q, torch.zeros_like(q), 16, ws)
+    g = gen(3)
+    m = matrix(torch, 300, 1024, 64, "f16", True, g)
+    x = torch.randn(64, 1024, generator=g, device="cuda")
+    y = torch.full((64, 300), 7.0, device="cuda")
+    q8.q4_gemv(q8.q4_mat(*m), y, x=x, ws=ws)
+    assert (y == 7).all()
+    with pytest.raises(q8.Q8Error) as e:
+        ws.check()
+    assert e.value.code == -4
+    q8.q4_gemv(q8.q4_mat(*m), y, x=x, ws=ws)
+    W = values(torch, m)
+    assert ((y.double() - x.double() @ W.T).abs() <= product_error(torch, W, x.double(), "f32")).all()
+    ws.check()
+    ws.close()
+
+
 # ---- the experts' products -------------------------------------------------------------------------------------------
 
 
@@ -509,6 +572,27 @@ def test_experts_of_a_row_longer_than_a_cta_holds(q8, ws, E, k, d, dff):
     y = torch.empty(1, d, device="cuda")
     q8.moe_down_combine_q4(q8.q4_mat(*down), ids, gates, y, h=h, ws=ws)
     check_combined(torch, y, values(torch, down), h.double(), ids, gates, None, d, "f32")
+
+
+def test_experts_of_more_tiles_than_a_cta_looks_up(q8, ws):
+    """Thousands of (expert, tile) items, the experts' rows from none to many."""
+    import torch
+    E, k, d, dff, rows = 300, 2, 128, 1280, 1500
+    g = gen(5)
+    gate, up, down = (matrix(torch, n, c, 32, "f16", False, g) for n, c in ((E * dff, d), (E * dff, d), (E * d, dff)))
+    score = torch.rand(rows, E, generator=g, device="cuda") + 0.4 * (torch.arange(E, device="cuda") % 3 == 0)
+    score[:, 7] = 2  # every row's
+    ids = score.topk(k, -1).indices.to(torch.int32)
+    gates = torch.rand(rows, k, generator=g, device="cuda")
+    plan, kept = plan_of(q8, torch, ids, E)
+    x = torch.randn(rows, d, generator=g, device="cuda") / 8
+    h = torch.full((rows, k, dff), math.nan, device="cuda")
+    q8.moe_gate_up_q4(q8.q4_mat(*gate), q8.q4_mat(*up), ids, h, x=x, plan=plan, ws=ws)
+    check_hidden(torch, h, values(torch, gate), values(torch, up), x.double(), ids, dff, "f32")
+    y = torch.full((rows, d), math.nan, device="cuda")
+    q8.moe_down_combine_q4(q8.q4_mat(*down), ids, gates, y, h=h, plan=plan, ws=ws)
+    check_combined(torch, y, values(torch, down), h.double(), ids, gates, None, d, "f32")
+    del kept
 
 
 def test_experts_out_of_range_and_the_same_expert_twice(q8, ws):
