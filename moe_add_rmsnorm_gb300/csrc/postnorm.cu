@@ -187,10 +187,11 @@ cudaError_t launch_postnorm(const PostnormCall& c, cudaStream_t st) {
         vec = vec && aligned16(q);
     const dim3 grid((unsigned)c.rows);
     if (!vec) return launch(postnorm_kernel<512, 8, false>, grid, dim3(512), 0, st, 1, p);
-    // A row's time is its chain of reductions: with few rows as many threads as it has vectors; with many, the CTAs of an SM
-    // hide one another's chains and 256 threads of several vectors spend less on the reductions.
+    // A row's time is its chain of reductions: up to a row an SM as many threads as it has vectors; with more, the CTAs of an SM
+    // hide one another's chains and 256 threads of several vectors spend less on the reductions.  Measured, us, rows of 2048: 152
+    // rows 3.5 and 3.9, 304 rows 5.0 and 4.7, 4096 rows 51 and 38; of 4096: 64 rows 5.2 and 6.0, 304 rows 8.7 and 7.3.
     const int n4 = (int)((c.d + 3) / 4);
-    const bool many = c.rows > 2 * device_info().sms;
+    const bool many = c.rows > device_info().sms;
 #define Q8_POSTNORM(T, PER) \
     if (n4 <= (T) * (PER)) return launch(postnorm_kernel<T, PER, true>, grid, dim3(T), 0, st, 1, p);
     if (many) {

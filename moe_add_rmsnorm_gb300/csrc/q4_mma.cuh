@@ -703,7 +703,7 @@ cudaError_t run_mma(MmaParams p, int64_t groups, Carve& ws, cudaStream_t st) {
     p.col_tiles = p.kind == Q4_DENSE ? (p.R + TN - 1) / TN : 1;
     const int64_t tiles = (int64_t)p.row_tiles * p.col_tiles;
     p.slices = 1;
-    if (p.kind == Q4_DENSE && tiles * 2 <= sms) {  // too few tiles for the SMs: four chunks a slice or more
+    if (p.kind == Q4_DENSE && tiles * 2 <= sms) {  // too few tiles for the SMs: four chunks a slice or more (2048 x 4096, 32 rows 22 -> 14 us)
         p.slices = (int)min(min((int64_t)sms / tiles, (int64_t)8), (int64_t)max(p.chunks / 4, 1));
         if (p.slices > 1) {
             p.sums = ws.take<float>((size_t)tiles * p.slices * TN * 128);
@@ -729,11 +729,18 @@ cudaError_t run_mma(MmaParams p, int64_t groups, Carve& ws, cudaStream_t st) {
 
 template <int FORM>
 cudaError_t launch_mma(const MmaParams& p, int64_t groups, Carve& ws, cudaStream_t st) {
-    // Rows a tile: the projection's, or an expert's average and one and a half deviations of a random choice.
+    // Rows a tile: the projection's, or an expert's average and one and a half deviations of a random choice.  Measured, us, 16, 32
+    // and 64 a tile, 6 of 64 experts of 2048 x 1408: 100 rows (9.4 an expert) 184, 199 and 276; 160 (15) 286, 211 and 282; 400 (37.5)
+    // 497, 387 and 319.
     const double mean = (double)p.R * p.K / groups;
     const double rows = p.kind == Q4_DENSE ? p.R : mean + 1.5 * sqrt(mean);
-    if (rows <= 16) return run_mma<FORM, 16>(p, groups, ws, st);
-    if (rows <= 32) return run_mma<FORM, 32>(p, groups, ws, st);
+    int tile = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    // A projection that leaves half of the SMs idle at half of that takes half: 2048 x 4096, 64 rows 17.5 and 14.7 us (64 and 32 a
+    // tile), 32 rows 13.9 and 13.0 (32 and 16); with more tiles the weights' second unpacking costs more, 8192 x 4096, 64 rows 22.5
+    // and 24.4.
+    if (p.kind == Q4_DENSE && tile > 16 && p.row_tiles * ((p.R + tile / 2 - 1) / (int64_t)(tile / 2)) * 2 <= device_info().sms) tile /= 2;
+    if (tile == 16) return run_mma<FORM, 16>(p, groups, ws, st);
+    if (tile == 32) return run_mma<FORM, 32>(p, groups, ws, st);
     return run_mma<FORM, 64>(p, groups, ws, st);
 }
 

@@ -3,7 +3,7 @@
 //
 // A first launch lays the activation rows out as f16 parts (q4.cuh) in the order of the products' operands; a second one
 // multiplies.  There a warp takes two tiles of 16 weight rows (gate-up: 16 gate rows and the 16 up rows beside them) by up
-// to NT tiles of eight columns, a column being one part of one activation row.  Weights and activation parts come through
+// to two tiles of eight columns, a column being one part of one activation row.  Weights and activation parts come through
 // rings of asynchronous 16-byte copies: the weights' is the warp's own, from where one matrix load gives each lane the words
 // it multiplies; the activation's is the CTA's, whose warps read the same columns.  A block's dots are scaled, two sums an
 // instruction, by the weights' scale (and a quantized activation's; an f32 row has one unit, taken out at the end).
@@ -15,6 +15,8 @@ namespace q8 {
 
 constexpr int kWarps = 8;    // a CTA
 constexpr int kStages = 4;   // of the rings: a stage is a chunk of four blocks for each of the warps that share a tile
+constexpr int kRowCtas = 2;  // an SM's CTAs (three leave a lane 80 registers, which spill: a batch's experts 98 -> 164 us)
+constexpr int NT = 2;        // tiles of eight columns a pass (four: 60 rows by 6 of 64 experts, 2048 x 1408, 148 -> 201 us)
 constexpr int kTileBytes = 2 * 16 * 64;
 
 struct RowsParams {
@@ -105,7 +107,7 @@ __device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t
 // A warp's chunk: the four blocks of its 32 rows (matrix tiles from `mat` on) by the first TN tiles of columns (at `bs`).  Without a
 // branch for every tile of columns, so that the products of one hide the scaling of another.  so, zo: lane t's
 // scales and zero points are block t's; `same` + 1 blocks share one.
-template <int FORM, int NT, int TN>
+template <int FORM, int TN>
 __device__ __forceinline__ void multiply_chunk(uint32_t mat, const char* bs, const float (&so)[2][2], const uint32_t (&zo)[2][2],
                                                bool has_z, int same, float2 (&acc)[2][NT][2]) {
     constexpr int BCHUNK = NT * 8 * 4 * 64;
@@ -167,8 +169,8 @@ __device__ __forceinline__ void multiply_chunk(uint32_t mat, const char* bs, con
     }
 }
 
-template <int FORM, int NT>
-__global__ void __launch_bounds__(32 * kWarps, 2) q4_rows_kernel(const RowsParams p) {
+template <int FORM>
+__global__ void __launch_bounds__(32 * kWarps, kRowCtas) q4_rows_kernel(const RowsParams p) {
     constexpr int PARTS = FORM == FORM_ONE ? 1 : 2;
     constexpr int COLS = 8 / PARTS;  // activation rows a tile of columns
     constexpr int NC = NT * COLS;
@@ -329,9 +331,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) q4_rows_kernel(const RowsParam
                 if (c < p.chunks) {
                     const uint32_t mat = matrix_at + at;
                     const char* bs = columns + bt + part_of * (BCHUNK + SCHUNK);
-                    if (NT >= 4 && tiles > 2) multiply_chunk<FORM, NT, NT >= 4 ? 4 : 1>(mat, bs, so, zo, has_z, same, acc);
-                    else if (tiles > 1) multiply_chunk<FORM, NT, 2>(mat, bs, so, zo, has_z, same, acc);
-                    else multiply_chunk<FORM, NT, 1>(mat, bs, so, zo, has_z, same, acc);
+                    if (tiles > 1) multiply_chunk<FORM, 2>(mat, bs, so, zo, has_z, same, acc);
+                    else multiply_chunk<FORM, 1>(mat, bs, so, zo, has_z, same, acc);
                 }
                 at = at == (kStages - 1) * kTileBytes ? 0 : at + kTileBytes;
                 bt = bt == (kStages - 1) * stage_b ? 0 : bt + stage_b;
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) q4_rows_kernel(const RowsParam
 
 constexpr size_t kRowsSmem = 220 << 10;
 
-template <int FORM, int NT>
+template <int FORM>
 cudaError_t run_rows(RowsParams p, int64_t groups, cudaStream_t st) {
     constexpr int NC = NT * 8 / (FORM == FORM_ONE ? 1 : 2);
     const int sms = device_info().sms;
@@ -403,17 +404,21 @@ cudaError_t run_rows(RowsParams p, int64_t groups, cudaStream_t st) {
         return (size_t)kStages * (kWarps * kTileBytes + wk * (NT * 2048 + (FORM == FORM_F32 ? 0 : NT * 128)));
     };
     const int64_t zs = p.kind == Q4_DENSE ? min((int64_t)(p.R + NC - 1) / NC, (int64_t)65535) : 1;
-    // Warps that share a tile: as many as it takes to give every SM its CTAs, while their columns fit.
-    p.wk = 1;
-    while (p.wk < kWarps && p.wk * 2 <= p.chunks && smem(p.wk * 2) <= kRowsSmem &&
-           p.row_tiles * groups * zs * p.wk < (int64_t)sms * kWarps)
-        p.wk *= 2;
+    // Warps that share a tile: those with the fewest steps in all, waves of CTAs times a CTA's steps and three for its ends.
+    // Measured, us, 1, 2, 4 and 8 warps: 8 rows by 8192 x 4096 33, 19, 12 and 15; by 2048 x 2048 17.5, 10.8, 7.3 and 5.6.
+    int64_t fewest = INT64_MAX;
+    for (int wk = 1; wk <= kWarps && wk <= p.chunks && smem(wk) <= kRowsSmem; wk *= 2) {
+        const int64_t ctas = (p.row_tiles + kWarps / wk - 1) / (kWarps / wk) * groups * zs;
+        const int64_t at_once = sms * min((int64_t)(kRowsSmem / smem(wk)), (int64_t)kRowCtas);
+        const int64_t steps = (ctas + at_once - 1) / at_once * ((p.chunks + wk - 1) / wk + 3);
+        if (steps < fewest) fewest = steps, p.wk = wk;
+    }
     const int side = kWarps / p.wk;
     const dim3 grid((unsigned)((p.row_tiles + side - 1) / side), (unsigned)min(groups, (int64_t)65535), (unsigned)zs);
     static std::atomic<uint64_t> done;
-    const cudaError_t e = allow_smem(q4_rows_kernel<FORM, NT>, kRowsSmem, done);
+    const cudaError_t e = allow_smem(q4_rows_kernel<FORM>, kRowsSmem, done);
     if (e != cudaSuccess) return e;
-    return launch(q4_rows_kernel<FORM, NT>, grid, dim3(32 * kWarps), smem(p.wk), st, 1, p);
+    return launch(q4_rows_kernel<FORM>, grid, dim3(32 * kWarps), smem(p.wk), st, 1, p);
 }
 
 // Both launches of a call of at most `groups` groups of rows.
@@ -422,10 +427,7 @@ cudaError_t launch_rows(const RowsParams& p, int64_t groups, cudaStream_t st) {
     const dim3 lay((unsigned)min(p.act_rows, (int64_t)device_info().sms * 8));
     const cudaError_t e = launch(q4_parts_kernel<FORM>, lay, dim3(256), 0, st, 1, p);
     if (e != cudaSuccess) return e;
-    // Tiles of columns a pass: those that twice an expert's average rows fill.
-    const int64_t rows = p.kind == Q4_DENSE ? p.R : 2 * ((int64_t)p.R * p.K / groups);
-    const int tile = FORM == FORM_ONE ? 8 : 4;
-    return rows <= 2 * tile ? run_rows<FORM, 2>(p, groups, st) : run_rows<FORM, 4>(p, groups, st);
+    return run_rows<FORM>(p, groups, st);
 }
 
 // One file each, so that they compile beside one another.

@@ -102,8 +102,9 @@ cudaError_t launch_q4_rows(const Q4Call& c, int form, Carve& ws, cudaStream_t st
     if (ws.overflow) return cudaSuccess;
     // Up to 16 columns (an activation's parts) a group on average, the warp-wide products are as fast or faster: they start
     // sooner and unpack with all their warps.  From there on the tensor cores' rows share what was unpacked.  Measured, warps and
-    // tensor cores, us: 8192 x 4096, group 128, f32: 4 rows 14 and 16, 16 rows 19 and 17, 64 rows 40 and 25; 6 of 64 experts of
-    // 2048 x 1408, group 32, f32: 24 rows (2.3 an expert) 124 and 155, 100 (9.4) 215 and 198, 256 (24) 310 and 239.
+    // tensor cores, us: 8192 x 4096, group 128, f32: 8 rows 12 and 16, 16 rows 19 and 16, 64 rows 40 and 23; 6 of 64 experts of
+    // 2048 x 1408, group 32, f32: 24 rows (2.3 an expert) 109 and 154, 60 (5.6) 151 and 176, 100 (9.4) 200 and 184, 256 (24) 412 and
+    // 254.
     const int64_t columns = c.R * c.K * (form == FORM_ONE ? 1 : 2);
     const cudaError_t e = columns <= 16 * groups ? launch_q4_warps(c, groups, form, out, ws, st)
                                                  : launch_q4_tensor(c, groups, form, out, ws, st);
