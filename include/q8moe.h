@@ -510,11 +510,12 @@ typedef struct {
 
 /* y[r][o] = sum_t W[o][t] x[r][t] for `rows` activation rows, x either f32 (rows x_stride values apart, 16-byte aligned, the
  * stride a multiple of 4) or, with x NULL, the quantized form xq (dense; the two-word form when xq->lo is not NULL).  y is
- * device f32, rows y_stride values apart, and overlaps no input (columns beside x's of one buffer do not).  Every 32-value block's dot of a quantized activation is the
- * exact integer, scaled and summed in f32; f32 activations enter as two f16 parts, which hold a value to 2^-22 of it or 2^-28
- * of the largest magnitude of its block (one row) or of its row (several), whichever is more, and are summed in f32.  With
- * several rows scales of magnitudes up to 2^80 leave the sums in range.  Calls of one row need no workspace; several take four
- * bytes of it an activation value and some MiB, a projection as many rows at a time as it holds. */
+ * device f32, rows y_stride values apart, and overlaps no input (columns beside x's of one buffer do not).  Every 32-value
+ * block's dot of a quantized activation is the exact integer, scaled and summed in f32; f32 activations enter as two f16
+ * parts, which hold a value to 2^-22 of it or 2^-28 of the largest magnitude of its block (one row) or of its row (several),
+ * whichever is more, and are summed in f32.  With several rows scales of magnitudes up to 2^80 leave the sums in range.  Calls
+ * of one row need no workspace; several take four bytes of it an activation value and some MiB, a projection as many rows at
+ * a time as it holds. */
 Q8_API int q4_gemv(const q4_mat *W, const float *x, int64_t x_stride, const q8_act *xq, int64_t rows, float *y,
                    int64_t y_stride, q8_ws *ws, q8_stream stream);
 

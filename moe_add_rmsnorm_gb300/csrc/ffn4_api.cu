@@ -108,6 +108,12 @@ int check_plan4(const q8_moe_plan* plan) {
     return Q8_OK;
 }
 
+// Whether `out` meets the arrays of a plan that several rows are multiplied by.
+bool meets_plan(const Range& out, const q8_moe_plan* plan, int64_t experts, int64_t rows, int k) {
+    return rows > 1 && (out.meets(Range(plan->offsets, 4 * (experts + 1))) || out.meets(Range(plan->active, 4 * (experts + 1))) ||
+                        out.meets(Range(plan->lists, 4 * rows * k)));
+}
+
 PlanPtrs plan_ptrs(const q8_moe_plan* plan) {
     PlanPtrs p;
     p.counts = plan->counts;
@@ -304,7 +310,7 @@ int moe_gate_up_q4(const q4_mat* gate, const q4_mat* up, int64_t dff, const floa
     if (!h || !aligned(h, 4)) return model_fail(Q8_EINVAL, "h: null or not 4-byte aligned");
     const Range out(h, 4 * rows * k * dff);
     if (meets_act(out, c.act, rows, gate->cols) || meets_mat(out, gate) || meets_mat(out, up) ||
-        out.meets(Range(ids, 4 * rows * k)))
+        out.meets(Range(ids, 4 * rows * k)) || meets_plan(out, plan, gate->rows / dff, rows, k))
         return model_fail(Q8_EINVAL, "h: overlaps an input");
     c.kind = Q4_GATE_UP;
     c.w0 = view_of(gate);
@@ -337,7 +343,8 @@ int moe_down_combine_q4(const q4_mat* down, int64_t d, const float* h, const q8_
     if (!y || !aligned(y, 4) || !aligned(residual, 4)) return model_fail(Q8_EINVAL, "y: null, or y or residual not 4-byte aligned");
     const Range out(y, 4 * rows * d);
     if (meets_act(out, c.act, rows * k, down->cols) || meets_mat(out, down) || out.meets(Range(ids, 4 * rows * k)) ||
-        out.meets(Range(gates, 4 * rows * k)) || (residual != y && out.meets(Range(residual, 4 * rows * d))))
+        out.meets(Range(gates, 4 * rows * k)) || (residual != y && out.meets(Range(residual, 4 * rows * d))) ||
+        meets_plan(out, plan, down->rows / d, rows, k))
         return model_fail(Q8_EINVAL, "y: overlaps an input");
     c.kind = Q4_DOWN;
     c.w0 = view_of(down);

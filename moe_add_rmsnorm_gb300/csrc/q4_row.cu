@@ -11,6 +11,10 @@
 //     with t != j read.  Lane (g, t) then receives the two parts' dots of its own block of its own rows.
 // Either way a block's dot meets its scales in the lane that loaded them: nothing is shuffled until a tile ends, and every
 // group size costs the same.
+// Measured, replayed: 151936 x 2048, group 128, one-word activations 29 us (163 MB, 5.6 TB/s, 82% of the measured copy rate;
+// f32 42); 5120 x 2048, f32, 5.5; eight experts of 2048 x 768 with their sum 17 (21 MB, two launches of one wave each, whose
+// start, first loads and end are most of it).  Why a ring of 16-byte copies: plain 16-byte loads into registers took 55 us for
+// the 29, a lane's loads in flight being bound by its registers.
 #include "ffn4.h"
 #include "q4.cuh"
 

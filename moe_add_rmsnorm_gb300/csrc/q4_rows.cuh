@@ -7,6 +7,10 @@
 // rings of asynchronous 16-byte copies: the weights' is the warp's own, from where one matrix load gives each lane the words
 // it multiplies; the activation's is the CTA's, whose warps read the same columns.  A block's dots are scaled, two sums an
 // instruction, by the weights' scale (and a quantized activation's; an f32 row has one unit, taken out at the end).
+// What bounds it is instructions: a warp's chunk of 32 rows by 128 values is some 470 of them, of which unpacking, needed once
+// however few the columns, is the larger part; 16 warps an SM issue in 56% of the cycles.  Measured, replayed: 24 rows by 8 of
+// 128 experts of 2048 x 768, one-word activations, 98 us (250 MB; 36.6 at the measured copy rate), 8 f32 rows by 8192 x 4096
+// 12.1.  The columns' ring is the CTA's since operands from L1 cost their latency every chunk (197 -> 131 us).
 #pragma once
 #include "ffn4.h"
 #include "q4.cuh"

@@ -5,7 +5,10 @@
 // those before it.  Scores are formed in f32 by the fast exponential and quotient, whose errors can exchange two experts that
 // 64 bits would order: where two of the gathered ones are closer than those errors reach, all of them are formed again in 64
 // bits and counted by those; where kept and left groups are, or a softmax with a bias (whose sum all scores share) or more
-// candidates than lanes, the whole row is chosen again in 64 bits.  What bounds it is instructions, about 600 a row of 256.
+// candidates than lanes, the whole row is chosen again in 64 bits.  What bounds it is instructions, about 1200 a row of 256
+// with eight groups, and where few rows share a warp's SM the rows with near ties, which take microseconds each.  Measured,
+// replayed: 15001 rows of 256 experts, 8 of 4 groups' chosen and grouped by expert, 41 us (17 MB, 2.5 at the measured copy rate);
+// 61 rows 8.3, one row of 128 without a plan 2.6.  Taking the largest K times over the lanes took 73 and 30.
 #include <math.h>
 
 #include "common.cuh"

@@ -149,6 +149,14 @@ def test_down(q8):
         assert word in q8.last_error()
 
 
+@pytest.mark.parametrize("array", [1, 2, 3])
+def test_outputs_over_the_plan(q8, array):
+    plan = [A, A, A, A]
+    plan[array] = 40 * A
+    assert gate_up(q8, plan=tuple(plan), h=40 * A + 4) == -1 and "h: overlaps" in q8.lib.q8_last_error().decode()
+    assert down(q8, plan=tuple(plan), y=40 * A + 4) == -1 and "y: overlaps" in q8.lib.q8_last_error().decode()
+
+
 def test_no_rows(q8):
     assert norm(q8, rows=0, a=None, b=None, sum=A) == 0
     assert route(q8, rows=0, logits=None, ids=None, gates=None, ws=None) == 0
