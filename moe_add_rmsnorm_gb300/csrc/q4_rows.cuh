@@ -7,9 +7,9 @@
 // rings of asynchronous 16-byte copies: the weights' is the warp's own, from where one matrix load gives each lane the words
 // it multiplies; the activation's is the CTA's, whose warps read the same columns.  A block's dots are scaled, two sums an
 // instruction, by the weights' scale (and a quantized activation's; an f32 row has one unit, taken out at the end).
-// What bounds it is instructions: a warp's chunk of 32 rows by 128 values is some 470 of them, of which unpacking, needed once
+// What bounds it is instructions: a warp's chunk of 32 rows by 128 values is some 440 of them, of which unpacking, needed once
 // however few the columns, is the larger part; 16 warps an SM issue in 56% of the cycles.  Measured, replayed: 24 rows by 8 of
-// 128 experts of 2048 x 768, one-word activations, 98 us (250 MB; 36.6 at the measured copy rate), 8 f32 rows by 8192 x 4096
+// 128 experts of 2048 x 768, one-word activations, 93 us (250 MB; 36.6 at the measured copy rate), 8 f32 rows by 8192 x 4096
 // 12.1.  The columns' ring is the CTA's since operands from L1 cost their latency every chunk (197 -> 131 us).
 #pragma once
 #include "ffn4.h"
@@ -109,10 +109,10 @@ __device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t
 }
 
 // A warp's chunk: the four blocks of its 32 rows (matrix tiles from `mat` on) by the first TN tiles of columns (at `bs`).  Without a
-// branch for every tile of columns, so that the products of one hide the scaling of another.  so, zo: lane t's
-// scales and zero points are block t's; `same` + 1 blocks share one.
+// branch for every tile of columns, so that the products of one hide the scaling of another.  so, zo: the scales and zero
+// points of the chunk's groups in row g + 8 (t & 1) of tile t >> 1; 2^same blocks share one.
 template <int FORM, int TN>
-__device__ __forceinline__ void multiply_chunk(uint32_t mat, const char* bs, const float (&so)[2][2], const uint32_t (&zo)[2][2],
+__device__ __forceinline__ void multiply_chunk(uint32_t mat, const char* bs, const float (&so)[4], const uint32_t (&zo)[4],
                                                bool has_z, int same, float2 (&acc)[2][NT][2]) {
     constexpr int BCHUNK = NT * 8 * 4 * 64;
     const int lane = threadIdx.x & 31, quad = lane & ~3;
@@ -123,7 +123,7 @@ __device__ __forceinline__ void multiply_chunk(uint32_t mat, const char* bs, con
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) zc[m][i] = zo[m][i], zf[m][i] = zero_less(zo[m][i]);
+        for (int i = 0; i < 2; ++i) zero_forms(8, zc[m][i], zf[m][i]);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         uint32_t words[2][4];  // [m][block 2 half: rows g, rows g + 8; block 2 half + 1: the same]
@@ -132,20 +132,19 @@ __device__ __forceinline__ void multiply_chunk(uint32_t mat, const char* bs, con
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int b = 2 * half + k;
-            if ((b & same) == 0) {
+            if ((b & ((1 << same) - 1)) == 0) {  // a group starts: its number in the chunk is b >> same
+                const float sg = b == 2 && same ? so[1] : so[b];
+                const uint32_t zg = b == 2 && same ? zo[1] : zo[b];
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) sw[m][i] = __shfl_sync(0xffffffffu, so[m][i], quad + b);
-                if (has_z) {
-#pragma unroll
-                    for (int m = 0; m < 2; ++m)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            zc[m][i] = __shfl_sync(0xffffffffu, zo[m][i], quad + b);
+                    for (int i = 0; i < 2; ++i) {
+                        sw[m][i] = __shfl_sync(0xffffffffu, sg, quad + 2 * m + i);
+                        if (has_z) {
+                            zc[m][i] = __shfl_sync(0xffffffffu, zg, quad + 2 * m + i);
                             zf[m][i] = zero_less(zc[m][i]);
                         }
-                }
+                    }
             }
             uint32_t h[2][2][4];
 #pragma unroll
@@ -200,10 +199,13 @@ __global__ void __launch_bounds__(32 * kWarps, kRowCtas) q4_rows_kernel(const Ro
     const uint32_t unit_at = (((unit_of / (4 * PARTS)) * NT * 8 + unit_row * PARTS + (unit_of >> 2) % PARTS) * 4 + (unit_of & 3)) * 16;
     const uint32_t scale_at = BCHUNK + ((threadIdx.x % 4) * NT * 8 + threadIdx.x / 4 * PARTS) * 4;
     const bool has_z = p.w0.z != nullptr;
-    const int same = (1 << (p.w0.group_log2 - 5)) - 1;
+    const int same = p.w0.group_log2 - 5, per_chunk = 4 >> same;
     const int total = p.R * p.K;
     const bool gate_up = p.kind == Q4_GATE_UP;
     const Q4View& second = gate_up ? p.w1 : p.w0;
+    // a chunk's scales (and zero points) in one load, where every row's stand at a multiple of their size
+    const bool wide = ngroups % per_chunk == 0 && (((uintptr_t)p.w0.s | (uintptr_t)second.s) % (2 * per_chunk)) == 0 &&
+                      (((uintptr_t)p.w0.z | (uintptr_t)second.z) % per_chunk) == 0;
     bool ready = false;
     int groups = 1;
     if (p.kind != Q4_DENSE) groups = p.plan.active ? min(max(p.plan.active[0], 0), (int)min(p.E, (int64_t)total)) : p.K;
@@ -221,32 +223,45 @@ __global__ void __launch_bounds__(32 * kWarps, kRowCtas) q4_rows_kernel(const Ro
         const int64_t base = (int64_t)e * p.out_rows;
         const int r0 = (gate_up ? 16 : 32) * tile, last = (int)p.out_rows - 1, top = min(r0, last);
         const uint8_t *qa = p.w0.q + (base + top) * row_bytes, *qb = second.q + (base + top) * row_bytes;
-        const uint16_t *sa = p.w0.s + (base + top) * ngroups, *sb = second.s + (base + top) * ngroups;
-        const uint8_t *za = p.w0.z + (base + top) * ngroups, *zb = second.z + (base + top) * ngroups;
-        int woff[2][2], goff_s[2][2];
+        int woff[2][2];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int row = min(r0 + (gate_up ? 0 : 16 * m) + g + 8 * i, last) - top;
                 woff[m][i] = row * row_bytes + 16 * t;
-                goff_s[m][i] = row * ngroups;
             }
+        // Of scales a lane loads those of one of its four rows.
+        const int64_t srow = (base + min(r0 + (gate_up ? 0 : 16 * (t >> 1)) + g + 8 * (t & 1), last)) * ngroups;
+        const uint16_t* sp = (t >> 1 ? second.s : p.w0.s) + srow;
+        const uint8_t* zp = (t >> 1 ? second.z : p.w0.z) + srow;
         for (int ct = blockIdx.z; ct * NC < count; ct += gridDim.z) {
             const int tiles = min((count - ct * NC + COLS - 1) / COLS, NT);
-            uint32_t s[2][2], z[2][2];  // the next chunk's scales and zero points: lane t block t's
-            int sc = part_of;           // that chunk
+            uint2 s;         // the next chunk's scales and zero points, packed
+            uint32_t z;
+            int sc = part_of;  // that chunk
             auto scales = [&]() {
-                const int b = 4 * sc + t, at = (32 * b) >> p.w0.group_log2;
-                const bool in = b < nb;
+                s = make_uint2(0, 0), z = 0;
+                if (sc < p.chunks) {
+                    const int at = sc * per_chunk;
+                    if (!wide) {
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int k = goff_s[m][i] + at;
-                        s[m][i] = in ? __ldg((m == 0 ? sa : sb) + k) : 0u;
-                        if (has_z) z[m][i] = in ? __ldg((m == 0 ? za : zb) + k) : 8u;
+                        for (int j = 0; j < 4; ++j) {
+                            if (j >= per_chunk || at + j >= ngroups) break;
+                            (j < 2 ? s.x : s.y) |= (uint32_t)__ldg(sp + at + j) << (16 * (j & 1));
+                            if (has_z) z |= (uint32_t)__ldg(zp + at + j) << (8 * j);
+                        }
+                    } else if (per_chunk == 4) {
+                        s = __ldg(reinterpret_cast<const uint2*>(sp + at));
+                        if (has_z) z = __ldg(reinterpret_cast<const uint32_t*>(zp + at));
+                    } else if (per_chunk == 2) {
+                        s.x = __ldg(reinterpret_cast<const uint32_t*>(sp + at));
+                        if (has_z) z = __ldg(reinterpret_cast<const uint16_t*>(zp + at));
+                    } else {
+                        s.x = __ldg(sp + at);
+                        if (has_z) z = __ldg(zp + at);
                     }
+                }
                 sc += p.wk;
             };
             int wc = part_of;  // the chunk of weights that is fetched next, its place in the ring, and of the columns'
@@ -322,15 +337,13 @@ __global__ void __launch_bounds__(32 * kWarps, kRowCtas) q4_rows_kernel(const Ro
                 fetch_weights();
                 fetch_columns();
                 asm volatile("cp.async.commit_group;" ::: "memory");
-                float so[2][2];
-                uint32_t zo[2][2];
+                float so[4];
+                uint32_t zo[4];
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        so[m][i] = scale_f32(s[m][i], p.w0.bf16);
-                        zo[m][i] = has_z ? 0x64006400u | (z[m][i] * 0x10001u) : 0x64086408u;
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    so[j] = scale_f32(((j < 2 ? s.x : s.y) >> (16 * (j & 1))) & 0xffffu, p.w0.bf16);
+                    zo[j] = 0x64006400u | (((z >> (8 * j)) & 0xffu) * 0x10001u);
+                }
                 scales();
                 if (c < p.chunks) {
                     const uint32_t mat = matrix_at + at;
