@@ -12,7 +12,7 @@
 // Either way a block's dot meets its scales in the lane that loaded them: nothing is shuffled until a tile ends, and every
 // group size costs the same.
 // Measured, replayed: 151936 x 2048, group 128, one-word activations 29 us (163 MB, 5.6 TB/s, 82% of the measured copy rate;
-// f32 42); 5120 x 2048, f32, 5.5; eight experts of 2048 x 768 with their sum 17 (21 MB, two launches of one wave each, whose
+// f32 42); 5120 x 2048, f32, 5.5; eight experts of 2048 x 768 with their sum 16 (21 MB, two launches of one wave each, whose
 // start, first loads and end are most of it).  Why a ring of 16-byte copies: plain 16-byte loads into registers took 55 us for
 // the 29, a lane's loads in flight being bound by its registers.
 #include "ffn4.h"
@@ -22,7 +22,9 @@ namespace q8 {
 namespace {
 
 constexpr int kRowWarps = 8;
-constexpr int kRowStages = 4;       // of a warp's ring
+// Of a warp's ring.  Three leave an SM room for the next launch's CTAs beside gate-up's: eight experts of 2048 x 768 17.4 us with
+// four, 15.7 with three, 15.4 with two; a long row of words needs three (151936 x 2048 29.1 and 32.4).
+constexpr int kRowStages = 3;
 constexpr int kStepBytes = 16 * 128;  // a step of one tile's rows
 
 // A block of the activation in shared memory.  f32: two parts of 64 bytes, and 16 more so that four blocks lie in different
