@@ -17,9 +17,9 @@
 //   16     issues the products
 //   17     copies the activations' chunks, 18 the weights', two at a time (rows of 128 bytes)
 // What bounds it is the chunks' way through the roles (950 to 1450 cycles for 128 rows by 128 values, of which an f32 row's
-// products are 256 up to 32 columns) and an item's start and end.  Measured, replayed: 200 f32 rows by 6 of 64 experts of 2048 x 1408 190 us
-// (295 MB; 43 at the measured copy rate), 61 f32 rows by 8192 x 4096 23 (21 MB; 3.1).  With the read-back in one set of four warps
-// it was slower: the loads from tensor memory and the scaling are the longest role.
+// products are 256 up to 32 columns) and an item's start and end.  Measured, replayed: 200 f32 rows by 6 of 64 experts of
+// 2048 x 1408 190 us (295 MB; 43 at the measured copy rate), 61 f32 rows by 8192 x 4096 23 (21 MB; 3.1).  With the read-back
+// in one set of four warps it was slower: the loads from tensor memory and the scaling are the longest role.
 // Every wait is bounded; one that gives up ends the CTA in order, with what is in flight waited for, and is recorded in the
 // workspace, on which such calls write nothing until q8_workspace_check.
 #pragma once
