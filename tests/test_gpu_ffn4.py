@@ -408,6 +408,22 @@ def test_projection_of_values_that_are_not_finite_and_of_extremes(q8, ws, rows):
     assert not y.any()
 
 
+@pytest.mark.parametrize("rows", [1, 5, 40])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_projection_with_scales_off_their_loads_alignment(q8, ws, rows, group):
+    """Scales at 2 bytes and zero points at 1 past an aligned address: the same results as from aligned ones."""
+    import torch
+    g = gen(rows + group)
+    q, s, z = matrix(torch, 200, 512, group, "bf16", True, g)
+    off = [torch.cat((t.new_zeros(1), t.flatten()))[1:].view(t.shape) for t in (s, z)]
+    assert off[0].data_ptr() % 4 == 2 and off[1].data_ptr() % 2 == 1
+    x = torch.randn(rows, 512, generator=g, device="cuda")
+    y, want = torch.empty(rows, 200, device="cuda"), torch.empty(rows, 200, device="cuda")
+    q8.q4_gemv(q8.q4_mat(q, s, z), want, x=x, ws=ws)
+    q8.q4_gemv(q8.q4_mat(q, *off), y, x=x, ws=ws)
+    assert torch.equal(y, want)
+
+
 def test_projection_into_columns_beside_its_rows(q8, ws):
     import torch
     g = gen(11)
