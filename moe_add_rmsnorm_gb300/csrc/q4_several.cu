@@ -11,11 +11,14 @@ struct CombineParams {
     const int32_t* ids;
     const float *gates, *residual, *out;
     float* y;
+    const int* failed;  // of products whose waits can give up, the workspace's word; else NULL
 };
 
-// y[r] = residual[r] + sum_j gates[r][j] out[r][j], in the order of the choices.
+// y[r] = residual[r] + sum_j gates[r][j] out[r][j], in the order of the choices.  Nothing where the products' waits gave up, in
+// this call or in an earlier one: `out` then holds an earlier call's sums.
 __global__ void __launch_bounds__(256) q4_combine_kernel(const CombineParams p) {
     griddep_wait();
+    const int failed = p.failed ? __ldcg(p.failed) : 0;  // (looked at only with the sums: its load is one among theirs)
     const int64_t o = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (o >= p.d) return;
     for (int64_t r = blockIdx.y; r < p.R; r += gridDim.y) {
@@ -27,7 +30,8 @@ __global__ void __launch_bounds__(256) q4_combine_kernel(const CombineParams p) 
             const float g = p.gates[c], v = p.out[c * p.d + o];
             if (e >= 0 && e < p.E) sum = fmaf(g, v, sum);
         }
-        p.y[r * p.d + o] = p.residual ? p.residual[r * p.d + o] + sum : sum;
+        sum = p.residual ? p.residual[r * p.d + o] + sum : sum;
+        if (failed == 0) p.y[r * p.d + o] = sum;
     }
 }
 
@@ -106,10 +110,10 @@ cudaError_t launch_q4_rows(const Q4Call& c, int form, Carve& ws, cudaStream_t st
     // 2048 x 1408, group 32, f32: 24 rows (2.3 an expert) 109 and 154, 60 (5.6) 151 and 176, 100 (9.4) 200 and 184, 256 (24) 412 and
     // 254.
     const int64_t columns = c.R * c.K * (form == FORM_ONE ? 1 : 2);
-    const cudaError_t e = columns <= 16 * groups ? launch_q4_warps(c, groups, form, out, ws, st)
-                                                 : launch_q4_tensor(c, groups, form, out, ws, st);
+    const bool warps = columns <= 16 * groups;
+    const cudaError_t e = warps ? launch_q4_warps(c, groups, form, out, ws, st) : launch_q4_tensor(c, groups, form, out, ws, st);
     if (e != cudaSuccess || ws.overflow || c.kind != Q4_DOWN) return e;
-    const CombineParams p = {c.E, c.out_rows, (int)c.R, c.K, c.ids, c.gates, c.residual, out, c.y};
+    const CombineParams p = {c.E, c.out_rows, (int)c.R, c.K, c.ids, c.gates, c.residual, out, c.y, warps ? nullptr : ws.failed};
     const dim3 grid((unsigned)((c.out_rows + 127) / 128), (unsigned)min(c.R, (int64_t)65535));
     return launch(q4_combine_kernel, grid, dim3(128), 0, st, 1, p);
 }

@@ -1,0 +1,64 @@
+"""GPU tests of the 4-bit feed-forward block at its edges.  Bounds and helpers as in test_gpu_ffn4.py."""
+import pytest
+
+from test_gpu_ffn4 import activation, check_combined, check_hidden, choices, gen, matrix, plan_of, quantize, values
+
+pytestmark = pytest.mark.gpu
+
+
+def give_up(q8, torch, ws):
+    """Marks the workspace: an attention on it whose waits run out."""
+    words = [torch.zeros(4, 2, 16, 64, dtype=torch.int8, device="cuda") for _ in range(2)]
+    scales = [torch.zeros(4, 2, 16, device="cuda") for _ in range(2)]
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    pages = q8.kv_pages(words[0], scales[0], words[1], scales[1])
+    q = torch.zeros(1, 4, 64, device="cuda")
+    q8.q8_paged_wait_selftest(pages, q8.kv_batch(i32(0, 1), i32(40), i32(0, 1, 2).view(1, 3)), q, torch.zeros_like(q), 16, ws)
+
+
+def experts(torch, rows, E, k, d, dff, form, seed):
+    """Matrices, choices, gates, an activation and hidden rows of a call."""
+    g = gen(seed)
+    mats = [matrix(torch, n, c, 32, "f16", True, g) for n, c in ((E * dff, d), (E * dff, d), (E * d, dff))]
+    ids = choices(torch, rows, E, k, g, False)
+    gates = torch.rand(rows, k, generator=g, device="cuda") + 0.1
+    call, x = activation(torch, rows, d, form, g)
+    h = torch.randn(rows, k, dff, generator=g, device="cuda")
+    if form == "f32":
+        hidden, hv = dict(h=h), h.double()
+    else:
+        q, lo, s = quantize(torch, h, form == "two")
+        hidden = dict(hq=q, hs=s, hl=lo)
+        hv = (q.double() if lo is None else q.double() + lo.double() / 128) * s.double().repeat_interleave(32, -1)
+    residual = torch.randn(rows, d, generator=g, device="cuda")
+    return mats, ids, gates, call, x, hidden, hv, residual
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("form", ["f32", "one"])
+def test_experts_on_a_workspace_of_which_a_wait_gave_up(q8, form, in_place):
+    """Products on the tensor cores, and the sum over their choices, write nothing until the workspace has been checked."""
+    import torch
+    rows, E, k, d, dff = 130, 6, 6, 128, 128
+    mats, ids, gates, call, x, hidden, hv, residual = experts(torch, rows, E, k, d, dff, form, 21)
+    m = [q8.q4_mat(*t) for t in mats]
+    plan, kept = plan_of(q8, torch, ids, E)
+    ws = q8.Workspace()
+    give_up(q8, torch, ws)
+    h = torch.full((rows, k, dff), 7.0, device="cuda")
+    y = residual.clone() if in_place else torch.full((rows, d), 7.0, device="cuda")
+    was = y.clone()
+    q8.moe_gate_up_q4(m[0], m[1], ids, h, **call, plan=plan, ws=ws)
+    q8.moe_down_combine_q4(m[2], ids, gates, y, **hidden, plan=plan, residual=y if in_place else residual, ws=ws)
+    assert (h == 7).all()
+    assert torch.equal(y, was)
+    with pytest.raises(q8.Q8Error) as e:
+        ws.check()
+    assert e.value.code == -4
+    q8.moe_gate_up_q4(m[0], m[1], ids, h, **call, plan=plan, ws=ws)
+    q8.moe_down_combine_q4(m[2], ids, gates, y, **hidden, plan=plan, residual=y if in_place else residual, ws=ws)
+    check_hidden(torch, h, values(torch, mats[0]), values(torch, mats[1]), x, ids, dff, form)
+    check_combined(torch, y, values(torch, mats[2]), hv, ids, gates, residual, d, form)
+    ws.check()
+    ws.close()
+    del kept
