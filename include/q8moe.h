@@ -100,8 +100,8 @@ Q8_API int q8_workspace_create(size_t bytes, q8_ws **ws);
 Q8_API void q8_workspace_destroy(q8_ws *ws);
 Q8_API size_t q8_workspace_bytes(const q8_ws *ws);
 /* Waits for `stream` and returns Q8_ETIMEOUT when a bounded wait of a q8_paged_attention, or of a product with 4-bit weights
- * (q4_gemv, moe_gate_up_q4, moe_down_combine_q4), on this workspace gave up: that
- * call's outputs are incomplete, and later ones on the workspace wrote nothing, because its counters may not have been
+ * (q4_gemv, moe_gate_up_q4, moe_down_combine_q4), on this workspace gave up: that call's outputs are incomplete, and later
+ * ones on the workspace, and moe_route_scored calls that fill a plan, wrote nothing, because its counters may not have been
  * zero.  (4-bit products of one row, and of so few rows that they leave the tensor cores alone, neither wait nor count, and are
  * computed as ever.)  The counters are zeroed and the failure cleared, so that the workspace can be used again; no other call on
  * it may be in flight. */

@@ -33,6 +33,7 @@ struct RouteParams {
     int32_t* hist;  // [CTAs][E] when a second launch groups the choices
     int* arrived;   // else: the CTAs that are done, zero between calls; the last one groups the choices
     int per;        // rows a CTA (0: rows are dealt out warp by warp)
+    const int* failed;  // with a plan: the workspace's word; when it is set `arrived` may not be zero, and nothing is written
 };
 
 // f32 -> an unsigned integer of the same order (both zeros alike).
@@ -146,14 +147,18 @@ __device__ __noinline__ void choose_exactly(const RouteParams& p, const float* r
 }
 
 // Adds the CTA's choices [first, first + n) (their experts in ids) to the lists, in ascending order: next[e] is expert e's
-// first free place.  wh is [warps][E] of shared memory.
+// first free place.  wh is [warps][E] of shared memory.  (What is no expert indexes nothing: ids that this call's launches did not
+// write, were the workspace in use by another call at the same time.)
 __device__ __forceinline__ void place_choices(const int32_t* ids, int first, int n, int E, int* wh, int* next, int32_t* lists) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, W = blockDim.x >> 5;
     const int seg = ((n + W - 1) / W + 31) & ~31;
     const int lo = min(w * seg, n), hi = min(lo + seg, n);
     for (int i = threadIdx.x; i < W * E; i += blockDim.x) wh[i] = 0;
     __syncthreads();
-    for (int i = lo + lane; i < hi; i += 32) atomicAdd(&wh[w * E + __ldcg(ids + first + i)], 1);
+    for (int i = lo + lane; i < hi; i += 32) {
+        const int e = __ldcg(ids + first + i);
+        if ((unsigned)e < (unsigned)E) atomicAdd(&wh[w * E + e], 1);
+    }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         int run = next[e];
@@ -165,8 +170,9 @@ __device__ __forceinline__ void place_choices(const int32_t* ids, int first, int
     }
     __syncthreads();
     for (int i = lo; i < hi; i += 32) {
-        const bool in = i + lane < hi;
-        const int e = in ? __ldcg(ids + first + i + lane) : E;  // (lanes past the end stand together)
+        int e = i + lane < hi ? __ldcg(ids + first + i + lane) : E;  // (lanes past the end stand together)
+        const bool in = (unsigned)e < (unsigned)E;
+        if (!in) e = E;
         const unsigned same = __match_any_sync(FULL, e);
         const int before = __popc(same & ((1u << lane) - 1));
         if (in) lists[wh[w * E + e] + before] = first + i + lane;
@@ -224,6 +230,7 @@ __global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_k
     float* cs = reinterpret_cast<float*>(c64);
     uint2* found = reinterpret_cast<uint2*>(smem) + w * max(p.E, 32);  // candidates' keys and experts, in the marks' place
     griddep_wait();  // (launches overlap up to here: nothing is read before the launch before has ended)
+    const int failed = p.failed ? __ldcg(p.failed) : 0;  // (looked at only with the first results)
     const int S = p.E / p.groups;
     uint32_t group[(NL + 3) / 4] = {};  // the group of expert lane + 32 i in byte i
     if (p.groups > 1) {
@@ -391,7 +398,7 @@ __global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_k
             zs = group_sum<32>(zs);
             if (v > -INFINITY) gate = expf(v - m0) / zs;
         }
-        if (kth) {
+        if (kth && failed == 0) {
             p.ids[(int64_t)r * p.K + rank] = id;
             p.gates[(int64_t)r * p.K + rank] = gate * p.scale;
         }
@@ -400,7 +407,7 @@ __global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_k
     if (!p.per || !p.plan.counts) return;
     // The grouping: by the last CTA of few choices, else this CTA's counts for the CTAs that place the choices.
     int from = first, n = (end - first) * p.K;
-    __syncthreads();
+    if (__syncthreads_or(failed)) return;
     if (!p.hist) {
         if (gridDim.x > 1) {
             if (threadIdx.x == 0) last_cta = atomic_add_acq_rel_gpu(p.arrived, 1) == (int)gridDim.x - 1;
@@ -415,7 +422,10 @@ __global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_k
     int* off = total + p.E;
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) total[e] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += blockDim.x) atomicAdd(&total[__ldcg(p.ids + (int64_t)from * p.K + i)], 1);
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int e = __ldcg(p.ids + (int64_t)from * p.K + i);
+        if ((unsigned)e < (unsigned)p.E) atomicAdd(&total[e], 1);
+    }
     __syncthreads();
     if (p.hist) {
         for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.hist[(int64_t)blockIdx.x * p.E + e] = total[e];
@@ -436,8 +446,9 @@ __global__ void __launch_bounds__(kPlaceThreads) place_kernel(const RouteParams 
     int* before = off + p.E;
     int* wh = before + p.E;
     griddep_wait();
+    const int failed = p.failed ? __ldcg(p.failed) : 0;
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) total[e] = before[e] = 0;
-    __syncthreads();
+    if (__syncthreads_or(failed)) return;  // (the histograms have not been written)
     const int mine = blockIdx.x;
     if (p.E % 4 == 0) {  // four experts a thread
         const int quads = p.E / 4, parts = max(1, (int)blockDim.x / quads);
@@ -499,6 +510,7 @@ cudaError_t run(RouteParams p, Carve& ws, cudaStream_t st) {
     const int W = few ? min(most, 8) : most;
     const int grid = few ? (p.rows + W - 1) / W : min(sms, (p.rows + W - 1) / W);
     p.per = (p.rows + grid - 1) / grid;
+    p.failed = ws.failed;
     if (few && grid > 1) p.arrived = ws.take_counters(1);
     if (!few) p.hist = ws.take<int32_t>((size_t)grid * p.E);
     if (ws.overflow) return cudaSuccess;
@@ -518,7 +530,7 @@ cudaError_t run(RouteParams p, Carve& ws, cudaStream_t st) {
 cudaError_t launch_route_scored(const RouteScoredCall& c, Carve& ws, cudaStream_t st) {
     RouteParams p = {c.logits, c.stride, (int)c.rows, c.E, c.K, c.rule.bias, c.rule.score == Q8_SCORE_SIGMOID,
                      c.rule.groups, c.rule.keep_groups, c.rule.group_top, c.rule.renorm, c.rule.scale, c.ids, c.gates, c.plan,
-                     nullptr, nullptr, 0};
+                     nullptr, nullptr, 0, nullptr};
     if (p.E <= 32) return run<1>(p, ws, st);
     if (p.E <= 64) return run<2>(p, ws, st);
     if (p.E <= 128) return run<4>(p, ws, st);

@@ -1,7 +1,8 @@
 """GPU tests of the 4-bit feed-forward block at its edges.  Bounds and helpers as in test_gpu_ffn4.py."""
 import pytest
 
-from test_gpu_ffn4 import activation, check_combined, check_hidden, choices, gen, matrix, plan_of, quantize, values
+from test_gpu_ffn4 import (activation, check_combined, check_hidden, check_route, choices, gen, matrix, plan_of, quantize, route,
+                           values)
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +63,26 @@ def test_experts_on_a_workspace_of_which_a_wait_gave_up(q8, form, in_place):
     ws.check()
     ws.close()
     del kept
+
+
+@pytest.mark.parametrize("rows", [1, 5, 61, 2311])
+def test_route_on_a_workspace_of_which_a_wait_gave_up(q8, rows):
+    """With a plan nothing is written until the workspace has been checked; without one no workspace is looked at."""
+    import torch
+    E, k, rule = 64, 6, dict(score=1, groups=4, keep_groups=2)
+    logits = torch.randn(rows, E, generator=gen(rows), device="cuda")
+    ids, gates = torch.full((rows, k), 3, dtype=torch.int32, device="cuda"), torch.full((rows, k), 7.0, device="cuda")
+    arrays = [torch.full((n,), -9, dtype=torch.int32, device="cuda") for n in (E, E + 1, rows * k, E + 1)]
+    ws = q8.Workspace()
+    give_up(q8, torch, ws)
+    for _ in range(2):
+        q8.moe_route_scored(logits, ids, gates, plan=q8.plan_struct(*arrays), ws=ws, **rule)
+    assert (ids == 3).all() and (gates == 7).all() and all((a == -9).all() for a in arrays)
+    check_route(torch, route(q8, torch, ws, logits, k, False, **rule), logits, k, False, **rule)
+    with pytest.raises(q8.Q8Error) as e:
+        ws.check()
+    assert e.value.code == -4
+    for _ in range(2):
+        check_route(torch, route(q8, torch, ws, logits, k, True, **rule), logits, k, True, **rule)
+    ws.check()
+    ws.close()
