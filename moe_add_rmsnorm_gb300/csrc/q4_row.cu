@@ -28,7 +28,7 @@ constexpr int kRowStages = 3;
 constexpr int kStepBytes = 16 * 128;  // a step of one tile's rows
 
 // A block of the activation in shared memory.  f32: two parts of 64 bytes, and 16 more so that four blocks lie in different
-// banks (its unit stands in the array behind).  Words: 32 bytes (and 32 of low words), then scale and sum.
+// banks (its unit stands in the array behind, as two factors).  Words: 32 bytes (and 32 of low words), then scale and sum.
 template <int FORM>
 constexpr int block_bytes() { return FORM == FORM_F32 ? 144 : FORM == FORM_ONE ? 48 : 80; }
 
@@ -69,7 +69,12 @@ __device__ __forceinline__ void stage_rows(const RowParams& p, char* vecs) {
             const ActParts a = split_values(x, m);
             *reinterpret_cast<uint4*>(at + (o & 3) * 16) = a.hi;
             *reinterpret_cast<uint4*>(at + 64 + (o & 3) * 16) = a.lo;
-            if ((o & 3) == 0) *reinterpret_cast<float*>(vecs + v * p.vec + 8 * p.steps * 144 + 4 * b) = a.scale;
+            // The unit 2^k as 2^(k >> 1) for the weights' scale and the rest for the dot: with the whole of it on the scale their
+            // product left f32's range below long before the block's result did.
+            const int k = (int)(__float_as_uint(a.scale) >> 23) - 127, half = k >> 1;
+            if ((o & 3) == 0)
+                *reinterpret_cast<float2*>(vecs + v * p.vec + 8 * p.steps * 144 + 8 * b) =
+                    make_float2(__int_as_float((127 + half) << 23), __int_as_float((127 + k - half) << 23));
         } else {
             const int64_t from = (int64_t)v * cols + 8 * o;
             const bool in = 8 * o < cols;
@@ -98,7 +103,7 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int m) { return m ==
 template <int FORM>
 struct Operand {
     uint4 v[FORM == FORM_F32 || FORM == FORM_TWO ? 4 : 2];
-    float scale;
+    float scale, rest;  // f32: the unit is their product
     int sum;
 };
 
@@ -119,8 +124,8 @@ __device__ __forceinline__ void multiply(const uint4 (&w)[2], const float (&sw)[
             mma16(d, h0[0], h1[0], h0[1], h1[1], x.v[m].x, x.v[m].y);
             mma16(d, h0[2], h1[2], h0[3], h1[3], x.v[m].z, x.v[m].w);
         }
-        acc[0] = fmaf(sw[0] * x.scale, d[0] + d[1], acc[0]);
-        acc[1] = fmaf(sw[1] * x.scale, d[2] + d[3], acc[1]);
+        acc[0] = fmaf(sw[0] * x.scale, (d[0] + d[1]) * x.rest, acc[0]);
+        acc[1] = fmaf(sw[1] * x.scale, (d[2] + d[3]) * x.rest, acc[1]);
     } else {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -279,7 +284,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) q4_row_kernel(const RowPara
                             const char* at = own ? vec + b * 144 + (g & 1) * 64 : reinterpret_cast<const char*>(zeros);
 #pragma unroll
                             for (int m = 0; m < 4; ++m) x.v[m] = *reinterpret_cast<const uint4*>(at + 16 * m);
-                            x.scale = *reinterpret_cast<const float*>(vec + 8 * p.steps * 144 + 4 * b);
+                            const float2 f = *reinterpret_cast<const float2*>(vec + 8 * p.steps * 144 + 8 * b);
+                            x.scale = f.x, x.rest = f.y;
                         } else {
                             const char* at = vec + b * block_bytes<FORM>();
 #pragma unroll
@@ -356,7 +362,7 @@ cudaError_t run(const RowParams& p, cudaStream_t st) {
 
 template <int FORM>
 cudaError_t run_kind(RowParams p, cudaStream_t st) {
-    p.vec = (uint32_t)(8 * p.steps * (block_bytes<FORM>() + (FORM == FORM_F32 ? 4 : 0)));
+    p.vec = (uint32_t)(8 * p.steps * (block_bytes<FORM>() + (FORM == FORM_F32 ? 8 : 0)));
     // The parts that leave an SM the fewest steps, counting half a one for each tile's end.  Measured, us, 1, 2, 4 and 8 parts, f32:
     // 2048 x 4096 13.3, 8.3, 5.7 and 4.3; 8192 x 4096 13.3, 8.3, 8.1 and 8.5; 151936 x 2048 42, 44, 49 and 57.
     int best = 0;
@@ -376,7 +382,7 @@ cudaError_t run_kind(RowParams p, cudaStream_t st) {
 // Whether the row's activations fit a CTA (an expert's hidden rows may be many and long).
 bool q4_row_fits(const Q4Call& c) {
     const size_t steps = (c.w0.cols + 255) / 256, vecs = c.kind == Q4_DOWN ? c.K : 1;
-    const size_t block = c.act.x ? 148 : c.act.lo ? 80 : 48;
+    const size_t block = c.act.x ? 152 : c.act.lo ? 80 : 48;
     const size_t mt = c.kind == Q4_GATE_UP ? 2 : 1, segs = 8 * vecs;
     return (size_t)kRowWarps * kRowStages * mt * kStepBytes + vecs * steps * 8 * block + 2 * segs * mt * 64 <= kRowSmem;
 }

@@ -1,10 +1,17 @@
 """GPU tests of the 4-bit feed-forward block at its edges.  Bounds and helpers as in test_gpu_ffn4.py."""
 import pytest
 
-from test_gpu_ffn4 import (activation, check_combined, check_hidden, check_route, choices, gen, matrix, plan_of, quantize, route,
-                           values)
+from test_gpu_ffn4 import (activation, check_combined, check_hidden, check_route, choices, gen, matrix, plan_of,
+                           product_error, quantize, route, values)
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ws(q8):
+    w = q8.Workspace()
+    yield w
+    w.close()
 
 
 def give_up(q8, torch, ws):
@@ -86,3 +93,20 @@ def test_route_on_a_workspace_of_which_a_wait_gave_up(q8, rows):
         check_route(torch, route(q8, torch, ws, logits, k, True, **rule), logits, k, True, **rule)
     ws.check()
     ws.close()
+
+
+@pytest.mark.parametrize("xe,se", [(-106, -23), (110, -60), (-100, 60), (120, -6), (-60, -60)])
+@pytest.mark.parametrize("rows", [1, 3, 40])
+def test_projection_of_magnitudes_far_from_1(q8, ws, rows, xe, se):
+    """Values of 2^xe by scales of 2^se, whose products' sums are normal numbers: the usual bound, and half a step of the
+    smallest numbers for every sum."""
+    import torch
+    g = gen(rows + 7)
+    q = torch.randint(0, 256, (50, 128), generator=g, device="cuda", dtype=torch.uint8)
+    s = (torch.randn(50, 8, generator=g, device="cuda", dtype=torch.float64) * 2.0 ** se).to(torch.bfloat16)
+    x = (torch.randn(rows, 256, generator=g, device="cuda", dtype=torch.float64) * 2.0 ** xe).float()
+    y = torch.empty(rows, 50, device="cuda")
+    q8.q4_gemv(q8.q4_mat(q, s), y, x=x, ws=ws)
+    W = values(torch, (q, s, None))
+    tol = product_error(torch, W, x.double(), "f32") + (8 + 8) * 2.0 ** -149
+    assert ((y.double() - x.double() @ W.T).abs() <= tol).all()
