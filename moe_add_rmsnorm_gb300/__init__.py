@@ -703,7 +703,7 @@ def moe_gate_up_q4(gate, up, ids, h, x=None, xq=None, xs=None, xl=None, plan=Non
     if h.dtype is not _torch.float32 or h.numel() != rows * k * dff or not h.is_contiguous():
         _refuse(f"h: not contiguous f32 [{rows}, {k}, dff]")
     xa, stride, qa = _q4_act(x, xq, xs, xl, rows, gate.cols, d, "x")
-    if rows > 1 and stride not in (0, gate.cols):
+    if rows > 1 and x is not None and stride != gate.cols:  # (rows 0 apart among them: the call reads dense ones)
         _refuse("x: not contiguous")
     _check(lib.moe_gate_up_q4(gate, up, dff, xa, qa, rows, k, ids.data_ptr(), _plan_ref(plan), h.data_ptr(), _ws_of(ws, d),
                               _stream_of(stream, d)))
