@@ -43,7 +43,8 @@ class q8_shared_expert(ctypes.Structure):
     _fields_ = [("gate", q8_mat), ("up", q8_mat), ("down", q8_mat)]
 
 
-class q8_moe_plan(ctypes.Structure):
+class q8_moe_plan(ctypes.Structure):  # built by plan_struct()
+    holds = tensors = None  # the device, experts and choices that its tensors are for
     _fields_ = [("counts", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("lists", ctypes.c_void_p),
                 ("active", ctypes.c_void_p)]
 
@@ -278,7 +279,16 @@ def set_streamed_batch_attention(min_batch: int):
 
 
 def plan_struct(counts, offsets, lists, active):
-    return q8_moe_plan(counts.data_ptr(), offsets.data_ptr(), lists.data_ptr(), active.data_ptr())
+    """A plan over device int32 tensors: counts [experts], offsets and active [experts + 1], lists [rows * k].  The struct keeps
+    the tensors; the calls that know their types, sizes and device check them."""
+    plan = q8_moe_plan(counts.data_ptr(), offsets.data_ptr(), lists.data_ptr(), active.data_ptr())
+    plan.tensors = counts, offsets, lists, active
+    kind, dev = _lazy_torch().int32, counts.get_device()
+    if all(t.dtype is kind and t.is_contiguous() and t.get_device() == dev for t in plan.tensors):
+        plan.holds = dev, min(counts.numel(), offsets.numel() - 1, active.numel() - 1), lists.numel()
+    else:
+        plan.holds = None, 0, 0
+    return plan
 
 
 def moe_route_topk(rq, rs, mode, k, ids, gates, x=None, xq=None, xs=None, rows=1, logits=None, plan=None, ws=None,
@@ -615,8 +625,15 @@ def postnorm_add_rmsnorm_q8(a, b, w_post, w_pre, eps, gate=None, scale=1.0, sum_
         _tensor(y_out, f32, shape, dev, "y_out"), act_, _stream_of(stream, dev)))
 
 
-def _plan_ref(plan):
-    return ctypes.byref(plan) if plan is not None else None
+def _plan_ref(plan, experts, places, device):
+    """The plan of a call of this many experts, and of rows * k places in its lists (None: NULL)."""
+    if plan is None:
+        return None
+    holds = plan.holds  # (one filled with addresses has nothing to check)
+    if holds is not None and (holds[0] != device or holds[1] < experts or holds[2] < places):
+        _refuse("plan: not contiguous int32 tensors on the current device" if holds[0] != device else
+                f"plan: for {holds[1]} experts and {holds[2]} choices, not {experts} and {places}")
+    return ctypes.byref(plan)
 
 
 def _choices(ids, device):
@@ -639,8 +656,8 @@ def moe_route_scored(logits, ids, gates, score=SCORE_SOFTMAX, bias=None, groups=
         _refuse("ids: rows differ")
     rule = q8_route_rule(score, _vec(bias, E, d, "bias"), groups, keep_groups, group_top, 1 if renorm else 0, scale)
     _check(lib.moe_route_scored(la, stride, rows, E, rule, k, ids.data_ptr(),
-                                _tensor(gates, _torch.float32, ids.shape, d, "gates"), _plan_ref(plan), _ws_of(ws, d),
-                                _stream_of(stream, d)))
+                                _tensor(gates, _torch.float32, ids.shape, d, "gates"),
+                                _plan_ref(plan, E, rows * k, d), _ws_of(ws, d), _stream_of(stream, d)))
 
 
 def q4_mat(q, s, z=None) -> q4_matrix:
@@ -705,8 +722,9 @@ def moe_gate_up_q4(gate, up, ids, h, x=None, xq=None, xs=None, xl=None, plan=Non
     xa, stride, qa = _q4_act(x, xq, xs, xl, rows, gate.cols, d, "x")
     if rows > 1 and x is not None and stride != gate.cols:  # (rows 0 apart among them: the call reads dense ones)
         _refuse("x: not contiguous")
-    _check(lib.moe_gate_up_q4(gate, up, dff, xa, qa, rows, k, ids.data_ptr(), _plan_ref(plan), h.data_ptr(), _ws_of(ws, d),
-                              _stream_of(stream, d)))
+    _check(lib.moe_gate_up_q4(gate, up, dff, xa, qa, rows, k, ids.data_ptr(),
+                              _plan_ref(plan, gate.rows // max(dff, 1), rows * k, d) if rows > 1 else None, h.data_ptr(),
+                              _ws_of(ws, d), _stream_of(stream, d)))
 
 
 def moe_down_combine_q4(down, ids, gates, y, h=None, hq=None, hs=None, hl=None, plan=None, residual=None, ws=None,
@@ -724,8 +742,9 @@ def moe_down_combine_q4(down, ids, gates, y, h=None, hq=None, hs=None, hl=None, 
         h = h.view(rows * k, down.cols)
     xa, _, qa = _q4_act(h, hq, hs, hl, rows * k, down.cols, dev, "h")
     _check(lib.moe_down_combine_q4(down, d, xa, qa, rows, k, ids.data_ptr(), _tensor(gates, f32, ids.shape, dev, "gates"),
-                                   _plan_ref(plan), _tensor(residual, f32, y.shape, dev, "residual"), y.data_ptr(),
-                                   _ws_of(ws, dev), _stream_of(stream, dev)))
+                                   _plan_ref(plan, down.rows // max(d, 1), rows * k, dev) if rows > 1 else None,
+                                   _tensor(residual, f32, y.shape, dev, "residual"), y.data_ptr(), _ws_of(ws, dev),
+                                   _stream_of(stream, dev)))
 
 
 class Model:

@@ -75,3 +75,57 @@ def test_other_rows_at_one_place(made):
     assert calls.pop()[1][2] == 0  # its stride: "x: rows 0 apart"
     q8.moe_route_scored(on(8).expand(3, 8), ids, gates, stream=1)
     assert calls.pop()[1][1] == 0
+
+
+@pytest.mark.parametrize("change,word", [
+    (dict(counts=3), "plan: for 3 experts and 6 choices, not 4 and 6"), (dict(offsets=4), "plan: for 3 experts"),
+    (dict(lists=5), "plan: for 4 experts and 5 choices"), (dict(active=4), "plan: for 3 experts"),
+    (dict(dtype="int64"), "plan: not contiguous int32"), (dict(device=1), "plan: not contiguous int32"),
+    (dict(device=-1), "plan: not contiguous int32"), (dict(apart=True), "plan: not contiguous int32")])
+def test_plans_that_do_not_hold_the_call(made, change, word):
+    """A plan of fewer experts or rows, of another type or device: the calls would write, or read, past it."""
+    import torch
+    q8, calls = made
+    gate, up, down = matrix(q8, 64, 128), matrix(q8, 64, 128), matrix(q8, 512, 32)
+    ids, gates = on(3, 2, dtype=torch.int32), on(3, 2)
+
+    def plan(counts=4, offsets=5, lists=6, active=5, dtype="int32", device=0, apart=False):
+        sizes = (counts, offsets, lists, active)
+        if apart:
+            return q8.plan_struct(*(on(2 * n, dtype=torch.int32)[::2] for n in sizes))
+        return q8.plan_struct(*(on(n, dtype=getattr(torch, dtype), device=device) for n in sizes))
+
+    def each(p):
+        yield lambda: q8.moe_route_scored(on(3, 4), ids, gates, plan=p, ws=Workspace, stream=1)
+        yield lambda: q8.moe_gate_up_q4(gate, up, ids, on(3, 2, 16), x=on(3, 128), plan=p, ws=Workspace, stream=1)
+        yield lambda: q8.moe_down_combine_q4(down, ids, gates, on(3, 128), h=on(3, 2, 32), plan=p, ws=Workspace, stream=1)
+
+    for call in each(plan(**change)):
+        refused(q8, calls, word, call)
+    for call in each(plan(counts=9, offsets=12, lists=100, active=10)):  # larger ones hold it
+        call()
+    assert len(calls) == 3
+
+
+def test_one_row_needs_no_plan(made):
+    """A row's choices are not grouped: whatever plan comes along is not looked at."""
+    import torch
+    q8, calls = made
+    gate, up, ids = matrix(q8, 64, 128), matrix(q8, 64, 128), on(1, 2, dtype=torch.int32)
+    plan = q8.plan_struct(*(on(1, dtype=torch.int32) for _ in range(4)))
+    q8.moe_gate_up_q4(gate, up, ids, on(1, 2, 16), x=on(1, 128), plan=plan, ws=Workspace, stream=1)
+    assert len(calls) == 1 and calls[0][1][8] is None
+
+
+def test_a_plan_keeps_its_tensors(made):
+    import gc
+    import weakref
+
+    import torch
+    q8, calls = made
+    arrays = [on(n, dtype=torch.int32) for n in (4, 5, 6, 5)]
+    held = [weakref.ref(a) for a in arrays]
+    plan = q8.plan_struct(*arrays)
+    del arrays
+    gc.collect()
+    assert all(r() is not None for r in held) and plan.lists == held[2]().data_ptr()
