@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) q4_mma_kernel(const __grid_con
         if (__all_sync(0xffffffffu, mbar_try_wait(x, px & 1u) || !ok)) return;
         ok = __all_sync(0xffffffffu, mma_wait_on(x, px, &sh.dead, p.failed));
     };
-    // After a wait that gave up nothing may be on its way into shared memory when the CTA ends.
+    // When the CTA ends nothing may be on its way into shared memory: a role that copies or multiplies waits for the last of
+    // its own, which the role that uses them may have given up on.
     auto drain = [&](uint64_t* x, unsigned px) {
         for (unsigned n = 0; n < 1024 && !mbar_try_wait(x, px & 1u); ++n) __nanosleep(64);
     };
@@ -479,10 +480,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1) q4_mma_kernel(const __grid_con
                     }
                 }
             }
-            for (unsigned i = gi > kColumns ? gi - kColumns : 0; i < gi && !ok; ++i) {
-                drain(&sh.b_full[i % kColumns], i / kColumns);
-                if (FORM != FORM_F32) drain(&sh.c_full[i % kScaleSlots], i / kScaleSlots);
-            }
+            for (unsigned i = gi > kColumns ? gi - kColumns : 0; i < gi; ++i) drain(&sh.b_full[i % kColumns], i / kColumns);
+            for (unsigned i = gi > kScaleSlots ? gi - kScaleSlots : 0; i < gi && FORM != FORM_F32; ++i)
+                drain(&sh.c_full[i % kScaleSlots], i / kScaleSlots);
         }
     } else if (w == 18) {
         // ---- the weights' copies -----------------------------------------------------------------------------------------
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) q4_mma_kernel(const __grid_con
                         if (gate_up) tile_g2s(sh.raw[to] + 64 * 128, &map1, 64 * c, row, &sh.raw_full[to]);
                     }
             }
-            for (unsigned i = pair > kRaw ? pair - kRaw : 0; i < pair && !ok; ++i) drain(&sh.raw_full[i % kRaw], i / kRaw);
+            for (unsigned i = pair > kRaw ? pair - kRaw : 0; i < pair; ++i) drain(&sh.raw_full[i % kRaw], i / kRaw);
         }
     } else if (w == 16) {
         // ---- the products -----------------------------------------------------------------------------------------------
@@ -552,10 +552,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1) q4_mma_kernel(const __grid_con
                 }
             }
         }
-        if (!ok) {  // (no product may be under way when its operands and its tensor memory go)
-            if (elected()) tc_commit(&sh.drain);
-            drain(&sh.drain, 0);
-        }
+        if (elected()) tc_commit(&sh.drain);  // (no product may be under way when its operands and its tensor memory go)
+        __syncwarp();
+        drain(&sh.drain, 0);
         __syncwarp();
     } else {
         // ---- read back -----------------------------------------------------------------------------------------------
