@@ -65,6 +65,10 @@ struct Group {
     int e, first, count, slot;  // e < 0: none
 };
 
+// The products' kernel reads the plan and the workspace's word before its dependency wait, as do the warps' products (q4_rows.cuh).
+// Only the launch that lays the rows out comes between, and it lets this one start after its own wait has returned in every
+// CTA: what earlier launches wrote is in L2 by then, and an SM's L1 keeps no line from before a launch's start.  Loads that pass
+// L1 by would say so without that second step, and took a chunk's experts from 190 to 192.5 us.
 __device__ __forceinline__ int mma_groups(const MmaParams& p) {
     if (p.kind == Q4_DENSE) return 1;
     return min(max(p.plan.active[0], 0), (int)min(p.E, (int64_t)p.R * p.K));
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) q4_mma_kernel(const __grid_con
     // Blocks whose dots share a buffer; buffers that are handed over together (a hand-over costs the warps 100 cycles and
     // more on either side: a chunk's buffers, or half of them where tensor memory holds no more); and such sets.
     const int unit_log2 = FORM == FORM_F32 ? p.w0.group_log2 - 5 : 0, unit = 1 << unit_log2, units = 4 >> unit_log2;
-    const int set = min(units, TN == 64 ? 2 : 4), sets = set == 4 || TN == 64 ? 2 : 4;
+    const int set = min(units, TN == 64 ? 2 : 4), sets = set == 4 || TN == 64 ? 2 : 4;  // (set * sets * TN: at most 256 columns)
     const int per_group = p.row_tiles * p.col_tiles * p.slices;
     const int items = mma_groups(p) * per_group;
     if (threadIdx.x == 0) {
@@ -558,9 +562,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1) q4_mma_kernel(const __grid_con
         __syncwarp();
     } else {
         // ---- read back -----------------------------------------------------------------------------------------------
-        // A chunk's scales are overwritten eight chunks on: the copies run at most four chunks ahead of the products (the
-        // unpacking three), and these at most two ahead of the reading, whose warps give a buffer back only after they
-        // have used the scales of all before it.
+        // A chunk's scales are overwritten kScaleSlots chunks on.  Chunk c's are written once the products of c - kOperands are
+        // done (copied: of c - kColumns), and these started once the reading had given back the buffers they use, which are
+        // those of `sets` sets before: of four chunks at most (an f32 row's groups of 64 and 128; words have two).  The
+        // reading gives a buffer back only after it has used the scales of all before it, so chunk c - 7's have been used.
+        static_assert(kScaleSlots >= kOperands + 4 && kScaleSlots >= kColumns + 2, "scales in use are not overwritten");
+        static_assert(kSums + 256 <= 512, "the operands' and the dots' columns of tensor memory");
         const int r = 32 * (w & 3) + lane;
         constexpr int HN = TN / 2;
         const int col0 = w >= 12 ? HN : 0;
