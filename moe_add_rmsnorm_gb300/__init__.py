@@ -618,7 +618,8 @@ def postnorm_add_rmsnorm_q8(a, b, w_post, w_pre, eps, gate=None, scale=1.0, sum_
         else:
             _refuse(f"gate: {tuple(g)}, expected [{d}], [{rows}, 1] or [{rows}, {d}]")
         ga = gate.data_ptr()
-    act_ = ctypes.byref(_words(yq, ys, yl, rows, d, dev, "yq")) if yq is not None or ys is not None else None
+    words = yq is not None or ys is not None or yl is not None
+    act_ = ctypes.byref(_words(yq, ys, yl, rows, d, dev, "yq")) if words else None
     _check(lib.postnorm_add_rmsnorm_q8(
         _tensor(a, f32, shape, dev, "a"), _tensor(b, f32, shape, dev, "b"), _vec(w_post, d, dev, "w_post"),
         _vec(w_pre, d, dev, "w_pre"), ga, gr, gc, scale, rows, d, eps, _tensor(sum_out, f32, shape, dev, "sum_out"),

@@ -129,3 +129,15 @@ def test_a_plan_keeps_its_tensors(made):
     del arrays
     gc.collect()
     assert all(r() is not None for r in held) and plan.lists == held[2]().data_ptr()
+
+
+def test_low_words_alone_are_refused(made):
+    """Low words without words would be left unwritten."""
+    import torch
+    q8, calls = made
+    a, b, w = on(2, 64), on(2, 64), on(64)
+    low = on(2, 64, dtype=torch.int8)
+    refused(q8, calls, "yq: words without scales", lambda: q8.postnorm_add_rmsnorm_q8(a, b, None, w, 1e-6, y_out=on(2, 64), yl=low,
+                                                                                      stream=1))
+    q8.postnorm_add_rmsnorm_q8(a, b, None, w, 1e-6, yq=on(2, 64, dtype=torch.int8), ys=on(2, 2), yl=low, stream=1)
+    assert len(calls) == 1
