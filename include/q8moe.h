@@ -512,7 +512,9 @@ typedef struct {
 /* y[r][o] = sum_t W[o][t] x[r][t] for `rows` activation rows, x either f32 (rows x_stride values apart, 16-byte aligned, the
  * stride a multiple of 4) or, with x NULL, the quantized form xq (dense; the two-word form when xq->lo is not NULL).  y is
  * device f32, rows y_stride values apart, and overlaps no input (columns beside x's of one buffer do not).  Every 32-value
- * block's dot of a quantized activation is the exact integer, scaled and summed in f32; f32 activations enter as two f16
+ * block's dot of a quantized activation is the exact integer, scaled and summed in f32 (with two words it is an integer of
+ * 128ths that f32 holds while |word - z| is at most 15, as with zero points of 4 bits; beyond it is rounded to 2^-24 of the
+ * block's absolute terms for each of its sums); f32 activations enter as two f16
  * parts, which hold a value to 2^-22 of it or 2^-28 of the largest magnitude of its block (one row) or of its row (several),
  * whichever is more, and are summed in f32.  With several rows scales of magnitudes up to 2^80 leave the sums in range.  Calls
  * of one row need no workspace; several take four bytes of it an activation value and some MiB, a projection as many rows at

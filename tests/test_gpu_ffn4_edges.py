@@ -110,3 +110,22 @@ def test_projection_of_magnitudes_far_from_1(q8, ws, rows, xe, se):
     W = values(torch, (q, s, None))
     tol = product_error(torch, W, x.double(), "f32") + (8 + 8) * 2.0 ** -149
     assert ((y.double() - x.double() @ W.T).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("zero", [None, 0, 15])
+@pytest.mark.parametrize("rows", [1, 5, 40])
+def test_two_word_dots_are_exact(q8, ws, rows, zero):
+    """A block's two-word dot is an integer of 128ths: with zero points up to 15 it is below 32 * 15 * 16383 < 2^23, which f32
+    holds exactly, as are all its parts' sums."""
+    import torch
+    g = gen(rows)
+    q = torch.randint(0, 256, (64, 16), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.ones(64, 1, dtype=torch.float16, device="cuda")
+    z = None if zero is None else torch.full((64, 1), zero, dtype=torch.uint8, device="cuda")
+    hi, lo = (torch.randint(-127, 128, (rows, 32), generator=g, device="cuda", dtype=torch.int8) for _ in range(2))
+    hi[0], lo[0] = 127, 127
+    q[0], q[1] = 0, 255
+    y = torch.empty(rows, 64, device="cuda")
+    q8.q4_gemv(q8.q4_mat(q, s, z), y, xq=hi, xs=torch.ones(rows, 1, device="cuda"), xl=lo, ws=ws)
+    x = hi.double() + lo.double() / 128
+    assert torch.equal(y.double(), x @ values(torch, (q, s, z)).T)
