@@ -1,4 +1,6 @@
 """GPU tests of the 4-bit feed-forward block at its edges.  Bounds and helpers as in test_gpu_ffn4.py."""
+import math
+
 import pytest
 
 from test_gpu_ffn4 import (activation, check_combined, check_hidden, check_route, choices, gen, matrix, plan_of,
@@ -129,3 +131,20 @@ def test_two_word_dots_are_exact(q8, ws, rows, zero):
     q8.q4_gemv(q8.q4_mat(q, s, z), y, xq=hi, xs=torch.ones(rows, 1, device="cuda"), xl=lo, ws=ws)
     x = hi.double() + lo.double() / 128
     assert torch.equal(y.double(), x @ values(torch, (q, s, z)).T)
+
+
+@pytest.mark.parametrize("form", ["f32", "one", "two"])
+@pytest.mark.parametrize("rows", [1, 7, 130])
+def test_combine_in_place(q8, ws, rows, form):
+    """The residual's own place as the result's: bit for bit what another place gets."""
+    import torch
+    E, k, d, dff = 9, 4, 256, 128
+    mats, ids, gates, call, x, hidden, hv, residual = experts(torch, rows, E, k, d, dff, form, rows)
+    m = q8.q4_mat(*mats[2])
+    plan, kept = plan_of(q8, torch, ids, E) if rows > 1 else (None, None)
+    y = torch.full((rows, d), math.nan, device="cuda")
+    q8.moe_down_combine_q4(m, ids, gates, y, **hidden, plan=plan, residual=residual, ws=ws)
+    check_combined(torch, y, values(torch, mats[2]), hv, ids, gates, residual, d, form)
+    q8.moe_down_combine_q4(m, ids, gates, residual, **hidden, plan=plan, residual=residual, ws=ws)
+    assert torch.equal(residual, y)
+    del kept
