@@ -148,3 +148,27 @@ def test_combine_in_place(q8, ws, rows, form):
     q8.moe_down_combine_q4(m, ids, gates, residual, **hidden, plan=plan, residual=residual, ws=ws)
     assert torch.equal(residual, y)
     del kept
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("rows", [1, 7, 130])
+def test_experts_of_values_that_are_not_finite(q8, ws, rows, bad):
+    """A row with such a value has hidden rows and a result that are not finite; the others do not see it."""
+    import torch
+    E, k, d, dff, r = 9, 4, 256, 128, rows // 2
+    mats, ids, gates, call, x, hidden, hv, residual = experts(torch, rows, E, k, d, dff, "f32", rows + 5)
+    m = [q8.q4_mat(*t) for t in mats]
+    plan, kept = plan_of(q8, torch, ids, E) if rows > 1 else (None, None)
+    clean, h = (torch.full((rows, k, dff), 5.0, device="cuda") for _ in range(2))
+    q8.moe_gate_up_q4(m[0], m[1], ids, clean, **call, plan=plan, ws=ws)
+    values_ = call["x"].clone()
+    values_[r, 33] = bad
+    q8.moe_gate_up_q4(m[0], m[1], ids, h, x=values_, plan=plan, ws=ws)
+    rest = [i for i in range(rows) if i != r]
+    assert not torch.isfinite(h[r]).any() and torch.equal(h[rest], clean[rest])
+    y, want = torch.empty(rows, d, device="cuda"), torch.empty(rows, d, device="cuda")
+    q8.moe_down_combine_q4(m[2], ids, gates, want, **hidden, plan=plan, ws=ws)
+    hidden["h"][r, 1, 33] = bad
+    q8.moe_down_combine_q4(m[2], ids, gates, y, **hidden, plan=plan, ws=ws)
+    assert not torch.isfinite(y[r]).any() and torch.equal(y[rest], want[rest])
+    del kept
