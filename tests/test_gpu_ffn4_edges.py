@@ -172,3 +172,23 @@ def test_experts_of_values_that_are_not_finite(q8, ws, rows, bad):
     q8.moe_down_combine_q4(m[2], ids, gates, y, **hidden, plan=plan, ws=ws)
     assert not torch.isfinite(y[r]).any() and torch.equal(y[rest], want[rest])
     del kept
+
+
+@pytest.mark.parametrize("rows", [9, 150])
+def test_products_by_a_plan_of_the_softmax_router(q8, ws, rows):
+    """moe_route_topk's plan groups the rows for the 4-bit products."""
+    import torch
+    E, k, d, dff = 32, 4, 256, 128
+    mats, _, _, call, x, hidden, hv, residual = experts(torch, rows, E, k, d, dff, "f32", rows + 2)
+    g = gen(rows)
+    rq = torch.randint(-127, 128, (E, d), generator=g, device="cuda", dtype=torch.int8)
+    rs = torch.full((E, d // 32), 1e-3, device="cuda")
+    ids, gates = torch.empty(rows, k, dtype=torch.int32, device="cuda"), torch.empty(rows, k, device="cuda")
+    arrays = [torch.zeros(n, dtype=torch.int32, device="cuda") for n in (E, E + 1, rows * k, E + 1)]
+    plan = q8.plan_struct(*arrays)
+    q8.moe_route_topk(rq, rs, 0, k, ids, gates, x=call["x"], rows=rows, plan=plan, ws=ws)
+    h, y = torch.full((rows, k, dff), math.nan, device="cuda"), torch.full((rows, d), math.nan, device="cuda")
+    q8.moe_gate_up_q4(q8.q4_mat(*mats[0]), q8.q4_mat(*mats[1]), ids, h, **call, plan=plan, ws=ws)
+    q8.moe_down_combine_q4(q8.q4_mat(*mats[2]), ids, gates, y, **hidden, plan=plan, residual=residual, ws=ws)
+    check_hidden(torch, h, values(torch, mats[0]), values(torch, mats[1]), x, ids, dff, "f32")
+    check_combined(torch, y, values(torch, mats[2]), hv, ids, gates, residual, d, "f32")
