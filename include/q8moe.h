@@ -518,7 +518,7 @@ typedef struct {
  * parts, which hold a value to 2^-22 of it or 2^-28 of the largest magnitude of its block (one row) or of its row (several),
  * whichever is more, and are summed in f32.  With several rows scales of magnitudes up to 2^80 leave the sums in range.  Calls
  * of one row need no workspace; several take four bytes of it an activation value and some MiB, a projection as many rows at
- * a time as it holds. */
+ * a time as it holds; the experts' calls take all their rows at once (see moe_down_combine_q4). */
 Q8_API int q4_gemv(const q4_mat *W, const float *x, int64_t x_stride, const q8_act *xq, int64_t rows, float *y,
                    int64_t y_stride, q8_ws *ws, q8_stream stream);
 
@@ -530,7 +530,11 @@ Q8_API int moe_gate_up_q4(const q4_mat *gate, const q4_mat *up, int64_t dff, con
 
 /* moe_down_combine with 4-bit weights: y[r] = residual[r] + sum_j gates[r][j] (Wd[e*d .. e*d+d) . h[r][j]), the sum over j
  * in order, down stacked [E*d, dff], the hidden rows h ([rows*k][dff]) or hq.  residual may be NULL, and may be y itself.
- * plan as above.  An id outside [0, E) adds nothing.  ws holds the choices' outputs of several rows. */
+ * plan as above.  An id outside [0, E) adds nothing.
+ * Workspace of several rows (and of one whose activations no CTA holds), of moe_gate_up_q4 and of this call: at most
+ * n (544 ceil(cols/128) + 4) + 1024 bytes with n = rows*k + 8 min(E, rows*k) + 16 and the matrices' cols, and here 4 rows*k*d
+ * more for the choices' outputs; Q8_ENOSPACE, and nothing is written, where it is too small.  The default one holds 600 rows of 8
+ * of 128 experts of 2048 x 768; longer prompts take a larger one, or blocks of rows with a plan each. */
 Q8_API int moe_down_combine_q4(const q4_mat *down, int64_t d, const float *h, const q8_act *hq, int64_t rows, int k,
                                const int32_t *ids, const float *gates, const q8_moe_plan *plan, const float *residual,
                                float *y, q8_ws *ws, q8_stream stream);

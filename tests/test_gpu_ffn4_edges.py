@@ -192,3 +192,36 @@ def test_products_by_a_plan_of_the_softmax_router(q8, ws, rows):
     q8.moe_down_combine_q4(q8.q4_mat(*mats[2]), ids, gates, y, **hidden, plan=plan, residual=residual, ws=ws)
     check_hidden(torch, h, values(torch, mats[0]), values(torch, mats[1]), x, ids, dff, "f32")
     check_combined(torch, y, values(torch, mats[2]), hv, ids, gates, residual, d, "f32")
+
+
+def need(rows, k, E, cols, d=0):
+    """The workspace that a call of several rows needs at most: of every choice, and up to eight more an expert, 544 bytes for
+    each 128 columns started and 4; for down also its outputs."""
+    n = rows * k + 8 * min(E, rows * k) + 16
+    return n * ((cols + 127) // 128 * 544 + 4) + 4 * rows * k * d + 1024
+
+
+@pytest.mark.parametrize("form", ["f32", "one", "two"])
+@pytest.mark.parametrize("rows,E,k,d,dff", [(7, 40, 3, 416, 96), (24, 32, 8, 256, 256), (130, 6, 6, 128, 160), (300, 4, 1, 256, 128)])
+def test_experts_in_a_workspace_that_just_holds_them(q8, ws, rows, E, k, d, dff, form):
+    import torch
+    mats, ids, gates, call, x, hidden, hv, residual = experts(torch, rows, E, k, d, dff, form, rows + E)
+    m = [q8.q4_mat(*t) for t in mats]
+    plan, kept = plan_of(q8, torch, ids, E)
+    small, tiny = [q8.Workspace(need(rows, k, E, d)), q8.Workspace(need(rows, k, E, dff, d))], q8.Workspace(4096)
+    h, y = torch.full((rows, k, dff), 7.0, device="cuda"), torch.full((rows, d), 7.0, device="cuda")
+    for call_ in (lambda w: q8.moe_gate_up_q4(m[0], m[1], ids, h, **call, plan=plan, ws=w),
+                  lambda w: q8.moe_down_combine_q4(m[2], ids, gates, y, **hidden, plan=plan, residual=residual, ws=w)):
+        with pytest.raises(q8.Q8Error) as e:
+            call_(tiny)
+        assert e.value.code == -5
+    assert (h == 7).all() and (y == 7).all()
+    want = torch.empty_like(h), torch.empty_like(y)
+    q8.moe_gate_up_q4(m[0], m[1], ids, want[0], **call, plan=plan, ws=ws)
+    q8.moe_down_combine_q4(m[2], ids, gates, want[1], **hidden, plan=plan, residual=residual, ws=ws)
+    q8.moe_gate_up_q4(m[0], m[1], ids, h, **call, plan=plan, ws=small[0])
+    q8.moe_down_combine_q4(m[2], ids, gates, y, **hidden, plan=plan, residual=residual, ws=small[1])
+    assert torch.equal(h, want[0]) and torch.equal(y, want[1])
+    for w in (*small, tiny):
+        w.close()
+    del kept
