@@ -147,8 +147,9 @@ __device__ __noinline__ void choose_exactly(const RouteParams& p, const float* r
 }
 
 // Adds the CTA's choices [first, first + n) (their experts in ids) to the lists, in ascending order: next[e] is expert e's
-// first free place.  wh is [warps][E] of shared memory.  (What is no expert indexes nothing: ids that this call's launches did not
-// write, were the workspace in use by another call at the same time.)
+// first free place.  wh is [warps][E] of shared memory.  HOLD: ids are held within [0, E) (the last CTA of a launch reads the
+// others' ids, which are not there yet should the workspace's counter be in use by another call at the same time).
+template <bool HOLD>
 __device__ __forceinline__ void place_choices(const int32_t* ids, int first, int n, int E, int* wh, int* next, int32_t* lists) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, W = blockDim.x >> 5;
     const int seg = ((n + W - 1) / W + 31) & ~31;
@@ -156,8 +157,8 @@ __device__ __forceinline__ void place_choices(const int32_t* ids, int first, int
     for (int i = threadIdx.x; i < W * E; i += blockDim.x) wh[i] = 0;
     __syncthreads();
     for (int i = lo + lane; i < hi; i += 32) {
-        const int e = __ldcg(ids + first + i);
-        if ((unsigned)e < (unsigned)E) atomicAdd(&wh[w * E + e], 1);
+        const unsigned e = __ldcg(ids + first + i);
+        atomicAdd(&wh[w * E + (HOLD ? min(e, (unsigned)E - 1) : e)], 1);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
@@ -170,9 +171,9 @@ __device__ __forceinline__ void place_choices(const int32_t* ids, int first, int
     }
     __syncthreads();
     for (int i = lo; i < hi; i += 32) {
-        int e = i + lane < hi ? __ldcg(ids + first + i + lane) : E;  // (lanes past the end stand together)
-        const bool in = (unsigned)e < (unsigned)E;
-        if (!in) e = E;
+        const bool in = i + lane < hi;
+        unsigned e = in ? __ldcg(ids + first + i + lane) : E;  // (lanes past the end stand together)
+        if (HOLD) e = min(e, in ? (unsigned)E - 1 : (unsigned)E);
         const unsigned same = __match_any_sync(FULL, e);
         const int before = __popc(same & ((1u << lane) - 1));
         if (in) lists[wh[w * E + e] + before] = first + i + lane;
@@ -423,8 +424,8 @@ __global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_k
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) total[e] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const int e = __ldcg(p.ids + (int64_t)from * p.K + i);
-        if ((unsigned)e < (unsigned)p.E) atomicAdd(&total[e], 1);
+        const unsigned e = __ldcg(p.ids + (int64_t)from * p.K + i);
+        atomicAdd(&total[min(e, (unsigned)p.E - 1)], 1);
     }
     __syncthreads();
     if (p.hist) {
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(NL <= 8 ? 1024 : NL == 16 ? 512 : 256) route_k
     }
     scan_totals(total, p.E, off, tmp, p.plan, true);
     __syncthreads();
-    place_choices(p.ids, 0, n, p.E, wh, off, p.plan.lists);
+    place_choices<true>(p.ids, 0, n, p.E, wh, off, p.plan.lists);
 }
 
 // CTA b places the choices of route_kernel's CTA b: the counts of all CTAs give every expert's total and where CTA b's
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(kPlaceThreads) place_kernel(const RouteParams 
     griddep_wait();
     const int failed = p.failed ? __ldcg(p.failed) : 0;
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) total[e] = before[e] = 0;
-    if (__syncthreads_or(failed)) return;  // (the histograms have not been written)
+    __syncthreads();
     const int mine = blockIdx.x;
     if (p.E % 4 == 0) {  // four experts a thread
         const int quads = p.E / 4, parts = max(1, (int)blockDim.x / quads);
@@ -477,13 +478,13 @@ __global__ void __launch_bounds__(kPlaceThreads) place_kernel(const RouteParams 
             total[e] = all, before[e] = pre;
         }
     }
-    __syncthreads();
+    if (__syncthreads_or(failed)) return;  // (the histograms have not been written)
     scan_totals(total, p.E, off, tmp, p.plan, mine == 0);
     __syncthreads();
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) off[e] += before[e];
     __syncthreads();
     const int first = mine * p.per, end = min(first + p.per, p.rows);
-    place_choices(p.ids, first * p.K, max(end - first, 0) * p.K, p.E, wh, off, p.plan.lists);
+    place_choices<false>(p.ids, first * p.K, max(end - first, 0) * p.K, p.E, wh, off, p.plan.lists);
 }
 
 template <int NL>
