@@ -202,7 +202,8 @@ class Workspace:
 
     def check(self, stream=None):
         """Waits for the stream; raises Q8_ETIMEOUT, and makes the workspace usable again, when a bounded wait of a
-        q8_paged_attention on it gave up."""
+        q8_paged_attention, or of a product with 4-bit weights, on it gave up (later ones, and routers that fill a plan, then
+        wrote nothing)."""
         _check(lib.q8_workspace_check(self.handle, _stream(stream)))
 
     def close(self):

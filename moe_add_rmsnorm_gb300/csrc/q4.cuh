@@ -15,7 +15,9 @@ namespace q8 {
 enum { FORM_F32 = 0, FORM_ONE = 1, FORM_TWO = 2 };  // activations: f32, int8 words, words and low words
 
 // The eight words of w less their zero point, as pairs of f16: values (0, 4), (1, 5), (2, 6), (3, 7).  A word placed in the
-// low mantissa bits of 1024 is 1024 + word, one placed four bits higher 1024 + 16 word = 16 (64 + word): both exact.
+// low mantissa bits of 1024 is 1024 + word, one placed four bits higher 1024 + 16 word = 16 (64 + word): both exact.  (The
+// conversion by 1024's mantissa bits is published: Kim, Henry, Fahim and Hassan Awadalla, "Who Says Elephants Can't Run:
+// Bringing Large Scale MoE Models into Cloud Scale Production", 2022.)
 // zc: 1024 + z twice; zf: -(64 + z) twice.
 __device__ __forceinline__ void words_f16(uint32_t w, uint32_t zc, uint32_t zf, uint32_t (&h)[4]) {
     const __half2 sixteenth = __float2half2_rn(0.0625f);

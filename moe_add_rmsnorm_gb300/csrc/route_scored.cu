@@ -7,8 +7,9 @@
 // bits and counted by those; where kept and left groups are, or a softmax with a bias (whose sum all scores share) or more
 // candidates than lanes, the whole row is chosen again in 64 bits.  What bounds it is instructions, about 1200 a row of 256
 // with eight groups, and where few rows share a warp's SM the rows with near ties, which take microseconds each.  Measured,
-// replayed: 15001 rows of 256 experts, 8 of 4 groups' chosen and grouped by expert, 41 us (17 MB, 2.5 at the measured copy rate);
-// 61 rows 8.3, one row of 128 without a plan 2.6.  Taking the largest K times over the lanes took 73 and 30.
+// replayed: 15001 rows of 256 experts, 8 of 4 groups' chosen and grouped by expert, 41.6 us (17 MB, 2.5 at the measured copy rate), of
+// which the grouping's own launch is a third: its CTAs each read all CTAs' counts.  61 rows 8.5, one row of 128 without a plan
+// 2.7.  Taking the largest K times over the lanes took 73 and 30.
 #include <math.h>
 
 #include "common.cuh"
