@@ -104,8 +104,8 @@ Q8_API size_t q8_workspace_bytes(const q8_ws *ws);
  * ones on the workspace, and moe_route_scored calls that fill a plan, wrote nothing, because its counters may not have been
  * zero.  (4-bit products of one row, and of so few rows that they leave the tensor cores alone, neither wait nor count, and are
  * computed as ever; the calls with Q8_0 weights do not look at the failure, and what they write on the workspace until it has
- * been checked is not to be used.)  The counters are zeroed and the failure cleared, so that the workspace can be used again; no other call on
- * it may be in flight. */
+ * been checked is not to be used.)  The counters are zeroed and the failure cleared, so that the workspace can be used again;
+ * no other call on it may be in flight. */
 Q8_API int q8_workspace_check(q8_ws *ws, q8_stream stream);
 
 /* ---- a1 / K4: quantisation and the residual add + RMSNorm -------------------------------------------------------- */
@@ -514,10 +514,10 @@ typedef struct {
  * stride a multiple of 4) or, with x NULL, the quantized form xq (dense; the two-word form when xq->lo is not NULL).  y is
  * device f32, rows y_stride values apart, and overlaps no input (columns beside x's of one buffer do not).  Every 32-value
  * block's dot of a quantized activation is the exact integer, scaled and summed in f32 (with two words it is an integer of
- * 128ths that f32 holds while |word - z| is at most 15, as with zero points of 4 bits; beyond, its sums are f32's, by steps that may be
- * cut off); f32 activations enter as two f16 parts, which hold a value to 2^-22 of it or 2^-28 of the largest magnitude of its
- * block (one row) or of its row (several), whichever is more, and are summed in f32.  With several rows scales of magnitudes up to 2^80 leave the sums in range.  Calls
- * of one row need no workspace; several take four bytes of it an activation value and some MiB, a projection as many rows at
+ * 128ths that f32 holds while |word - z| is at most 15, as with zero points of 4 bits; beyond, its sums are f32's, by steps
+ * that may be cut off); f32 activations enter as two f16 parts, which hold a value to 2^-22 of it or 2^-28 of the largest
+ * magnitude of its block (one row) or of its row (several), whichever is more, and are summed in f32.  With several rows scales
+ * of magnitudes up to 2^80 leave the sums in range.  Calls of one row need no workspace; several take four bytes of it an activation value and some MiB, a projection as many rows at
  * a time as it holds; the experts' calls take all their rows at once (see moe_down_combine_q4). */
 Q8_API int q4_gemv(const q4_mat *W, const float *x, int64_t x_stride, const q8_act *xq, int64_t rows, float *y,
                    int64_t y_stride, q8_ws *ws, q8_stream stream);
