@@ -517,8 +517,9 @@ typedef struct {
  * 128ths that f32 holds while |word - z| is at most 15, as with zero points of 4 bits; beyond, its sums are f32's, by steps
  * that may be cut off); f32 activations enter as two f16 parts, which hold a value to 2^-22 of it or 2^-28 of the largest
  * magnitude of its block (one row) or of its row (several), whichever is more, and are summed in f32.  With several rows scales
- * of magnitudes up to 2^80 leave the sums in range.  Calls of one row need no workspace; several take four bytes of it an activation value and some MiB, a projection as many rows at
- * a time as it holds; the experts' calls take all their rows at once (see moe_down_combine_q4). */
+ * of magnitudes up to 2^80 leave the sums in range.  Calls of one row need no workspace; several take four bytes of it an
+ * activation value and some MiB, a projection as many rows at a time as it holds; the experts' calls take all their rows at once
+ * (see moe_down_combine_q4). */
 Q8_API int q4_gemv(const q4_mat *W, const float *x, int64_t x_stride, const q8_act *xq, int64_t rows, float *y,
                    int64_t y_stride, q8_ws *ws, q8_stream stream);
 
